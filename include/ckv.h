@@ -336,6 +336,126 @@ ckv_status ckv_sparse_decode_attn_noalloc(const void* q, int32_t q_dtype, const 
                                           int32_t clustered_end, int32_t cur_len, int32_t B,
                                           float* out, int32_t* dev_err, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache: K/V rows in fixed-size pages handed out by the caller, with
+ * dense decode attention over all rows held, and eviction of the rows with the
+ * least accumulated attention weight.  It serves what the recallable path does
+ * not: layers and sequences attended in full, batches whose sequences grow,
+ * end and share memory, and the non-recallable alternative (drop rows for
+ * good; ClusterKV page, section "Background and design principles": methods
+ * that evict by attention weight) next to the recallable selection.
+ *
+ *   K, V      pools of n_pages pages; element (page, head, slot, channel) at
+ *             page * stride[0] + head * stride[1] + slot * stride[2] + channel
+ *             (strides in elements, multiples of 16 bytes, at least d where
+ *             the extent is above one), so [n_pages][heads][page_size][d],
+ *             [n_pages][page_size][heads][d] and slices of larger pools fit.
+ *             Rows of one pool must not overlap each other.
+ *   table     [seqs][max_pages] int32: row r of (sequence s, KV head h) is slot
+ *             r % page_size of page table[s][r / page_size].  Entries past the
+ *             last held row's page are never read.
+ *   lens      [seqs] int32, rows held by every KV head of the sequence, 0 to
+ *             max_pages * page_size = R.
+ *   mass      [seqs][heads][R] float: accumulated attention weight of a row.
+ *   pos       [seqs][heads][R] int32: token position of a row (after an
+ *             eviction rows are in no particular order).
+ *   seen      [seqs] int32: tokens the sequence has seen, the next position.
+ * mass, pos and seen may be NULL in calls that do not need them (append then
+ * leaves them out; pos needs seen).  Pages of several sequences may be shared
+ * while nothing is appended to or evicted from them.  All lens, counts and
+ * positions live on the device, so a whole decode step can be captured once
+ * and replayed.  dev_err is an optional device int32 that receives CKV_DEV_*
+ * codes (the first error stays until the caller clears it): a length outside
+ * [0, R] is clamped (CKV_DEV_BAD_COUNT), a page id outside [0, n_pages) is
+ * skipped with its rows (CKV_DEV_BAD_INDEX).
+ * Common errors: CKV_ERR_ARG (null pointer, d != 128, page_size not a multiple
+ * of 16, a non-positive extent, R above 2^31 - 17, a stride too small),
+ * CKV_ERR_DTYPE, CKV_ERR_ALIGN. */
+typedef struct {
+    void* K;
+    void* V;
+    int64_t k_stride[3]; /* page, head, row */
+    int64_t v_stride[3];
+    const int32_t* table;
+    int32_t* lens;
+    float* mass;
+    int32_t* pos;
+    int32_t* seen;
+    int32_t* dev_err;
+    int32_t n_pages;
+    int32_t heads; /* KV heads */
+    int32_t page_size;
+    int32_t seqs;
+    int32_t max_pages;
+    int32_t d;
+    int32_t kv_dtype;
+} ckv_paged_cache;
+
+/* Appends counts[s] <= n rows (all n when counts is NULL) to every KV head of
+ * every sequence: rows r0 .. r0 + counts[s] - 1 of K and V := rows 0 ..
+ * counts[s] - 1 of k_src and v_src (row j of (s, h) at s * stride[0] + h *
+ * stride[1] + j * stride[2] elements; strides multiples of 16 bytes), pos :=
+ * p0 + j, mass := 0.  r0 is start[s], or lens[s] when start is NULL, p0 is
+ * first[s], or seen[s] when first is NULL; then lens[s] := r0 + counts[s] and
+ * seen[s] := p0 + counts[s].  A sequence whose r0 or count is negative, whose
+ * count is above n or that would pass R is left as it is (CKV_DEV_BAD_COUNT).
+ * The sources may be mapped pinned host memory.  start and first must not
+ * overlap lens and seen unless they are the same pointers.
+ * Errors: as above; CKV_ERR_ARG (n < 1, pos without seen). */
+ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void* k_src, const void* v_src,
+                            const int64_t* k_src_stride, const int64_t* v_src_stride, int32_t n,
+                            const int32_t* counts, const int32_t* start, const int32_t* first, void* stream);
+
+/* Bytes of workspace that ckv_paged_decode_attn needs for this cache with g
+ * query heads per KV head, with (with_mass = 1) or without mass_out.  It
+ * depends on the extents alone, not on lens. */
+ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int32_t with_mass, int64_t* bytes);
+
+/* Decode attention of one new token per sequence over all rows held.  For
+ * query head j of KV head h (heads h * g + j of q, j < g <= 16) with s_r =
+ * scale * q . K_r, r < lens[s]:
+ *   lse = ln sum_r e^{s_r},  out = sum_r e^{s_r - lse} V_r,
+ *   mass_out[s][h][r] = mass_in[s][h][r] + sum_j e^{s_r - lse_j}.
+ * A sequence with no rows gives out = 0 and lse = -inf.  q: query head i of
+ * sequence s at s * q_stride[0] + i * q_stride[1] elements, of kv_dtype; out
+ * [seqs][heads * g][d] float; lse [seqs][heads * g] float or NULL; mass_out
+ * [seqs][heads][R] float or NULL, mass_in the same or NULL (taken as 0), and
+ * may be mass_out itself; entries of rows not held are left as they are.  fp32
+ * arithmetic on products of the operands as they are.  Values of rows not held
+ * are never used, whatever they are; held rows must be finite.
+ * Results do not depend on the order in which the GPU runs the blocks.
+ * workspace: caller-owned, 256-byte aligned, at least the size given above; its
+ * contents need no initialisation and are not kept, but calls that can overlap
+ * on the GPU (two streams, two graphs) need workspaces of their own.
+ * Errors: as above; CKV_ERR_ARG (g outside [1, 16], scale not finite, mass_in
+ * without mass_out), CKV_ERR_CAPACITY (workspace too small). */
+ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, int32_t q_dtype, const int64_t* q_stride,
+                                 int32_t g, float scale, float* out, float* lse, const float* mass_in,
+                                 float* mass_out, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Eviction by accumulated attention weight, in two calls.  _select chooses: of
+ * every (s, h) with lens[s] > budget it keeps `budget` rows, first those with
+ * pos < sinks or pos >= seen[s] - recent, then by mass descending (NaN lowest,
+ * -0 = +0), ties to the lower row.  The cache need not stay in order, so only
+ * the kept rows at or past the budget have to move, into the slots below it
+ * that were not kept: moves[s][h][k] = (source row, destination row), k <
+ * n_moves[s][h], the k-th mover and the k-th hole in ascending order.  Entries
+ * past n_moves are left unchanged; a sequence at or below the budget gets
+ * n_moves = 0.  moves [seqs][heads][max_moves][2] int32 with max_moves >=
+ * min(budget, R - budget).  Reads mass, pos, seen and lens; changes no cache.
+ * _apply carries the moves out for K, V and (where not NULL) mass and pos, and
+ * sets lens[s] := min(lens[s], budget); pages past the budget are then free.
+ * Sources lie at or past the budget and destinations below it, so the moves
+ * have no order and repeating the call changes nothing; a move outside those
+ * ranges is skipped (CKV_DEV_BAD_INDEX), n_moves outside [0, max_moves] is
+ * clamped (CKV_DEV_BAD_COUNT).
+ * Errors: as above; CKV_ERR_ARG (budget < 1, sinks, recent or max_moves < 0,
+ * sinks + recent > budget), CKV_ERR_CAPACITY (max_moves too small). */
+ckv_status ckv_paged_evict_select(const ckv_paged_cache* cache, int32_t budget, int32_t sinks, int32_t recent,
+                                  int32_t max_moves, int32_t* moves, int32_t* n_moves, void* stream);
+ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, int32_t max_moves,
+                                 const int32_t* moves, const int32_t* n_moves, void* stream);
+
 /* Host-side copy of the context's counters. */
 ckv_status ckv_get_info(ckv_ctx* ctx, ckv_info* info);
 

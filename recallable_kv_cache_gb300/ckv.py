@@ -47,6 +47,11 @@ SIGNATURES = {
     "ckv_get_device_error": ([_P, ctypes.POINTER(_I)], _I),
     "ckv_set_wait_limit": ([_P, ctypes.c_int64, _I], _I),
     "ckv_set_l2_persistence": ([_P, ctypes.c_int64], _I),
+    "ckv_paged_append": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _P], _I),
+    "ckv_paged_attn_workspace": ([_P, _I, _I, ctypes.POINTER(ctypes.c_int64)], _I),
+    "ckv_paged_decode_attn": ([_P, _P, _I, _P, _I, _F, _P, _P, _P, _P, _P, ctypes.c_int64, _P], _I),
+    "ckv_paged_evict_select": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
+    "ckv_paged_evict_apply": ([_P, _I, _I, _P, _P, _P], _I),
     "ckv_sparse_decode_attn_noalloc": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
 }
 
@@ -60,6 +65,15 @@ class Config(ctypes.Structure):
 class Info(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "n_clusters", "prefill_clusters", "prefill_len", "clustered_end")]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """ckv_paged_cache."""
+    _fields_ = ([(n, _P) for n in ("K", "V")]
+                + [(n, ctypes.c_int64 * 3) for n in ("k_stride", "v_stride")]
+                + [(n, _P) for n in ("table", "lens", "mass", "pos", "seen", "dev_err")]
+                + [(n, ctypes.c_int32) for n in ("n_pages", "heads", "page_size", "seqs", "max_pages", "d",
+                                                 "kv_dtype")])
 
 
 class CKVError(RuntimeError):
@@ -343,3 +357,140 @@ def append_kv(k_src, v_src, K, V, pos: int, n: int | None = None, stream=None):
         n = k_src.shape[1] if n is None else n
     _check(lib().ckv_append_kv(ptr(k_src), ptr(v_src), src_len, _dtype_code(K), units, max_len, pos, n, ptr(K),
                                ptr(V), _stream(stream)), "ckv_append_kv")
+
+
+class PagedCache:
+    """A paged K/V cache over the caller's tensors (see the paged cache section
+    of ckv.h): ``K``, ``V`` [n_pages, heads, page_size, 128] bf16 or float32, any
+    strides with contiguous channels; ``table`` [seqs, max_pages] and ``lens``
+    [seqs] int32; optionally ``mass`` (float32) and ``pos`` (int32) [seqs, heads,
+    max_pages * page_size], ``seen`` [seqs] int32 and ``dev_err`` [1] int32.
+
+    ``g`` is the number of query heads per KV head.  The handle keeps the
+    tensors alive and owns the attention's workspace, allocated here (so that
+    every call may be captured into a CUDA graph).  Like a Context, one handle
+    must not be used from two streams at the same time; another handle over the
+    same tensors has a workspace of its own.  Calls run on the tensors' device,
+    on ``stream`` or that device's current stream.  A tensor of another shape,
+    dtype, device or layout raises ValueError (TypeError for dtypes) and nothing
+    is launched."""
+
+    def __init__(self, K, V, table, lens, g: int = 1, mass=None, pos=None, seen=None, dev_err=None):
+        import torch
+        self.device = K.device
+        if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype:
+            raise ValueError("K and V must be [n_pages, heads, page_size, 128] of one dtype, got "
+                             f"{tuple(K.shape)} {K.dtype}, {tuple(V.shape)} {V.dtype}")
+        if K.stride(3) != 1 or V.stride(3) != 1:
+            raise ValueError("the channels of K and V must be contiguous")
+        code = _dtype_code(K)
+        n_pages, heads, page, d = K.shape
+        if table.dim() != 2:
+            raise ValueError(f"table must be [seqs, max_pages], got {tuple(table.shape)}")
+        seqs, width = table.shape
+        self.seqs, self.heads, self.g, self.rows = seqs, heads, g, width * page
+        self.dtype, self._code = K.dtype, code
+        for name, t, shape, dtype in (
+                ("V", V, tuple(K.shape), K.dtype), ("table", table, (seqs, width), torch.int32),
+                ("lens", lens, (seqs,), torch.int32), ("mass", mass, (seqs, heads, self.rows), torch.float32),
+                ("pos", pos, (seqs, heads, self.rows), torch.int32), ("seen", seen, (seqs,), torch.int32),
+                ("dev_err", dev_err, (1,), torch.int32)):
+            self._tensor(name, t, shape, dtype, contiguous=name != "V")
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache must be on a CUDA device, got {self.device}")
+        self.K, self.V, self.table, self.lens = K, V, table, lens
+        self.mass, self.pos, self.seen, self.dev_err = mass, pos, seen, dev_err
+        self._struct = PagedCacheStruct(
+            ptr(K), ptr(V), (ctypes.c_int64 * 3)(*K.stride()[:3]), (ctypes.c_int64 * 3)(*V.stride()[:3]), ptr(table),
+            ptr(lens), ptr(mass), ptr(pos), ptr(seen), ptr(dev_err), n_pages, heads, page, seqs, width, d, code)
+        self._ref = ctypes.addressof(self._struct)
+        need = ctypes.c_int64()
+        _check(lib().ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),
+               "ckv_paged_attn_workspace")
+        self.workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+        self._workspace = (ptr(self.workspace), need.value)
+
+    def _tensor(self, name, t, shape, dtype, contiguous=True):
+        """None is passed on (the C call says which arguments it needs)."""
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape or (contiguous and not t.is_contiguous()):
+            raise ValueError(f"{name} must be {'contiguous ' if contiguous else ''}{list(shape)}, got "
+                             f"{list(t.shape)} with strides {list(t.stride())}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        return t.data_ptr()
+
+    def _call(self, name, stream, *args):
+        import torch
+        fn = getattr(lib(), name)
+        index = self.device.index
+        if index is None or index == torch.cuda.current_device():
+            _check(fn(self._ref, *args, _stream(stream)), name)
+        else:
+            with torch.cuda.device(index):
+                _check(fn(self._ref, *args, _stream(stream)), name)
+
+    def append(self, k, v, counts=None, start=None, first=None, stream=None):
+        """counts[s] rows of k, v [seqs, heads, n, 128] (any strides with
+        contiguous channels) to every sequence (see ckv_paged_append); k and v
+        may live in pinned host memory the device maps."""
+        import torch
+        n = k.shape[2] if k.dim() == 4 else 0
+        for name, t in (("k", k), ("v", v)):
+            if tuple(t.shape) != (self.seqs, self.heads, n, 128) or t.stride(3) != 1:
+                raise ValueError(f"{name} must be [{self.seqs}, {self.heads}, n, 128] with contiguous channels, got "
+                                 f"{tuple(t.shape)}")
+            if t.dtype != self.dtype:
+                raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+            if t.device != self.device and not (t.device.type == "cpu" and t.is_pinned()):
+                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        per_seq = [self._tensor(name, t, (self.seqs,), torch.int32)
+                   for name, t in (("counts", counts), ("start", start), ("first", first))]
+        self._call("ckv_paged_append", stream, ptr(k), ptr(v), (ctypes.c_int64 * 3)(*k.stride()[:3]),
+                   (ctypes.c_int64 * 3)(*v.stride()[:3]), n, *per_seq)
+
+    def decode_attn(self, q, out, lse=None, mass_in=None, mass_out=None, scale=None, stream=None):
+        """Attention of q [seqs, heads * g, 128] over the rows held into out
+        [seqs, heads * g, 128] float32 (see ckv_paged_decode_attn).  With
+        ``mass_out`` (for instance the cache's own mass, given as mass_in too)
+        each row's weight is added to mass_in.  scale: 1 / sqrt(128) if None."""
+        import torch
+        hq = self.heads * self.g
+        if tuple(q.shape) != (self.seqs, hq, 128) or q.stride(2) != 1:
+            raise ValueError(f"q must be [{self.seqs}, {hq}, 128] with contiguous channels, got {tuple(q.shape)}")
+        if q.dtype != self.dtype:
+            raise TypeError(f"q must be {self.dtype}, got {q.dtype}")
+        if q.device != self.device:
+            raise ValueError(f"q is on {q.device}, the cache on {self.device}")
+        rows = (self.seqs, self.heads, self.rows)
+        f32 = torch.float32
+        self._call("ckv_paged_decode_attn", stream, ptr(q), self._code, (ctypes.c_int64 * 2)(q.stride(0), q.stride(1)),
+                   self.g, 128 ** -0.5 if scale is None else scale, self._tensor("out", out, (self.seqs, hq, 128), f32),
+                   self._tensor("lse", lse, (self.seqs, hq), f32), self._tensor("mass_in", mass_in, rows, f32),
+                   self._tensor("mass_out", mass_out, rows, f32), *self._workspace)
+
+    def _moves(self, moves, n_moves):
+        import torch
+        if moves.dim() != 4:
+            raise ValueError(f"moves must be [seqs, heads, max_moves, 2], got {tuple(moves.shape)}")
+        most = moves.shape[2]
+        return (most, self._tensor("moves", moves, (self.seqs, self.heads, most, 2), torch.int32),
+                self._tensor("n_moves", n_moves, (self.seqs, self.heads), torch.int32))
+
+    def evict_select(self, budget: int, sinks: int, recent: int, moves, n_moves, stream=None):
+        """The rows to move when every KV head keeps ``budget`` of its rows (see
+        ckv_paged_evict_select): moves [seqs, heads, max_moves, 2], n_moves
+        [seqs, heads] int32."""
+        self._call("ckv_paged_evict_select", stream, budget, sinks, recent, *self._moves(moves, n_moves))
+
+    def evict_apply(self, budget: int, moves, n_moves, stream=None):
+        """Carries the moves out and shortens lens (see ckv_paged_evict_apply)."""
+        self._call("ckv_paged_evict_apply", stream, budget, *self._moves(moves, n_moves))
+
+    def evict(self, budget: int, sinks: int, recent: int, moves, n_moves, stream=None):
+        """evict_select, then evict_apply."""
+        self.evict_select(budget, sinks, recent, moves, n_moves, stream)
+        self.evict_apply(budget, moves, n_moves, stream)

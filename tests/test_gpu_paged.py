@@ -1,0 +1,673 @@
+"""GPU parity of the paged cache (append, decode attention with the accumulated
+weights, eviction) against its float64 oracle, through the public handle.
+
+Tolerances of the attention.  Let S = max_r scale * sum_i |q_i k_ri|, n the rows.
+  * a score sums 128 products in fp32, each step off by at most one unit in the
+    last place of the running sum (a tensor core may truncate): es = 2^-16 S
+    covers 128 * 2^-23 S and the rounding of the scale and of log2(e);
+  * a weight's numerator and denominator each inherit es: 2 es, doubled for the
+    second order; the exponential and a weight carried as two or more bf16 terms
+    add at most 2^-17 together, doubled for the denominator: 2^-16;
+  * sums over rows take at most n / 16 + 200 sequential steps (a tile of 16
+    rows is one tensor-core step, partial sums are joined), each off by 2^-23.
+So |out - exact| <= (4 es + 2^-16 + 2 * 2^-23 (n / 16 + 200)) sum_r w_r |v_r|,
+the weights by the same factor, and lse by 2 es + 2^-19 + 2^-23 (n / 16 + 200 +
+|lse|).  Copies and choices are exact."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as po
+from recallable_kv_cache_gb300 import ckv
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+D = 128
+
+
+def pools(n_pages, heads, page, dtype, layout, gen):
+    """K, V [n_pages, heads, page, 128] of normal values in one of four layouts."""
+    if layout == "hpd":
+        shape, view = (2, n_pages, heads, page, D), lambda x: (x[0], x[1])
+    elif layout == "phd":
+        shape, view = (2, n_pages, page, heads, D), lambda x: (x[0].transpose(1, 2), x[1].transpose(1, 2))
+    elif layout == "kv_in_page":
+        shape, view = (n_pages, 2, heads, page, D), lambda x: (x[:, 0], x[:, 1])
+    else:  # "wide": rows 160 channels apart, a slice of a wider pool
+        shape, view = (2, n_pages, heads, page, 160), lambda x: (x[0][..., 8:136], x[1][..., 16:144])
+    x = torch.randn(shape, generator=gen).to(DT[dtype]).cuda()
+    return view(x)
+
+
+class Case:
+    """A cache of random contents: every row and page that is not held is NaN."""
+
+    def __init__(self, lens, heads=2, g=4, page=16, dtype="bf16", layout="hpd", spare=3, width=None, seed=0,
+                 q_scale=1.5, garbage=float("nan")):
+        gen = torch.Generator().manual_seed(seed)
+        S = len(lens)
+        need = [-(-n // page) for n in lens]
+        width = width or max(1, max(need))
+        n_pages = sum(need) + spare
+        self.K, self.V = pools(n_pages, heads, page, dtype, layout, gen)
+        perm = torch.randperm(n_pages, generator=gen).to(torch.int32)
+        table = torch.full((S, width), 2 ** 31 - 1, dtype=torch.int32)
+        held = torch.zeros(n_pages, page, dtype=torch.bool)
+        at = 0
+        for s, n in enumerate(lens):
+            table[s, :need[s]] = perm[at:at + need[s]]
+            for i in range(need[s]):
+                held[perm[at + i].long(), :min(page, n - i * page)] = True
+            at += need[s]
+        mask = ~held.cuda()[:, None, :, None].expand(n_pages, heads, page, D)
+        self.K.masked_fill_(mask, garbage)
+        self.V.masked_fill_(mask, garbage)
+        R = width * page
+        self.S, self.heads, self.g, self.page, self.R, self.n_pages, self.dtype = S, heads, g, page, R, n_pages, dtype
+        self.lens_list = list(lens)
+        self.table, self.lens = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.mass = torch.rand(S, heads, R, generator=gen).cuda()
+        self.pos = torch.arange(R, dtype=torch.int32).expand(S, heads, R).contiguous().cuda()
+        self.seen = self.lens.clone()
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.q = (q_scale * torch.randn(S, heads * g, D, generator=gen)).to(DT[dtype]).cuda()
+        self.out = torch.full((S, heads * g, D), float("nan"), device="cuda")
+        self.lse = torch.full((S, heads * g), float("nan"), device="cuda")
+        self.handle = self.make()
+
+    def make(self):
+        return ckv.PagedCache(self.K, self.V, self.table, self.lens, g=self.g, mass=self.mass, pos=self.pos,
+                              seen=self.seen, dev_err=self.err)
+
+    def rows(self, s, h, n=None):
+        n = self.lens_list[s] if n is None else n
+        t = self.table[s].cpu().numpy()
+        k, ok = po.rows(self.host("K"), t, h, n, self.n_pages)
+        v, _ = po.rows(self.host("V"), t, h, n, self.n_pages)
+        return k, v, ok
+
+    def host(self, name):
+        key = "_host_" + name
+        if not hasattr(self, key):
+            setattr(self, key, getattr(self, name).double().cpu().numpy())
+        return getattr(self, key)
+
+    def check_attention(self, scale=None, mass_in=None, mass_out=None, mass_before=None):
+        """out, lse (and mass_out) against the oracle within the derived bounds."""
+        scale = D ** -0.5 if scale is None else scale
+        out, lse = self.out.double().cpu().numpy(), self.lse.double().cpu().numpy()
+        q = self.q.double().cpu().numpy()
+        mo = None if mass_out is None else mass_out.double().cpu().numpy()
+        for s in range(self.S):
+            for h in range(self.heads):
+                k, v, ok = self.rows(s, h)
+                qs = q[s, h * self.g:(h + 1) * self.g]
+                o, z, w = po.attend(qs, k, v, ok, scale)
+                got, gl = out[s, h * self.g:(h + 1) * self.g], lse[s, h * self.g:(h + 1) * self.g]
+                n = self.lens_list[s]
+                es = 2.0 ** -16 * abs(scale) * max([np.abs(qs) @ np.abs(x) for x in k[ok]], key=np.max).max() if ok.any() else 0.0
+                sums = 2.0 ** -23 * (n / 16 + 200)
+                eps = 4 * es + 2.0 ** -16 + 2 * sums
+                for j in range(self.g):
+                    if not ok.any():
+                        assert not got[j].any() and gl[j] == -math.inf
+                        continue
+                    p = np.exp(scale * (k[ok] @ qs[j]) - z[j])
+                    bound = eps * (p @ np.abs(v[ok])) + 1e-30
+                    assert (np.abs(got[j] - o[j]) <= bound).all(), (s, h, j, np.abs(got[j] - o[j]).max(), bound.min())
+                    assert abs(gl[j] - z[j]) <= 2 * es + 2.0 ** -19 + sums + 2.0 ** -23 * abs(z[j])
+                if mo is not None:
+                    base = np.zeros(n) if mass_in is None else mass_in[s, h, :n]
+                    want = base + w
+                    assert (np.abs(mo[s, h, :n] - want) <= eps * w + 2.0 ** -23 * np.abs(want) + 1e-30).all()
+                    assert np.array_equal(mo[s, h, n:], mass_before[s, h, n:])
+
+
+ATTEND = [
+    # lens, heads, g, page, dtype, layout
+    ([1], 1, 1, 16, "bf16", "hpd"),
+    ([1], 1, 1, 16, "f32", "hpd"),
+    ([0], 1, 4, 16, "bf16", "hpd"),
+    ([0, 0, 0], 3, 2, 16, "f32", "hpd"),
+    ([15, 16, 17, 31, 32, 33], 2, 4, 16, "bf16", "hpd"),
+    ([15, 16, 17, 31, 32, 33], 2, 4, 16, "f32", "phd"),
+    ([0, 7, 0, 129, 1, 0], 3, 8, 48, "bf16", "phd"),
+    ([0, 7, 0, 129, 1, 0], 3, 8, 48, "f32", "kv_in_page"),
+    ([63, 64, 65, 2], 8, 3, 64, "bf16", "kv_in_page"),
+    ([500, 3], 5, 5, 32, "f32", "wide"),
+    ([500, 3], 5, 7, 32, "bf16", "wide"),
+    ([700, 255, 256, 257], 2, 9, 128, "bf16", "phd"),
+    ([700, 255, 256, 257], 2, 12, 128, "f32", "hpd"),
+    ([333, 1000], 1, 16, 16, "bf16", "hpd"),
+    ([333, 1000], 1, 16, 16, "f32", "phd"),
+    ([4097], 1, 2, 2048, "bf16", "hpd"),
+    ([4097], 2, 6, 16, "f32", "hpd"),
+    ([5000, 1, 77], 4, 1, 64, "bf16", "phd"),
+    ([3] * 70, 7, 4, 16, "bf16", "hpd"),
+    ([3, 0, 20] * 60, 11, 2, 16, "f32", "hpd"),
+]
+
+
+@pytest.mark.parametrize("lens,heads,g,page,dtype,layout", ATTEND)
+@pytest.mark.parametrize("mass", [False, True])
+def test_attention(lens, heads, g, page, dtype, layout, mass):
+    c = Case(lens, heads, g, page, dtype, layout, seed=len(lens) + g)
+    mass_out = torch.full_like(c.mass, 7.0) if mass else None
+    before = None if mass_out is None else mass_out.double().cpu().numpy()
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_in=c.mass if mass else None, mass_out=mass_out)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    c.check_attention(mass_in=c.mass.double().cpu().numpy(), mass_out=mass_out, mass_before=before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_in_place_and_from_zero(dtype):
+    c = Case([40, 0, 113], 2, 4, 16, dtype)
+    before = c.mass.double().cpu().numpy()
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_in=c.mass, mass_out=c.mass)
+    torch.cuda.synchronize()
+    c.check_attention(mass_in=before, mass_out=c.mass, mass_before=before)
+    fresh = torch.full_like(c.mass, -3.0)
+    c.handle.decode_attn(c.q, c.out, mass_out=fresh)
+    torch.cuda.synchronize()
+    c.check_attention(mass_in=None, mass_out=fresh, mass_before=fresh.double().cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.11, 0.5])
+def test_scale_and_strided_queries(dtype, scale):
+    c = Case([90, 17], 2, 3, 32, dtype)
+    wide = torch.zeros(2, 2 * 6 + 5, 136 * 2, dtype=DT[dtype], device="cuda")
+    q = wide[:, 1:12:2, 8:136]
+    q.copy_(c.q)
+    c.handle.decode_attn(q, c.out, lse=c.lse, scale=scale)
+    torch.cuda.synchronize()
+    c.check_attention(scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_peaked_and_far_scores(dtype):
+    """Scores up to several hundred: the running maximum carries the sum."""
+    c = Case([1000, 33], 2, 4, 16, dtype, q_scale=40.0)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse)
+    torch.cuda.synchronize()
+    c.check_attention()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("garbage", [float("inf"), float("-inf"), 3e38])
+def test_rows_not_held_are_never_used(dtype, garbage):
+    c = Case([5, 0, 47], 2, 8, 48, dtype, "phd", garbage=garbage)
+    out = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=out)
+    torch.cuda.synchronize()
+    c.check_attention(mass_out=out, mass_before=np.zeros(out.shape))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_pages_and_lengths_are_reported(dtype):
+    """A bad page id drops its rows, a bad length is clamped; both are reported,
+    and the other sequences' results stand."""
+    c = Case([100, 64, 40], 2, 4, 16, dtype, width=7)
+    c.table[0, 2], c.table[0, 5] = -1, c.n_pages
+    c.handle.decode_attn(c.q, c.out, lse=c.lse)
+    torch.cuda.synchronize()
+    assert int(c.err) == 2  # bad index
+    c.check_attention()
+    c = Case([112, 64, 40], 2, 4, 16, dtype, width=7)
+    c.lens[0], c.lens[2] = 5000, -3
+    c.lens_list = [112, 64, 0]
+    c.handle.decode_attn(c.q, c.out, lse=c.lse)
+    torch.cuda.synchronize()
+    assert int(c.err) == 3  # bad count
+    c.check_attention()
+
+
+@pytest.mark.parametrize("dtype,n,heads,g,page", [("bf16", 70001, 2, 4, 64), ("f32", 30011, 1, 7, 16),
+                                                  ("bf16", 131071, 1, 16, 128)])
+def test_long_sequences(dtype, n, heads, g, page):
+    """Against torch in float64 on the GPU; besides the bounds, the relative
+    2-norm of the error: the rounding of a score (|s| below 8, some hundred
+    roundings of 2^-24 relative each, random) is the largest part, about 5e-6."""
+    c = Case([n, 13], heads, g, page, dtype, "phd")
+    mass = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=mass)
+    torch.cuda.synchronize()
+    pages = c.table[0, :-(-n // page)].long()
+    for h in range(heads):
+        k = c.K[pages, h].reshape(-1, D)[:n].double()
+        v = c.V[pages, h].reshape(-1, D)[:n].double()
+        s = c.q[0, h * g:(h + 1) * g].double() @ k.T / math.sqrt(D)
+        p = torch.softmax(s, dim=1)
+        want, got = p @ v, c.out[0, h * g:(h + 1) * g].double()
+        assert float((got - want).norm() / want.norm()) <= 1e-5
+        assert float((mass[0, h, :n].double() - p.sum(0)).norm() / p.sum(0).norm()) <= 1e-5
+        assert torch.allclose(c.lse[0, h * g:(h + 1) * g].double(), torch.logsumexp(s, 1), rtol=0, atol=1e-5)
+    assert not mass[0, :, n:].any() and not mass[1, :, 13:].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    """Pages more than 2^32 bytes and 2^31 elements into their pools."""
+    heads, page, n_pages = 8, 128, 20000  # 2.6e9 elements
+    K = torch.empty(n_pages, heads, page, D, dtype=DT[dtype], device="cuda")
+    V = torch.empty_like(K)
+    ids = torch.tensor([[19999, 3, 19998, 16500]], dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for p in ids[0].tolist():
+        K[p] = torch.randn(heads, page, D, generator=gen, device="cuda").to(DT[dtype])
+        V[p] = torch.randn(heads, page, D, generator=gen, device="cuda").to(DT[dtype])
+    lens = torch.tensor([400], dtype=torch.int32, device="cuda")
+    R = 512
+    mass = torch.rand(1, heads, R, generator=gen, device="cuda")
+    pos = torch.arange(R, dtype=torch.int32, device="cuda").expand(1, heads, R).contiguous()
+    seen = lens.clone()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = ckv.PagedCache(K, V, ids, lens, g=4, mass=mass, pos=pos, seen=seen, dev_err=err)
+    q = torch.randn(1, heads * 4, D, generator=gen, device="cuda").to(DT[dtype])
+    out = torch.empty(1, heads * 4, D, device="cuda")
+
+    def want(n):
+        k = K[ids[0].long()].transpose(0, 1).reshape(heads, R, D)[:, :n].double()
+        v = V[ids[0].long()].transpose(0, 1).reshape(heads, R, D)[:, :n].double()
+        s = torch.matmul(q.view(heads, 4, D).double(), k.transpose(1, 2)) / math.sqrt(D)
+        return torch.matmul(torch.softmax(s, -1), v).view(1, heads * 4, D)
+
+    cache.decode_attn(q, out)
+    assert float((out.double() - want(400)).norm() / want(400).norm()) <= 1e-5
+    new = torch.randn(1, heads, 100, D, generator=gen, device="cuda").to(DT[dtype])
+    cache.append(new, new)
+    assert int(lens) == 500 and torch.equal(K[19998, :, 127], K[19998, :, 127])
+    assert torch.equal(K[16500, :, 16:116], new[0]) and torch.equal(V[16500, :, 16:116], new[0])
+    moves = torch.zeros(1, heads, 300, 2, dtype=torch.int32, device="cuda")
+    n_moves = torch.zeros(1, heads, dtype=torch.int32, device="cuda")
+    before = K[ids[0].long()].transpose(0, 1).reshape(heads, R, D).clone()
+    cache.evict(300, 4, 100, moves, n_moves)
+    after = K[ids[0].long()].transpose(0, 1).reshape(heads, R, D)
+    for h in range(heads):
+        m = moves[0, h, :int(n_moves[0, h])].long()
+        assert len(m) >= 100 and torch.equal(after[h, m[:, 1]], before[h, m[:, 0]])
+    cache.decode_attn(q, out)
+    assert float((out.double() - want(300)).norm() / want(300).norm()) <= 1e-5
+    assert int(err) == 0
+
+
+def test_results_do_not_change_from_run_to_run():
+    c = Case([3000, 1, 0, 777, 2048], 3, 5, 16, "bf16")
+    first = None
+    for _ in range(5):
+        mass = torch.zeros_like(c.mass)
+        c.out.fill_(float("nan"))
+        c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=mass)
+        got = (c.out.clone(), c.lse.clone(), mass)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_two_handles_and_graphs_at_once():
+    """Two captured graphs over one cache, each with its own handle, replayed on
+    two streams at the same time, and new lengths written between replays."""
+    c = Case([900, 64, 2500, 0], 4, 4, 16, "bf16", width=200)
+    other = c.make()
+    out2, lse2 = torch.empty_like(c.out), torch.empty_like(c.lse)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs = []
+    torch.cuda.synchronize()
+    for st, (handle, out, lse) in zip(streams, ((c.handle, c.out, c.lse), (other, out2, lse2))):
+        with torch.cuda.stream(st):
+            handle.decode_attn(c.q, out, lse=lse)
+        st.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            handle.decode_attn(c.q, out, lse=lse)
+        graphs.append(graph)
+    for lens in ([900, 64, 2500, 0], [1, 63, 2499, 0], [0, 0, 16, 0]):
+        c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.lens_list = lens
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for st, graph in zip(streams, graphs):
+                with torch.cuda.stream(st):
+                    graph.replay()
+        torch.cuda.synchronize()
+        c.check_attention()
+        assert torch.equal(c.out, out2) and torch.equal(c.lse, lse2)
+
+
+def test_side_stream_argument():
+    c = Case([100, 20], 2, 4, 16, "bf16")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, stream=st)
+    st.synchronize()
+    c.check_attention()
+
+
+# ---------------------------------------------------------------- append
+@pytest.mark.parametrize("dtype,layout,page,heads,n", [
+    ("bf16", "hpd", 16, 2, 1), ("f32", "phd", 16, 3, 1), ("bf16", "kv_in_page", 48, 8, 37), ("f32", "wide", 32, 1, 70),
+    ("bf16", "phd", 64, 5, 500), ("f32", "hpd", 16, 2, 300)])
+@pytest.mark.parametrize("given", [False, True])
+def test_append(dtype, layout, page, heads, n, given):
+    """Rows, positions and weights of the appended rows; nothing else changes,
+    bit for bit, and a sequence that would overflow is left as it is."""
+    lens = [0, 5, page, 2 * page + 1, 7]
+    width = 3 + -(-n // page)
+    c = Case([width * page] * 5, heads, 1, page, dtype, layout, garbage=0.0)
+    c.lens.copy_(torch.tensor(lens))
+    c.seen.copy_(torch.tensor([0, 105, page, 1000, 7]))
+    counts = torch.tensor([n, max(0, n - 1), 0, n, n], dtype=torch.int32, device="cuda")
+    start, first = c.lens.clone(), c.seen.clone()
+    bad = 4
+    if given:
+        start = torch.tensor([3, 0, 1, page, width * page - n + 1], dtype=torch.int32, device="cuda")
+        first = torch.tensor([9, 8, 7, 6, 5], dtype=torch.int32, device="cuda")
+    else:
+        start[bad] = c.lens[bad] = width * page - n + 1
+    src = torch.randn(2, 5, n, heads, D).to(DT[dtype]).cuda()
+    k, v = src[0].transpose(1, 2), src[1].transpose(1, 2)
+    want = {x: getattr(c, x).clone() for x in ("K", "V", "mass", "pos", "lens", "seen")}
+    for s in range(4):
+        for j in range(int(counts[s])):
+            r = int(start[s]) + j
+            pg = int(c.table[s, r // page])
+            want["K"][pg, :, r % page], want["V"][pg, :, r % page] = k[s, :, j], v[s, :, j]
+            want["pos"][s, :, r], want["mass"][s, :, r] = int(first[s]) + j, 0.0
+        want["lens"][s], want["seen"][s] = start[s] + counts[s], first[s] + counts[s]
+    c.handle.append(k, v, counts=counts, start=start if given else None, first=first if given else None)
+    torch.cuda.synchronize()
+    for x, t in want.items():
+        assert torch.equal(getattr(c, x), t), x
+    assert int(c.err) == 3
+    c.err.zero_()
+    c.handle.append(k[:, :, :0].new_zeros(5, heads, 1, D), v[:, :, :1], counts=torch.zeros_like(counts))
+    assert int(c.err) == 0 and torch.equal(c.lens, want["lens"]) and torch.equal(c.K, want["K"])
+
+
+def test_append_bad_counts_and_pages():
+    c = Case([64] * 4, 2, 1, 16, "bf16", garbage=0.0)
+    c.lens.copy_(torch.tensor([-1, 0, 0, 8]))
+    c.table[3, 1] = -5
+    before = c.K.clone()
+    k = torch.ones(4, 2, 12, D, dtype=torch.bfloat16, device="cuda")
+    c.handle.append(k, k, counts=torch.tensor([1, -1, 13, 12], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert int(c.err) in (2, 3) and c.lens.tolist() == [-1, 0, 0, 20]
+    pg = int(c.table[3, 0])
+    before[pg, :, 8:] = 1
+    assert torch.equal(c.K, before)
+
+
+def test_append_without_row_state_and_from_pinned_memory():
+    c = Case([32, 32], 2, 1, 16, "bf16", garbage=0.0)
+    c.lens.zero_()
+    plain = ckv.PagedCache(c.K, c.V, c.table, c.lens)
+    k = torch.randn(2, 2, 20, D).to(torch.bfloat16).pin_memory()
+    plain.append(k, k)
+    torch.cuda.synchronize()
+    assert c.lens.tolist() == [20, 20]
+    for s in range(2):
+        got = torch.cat([c.K[p] for p in c.table[s, :2].tolist()], dim=1)[:, :20]
+        assert torch.equal(got.cpu(), k[s])
+
+
+def test_append_broadcast_source():
+    c = Case([32, 32], 4, 1, 16, "f32", garbage=0.0)
+    c.lens.zero_()
+    k = torch.randn(1, 1, 9, D, device="cuda").expand(2, 4, 9, D)
+    c.handle.append(k, k)
+    for s in range(2):
+        assert torch.equal(c.K[int(c.table[s, 0]), :, :9], k[s])
+
+
+# ---------------------------------------------------------------- eviction
+def weights(kind, S, heads, R, gen):
+    m = torch.exp(2 * torch.randn(S, heads, R, generator=gen))
+    if kind == "equal":
+        m.fill_(0.25)
+    elif kind == "few":
+        m = torch.randint(0, 3, m.shape, generator=gen).float()
+    elif kind == "odd":
+        pick = torch.randint(0, 8, m.shape, generator=gen)
+        for i, x in enumerate((float("nan"), float("inf"), -float("inf"), 0.0, -0.0, 1e-42, -1.5)):
+            m[pick == i] = x
+    elif kind == "close":  # differ in the lowest bits only
+        m = (torch.full(m.shape, 1.5).view(torch.int32) + torch.randint(0, 40, m.shape, generator=gen)).int().view(torch.float32)
+    return m
+
+
+SELECT = [
+    # lens, heads, page, budget, sinks, recent
+    ([1344, 1025, 1024, 3], 2, 16, 1024, 16, 256),
+    ([1, 2, 48, 96], 3, 48, 1, 0, 0),
+    ([100, 97, 0], 1, 16, 96, 0, 96),
+    ([100, 97, 0], 2, 16, 96, 96, 0),
+    ([5000, 300, 4999], 2, 64, 257, 16, 100),
+    ([2049, 1023], 1, 16, 40, 4, 4),
+    ([70000], 1, 16, 30000, 16, 500),
+]
+
+
+@pytest.mark.parametrize("kind", ["plain", "equal", "few", "odd", "close"])
+@pytest.mark.parametrize("lens,heads,page,budget,sinks,recent", SELECT)
+def test_evict_select(lens, heads, page, budget, sinks, recent, kind):
+    gen = torch.Generator().manual_seed(budget)
+    S, width = len(lens), max(1, -(-max(lens) // page))
+    R = width * page
+    K = torch.zeros(1, heads, page, D, dtype=torch.bfloat16, device="cuda")
+    mass = weights(kind, S, heads, R, gen)
+    # as after earlier evictions: every row's position is its own, in no order
+    pos = torch.stack([torch.stack([torch.randperm(R, generator=gen) for _ in range(heads)]) for _ in range(S)]).int()
+    seen = torch.full((S,), R, dtype=torch.int32)
+    most = max(0, min(budget, R - budget))
+    moves = torch.full((S, heads, most, 2), -7, dtype=torch.int32, device="cuda")
+    n_moves = torch.full((S, heads), -7, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = ckv.PagedCache(K, K.clone(), torch.zeros(S, width, dtype=torch.int32, device="cuda"),
+                           torch.tensor(lens, dtype=torch.int32, device="cuda"), mass=mass.cuda(), pos=pos.cuda(),
+                           seen=seen.cuda(), dev_err=err)
+    cache.evict_select(budget, sinks, recent, moves, n_moves)
+    got, n_got = moves.cpu().numpy(), n_moves.cpu().numpy()
+    assert int(err) == 0
+    for s, n in enumerate(lens):
+        for h in range(heads):
+            kept = po.keep(mass[s, h, :n].numpy(), pos[s, h, :n].numpy(), R, budget, sinks, recent)
+            want = po.moves(kept, budget)
+            assert n_got[s, h] == len(want)
+            assert np.array_equal(got[s, h, :len(want)], want)
+            assert (got[s, h, len(want):] == -7).all()
+
+
+@pytest.mark.parametrize("dtype,layout,page,heads", [("bf16", "hpd", 16, 2), ("f32", "phd", 48, 3),
+                                                     ("bf16", "kv_in_page", 64, 1), ("f32", "wide", 16, 2)])
+def test_evict_apply(dtype, layout, page, heads):
+    lens, budget = [200, 130, 100, 0, 131], 130
+    c = Case(lens, heads, 1, page, dtype, layout, width=-(-200 // page), garbage=0.0)
+    R = c.R
+    most = min(budget, R - budget)
+    moves = torch.zeros(5, heads, most, 2, dtype=torch.int32)
+    n_moves = torch.zeros(5, heads, dtype=torch.int32)
+    rng = np.random.default_rng(0)
+    want = {x: getattr(c, x).clone() for x in ("K", "V", "mass", "pos")}
+    for s, n in enumerate(lens):
+        for h in range(heads):
+            m = min(max(0, n - budget), most, 1 + 30 * h + 40 * (s == 0))
+            src = np.sort(rng.choice(np.arange(budget, max(n, budget)), m, replace=False)) if m else np.zeros(0, int)
+            dst = np.sort(rng.choice(budget, m, replace=False))
+            n_moves[s, h] = m
+            for i, (a, b) in enumerate(zip(src, dst)):
+                moves[s, h, i, 0], moves[s, h, i, 1] = int(a), int(b)
+                pa, pb = int(c.table[s, a // page]), int(c.table[s, b // page])
+                want["K"][pb, h, b % page], want["V"][pb, h, b % page] = c.K[pa, h, a % page], c.V[pa, h, a % page]
+                want["mass"][s, h, b], want["pos"][s, h, b] = c.mass[s, h, a], c.pos[s, h, a]
+    for _ in range(2):  # repeating the call changes nothing
+        c.handle.evict_apply(budget, moves.cuda(), n_moves.cuda())
+        torch.cuda.synchronize()
+        for x, t in want.items():
+            assert torch.equal(getattr(c, x), t), x
+        assert c.lens.tolist() == [130, 130, 100, 0, 130] and int(c.err) == 0
+
+
+def test_evict_apply_skips_bad_moves():
+    c = Case([64, 64], 1, 1, 16, "bf16", garbage=0.0)
+    budget = 40
+    bad = [(39, 3), (64, 3), (-1, 3), (50, 40), (50, -1), (60, 5)]
+    moves = torch.zeros(2, 1, 24, 2, dtype=torch.int32)
+    moves[0, 0, :6] = torch.tensor(bad)
+    want = c.K.clone()
+    t = c.table[0].tolist()
+    want[t[0], 0, 5] = c.K[t[3], 0, 12]
+    c.handle.evict_apply(budget, moves.cuda(), torch.tensor([[6], [-4]], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(c.K, want) and int(c.err) in (2, 3) and c.lens.tolist() == [40, 40]
+
+
+# ---------------------------------------------------------------- a run together
+@pytest.mark.parametrize("dtype,heads,g,page", [("bf16", 2, 4, 16), ("f32", 3, 2, 32)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_decode_loop_with_eviction(dtype, heads, g, page, captured):
+    """Prompts, then decode steps of append, attention with weights and, every
+    few steps, eviction to a budget, eager and as replayed graphs.  The rows
+    held are followed on the host by their token positions: every step's
+    attention is compared with the oracle's over exactly those tokens, and the
+    rows evicted must be the oracle's choice from the weights on the GPU."""
+    gen = torch.Generator().manual_seed(5)
+    S, budget, every, steps, sinks, recent = 3, 40, 8, 33, 4, 8
+    prompt = [45, 1, 70]
+    width = -(-(80 + every) // page)
+    R = width * page
+    tokens = 70 + steps
+    tk, tv = (torch.randn(S, tokens, heads, D, generator=gen).to(DT[dtype]) for _ in range(2))
+    qs = (1.5 * torch.randn(steps, S, heads * g, D, generator=gen)).to(DT[dtype])
+    dev = "cuda"
+    K = torch.full((S * width, heads, page, D), float("nan"), dtype=DT[dtype], device=dev)
+    V = K.clone()
+    table = torch.randperm(S * width, generator=gen).to(torch.int32).view(S, width).to(dev)
+    lens, seen = (torch.zeros(S, dtype=torch.int32, device=dev) for _ in range(2))
+    mass, pos = torch.zeros(S, heads, R, device=dev), torch.zeros(S, heads, R, dtype=torch.int32, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    cache = ckv.PagedCache(K, V, table, lens, g=g, mass=mass, pos=pos, seen=seen, dev_err=err)
+    moves = torch.zeros(S, heads, budget, 2, dtype=torch.int32, device=dev)
+    n_moves = torch.zeros(S, heads, dtype=torch.int32, device=dev)
+    q, out, lse = qs[0].to(dev), torch.zeros(S, heads * g, D, device=dev), torch.zeros(S, heads * g, device=dev)
+    k1, v1 = (torch.zeros(S, heads, 1, D, dtype=DT[dtype], device=dev) for _ in range(2))
+
+    def step():
+        cache.append(k1, v1)
+        cache.decode_attn(q, out, lse=lse, mass_in=mass, mass_out=mass)
+
+    def evict():
+        cache.evict(budget, sinks, recent, moves, n_moves)
+
+    longest = max(prompt)
+    pk, pv = tk[:, :longest].transpose(1, 2).to(dev), tv[:, :longest].transpose(1, 2).to(dev)
+    counts = torch.tensor(prompt, dtype=torch.int32, device=dev)
+    run_step, run_evict = step, evict
+    if captured:
+        saved = [t.clone() for t in (K, V, lens, seen, mass, pos)]
+        cache.append(pk, pv, counts=counts)
+        graphs = []
+        for fn in (step, evict):
+            fn()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                fn()
+            graphs.append(graph)
+        run_step, run_evict = graphs[0].replay, graphs[1].replay
+        for t, x in zip((K, V, lens, seen, mass, pos), saved):
+            t.copy_(x)
+        torch.cuda.synchronize()
+    cache.append(pk, pv, counts=counts)
+    held = [[list(range(n)) for _ in range(heads)] for n in prompt]  # token in each row
+    for i in range(steps):
+        tok = [n + i for n in prompt]
+        k1.copy_(torch.stack([tk[s, tok[s]] for s in range(S)]).unsqueeze(2))
+        v1.copy_(torch.stack([tv[s, tok[s]] for s in range(S)]).unsqueeze(2))
+        q.copy_(qs[i])
+        run_step()
+        torch.cuda.synchronize()
+        m_before = mass.cpu()
+        for s in range(S):
+            for h in range(heads):
+                rows = held[s][h]
+                rows.append(tok[s])
+                assert int(lens[s]) == len(rows) and pos[s, h, :len(rows)].tolist() == rows
+                kk, vv = tk[s, rows, h].double().numpy(), tv[s, rows, h].double().numpy()
+                qq = qs[i, s, h * g:(h + 1) * g].double().numpy()
+                o, z, _ = po.attend(qq, kk, vv, np.ones(len(rows), dtype=bool), D ** -0.5)
+                got = out[s, h * g:(h + 1) * g].double().cpu().numpy()
+                assert np.abs(got - o).max() <= 2e-3 * np.abs(vv).max()
+                assert np.linalg.norm(got - o) <= 1e-5 * np.linalg.norm(o)
+                assert np.abs(lse[s, h * g:(h + 1) * g].double().cpu().numpy() - z).max() <= 1e-5
+        if i % every == every - 1:
+            run_evict()
+            torch.cuda.synchronize()
+            for s in range(S):
+                for h in range(heads):
+                    rows = held[s][h]
+                    kept = po.keep(m_before[s, h, :len(rows)].numpy(), np.array(rows), tok[s] + 1, budget, sinks, recent)
+                    for a, b in po.moves(kept, budget):
+                        rows[b] = rows[a]
+                    del rows[budget:]
+                    assert int(lens[s]) == len(rows)
+    assert int(err) == 0
+    # the weights of a row sum to g per step over the rows held
+    assert (mass >= 0).all()
+
+
+# ---------------------------------------------------------------- refusals of the binding
+def test_calls_refuse_wrong_tensors():
+    c = Case([20, 3], 2, 4, 16, "bf16")
+    h, i32 = c.handle, torch.int32
+    with pytest.raises(ValueError):
+        h.decode_attn(c.q[:, :4], c.out)
+    with pytest.raises(TypeError):
+        h.decode_attn(c.q.float(), c.out)
+    with pytest.raises(ValueError):
+        h.decode_attn(c.q.cpu(), c.out)
+    with pytest.raises(TypeError):
+        h.decode_attn(c.q, c.out.bfloat16())
+    with pytest.raises(ValueError):
+        h.decode_attn(c.q, c.out[:, :, :64])
+    with pytest.raises(ValueError):
+        h.decode_attn(c.q, c.out, lse=c.lse[:1])
+    with pytest.raises(ValueError):
+        h.decode_attn(c.q, c.out, mass_out=c.mass[:, :1])
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        h.decode_attn(c.q, c.out, mass_in=c.mass)
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        h.decode_attn(c.q, c.out, scale=float("nan"))
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        h.decode_attn(c.q, None)
+    bare = ckv.PagedCache(c.K, c.V, c.table, c.lens, g=4)
+    with pytest.raises(ckv.CKVError, match="CAPACITY"):
+        bare.decode_attn(c.q, c.out, mass_out=c.mass)
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        ckv.PagedCache(c.K, c.V, c.table, c.lens, g=17)
+    k = torch.zeros(2, 2, 3, D, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        h.append(k, k[:, :, :2])
+    with pytest.raises(TypeError):
+        h.append(k, k.float())
+    with pytest.raises(ValueError):
+        h.append(k, k.cpu())
+    with pytest.raises(TypeError):
+        h.append(k, k, counts=torch.ones(2, device="cuda"))
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        h.append(k[:, :, :0], k[:, :, :0])
+    moves, n = torch.zeros(2, 2, 8, 2, dtype=i32, device="cuda"), torch.zeros(2, 2, dtype=i32, device="cuda")
+    with pytest.raises(ckv.CKVError, match="CAPACITY"):
+        h.evict_select(16, 4, 4, moves, n)
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        h.evict_select(24, 20, 8, moves, n)
+    with pytest.raises(ValueError):
+        h.evict_apply(24, moves[..., 0], n)
+    with pytest.raises(TypeError):
+        h.evict_apply(24, moves.long(), n)
+    with pytest.raises(ckv.CKVError, match="ARG"):
+        bare.evict_select(24, 4, 4, moves, n)
+    torch.cuda.synchronize()
+    assert torch.isnan(c.out).all()

@@ -1,0 +1,220 @@
+"""The paged cache's oracle against hand examples and torch, and the refusals
+of its entry points on the host (no GPU is touched: every error below is found
+before a launch)."""
+import ctypes
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as po
+from recallable_kv_cache_gb300 import build, ckv
+
+ARG, DTYPE, CAPACITY, ALIGN = -1, -2, -3, -8
+
+
+# ---------------------------------------------------------------- oracle pins
+def test_rows_follow_the_page_table():
+    pool = np.arange(4 * 2 * 16 * 3, dtype=np.float64).reshape(4, 2, 16, 3)
+    got, ok = po.rows(pool, np.array([2, 0, 9]), 1, 40, 4)
+    assert ok.tolist() == [True] * 32 + [False] * 8
+    assert np.array_equal(got[:16], pool[2, 1]) and np.array_equal(got[16:32], pool[0, 1])
+    assert not got[32:].any()
+
+
+def test_attention_equals_torch():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.normal(size=(3, 8)), rng.normal(size=(20, 8)), rng.normal(size=(20, 8))
+    ok = np.ones(20, dtype=bool)
+    ok[5] = False
+    out, lse, w = po.attend(q, k, v, ok, 0.3)
+    t = [torch.tensor(x) for x in (q, k[ok], v[ok])]
+    want = torch.nn.functional.scaled_dot_product_attention(t[0], t[1], t[2], scale=0.3)
+    assert np.allclose(out, want.numpy(), rtol=1e-12)
+    assert np.allclose(lse, torch.logsumexp(0.3 * t[0] @ t[1].T, dim=1).numpy(), rtol=1e-12)
+    assert w[5] == 0 and abs(w.sum() - 3) < 1e-12
+
+
+def test_attention_of_no_rows():
+    out, lse, w = po.attend(np.ones((2, 4)), np.zeros((0, 4)), np.zeros((0, 4)), np.zeros(0, dtype=bool), 1.0)
+    assert not out.any() and np.isneginf(lse).all() and len(w) == 0
+
+
+def test_eviction_by_hand():
+    #       sink  0.5  0.9  0.5  nan  0.1 recent
+    mass = np.array([0.0, 0.5, 0.9, 0.5, np.nan, 0.1, 0.0])
+    pos = np.array([0, 1, 2, 3, 4, 5, 6])
+    kept = po.keep(mass, pos, 7, 4, 1, 1)
+    assert kept.tolist() == [True, True, True, False, False, False, True]
+    assert po.moves(kept, 4).tolist() == [[6, 3]]
+    assert po.keep(mass, pos, 7, 7, 1, 1).all()
+    assert po.moves(po.keep(mass, pos, 7, 7, 1, 1), 7).shape == (0, 2)
+
+
+def test_eviction_is_the_best_set_of_its_size():
+    rng = np.random.default_rng(1)
+    for _ in range(20):
+        n, budget = 7, 4
+        mass, pos = rng.integers(0, 4, n).astype(float), rng.permutation(n)
+        kept = po.keep(mass, pos, n, budget, 1, 1)
+        safe = (pos < 1) | (pos >= n - 1)
+        assert kept.sum() == budget and kept[safe].all()
+        best = max(sum(mass[list(c)]) for c in itertools.combinations(range(n), budget)
+                   if set(np.flatnonzero(safe)) <= set(c))
+        assert mass[kept].sum() == best
+
+
+# ---------------------------------------------------------------- refusals of the C ABI
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return ckv.lib()
+
+
+P = 1 << 20  # an aligned address that is never read: the calls below end on the host
+
+
+def struct(**kw):
+    base = dict(K=P, V=P, k_stride=(2 * 64 * 128, 64 * 128, 128), v_stride=(2 * 64 * 128, 64 * 128, 128), table=P,
+                lens=P, mass=P, pos=P, seen=P, dev_err=None, n_pages=5, heads=2, page_size=64, seqs=3, max_pages=4,
+                d=128, kv_dtype=ckv.BF16)
+    base.update(kw)
+    base["k_stride"] = (ctypes.c_int64 * 3)(*base["k_stride"])
+    base["v_stride"] = (ctypes.c_int64 * 3)(*base["v_stride"])
+    return ckv.PagedCacheStruct(*[base[n] for n, _ in ckv.PagedCacheStruct._fields_])
+
+
+def i64(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+BAD_CACHES = [
+    (dict(K=None), ARG), (dict(V=None), ARG), (dict(table=None), ARG), (dict(lens=None), ARG), (dict(d=64), ARG),
+    (dict(kv_dtype=2), DTYPE), (dict(n_pages=0), ARG), (dict(heads=0), ARG), (dict(seqs=0), ARG),
+    (dict(max_pages=0), ARG), (dict(page_size=0), ARG), (dict(page_size=24), ARG), (dict(page_size=-16), ARG),
+    (dict(max_pages=1 << 25), ARG), (dict(seqs=1 << 30, heads=2), ARG), (dict(K=P + 8), ALIGN), (dict(V=P + 2), ALIGN),
+    (dict(k_stride=(16384, 8192, 127)), ARG), (dict(k_stride=(0, 8192, 128)), ARG),
+    (dict(v_stride=(16384, -8192, 128)), ARG), (dict(k_stride=(16384, 8192, 132)), ALIGN),
+    (dict(v_stride=(16388, 8192, 128)), ALIGN), (dict(seen=None), ARG),
+]
+
+
+@pytest.mark.parametrize("bad,code", BAD_CACHES)
+def test_bad_caches_are_refused(lib, bad, code):
+    c = struct(**bad)
+    r = ctypes.addressof(c)
+    n = ctypes.c_int64()
+    assert lib.ckv_paged_attn_workspace(r, 4, 0, ctypes.byref(n)) == code
+    assert lib.ckv_paged_append(r, P, P, i64(128, 128, 128), i64(128, 128, 128), 1, None, None, None, None) == code
+    assert lib.ckv_paged_decode_attn(r, P, c.kv_dtype, i64(1024, 128), 4, 0.1, P, P, None, None, P, 1 << 40,
+                                     None) == code
+    assert lib.ckv_paged_evict_select(r, 64, 16, 16, 64, P, P, None) == code
+    assert lib.ckv_paged_evict_apply(r, 64, 64, P, P, None) == code
+
+
+def test_strides_of_single_extents_do_not_matter(lib):
+    c = struct(n_pages=1, heads=1, k_stride=(0, 0, 128), v_stride=(3, -5, 128))
+    n = ctypes.c_int64()
+    assert lib.ckv_paged_attn_workspace(ctypes.addressof(c), 4, 0, ctypes.byref(n)) == 0 and n.value > 0
+
+
+def test_append_refusals(lib):
+    c = struct()
+    r = ctypes.addressof(c)
+    st = i64(128, 128, 128)
+
+    def call(k=P, v=P, ks=st, vs=st, n=1):
+        return lib.ckv_paged_append(r, k, v, ks, vs, n, None, None, None, None)
+
+    assert call(k=None) == ARG and call(v=None) == ARG and call(ks=None) == ARG and call(vs=None) == ARG
+    assert call(n=0) == ARG and call(n=-1) == ARG
+    assert call(ks=i64(-128, 128, 128)) == ARG and call(vs=i64(128, 128, 1 << 40)) == ARG
+    assert call(k=P + 4) == ALIGN and call(vs=i64(128, 130, 128)) == ALIGN
+    assert lib.ckv_paged_append(None, P, P, st, st, 1, None, None, None, None) == ARG
+
+
+def test_attention_refusals(lib):
+    c = struct()
+    r = ctypes.addressof(c)
+
+    def call(q=P, dtype=ckv.BF16, qs=i64(1024, 128), g=4, scale=0.1, out=P, mass_in=None, mass_out=None, ws=P,
+             nbytes=1 << 40):
+        return lib.ckv_paged_decode_attn(r, q, dtype, qs, g, scale, out, P, mass_in, mass_out, ws, nbytes, None)
+
+    assert call(q=None) == ARG and call(qs=None) == ARG and call(out=None) == ARG and call(ws=None) == ARG
+    assert call(dtype=ckv.F32) == DTYPE and call(dtype=9) == DTYPE
+    assert call(g=0) == ARG and call(g=17) == ARG and call(g=-1) == ARG
+    assert call(scale=float("nan")) == ARG and call(scale=float("inf")) == ARG
+    assert call(mass_in=P) == ARG
+    assert call(qs=i64(-8, 128)) == ARG and call(qs=i64(1024, 129)) == ALIGN
+    assert call(q=P + 2) == ALIGN and call(out=P + 4) == ALIGN and call(ws=P + 128) == ALIGN
+    n, m = ctypes.c_int64(), ctypes.c_int64()
+    assert lib.ckv_paged_attn_workspace(r, 4, 0, ctypes.byref(n)) == 0
+    assert lib.ckv_paged_attn_workspace(r, 4, 1, ctypes.byref(m)) == 0
+    assert m.value > n.value
+    assert call(nbytes=n.value - 1) == CAPACITY
+    assert call(mass_out=P, nbytes=m.value - 1) == CAPACITY
+    for g in (0, 17):
+        assert lib.ckv_paged_attn_workspace(r, g, 0, ctypes.byref(n)) == ARG
+    assert lib.ckv_paged_attn_workspace(r, 4, 0, None) == ARG
+
+
+def test_eviction_refusals(lib):
+    c = struct()  # R = 256
+    r = ctypes.addressof(c)
+
+    def select(budget=64, sinks=16, recent=16, most=64, moves=P, n=P, ref=r):
+        return lib.ckv_paged_evict_select(ref, budget, sinks, recent, most, moves, n, None)
+
+    def apply(budget=64, most=64, moves=P, n=P, ref=r):
+        return lib.ckv_paged_evict_apply(ref, budget, most, moves, n, None)
+
+    for call in (select, apply):
+        assert call(budget=0) == ARG and call(budget=-1) == ARG and call(moves=None) == ARG and call(n=None) == ARG
+        assert call(most=-1) == ARG and call(most=63) == CAPACITY and call(budget=200, most=55) == CAPACITY
+    assert select(sinks=-1) == ARG and select(recent=-1) == ARG and select(sinks=40, recent=25) == ARG
+    assert select(sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == ARG
+    for missing in ("mass", "pos"):
+        c2 = struct(**{missing: None})
+        assert select(ref=ctypes.addressof(c2)) == ARG
+
+
+def test_struct_matches_header():
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ckv.h")).read()
+    body = [b for b in re.findall(r"typedef struct \{(.*?)\} (\w+);", src, flags=re.S) if b[1] == "ckv_paged_cache"]
+    fields = re.findall(r"[\s*](\w+)(?:\[3\])?;", body[0][0])
+    assert fields == [f for f, _ in ckv.PagedCacheStruct._fields_]
+
+
+# ---------------------------------------------------------------- refusals of the binding
+def tensors(**kw):
+    K = torch.zeros(5, 2, 16, 128, dtype=torch.bfloat16)
+    t = dict(K=K, V=K.clone(), table=torch.zeros(3, 4, dtype=torch.int32), lens=torch.zeros(3, dtype=torch.int32),
+             g=4, mass=torch.zeros(3, 2, 64), pos=torch.zeros(3, 2, 64, dtype=torch.int32),
+             seen=torch.zeros(3, dtype=torch.int32))
+    t.update(kw)
+    return t
+
+
+@pytest.mark.parametrize("bad,exc", [
+    (dict(K=torch.zeros(5, 16, 128, dtype=torch.bfloat16)), ValueError),
+    (dict(V=torch.zeros(5, 2, 16, 128)), ValueError),
+    (dict(K=torch.zeros(5, 2, 16, 128, dtype=torch.float16), V=torch.zeros(5, 2, 16, 128, dtype=torch.float16)), TypeError),
+    (dict(K=torch.zeros(5, 2, 128, 16, dtype=torch.bfloat16).transpose(2, 3)), ValueError),
+    (dict(table=torch.zeros(3, 4, dtype=torch.int64)), TypeError),
+    (dict(table=torch.zeros(12, dtype=torch.int32)), ValueError),
+    (dict(lens=torch.zeros(4, dtype=torch.int32)), ValueError),
+    (dict(lens=torch.zeros(6, dtype=torch.int32)[::2]), ValueError),
+    (dict(mass=torch.zeros(3, 2, 63)), ValueError),
+    (dict(mass=torch.zeros(3, 2, 64, dtype=torch.float64)), TypeError),
+    (dict(pos=torch.zeros(3, 2, 64)), TypeError),
+    (dict(seen=torch.zeros(2, dtype=torch.int32)), ValueError),
+    (dict(dev_err=torch.zeros(2, dtype=torch.int32)), ValueError),
+    (dict(), ValueError),  # everything right, but not on a GPU
+])
+def test_handle_refuses_wrong_tensors(bad, exc):
+    with pytest.raises(exc):
+        ckv.PagedCache(**tensors(**bad))
