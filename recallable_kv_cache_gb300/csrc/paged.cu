@@ -30,7 +30,7 @@ namespace {
 bool strides_ok(const int64_t* st, const int32_t* extent, int n, int elem, long long* out) {
     for (int i = 0; i < n; ++i) {
         long long b = (long long)st[i];
-        if (extent[i] > 1 && (b < D || b > (1LL << 38))) return false;
+        if (extent[i] > 1 && (b < D || b > MAX_STRIDE)) return false;
         if (extent[i] <= 1) b = D;  // never multiplied by more than 0
         out[i] = b * elem;
     }
@@ -335,8 +335,8 @@ extern "C" ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void*
     const int elem = cache->kv_dtype == CKV_BF16 ? 2 : 4;
     for (int i = 0; i < 3; ++i) {
         // sources are only read: a stride of 0 (one row for all) is allowed
-        if (k_src_stride[i] < 0 || v_src_stride[i] < 0 || k_src_stride[i] > (1LL << 38) ||
-            v_src_stride[i] > (1LL << 38))
+        if (k_src_stride[i] < 0 || v_src_stride[i] < 0 || k_src_stride[i] > MAX_STRIDE ||
+            v_src_stride[i] > MAX_STRIDE)
             return CKV_ERR_ARG;
         a.kst[i] = k_src_stride[i] * elem;
         a.vst[i] = v_src_stride[i] * elem;

@@ -11,6 +11,7 @@ namespace paged {
 constexpr int TILE = 16;         // pages are multiples of this many rows
 constexpr int MAX_G = 16;        // query heads per KV head
 constexpr int MAX_DEVICES = 64;
+constexpr long long MAX_STRIDE = 1LL << 37;  // elements; a tensor map's strides stay below 2^40 bytes
 
 // What the kernels take of a ckv_paged_cache.
 struct Cache {

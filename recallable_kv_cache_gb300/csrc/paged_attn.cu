@@ -3,15 +3,30 @@
 //   s_jr = scale q_j . K_r,  lse_j = ln sum_r e^{s_jr},  o_j = sum_r e^{s_jr - lse_j} V_r
 //
 // for the g query heads j that share a KV head, over its rows r < lens[s].
-// The rows are cut into blocks of SPLIT; a CTA computes one block's maximum,
-// sum and weighted V (and, where the accumulated weights are wanted, leaves
-// the scores in the workspace); the join merges the blocks of a (sequence, KV
-// head) and a last kernel adds e^{s - lse} to the accumulated weights.
+//
+// Every held row is read once for all g heads, so the call is bound by HBM:
+// 512 bytes a row (bf16) for 4 g 128 operations.  The rows of every (sequence,
+// KV head), a unit, are cut into tiles; all tiles of the call, unit after
+// unit, are dealt out evenly to the warps of a persistent grid (lens lives on
+// the device, so every CTA derives the deal from it by a scan).  A warp streams
+// its tiles through a ring of its own: one tensor-map copy (TMA) for the K
+// rows of a tile and one for the V rows, a stage's mbarrier telling when both
+// have landed; it keeps the running maximum and sum of the softmax and the
+// unnormalised output in registers.  A tile never crosses a page (pages are
+// multiples of 16 rows).  Where a unit ends inside the warp's share its result
+// is final; the parts of a unit that several warps share are merged in tile
+// order, first inside the CTA, then (paged_finish_kernel) across CTAs, so the
+// result does not depend on timing.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "mma_sync.cuh"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -19,10 +34,20 @@ namespace ckv {
 namespace paged {
 namespace {
 
+using namespace mmas;
+
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int SPLIT = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr int STAGE = 8192;  // K rows, then V rows of one tile
+
+// where a CTA's share of the tiles begins: left for the finish kernel
+struct Begin {
+    long long total;  // tiles of the call
+    int n_cta;        // CTAs that share them
+    int s, h, k, nt;  // the first tile: sequence, KV head, tile in the unit, tiles of the unit
+    int pad;
+};
 
 struct AttnArgs {
     Cache c;
@@ -34,157 +59,810 @@ struct AttnArgs {
     float* lse;
     const float* mass_in;
     float* mass_out;
-    float* part;    // [units][splits][g][D + 2]
+    Begin* begin;   // [grid + 1]
+    float* part;    // [grid][2] partials of units that several CTAs share
+    float* head;    // [grid][warps] partials of a unit that a warp entered part-way and left
+    float* lse2;    // [units][g], base 2
     float* scores;  // [units][g][rows], base 2
-    float* lse2;    // [units][g]
-    int splits;
+    long long wait_limit;
 };
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&f)[4]);
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(w.x << 16);
-    f[1] = __uint_as_float(w.x & 0xffff0000u);
-    f[2] = __uint_as_float(w.y << 16);
-    f[3] = __uint_as_float(w.y & 0xffff0000u);
+// A partial: O [g][D], then the maxima [g], then the sums [g]; a multiple of
+// 16 bytes, as O is read and written 16 bytes at a time.
+__host__ __device__ __forceinline__ size_t part_floats(int g) { return ((size_t)g * (D + 2) + 3) / 4 * 4; }
+
+// ---------------------------------------------------------------- the deal
+template <int TR>
+__device__ __forceinline__ int tiles_of(const Cache& c, int s) {
+    return (rows_held(c, s) + TR - 1) / TR;
 }
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x;
-    f[1] = v.y;
-    f[2] = v.z;
-    f[3] = v.w;
+struct Pos {
+    int s, h, k, nt;  // nt = 0: past the last tile
+};
+// l tiles further on
+template <int TR>
+__device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
+    p.k += l;
+    while (p.nt && p.k >= p.nt) {
+        p.k -= p.nt;
+        if (++p.h == c.heads) {
+            p.h = 0;
+            do {
+                ++p.s;
+                p.nt = p.s < c.seqs ? tiles_of<TR>(c, p.s) : 0;
+            } while (p.nt == 0 && p.s < c.seqs);
+        }
+    }
+    return p;
+}
+// Exclusive prefix sums of the sequences' tiles, one per thread's chunk of
+// sequences; returns the total.
+template <int TR, int NT>
+__device__ long long scan_tiles(const Cache& c, long long* pre) {
+    __shared__ long long warp_sum[NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (c.seqs + NT - 1) / NT;
+    long long v = 0;
+    for (int s = tid * chunk; s < min(c.seqs, (tid + 1) * chunk); ++s) v += tiles_of<TR>(c, s);
+    v *= c.heads;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) base += warp_sum[w];
+        total += warp_sum[w];
+    }
+    pre[tid] = base + x - v;
+    __syncthreads();
+    return total;
+}
+// the place of tile t < total
+template <int TR, int NT>
+__device__ Pos locate(const Cache& c, const long long* pre, long long t) {
+    const int chunk = (c.seqs + NT - 1) / NT;
+    int lo = 0, hi = NT;  // pre[lo] <= t; the last such one holds t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pre[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    long long left = t - pre[lo];
+    Pos p{lo * chunk, 0, 0, 0};
+    for (; p.s < c.seqs; ++p.s) {
+        p.nt = tiles_of<TR>(c, p.s);
+        if (left < (long long)p.nt * c.heads) break;
+        left -= (long long)p.nt * c.heads;
+    }
+    if (p.s >= c.seqs) return Pos{c.seqs, 0, 0, 0};
+    p.h = (int)(left / p.nt);
+    p.k = (int)(left % p.nt);
+    return p;
+}
+// A warp gets at least this many tiles before the work is spread over more
+// CTAs.
+constexpr int MIN_TILES = 2;
+__device__ __forceinline__ int ctas_used(long long total, int warps, int grid) {
+    const long long n = (total + warps * MIN_TILES - 1) / (warps * MIN_TILES);
+    return n < 1 ? 1 : (n > grid ? grid : (int)n);
+}
+__device__ __forceinline__ long long share_begin(long long total, int parts, int i) { return total * i / parts; }
+// the CTA whose share holds tile t
+__device__ __forceinline__ int cta_of(long long total, int n, long long t) { return (int)(((t + 1) * n - 1) / total); }
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(ptx::smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(ptx::smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(ptx::smem_u32(bar))
+        : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(D) paged_attn_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ float sc[MAX_G][SPLIT];
-    ptx::grid_dependency_wait();
-    ptx::allow_dependent_launch();
-    const int u = blockIdx.x / a.splits, b = blockIdx.x % a.splits;
-    const int s = u / a.c.heads, h = u % a.c.heads;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (h == 0 && b == 0 && tid == 0) check_len(a.c, s);
-    const int len = rows_held(a.c, s), r0 = b * SPLIT;
-    if (r0 >= len) return;
-    const int n = min(SPLIT, len - r0);
-    for (int j = 0; j < a.g; ++j) {
-        float q[4];
-        load4(static_cast<const T*>(a.q) + s * a.qst[0] + (h * a.g + j) * a.qst[1] + 4 * lane, q);
-        for (int i = warp; i < n; i += 4) {
-            const int r = r0 + i, pg = page_of(a.c, s, r);
-            float x = -INFINITY;
-            if (pg >= 0) {
-                float k[4];
-                load4(reinterpret_cast<const T*>(a.c.K + pg * a.c.ks[0] + h * a.c.ks[1] + (r % a.c.page) * a.c.ks[2]) +
-                          4 * lane, k);
-                x = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+// ---------------------------------------------------------------- bf16 tiles on the tensor cores
+// 16 rows a tile.  A tile lands as two halves of 64 channels, [half][row][128
+// bytes], 128-byte swizzled (16-byte chunk c of row r at c ^ (r & 7)), which
+// keeps ldmatrix free of bank conflicts.
+//   S[h][r] = q[h] . K[r]        m16n8k16: M = heads (NB blocks of 8), N = 8 rows
+//   O[c][h] += V[r][c] P[h][r]   M = 16 channels, N = 8 heads, K = 16 rows
+// bf16 products are exact and add up in fp32.  P is fed to the second product
+// as a sum of bf16 terms.
+template <int NB>
+struct TilesBf16 {
+    using T = __nv_bfloat16;
+    static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0;
+    uint32_t qa[8][2 * NB];
+    float o[NB][8][4];
+    float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
+
+    static __device__ __forceinline__ void load(unsigned char* dst, const CUtensorMap* tk, const CUtensorMap* tv,
+                                                int page, int h, int slot, uint64_t* bar) {
+        tma_load_5d(dst, tk, 0, slot, 0, h, page, bar);
+        tma_load_5d(dst + STAGE / 2, tv, 0, slot, 0, h, page, bar);
+    }
+    __device__ __forceinline__ void reset(const T* q, long long stride, int g, int lane) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
-                x *= a.qscale;
+        for (int b = 0; b < NB; ++b) {
+            const int j = (lane >> 2) + 8 * b;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t* qp = reinterpret_cast<const uint32_t*>(q + j * stride + 16 * ks) + (lane & 3);
+                qa[ks][b] = j < g ? qp[0] : 0u;
+                qa[ks][NB + b] = j < g ? qp[4] : 0u;
             }
-            if (lane == 0) {
-                sc[j][i] = x;
-                if (a.scores) a.scores[((size_t)u * a.g + j) * a.c.rows + r] = x;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[b][mt][e] = 0.f;
+            mrun[b] = -INFINITY;
+            lrun[b] = 0.f;
+        }
+    }
+    // n of the stage's rows are held; the others' V rows must count as zero
+    __device__ __forceinline__ void tile(unsigned char* stage, float*, int n, float qscale, int g, float* scores,
+                                         size_t rows, int lane) {
+        const uint32_t kb = ptx::smem_u32(stage), vb = kb + STAGE / 2;
+        if (n < TR) {
+            for (int i = n * 16 + lane; i < TR * 16; i += 32)
+                *reinterpret_cast<uint4*>(stage + STAGE / 2 + (i & 1) * 2048 + (i >> 4) * 128 + ((i >> 1) & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
+        float s[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int chunk = 4 * kk + (lane >> 3);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                const int row = nt * 8 + (lane & 7);
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(kb + (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), b0, b1, b2, b3);
+                mma(s[nt], qa[2 * kk][0], NB == 2 ? qa[2 * kk][NB - 1] : 0u, qa[2 * kk][NB],
+                    NB == 2 ? qa[2 * kk][2 * NB - 1] : 0u, b0, b1);
+                mma(s[nt], qa[2 * kk + 1][0], NB == 2 ? qa[2 * kk + 1][NB - 1] : 0u, qa[2 * kk + 1][NB],
+                    NB == 2 ? qa[2 * kk + 1][2 * NB - 1] : 0u, b2, b3);
             }
         }
+        const int r0 = (lane & 3) * 2;
+        uint32_t ph[NB][2], pm[NB][2];
+        float sc[NB];
+        bool grew = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = r0 + (e & 1) + 8 * (e >> 1);
+                v[e] = r < n ? s[e >> 1][2 * b + (e & 1)] * qscale : -INFINITY;
+            }
+            const int j = (lane >> 2) + 8 * b;
+            if (scores && j < g) {
+                float* sp = scores + (size_t)j * rows + r0;
+                *reinterpret_cast<float2*>(sp) = make_float2(v[0], v[1]);
+                *reinterpret_cast<float2*>(sp + 8) = make_float2(v[2], v[3]);
+            }
+            float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 1));
+            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 2));
+            const float mnew = fmaxf(mrun[b], tm);
+            const float ms = mnew == -INFINITY ? 0.f : mnew;  // -inf - -inf is avoided: ex2(-inf) = 0
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = ex2(v[e] - ms);
+            sc[b] = 1.f;
+            if (mnew != mrun[b]) {
+                sc[b] = ex2(mrun[b] - ms);
+                grew = true;
+            }
+            lrun[b] = lrun[b] * sc[b] + ((p[0] + p[1]) + (p[2] + p[3]));
+            mrun[b] = mnew;
+            // P = hi + mid, each rounded to bf16: off by at most 2^-17 of itself
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ph[b][i] = pack2(p[2 * i], p[2 * i + 1]);
+                pm[b][i] = pack2(p[2 * i] - lo_of(ph[b][i]), p[2 * i + 1] - hi_of(ph[b][i]));
+            }
+        }
+        if (__any_sync(FULL, grew)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float sc0 = __shfl_sync(FULL, sc[b], (lane & 3) * 8);
+                const float sc1 = __shfl_sync(FULL, sc[b], (lane & 3) * 8 + 4);
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    o[b][mt][0] *= sc0;
+                    o[b][mt][1] *= sc1;
+                    o[b][mt][2] *= sc0;
+                    o[b][mt][3] *= sc1;
+                }
+            }
+        }
+        const int vrow = ((lane >> 3) >> 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            const int chunk = 2 * mt + ((lane >> 3) & 1);
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4_t(vb + (chunk >> 3) * 2048 + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), a0, a1, a2, a3);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                mma(o[b][mt], a0, a1, a2, a3, ph[b][0], ph[b][1]);
+                mma(o[b][mt], a0, a1, a2, a3, pm[b][0], pm[b][1]);
+            }
+        }
+        // zeros above were written by this thread's view of shared memory: the
+        // next copy into the stage must come after them
+        if (n < TR) ptx::fence_proxy_async_smem();
+    }
+    // O[j][c] (times w_j), maxima and sums to `put(j, c, value)`, `stat(j, m, l)`
+    template <typename Put, typename Stat>
+    __device__ __forceinline__ void leave(int g, int lane, bool normalise, Put put, Stat stat) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float l = lrun[b];
+            l += __shfl_xor_sync(FULL, l, 1);
+            l += __shfl_xor_sync(FULL, l, 2);
+            const int j = (lane >> 2) + 8 * b;
+            if ((lane & 3) == 0 && j < g) stat(j, mrun[b], l);
+            const float w = !normalise ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            const float w0 = __shfl_sync(FULL, w, (lane & 3) * 8), w1 = __shfl_sync(FULL, w, (lane & 3) * 8 + 4);
+            const int j0 = (lane & 3) * 2 + 8 * b;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+                const int c = 16 * mt + (lane >> 2);
+                if (j0 < g) {
+                    put(j0, c, o[b][mt][0] * w0);
+                    put(j0, c + 8, o[b][mt][2] * w0);
+                }
+                if (j0 + 1 < g) {
+                    put(j0 + 1, c, o[b][mt][1] * w1);
+                    put(j0 + 1, c + 8, o[b][mt][3] * w1);
+                }
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------- fp32 tiles
+// 8 rows a tile, [row][512 bytes].  Scores: LPR lanes share a row (16 bytes a
+// lane at a time, so eight lanes read 128 consecutive bytes) and add up their
+// parts by shuffles; the tile's scores go through a small array in shared
+// memory, in which a lane then holds the values of one head, j = lane % GP.
+// Output: a lane owns 4 channels of every head.
+template <int GP>
+struct TilesF32 {
+    using T = float;
+    static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP;
+    static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
+    static constexpr int QV = 32 / LPR;          // float4 of a row per lane
+    static constexpr int RP = 32 / LPR;          // rows at a time
+    static constexpr int NV = (TR * GP + 31) / 32;
+    float4 qv[GP][QV];
+    float4 o[GP];
+    float mrun, lrun;
+
+    static __device__ __forceinline__ void load(unsigned char* dst, const CUtensorMap* tk, const CUtensorMap* tv,
+                                                int page, int h, int slot, uint64_t* bar) {
+        tma_load_4d(dst, tk, 0, slot, h, page, bar);
+        tma_load_4d(dst + STAGE / 2, tv, 0, slot, h, page, bar);
+    }
+    __device__ __forceinline__ void reset(const T* q, long long stride, int g, int lane) {
+#pragma unroll
+        for (int j = 0; j < GP; ++j) {
+#pragma unroll
+            for (int i = 0; i < QV; ++i)
+                qv[j][i] = j < g ? *reinterpret_cast<const float4*>(q + j * stride + 4 * ((lane % LPR) + LPR * i))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        mrun = -INFINITY;
+        lrun = 0.f;
+    }
+    __device__ __forceinline__ void tile(unsigned char* stage, float* ps, int n, float qscale, int g, float* scores,
+                                         size_t rows, int lane) {
+        const float4* K = reinterpret_cast<const float4*>(stage);
+        const float4* V = reinterpret_cast<const float4*>(stage + STAGE / 2);
+#pragma unroll
+        for (int rr = 0; rr < TR / RP; ++rr) {
+            const int row = rr * RP + lane / LPR;
+            float s[GP];
+#pragma unroll
+            for (int j = 0; j < GP; ++j) s[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < QV; ++i) {
+                const float4 k = K[row * 32 + (lane % LPR) + LPR * i];
+#pragma unroll
+                for (int j = 0; j < GP; ++j) {
+                    s[j] = fmaf(qv[j][i].x, k.x, s[j]);
+                    s[j] = fmaf(qv[j][i].y, k.y, s[j]);
+                    s[j] = fmaf(qv[j][i].z, k.z, s[j]);
+                    s[j] = fmaf(qv[j][i].w, k.w, s[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < GP; ++j) {
+#pragma unroll
+                for (int d = LPR / 2; d > 0; d >>= 1) s[j] += __shfl_xor_sync(FULL, s[j], d);
+                if (lane % LPR == j % LPR) ps[row * GP + j] = s[j];
+            }
+        }
+        __syncwarp();
+        const int j = lane % GP;
+        float v[NV], tm = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int x = lane + 32 * i, r = x / GP;
+            v[i] = x < TR * GP && r < n ? ps[x] * qscale : -INFINITY;
+            if (scores && x < TR * GP && j < g) scores[(size_t)j * rows + r] = v[i];
+            tm = fmaxf(tm, v[i]);
+        }
+#pragma unroll
+        for (int d = GP; d < 32; d <<= 1) tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, d));
+        const float mnew = fmaxf(mrun, tm), ms = mnew == -INFINITY ? 0.f : mnew;
+        const bool grew = mnew != mrun;
+        const float sc = grew ? ex2(mrun - ms) : 1.f;
+        lrun *= sc;
+        mrun = mnew;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float p = ex2(v[i] - ms);
+            lrun += p;
+            if (lane + 32 * i < TR * GP) ps[lane + 32 * i] = p;
+        }
+        if (__any_sync(FULL, grew)) {
+#pragma unroll
+            for (int jj = 0; jj < GP; ++jj) {
+                const float w = __shfl_sync(FULL, sc, jj);
+                o[jj].x *= w;
+                o[jj].y *= w;
+                o[jj].z *= w;
+                o[jj].w *= w;
+            }
+        }
+        __syncwarp();
+        for (int r = 0; r < n; ++r) {  // rows not held are not read
+            const float4 vv = V[r * 32 + lane];
+#pragma unroll
+            for (int jj = 0; jj < GP; ++jj) {
+                const float p = ps[r * GP + jj];
+                o[jj].x = fmaf(p, vv.x, o[jj].x);
+                o[jj].y = fmaf(p, vv.y, o[jj].y);
+                o[jj].z = fmaf(p, vv.z, o[jj].z);
+                o[jj].w = fmaf(p, vv.w, o[jj].w);
+            }
+        }
+    }
+    template <typename Put, typename Stat>
+    __device__ __forceinline__ void leave(int g, int lane, bool normalise, Put put, Stat stat) {
+        float l = lrun;
+#pragma unroll
+        for (int d = GP; d < 32; d <<= 1) l += __shfl_xor_sync(FULL, l, d);
+        if (lane < GP && lane < g) stat(lane, mrun, l);
+        const float w = !normalise ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll
+        for (int j = 0; j < GP; ++j) {
+            const float wj = __shfl_sync(FULL, w, j);
+            if (j < g) {
+                put(j, 4 * lane, o[j].x * wj);
+                put(j, 4 * lane + 1, o[j].y * wj);
+                put(j, 4 * lane + 2, o[j].z * wj);
+                put(j, 4 * lane + 3, o[j].w * wj);
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------- attention
+struct Seg {
+    int u, nt;    // unit (-1: none), its tiles
+    long long a;  // its first tile
+};
+
+template <typename E>
+__global__ void __launch_bounds__(E::WARPS * 32, 1)
+    paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv) {
+    constexpr int TR = E::TR, NW = E::WARPS, NST = E::NST, NT = NW * 32;
+    using T = typename E::T;
+    extern __shared__ unsigned char smem_raw[];
+    // swizzled tiles need 1024-byte alignment
+    unsigned char* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
+    __shared__ long long pre[NT];
+    __shared__ __align__(8) uint64_t full[NW][NST];
+    __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
+    __shared__ Seg segs[NW][2];     // partials left: [0] in a.head, [1] in the warp's ring
+    __shared__ float scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+        for (int i = 0; i < NST; ++i) ptx::mbar_init(&full[warp][i], 1);
+        ptx::fence_barrier_init();
+        segs[warp][0].u = segs[warp][1].u = -1;
+    }
+    ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
+    ptx::allow_dependent_launch();
+    if (blockIdx.x == 0)
+        for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
+    const long long total = scan_tiles<TR, NT>(a.c, pre);
+    const int n_cta = ctas_used(total, NW, gridDim.x);
+    // units without rows: nothing else writes their outputs
+    for (int s = blockIdx.x; s < a.c.seqs; s += gridDim.x)
+        if (rows_held(a.c, s) == 0)
+            for (long long i = threadIdx.x; i < (long long)a.c.heads * a.g * D; i += NT) {
+                const size_t o = (size_t)s * a.c.heads * a.g;
+                a.out[o * D + i] = 0.f;
+                if (a.lse && i < (long long)a.c.heads * a.g) a.lse[o + i] = -INFINITY;
+            }
+    if (threadIdx.x == 0) {
+        const long long t0 = (int)blockIdx.x < n_cta ? share_begin(total, n_cta, blockIdx.x) : total;
+        Begin b{total, n_cta, a.c.seqs, 0, 0, 0, 0};
+        if (t0 < total) {
+            const Pos p = locate<TR, NT>(a.c, pre, t0);
+            b = Begin{total, n_cta, p.s, p.h, p.k, p.nt, 0};
+        }
+        a.begin[blockIdx.x] = b;
+    }
+    if ((int)blockIdx.x >= n_cta) return;
+    const long long cta_begin = share_begin(total, n_cta, blockIdx.x);
+    const long long cta_end = share_begin(total, n_cta, blockIdx.x + 1);
+    const long long t_begin = share_begin(total, n_cta * NW, blockIdx.x * NW + warp);
+    const long long t_end = share_begin(total, n_cta * NW, blockIdx.x * NW + warp + 1);
+    unsigned char* ring = smem + (size_t)warp * NST * STAGE;
+    const size_t pf = part_floats(a.g);
+
+    if (t_begin < t_end) {
+        // ---- the producer's view: lane l knows the place of tile block + l
+        Pos base = locate<TR, NT>(a.c, pre, t_begin);
+        long long block = t_begin - 32;
+        int p_page = 0, p_slot = 0;
+        Pos p{};
+        int p_rows = 0;
+        auto next_block = [&]() {
+            block += 32;
+            const bool mine = block + lane < t_end;
+            if (mine) {
+                p = advance<TR>(a.c, base, lane);
+                const int row = p.k * TR;
+                p_rows = min(TR, rows_held(a.c, p.s) - row);
+                p_page = page_of(a.c, p.s, row);
+                p_slot = row % a.c.page;
+                if (p_page < 0) p_rows = 0;
+            }
+            if (block + 32 < t_end) {
+                const Pos last{__shfl_sync(FULL, p.s, 31), __shfl_sync(FULL, p.h, 31), __shfl_sync(FULL, p.k, 31),
+                               __shfl_sync(FULL, p.nt, 31)};
+                base = advance<TR>(a.c, last, 1);
+            }
+        };
+        auto issue = [&](int st, long long t) {
+            if (t >= t_end) return;
+            if (t >= block + 32) next_block();
+            const int l = (int)(t - block);
+            if (lane == l) {
+                meta[warp][st] = make_int4(p.s * a.c.heads + p.h, p_rows, p.k, p.nt);
+                if (p_rows > 0) {
+                    ptx::mbar_arrive_expect_tx(&full[warp][st], STAGE);
+                    E::load(ring + st * STAGE, &tk, &tv, p_page, p.h, p_slot, &full[warp][st]);
+                } else {
+                    ptx::mbar_arrive(&full[warp][st]);  // a bad page id: nothing to load
+                }
+            }
+        };
+        next_block();
+#pragma unroll
+        for (int i = 0; i < NST; ++i) issue(i, t_begin + i);
+        __syncwarp();
+
+        E e;
+        int u = -1, nt = 0;
+        long long first = 0;  // first tile of unit u
+        auto leave = [&](bool tail) {
+            if (first >= t_begin && first + nt <= t_end) {
+                // the whole unit was this warp's
+                const size_t o = (size_t)u * a.g;
+                e.leave(a.g, lane, true, [&](int j, int c, float v) { a.out[(o + j) * D + c] = v; },
+                        [&](int j, float m, float l) {
+                            const float z = l == 0.f ? -INFINITY : m + log2f(l);
+                            a.lse2[o + j] = z;
+                            if (a.lse) a.lse[o + j] = z * LN2;
+                        });
+                return;
+            }
+            float* dst = tail ? reinterpret_cast<float*>(ring) : a.head + ((size_t)blockIdx.x * NW + warp) * pf;
+            e.leave(a.g, lane, false, [&](int j, int c, float v) { dst[j * D + c] = v; },
+                    [&](int j, float m, float l) {
+                        dst[a.g * D + j] = m;
+                        dst[a.g * D + a.g + j] = l;
+                    });
+            if (lane == 0) segs[warp][tail] = Seg{u, nt, first};
+        };
+        int st = 0, parity = 0;
+        bool ok = true;
+        for (long long t = t_begin; t < t_end; ++t) {
+            if (!ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr)) {
+                ok = false;
+                break;
+            }
+            const int4 m = meta[warp][st];
+            if (m.x != u) {
+                if (u >= 0) leave(false);
+                u = m.x;
+                nt = m.w;
+                first = t - m.z;
+                const int s = u / a.c.heads, h = u % a.c.heads;
+                e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
+            }
+            if (m.y > 0)
+                e.tile(ring + st * STAGE, scratch[warp], m.y, a.qscale, a.g,
+                       a.scores ? a.scores + (size_t)u * a.g * a.c.rows + (size_t)m.z * TR : nullptr, a.c.rows, lane);
+            else if (a.scores)
+                for (int i = lane; i < TR * a.g; i += 32)
+                    a.scores[((size_t)u * a.g + i / TR) * a.c.rows + (size_t)m.z * TR + i % TR] = -INFINITY;
+            __syncwarp();
+            issue(st, t + NST);
+            __syncwarp();
+            if (++st == NST) {
+                st = 0;
+                parity ^= 1;
+            }
+        }
+        if (!ok) {
+            // a copy never landed: report, give the others in flight their time
+            if (lane == 0) report(a.c.dev_err, CKV_DEV_TIMEOUT);
+            for (int i = 1; i < NST; ++i) {
+                if (++st == NST) {
+                    st = 0;
+                    parity ^= 1;
+                }
+                ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr);
+            }
+        }
+        if (u >= 0) leave(true);
     }
     __syncthreads();
-    float* pp = a.part + ((size_t)u * a.splits + b) * a.g * (D + 2);
-    for (int j = warp; j < a.g; j += 4) {
-        float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, sc[j][i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        const float ms = m == -INFINITY ? 0.f : m;
-        for (int i = lane; i < n; i += 32) {
-            const float p = exp2f(sc[j][i] - ms);
-            sc[j][i] = p;
-            l += p;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
-        if (lane == 0) {
-            pp[j * (D + 2) + D] = m;
-            pp[j * (D + 2) + D + 1] = l;
+
+    // ---- parts of units that several warps of this CTA hold, merged in warp order
+    bool leads = false;
+    if (lane < 2 * NW) {
+        const Seg sg = segs[lane >> 1][lane & 1];
+        const long long tb = share_begin(total, n_cta * NW, blockIdx.x * NW + (lane >> 1));
+        leads = sg.u >= 0 && (sg.a >= tb || tb == cta_begin);
+    }
+    unsigned todo = __ballot_sync(FULL, leads);
+    for (int item = 0; todo; todo &= todo - 1) {
+        const int cand = __ffs(todo) - 1, w0 = cand >> 1;
+        const Seg sg = segs[w0][cand & 1];
+        const bool whole = sg.a >= cta_begin && sg.a + sg.nt <= cta_end;
+        for (int j = 0; j < a.g; ++j, ++item) {
+            if (item % NW != warp) continue;
+            float M = -INFINITY, L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int pass = 0; pass < 2; ++pass) {
+                const float ms = M == -INFINITY ? 0.f : M;
+                for (int w = w0; w < NW; ++w) {
+                    const float* src = segs[w][1].u == sg.u ? reinterpret_cast<const float*>(smem + (size_t)w * NST * STAGE)
+                                       : segs[w][0].u == sg.u ? a.head + ((size_t)blockIdx.x * NW + w) * pf
+                                                              : nullptr;
+                    if (!src) continue;
+                    const float m = src[a.g * D + j];
+                    if (pass == 0) {
+                        M = fmaxf(M, m);
+                        continue;
+                    }
+                    const float f = ex2(m - ms);
+                    const float4 v = *reinterpret_cast<const float4*>(src + j * D + 4 * lane);
+                    L += f * src[a.g * D + a.g + j];
+                    o.x += f * v.x;
+                    o.y += f * v.y;
+                    o.z += f * v.z;
+                    o.w += f * v.w;
+                }
+            }
+            if (whole) {
+                const float f = L == 0.f ? 0.f : 1.f / L;
+                const size_t at = (size_t)sg.u * a.g + j;
+                *reinterpret_cast<float4*>(a.out + at * D + 4 * lane) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                if (lane == 0) {
+                    const float z = L == 0.f ? -INFINITY : M + log2f(L);
+                    a.lse2[at] = z;
+                    if (a.lse) a.lse[at] = z * LN2;
+                }
+            } else {
+                float* dst = a.part + ((size_t)blockIdx.x * 2 + (sg.a >= cta_begin)) * pf;
+                *reinterpret_cast<float4*>(dst + j * D + 4 * lane) = o;
+                if (lane == 0) {
+                    dst[a.g * D + j] = M;
+                    dst[a.g * D + a.g + j] = L;
+                }
+            }
         }
     }
+}
+
+// ---------------------------------------------------------------- finish
+// CTA i merges its share of the outputs of the (at most two) units that it has
+// in common with other CTAs, and adds its tiles' weights to the accumulated
+// ones.
+constexpr int FIN_THREADS = 256;
+
+template <int TR>
+__global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ float z[2][MAX_G];  // base-2 lse of the first and the last unit
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Begin b = a.begin[i];
+    if (i >= b.n_cta || b.total == 0) return;
+    const long long t0 = share_begin(b.total, b.n_cta, i), t1 = share_begin(b.total, b.n_cta, i + 1);
+    const size_t pf = part_floats(a.g);
+    // the unit shared with the CTA before, and the one shared with the CTA behind
+    int us[2] = {-1, -1};
+    long long first[2] = {0, 0};
+    int nts[2] = {0, 0};
+    if (b.k > 0 || b.nt > t1 - t0) {
+        us[0] = b.s * a.c.heads + b.h;
+        first[0] = t0 - b.k;
+        nts[0] = b.nt;
+    }
+    if (i + 1 < b.n_cta) {
+        const Begin nx = a.begin[i + 1];
+        const int u = nx.s * a.c.heads + nx.h;
+        if (nx.k > 0 && u != us[0]) {
+            us[1] = u;
+            first[1] = t1 - nx.k;
+            nts[1] = nx.nt;
+        }
+    }
+    for (int x = 0; x < 2; ++x) {
+        if (us[x] < 0) continue;
+        const int c0 = cta_of(b.total, b.n_cta, first[x]), c1 = cta_of(b.total, b.n_cta, first[x] + nts[x] - 1);
+        const int parts = c1 - c0 + 1;
+        // 32 channels of a head are an item; the unit's CTAs take them in turn
+        for (int item = i - c0 + parts * warp; item < a.g * 4; item += parts * (FIN_THREADS / 32)) {
+            const int j = item >> 2, c = (item & 3) * 32 + lane;
+            float M = -INFINITY;
+            for (int q = c0 + lane; q <= c1; q += 32) M = fmaxf(M, a.part[((size_t)q * 2 + (q == c0)) * pf + a.g * D + j]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+            const float ms = M == -INFINITY ? 0.f : M;
+            float L = 0.f, o = 0.f;
+            for (int q = c0; q <= c1; ++q) {
+                const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf;
+                const float f = ex2(src[a.g * D + j] - ms);
+                L += f * src[a.g * D + a.g + j];
+                o += f * src[j * D + c];
+            }
+            const size_t at = (size_t)us[x] * a.g + j;
+            a.out[at * D + c] = L == 0.f ? 0.f : o / L;
+            if (a.lse && c == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+        }
+        if (a.mass_out) {
+            for (int j = warp; j < a.g; j += FIN_THREADS / 32) {
+                float M = -INFINITY, L = 0.f;
+                for (int q = c0 + lane; q <= c1; q += 32)
+                    M = fmaxf(M, a.part[((size_t)q * 2 + (q == c0)) * pf + a.g * D + j]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+                const float ms = M == -INFINITY ? 0.f : M;
+                for (int q = c0 + lane; q <= c1; q += 32) {
+                    const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
+                    L += ex2(src[j] - ms) * src[a.g + j];
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+                if (lane == 0) z[x][j] = L == 0.f ? -INFINITY : M + log2f(L);
+            }
+        }
+    }
+    if (!a.mass_out) return;
     __syncthreads();
-    float o[MAX_G];
-#pragma unroll
-    for (int j = 0; j < MAX_G; ++j) o[j] = 0.f;
-    for (int i = 0; i < n; ++i) {
-        const int r = r0 + i, pg = page_of(a.c, s, r);
-        if (pg < 0) continue;
-        const float v = static_cast<float>(
-            reinterpret_cast<const T*>(a.c.V + pg * a.c.vs[0] + h * a.c.vs[1] + (r % a.c.page) * a.c.vs[2])[tid]);
-#pragma unroll
-        for (int j = 0; j < MAX_G; ++j)
-            if (j < a.g) o[j] += sc[j][i] * v;
-    }
-#pragma unroll
-    for (int j = 0; j < MAX_G; ++j)
-        if (j < a.g) pp[j * (D + 2) + tid] = o[j];
-}
-
-__global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ AttnArgs a) {
-    ptx::grid_dependency_wait();
-    ptx::allow_dependent_launch();
-    const int u = blockIdx.x / a.g, j = blockIdx.x % a.g, tid = threadIdx.x;
-    const int len = rows_held(a.c, u / a.c.heads);
-    const int ns = (len + SPLIT - 1) / SPLIT;
-    const float* pp = a.part + ((size_t)u * a.splits * a.g + j) * (D + 2);
-    const size_t step = (size_t)a.g * (D + 2);
-    float m = -INFINITY;
-    for (int i = 0; i < ns; ++i) m = fmaxf(m, pp[i * step + D]);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o = 0.f;
-    for (int i = 0; i < ns; ++i) {
-        const float w = exp2f(pp[i * step + D] - ms);
-        l += w * pp[i * step + D + 1];
-        o += w * pp[i * step + tid];
-    }
-    a.out[((size_t)u * a.g + j) * D + tid] = l > 0.f ? o / l : (l == 0.f ? 0.f : l);
-    if (tid == 0) {
-        const float x = l == 0.f ? -INFINITY : ms + log2f(l);
-        if (a.lse) a.lse[(size_t)u * a.g + j] = x * LN2;
-        a.lse2[(size_t)u * a.g + j] = x;
-    }
-}
-
-__global__ void __launch_bounds__(256) paged_mass_kernel(const __grid_constant__ AttnArgs a, int blocks) {
-    ptx::grid_dependency_wait();
-    ptx::allow_dependent_launch();
-    const int u = blockIdx.x / blocks, b = blockIdx.x % blocks;
-    const int len = rows_held(a.c, u / a.c.heads);
-    for (int r = b * 256 + threadIdx.x; r < len; r += blocks * 256) {
-        float w = 0.f;
-        for (int j = 0; j < a.g; ++j) {
-            const float x = a.scores[((size_t)u * a.g + j) * a.c.rows + r], z = a.lse2[(size_t)u * a.g + j];
-            w += z == -INFINITY ? 0.f : exp2f(x - z);
+    Pos p{b.s, b.h, b.k, b.nt};
+    for (long long t = t0; t < t1 && p.nt;) {
+        const int u = p.s * a.c.heads + p.h;
+        const int n = (int)min((long long)(p.nt - p.k), t1 - t);  // tiles of this unit in the share
+        const float* zz = u == us[0] ? z[0] : (u == us[1] ? z[1] : a.lse2 + (size_t)u * a.g);
+        const int r1 = min(rows_held(a.c, p.s), (p.k + n) * TR);
+        for (int r = p.k * TR + tid; r < r1; r += FIN_THREADS) {
+            float w = 0.f;
+            for (int j = 0; j < a.g; ++j) {
+                const float lz = zz[j];
+                const float x = a.scores[((size_t)u * a.g + j) * a.c.rows + r];
+                w += lz == -INFINITY ? 0.f : ex2(x - lz);
+            }
+            const size_t o = (size_t)u * a.c.rows + r;
+            a.mass_out[o] = (a.mass_in ? a.mass_in[o] : 0.f) + w;
         }
-        const size_t o = (size_t)u * a.c.rows + r;
-        a.mass_out[o] = (a.mass_in ? a.mass_in[o] : 0.f) + w;
+        t += n;
+        p = advance<TR>(a.c, p, n);
     }
 }
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+    static std::atomic<void*> fn{nullptr};
+    void* p = fn.load(std::memory_order_relaxed);
+    if (!p) {
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+}
+
+// The pool as a tensor map whose boxes are tiles of one page and KV head: bf16
+// [page][head][half][slot][64 channels] (two halves of 128 bytes, swizzled),
+// fp32 [page][head][slot][128 channels].
+bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long long* st, bool bf16, int tile_rows) {
+    const auto enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t slot = (cuuint64_t)st[2], head = (cuuint64_t)st[1], page = (cuuint64_t)st[0];
+    const cuuint64_t dims5[5] = {64, (cuuint64_t)c.page, 2, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
+    const cuuint64_t str5[4] = {slot, 128, head, page};
+    const cuuint32_t box5[5] = {64, (cuuint32_t)tile_rows, 2, 1, 1};
+    const cuuint64_t dims4[4] = {128, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
+    const cuuint64_t str4[3] = {slot, head, page};
+    const cuuint32_t box4[4] = {128, (cuuint32_t)tile_rows, 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    const CUresult r =
+        bf16 ? enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims5, str5, box5, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)
+             : enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims4, str4, box4, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
+constexpr int MAX_WARPS = 12;
 
 struct Layout {
-    int splits;
-    size_t part, lse2, scores, total;  // byte offsets
+    size_t begin, part, head, lse2, scores, total;  // byte offsets
 };
 Layout layout_of(const Cache& c, int g, bool with_mass) {
     Layout l;
-    const size_t units = (size_t)c.seqs * c.heads;
-    l.splits = ceil_div(c.rows, SPLIT);
+    const size_t units = (size_t)c.seqs * c.heads, pf = part_floats(g) * sizeof(float);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.part = 0;
-    l.lse2 = up(units * l.splits * g * (D + 2) * sizeof(float));
+    l.begin = 0;
+    l.part = up((MAX_GRID + 1) * sizeof(Begin));
+    l.head = l.part + up(MAX_GRID * 2 * pf);
+    l.lse2 = l.head + up((size_t)MAX_GRID * MAX_WARPS * pf);
     l.scores = l.lse2 + up(units * g * sizeof(float));
     l.total = l.scores + (with_mass ? up(units * g * (size_t)c.rows * sizeof(float)) : 0);
     return l;
+}
+
+template <typename E>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int grid, int dev, cudaStream_t s) {
+    static_assert(E::WARPS <= MAX_WARPS, "workspace layout");
+    constexpr size_t smem = (size_t)E::WARPS * E::NST * STAGE + 1024;
+    static std::atomic<bool> set[MAX_DEVICES];
+    if (!set[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        set[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(E::WARPS * 32), smem, s, a, tk, tv);
+    if (e == cudaSuccess) e = launch_dependent(paged_finish_kernel<E::TR>, dim3(grid), dim3(FIN_THREADS), 0, s, a);
+    return e;
 }
 
 }  // namespace
@@ -215,10 +893,10 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     if (!q || !q_stride || !out || !workspace) return CKV_ERR_ARG;
     if (q_dtype != cache->kv_dtype) return CKV_ERR_DTYPE;
     if (g < 1 || g > MAX_G || !isfinite(scale) || (mass_in && !mass_out)) return CKV_ERR_ARG;
-    const int elem = q_dtype == CKV_BF16 ? 2 : 4;
+    const bool bf16 = q_dtype == CKV_BF16;
     for (int i = 0; i < 2; ++i) {
-        if (q_stride[i] < 0 || q_stride[i] > (1LL << 38)) return CKV_ERR_ARG;
-        if (q_stride[i] * elem & 15) return CKV_ERR_ALIGN;
+        if (q_stride[i] < 0 || q_stride[i] > MAX_STRIDE) return CKV_ERR_ARG;
+        if (q_stride[i] * (bf16 ? 2 : 4) & 15) return CKV_ERR_ALIGN;
         a.qst[i] = q_stride[i];
     }
     if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return CKV_ERR_ALIGN;
@@ -232,20 +910,27 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.lse = lse;
     a.mass_in = mass_in;
     a.mass_out = mass_out;
+    a.begin = reinterpret_cast<Begin*>(w + l.begin);
     a.part = reinterpret_cast<float*>(w + l.part);
+    a.head = reinterpret_cast<float*>(w + l.head);
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
     a.scores = mass_out ? reinterpret_cast<float*>(w + l.scores) : nullptr;
-    a.splits = l.splits;
-    const long long units = (long long)a.c.seqs * a.c.heads;
-    if (units * l.splits > 0x7fffffffLL || units * g > 0x7fffffffLL) return CKV_ERR_ARG;
+    a.wait_limit = WAIT_LIMIT;
+    int dev = 0;
+    int grid = sm_count(&dev);
+    if (grid < 1) return CKV_ERR_CUDA;
+    if (grid > MAX_GRID) grid = MAX_GRID;
+    const int tile_rows = bf16 ? TilesBf16<1>::TR : TilesF32<1>::TR;
+    CUtensorMap tk, tv;
+    if (!encode_pool(&tk, a.c, a.c.K, a.c.ks, bf16, tile_rows) || !encode_pool(&tv, a.c, a.c.V, a.c.vs, bf16, tile_rows))
+        return CKV_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    const dim3 grid((unsigned)(units * l.splits));
-    cudaError_t e = q_dtype == CKV_BF16 ? launch_dependent(paged_attn_kernel<__nv_bfloat16>, grid, dim3(D), 0, s, a)
-                                        : launch_dependent(paged_attn_kernel<float>, grid, dim3(D), 0, s, a);
-    if (e == cudaSuccess) e = launch_dependent(paged_join_kernel, dim3((unsigned)(units * g)), dim3(D), 0, s, a);
-    if (e == cudaSuccess && mass_out) {
-        const int blocks = ceil_div(a.c.rows, 4096);
-        e = launch_dependent(paged_mass_kernel, dim3((unsigned)(units * blocks)), dim3(256), 0, s, a, blocks);
-    }
+    cudaError_t e;
+    if (bf16) e = g <= 8 ? launch<TilesBf16<1>>(a, tk, tv, grid, dev, s) : launch<TilesBf16<2>>(a, tk, tv, grid, dev, s);
+    else if (g == 1) e = launch<TilesF32<1>>(a, tk, tv, grid, dev, s);
+    else if (g == 2) e = launch<TilesF32<2>>(a, tk, tv, grid, dev, s);
+    else if (g <= 4) e = launch<TilesF32<4>>(a, tk, tv, grid, dev, s);
+    else if (g <= 8) e = launch<TilesF32<8>>(a, tk, tv, grid, dev, s);
+    else e = launch<TilesF32<16>>(a, tk, tv, grid, dev, s);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;
 }
