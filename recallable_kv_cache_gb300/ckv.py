@@ -359,6 +359,9 @@ def append_kv(k_src, v_src, K, V, pos: int, n: int | None = None, stream=None):
                                ptr(V), _stream(stream)), "ckv_append_kv")
 
 
+_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+
 class PagedCache:
     """A paged K/V cache over the caller's tensors (see the paged cache section
     of ckv.h): ``K``, ``V`` [n_pages, heads, page_size, 128] bf16 or float32, any
@@ -390,105 +393,119 @@ class PagedCache:
         seqs, width = table.shape
         self.seqs, self.heads, self.g, self.rows = seqs, heads, g, width * page
         self.dtype, self._code = K.dtype, code
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._per_seq, self._per_row = (seqs,), (seqs, heads, self.rows)
+        self._q_shape, self._lse_shape = (seqs, heads * g, 128), (seqs, heads * g)
         for name, t, shape, dtype in (
-                ("V", V, tuple(K.shape), K.dtype), ("table", table, (seqs, width), torch.int32),
-                ("lens", lens, (seqs,), torch.int32), ("mass", mass, (seqs, heads, self.rows), torch.float32),
-                ("pos", pos, (seqs, heads, self.rows), torch.int32), ("seen", seen, (seqs,), torch.int32),
-                ("dev_err", dev_err, (1,), torch.int32)):
+                ("V", V, tuple(K.shape), K.dtype), ("table", table, (seqs, width), self._i32),
+                ("lens", lens, self._per_seq, self._i32), ("mass", mass, self._per_row, self._f32),
+                ("pos", pos, self._per_row, self._i32), ("seen", seen, self._per_seq, self._i32),
+                ("dev_err", dev_err, (1,), self._i32)):
             self._tensor(name, t, shape, dtype, contiguous=name != "V")
         if self.device.type != "cuda":
             raise ValueError(f"the cache must be on a CUDA device, got {self.device}")
         self.K, self.V, self.table, self.lens = K, V, table, lens
         self.mass, self.pos, self.seen, self.dev_err = mass, pos, seen, dev_err
         self._struct = PagedCacheStruct(
-            ptr(K), ptr(V), (ctypes.c_int64 * 3)(*K.stride()[:3]), (ctypes.c_int64 * 3)(*V.stride()[:3]), ptr(table),
+            ptr(K), ptr(V), _I64x3(*K.stride()[:3]), _I64x3(*V.stride()[:3]), ptr(table),
             ptr(lens), ptr(mass), ptr(pos), ptr(seen), ptr(dev_err), n_pages, heads, page, seqs, width, d, code)
         self._ref = ctypes.addressof(self._struct)
+        so = lib()
+        self._append, self._attn = so.ckv_paged_append, so.ckv_paged_decode_attn
+        self._select, self._apply = so.ckv_paged_evict_select, so.ckv_paged_evict_apply
+        self._cuda, self._current_device = torch.cuda, torch.cuda.current_device
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         need = ctypes.c_int64()
-        _check(lib().ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),
+        _check(so.ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),
                "ckv_paged_attn_workspace")
         self.workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
         self._workspace = (ptr(self.workspace), need.value)
 
     def _tensor(self, name, t, shape, dtype, contiguous=True):
-        """None is passed on (the C call says which arguments it needs)."""
+        """Address of t after the checks; None is passed on (the C call says
+        which arguments it needs)."""
         if t is None:
             return None
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape or (contiguous and not t.is_contiguous()):
+        if t.shape != shape or (contiguous and not t.is_contiguous()):
             raise ValueError(f"{name} must be {'contiguous ' if contiguous else ''}{list(shape)}, got "
                              f"{list(t.shape)} with strides {list(t.stride())}")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         return t.data_ptr()
 
-    def _call(self, name, stream, *args):
-        import torch
-        fn = getattr(lib(), name)
+    def _call(self, fn, stream, *args):
         index = self.device.index
-        if index is None or index == torch.cuda.current_device():
-            _check(fn(self._ref, *args, _stream(stream)), name)
+        # the raw handle: building a Stream object takes longer than the launch
+        stream = self._raw_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
+        if index == self._current_device():
+            status = fn(self._ref, *args, stream)
         else:
-            with torch.cuda.device(index):
-                _check(fn(self._ref, *args, _stream(stream)), name)
+            with self._cuda.device(index):
+                status = fn(self._ref, *args, stream)
+        if status:
+            raise CKVError(status, fn.__name__)
 
     def append(self, k, v, counts=None, start=None, first=None, stream=None):
         """counts[s] rows of k, v [seqs, heads, n, 128] (any strides with
         contiguous channels) to every sequence (see ckv_paged_append); k and v
         may live in pinned host memory the device maps."""
-        import torch
-        n = k.shape[2] if k.dim() == 4 else 0
-        for name, t in (("k", k), ("v", v)):
-            if tuple(t.shape) != (self.seqs, self.heads, n, 128) or t.stride(3) != 1:
-                raise ValueError(f"{name} must be [{self.seqs}, {self.heads}, n, 128] with contiguous channels, got "
-                                 f"{tuple(t.shape)}")
-            if t.dtype != self.dtype:
-                raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+        shape = k.shape
+        if len(shape) != 4 or shape[0] != self.seqs or shape[1] != self.heads or shape[3] != 128 or v.shape != shape:
+            raise ValueError(f"k and v must be [{self.seqs}, {self.heads}, n, 128], got {tuple(shape)}, "
+                             f"{tuple(v.shape)}")
+        ks, vs = k.stride(), v.stride()
+        if ks[3] != 1 or vs[3] != 1:
+            raise ValueError("the channels of k and v must be contiguous")
+        if k.dtype != self.dtype or v.dtype != self.dtype:
+            raise TypeError(f"k and v must be {self.dtype}, got {k.dtype}, {v.dtype}")
+        for t in (k, v):
             if t.device != self.device and not (t.device.type == "cpu" and t.is_pinned()):
-                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        per_seq = [self._tensor(name, t, (self.seqs,), torch.int32)
-                   for name, t in (("counts", counts), ("start", start), ("first", first))]
-        self._call("ckv_paged_append", stream, ptr(k), ptr(v), (ctypes.c_int64 * 3)(*k.stride()[:3]),
-                   (ctypes.c_int64 * 3)(*v.stride()[:3]), n, *per_seq)
+                raise ValueError(f"k and v must be on {self.device} or pinned, got {t.device}")
+        per_seq, i32 = self._per_seq, self._i32
+        self._call(self._append, stream, k.data_ptr(), v.data_ptr(), _I64x3(ks[0], ks[1], ks[2]),
+                   _I64x3(vs[0], vs[1], vs[2]), shape[2],
+                   None if counts is None else self._tensor("counts", counts, per_seq, i32),
+                   None if start is None else self._tensor("start", start, per_seq, i32),
+                   None if first is None else self._tensor("first", first, per_seq, i32))
 
     def decode_attn(self, q, out, lse=None, mass_in=None, mass_out=None, scale=None, stream=None):
         """Attention of q [seqs, heads * g, 128] over the rows held into out
         [seqs, heads * g, 128] float32 (see ckv_paged_decode_attn).  With
         ``mass_out`` (for instance the cache's own mass, given as mass_in too)
         each row's weight is added to mass_in.  scale: 1 / sqrt(128) if None."""
-        import torch
-        hq = self.heads * self.g
-        if tuple(q.shape) != (self.seqs, hq, 128) or q.stride(2) != 1:
-            raise ValueError(f"q must be [{self.seqs}, {hq}, 128] with contiguous channels, got {tuple(q.shape)}")
+        qs = q.stride()
+        if q.shape != self._q_shape or qs[2] != 1:
+            raise ValueError(f"q must be {list(self._q_shape)} with contiguous channels, got {tuple(q.shape)}")
         if q.dtype != self.dtype:
             raise TypeError(f"q must be {self.dtype}, got {q.dtype}")
         if q.device != self.device:
             raise ValueError(f"q is on {q.device}, the cache on {self.device}")
-        rows = (self.seqs, self.heads, self.rows)
-        f32 = torch.float32
-        self._call("ckv_paged_decode_attn", stream, ptr(q), self._code, (ctypes.c_int64 * 2)(q.stride(0), q.stride(1)),
-                   self.g, 128 ** -0.5 if scale is None else scale, self._tensor("out", out, (self.seqs, hq, 128), f32),
-                   self._tensor("lse", lse, (self.seqs, hq), f32), self._tensor("mass_in", mass_in, rows, f32),
-                   self._tensor("mass_out", mass_out, rows, f32), *self._workspace)
+        f32 = self._f32
+        self._call(self._attn, stream, q.data_ptr(), self._code, _I64x2(qs[0], qs[1]), self.g,
+                   128 ** -0.5 if scale is None else scale, self._tensor("out", out, self._q_shape, f32),
+                   None if lse is None else self._tensor("lse", lse, self._lse_shape, f32),
+                   None if mass_in is None else self._tensor("mass_in", mass_in, self._per_row, f32),
+                   None if mass_out is None else self._tensor("mass_out", mass_out, self._per_row, f32),
+                   *self._workspace)
 
     def _moves(self, moves, n_moves):
-        import torch
-        if moves.dim() != 4:
-            raise ValueError(f"moves must be [seqs, heads, max_moves, 2], got {tuple(moves.shape)}")
-        most = moves.shape[2]
-        return (most, self._tensor("moves", moves, (self.seqs, self.heads, most, 2), torch.int32),
-                self._tensor("n_moves", n_moves, (self.seqs, self.heads), torch.int32))
+        shape = moves.shape
+        if len(shape) != 4:
+            raise ValueError(f"moves must be [seqs, heads, max_moves, 2], got {tuple(shape)}")
+        return (shape[2], self._tensor("moves", moves, (self.seqs, self.heads, shape[2], 2), self._i32),
+                self._tensor("n_moves", n_moves, (self.seqs, self.heads), self._i32))
 
     def evict_select(self, budget: int, sinks: int, recent: int, moves, n_moves, stream=None):
         """The rows to move when every KV head keeps ``budget`` of its rows (see
         ckv_paged_evict_select): moves [seqs, heads, max_moves, 2], n_moves
         [seqs, heads] int32."""
-        self._call("ckv_paged_evict_select", stream, budget, sinks, recent, *self._moves(moves, n_moves))
+        self._call(self._select, stream, budget, sinks, recent, *self._moves(moves, n_moves))
 
     def evict_apply(self, budget: int, moves, n_moves, stream=None):
         """Carries the moves out and shortens lens (see ckv_paged_evict_apply)."""
-        self._call("ckv_paged_evict_apply", stream, budget, *self._moves(moves, n_moves))
+        self._call(self._apply, stream, budget, *self._moves(moves, n_moves))
 
     def evict(self, budget: int, sinks: int, recent: int, moves, n_moves, stream=None):
         """evict_select, then evict_apply."""

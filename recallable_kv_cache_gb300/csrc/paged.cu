@@ -56,7 +56,7 @@ ckv_status check_cache(const ckv_paged_cache* c, Cache* o) {
     const int32_t extent[3] = {c->n_pages, c->heads, c->page_size};
     if (!strides_ok(c->k_stride, extent, 3, elem, o->ks) || !strides_ok(c->v_stride, extent, 3, elem, o->vs))
         return CKV_ERR_ARG;
-    if (!aligned16(c->K) || !aligned16(c->V) || !strides_aligned(o->ks, 3) || !strides_aligned(o->vs, 3))
+    if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->mass) || !aligned16(c->pos) || !strides_aligned(o->ks, 3) || !strides_aligned(o->vs, 3))
         return CKV_ERR_ALIGN;
     if (c->pos && !c->seen) return CKV_ERR_ARG;
     o->K = static_cast<unsigned char*>(c->K);
@@ -82,6 +82,7 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // ---------------------------------------------------------------- append
 constexpr int APPEND_THREADS = 256;
+constexpr int IN_FLIGHT = 4;  // rows whose K and V pieces a thread has in flight
 
 struct AppendArgs {
     Cache c;
@@ -114,31 +115,49 @@ __device__ __forceinline__ void append_advance(const AppendArgs& a, int s, int r
 }
 
 // A copy of 16-byte pieces, VPR of them per row of 128 channels; consecutive
-// threads take consecutive pieces of a row, then the KV heads of a token.
+// threads take consecutive pieces of a row, then the KV heads of a token.  One
+// token's rows of 256 units are a matter of latency (2 us); long prompts of
+// bandwidth, for which every thread has the pieces of IN_FLIGHT rows under way.
 template <int VPR>
 __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __grid_constant__ AppendArgs a) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
+    constexpr int ROWS = APPEND_THREADS / VPR;
     const int s = blockIdx.x / a.blocks_per_seq, b = blockIdx.x % a.blocks_per_seq;
     int r0, p0;
     const int cnt = append_plan(a, s, &r0, &p0);
     const int H = a.c.heads;
     const int piece = threadIdx.x % VPR;
     const long long items = cnt < 0 ? 0 : (long long)cnt * H;
-    const long long step = (long long)a.blocks_per_seq * (APPEND_THREADS / VPR);
-    for (long long i = (long long)b * (APPEND_THREADS / VPR) + threadIdx.x / VPR; i < items; i += step) {
-        const int j = (int)(i / H), h = (int)(i % H), r = r0 + j;
-        const int pg = page_of(a.c, s, r);
-        if (pg < 0) continue;
-        const int slot = r % a.c.page;
-        const uint4 kv = *reinterpret_cast<const uint4*>(a.k_src + s * a.kst[0] + h * a.kst[1] + j * a.kst[2] + piece * 16);
-        const uint4 vv = *reinterpret_cast<const uint4*>(a.v_src + s * a.vst[0] + h * a.vst[1] + j * a.vst[2] + piece * 16);
-        *reinterpret_cast<uint4*>(a.c.K + pg * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2] + piece * 16) = kv;
-        *reinterpret_cast<uint4*>(a.c.V + pg * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2] + piece * 16) = vv;
-        if (piece == 0) {
-            const size_t o = ((size_t)s * H + h) * a.c.rows + r;
-            if (a.c.pos) a.c.pos[o] = p0 + j;
-            if (a.c.mass) a.c.mass[o] = 0.f;
+    const long long step = (long long)a.blocks_per_seq * ROWS * IN_FLIGHT;
+    for (long long i0 = (long long)b * ROWS * IN_FLIGHT + threadIdx.x / VPR; i0 < items; i0 += step) {
+        uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
+        int j[IN_FLIGHT], h[IN_FLIGHT], pg[IN_FLIGHT];
+#pragma unroll
+        for (int x = 0; x < IN_FLIGHT; ++x) {
+            const long long i = i0 + x * ROWS;
+            pg[x] = -1;
+            if (i < items) {
+                j[x] = (int)(i / H);
+                h[x] = (int)(i % H);
+                const unsigned char* k = a.k_src + s * a.kst[0] + h[x] * a.kst[1] + j[x] * a.kst[2] + piece * 16;
+                const unsigned char* v = a.v_src + s * a.vst[0] + h[x] * a.vst[1] + j[x] * a.vst[2] + piece * 16;
+                kv[x] = *reinterpret_cast<const uint4*>(k);
+                vv[x] = *reinterpret_cast<const uint4*>(v);
+                pg[x] = page_of(a.c, s, r0 + j[x]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < IN_FLIGHT; ++x) {
+            if (pg[x] < 0) continue;
+            const int r = r0 + j[x], slot = r % a.c.page;
+            *reinterpret_cast<uint4*>(a.c.K + pg[x] * a.c.ks[0] + h[x] * a.c.ks[1] + slot * a.c.ks[2] + piece * 16) = kv[x];
+            *reinterpret_cast<uint4*>(a.c.V + pg[x] * a.c.vs[0] + h[x] * a.c.vs[1] + slot * a.c.vs[2] + piece * 16) = vv[x];
+            if (piece == 0) {
+                const size_t o = ((size_t)s * H + h[x]) * a.c.rows + r;
+                if (a.c.pos) a.c.pos[o] = p0 + j[x];
+                if (a.c.mass) a.c.mass[o] = 0.f;
+            }
         }
     }
     if (a.advance) {
@@ -160,7 +179,11 @@ __global__ void __launch_bounds__(128) paged_advance_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- eviction: selection
-constexpr int SEL_THREADS = 1024;
+constexpr int SEL_THREADS = 512;
+constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_BINS = 2048;        // 11 bits of the key a pass: 11, 11 and 10
+constexpr int SEL_MAX_CLUSTER = 8;
+constexpr int SEL_MAX_SLICE = 45056;  // keys of one CTA that stay in shared memory (176 KB)
 
 struct SelectArgs {
     Cache c;
@@ -180,93 +203,240 @@ __device__ __forceinline__ uint32_t evict_key(float mass, int pos, int sinks, in
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int w = warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL, w, o);
-            if (lane >= o) w += y;
-        }
-        warp_sums[lane] = w;
-    }
-    __syncthreads();
-    const int base = warp ? warp_sums[warp - 1] : 0;
-    *total = warp_sums[31];
-    __syncthreads();
-    return base + x - v;
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// word at p (an address of this CTA's shared memory) in the CTA of that rank
+__device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
-// One CTA per (sequence, KV head).  The key of the budget-th row by a radix
-// select (8 bits a pass, histogram in shared memory), then one pass in row
-// order: rows above that key are kept, of those equal to it the first ones
-// that fit; movers and holes take their ranks from a scan.
+// A cluster of CS CTAs per (sequence, KV head), each with a slice of its rows.
+// One pass over mass and pos turns them into keys, kept in shared memory
+// (CACHED; longer caches read them again), and counts the keys' top 11 bits;
+// the key of the budget-th row follows digit by digit from the histograms,
+// which every CTA adds up from its peers' shared memory.  Then a row is kept if
+// its key is above that one, or equal and among the first that fit.  With
+// gt(r), eq(r) the rows before r above and equal, kept(r) = gt(r) + min(eq(r),
+// fitting) rows are kept before r, so the k-th hole is the row r < budget, not
+// kept, with r - kept(r) = k and the k-th mover the kept row r >= budget with
+// kept(r) - kept(budget) = k: one counting pass and one writing pass.
+template <int CS, bool CACHED>
 __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_constant__ SelectArgs a) {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[32];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
+    extern __shared__ uint32_t keys[];
+    __shared__ int hist[3][SEL_BINS];
+    __shared__ int warp_sum[SEL_WARPS];
+    __shared__ int counts[SEL_WARPS][4];  // rows above, equal; the same of rows below the budget
+    __shared__ int cta_counts[4];
+    __shared__ int found[2];
+    const int u = blockIdx.x / CS, s = u / a.c.heads;
+    const int rank = CS > 1 ? (int)cluster_rank() : 0;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto sync_all = [] {
+        if (CS > 1) cluster_sync();
+        else __syncthreads();
+    };
+    for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int u = blockIdx.x, s = u / a.c.heads, tid = threadIdx.x;
-    if (tid == 0) check_len(a.c, s);
+    if (tid == 0 && rank == 0) check_len(a.c, s);
     const int len = rows_held(a.c, s);
-    if (len <= a.budget) {
-        if (tid == 0) a.n_moves[u] = 0;
+    if (len <= a.budget) {  // for every CTA of the cluster
+        if (tid == 0 && rank == 0) a.n_moves[u] = 0;
         return;
     }
-    const float* mass = a.c.mass + (size_t)u * a.c.rows;
-    const int32_t* pos = a.c.pos + (size_t)u * a.c.rows;
+    const int slice = ((len + CS - 1) / CS + 127) / 128 * 128;
+    const int r0 = min(len, rank * slice), n = min(len, r0 + slice) - r0;
+    const float* mass = a.c.mass + (size_t)u * a.c.rows + r0;
+    const int32_t* pos = a.c.pos + (size_t)u * a.c.rows + r0;
     const int recent_from = a.c.seen[s] - a.recent;
+    auto key_at = [&](int i) { return CACHED ? keys[i] : evict_key(mass[i], pos[i], a.sinks, recent_from); };
+    __syncthreads();
+    // rows are a multiple of 16 per (sequence, KV head): reading up to three
+    // past n stays inside
+    for (int i = 4 * tid; i < n; i += 4 * SEL_THREADS) {
+        const float4 m = *reinterpret_cast<const float4*>(mass + i);
+        const int4 p = *reinterpret_cast<const int4*>(pos + i);
+        const uint32_t k[4] = {evict_key(m.x, p.x, a.sinks, recent_from), evict_key(m.y, p.y, a.sinks, recent_from),
+                               evict_key(m.z, p.z, a.sinks, recent_from), evict_key(m.w, p.w, a.sinks, recent_from)};
+        if (CACHED) *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i + e < n) atomicAdd(&hist[0][k[e] >> 21], 1);
+    }
     uint32_t prefix = 0, mask = 0;
     int need = a.budget;  // rows still to take among those whose key matches the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const uint32_t digit = pass == 2 ? 1023u : 2047u;
+        if (pass > 0) {
+            for (int i = tid; i < n; i += SEL_THREADS) {
+                const uint32_t k = key_at(i);
+                if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & digit], 1);
+            }
+        }
+        sync_all();
+        // four bins a thread, from the highest down
+        constexpr int BPT = SEL_BINS / SEL_THREADS;
+        int c[BPT], sum = 0;
+#pragma unroll
+        for (int e = 0; e < BPT; ++e) {
+            const int* bin = &hist[pass][SEL_BINS - 1 - (tid * BPT + e)];
+            c[e] = 0;
+            if (CS == 1) c[e] = *bin;
+            else
+#pragma unroll
+                for (int r = 0; r < CS; ++r) c[e] += peer_word(bin, r);
+            sum += c[e];
+        }
+        int x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
-        for (int r = tid; r < len; r += SEL_THREADS) {
-            const uint32_t k = evict_key(mass[r], pos[r], a.sinks, recent_from);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+        int before = x - sum;
+#pragma unroll
+        for (int w = 0; w < SEL_WARPS; ++w)
+            if (w < warp) before += warp_sum[w];
+        if (before < need && need <= before + sum) {
+#pragma unroll
+            for (int e = 0; e < BPT; ++e) {
+                if (before < need && need <= before + c[e]) {
+                    found[0] = SEL_BINS - 1 - (tid * BPT + e);
+                    found[1] = need - before;
+                }
+                before += c[e];
+            }
         }
         __syncthreads();
-        if (tid == 0) {
-            int left = need, b = 255;
-            while (b > 0 && left > hist[b]) left -= hist[b--];
-            s_prefix = prefix | ((uint32_t)b << shift);
-            s_need = left;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
-        mask |= 255u << shift;
+        prefix |= (uint32_t)found[0] << shift;
+        need = found[1];
+        mask |= digit << shift;
     }
-    int ties = 0, movers = 0, holes = 0;
+    // every warp's share of the slice, in row order
+    const int sub = ((n + SEL_WARPS - 1) / SEL_WARPS + 31) / 32 * 32;
+    const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
+    int gt = 0, eq = 0, gt_b = 0, eq_b = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t k = key_at(i);
+        const int is_gt = k > prefix, is_eq = k == prefix, low = r0 + i < a.budget;
+        gt += is_gt;
+        eq += is_eq;
+        gt_b += is_gt & low;
+        eq_b += is_eq & low;
+    }
+    gt = __reduce_add_sync(FULL, gt);
+    eq = __reduce_add_sync(FULL, eq);
+    gt_b = __reduce_add_sync(FULL, gt_b);
+    eq_b = __reduce_add_sync(FULL, eq_b);
+    if (lane == 0) {
+        counts[warp][0] = gt;
+        counts[warp][1] = eq;
+        counts[warp][2] = gt_b;
+        counts[warp][3] = eq_b;
+    }
+    __syncthreads();
+    if (tid < 4) {
+        int t = 0;
+        for (int w = 0; w < SEL_WARPS; ++w) t += counts[w][tid];
+        cta_counts[tid] = t;
+    }
+    sync_all();
+    int g = 0, e = 0, gb = 0, eb = 0;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+        const int v0 = CS == 1 ? cta_counts[0] : peer_word(&cta_counts[0], r);
+        const int v1 = CS == 1 ? cta_counts[1] : peer_word(&cta_counts[1], r);
+        if (r < rank) {
+            g += v0;
+            e += v1;
+        }
+        gb += CS == 1 ? cta_counts[2] : peer_word(&cta_counts[2], r);
+        eb += CS == 1 ? cta_counts[3] : peer_word(&cta_counts[3], r);
+    }
+    for (int w = 0; w < warp; ++w) {
+        g += counts[w][0];
+        e += counts[w][1];
+    }
+    const int kept_b = gb + min(eb, need);  // rows kept before the budget
     int32_t* out = a.moves + (size_t)u * a.max_moves * 2;
-    for (int base = 0; base < len; base += SEL_THREADS) {
-        const int r = base + tid;
-        const uint32_t k = r < len ? evict_key(mass[r], pos[r], a.sinks, recent_from) : 0u;
-        const int tie = r < len && k == prefix;
-        int total;
-        const int before = block_exclusive_scan(tie, warp_sums, &total);
-        const bool kept = r < len && (k > prefix || (tie && ties + before < need));
-        ties += total;
-        const int mover = kept && r >= a.budget, hole = !kept && r < a.budget;
-        const int m = block_exclusive_scan(mover, warp_sums, &total) + movers;
-        movers += total;
-        const int h = block_exclusive_scan(hole, warp_sums, &total) + holes;
-        holes += total;
-        if (mover && m < a.max_moves) out[2 * m] = r;
-        if (hole && h < a.max_moves) out[2 * h + 1] = r;
+    const unsigned below = (1u << lane) - 1u;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane, r = r0 + i;
+        const uint32_t k = i < w1 ? key_at(i) : 0u;
+        const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
+        const unsigned mg = __ballot_sync(FULL, is_gt), me = __ballot_sync(FULL, is_eq);
+        const int eq_before = e + __popc(me & below);
+        const int kept_before = g + __popc(mg & below) + min(eq_before, need);
+        const bool kept = is_gt || (is_eq && eq_before < need);
+        if (i < w1) {
+            const int m = kept_before - kept_b, h = r - kept_before;
+            if (kept && r >= a.budget && m < a.max_moves) out[2 * m] = r;
+            if (!kept && r < a.budget && h < a.max_moves) out[2 * h + 1] = r;
+        }
+        g += __popc(mg);
+        e += __popc(me);
     }
-    if (tid == 0) a.n_moves[u] = movers;
+    if (tid == 0 && rank == 0) a.n_moves[u] = a.budget - kept_b;
+    if (CS > 1) cluster_sync();  // no CTA leaves while a peer may read its counts
+}
+
+template <int CS, bool CACHED>
+cudaError_t launch_select_cs(const SelectArgs& a, int dev, cudaStream_t s) {
+    const int slice = round_up(ceil_div(a.c.rows, CS), 128);
+    const size_t smem = CACHED ? (size_t)slice * 4 : 0;
+    static std::atomic<bool> set[MAX_DEVICES];
+    if (CACHED && !set[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<CS, CACHED>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_MAX_SLICE * 4);
+        if (e != cudaSuccess) return e;
+        set[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.c.seqs * a.c.heads * CS));
+    cfg.blockDim = dim3(SEL_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CS;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, paged_select_kernel<CS, CACHED>, a);
+}
+
+cudaError_t launch_evict_select(const SelectArgs& a, int sms, int dev, cudaStream_t s) {
+    const long long units = (long long)a.c.seqs * a.c.heads;
+    // more CTAs per unit while they would fit side by side (two to an SM) and
+    // have rows to work on, and as many as the keys need
+    int cs = 1;
+    while (cs < SEL_MAX_CLUSTER && (a.c.rows > cs * (long long)SEL_MAX_SLICE ||
+                                    (units * cs * 2 <= 2LL * sms && a.c.rows / cs >= 8 * SEL_THREADS)))
+        cs *= 2;
+    if (a.c.rows > cs * (long long)SEL_MAX_SLICE) return launch_select_cs<SEL_MAX_CLUSTER, false>(a, dev, s);
+    switch (cs) {
+        case 1: return launch_select_cs<1, true>(a, dev, s);
+        case 2: return launch_select_cs<2, true>(a, dev, s);
+        case 4: return launch_select_cs<4, true>(a, dev, s);
+        default: return launch_select_cs<8, true>(a, dev, s);
+    }
 }
 
 // ---------------------------------------------------------------- eviction: moves
@@ -279,10 +449,13 @@ struct ApplyArgs {
     const int32_t* n_moves;
 };
 
+// VPR threads carry one row, 16 bytes of K and of V each, and have IN_FLIGHT
+// rows under way.
 template <int VPR>
 __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid_constant__ ApplyArgs a) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
+    constexpr int ROWS = APPLY_THREADS / VPR;
     const int u = blockIdx.x / a.blocks_per_unit, b = blockIdx.x % a.blocks_per_unit;
     const int s = u / a.c.heads, h = u % a.c.heads;
     int n = a.n_moves[u];
@@ -290,26 +463,51 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
         if (b == 0 && threadIdx.x == 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
         n = n < 0 ? 0 : a.max_moves;
     }
-    const int32_t* mv = a.moves + (size_t)u * a.max_moves * 2;
+    const int2* mv = reinterpret_cast<const int2*>(a.moves) + (size_t)u * a.max_moves;
     const int piece = threadIdx.x % VPR;
-    for (int k = b * (APPLY_THREADS / VPR) + threadIdx.x / VPR; k < n;
-         k += a.blocks_per_unit * (APPLY_THREADS / VPR)) {
-        const int src = mv[2 * k], dst = mv[2 * k + 1];
-        if (src < a.budget || src >= a.c.rows || dst < 0 || dst >= a.budget || dst >= a.c.rows) {
-            report(a.c.dev_err, CKV_DEV_BAD_INDEX);
-            continue;
+    const size_t o = (size_t)u * a.c.rows;
+    for (int k0 = b * ROWS * IN_FLIGHT + threadIdx.x / VPR; k0 < n; k0 += a.blocks_per_unit * ROWS * IN_FLIGHT) {
+        int2 m[IN_FLIGHT];
+        int p0[IN_FLIGHT], p1[IN_FLIGHT];
+        uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
+        float mass[IN_FLIGHT];
+        int pos[IN_FLIGHT];
+#pragma unroll
+        for (int x = 0; x < IN_FLIGHT; ++x)
+            if (k0 + x * ROWS < n) m[x] = mv[k0 + x * ROWS];
+#pragma unroll
+        for (int x = 0; x < IN_FLIGHT; ++x) {
+            p0[x] = p1[x] = -1;
+            if (k0 + x * ROWS >= n) continue;
+            const int src = m[x].x, dst = m[x].y;
+            if (src < a.budget || src >= a.c.rows || dst < 0 || dst >= a.budget || dst >= a.c.rows) {
+                report(a.c.dev_err, CKV_DEV_BAD_INDEX);
+                continue;
+            }
+            p0[x] = page_of(a.c, s, src);
+            p1[x] = page_of(a.c, s, dst);
         }
-        const int p0 = page_of(a.c, s, src), p1 = page_of(a.c, s, dst);
-        if (p0 < 0 || p1 < 0) continue;
-        const int s0 = src % a.c.page, s1 = dst % a.c.page;
-        const uint4 kv = *reinterpret_cast<const uint4*>(a.c.K + p0 * a.c.ks[0] + h * a.c.ks[1] + s0 * a.c.ks[2] + piece * 16);
-        const uint4 vv = *reinterpret_cast<const uint4*>(a.c.V + p0 * a.c.vs[0] + h * a.c.vs[1] + s0 * a.c.vs[2] + piece * 16);
-        *reinterpret_cast<uint4*>(a.c.K + p1 * a.c.ks[0] + h * a.c.ks[1] + s1 * a.c.ks[2] + piece * 16) = kv;
-        *reinterpret_cast<uint4*>(a.c.V + p1 * a.c.vs[0] + h * a.c.vs[1] + s1 * a.c.vs[2] + piece * 16) = vv;
-        if (piece == 0) {
-            const size_t o = (size_t)u * a.c.rows;
-            if (a.c.mass) a.c.mass[o + dst] = a.c.mass[o + src];
-            if (a.c.pos) a.c.pos[o + dst] = a.c.pos[o + src];
+#pragma unroll
+        for (int x = 0; x < IN_FLIGHT; ++x) {
+            if (p0[x] < 0 || p1[x] < 0) continue;
+            const int slot = m[x].x % a.c.page;
+            kv[x] = *reinterpret_cast<const uint4*>(a.c.K + p0[x] * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2] + piece * 16);
+            vv[x] = *reinterpret_cast<const uint4*>(a.c.V + p0[x] * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2] + piece * 16);
+            if (piece == 0) {
+                if (a.c.mass) mass[x] = a.c.mass[o + m[x].x];
+                if (a.c.pos) pos[x] = a.c.pos[o + m[x].x];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < IN_FLIGHT; ++x) {
+            if (p0[x] < 0 || p1[x] < 0) continue;
+            const int slot = m[x].y % a.c.page;
+            *reinterpret_cast<uint4*>(a.c.K + p1[x] * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2] + piece * 16) = kv[x];
+            *reinterpret_cast<uint4*>(a.c.V + p1[x] * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2] + piece * 16) = vv[x];
+            if (piece == 0) {
+                if (a.c.mass) a.c.mass[o + m[x].y] = mass[x];
+                if (a.c.pos) a.c.pos[o + m[x].y] = pos[x];
+            }
         }
     }
     // nothing in this kernel reads lens
@@ -350,8 +548,8 @@ extern "C" ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void*
     a.first = first == a.c.seen ? nullptr : first;
     a.n = n;
     const int vpr = D * elem / 16;
-    const long long per_pass = APPEND_THREADS / vpr;
-    long long blocks = ((long long)n * a.c.heads + 4 * per_pass - 1) / (4 * per_pass);
+    const long long per_pass = APPEND_THREADS / vpr * IN_FLIGHT;
+    long long blocks = ((long long)n * a.c.heads + per_pass - 1) / per_pass;
     if (blocks > 4096) blocks = 4096;
     while (blocks * a.c.seqs > 0x7fffffffLL) blocks = (blocks + 1) / 2;
     a.blocks_per_seq = (int)blocks;
@@ -384,6 +582,7 @@ extern "C" ckv_status ckv_paged_evict_select(const ckv_paged_cache* cache, int32
     ckv_status st = check_cache(cache, &a.c);
     if (st != CKV_OK) return st;
     if (!a.c.mass || !a.c.pos || !a.c.seen || !moves || !n_moves) return CKV_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(moves) & 7u) return CKV_ERR_ALIGN;
     if (sinks < 0 || recent < 0 || (long long)sinks + recent > budget) return CKV_ERR_ARG;
     st = check_evict(a.c, budget, max_moves);
     if (st != CKV_OK) return st;
@@ -393,8 +592,11 @@ extern "C" ckv_status ckv_paged_evict_select(const ckv_paged_cache* cache, int32
     a.max_moves = max_moves;
     a.moves = moves;
     a.n_moves = n_moves;
-    const cudaError_t e = launch_dependent(paged_select_kernel, dim3(a.c.seqs * a.c.heads), dim3(SEL_THREADS), 0,
-                                           (cudaStream_t)stream, a);
+    if ((long long)a.c.seqs * a.c.heads > 0x7fffffffLL / SEL_MAX_CLUSTER) return CKV_ERR_ARG;
+    int dev = 0;
+    const int sms = sm_count(&dev);
+    if (sms < 1) return CKV_ERR_CUDA;
+    const cudaError_t e = launch_evict_select(a, sms, dev, (cudaStream_t)stream);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;
 }
 
@@ -405,6 +607,7 @@ extern "C" ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_
     ckv_status st = check_cache(cache, &a.c);
     if (st != CKV_OK) return st;
     if (!moves || !n_moves) return CKV_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(moves) & 7u) return CKV_ERR_ALIGN;
     st = check_evict(a.c, budget, max_moves);
     if (st != CKV_OK) return st;
     a.budget = budget;
@@ -412,11 +615,15 @@ extern "C" ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_
     a.moves = moves;
     a.n_moves = n_moves;
     const int vpr = D * (cache->kv_dtype == CKV_BF16 ? 2 : 4) / 16;
-    const int per_pass = APPLY_THREADS / vpr;
-    long long blocks = ((long long)max_moves + 4 * per_pass - 1) / (4 * per_pass);
-    if (blocks < 1) blocks = 1;
+    const int per_pass = APPLY_THREADS / vpr * IN_FLIGHT;
     const long long units = (long long)a.c.seqs * a.c.heads;
-    while (blocks > 1 && blocks * units > (1 << 20)) blocks = (blocks + 1) / 2;
+    const int sms = sm_count(nullptr);
+    if (sms < 1) return CKV_ERR_CUDA;
+    // as many blocks as the moves could keep busy, up to eight to an SM in all
+    long long blocks = ((long long)max_moves + per_pass - 1) / per_pass;
+    const long long most = (8LL * sms + units - 1) / units;
+    if (blocks > most) blocks = most;
+    if (blocks < 1) blocks = 1;
     a.blocks_per_unit = (int)blocks;
     cudaStream_t s = (cudaStream_t)stream;
     const dim3 grid((unsigned)(blocks * units)), block(APPLY_THREADS);

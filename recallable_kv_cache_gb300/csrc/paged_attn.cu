@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
 // CTA i merges its share of the outputs of the (at most two) units that it has
 // in common with other CTAs, and adds its tiles' weights to the accumulated
 // ones.
-constexpr int FIN_THREADS = 256;
+constexpr int FIN_THREADS = 512;
 
 template <int TR>
 __global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_constant__ AttnArgs a) {
@@ -771,21 +771,42 @@ __global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_
     }
     if (!a.mass_out) return;
     __syncthreads();
-    Pos p{b.s, b.h, b.k, b.nt};
-    for (long long t = t0; t < t1 && p.nt;) {
+    // every warp its part of the share's tiles, a lane four rows at a time
+    constexpr int NW = FIN_THREADS / 32;
+    const long long w0 = t0 + share_begin(t1 - t0, NW, warp), w1 = t0 + share_begin(t1 - t0, NW, warp + 1);
+    Pos p = advance<TR>(a.c, Pos{b.s, b.h, b.k, b.nt}, (int)(w0 - t0));
+    for (long long t = w0; t < w1 && p.nt;) {
         const int u = p.s * a.c.heads + p.h;
-        const int n = (int)min((long long)(p.nt - p.k), t1 - t);  // tiles of this unit in the share
+        const int n = (int)min((long long)(p.nt - p.k), w1 - t);  // tiles of this unit in the part
         const float* zz = u == us[0] ? z[0] : (u == us[1] ? z[1] : a.lse2 + (size_t)u * a.g);
+        const float* sc = a.scores + (size_t)u * a.g * a.c.rows;
         const int r1 = min(rows_held(a.c, p.s), (p.k + n) * TR);
-        for (int r = p.k * TR + tid; r < r1; r += FIN_THREADS) {
-            float w = 0.f;
-            for (int j = 0; j < a.g; ++j) {
-                const float lz = zz[j];
-                const float x = a.scores[((size_t)u * a.g + j) * a.c.rows + r];
-                w += lz == -INFINITY ? 0.f : ex2(x - lz);
-            }
+        for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
             const size_t o = (size_t)u * a.c.rows + r;
-            a.mass_out[o] = (a.mass_in ? a.mass_in[o] : 0.f) + w;
+            float4 w = a.mass_in ? *reinterpret_cast<const float4*>(a.mass_in + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int j = 0; j < a.g; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(sc + (size_t)j * a.c.rows + r);
+                const float lz = zz[j];
+                if (lz != -INFINITY) {
+                    add.x += ex2(x.x - lz);
+                    add.y += ex2(x.y - lz);
+                    add.z += ex2(x.z - lz);
+                    add.w += ex2(x.w - lz);
+                }
+            }
+            w.x += add.x;
+            w.y += add.y;
+            w.z += add.z;
+            w.w += add.w;
+            if (r + 4 <= r1) {
+                *reinterpret_cast<float4*>(a.mass_out + o) = w;
+            } else {  // the rows behind the last one stay as they are
+                a.mass_out[o] = w.x;
+                if (r + 1 < r1) a.mass_out[o + 1] = w.y;
+                if (r + 2 < r1) a.mass_out[o + 2] = w.z;
+            }
         }
         t += n;
         p = advance<TR>(a.c, p, n);
@@ -899,7 +920,7 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
         if (q_stride[i] * (bf16 ? 2 : 4) & 15) return CKV_ERR_ALIGN;
         a.qst[i] = q_stride[i];
     }
-    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return CKV_ERR_ALIGN;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(mass_in) || !aligned16(mass_out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return CKV_ERR_ALIGN;
     const Layout l = layout_of(a.c, g, mass_out != nullptr);
     if (workspace_bytes < (int64_t)l.total) return CKV_ERR_CAPACITY;
     unsigned char* w = static_cast<unsigned char*>(workspace);

@@ -447,6 +447,8 @@ SELECT = [
     ([5000, 300, 4999], 2, 64, 257, 16, 100),
     ([2049, 1023], 1, 16, 40, 4, 4),
     ([70000], 1, 16, 30000, 16, 500),
+    ([9001, 8000], 1, 48, 3001, 16, 500),
+    ([400001], 1, 16, 1000, 16, 500),
 ]
 
 

@@ -96,7 +96,8 @@ BAD_CACHES = [
     (dict(max_pages=1 << 25), ARG), (dict(seqs=1 << 30, heads=2), ARG), (dict(K=P + 8), ALIGN), (dict(V=P + 2), ALIGN),
     (dict(k_stride=(16384, 8192, 127)), ARG), (dict(k_stride=(0, 8192, 128)), ARG),
     (dict(v_stride=(16384, -8192, 128)), ARG), (dict(k_stride=(16384, 8192, 132)), ALIGN),
-    (dict(v_stride=(16388, 8192, 128)), ALIGN), (dict(seen=None), ARG),
+    (dict(v_stride=(16388, 8192, 128)), ALIGN), (dict(seen=None), ARG), (dict(mass=P + 4), ALIGN),
+    (dict(pos=P + 8), ALIGN),
 ]
 
 
@@ -146,7 +147,7 @@ def test_attention_refusals(lib):
     assert call(dtype=ckv.F32) == DTYPE and call(dtype=9) == DTYPE
     assert call(g=0) == ARG and call(g=17) == ARG and call(g=-1) == ARG
     assert call(scale=float("nan")) == ARG and call(scale=float("inf")) == ARG
-    assert call(mass_in=P) == ARG
+    assert call(mass_in=P) == ARG and call(mass_out=P + 4) == ALIGN and call(mass_in=P + 8, mass_out=P) == ALIGN
     assert call(qs=i64(-8, 128)) == ARG and call(qs=i64(1024, 129)) == ALIGN
     assert call(q=P + 2) == ALIGN and call(out=P + 4) == ALIGN and call(ws=P + 128) == ALIGN
     n, m = ctypes.c_int64(), ctypes.c_int64()
@@ -173,6 +174,7 @@ def test_eviction_refusals(lib):
     for call in (select, apply):
         assert call(budget=0) == ARG and call(budget=-1) == ARG and call(moves=None) == ARG and call(n=None) == ARG
         assert call(most=-1) == ARG and call(most=63) == CAPACITY and call(budget=200, most=55) == CAPACITY
+        assert call(moves=P + 4) == ALIGN
     assert select(sinks=-1) == ARG and select(recent=-1) == ARG and select(sinks=40, recent=25) == ARG
     assert select(sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == ARG
     for missing in ("mass", "pos"):
