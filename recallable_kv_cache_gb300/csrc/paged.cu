@@ -73,6 +73,8 @@ ckv_status check_cache(const ckv_paged_cache* c, Cache* o) {
     o->seqs = c->seqs;
     o->max_pages = c->max_pages;
     o->rows = (int)rows;
+    o->by_page = FastDiv((uint32_t)c->page_size);
+    o->by_heads = FastDiv((uint32_t)c->heads);
     return CKV_OK;
 }
 
@@ -93,7 +95,7 @@ struct AppendArgs {
     const int32_t* start;
     const int32_t* first;
     int n;
-    int blocks_per_seq;
+    FastDiv by_blocks;  // blocks per sequence
     int advance;  // this kernel writes lens and seen
 };
 
@@ -123,38 +125,37 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     constexpr int ROWS = APPEND_THREADS / VPR;
-    const int s = blockIdx.x / a.blocks_per_seq, b = blockIdx.x % a.blocks_per_seq;
+    int b;
+    const int s = a.by_blocks.quot(blockIdx.x, &b);
     int r0, p0;
     const int cnt = append_plan(a, s, &r0, &p0);
-    const int H = a.c.heads;
     const int piece = threadIdx.x % VPR;
-    const long long items = cnt < 0 ? 0 : (long long)cnt * H;
-    const long long step = (long long)a.blocks_per_seq * ROWS * IN_FLIGHT;
-    for (long long i0 = (long long)b * ROWS * IN_FLIGHT + threadIdx.x / VPR; i0 < items; i0 += step) {
+    const int items = cnt < 0 ? 0 : cnt * a.c.heads;  // rows of all KV heads, the heads of a token side by side
+    const unsigned char* ksrc = a.k_src + s * a.kst[0] + piece * 16;
+    const unsigned char* vsrc = a.v_src + s * a.vst[0] + piece * 16;
+    unsigned char* K = a.c.K + piece * 16;
+    unsigned char* V = a.c.V + piece * 16;
+    for (int i0 = b * ROWS * IN_FLIGHT + threadIdx.x / VPR; i0 < items; i0 += a.by_blocks.d * ROWS * IN_FLIGHT) {
         uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
-        int j[IN_FLIGHT], h[IN_FLIGHT], pg[IN_FLIGHT];
+        int j[IN_FLIGHT], h[IN_FLIGHT], pg[IN_FLIGHT], slot[IN_FLIGHT];
 #pragma unroll
         for (int x = 0; x < IN_FLIGHT; ++x) {
-            const long long i = i0 + x * ROWS;
+            const int i = i0 + x * ROWS;
             pg[x] = -1;
             if (i < items) {
-                j[x] = (int)(i / H);
-                h[x] = (int)(i % H);
-                const unsigned char* k = a.k_src + s * a.kst[0] + h[x] * a.kst[1] + j[x] * a.kst[2] + piece * 16;
-                const unsigned char* v = a.v_src + s * a.vst[0] + h[x] * a.vst[1] + j[x] * a.vst[2] + piece * 16;
-                kv[x] = *reinterpret_cast<const uint4*>(k);
-                vv[x] = *reinterpret_cast<const uint4*>(v);
-                pg[x] = page_of(a.c, s, r0 + j[x]);
+                j[x] = a.c.by_heads.quot(i, &h[x]);
+                kv[x] = *reinterpret_cast<const uint4*>(ksrc + h[x] * a.kst[1] + j[x] * a.kst[2]);
+                vv[x] = *reinterpret_cast<const uint4*>(vsrc + h[x] * a.vst[1] + j[x] * a.vst[2]);
+                pg[x] = page_of(a.c, s, r0 + j[x], &slot[x]);
             }
         }
 #pragma unroll
         for (int x = 0; x < IN_FLIGHT; ++x) {
             if (pg[x] < 0) continue;
-            const int r = r0 + j[x], slot = r % a.c.page;
-            *reinterpret_cast<uint4*>(a.c.K + pg[x] * a.c.ks[0] + h[x] * a.c.ks[1] + slot * a.c.ks[2] + piece * 16) = kv[x];
-            *reinterpret_cast<uint4*>(a.c.V + pg[x] * a.c.vs[0] + h[x] * a.c.vs[1] + slot * a.c.vs[2] + piece * 16) = vv[x];
+            *reinterpret_cast<uint4*>(K + pg[x] * a.c.ks[0] + h[x] * a.c.ks[1] + slot[x] * a.c.ks[2]) = kv[x];
+            *reinterpret_cast<uint4*>(V + pg[x] * a.c.vs[0] + h[x] * a.c.vs[1] + slot[x] * a.c.vs[2]) = vv[x];
             if (piece == 0) {
-                const size_t o = ((size_t)s * H + h[x]) * a.c.rows + r;
+                const size_t o = ((size_t)s * a.c.heads + h[x]) * a.c.rows + r0 + j[x];
                 if (a.c.pos) a.c.pos[o] = p0 + j[x];
                 if (a.c.mass) a.c.mass[o] = 0.f;
             }
@@ -211,6 +212,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// adds v to the word at p (an address of this CTA's shared memory) in the CTA of that rank
+__device__ __forceinline__ void peer_add(int* p, uint32_t rank, int v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
+    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 // word at p (an address of this CTA's shared memory) in the CTA of that rank
 __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
     uint32_t at;
@@ -223,8 +230,10 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 // A cluster of CS CTAs per (sequence, KV head), each with a slice of its rows.
 // One pass over mass and pos turns them into keys, kept in shared memory
 // (CACHED; longer caches read them again), and counts the keys' top 11 bits;
-// the key of the budget-th row follows digit by digit from the histograms,
-// which every CTA adds up from its peers' shared memory.  Then a row is kept if
+// the key of the budget-th row follows digit by digit from the histograms, to
+// which every CTA adds its occupied bins in all its peers' shared memory (few
+// of the 2048 are occupied; every CTA reading all bins of its peers took 97 us
+// for 32 units of 128k rows where this takes PERIOD us).  Then a row is kept if
 // its key is above that one, or equal and among the first that fit.  With
 // gt(r), eq(r) the rows before r above and equal, kept(r) = gt(r) + min(eq(r),
 // fitting) rows are kept before r, so the k-th hole is the row r < budget, not
@@ -233,7 +242,8 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 template <int CS, bool CACHED>
 __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_constant__ SelectArgs a) {
     extern __shared__ uint32_t keys[];
-    __shared__ int hist[3][SEL_BINS];
+    __shared__ int hist[3][SEL_BINS];  // the unit's, one a pass
+    __shared__ int mine[CS > 1 ? SEL_BINS : 1];
     __shared__ int warp_sum[SEL_WARPS];
     __shared__ int counts[SEL_WARPS][4];  // rows above, equal; the same of rows below the budget
     __shared__ int cta_counts[4];
@@ -246,6 +256,8 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         else __syncthreads();
     };
     for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
+    if (CS > 1)
+        for (int i = tid; i < SEL_BINS; i += SEL_THREADS) mine[i] = 0;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     if (tid == 0 && rank == 0) check_len(a.c, s);
@@ -259,10 +271,12 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     const float* mass = a.c.mass + (size_t)u * a.c.rows + r0;
     const int32_t* pos = a.c.pos + (size_t)u * a.c.rows + r0;
     const int recent_from = a.c.seen[s] - a.recent;
+    int* local = CS > 1 ? mine : hist[0];
     auto key_at = [&](int i) { return CACHED ? keys[i] : evict_key(mass[i], pos[i], a.sinks, recent_from); };
-    __syncthreads();
+    sync_all();  // every CTA's histograms are cleared
     // rows are a multiple of 16 per (sequence, KV head): reading up to three
     // past n stays inside
+#pragma unroll 2
     for (int i = 4 * tid; i < n; i += 4 * SEL_THREADS) {
         const float4 m = *reinterpret_cast<const float4*>(mass + i);
         const int4 p = *reinterpret_cast<const int4*>(pos + i);
@@ -271,7 +285,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         if (CACHED) *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (i + e < n) atomicAdd(&hist[0][k[e] >> 21], 1);
+            if (i + e < n) atomicAdd(&local[k[e] >> 21], 1);
     }
     uint32_t prefix = 0, mask = 0;
     int need = a.budget;  // rows still to take among those whose key matches the prefix
@@ -280,9 +294,20 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         const uint32_t digit = pass == 2 ? 1023u : 2047u;
         if (pass > 0) {
+            if (CS == 1) local = hist[pass];
             for (int i = tid; i < n; i += SEL_THREADS) {
                 const uint32_t k = key_at(i);
-                if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & digit], 1);
+                if ((k & mask) == prefix) atomicAdd(&local[(k >> shift) & digit], 1);
+            }
+        }
+        if (CS > 1) {
+            __syncthreads();
+            for (int i = tid; i < SEL_BINS; i += SEL_THREADS) {
+                const int v = mine[i];
+                if (v == 0) continue;
+                mine[i] = 0;
+#pragma unroll
+                for (int r = 0; r < CS; ++r) peer_add(&hist[pass][i], r, v);
             }
         }
         sync_all();
@@ -291,12 +316,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         int c[BPT], sum = 0;
 #pragma unroll
         for (int e = 0; e < BPT; ++e) {
-            const int* bin = &hist[pass][SEL_BINS - 1 - (tid * BPT + e)];
-            c[e] = 0;
-            if (CS == 1) c[e] = *bin;
-            else
-#pragma unroll
-                for (int r = 0; r < CS; ++r) c[e] += peer_word(bin, r);
+            c[e] = hist[pass][SEL_BINS - 1 - (tid * BPT + e)];
             sum += c[e];
         }
         int x = sum;
@@ -444,7 +464,8 @@ constexpr int APPLY_THREADS = 256;
 
 struct ApplyArgs {
     Cache c;
-    int budget, max_moves, blocks_per_unit;
+    int budget, max_moves;
+    FastDiv by_blocks;  // blocks per unit
     const int32_t* moves;
     const int32_t* n_moves;
 };
@@ -456,8 +477,8 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     constexpr int ROWS = APPLY_THREADS / VPR;
-    const int u = blockIdx.x / a.blocks_per_unit, b = blockIdx.x % a.blocks_per_unit;
-    const int s = u / a.c.heads, h = u % a.c.heads;
+    int b, h;
+    const int u = a.by_blocks.quot(blockIdx.x, &b), s = a.c.by_heads.quot(u, &h);
     int n = a.n_moves[u];
     if (n < 0 || n > a.max_moves) {
         if (b == 0 && threadIdx.x == 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
@@ -466,9 +487,11 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
     const int2* mv = reinterpret_cast<const int2*>(a.moves) + (size_t)u * a.max_moves;
     const int piece = threadIdx.x % VPR;
     const size_t o = (size_t)u * a.c.rows;
-    for (int k0 = b * ROWS * IN_FLIGHT + threadIdx.x / VPR; k0 < n; k0 += a.blocks_per_unit * ROWS * IN_FLIGHT) {
+    unsigned char* K = a.c.K + h * a.c.ks[1] + piece * 16;
+    unsigned char* V = a.c.V + h * a.c.vs[1] + piece * 16;
+    for (int k0 = b * ROWS * IN_FLIGHT + threadIdx.x / VPR; k0 < n; k0 += a.by_blocks.d * ROWS * IN_FLIGHT) {
         int2 m[IN_FLIGHT];
-        int p0[IN_FLIGHT], p1[IN_FLIGHT];
+        int p0[IN_FLIGHT], p1[IN_FLIGHT], s0[IN_FLIGHT], s1[IN_FLIGHT];
         uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
         float mass[IN_FLIGHT];
         int pos[IN_FLIGHT];
@@ -484,15 +507,14 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
                 report(a.c.dev_err, CKV_DEV_BAD_INDEX);
                 continue;
             }
-            p0[x] = page_of(a.c, s, src);
-            p1[x] = page_of(a.c, s, dst);
+            p0[x] = page_of(a.c, s, src, &s0[x]);
+            p1[x] = page_of(a.c, s, dst, &s1[x]);
         }
 #pragma unroll
         for (int x = 0; x < IN_FLIGHT; ++x) {
             if (p0[x] < 0 || p1[x] < 0) continue;
-            const int slot = m[x].x % a.c.page;
-            kv[x] = *reinterpret_cast<const uint4*>(a.c.K + p0[x] * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2] + piece * 16);
-            vv[x] = *reinterpret_cast<const uint4*>(a.c.V + p0[x] * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2] + piece * 16);
+            kv[x] = *reinterpret_cast<const uint4*>(K + p0[x] * a.c.ks[0] + s0[x] * a.c.ks[2]);
+            vv[x] = *reinterpret_cast<const uint4*>(V + p0[x] * a.c.vs[0] + s0[x] * a.c.vs[2]);
             if (piece == 0) {
                 if (a.c.mass) mass[x] = a.c.mass[o + m[x].x];
                 if (a.c.pos) pos[x] = a.c.pos[o + m[x].x];
@@ -501,9 +523,8 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
 #pragma unroll
         for (int x = 0; x < IN_FLIGHT; ++x) {
             if (p0[x] < 0 || p1[x] < 0) continue;
-            const int slot = m[x].y % a.c.page;
-            *reinterpret_cast<uint4*>(a.c.K + p1[x] * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2] + piece * 16) = kv[x];
-            *reinterpret_cast<uint4*>(a.c.V + p1[x] * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2] + piece * 16) = vv[x];
+            *reinterpret_cast<uint4*>(K + p1[x] * a.c.ks[0] + s1[x] * a.c.ks[2]) = kv[x];
+            *reinterpret_cast<uint4*>(V + p1[x] * a.c.vs[0] + s1[x] * a.c.vs[2]) = vv[x];
             if (piece == 0) {
                 if (a.c.mass) a.c.mass[o + m[x].y] = mass[x];
                 if (a.c.pos) a.c.pos[o + m[x].y] = pos[x];
@@ -551,8 +572,10 @@ extern "C" ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void*
     const long long per_pass = APPEND_THREADS / vpr * IN_FLIGHT;
     long long blocks = ((long long)n * a.c.heads + per_pass - 1) / per_pass;
     if (blocks > 4096) blocks = 4096;
-    while (blocks * a.c.seqs > 0x7fffffffLL) blocks = (blocks + 1) / 2;
-    a.blocks_per_seq = (int)blocks;
+    while (blocks > 1 && blocks * a.c.seqs > 0x7fffffffLL) blocks = (blocks + 1) / 2;
+    // a thread's item index plus a step stays below 2^31
+    if ((long long)n * a.c.heads + (blocks + 1) * per_pass > 0x7fffffffLL) return CKV_ERR_ARG;
+    a.by_blocks = FastDiv((uint32_t)blocks);
     // lens and seen may be advanced by the copying kernel where no other
     // block can still read the old values
     const bool in_place = !a.start || (a.c.seen && !a.first);
@@ -624,7 +647,7 @@ extern "C" ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_
     const long long most = (8LL * sms + units - 1) / units;
     if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
-    a.blocks_per_unit = (int)blocks;
+    a.by_blocks = FastDiv((uint32_t)blocks);
     cudaStream_t s = (cudaStream_t)stream;
     const dim3 grid((unsigned)(blocks * units)), block(APPLY_THREADS);
     const cudaError_t e = vpr == 16 ? launch_dependent(paged_apply_kernel<16>, grid, block, 0, s, a)

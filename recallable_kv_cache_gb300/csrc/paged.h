@@ -13,6 +13,25 @@ constexpr int MAX_G = 16;        // query heads per KV head
 constexpr int MAX_DEVICES = 64;
 constexpr long long MAX_STRIDE = 1LL << 37;  // elements; a tensor map's strides stay below 2^40 bytes
 
+// Quotient by a divisor fixed at launch, for dividends below 2^31: with s =
+// ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(m n) + n) >> s
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994; n below 2^31 keeps the sum inside 32 bits).
+struct FastDiv {
+    uint32_t d, m, s;
+    __host__ __device__ FastDiv() : d(1), m(1), s(0) {}
+    __host__ explicit FastDiv(uint32_t div) : d(div), s(0) {
+        while ((1ull << s) < d) ++s;
+        m = (uint32_t)((((1ull << s) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ int quot(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s); }
+    __device__ __forceinline__ int quot(int n, int* rem) const {
+        const int q = quot(n);
+        *rem = n - q * (int)d;
+        return q;
+    }
+};
+
 // What the kernels take of a ckv_paged_cache.
 struct Cache {
     unsigned char* K;
@@ -26,6 +45,7 @@ struct Cache {
     int32_t* dev_err;
     int n_pages, heads, page, seqs, max_pages;
     int rows;  // max_pages * page
+    FastDiv by_page, by_heads;
 };
 
 ckv_status check_cache(const ckv_paged_cache* c, Cache* out);
@@ -47,8 +67,8 @@ __device__ __forceinline__ void check_len(const Cache& c, int s) {
     if (n < 0 || n > c.rows) report(c.dev_err, CKV_DEV_BAD_COUNT);
 }
 // page holding row r of sequence s, -1 (and the error word) if the id is bad
-__device__ __forceinline__ int page_of(const Cache& c, int s, int r) {
-    const int p = c.table[(size_t)s * c.max_pages + r / c.page];
+__device__ __forceinline__ int page_of(const Cache& c, int s, int r, int* slot) {
+    const int p = c.table[(size_t)s * c.max_pages + c.by_page.quot(r, slot)];
     if (p >= 0 && p < c.n_pages) return p;
     report(c.dev_err, CKV_DEV_BAD_INDEX);
     return -1;

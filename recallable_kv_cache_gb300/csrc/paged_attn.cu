@@ -41,12 +41,11 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int STAGE = 8192;  // K rows, then V rows of one tile
 
-// where a CTA's share of the tiles begins: left for the finish kernel
-struct Begin {
-    long long total;  // tiles of the call
-    int n_cta;        // CTAs that share them
-    int s, h, k, nt;  // the first tile: sequence, KV head, tile in the unit, tiles of the unit
-    int pad;
+// Where a CTA's share of the tiles begins: left for the finish kernel.
+struct __align__(16) Begin {
+    int total, n_cta;  // tiles of the call, CTAs that share them
+    int s, h, k, nt;   // the first tile: sequence, KV head, tile in the unit, tiles of the unit
+    int pad[2];
 };
 
 struct AttnArgs {
@@ -96,24 +95,24 @@ __device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
     return p;
 }
 // Exclusive prefix sums of the sequences' tiles, one per thread's chunk of
-// sequences; returns the total.
+// sequences; returns the total (below 2^31, checked for the cache's extents).
 template <int TR, int NT>
-__device__ long long scan_tiles(const Cache& c, long long* pre) {
-    __shared__ long long warp_sum[NT / 32];
+__device__ int scan_tiles(const Cache& c, int* pre) {
+    __shared__ int warp_sum[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = (c.seqs + NT - 1) / NT;
-    long long v = 0;
+    int v = 0;
     for (int s = tid * chunk; s < min(c.seqs, (tid + 1) * chunk); ++s) v += tiles_of<TR>(c, s);
     v *= c.heads;
-    long long x = v;
+    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(FULL, x, o);
+        const int y = __shfl_up_sync(FULL, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    long long base = 0, total = 0;
+    int base = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) base += warp_sum[w];
@@ -123,38 +122,48 @@ __device__ long long scan_tiles(const Cache& c, long long* pre) {
     __syncthreads();
     return total;
 }
-// the place of tile t < total
+// the place of tile t < total, for a whole warp
 template <int TR, int NT>
-__device__ Pos locate(const Cache& c, const long long* pre, long long t) {
+__device__ Pos locate(const Cache& c, const int* pre, int t, int lane) {
     const int chunk = (c.seqs + NT - 1) / NT;
-    int lo = 0, hi = NT;  // pre[lo] <= t; the last such one holds t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (pre[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    long long left = t - pre[lo];
-    Pos p{lo * chunk, 0, 0, 0};
+    int at = -1;  // the last chunk with pre <= t holds t; a lane looks at NT / 32 of them in a row
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i)
+        if (pre[lane * (NT / 32) + i] <= t) at = lane * (NT / 32) + i;
+    at = __reduce_max_sync(FULL, at);
+    int left = t - pre[at];
+    Pos p{at * chunk, 0, 0, 0};
     for (; p.s < c.seqs; ++p.s) {
         p.nt = tiles_of<TR>(c, p.s);
-        if (left < (long long)p.nt * c.heads) break;
-        left -= (long long)p.nt * c.heads;
+        if (left < p.nt * c.heads) break;
+        left -= p.nt * c.heads;
     }
     if (p.s >= c.seqs) return Pos{c.seqs, 0, 0, 0};
-    p.h = (int)(left / p.nt);
-    p.k = (int)(left % p.nt);
+    p.h = left / p.nt;
+    p.k = left % p.nt;
     return p;
 }
-// A warp gets at least this many tiles before the work is spread over more
-// CTAs.
+// The deal: `total` tiles to the warps of n_cta CTAs, in order, as evenly as
+// they go (shares of q + 1 tiles, then of q).  A warp gets at least MIN_TILES
+// before the work is spread over more CTAs.
 constexpr int MIN_TILES = 2;
-__device__ __forceinline__ int ctas_used(long long total, int warps, int grid) {
-    const long long n = (total + warps * MIN_TILES - 1) / (warps * MIN_TILES);
-    return n < 1 ? 1 : (n > grid ? grid : (int)n);
-}
-__device__ __forceinline__ long long share_begin(long long total, int parts, int i) { return total * i / parts; }
-// the CTA whose share holds tile t
-__device__ __forceinline__ int cta_of(long long total, int n, long long t) { return (int)(((t + 1) * n - 1) / total); }
+struct Deal {
+    int total, n_cta, warps, q, r;
+    __device__ __forceinline__ Deal(int total_, int n_cta_, int warps_) : total(total_), n_cta(n_cta_), warps(warps_) {
+        q = total / (n_cta * warps);
+        r = total - q * (n_cta * warps);
+    }
+    static __device__ __forceinline__ int ctas(int total, int warps, int grid) {
+        return max(1, min(grid, (total + warps * MIN_TILES - 1) / (warps * MIN_TILES)));
+    }
+    __device__ __forceinline__ int begin_warp(int w) const { return w * q + min(w, r); }  // w: across CTAs
+    __device__ __forceinline__ int begin_cta(int c) const { return begin_warp(c * warps); }
+    // the CTA whose share holds tile t
+    __device__ __forceinline__ int cta_of(int t) const {
+        const int w = t < (q + 1) * r ? t / (q + 1) : r + (t - (q + 1) * r) / q;
+        return w / warps;
+    }
+};
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
     asm volatile(
@@ -212,7 +221,7 @@ struct TilesBf16 {
         }
     }
     // n of the stage's rows are held; the others' V rows must count as zero
-    __device__ __forceinline__ void tile(unsigned char* stage, float*, int n, float qscale, int g, float* scores,
+    __device__ __forceinline__ void tile(unsigned char* stage, float2*, int n, float qscale, int g, float* scores,
                                          size_t rows, int lane) {
         const uint32_t kb = ptx::smem_u32(stage), vb = kb + STAGE / 2;
         if (n < TR) {
@@ -340,11 +349,51 @@ struct TilesBf16 {
 };
 
 // ---------------------------------------------------------------- fp32 tiles
+// Two fp32 values in one 64-bit register: the packed multiply-add does two
+// channels an instruction.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t d) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+    return f;
+}
+// Sums v[0 .. N) over L neighbouring lanes; every lane keeps N / L of the sums
+// (one where N < L), those from the returned index on: each step halves what a
+// lane still adds up, so a value costs about one shuffle instead of log2 L.
+template <int N, int L>
+__device__ __forceinline__ int reduce_scatter(float* v, int lane) {
+    if constexpr (L > 1) {
+        constexpr int d = L / 2;
+        if constexpr (N > 1) {
+            const bool up = lane & d;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float send = up ? v[i] : v[i + N / 2], keep = up ? v[i + N / 2] : v[i];
+                v[i] = keep + __shfl_xor_sync(FULL, send, d);
+            }
+            return (up ? N / 2 : 0) + reduce_scatter<N / 2, d>(v, lane);
+        } else {
+            v[0] += __shfl_xor_sync(FULL, v[0], d);
+            return reduce_scatter<1, d>(v, lane);
+        }
+    }
+    return 0;
+}
+
 // 8 rows a tile, [row][512 bytes].  Scores: LPR lanes share a row (16 bytes a
 // lane at a time, so eight lanes read 128 consecutive bytes) and add up their
-// parts by shuffles; the tile's scores go through a small array in shared
-// memory, in which a lane then holds the values of one head, j = lane % GP.
-// Output: a lane owns 4 channels of every head.
+// parts; the tile's scores go through a small array in shared memory, in which
+// a lane then holds the values of one head, j = lane % GP.  Output: a lane owns
+// 4 channels of every head, the weights come back as pairs (p, p).
 template <int GP>
 struct TilesF32 {
     using T = float;
@@ -352,9 +401,10 @@ struct TilesF32 {
     static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
+    static constexpr int BR = TR / RP * GP <= 32 ? TR / RP : 32 / GP;  // of those, summed together
     static constexpr int NV = (TR * GP + 31) / 32;
-    float4 qv[GP][QV];
-    float4 o[GP];
+    uint64_t qv[GP][QV][2];
+    uint64_t o[GP][2];
     float mrun, lrun;
 
     static __device__ __forceinline__ void load(unsigned char* dst, const CUtensorMap* tk, const CUtensorMap* tv,
@@ -366,40 +416,48 @@ struct TilesF32 {
 #pragma unroll
         for (int j = 0; j < GP; ++j) {
 #pragma unroll
-            for (int i = 0; i < QV; ++i)
-                qv[j][i] = j < g ? *reinterpret_cast<const float4*>(q + j * stride + 4 * ((lane % LPR) + LPR * i))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < QV; ++i) {
+                const float4 x = j < g ? *reinterpret_cast<const float4*>(q + j * stride + 4 * ((lane % LPR) + LPR * i))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                qv[j][i][0] = pair(x.x, x.y);
+                qv[j][i][1] = pair(x.z, x.w);
+            }
+            o[j][0] = o[j][1] = 0;
         }
         mrun = -INFINITY;
         lrun = 0.f;
     }
-    __device__ __forceinline__ void tile(unsigned char* stage, float* ps, int n, float qscale, int g, float* scores,
+    __device__ __forceinline__ void tile(unsigned char* stage, float2* ps, int n, float qscale, int g, float* scores,
                                          size_t rows, int lane) {
-        const float4* K = reinterpret_cast<const float4*>(stage);
-        const float4* V = reinterpret_cast<const float4*>(stage + STAGE / 2);
+        const ulonglong2* K = reinterpret_cast<const ulonglong2*>(stage);
+        const ulonglong2* V = reinterpret_cast<const ulonglong2*>(stage + STAGE / 2);
 #pragma unroll
-        for (int rr = 0; rr < TR / RP; ++rr) {
-            const int row = rr * RP + lane / LPR;
-            float s[GP];
+        for (int b = 0; b < TR / RP; b += BR) {
+            float s[BR * GP];
 #pragma unroll
-            for (int j = 0; j < GP; ++j) s[j] = 0.f;
+            for (int rr = 0; rr < BR; ++rr) {
+                const int row = (b + rr) * RP + lane / LPR;
+                uint64_t acc[GP];
 #pragma unroll
-            for (int i = 0; i < QV; ++i) {
-                const float4 k = K[row * 32 + (lane % LPR) + LPR * i];
+                for (int j = 0; j < GP; ++j) acc[j] = 0;
+#pragma unroll
+                for (int i = 0; i < QV; ++i) {
+                    const ulonglong2 k = K[row * 32 + (lane % LPR) + LPR * i];
+#pragma unroll
+                    for (int j = 0; j < GP; ++j) acc[j] = fma2(qv[j][i][1], k.y, fma2(qv[j][i][0], k.x, acc[j]));
+                }
 #pragma unroll
                 for (int j = 0; j < GP; ++j) {
-                    s[j] = fmaf(qv[j][i].x, k.x, s[j]);
-                    s[j] = fmaf(qv[j][i].y, k.y, s[j]);
-                    s[j] = fmaf(qv[j][i].z, k.z, s[j]);
-                    s[j] = fmaf(qv[j][i].w, k.w, s[j]);
+                    const float2 f = unpair(acc[j]);
+                    s[rr * GP + j] = f.x + f.y;
                 }
             }
+            const int x0 = reduce_scatter<BR * GP, LPR>(s, lane % LPR);
+            constexpr int KEPT = BR * GP > LPR ? BR * GP / LPR : 1;
 #pragma unroll
-            for (int j = 0; j < GP; ++j) {
-#pragma unroll
-                for (int d = LPR / 2; d > 0; d >>= 1) s[j] += __shfl_xor_sync(FULL, s[j], d);
-                if (lane % LPR == j % LPR) ps[row * GP + j] = s[j];
+            for (int i = 0; i < KEPT; ++i) {
+                const int x = x0 + i;
+                ps[((b + x / GP) * RP + lane / LPR) * GP + x % GP].x = s[i];
             }
         }
         __syncwarp();
@@ -408,7 +466,7 @@ struct TilesF32 {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int x = lane + 32 * i, r = x / GP;
-            v[i] = x < TR * GP && r < n ? ps[x] * qscale : -INFINITY;
+            v[i] = x < TR * GP && r < n ? ps[x].x * qscale : -INFINITY;
             if (scores && x < TR * GP && j < g) scores[(size_t)j * rows + r] = v[i];
             tm = fmaxf(tm, v[i]);
         }
@@ -423,28 +481,28 @@ struct TilesF32 {
         for (int i = 0; i < NV; ++i) {
             const float p = ex2(v[i] - ms);
             lrun += p;
-            if (lane + 32 * i < TR * GP) ps[lane + 32 * i] = p;
+            if (lane + 32 * i < TR * GP) ps[lane + 32 * i] = make_float2(p, p);
         }
         if (__any_sync(FULL, grew)) {
 #pragma unroll
             for (int jj = 0; jj < GP; ++jj) {
                 const float w = __shfl_sync(FULL, sc, jj);
-                o[jj].x *= w;
-                o[jj].y *= w;
-                o[jj].z *= w;
-                o[jj].w *= w;
+                const uint64_t ww = pair(w, w);
+                o[jj][0] = fma2(o[jj][0], ww, 0);
+                o[jj][1] = fma2(o[jj][1], ww, 0);
             }
         }
         __syncwarp();
-        for (int r = 0; r < n; ++r) {  // rows not held are not read
-            const float4 vv = V[r * 32 + lane];
+#pragma unroll
+        for (int r = 0; r < TR; ++r) {
+            if (r >= n) break;  // rows not held are not read
+            const ulonglong2 vv = V[r * 32 + lane];
+            const uint64_t* pp = reinterpret_cast<const uint64_t*>(ps + r * GP);
 #pragma unroll
             for (int jj = 0; jj < GP; ++jj) {
-                const float p = ps[r * GP + jj];
-                o[jj].x = fmaf(p, vv.x, o[jj].x);
-                o[jj].y = fmaf(p, vv.y, o[jj].y);
-                o[jj].z = fmaf(p, vv.z, o[jj].z);
-                o[jj].w = fmaf(p, vv.w, o[jj].w);
+                const uint64_t p = pp[jj];
+                o[jj][0] = fma2(p, vv.x, o[jj][0]);
+                o[jj][1] = fma2(p, vv.y, o[jj][1]);
             }
         }
     }
@@ -459,10 +517,11 @@ struct TilesF32 {
         for (int j = 0; j < GP; ++j) {
             const float wj = __shfl_sync(FULL, w, j);
             if (j < g) {
-                put(j, 4 * lane, o[j].x * wj);
-                put(j, 4 * lane + 1, o[j].y * wj);
-                put(j, 4 * lane + 2, o[j].z * wj);
-                put(j, 4 * lane + 3, o[j].w * wj);
+                const float2 x = unpair(o[j][0]), y = unpair(o[j][1]);
+                put(j, 4 * lane, x.x * wj);
+                put(j, 4 * lane + 1, x.y * wj);
+                put(j, 4 * lane + 2, y.x * wj);
+                put(j, 4 * lane + 3, y.y * wj);
             }
         }
     }
@@ -470,8 +529,7 @@ struct TilesF32 {
 
 // ---------------------------------------------------------------- attention
 struct Seg {
-    int u, nt;    // unit (-1: none), its tiles
-    long long a;  // its first tile
+    int u, nt, a;  // unit (-1: none), its tiles, its first tile
 };
 
 template <typename E>
@@ -483,52 +541,36 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     extern __shared__ unsigned char smem_raw[];
     // swizzled tiles need 1024-byte alignment
     unsigned char* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ long long pre[NT];
+    __shared__ int pre[NT];
     __shared__ __align__(8) uint64_t full[NW][NST];
     __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
     __shared__ Seg segs[NW][2];     // partials left: [0] in a.head, [1] in the warp's ring
-    __shared__ float scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
+    __shared__ __align__(16) float2 scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) ptx::mbar_init(&full[warp][i], 1);
         ptx::fence_barrier_init();
         segs[warp][0].u = segs[warp][1].u = -1;
     }
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tmap(&tk);
+        ptx::prefetch_tmap(&tv);
+    }
     ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
-    if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
-    const long long total = scan_tiles<TR, NT>(a.c, pre);
-    const int n_cta = ctas_used(total, NW, gridDim.x);
-    // units without rows: nothing else writes their outputs
-    for (int s = blockIdx.x; s < a.c.seqs; s += gridDim.x)
-        if (rows_held(a.c, s) == 0)
-            for (long long i = threadIdx.x; i < (long long)a.c.heads * a.g * D; i += NT) {
-                const size_t o = (size_t)s * a.c.heads * a.g;
-                a.out[o * D + i] = 0.f;
-                if (a.lse && i < (long long)a.c.heads * a.g) a.lse[o + i] = -INFINITY;
-            }
-    if (threadIdx.x == 0) {
-        const long long t0 = (int)blockIdx.x < n_cta ? share_begin(total, n_cta, blockIdx.x) : total;
-        Begin b{total, n_cta, a.c.seqs, 0, 0, 0, 0};
-        if (t0 < total) {
-            const Pos p = locate<TR, NT>(a.c, pre, t0);
-            b = Begin{total, n_cta, p.s, p.h, p.k, p.nt, 0};
-        }
-        a.begin[blockIdx.x] = b;
-    }
-    if ((int)blockIdx.x >= n_cta) return;
-    const long long cta_begin = share_begin(total, n_cta, blockIdx.x);
-    const long long cta_end = share_begin(total, n_cta, blockIdx.x + 1);
-    const long long t_begin = share_begin(total, n_cta * NW, blockIdx.x * NW + warp);
-    const long long t_end = share_begin(total, n_cta * NW, blockIdx.x * NW + warp + 1);
+    const int total = scan_tiles<TR, NT>(a.c, pre);
+    const Deal deal(total, Deal::ctas(total, NW, gridDim.x), NW);
+    const bool works = (int)blockIdx.x < deal.n_cta;
+    const int t_begin = works ? deal.begin_warp(blockIdx.x * NW + warp) : 0;
+    const int t_end = works ? deal.begin_warp(blockIdx.x * NW + warp + 1) : 0;
     unsigned char* ring = smem + (size_t)warp * NST * STAGE;
     const size_t pf = part_floats(a.g);
 
     if (t_begin < t_end) {
         // ---- the producer's view: lane l knows the place of tile block + l
-        Pos base = locate<TR, NT>(a.c, pre, t_begin);
-        long long block = t_begin - 32;
+        Pos base = locate<TR, NT>(a.c, pre, t_begin, lane);
+        const Pos here = base;
+        int block = t_begin - 32;
         int p_page = 0, p_slot = 0;
         Pos p{};
         int p_rows = 0;
@@ -539,8 +581,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
                 p = advance<TR>(a.c, base, lane);
                 const int row = p.k * TR;
                 p_rows = min(TR, rows_held(a.c, p.s) - row);
-                p_page = page_of(a.c, p.s, row);
-                p_slot = row % a.c.page;
+                p_page = page_of(a.c, p.s, row, &p_slot);
                 if (p_page < 0) p_rows = 0;
             }
             if (block + 32 < t_end) {
@@ -549,11 +590,10 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
                 base = advance<TR>(a.c, last, 1);
             }
         };
-        auto issue = [&](int st, long long t) {
+        auto issue = [&](int st, int t) {
             if (t >= t_end) return;
             if (t >= block + 32) next_block();
-            const int l = (int)(t - block);
-            if (lane == l) {
+            if (lane == t - block) {
                 meta[warp][st] = make_int4(p.s * a.c.heads + p.h, p_rows, p.k, p.nt);
                 if (p_rows > 0) {
                     ptx::mbar_arrive_expect_tx(&full[warp][st], STAGE);
@@ -569,8 +609,16 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
         __syncwarp();
 
         E e;
-        int u = -1, nt = 0;
-        long long first = 0;  // first tile of unit u
+        int u, nt, first;  // the unit, its tiles, its first tile
+        auto enter = [&](int s, int h, int tiles, int at) {
+            u = s * a.c.heads + h;
+            nt = tiles;
+            first = at;
+            e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
+        };
+        enter(here.s, here.h, here.nt, t_begin - here.k);  // q arrives with the first tiles
+        if (warp == 0 && lane == 0)
+            a.begin[blockIdx.x] = Begin{total, deal.n_cta, here.s, here.h, here.k, here.nt, {0, 0}};
         auto leave = [&](bool tail) {
             if (first >= t_begin && first + nt <= t_end) {
                 // the whole unit was this warp's
@@ -593,19 +641,17 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
         };
         int st = 0, parity = 0;
         bool ok = true;
-        for (long long t = t_begin; t < t_end; ++t) {
+        for (int t = t_begin; t < t_end; ++t) {
             if (!ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr)) {
                 ok = false;
                 break;
             }
             const int4 m = meta[warp][st];
             if (m.x != u) {
-                if (u >= 0) leave(false);
-                u = m.x;
-                nt = m.w;
-                first = t - m.z;
-                const int s = u / a.c.heads, h = u % a.c.heads;
-                e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
+                leave(false);
+                int h;
+                const int s = a.c.by_heads.quot(m.x, &h);
+                enter(s, h, m.w, t - m.z);
             }
             if (m.y > 0)
                 e.tile(ring + st * STAGE, scratch[warp], m.y, a.qscale, a.g,
@@ -632,15 +678,29 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
                 ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr);
             }
         }
-        if (u >= 0) leave(true);
+        leave(true);
     }
+    if (blockIdx.x == 0) {
+        if (total == 0 && threadIdx.x == 0) a.begin[0] = Begin{0, 1, 0, 0, 0, 0, {0, 0}};
+        for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
+    }
+    // units without rows: nothing else writes their outputs
+    for (int s = blockIdx.x; s < a.c.seqs; s += gridDim.x)
+        if (rows_held(a.c, s) == 0)
+            for (long long i = threadIdx.x; i < (long long)a.c.heads * a.g * D; i += NT) {
+                const size_t o = (size_t)s * a.c.heads * a.g;
+                a.out[o * D + i] = 0.f;
+                if (a.lse && i < (long long)a.c.heads * a.g) a.lse[o + i] = -INFINITY;
+            }
+    if (!works) return;
     __syncthreads();
 
     // ---- parts of units that several warps of this CTA hold, merged in warp order
+    const int cta_begin = deal.begin_cta(blockIdx.x), cta_end = deal.begin_cta(blockIdx.x + 1);
     bool leads = false;
     if (lane < 2 * NW) {
         const Seg sg = segs[lane >> 1][lane & 1];
-        const long long tb = share_begin(total, n_cta * NW, blockIdx.x * NW + (lane >> 1));
+        const int tb = deal.begin_warp(blockIdx.x * NW + (lane >> 1));
         leads = sg.u >= 0 && (sg.a >= tb || tb == cta_begin);
     }
     unsigned todo = __ballot_sync(FULL, leads);
@@ -699,28 +759,55 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
 // in common with other CTAs, and adds its tiles' weights to the accumulated
 // ones.
 constexpr int FIN_THREADS = 512;
+constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 
-template <int TR>
+// maximum and sum of head j over the partials of CTAs c0 .. c1, for a whole warp
+__device__ __forceinline__ float2 merge_stats(const AttnArgs& a, size_t pf, int c0, int c1, int j, int lane) {
+    constexpr int PER = MAX_GRID / 32;
+    float m[PER], l[PER], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int q = c0 + lane + 32 * i;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        if (q <= c1) {
+            const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
+            m[i] = src[j];
+            l[i] = src[a.g + j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) M = fmaxf(M, m[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) L += ex2(m[i] - ms) * l[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+    return make_float2(ms, L);
+}
+
+template <int TR, int ATTN_WARPS>
 __global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ float z[2][MAX_G];  // base-2 lse of the first and the last unit
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Begin b = a.begin[i];
-    if (i >= b.n_cta || b.total == 0) return;
-    const long long t0 = share_begin(b.total, b.n_cta, i), t1 = share_begin(b.total, b.n_cta, i + 1);
+    const int total = a.begin[0].total, n_cta = a.begin[0].n_cta;
+    const Begin b = a.begin[i], nx = a.begin[i + 1];  // stale past the last CTA that worked
+    if (i >= n_cta || total == 0) return;
+    const Deal deal(total, n_cta, ATTN_WARPS);
+    const int t0 = deal.begin_cta(i), t1 = deal.begin_cta(i + 1);
     const size_t pf = part_floats(a.g);
     // the unit shared with the CTA before, and the one shared with the CTA behind
-    int us[2] = {-1, -1};
-    long long first[2] = {0, 0};
-    int nts[2] = {0, 0};
+    int us[2] = {-1, -1}, first[2] = {0, 0}, nts[2] = {0, 0};
     if (b.k > 0 || b.nt > t1 - t0) {
         us[0] = b.s * a.c.heads + b.h;
         first[0] = t0 - b.k;
         nts[0] = b.nt;
     }
-    if (i + 1 < b.n_cta) {
-        const Begin nx = a.begin[i + 1];
+    if (i + 1 < n_cta) {
         const int u = nx.s * a.c.heads + nx.h;
         if (nx.k > 0 && u != us[0]) {
             us[1] = u;
@@ -730,54 +817,38 @@ __global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_
     }
     for (int x = 0; x < 2; ++x) {
         if (us[x] < 0) continue;
-        const int c0 = cta_of(b.total, b.n_cta, first[x]), c1 = cta_of(b.total, b.n_cta, first[x] + nts[x] - 1);
+        const int c0 = deal.cta_of(first[x]), c1 = deal.cta_of(first[x] + nts[x] - 1);
         const int parts = c1 - c0 + 1;
+        if (a.mass_out)
+            for (int j = warp; j < a.g; j += FIN_THREADS / 32) {
+                const float2 st = merge_stats(a, pf, c0, c1, j, lane);
+                if (lane == 0) z[x][j] = st.y == 0.f ? -INFINITY : st.x + log2f(st.y);
+            }
         // 32 channels of a head are an item; the unit's CTAs take them in turn
         for (int item = i - c0 + parts * warp; item < a.g * 4; item += parts * (FIN_THREADS / 32)) {
             const int j = item >> 2, c = (item & 3) * 32 + lane;
-            float M = -INFINITY;
-            for (int q = c0 + lane; q <= c1; q += 32) M = fmaxf(M, a.part[((size_t)q * 2 + (q == c0)) * pf + a.g * D + j]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-            const float ms = M == -INFINITY ? 0.f : M;
-            float L = 0.f, o = 0.f;
+            const float2 st = merge_stats(a, pf, c0, c1, j, lane);
+            float o = 0.f;
+#pragma unroll 8
             for (int q = c0; q <= c1; ++q) {
                 const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf;
-                const float f = ex2(src[a.g * D + j] - ms);
-                L += f * src[a.g * D + a.g + j];
-                o += f * src[j * D + c];
+                o += ex2(src[a.g * D + j] - st.x) * src[j * D + c];
             }
             const size_t at = (size_t)us[x] * a.g + j;
-            a.out[at * D + c] = L == 0.f ? 0.f : o / L;
-            if (a.lse && c == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
-        }
-        if (a.mass_out) {
-            for (int j = warp; j < a.g; j += FIN_THREADS / 32) {
-                float M = -INFINITY, L = 0.f;
-                for (int q = c0 + lane; q <= c1; q += 32)
-                    M = fmaxf(M, a.part[((size_t)q * 2 + (q == c0)) * pf + a.g * D + j]);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-                const float ms = M == -INFINITY ? 0.f : M;
-                for (int q = c0 + lane; q <= c1; q += 32) {
-                    const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
-                    L += ex2(src[j] - ms) * src[a.g + j];
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
-                if (lane == 0) z[x][j] = L == 0.f ? -INFINITY : M + log2f(L);
-            }
+            a.out[at * D + c] = st.y == 0.f ? 0.f : o / st.y;
+            if (a.lse && c == 0) a.lse[at] = st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * LN2;
         }
     }
     if (!a.mass_out) return;
     __syncthreads();
     // every warp its part of the share's tiles, a lane four rows at a time
     constexpr int NW = FIN_THREADS / 32;
-    const long long w0 = t0 + share_begin(t1 - t0, NW, warp), w1 = t0 + share_begin(t1 - t0, NW, warp + 1);
-    Pos p = advance<TR>(a.c, Pos{b.s, b.h, b.k, b.nt}, (int)(w0 - t0));
-    for (long long t = w0; t < w1 && p.nt;) {
+    const Deal own(t1 - t0, 1, NW);
+    const int w0 = t0 + own.begin_warp(warp), w1 = t0 + own.begin_warp(warp + 1);
+    Pos p = advance<TR>(a.c, Pos{b.s, b.h, b.k, b.nt}, w0 - t0);
+    for (int t = w0; t < w1 && p.nt;) {
         const int u = p.s * a.c.heads + p.h;
-        const int n = (int)min((long long)(p.nt - p.k), w1 - t);  // tiles of this unit in the part
+        const int n = min(p.nt - p.k, w1 - t);  // tiles of this unit in the part
         const float* zz = u == us[0] ? z[0] : (u == us[1] ? z[1] : a.lse2 + (size_t)u * a.g);
         const float* sc = a.scores + (size_t)u * a.g * a.c.rows;
         const int r1 = min(rows_held(a.c, p.s), (p.k + n) * TR);
@@ -852,7 +923,6 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
     return r == CUDA_SUCCESS;
 }
 
-constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 constexpr int MAX_WARPS = 12;
 
 struct Layout {
@@ -882,7 +952,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& 
         set[dev].store(true, std::memory_order_relaxed);
     }
     cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(E::WARPS * 32), smem, s, a, tk, tv);
-    if (e == cudaSuccess) e = launch_dependent(paged_finish_kernel<E::TR>, dim3(grid), dim3(FIN_THREADS), 0, s, a);
+    if (e == cudaSuccess) e = launch_dependent(paged_finish_kernel<E::TR, E::WARPS>, dim3(grid), dim3(FIN_THREADS), 0, s, a);
     return e;
 }
 
@@ -920,6 +990,8 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
         if (q_stride[i] * (bf16 ? 2 : 4) & 15) return CKV_ERR_ALIGN;
         a.qst[i] = q_stride[i];
     }
+    // tile numbers are 32-bit: 2^31 tiles of fp32 rows are 17 TB of K and V
+    if ((long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, 8) > 0x7ffffff0LL) return CKV_ERR_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(mass_in) || !aligned16(mass_out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return CKV_ERR_ALIGN;
     const Layout l = layout_of(a.c, g, mass_out != nullptr);
     if (workspace_bytes < (int64_t)l.total) return CKV_ERR_CAPACITY;
