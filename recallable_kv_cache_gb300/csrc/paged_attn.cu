@@ -192,7 +192,7 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0,
 template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
-    static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0;
+    static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0, PER_SM = 1, SHARES = 1;
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -397,7 +397,7 @@ __device__ __forceinline__ int reduce_scatter(float* v, int lane) {
 template <int GP>
 struct TilesF32 {
     using T = float;
-    static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP;
+    static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP, PER_SM = 1, SHARES = 1;
     static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
@@ -533,7 +533,7 @@ struct Seg {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(E::WARPS * 32, 1)
+__global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
     constexpr int TR = E::TR, NW = E::WARPS, NST = E::NST, NT = NW * 32;
@@ -570,6 +570,17 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
         // ---- the producer's view: lane l knows the place of tile block + l
         Pos base = locate<TR, NT>(a.c, pre, t_begin, lane);
         const Pos here = base;
+        E e;
+        int u, nt, first;  // the unit, its tiles, its first tile
+        auto enter = [&](int s, int h, int tiles, int at) {
+            u = s * a.c.heads + h;
+            nt = tiles;
+            first = at;
+            e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
+        };
+        // q is asked for before the tiles: behind them it would wait for all
+        // the copies in flight (some 4 us at full bandwidth)
+        enter(here.s, here.h, here.nt, t_begin - here.k);
         int block = t_begin - 32;
         int p_page = 0, p_slot = 0;
         Pos p{};
@@ -608,15 +619,6 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
         for (int i = 0; i < NST; ++i) issue(i, t_begin + i);
         __syncwarp();
 
-        E e;
-        int u, nt, first;  // the unit, its tiles, its first tile
-        auto enter = [&](int s, int h, int tiles, int at) {
-            u = s * a.c.heads + h;
-            nt = tiles;
-            first = at;
-            e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
-        };
-        enter(here.s, here.h, here.nt, t_begin - here.k);  // q arrives with the first tiles
         if (warp == 0 && lane == 0)
             a.begin[blockIdx.x] = Begin{total, deal.n_cta, here.s, here.h, here.k, here.nt, {0, 0}};
         auto leave = [&](bool tail) {
@@ -759,30 +761,24 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
 // in common with other CTAs, and adds its tiles' weights to the accumulated
 // ones.
 constexpr int FIN_THREADS = 512;
-constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
+constexpr int MAX_GRID = 2048;  // CTAs a workspace is laid out for
 
 // maximum and sum of head j over the partials of CTAs c0 .. c1, for a whole warp
 __device__ __forceinline__ float2 merge_stats(const AttnArgs& a, size_t pf, int c0, int c1, int j, int lane) {
-    constexpr int PER = MAX_GRID / 32;
-    float m[PER], l[PER], M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int q = c0 + lane + 32 * i;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        if (q <= c1) {
-            const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
-            m[i] = src[j];
-            l[i] = src[a.g + j];
-        }
+    float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+    for (int q = c0 + lane; q <= c1; q += 32) {
+        const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
+        const float m = src[j], l = src[a.g + j];
+        const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
+        L = L * ex2(M - ms) + l * ex2(m - ms);
+        M = mn;
     }
+    float T = M;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) M = fmaxf(M, m[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-    const float ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) L += ex2(m[i] - ms) * l[i];
+    for (int o = 16; o > 0; o >>= 1) T = fmaxf(T, __shfl_xor_sync(FULL, T, o));
+    const float ms = T == -INFINITY ? 0.f : T;
+    L *= ex2(M - ms);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
     return make_float2(ms, L);
@@ -942,7 +938,12 @@ Layout layout_of(const Cache& c, int g, bool with_mass) {
 }
 
 template <typename E>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int grid, int dev, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
+    const long long most = (long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, E::TR);  // tiles
+    const long long useful = (most + E::WARPS * MIN_TILES - 1) / (E::WARPS * MIN_TILES);
+    int grid = sms * E::PER_SM * E::SHARES;
+    if (grid > MAX_GRID) grid = MAX_GRID;
+    if (grid > useful) grid = (int)useful;
     static_assert(E::WARPS <= MAX_WARPS, "workspace layout");
     constexpr size_t smem = (size_t)E::WARPS * E::NST * STAGE + 1024;
     static std::atomic<bool> set[MAX_DEVICES];
@@ -1010,9 +1011,8 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.scores = mass_out ? reinterpret_cast<float*>(w + l.scores) : nullptr;
     a.wait_limit = WAIT_LIMIT;
     int dev = 0;
-    int grid = sm_count(&dev);
+    const int grid = sm_count(&dev);
     if (grid < 1) return CKV_ERR_CUDA;
-    if (grid > MAX_GRID) grid = MAX_GRID;
     const int tile_rows = bf16 ? TilesBf16<1>::TR : TilesF32<1>::TR;
     CUtensorMap tk, tv;
     if (!encode_pool(&tk, a.c, a.c.K, a.c.ks, bf16, tile_rows) || !encode_pool(&tv, a.c, a.c.V, a.c.vs, bf16, tile_rows))
