@@ -369,7 +369,8 @@ ckv_status ckv_sparse_decode_attn_noalloc(const void* q, int32_t q_dtype, const 
  * [0, R] is clamped (CKV_DEV_BAD_COUNT), a page id outside [0, n_pages) is
  * skipped with its rows (CKV_DEV_BAD_INDEX).
  * Common errors: CKV_ERR_ARG (null pointer, d != 128, page_size not a multiple
- * of 16, a non-positive extent, R above 2^31 - 17, a stride too small),
+ * of 16, a non-positive extent, R above 2^31 - 17, a stride too small or above
+ * 2^37 elements),
  * CKV_ERR_DTYPE, CKV_ERR_ALIGN. */
 typedef struct {
     void* K;
@@ -424,11 +425,12 @@ ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int
  * arithmetic on products of the operands as they are.  Values of rows not held
  * are never used, whatever they are; held rows must be finite.
  * Results do not depend on the order in which the GPU runs the blocks.
- * workspace: caller-owned, 256-byte aligned, at least the size given above; its
- * contents need no initialisation and are not kept, but calls that can overlap
- * on the GPU (two streams, two graphs) need workspaces of their own.
+ * workspace: caller-owned, 256-byte aligned, at least the size given above,
+ * zeroed by the caller before its first use (every call leaves the counters at
+ * its start zero again).  Calls that can overlap on the GPU (two streams, two
+ * graphs) need workspaces of their own.
  * Errors: as above; CKV_ERR_ARG (g outside [1, 16], scale not finite, mass_in
- * without mass_out), CKV_ERR_CAPACITY (workspace too small). */
+ * without mass_out, seqs * heads * R of 2^34 and more), CKV_ERR_CAPACITY (workspace too small). */
 ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, int32_t q_dtype, const int64_t* q_stride,
                                  int32_t g, float scale, float* out, float* lse, const float* mass_in,
                                  float* mass_out, void* workspace, int64_t workspace_bytes, void* stream);

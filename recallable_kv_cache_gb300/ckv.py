@@ -371,7 +371,8 @@ class PagedCache:
 
     ``g`` is the number of query heads per KV head.  The handle keeps the
     tensors alive and owns the attention's workspace, allocated here (so that
-    every call may be captured into a CUDA graph).  Like a Context, one handle
+    every call may be captured into a CUDA graph; the handle itself is made
+    outside a capture).  Like a Context, one handle
     must not be used from two streams at the same time; another handle over the
     same tensors has a workspace of its own.  Calls run on the tensors' device,
     on ``stream`` or that device's current stream.  A tensor of another shape,
@@ -418,7 +419,9 @@ class PagedCache:
         need = ctypes.c_int64()
         _check(so.ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),
                "ckv_paged_attn_workspace")
-        self.workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=self.device)
+        self.workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        self.workspace[:4096].zero_()  # the counters; calls leave them zero
+        torch.cuda.current_stream(self.device).synchronize()  # whatever stream the first call is on
         self._workspace = (ptr(self.workspace), need.value)
 
     def _tensor(self, name, t, shape, dtype, contiguous=True):

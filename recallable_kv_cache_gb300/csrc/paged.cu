@@ -460,79 +460,88 @@ cudaError_t launch_evict_select(const SelectArgs& a, int sms, int dev, cudaStrea
 }
 
 // ---------------------------------------------------------------- eviction: moves
-constexpr int APPLY_THREADS = 256;
+constexpr int APPLY_THREADS = 128;
+constexpr int BATCH = 16;  // moves of a warp at a time
 
 struct ApplyArgs {
     Cache c;
     int budget, max_moves;
-    FastDiv by_blocks;  // blocks per unit
+    FastDiv by_warps;  // warps per unit
+    int units;
     const int32_t* moves;
     const int32_t* n_moves;
 };
 
-// VPR threads carry one row, 16 bytes of K and of V each, and have IN_FLIGHT
-// rows under way.
+// A warp takes BATCH moves: lane l looks up the page of move l's source, lane
+// 16 + l that of its destination, so that the chain count -> moves -> page ids
+// -> rows is walked once for all of them; then VPR lanes carry a row, 16 bytes
+// of K and of V each, with IN_FLIGHT rows under way.
 template <int VPR>
 __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid_constant__ ApplyArgs a) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    constexpr int ROWS = APPLY_THREADS / VPR;
-    int b, h;
-    const int u = a.by_blocks.quot(blockIdx.x, &b), s = a.c.by_heads.quot(u, &h);
+    const int lane = threadIdx.x & 31;
+    int first, h;
+    const int u = a.by_warps.quot(blockIdx.x * (APPLY_THREADS / 32) + (threadIdx.x >> 5), &first);
+    if (u >= a.units) return;
+    const int s = a.c.by_heads.quot(u, &h);
     int n = a.n_moves[u];
     if (n < 0 || n > a.max_moves) {
-        if (b == 0 && threadIdx.x == 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+        if (first == 0 && lane == 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
         n = n < 0 ? 0 : a.max_moves;
     }
-    const int2* mv = reinterpret_cast<const int2*>(a.moves) + (size_t)u * a.max_moves;
-    const int piece = threadIdx.x % VPR;
+    const int32_t* mv = a.moves + (size_t)u * a.max_moves * 2;
     const size_t o = (size_t)u * a.c.rows;
-    unsigned char* K = a.c.K + h * a.c.ks[1] + piece * 16;
-    unsigned char* V = a.c.V + h * a.c.vs[1] + piece * 16;
-    for (int k0 = b * ROWS * IN_FLIGHT + threadIdx.x / VPR; k0 < n; k0 += a.by_blocks.d * ROWS * IN_FLIGHT) {
-        int2 m[IN_FLIGHT];
-        int p0[IN_FLIGHT], p1[IN_FLIGHT], s0[IN_FLIGHT], s1[IN_FLIGHT];
-        uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
-        float mass[IN_FLIGHT];
-        int pos[IN_FLIGHT];
-#pragma unroll
-        for (int x = 0; x < IN_FLIGHT; ++x)
-            if (k0 + x * ROWS < n) m[x] = mv[k0 + x * ROWS];
-#pragma unroll
-        for (int x = 0; x < IN_FLIGHT; ++x) {
-            p0[x] = p1[x] = -1;
-            if (k0 + x * ROWS >= n) continue;
-            const int src = m[x].x, dst = m[x].y;
-            if (src < a.budget || src >= a.c.rows || dst < 0 || dst >= a.budget || dst >= a.c.rows) {
+    constexpr int RP = 32 / VPR;  // rows at a time
+    const int piece = (lane % VPR) * 16, sub = lane / VPR;
+    for (int k0 = first * BATCH; k0 < n; k0 += (int)a.by_warps.d * BATCH) {
+        const int k = k0 + (lane & 15);
+        const bool is_dst = lane >= 16;
+        int row = -1;
+        if (k < n) {
+            row = mv[2 * k + is_dst];
+            if (is_dst ? row < 0 || row >= a.budget || row >= a.c.rows : row < a.budget || row >= a.c.rows) {
                 report(a.c.dev_err, CKV_DEV_BAD_INDEX);
-                continue;
-            }
-            p0[x] = page_of(a.c, s, src, &s0[x]);
-            p1[x] = page_of(a.c, s, dst, &s1[x]);
-        }
-#pragma unroll
-        for (int x = 0; x < IN_FLIGHT; ++x) {
-            if (p0[x] < 0 || p1[x] < 0) continue;
-            kv[x] = *reinterpret_cast<const uint4*>(K + p0[x] * a.c.ks[0] + s0[x] * a.c.ks[2]);
-            vv[x] = *reinterpret_cast<const uint4*>(V + p0[x] * a.c.vs[0] + s0[x] * a.c.vs[2]);
-            if (piece == 0) {
-                if (a.c.mass) mass[x] = a.c.mass[o + m[x].x];
-                if (a.c.pos) pos[x] = a.c.pos[o + m[x].x];
+                row = -1;
             }
         }
+        int slot = 0;
+        const int pg = row < 0 ? -1 : page_of(a.c, s, row, &slot);
+        const long long ko = pg * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2];
+        const long long vo = pg * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2];
+        const int dst = __shfl_sync(FULL, row, (lane & 15) + 16);
+        const unsigned known = __ballot_sync(FULL, pg >= 0);
+        const unsigned good = known & (known >> 16);  // bit l: move l
+        if (lane < 16 && ((good >> lane) & 1)) {
+            if (a.c.mass) a.c.mass[o + dst] = a.c.mass[o + row];
+            if (a.c.pos) a.c.pos[o + dst] = a.c.pos[o + row];
+        }
 #pragma unroll
-        for (int x = 0; x < IN_FLIGHT; ++x) {
-            if (p0[x] < 0 || p1[x] < 0) continue;
-            *reinterpret_cast<uint4*>(K + p1[x] * a.c.ks[0] + s1[x] * a.c.ks[2]) = kv[x];
-            *reinterpret_cast<uint4*>(V + p1[x] * a.c.vs[0] + s1[x] * a.c.vs[2]) = vv[x];
-            if (piece == 0) {
-                if (a.c.mass) a.c.mass[o + m[x].y] = mass[x];
-                if (a.c.pos) a.c.pos[o + m[x].y] = pos[x];
+        for (int b = 0; b < BATCH; b += RP * IN_FLIGHT) {
+            if (k0 + b >= n) break;
+            uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
+#pragma unroll
+            for (int x = 0; x < IN_FLIGHT; ++x) {
+                const int m = b + x * RP + sub;
+                const long long ks = __shfl_sync(FULL, ko, m), vs = __shfl_sync(FULL, vo, m);
+                if ((good >> m) & 1) {
+                    kv[x] = *reinterpret_cast<const uint4*>(a.c.K + ks + piece);
+                    vv[x] = *reinterpret_cast<const uint4*>(a.c.V + vs + piece);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < IN_FLIGHT; ++x) {
+                const int m = b + x * RP + sub;
+                const long long kd = __shfl_sync(FULL, ko, m + 16), vd = __shfl_sync(FULL, vo, m + 16);
+                if ((good >> m) & 1) {
+                    *reinterpret_cast<uint4*>(a.c.K + kd + piece) = kv[x];
+                    *reinterpret_cast<uint4*>(a.c.V + vd + piece) = vv[x];
+                }
             }
         }
     }
     // nothing in this kernel reads lens
-    if (h == 0 && b == 0 && threadIdx.x == 0 && a.c.lens[s] > a.budget) a.c.lens[s] = a.budget;
+    if (h == 0 && first == 0 && lane == 0 && a.c.lens[s] > a.budget) a.c.lens[s] = a.budget;
 }
 
 }  // namespace
@@ -638,18 +647,21 @@ extern "C" ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_
     a.moves = moves;
     a.n_moves = n_moves;
     const int vpr = D * (cache->kv_dtype == CKV_BF16 ? 2 : 4) / 16;
-    const int per_pass = APPLY_THREADS / vpr * IN_FLIGHT;
     const long long units = (long long)a.c.seqs * a.c.heads;
     const int sms = sm_count(nullptr);
     if (sms < 1) return CKV_ERR_CUDA;
-    // as many blocks as the moves could keep busy, up to eight to an SM in all
-    long long blocks = ((long long)max_moves + per_pass - 1) / per_pass;
-    const long long most = (8LL * sms + units - 1) / units;
-    if (blocks > most) blocks = most;
-    if (blocks < 1) blocks = 1;
-    a.by_blocks = FastDiv((uint32_t)blocks);
+    // as many warps as the moves could keep busy, up to 32 to an SM in all
+    long long warps = ceil_div(max_moves, BATCH);
+    const long long most = (32LL * sms + units - 1) / units;
+    if (warps > most) warps = most;
+    if (warps < 1) warps = 1;
+    a.by_warps = FastDiv((uint32_t)warps);
+    a.units = (int)units;
+    const long long blocks = (warps * units + APPLY_THREADS / 32 - 1) / (APPLY_THREADS / 32);
+    if (blocks * (APPLY_THREADS / 32) > 0x7fffffffLL || (long long)max_moves + warps * BATCH > 0x7fffffffLL)
+        return CKV_ERR_ARG;
     cudaStream_t s = (cudaStream_t)stream;
-    const dim3 grid((unsigned)(blocks * units)), block(APPLY_THREADS);
+    const dim3 grid((unsigned)blocks), block(APPLY_THREADS);
     const cudaError_t e = vpr == 16 ? launch_dependent(paged_apply_kernel<16>, grid, block, 0, s, a)
                                     : launch_dependent(paged_apply_kernel<32>, grid, block, 0, s, a);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;

@@ -15,8 +15,10 @@
 // unnormalised output in registers.  A tile never crosses a page (pages are
 // multiples of 16 rows).  Where a unit ends inside the warp's share its result
 // is final; the parts of a unit that several warps share are merged in tile
-// order, first inside the CTA, then (paged_finish_kernel) across CTAs, so the
-// result does not depend on timing.
+// order, first inside the CTA, then across CTAs by the one that finishes its
+// part last, so the result does not depend on timing.  Where the accumulated
+// weights are wanted the scores are left in the workspace, and
+// paged_weights_kernel adds e^{s - lse}.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -41,13 +43,6 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int STAGE = 8192;  // K rows, then V rows of one tile
 
-// Where a CTA's share of the tiles begins: left for the finish kernel.
-struct __align__(16) Begin {
-    int total, n_cta;  // tiles of the call, CTAs that share them
-    int s, h, k, nt;   // the first tile: sequence, KV head, tile in the unit, tiles of the unit
-    int pad[2];
-};
-
 struct AttnArgs {
     Cache c;
     const void* q;
@@ -58,10 +53,12 @@ struct AttnArgs {
     float* lse;
     const float* mass_in;
     float* mass_out;
-    Begin* begin;   // [grid + 1]
-    float* part;    // [grid][2] partials of units that several CTAs share
-    float* head;    // [grid][warps] partials of a unit that a warp entered part-way and left
-    float* lse2;    // [units][g], base 2
+    unsigned* arrived;  // [grid] CTAs that have left their part of the unit that begins in CTA i; zero between calls
+    int4* start;        // [grid][warps] where a warp's tiles begin: sequence, KV head, tile in the unit, tiles of the unit
+    int2* deal;         // tiles of the call, CTAs that share them
+    float* part;        // [grid][2] partials of units that several CTAs share
+    float* head;        // [grid][warps] partials of a unit that a warp entered part-way and left
+    float* lse2;        // [units][g], base 2
     float* scores;  // [units][g][rows], base 2
     long long wait_limit;
 };
@@ -94,55 +91,6 @@ __device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
     }
     return p;
 }
-// Exclusive prefix sums of the sequences' tiles, one per thread's chunk of
-// sequences; returns the total (below 2^31, checked for the cache's extents).
-template <int TR, int NT>
-__device__ int scan_tiles(const Cache& c, int* pre) {
-    __shared__ int warp_sum[NT / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int chunk = (c.seqs + NT - 1) / NT;
-    int v = 0;
-    for (int s = tid * chunk; s < min(c.seqs, (tid + 1) * chunk); ++s) v += tiles_of<TR>(c, s);
-    v *= c.heads;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    int base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) base += warp_sum[w];
-        total += warp_sum[w];
-    }
-    pre[tid] = base + x - v;
-    __syncthreads();
-    return total;
-}
-// the place of tile t < total, for a whole warp
-template <int TR, int NT>
-__device__ Pos locate(const Cache& c, const int* pre, int t, int lane) {
-    const int chunk = (c.seqs + NT - 1) / NT;
-    int at = -1;  // the last chunk with pre <= t holds t; a lane looks at NT / 32 of them in a row
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i)
-        if (pre[lane * (NT / 32) + i] <= t) at = lane * (NT / 32) + i;
-    at = __reduce_max_sync(FULL, at);
-    int left = t - pre[at];
-    Pos p{at * chunk, 0, 0, 0};
-    for (; p.s < c.seqs; ++p.s) {
-        p.nt = tiles_of<TR>(c, p.s);
-        if (left < p.nt * c.heads) break;
-        left -= p.nt * c.heads;
-    }
-    if (p.s >= c.seqs) return Pos{c.seqs, 0, 0, 0};
-    p.h = left / p.nt;
-    p.k = left % p.nt;
-    return p;
-}
 // The deal: `total` tiles to the warps of n_cta CTAs, in order, as evenly as
 // they go (shares of q + 1 tiles, then of q).  A warp gets at least MIN_TILES
 // before the work is spread over more CTAs.
@@ -164,6 +112,54 @@ struct Deal {
         return w / warps;
     }
 };
+
+// The deal of this call, and where the shares of this CTA's warps begin.  Every
+// thread adds up a chunk of the sequences' tiles; a scan gives the total (below
+// 2^31, checked for the cache's extents) and the thread in whose chunk a
+// warp's first tile falls leaves its place.
+template <int TR, int NT>
+__device__ Deal deal_out(const Cache& c, int4* start) {
+    constexpr int NW = NT / 32;
+    __shared__ int warp_sum[NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (c.seqs + NT - 1) / NT;
+    const int s0 = tid * chunk, s1 = min(c.seqs, s0 + chunk);
+    int v = 0;
+    for (int s = s0; s < s1; ++s) v += tiles_of<TR>(c, s);
+    v *= c.heads;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = x - v, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    const Deal deal(total, Deal::ctas(total, NW, gridDim.x), NW);
+    if (v > 0 && before < deal.begin_cta(blockIdx.x + 1) && before + v > deal.begin_cta(blockIdx.x)) {
+        int s = s0, nt = 0, at = before;  // first tile of sequence s
+        for (int w = 0; w < NW; ++w) {
+            const int t = deal.begin_warp(blockIdx.x * NW + w);
+            if (t < before || t >= before + v) continue;
+            while (true) {
+                nt = tiles_of<TR>(c, s);
+                if (t - at < nt * c.heads) break;
+                at += nt * c.heads;
+                ++s;
+            }
+            const int h = (t - at) / nt;
+            start[w] = make_int4(s, h, t - at - h * nt, nt);
+        }
+    }
+    __syncthreads();
+    return deal;
+}
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
     asm volatile(
@@ -192,7 +188,7 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0,
 template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
-    static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0, PER_SM = 1, SHARES = 1;
+    static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0;
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -397,7 +393,7 @@ __device__ __forceinline__ int reduce_scatter(float* v, int lane) {
 template <int GP>
 struct TilesF32 {
     using T = float;
-    static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP, PER_SM = 1, SHARES = 1;
+    static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP;
     static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
@@ -532,8 +528,79 @@ struct Seg {
     int u, nt, a;  // unit (-1: none), its tiles, its first tile
 };
 
+// Merges the parts of unit u that CTAs c0 .. c1 left, in their order; by a
+// whole CTA, `red` its shared memory.
+template <int NT>
+__device__ void merge_parts(const AttnArgs& a, size_t pf, int u, int c0, int c1, float* red) {
+    __shared__ float stat[2][MAX_G];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int j = warp; j < a.g; j += NT / 32) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+        for (int q = c0 + lane; q <= c1; q += 32) {
+            const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
+            const float m = __ldcg(src + j), l = __ldcg(src + a.g + j);
+            const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
+            L = L * ex2(M - ms) + l * ex2(m - ms);
+            M = mn;
+        }
+        float T = M;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) T = fmaxf(T, __shfl_xor_sync(FULL, T, o));
+        const float ms = T == -INFINITY ? 0.f : T;
+        L *= ex2(M - ms);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+        if (lane == 0) {
+            stat[0][j] = ms;
+            stat[1][j] = L;
+            const float z = L == 0.f ? -INFINITY : ms + log2f(L);
+            a.lse2[(size_t)u * a.g + j] = z;
+            if (a.lse) a.lse[(size_t)u * a.g + j] = z * LN2;
+        }
+    }
+    __syncthreads();
+    // four channels of a head to a thread, the parts dealt to NS threads of it
+    constexpr int NS = NT / 128;
+    const int slice = tid >> 7, c = (tid & 31) * 4;
+    for (int j0 = 0; j0 < a.g; j0 += 4) {
+        const int j = j0 + ((tid >> 5) & 3);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < a.g) {
+            const float ms = stat[0][j];
+#pragma unroll 4
+            for (int q = c0 + slice; q <= c1; q += NS) {
+                const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf;
+                const float f = ex2(__ldcg(src + a.g * D + j) - ms);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + j * D + c));
+                o.x += f * v.x;
+                o.y += f * v.y;
+                o.z += f * v.z;
+                o.w += f * v.w;
+            }
+        }
+        float4* r = reinterpret_cast<float4*>(red) + tid;
+        *r = o;
+        __syncthreads();
+        if (slice == 0 && j < a.g) {
+#pragma unroll
+            for (int x = 1; x < NS; ++x) {
+                const float4 v = r[x * 128];
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
+            }
+            const float f = stat[1][j] == 0.f ? 0.f : 1.f / stat[1][j];
+            *reinterpret_cast<float4*>(a.out + ((size_t)u * a.g + j) * D + c) =
+                make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        }
+        __syncthreads();
+    }
+}
+
 template <typename E>
-__global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
+__global__ void __launch_bounds__(E::WARPS * 32, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
     constexpr int TR = E::TR, NW = E::WARPS, NST = E::NST, NT = NW * 32;
@@ -541,35 +608,34 @@ __global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
     extern __shared__ unsigned char smem_raw[];
     // swizzled tiles need 1024-byte alignment
     unsigned char* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ int pre[NT];
+    __shared__ int4 start[NW];
     __shared__ __align__(8) uint64_t full[NW][NST];
     __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
-    __shared__ Seg segs[NW][2];     // partials left: [0] in a.head, [1] in the warp's ring
+    __shared__ Seg segs[2 * NW];    // partials left: [2 w] in a.head, [2 w + 1] in the warp's ring
     __shared__ __align__(16) float2 scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
+    __shared__ int4 shared_units[2];  // units shared with other CTAs: unit, first and last CTA
+    __shared__ int last[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) ptx::mbar_init(&full[warp][i], 1);
         ptx::fence_barrier_init();
-        segs[warp][0].u = segs[warp][1].u = -1;
+        segs[2 * warp].u = segs[2 * warp + 1].u = -1;
     }
-    if (threadIdx.x == 0) {
-        ptx::prefetch_tmap(&tk);
-        ptx::prefetch_tmap(&tv);
+    if (threadIdx.x < 2) {
+        ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
+        shared_units[threadIdx.x].x = -1;
+        last[threadIdx.x] = 0;
     }
     ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
-    const int total = scan_tiles<TR, NT>(a.c, pre);
-    const Deal deal(total, Deal::ctas(total, NW, gridDim.x), NW);
-    const bool works = (int)blockIdx.x < deal.n_cta;
+    const Deal deal = deal_out<TR, NT>(a.c, start);
+    const bool works = (int)blockIdx.x < deal.n_cta && deal.total > 0;
     const int t_begin = works ? deal.begin_warp(blockIdx.x * NW + warp) : 0;
     const int t_end = works ? deal.begin_warp(blockIdx.x * NW + warp + 1) : 0;
     unsigned char* ring = smem + (size_t)warp * NST * STAGE;
     const size_t pf = part_floats(a.g);
 
     if (t_begin < t_end) {
-        // ---- the producer's view: lane l knows the place of tile block + l
-        Pos base = locate<TR, NT>(a.c, pre, t_begin, lane);
-        const Pos here = base;
         E e;
         int u, nt, first;  // the unit, its tiles, its first tile
         auto enter = [&](int s, int h, int tiles, int at) {
@@ -578,35 +644,36 @@ __global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
             first = at;
             e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
         };
+        Pos base{start[warp].x, start[warp].y, start[warp].z, start[warp].w};
         // q is asked for before the tiles: behind them it would wait for all
         // the copies in flight (some 4 us at full bandwidth)
-        enter(here.s, here.h, here.nt, t_begin - here.k);
+        enter(base.s, base.h, base.nt, t_begin - base.k);
+        // ---- the producer's view: lane l knows the place of tile block + l
         int block = t_begin - 32;
-        int p_page = 0, p_slot = 0;
+        int p_page = 0, p_slot = 0, p_rows = 0;
         Pos p{};
-        int p_rows = 0;
-        auto next_block = [&]() {
-            block += 32;
-            const bool mine = block + lane < t_end;
-            if (mine) {
-                p = advance<TR>(a.c, base, lane);
-                const int row = p.k * TR;
-                p_rows = min(TR, rows_held(a.c, p.s) - row);
-                p_page = page_of(a.c, p.s, row, &p_slot);
-                if (p_page < 0) p_rows = 0;
-            }
-            if (block + 32 < t_end) {
-                const Pos last{__shfl_sync(FULL, p.s, 31), __shfl_sync(FULL, p.h, 31), __shfl_sync(FULL, p.k, 31),
-                               __shfl_sync(FULL, p.nt, 31)};
-                base = advance<TR>(a.c, last, 1);
-            }
-        };
+        bool gave_up = false, dead = false;  // a copy never landed: the rest of the share is walked without its rows
         auto issue = [&](int st, int t) {
-            if (t >= t_end) return;
-            if (t >= block + 32) next_block();
+            if (t >= block + 32) {
+                block += 32;
+                if (block + lane < t_end) {
+                    p = advance<TR>(a.c, base, lane);
+                    const int row = p.k * TR;
+                    p_rows = min(TR, rows_held(a.c, p.s) - row);
+                    p_page = page_of(a.c, p.s, row, &p_slot);
+                    if (p_page < 0) p_rows = 0;
+                }
+                if (block + 32 < t_end) {
+                    const Pos end{__shfl_sync(FULL, p.s, 31), __shfl_sync(FULL, p.h, 31), __shfl_sync(FULL, p.k, 31),
+                                  __shfl_sync(FULL, p.nt, 31)};
+                    base = advance<TR>(a.c, end, 1);
+                }
+            }
             if (lane == t - block) {
                 meta[warp][st] = make_int4(p.s * a.c.heads + p.h, p_rows, p.k, p.nt);
-                if (p_rows > 0) {
+                if (dead) {
+                    // nothing more is loaded
+                } else if (p_rows > 0) {
                     ptx::mbar_arrive_expect_tx(&full[warp][st], STAGE);
                     E::load(ring + st * STAGE, &tk, &tv, p_page, p.h, p_slot, &full[warp][st]);
                 } else {
@@ -614,13 +681,6 @@ __global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
                 }
             }
         };
-        next_block();
-#pragma unroll
-        for (int i = 0; i < NST; ++i) issue(i, t_begin + i);
-        __syncwarp();
-
-        if (warp == 0 && lane == 0)
-            a.begin[blockIdx.x] = Begin{total, deal.n_cta, here.s, here.h, here.k, here.nt, {0, 0}};
         auto leave = [&](bool tail) {
             if (first >= t_begin && first + nt <= t_end) {
                 // the whole unit was this warp's
@@ -639,51 +699,53 @@ __global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
                         dst[a.g * D + j] = m;
                         dst[a.g * D + a.g + j] = l;
                     });
-            if (lane == 0) segs[warp][tail] = Seg{u, nt, first};
+            if (lane == 0) segs[2 * warp + tail] = Seg{u, nt, first};
         };
         int st = 0, parity = 0;
-        bool ok = true;
-        for (int t = t_begin; t < t_end; ++t) {
-            if (!ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr)) {
-                ok = false;
-                break;
+        // the first NST turns only ask for tiles
+        for (int t = t_begin - NST; t < t_end; ++t) {
+            if (t >= t_begin) {
+                if (!dead && !ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr)) dead = true;
+                if (__any_sync(FULL, dead) && !gave_up) {
+                    dead = gave_up = true;
+                    if (lane == 0) report(a.c.dev_err, CKV_DEV_TIMEOUT);
+                    // the copies in flight get their time
+                    for (int i = 1, s2 = st, p2 = parity; i < NST && t + i < t_end; ++i) {
+                        if (++s2 == NST) {
+                            s2 = 0;
+                            p2 ^= 1;
+                        }
+                        ptx::mbar_wait(&full[warp][s2], p2, a.wait_limit, nullptr);
+                    }
+                }
+                const int4 m = meta[warp][st];
+                if (m.x != u) {
+                    leave(false);
+                    int h;
+                    const int s = a.c.by_heads.quot(m.x, &h);
+                    enter(s, h, m.w, t - m.z);
+                }
+                if (dead) {
+                } else if (m.y > 0)
+                    e.tile(ring + st * STAGE, scratch[warp], m.y, a.qscale, a.g,
+                           a.scores ? a.scores + (size_t)u * a.g * a.c.rows + (size_t)m.z * TR : nullptr, a.c.rows, lane);
+                else if (a.scores)
+                    for (int i = lane; i < TR * a.g; i += 32)
+                        a.scores[((size_t)u * a.g + i / TR) * a.c.rows + (size_t)m.z * TR + i % TR] = -INFINITY;
+                __syncwarp();
             }
-            const int4 m = meta[warp][st];
-            if (m.x != u) {
-                leave(false);
-                int h;
-                const int s = a.c.by_heads.quot(m.x, &h);
-                enter(s, h, m.w, t - m.z);
-            }
-            if (m.y > 0)
-                e.tile(ring + st * STAGE, scratch[warp], m.y, a.qscale, a.g,
-                       a.scores ? a.scores + (size_t)u * a.g * a.c.rows + (size_t)m.z * TR : nullptr, a.c.rows, lane);
-            else if (a.scores)
-                for (int i = lane; i < TR * a.g; i += 32)
-                    a.scores[((size_t)u * a.g + i / TR) * a.c.rows + (size_t)m.z * TR + i % TR] = -INFINITY;
-            __syncwarp();
-            issue(st, t + NST);
+            if (t + NST < t_end) issue(st, t + NST);
             __syncwarp();
             if (++st == NST) {
                 st = 0;
-                parity ^= 1;
-            }
-        }
-        if (!ok) {
-            // a copy never landed: report, give the others in flight their time
-            if (lane == 0) report(a.c.dev_err, CKV_DEV_TIMEOUT);
-            for (int i = 1; i < NST; ++i) {
-                if (++st == NST) {
-                    st = 0;
-                    parity ^= 1;
-                }
-                ptx::mbar_wait(&full[warp][st], parity, a.wait_limit, nullptr);
+                parity ^= t >= t_begin;
             }
         }
         leave(true);
+        if (a.mass_out && lane == 0) a.start[blockIdx.x * NW + warp] = start[warp];
     }
     if (blockIdx.x == 0) {
-        if (total == 0 && threadIdx.x == 0) a.begin[0] = Begin{0, 1, 0, 0, 0, 0, {0, 0}};
+        if (threadIdx.x == 0) *a.deal = make_int2(deal.total, deal.n_cta);
         for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
     }
     // units without rows: nothing else writes their outputs
@@ -697,155 +759,106 @@ __global__ void __launch_bounds__(E::WARPS * 32, E::PER_SM)
     if (!works) return;
     __syncthreads();
 
-    // ---- parts of units that several warps of this CTA hold, merged in warp order
+    // ---- parts of units that several warps of this CTA hold, merged in warp
+    // order: lane l looks after partial l
     const int cta_begin = deal.begin_cta(blockIdx.x), cta_end = deal.begin_cta(blockIdx.x + 1);
+    Seg sg{-1, 0, 0};
+    const float* src = nullptr;
     bool leads = false;
     if (lane < 2 * NW) {
-        const Seg sg = segs[lane >> 1][lane & 1];
-        const int tb = deal.begin_warp(blockIdx.x * NW + (lane >> 1));
+        const int w = lane >> 1, tb = deal.begin_warp(blockIdx.x * NW + w);
+        sg = segs[lane];
+        src = lane & 1 ? reinterpret_cast<const float*>(smem + (size_t)w * NST * STAGE)
+                       : a.head + ((size_t)blockIdx.x * NW + w) * pf;
         leads = sg.u >= 0 && (sg.a >= tb || tb == cta_begin);
     }
-    unsigned todo = __ballot_sync(FULL, leads);
-    for (int item = 0; todo; todo &= todo - 1) {
-        const int cand = __ffs(todo) - 1, w0 = cand >> 1;
-        const Seg sg = segs[w0][cand & 1];
-        const bool whole = sg.a >= cta_begin && sg.a + sg.nt <= cta_end;
+    int item = 0;
+    for (unsigned todo = __ballot_sync(FULL, leads); todo; todo &= todo - 1) {
+        const int cand = __ffs(todo) - 1;
+        const int gu = __shfl_sync(FULL, sg.u, cand), ga = __shfl_sync(FULL, sg.a, cand), gn = __shfl_sync(FULL, sg.nt, cand);
+        const unsigned members = __ballot_sync(FULL, sg.u == gu);
+        const bool whole = ga >= cta_begin && ga + gn <= cta_end;
+        float* part = a.part + ((size_t)blockIdx.x * 2 + (ga >= cta_begin)) * pf;
         for (int j = 0; j < a.g; ++j, ++item) {
             if (item % NW != warp) continue;
-            float M = -INFINITY, L = 0.f;
+            float m = -INFINITY, l = 0.f;
+            if (sg.u == gu) {
+                m = src[a.g * D + j];
+                l = src[a.g * D + a.g + j];
+            }
+            float M = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+            const float f = ex2(m - (M == -INFINITY ? 0.f : M));
+            float L = f * l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int pass = 0; pass < 2; ++pass) {
-                const float ms = M == -INFINITY ? 0.f : M;
-                for (int w = w0; w < NW; ++w) {
-                    const float* src = segs[w][1].u == sg.u ? reinterpret_cast<const float*>(smem + (size_t)w * NST * STAGE)
-                                       : segs[w][0].u == sg.u ? a.head + ((size_t)blockIdx.x * NW + w) * pf
-                                                              : nullptr;
-                    if (!src) continue;
-                    const float m = src[a.g * D + j];
-                    if (pass == 0) {
-                        M = fmaxf(M, m);
-                        continue;
-                    }
-                    const float f = ex2(m - ms);
-                    const float4 v = *reinterpret_cast<const float4*>(src + j * D + 4 * lane);
-                    L += f * src[a.g * D + a.g + j];
-                    o.x += f * v.x;
-                    o.y += f * v.y;
-                    o.z += f * v.z;
-                    o.w += f * v.w;
-                }
+            for (unsigned left = members; left; left &= left - 1) {
+                const int x = __ffs(left) - 1;
+                const float fx = __shfl_sync(FULL, f, x);
+                const float4 v = *reinterpret_cast<const float4*>(
+                    reinterpret_cast<const float*>(__shfl_sync(FULL, (unsigned long long)src, x)) + j * D + 4 * lane);
+                o.x += fx * v.x;
+                o.y += fx * v.y;
+                o.z += fx * v.z;
+                o.w += fx * v.w;
             }
             if (whole) {
-                const float f = L == 0.f ? 0.f : 1.f / L;
-                const size_t at = (size_t)sg.u * a.g + j;
-                *reinterpret_cast<float4*>(a.out + at * D + 4 * lane) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                const float r = L == 0.f ? 0.f : 1.f / L;
+                const size_t at = (size_t)gu * a.g + j;
+                *reinterpret_cast<float4*>(a.out + at * D + 4 * lane) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
                 if (lane == 0) {
                     const float z = L == 0.f ? -INFINITY : M + log2f(L);
                     a.lse2[at] = z;
                     if (a.lse) a.lse[at] = z * LN2;
                 }
             } else {
-                float* dst = a.part + ((size_t)blockIdx.x * 2 + (sg.a >= cta_begin)) * pf;
-                *reinterpret_cast<float4*>(dst + j * D + 4 * lane) = o;
+                *reinterpret_cast<float4*>(part + j * D + 4 * lane) = o;
                 if (lane == 0) {
-                    dst[a.g * D + j] = M;
-                    dst[a.g * D + a.g + j] = L;
+                    part[a.g * D + j] = M;
+                    part[a.g * D + a.g + j] = L;
                 }
             }
         }
+        if (!whole && threadIdx.x == 0)
+            shared_units[ga >= cta_begin] = make_int4(gu, deal.cta_of(ga), deal.cta_of(ga + gn - 1), 0);
     }
+    __syncthreads();
+    // ---- across CTAs: the one that leaves its part of a unit last merges them
+    if (threadIdx.x < 2 && shared_units[threadIdx.x].x >= 0) {
+        const int4 su = shared_units[threadIdx.x];
+        __threadfence();
+        if (atomicAdd(&a.arrived[su.y], 1u) == (unsigned)(su.z - su.y)) {
+            a.arrived[su.y] = 0;  // for the next call
+            last[threadIdx.x] = 1;
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    for (int x = 0; x < 2; ++x)
+        if (last[x])
+            merge_parts<NT>(a, pf, shared_units[x].x, shared_units[x].y, shared_units[x].z, reinterpret_cast<float*>(smem));
 }
 
-// ---------------------------------------------------------------- finish
-// CTA i merges its share of the outputs of the (at most two) units that it has
-// in common with other CTAs, and adds its tiles' weights to the accumulated
-// ones.
-constexpr int FIN_THREADS = 512;
-constexpr int MAX_GRID = 2048;  // CTAs a workspace is laid out for
-
-// maximum and sum of head j over the partials of CTAs c0 .. c1, for a whole warp
-__device__ __forceinline__ float2 merge_stats(const AttnArgs& a, size_t pf, int c0, int c1, int j, int lane) {
-    float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-    for (int q = c0 + lane; q <= c1; q += 32) {
-        const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
-        const float m = src[j], l = src[a.g + j];
-        const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
-        L = L * ex2(M - ms) + l * ex2(m - ms);
-        M = mn;
-    }
-    float T = M;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) T = fmaxf(T, __shfl_xor_sync(FULL, T, o));
-    const float ms = T == -INFINITY ? 0.f : T;
-    L *= ex2(M - ms);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
-    return make_float2(ms, L);
-}
-
-template <int TR, int ATTN_WARPS>
-__global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ float z[2][MAX_G];  // base-2 lse of the first and the last unit
+// ---------------------------------------------------------------- accumulated weights
+// mass_out = mass_in + sum_j e^{s_j - lse_j}: warp for warp the tiles of the
+// attention kernel, a lane four rows at a time.
+template <int TR, int NW>
+__global__ void __launch_bounds__(NW * 32) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int total = a.begin[0].total, n_cta = a.begin[0].n_cta;
-    const Begin b = a.begin[i], nx = a.begin[i + 1];  // stale past the last CTA that worked
-    if (i >= n_cta || total == 0) return;
-    const Deal deal(total, n_cta, ATTN_WARPS);
-    const int t0 = deal.begin_cta(i), t1 = deal.begin_cta(i + 1);
-    const size_t pf = part_floats(a.g);
-    // the unit shared with the CTA before, and the one shared with the CTA behind
-    int us[2] = {-1, -1}, first[2] = {0, 0}, nts[2] = {0, 0};
-    if (b.k > 0 || b.nt > t1 - t0) {
-        us[0] = b.s * a.c.heads + b.h;
-        first[0] = t0 - b.k;
-        nts[0] = b.nt;
-    }
-    if (i + 1 < n_cta) {
-        const int u = nx.s * a.c.heads + nx.h;
-        if (nx.k > 0 && u != us[0]) {
-            us[1] = u;
-            first[1] = t1 - nx.k;
-            nts[1] = nx.nt;
-        }
-    }
-    for (int x = 0; x < 2; ++x) {
-        if (us[x] < 0) continue;
-        const int c0 = deal.cta_of(first[x]), c1 = deal.cta_of(first[x] + nts[x] - 1);
-        const int parts = c1 - c0 + 1;
-        if (a.mass_out)
-            for (int j = warp; j < a.g; j += FIN_THREADS / 32) {
-                const float2 st = merge_stats(a, pf, c0, c1, j, lane);
-                if (lane == 0) z[x][j] = st.y == 0.f ? -INFINITY : st.x + log2f(st.y);
-            }
-        // 32 channels of a head are an item; the unit's CTAs take them in turn
-        for (int item = i - c0 + parts * warp; item < a.g * 4; item += parts * (FIN_THREADS / 32)) {
-            const int j = item >> 2, c = (item & 3) * 32 + lane;
-            const float2 st = merge_stats(a, pf, c0, c1, j, lane);
-            float o = 0.f;
-#pragma unroll 8
-            for (int q = c0; q <= c1; ++q) {
-                const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf;
-                o += ex2(src[a.g * D + j] - st.x) * src[j * D + c];
-            }
-            const size_t at = (size_t)us[x] * a.g + j;
-            a.out[at * D + c] = st.y == 0.f ? 0.f : o / st.y;
-            if (a.lse && c == 0) a.lse[at] = st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * LN2;
-        }
-    }
-    if (!a.mass_out) return;
-    __syncthreads();
-    // every warp its part of the share's tiles, a lane four rows at a time
-    constexpr int NW = FIN_THREADS / 32;
-    const Deal own(t1 - t0, 1, NW);
-    const int w0 = t0 + own.begin_warp(warp), w1 = t0 + own.begin_warp(warp + 1);
-    Pos p = advance<TR>(a.c, Pos{b.s, b.h, b.k, b.nt}, w0 - t0);
-    for (int t = w0; t < w1 && p.nt;) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gw = blockIdx.x * NW + warp;
+    const int4 at = a.start[gw];  // stale where the warp had no tiles
+    const int2 d = *a.deal;
+    if ((int)blockIdx.x >= d.y || d.x == 0) return;
+    const Deal deal(d.x, d.y, NW);
+    const int t1 = deal.begin_warp(gw + 1);
+    Pos p{at.x, at.y, at.z, at.w};
+    for (int t = deal.begin_warp(gw); t < t1;) {
         const int u = p.s * a.c.heads + p.h;
-        const int n = min(p.nt - p.k, w1 - t);  // tiles of this unit in the part
-        const float* zz = u == us[0] ? z[0] : (u == us[1] ? z[1] : a.lse2 + (size_t)u * a.g);
+        const int n = min(p.nt - p.k, t1 - t);  // tiles of this unit
+        const float* lse2 = a.lse2 + (size_t)u * a.g;
         const float* sc = a.scores + (size_t)u * a.g * a.c.rows;
         const int r1 = min(rows_held(a.c, p.s), (p.k + n) * TR);
         for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
@@ -855,7 +868,7 @@ __global__ void __launch_bounds__(FIN_THREADS) paged_finish_kernel(const __grid_
 #pragma unroll 4
             for (int j = 0; j < a.g; ++j) {
                 const float4 x = *reinterpret_cast<const float4*>(sc + (size_t)j * a.c.rows + r);
-                const float lz = zz[j];
+                const float lz = lse2[j];
                 if (lz != -INFINITY) {
                     add.x += ex2(x.x - lz);
                     add.y += ex2(x.y - lz);
@@ -919,17 +932,19 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
     return r == CUDA_SUCCESS;
 }
 
+constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 constexpr int MAX_WARPS = 12;
 
 struct Layout {
-    size_t begin, part, head, lse2, scores, total;  // byte offsets
+    size_t deal, start, part, head, lse2, scores, total;  // byte offsets; the arrivals come first
 };
 Layout layout_of(const Cache& c, int g, bool with_mass) {
     Layout l;
     const size_t units = (size_t)c.seqs * c.heads, pf = part_floats(g) * sizeof(float);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.begin = 0;
-    l.part = up((MAX_GRID + 1) * sizeof(Begin));
+    l.deal = MAX_GRID * sizeof(unsigned);
+    l.start = l.deal + 256;
+    l.part = l.start + MAX_GRID * MAX_WARPS * sizeof(int4);
     l.head = l.part + up(MAX_GRID * 2 * pf);
     l.lse2 = l.head + up((size_t)MAX_GRID * MAX_WARPS * pf);
     l.scores = l.lse2 + up(units * g * sizeof(float));
@@ -939,12 +954,11 @@ Layout layout_of(const Cache& c, int g, bool with_mass) {
 
 template <typename E>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
+    static_assert(E::WARPS <= MAX_WARPS && E::WARPS % 4 == 0, "workspace layout, merge_parts");
     const long long most = (long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, E::TR);  // tiles
     const long long useful = (most + E::WARPS * MIN_TILES - 1) / (E::WARPS * MIN_TILES);
-    int grid = sms * E::PER_SM * E::SHARES;
-    if (grid > MAX_GRID) grid = MAX_GRID;
+    int grid = sms < MAX_GRID ? sms : MAX_GRID;
     if (grid > useful) grid = (int)useful;
-    static_assert(E::WARPS <= MAX_WARPS, "workspace layout");
     constexpr size_t smem = (size_t)E::WARPS * E::NST * STAGE + 1024;
     static std::atomic<bool> set[MAX_DEVICES];
     if (!set[dev].load(std::memory_order_relaxed)) {
@@ -953,7 +967,8 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& 
         set[dev].store(true, std::memory_order_relaxed);
     }
     cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(E::WARPS * 32), smem, s, a, tk, tv);
-    if (e == cudaSuccess) e = launch_dependent(paged_finish_kernel<E::TR, E::WARPS>, dim3(grid), dim3(FIN_THREADS), 0, s, a);
+    if (e == cudaSuccess && a.mass_out)
+        e = launch_dependent(paged_weights_kernel<E::TR, E::WARPS>, dim3(grid), dim3(E::WARPS * 32), 0, s, a);
     return e;
 }
 
@@ -1004,7 +1019,9 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.lse = lse;
     a.mass_in = mass_in;
     a.mass_out = mass_out;
-    a.begin = reinterpret_cast<Begin*>(w + l.begin);
+    a.arrived = reinterpret_cast<unsigned*>(w);
+    a.deal = reinterpret_cast<int2*>(w + l.deal);
+    a.start = reinterpret_cast<int4*>(w + l.start);
     a.part = reinterpret_cast<float*>(w + l.part);
     a.head = reinterpret_cast<float*>(w + l.head);
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
