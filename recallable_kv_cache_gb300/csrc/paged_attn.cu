@@ -54,10 +54,10 @@ struct AttnArgs {
     const float* mass_in;
     float* mass_out;
     unsigned* arrived;  // [grid] CTAs that have left their part of the unit that begins in CTA i; zero between calls
-    int4* start;        // [grid][warps] where a warp's tiles begin: sequence, KV head, tile in the unit, tiles of the unit
+    int4* start;        // [grid][warps] where a warp's tiles begin: sequence, KV head, tile in the unit, rows of the unit
     int2* deal;         // tiles of the call, CTAs that share them
     float* part;        // [grid][2] partials of units that several CTAs share
-    float* head;        // [grid][warps] partials of a unit that a warp entered part-way and left
+    float* head;        // [grid][warps] partials of a unit that a warp entered part-way and left; null: in shared memory
     float* lse2;        // [units][g], base 2
     float* scores;  // [units][g][rows], base 2
     long long wait_limit;
@@ -116,9 +116,10 @@ struct Deal {
 // The deal of this call, and where the shares of this CTA's warps begin.  Every
 // thread adds up a chunk of the sequences' tiles; a scan gives the total (below
 // 2^31, checked for the cache's extents) and the thread in whose chunk a
-// warp's first tile falls leaves its place.
+// warp's first tile falls leaves the chunk's first sequence and how many tiles
+// behind it the warp begins.
 template <int TR, int NT>
-__device__ Deal deal_out(const Cache& c, int4* start) {
+__device__ Deal deal_out(const Cache& c, int2* start) {
     constexpr int NW = NT / 32;
     __shared__ int warp_sum[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -142,23 +143,24 @@ __device__ Deal deal_out(const Cache& c, int4* start) {
         total += warp_sum[w];
     }
     const Deal deal(total, Deal::ctas(total, NW, gridDim.x), NW);
-    if (v > 0 && before < deal.begin_cta(blockIdx.x + 1) && before + v > deal.begin_cta(blockIdx.x)) {
-        int s = s0, nt = 0, at = before;  // first tile of sequence s
-        for (int w = 0; w < NW; ++w) {
-            const int t = deal.begin_warp(blockIdx.x * NW + w);
-            if (t < before || t >= before + v) continue;
-            while (true) {
-                nt = tiles_of<TR>(c, s);
-                if (t - at < nt * c.heads) break;
-                at += nt * c.heads;
-                ++s;
-            }
-            const int h = (t - at) / nt;
-            start[w] = make_int4(s, h, t - at - h * nt, nt);
-        }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const int t = deal.begin_warp(blockIdx.x * NW + w);
+        if (t >= before && t < before + v) start[w] = make_int2(s0, t - before);
     }
     __syncthreads();
     return deal;
+}
+// the place of the tile that is `left` tiles behind the first of sequence s
+template <int TR>
+__device__ __forceinline__ Pos walk(const Cache& c, int s, int left) {
+    int nt;
+    while (left >= (nt = tiles_of<TR>(c, s)) * c.heads) {
+        left -= nt * c.heads;
+        ++s;
+    }
+    const int h = left / nt;
+    return Pos{s, h, left - h * nt, nt};
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
@@ -189,6 +191,7 @@ template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
     static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0;
+    static constexpr size_t STATIC_SMEM = 2048;  // what the kernel declares, at most
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -394,6 +397,7 @@ template <int GP>
 struct TilesF32 {
     using T = float;
     static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP;
+    static constexpr size_t STATIC_SMEM = 2048 + WARPS * SCRATCH * 8;
     static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
@@ -528,72 +532,146 @@ struct Seg {
     int u, nt, a;  // unit (-1: none), its tiles, its first tile
 };
 
-// Merges the parts of unit u that CTAs c0 .. c1 left, in their order; by a
-// whole CTA, `red` its shared memory.
-template <int NT>
-__device__ void merge_parts(const AttnArgs& a, size_t pf, int u, int c0, int c1, float* red) {
-    __shared__ float stat[2][MAX_G];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int j = warp; j < a.g; j += NT / 32) {
-        float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-        for (int q = c0 + lane; q <= c1; q += 32) {
-            const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf + a.g * D;
-            const float m = __ldcg(src + j), l = __ldcg(src + a.g + j);
-            const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
-            L = L * ex2(M - ms) + l * ex2(m - ms);
-            M = mn;
-        }
-        float T = M;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) T = fmaxf(T, __shfl_xor_sync(FULL, T, o));
-        const float ms = T == -INFINITY ? 0.f : T;
-        L *= ex2(M - ms);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
-        if (lane == 0) {
-            stat[0][j] = ms;
-            stat[1][j] = L;
-            const float z = L == 0.f ? -INFINITY : ms + log2f(L);
-            a.lse2[(size_t)u * a.g + j] = z;
-            if (a.lse) a.lse[(size_t)u * a.g + j] = z * LN2;
-        }
+// ---- merging.
+struct Dest {
+    float* out;
+    float* lse;
+    float* lse2;
+    float* part;        // of all CTAs
+    const float* head;  // of this CTA's warps
+    int g;
+    int cta, begin, end;  // the CTA and its share of the tiles
+};
+__device__ __forceinline__ void put_lse(const Dest& d, size_t at, float M, float L) {
+    const float z = L == 0.f ? -INFINITY : M + log2f(L);
+    d.lse2[at] = z;
+    if (d.lse) d.lse[at] = z * LN2;
+}
+
+// Parts of units that several warps of this CTA hold, merged in warp order; lane
+// l looks after partial l.  Units shared with other CTAs go to d.part and are
+// named in `shared_units` (unit, first tile, tiles).
+template <int NW>
+__device__ __forceinline__ void merge_warps(const Dest& d, const Deal& deal, const Seg* segs, const unsigned char* rings,
+                                         int ring_bytes, int4* shared_units) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t pf = part_floats(d.g);
+    Seg sg{-1, 0, 0};
+    const float* src = nullptr;
+    bool leads = false;
+    if (lane < 2 * NW) {
+        const int w = lane >> 1, tb = deal.begin_warp(d.cta * NW + w);
+        sg = segs[lane];
+        src = lane & 1 ? reinterpret_cast<const float*>(rings + (size_t)w * ring_bytes) : d.head + w * pf;
+        leads = sg.u >= 0 && (sg.a >= tb || tb == d.begin);
     }
-    __syncthreads();
-    // four channels of a head to a thread, the parts dealt to NS threads of it
-    constexpr int NS = NT / 128;
-    const int slice = tid >> 7, c = (tid & 31) * 4;
-    for (int j0 = 0; j0 < a.g; j0 += 4) {
-        const int j = j0 + ((tid >> 5) & 3);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < a.g) {
-            const float ms = stat[0][j];
-#pragma unroll 4
-            for (int q = c0 + slice; q <= c1; q += NS) {
-                const float* src = a.part + ((size_t)q * 2 + (q == c0)) * pf;
-                const float f = ex2(__ldcg(src + a.g * D + j) - ms);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + j * D + c));
-                o.x += f * v.x;
-                o.y += f * v.y;
-                o.z += f * v.z;
-                o.w += f * v.w;
+    int item = 0;
+    for (unsigned todo = __ballot_sync(FULL, leads); todo; todo &= todo - 1) {
+        const int cand = __ffs(todo) - 1;
+        const int gu = __shfl_sync(FULL, sg.u, cand), ga = __shfl_sync(FULL, sg.a, cand), gn = __shfl_sync(FULL, sg.nt, cand);
+        const unsigned members = __ballot_sync(FULL, sg.u == gu);
+        const bool whole = ga >= d.begin && ga + gn <= d.end;
+        float* part = d.part + ((size_t)d.cta * 2 + (ga >= d.begin)) * pf;
+        for (int j = 0; j < d.g; ++j, ++item) {
+            if (item % NW != warp) continue;
+            float m = -INFINITY, l = 0.f;
+            if (sg.u == gu) {
+                m = src[d.g * D + j];
+                l = src[d.g * D + d.g + j];
+            }
+            float M = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+            const float f = ex2(m - (M == -INFINITY ? 0.f : M));
+            float L = f * l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = cand >> 1; w < NW; ++w) {
+                const bool tail = (members >> (2 * w + 1)) & 1;
+                if (!tail && !((members >> (2 * w)) & 1)) break;  // members follow one another
+                const float fx = __shfl_sync(FULL, f, 2 * w + tail);
+                const float* p = tail ? reinterpret_cast<const float*>(rings + (size_t)w * ring_bytes) : d.head + w * pf;
+                const float4 v = *reinterpret_cast<const float4*>(p + j * D + 4 * lane);
+                o.x += fx * v.x;
+                o.y += fx * v.y;
+                o.z += fx * v.z;
+                o.w += fx * v.w;
+            }
+            const size_t at = (size_t)gu * d.g + j;
+            const float r = !whole ? 1.f : (L == 0.f ? 0.f : 1.f / L);
+            *reinterpret_cast<float4*>((whole ? d.out + at * D : part + j * D) + 4 * lane) =
+                make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+            if (lane == 0) {
+                if (whole) {
+                    put_lse(d, at, M, L);
+                } else {
+                    part[d.g * D + j] = M;
+                    part[d.g * D + d.g + j] = L;
+                }
             }
         }
-        float4* r = reinterpret_cast<float4*>(red) + tid;
-        *r = o;
-        __syncthreads();
-        if (slice == 0 && j < a.g) {
+        if (!whole && threadIdx.x == 0) shared_units[ga >= d.begin] = make_int4(gu, ga, gn, 0);
+    }
+}
+
+// The parts of unit u that CTAs c0 .. c1 left, merged in their order by a whole
+// CTA; `red` is its shared memory.  Four channels of a head to a thread, the
+// parts dealt to NS threads of it, which ask for PB parts at a time: a round
+// trip to L2 costs half a microsecond here, and with up to PB * NS parts there
+// is only one.
+struct Merged {
+    float4 o;
+    float m, l;
+    __device__ __forceinline__ void add(float m2, float l2, float4 o2) {
+        const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - ms), f2 = ex2(m2 - ms);
+        o.x = o.x * f + o2.x * f2;
+        o.y = o.y * f + o2.y * f2;
+        o.z = o.z * f + o2.z * f2;
+        o.w = o.w * f + o2.w * f2;
+        l = l * f + l2 * f2;
+        m = mn;
+    }
+};
+template <int NT>
+__device__ __noinline__ void merge_ctas(const Dest& d, int u, int c0, int c1, Merged* red) {
+    constexpr int NS = NT / 128, PB = 8;
+    const int tid = threadIdx.x, slice = tid >> 7, c = (tid & 31) * 4;
+    const size_t pf = part_floats(d.g);
+    for (int j0 = 0; j0 < d.g; j0 += 4) {
+        const int j = j0 + ((tid >> 5) & 3);
+        Merged x{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+        if (j < d.g)
+            for (int q0 = c0 + slice; q0 <= c1; q0 += NS * PB) {
+                float m[PB], l[PB];
+                float4 v[PB];
 #pragma unroll
-            for (int x = 1; x < NS; ++x) {
-                const float4 v = r[x * 128];
-                o.x += v.x;
-                o.y += v.y;
-                o.z += v.z;
-                o.w += v.w;
+                for (int i = 0; i < PB; ++i) {
+                    const int q = q0 + i * NS;
+                    const float* src = d.part + ((size_t)q * 2 + (q == c0)) * pf;
+                    if (q <= c1) {
+                        m[i] = __ldcg(src + d.g * D + j);
+                        l[i] = __ldcg(src + d.g * D + d.g + j);
+                        v[i] = __ldcg(reinterpret_cast<const float4*>(src + j * D + c));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    if (q0 + i * NS <= c1) x.add(m[i], l[i], v[i]);
             }
-            const float f = stat[1][j] == 0.f ? 0.f : 1.f / stat[1][j];
-            *reinterpret_cast<float4*>(a.out + ((size_t)u * a.g + j) * D + c) =
-                make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        red[tid] = x;
+        __syncthreads();
+        if (slice == 0 && j < d.g) {
+#pragma unroll
+            for (int i = 1; i < NS; ++i) {
+                const Merged y = red[tid + i * 128];
+                x.add(y.m, y.l, y.o);
+            }
+            const float f = x.l == 0.f ? 0.f : 1.f / x.l;
+            const size_t at = (size_t)u * d.g + j;
+            *reinterpret_cast<float4*>(d.out + at * D + c) = make_float4(x.o.x * f, x.o.y * f, x.o.z * f, x.o.w * f);
+            if (c == 0) put_lse(d, at, x.m, x.l);
         }
         __syncthreads();
     }
@@ -608,21 +686,21 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     extern __shared__ unsigned char smem_raw[];
     // swizzled tiles need 1024-byte alignment
     unsigned char* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ int4 start[NW];
+    __shared__ int2 start[NW];
     __shared__ __align__(8) uint64_t full[NW][NST];
     __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
     __shared__ Seg segs[2 * NW];    // partials left: [2 w] in a.head, [2 w + 1] in the warp's ring
     __shared__ __align__(16) float2 scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
-    __shared__ int4 shared_units[2];  // units shared with other CTAs: unit, first and last CTA
+    __shared__ int4 shared_units[2];  // units shared with other CTAs: unit, first tile, tiles
     __shared__ int last[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) ptx::mbar_init(&full[warp][i], 1);
         ptx::fence_barrier_init();
-        segs[2 * warp].u = segs[2 * warp + 1].u = -1;
     }
+    if (threadIdx.x < 2) ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
+    if (lane == 0) segs[2 * warp].u = segs[2 * warp + 1].u = -1;
     if (threadIdx.x < 2) {
-        ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
         shared_units[threadIdx.x].x = -1;
         last[threadIdx.x] = 0;
     }
@@ -634,6 +712,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     const int t_end = works ? deal.begin_warp(blockIdx.x * NW + warp + 1) : 0;
     unsigned char* ring = smem + (size_t)warp * NST * STAGE;
     const size_t pf = part_floats(a.g);
+    float* heads = a.head ? a.head + (size_t)blockIdx.x * NW * pf : reinterpret_cast<float*>(smem + NW * NST * STAGE);
 
     if (t_begin < t_end) {
         E e;
@@ -644,7 +723,8 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
             first = at;
             e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
         };
-        Pos base{start[warp].x, start[warp].y, start[warp].z, start[warp].w};
+        Pos base = walk<TR>(a.c, start[warp].x, start[warp].y);
+        if (a.mass_out && lane == 0) a.start[blockIdx.x * NW + warp] = make_int4(base.s, base.h, base.k, rows_held(a.c, base.s));
         // q is asked for before the tiles: behind them it would wait for all
         // the copies in flight (some 4 us at full bandwidth)
         enter(base.s, base.h, base.nt, t_begin - base.k);
@@ -693,7 +773,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
                         });
                 return;
             }
-            float* dst = tail ? reinterpret_cast<float*>(ring) : a.head + ((size_t)blockIdx.x * NW + warp) * pf;
+            float* dst = tail ? reinterpret_cast<float*>(ring) : heads + warp * pf;
             e.leave(a.g, lane, false, [&](int j, int c, float v) { dst[j * D + c] = v; },
                     [&](int j, float m, float l) {
                         dst[a.g * D + j] = m;
@@ -742,7 +822,6 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
             }
         }
         leave(true);
-        if (a.mass_out && lane == 0) a.start[blockIdx.x * NW + warp] = start[warp];
     }
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) *a.deal = make_int2(deal.total, deal.n_cta);
@@ -759,86 +838,27 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     if (!works) return;
     __syncthreads();
 
-    // ---- parts of units that several warps of this CTA hold, merged in warp
-    // order: lane l looks after partial l
-    const int cta_begin = deal.begin_cta(blockIdx.x), cta_end = deal.begin_cta(blockIdx.x + 1);
-    Seg sg{-1, 0, 0};
-    const float* src = nullptr;
-    bool leads = false;
-    if (lane < 2 * NW) {
-        const int w = lane >> 1, tb = deal.begin_warp(blockIdx.x * NW + w);
-        sg = segs[lane];
-        src = lane & 1 ? reinterpret_cast<const float*>(smem + (size_t)w * NST * STAGE)
-                       : a.head + ((size_t)blockIdx.x * NW + w) * pf;
-        leads = sg.u >= 0 && (sg.a >= tb || tb == cta_begin);
-    }
-    int item = 0;
-    for (unsigned todo = __ballot_sync(FULL, leads); todo; todo &= todo - 1) {
-        const int cand = __ffs(todo) - 1;
-        const int gu = __shfl_sync(FULL, sg.u, cand), ga = __shfl_sync(FULL, sg.a, cand), gn = __shfl_sync(FULL, sg.nt, cand);
-        const unsigned members = __ballot_sync(FULL, sg.u == gu);
-        const bool whole = ga >= cta_begin && ga + gn <= cta_end;
-        float* part = a.part + ((size_t)blockIdx.x * 2 + (ga >= cta_begin)) * pf;
-        for (int j = 0; j < a.g; ++j, ++item) {
-            if (item % NW != warp) continue;
-            float m = -INFINITY, l = 0.f;
-            if (sg.u == gu) {
-                m = src[a.g * D + j];
-                l = src[a.g * D + a.g + j];
-            }
-            float M = m;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-            const float f = ex2(m - (M == -INFINITY ? 0.f : M));
-            float L = f * l;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (unsigned left = members; left; left &= left - 1) {
-                const int x = __ffs(left) - 1;
-                const float fx = __shfl_sync(FULL, f, x);
-                const float4 v = *reinterpret_cast<const float4*>(
-                    reinterpret_cast<const float*>(__shfl_sync(FULL, (unsigned long long)src, x)) + j * D + 4 * lane);
-                o.x += fx * v.x;
-                o.y += fx * v.y;
-                o.z += fx * v.z;
-                o.w += fx * v.w;
-            }
-            if (whole) {
-                const float r = L == 0.f ? 0.f : 1.f / L;
-                const size_t at = (size_t)gu * a.g + j;
-                *reinterpret_cast<float4*>(a.out + at * D + 4 * lane) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-                if (lane == 0) {
-                    const float z = L == 0.f ? -INFINITY : M + log2f(L);
-                    a.lse2[at] = z;
-                    if (a.lse) a.lse[at] = z * LN2;
-                }
-            } else {
-                *reinterpret_cast<float4*>(part + j * D + 4 * lane) = o;
-                if (lane == 0) {
-                    part[a.g * D + j] = M;
-                    part[a.g * D + a.g + j] = L;
-                }
-            }
-        }
-        if (!whole && threadIdx.x == 0)
-            shared_units[ga >= cta_begin] = make_int4(gu, deal.cta_of(ga), deal.cta_of(ga + gn - 1), 0);
-    }
+    const Dest d{a.out, a.lse, a.lse2, a.part, heads, a.g,
+                 (int)blockIdx.x, deal.begin_cta(blockIdx.x), deal.begin_cta(blockIdx.x + 1)};
+    merge_warps<NW>(d, deal, segs, smem, NST * STAGE, shared_units);
     __syncthreads();
-    // ---- across CTAs: the one that leaves its part of a unit last merges them
+    // across CTAs: the one that leaves its part of a unit last merges them
     if (threadIdx.x < 2 && shared_units[threadIdx.x].x >= 0) {
-        const int4 su = shared_units[threadIdx.x];
-        __threadfence();
-        if (atomicAdd(&a.arrived[su.y], 1u) == (unsigned)(su.z - su.y)) {
-            a.arrived[su.y] = 0;  // for the next call
+        int4& su = shared_units[threadIdx.x];
+        const int c0 = deal.cta_of(su.y), c1 = deal.cta_of(su.y + su.z - 1);
+        su.y = c0;
+        su.z = c1;
+        unsigned before;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + c0) : "memory");
+        if (before == (unsigned)(c1 - c0)) {
+            a.arrived[c0] = 0;  // for the next call
             last[threadIdx.x] = 1;
-            __threadfence();
         }
     }
     __syncthreads();
     for (int x = 0; x < 2; ++x)
         if (last[x])
-            merge_parts<NT>(a, pf, shared_units[x].x, shared_units[x].y, shared_units[x].z, reinterpret_cast<float*>(smem));
+            merge_ctas<NT>(d, shared_units[x].x, shared_units[x].y, shared_units[x].z, reinterpret_cast<Merged*>(smem));
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -854,42 +874,65 @@ __global__ void __launch_bounds__(NW * 32) paged_weights_kernel(const __grid_con
     if ((int)blockIdx.x >= d.y || d.x == 0) return;
     const Deal deal(d.x, d.y, NW);
     const int t1 = deal.begin_warp(gw + 1);
-    Pos p{at.x, at.y, at.z, at.w};
+    int len = at.w;
+    Pos p{at.x, at.y, at.z, (len + TR - 1) / TR};
     for (int t = deal.begin_warp(gw); t < t1;) {
         const int u = p.s * a.c.heads + p.h;
         const int n = min(p.nt - p.k, t1 - t);  // tiles of this unit
         const float* lse2 = a.lse2 + (size_t)u * a.g;
         const float* sc = a.scores + (size_t)u * a.g * a.c.rows;
-        const int r1 = min(rows_held(a.c, p.s), (p.k + n) * TR);
-        for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
-            const size_t o = (size_t)u * a.c.rows + r;
-            float4 w = a.mass_in ? *reinterpret_cast<const float4*>(a.mass_in + o) : make_float4(0.f, 0.f, 0.f, 0.f);
-            float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int j = 0; j < a.g; ++j) {
-                const float4 x = *reinterpret_cast<const float4*>(sc + (size_t)j * a.c.rows + r);
-                const float lz = lse2[j];
-                if (lz != -INFINITY) {
-                    add.x += ex2(x.x - lz);
-                    add.y += ex2(x.y - lz);
-                    add.z += ex2(x.z - lz);
-                    add.w += ex2(x.w - lz);
+        const int r1 = min(len, (p.k + n) * TR);
+        for (int r0 = p.k * TR + 4 * lane; r0 < r1; r0 += 256) {
+            float4 w[2], x[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                w[e] = a.mass_in && r0 + 128 * e < r1
+                           ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r0 + 128 * e)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 add[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+            for (int j = 0; j < a.g; j += 4) {
+                float lz[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lz[i] = j + i < a.g ? lse2[j + i] : -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (j + i < a.g && r0 + 128 * e < r1)
+                            x[e][i] = *reinterpret_cast<const float4*>(sc + (size_t)(j + i) * a.c.rows + r0 + 128 * e);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (lz[i] != -INFINITY && r0 + 128 * e < r1) {
+                            add[e].x += ex2(x[e][i].x - lz[i]);
+                            add[e].y += ex2(x[e][i].y - lz[i]);
+                            add[e].z += ex2(x[e][i].z - lz[i]);
+                            add[e].w += ex2(x[e][i].w - lz[i]);
+                        }
             }
-            w.x += add.x;
-            w.y += add.y;
-            w.z += add.z;
-            w.w += add.w;
-            if (r + 4 <= r1) {
-                *reinterpret_cast<float4*>(a.mass_out + o) = w;
-            } else {  // the rows behind the last one stay as they are
-                a.mass_out[o] = w.x;
-                if (r + 1 < r1) a.mass_out[o + 1] = w.y;
-                if (r + 2 < r1) a.mass_out[o + 2] = w.z;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 128 * e;
+                if (r >= r1) continue;
+                const size_t o = (size_t)u * a.c.rows + r;
+                w[e].x += add[e].x;
+                w[e].y += add[e].y;
+                w[e].z += add[e].z;
+                w[e].w += add[e].w;
+                if (r + 4 <= r1) {
+                    *reinterpret_cast<float4*>(a.mass_out + o) = w[e];
+                } else {  // the rows behind the last one stay as they are
+                    a.mass_out[o] = w[e].x;
+                    if (r + 1 < r1) a.mass_out[o + 1] = w[e].y;
+                    if (r + 2 < r1) a.mass_out[o + 2] = w[e].z;
+                }
             }
         }
         t += n;
+        const int s = p.s;
         p = advance<TR>(a.c, p, n);
+        if (p.s != s && p.nt) len = rows_held(a.c, p.s);
     }
 }
 
@@ -934,6 +977,7 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
 
 constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 constexpr int MAX_WARPS = 12;
+constexpr size_t MAX_SMEM = 227 * 1024;
 
 struct Layout {
     size_t deal, start, part, head, lse2, scores, total;  // byte offsets; the arrivals come first
@@ -953,16 +997,24 @@ Layout layout_of(const Cache& c, int g, bool with_mass) {
 }
 
 template <typename E>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
+cudaError_t launch(AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
     static_assert(E::WARPS <= MAX_WARPS && E::WARPS % 4 == 0, "workspace layout, merge_parts");
     const long long most = (long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, E::TR);  // tiles
     const long long useful = (most + E::WARPS * MIN_TILES - 1) / (E::WARPS * MIN_TILES);
     int grid = sms < MAX_GRID ? sms : MAX_GRID;
     if (grid > useful) grid = (int)useful;
-    constexpr size_t smem = (size_t)E::WARPS * E::NST * STAGE + 1024;
+    // partials that warps leave on the way stay in shared memory where there is
+    // room beside the rings (under load, L2 answers in 2 us at the merge)
+    size_t smem = (size_t)E::WARPS * E::NST * STAGE + 1024;
+    const size_t heads = E::WARPS * part_floats(a.g) * sizeof(float);
+    if (smem + heads <= MAX_SMEM - E::STATIC_SMEM) {
+        smem += heads;
+        a.head = nullptr;
+    }
     static std::atomic<bool> set[MAX_DEVICES];
     if (!set[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   MAX_SMEM - E::STATIC_SMEM);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
