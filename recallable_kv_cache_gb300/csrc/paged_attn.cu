@@ -41,6 +41,7 @@ using namespace mmas;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 constexpr int STAGE = 8192;  // K rows, then V rows of one tile
 
 struct AttnArgs {
@@ -191,7 +192,7 @@ template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
     static constexpr int TR = 16, WARPS = 12, NST = 2, SCRATCH = 0;
-    static constexpr size_t STATIC_SMEM = 2048;  // what the kernel declares, at most
+    static constexpr size_t STATIC_SMEM = 5120;  // what the kernel declares, at most
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -397,7 +398,7 @@ template <int GP>
 struct TilesF32 {
     using T = float;
     static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP;
-    static constexpr size_t STATIC_SMEM = 2048 + WARPS * SCRATCH * 8;
+    static constexpr size_t STATIC_SMEM = 5120 + WARPS * SCRATCH * 8;
     static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
@@ -532,149 +533,49 @@ struct Seg {
     int u, nt, a;  // unit (-1: none), its tiles, its first tile
 };
 
-// ---- merging.
-struct Dest {
-    float* out;
-    float* lse;
-    float* lse2;
-    float* part;        // of all CTAs
-    const float* head;  // of this CTA's warps
-    int g;
-    int cta, begin, end;  // the CTA and its share of the tiles
+// A partial result of a unit to merge with others, or what the merging gives.
+struct Job {
+    int src, n;  // its sources in the list of sources
+    int u;       // final: the unit whose outputs it gives; else -1
+    float* dst;  // not final: where the merged partial goes
 };
-__device__ __forceinline__ void put_lse(const Dest& d, size_t at, float M, float L) {
-    const float z = L == 0.f ? -INFINITY : M + log2f(L);
-    d.lse2[at] = z;
-    if (d.lse) d.lse[at] = z * LN2;
-}
-
-// Parts of units that several warps of this CTA hold, merged in warp order; lane
-// l looks after partial l.  Units shared with other CTAs go to d.part and are
-// named in `shared_units` (unit, first tile, tiles).
-template <int NW>
-__device__ __forceinline__ void merge_warps(const Dest& d, const Deal& deal, const Seg* segs, const unsigned char* rings,
-                                         int ring_bytes, int4* shared_units) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t pf = part_floats(d.g);
-    Seg sg{-1, 0, 0};
-    const float* src = nullptr;
-    bool leads = false;
-    if (lane < 2 * NW) {
-        const int w = lane >> 1, tb = deal.begin_warp(d.cta * NW + w);
-        sg = segs[lane];
-        src = lane & 1 ? reinterpret_cast<const float*>(rings + (size_t)w * ring_bytes) : d.head + w * pf;
-        leads = sg.u >= 0 && (sg.a >= tb || tb == d.begin);
+// Head j of the partials src[0 .. n), merged in that order by a warp.
+__device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, const float* const* src, int j, int lane) {
+    const int sm = a.g * D + j, sl = sm + a.g;  // where a partial keeps its maximum and sum
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < job.n; i += 32) M = fmaxf(M, src[i][sm]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    const float ms = M == -INFINITY ? 0.f : M;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < job.n; ++i) {
+        const float* p = src[i];
+        const float f = ex2(p[sm] - ms);
+        const float4 v = *reinterpret_cast<const float4*>(p + j * D + 4 * lane);
+        L += f * p[sl];
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
     }
-    int item = 0;
-    for (unsigned todo = __ballot_sync(FULL, leads); todo; todo &= todo - 1) {
-        const int cand = __ffs(todo) - 1;
-        const int gu = __shfl_sync(FULL, sg.u, cand), ga = __shfl_sync(FULL, sg.a, cand), gn = __shfl_sync(FULL, sg.nt, cand);
-        const unsigned members = __ballot_sync(FULL, sg.u == gu);
-        const bool whole = ga >= d.begin && ga + gn <= d.end;
-        float* part = d.part + ((size_t)d.cta * 2 + (ga >= d.begin)) * pf;
-        for (int j = 0; j < d.g; ++j, ++item) {
-            if (item % NW != warp) continue;
-            float m = -INFINITY, l = 0.f;
-            if (sg.u == gu) {
-                m = src[d.g * D + j];
-                l = src[d.g * D + d.g + j];
-            }
-            float M = m;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-            const float f = ex2(m - (M == -INFINITY ? 0.f : M));
-            float L = f * l;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = cand >> 1; w < NW; ++w) {
-                const bool tail = (members >> (2 * w + 1)) & 1;
-                if (!tail && !((members >> (2 * w)) & 1)) break;  // members follow one another
-                const float fx = __shfl_sync(FULL, f, 2 * w + tail);
-                const float* p = tail ? reinterpret_cast<const float*>(rings + (size_t)w * ring_bytes) : d.head + w * pf;
-                const float4 v = *reinterpret_cast<const float4*>(p + j * D + 4 * lane);
-                o.x += fx * v.x;
-                o.y += fx * v.y;
-                o.z += fx * v.z;
-                o.w += fx * v.w;
-            }
-            const size_t at = (size_t)gu * d.g + j;
-            const float r = !whole ? 1.f : (L == 0.f ? 0.f : 1.f / L);
-            *reinterpret_cast<float4*>((whole ? d.out + at * D : part + j * D) + 4 * lane) =
-                make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-            if (lane == 0) {
-                if (whole) {
-                    put_lse(d, at, M, L);
-                } else {
-                    part[d.g * D + j] = M;
-                    part[d.g * D + d.g + j] = L;
-                }
-            }
+    __syncwarp();  // the destination may be one of the sources
+    float* dst = job.dst;
+    if (job.u >= 0) {
+        const size_t at = (size_t)job.u * a.g;
+        dst = a.out + at * D;
+        const float r = L == 0.f ? 0.f : 1.f / L;
+        o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+        if (lane == 0) {
+            const float z = L == 0.f ? -INFINITY : M + log2f(L);
+            a.lse2[at + j] = z;
+            if (a.lse) a.lse[at + j] = z * LN2;
         }
-        if (!whole && threadIdx.x == 0) shared_units[ga >= d.begin] = make_int4(gu, ga, gn, 0);
+    } else if (lane == 0) {
+        dst[sm] = M;
+        dst[sl] = L;
     }
-}
-
-// The parts of unit u that CTAs c0 .. c1 left, merged in their order by a whole
-// CTA; `red` is its shared memory.  Four channels of a head to a thread, the
-// parts dealt to NS threads of it, which ask for PB parts at a time: a round
-// trip to L2 costs half a microsecond here, and with up to PB * NS parts there
-// is only one.
-struct Merged {
-    float4 o;
-    float m, l;
-    __device__ __forceinline__ void add(float m2, float l2, float4 o2) {
-        const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2(m - ms), f2 = ex2(m2 - ms);
-        o.x = o.x * f + o2.x * f2;
-        o.y = o.y * f + o2.y * f2;
-        o.z = o.z * f + o2.z * f2;
-        o.w = o.w * f + o2.w * f2;
-        l = l * f + l2 * f2;
-        m = mn;
-    }
-};
-template <int NT>
-__device__ __noinline__ void merge_ctas(const Dest& d, int u, int c0, int c1, Merged* red) {
-    constexpr int NS = NT / 128, PB = 8;
-    const int tid = threadIdx.x, slice = tid >> 7, c = (tid & 31) * 4;
-    const size_t pf = part_floats(d.g);
-    for (int j0 = 0; j0 < d.g; j0 += 4) {
-        const int j = j0 + ((tid >> 5) & 3);
-        Merged x{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
-        if (j < d.g)
-            for (int q0 = c0 + slice; q0 <= c1; q0 += NS * PB) {
-                float m[PB], l[PB];
-                float4 v[PB];
-#pragma unroll
-                for (int i = 0; i < PB; ++i) {
-                    const int q = q0 + i * NS;
-                    const float* src = d.part + ((size_t)q * 2 + (q == c0)) * pf;
-                    if (q <= c1) {
-                        m[i] = __ldcg(src + d.g * D + j);
-                        l[i] = __ldcg(src + d.g * D + d.g + j);
-                        v[i] = __ldcg(reinterpret_cast<const float4*>(src + j * D + c));
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < PB; ++i)
-                    if (q0 + i * NS <= c1) x.add(m[i], l[i], v[i]);
-            }
-        red[tid] = x;
-        __syncthreads();
-        if (slice == 0 && j < d.g) {
-#pragma unroll
-            for (int i = 1; i < NS; ++i) {
-                const Merged y = red[tid + i * 128];
-                x.add(y.m, y.l, y.o);
-            }
-            const float f = x.l == 0.f ? 0.f : 1.f / x.l;
-            const size_t at = (size_t)u * d.g + j;
-            *reinterpret_cast<float4*>(d.out + at * D + c) = make_float4(x.o.x * f, x.o.y * f, x.o.z * f, x.o.w * f);
-            if (c == 0) put_lse(d, at, x.m, x.l);
-        }
-        __syncthreads();
-    }
+    *reinterpret_cast<float4*>(dst + j * D + 4 * lane) = o;
 }
 
 template <typename E>
@@ -691,8 +592,13 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
     __shared__ Seg segs[2 * NW];    // partials left: [2 w] in a.head, [2 w + 1] in the warp's ring
     __shared__ __align__(16) float2 scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
-    __shared__ int4 shared_units[2];  // units shared with other CTAs: unit, first tile, tiles
-    __shared__ int last[2];
+    // merging: jobs and their sources; the units shared with other CTAs (unit,
+    // first CTA, CTAs; unit -1: none, or not this CTA's to merge)
+    constexpr int MAX_SRC = 2 * NW + MAX_GRID;
+    __shared__ const float* src[MAX_SRC];
+    __shared__ Job jobs[2 * NW];
+    __shared__ int n_jobs;
+    __shared__ int4 shared_units[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) ptx::mbar_init(&full[warp][i], 1);
@@ -700,10 +606,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     }
     if (threadIdx.x < 2) ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
     if (lane == 0) segs[2 * warp].u = segs[2 * warp + 1].u = -1;
-    if (threadIdx.x < 2) {
-        shared_units[threadIdx.x].x = -1;
-        last[threadIdx.x] = 0;
-    }
+    if (threadIdx.x < 2) shared_units[threadIdx.x].x = -1;
     ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
     const Deal deal = deal_out<TR, NT>(a.c, start);
@@ -762,24 +665,22 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
             }
         };
         auto leave = [&](bool tail) {
-            if (first >= t_begin && first + nt <= t_end) {
-                // the whole unit was this warp's
-                const size_t o = (size_t)u * a.g;
-                e.leave(a.g, lane, true, [&](int j, int c, float v) { a.out[(o + j) * D + c] = v; },
-                        [&](int j, float m, float l) {
+            // final where the whole unit was this warp's, else left to be merged
+            const bool whole = first >= t_begin && first + nt <= t_end;
+            const size_t o = (size_t)u * a.g;
+            float* dst = whole ? a.out + o * D : (tail ? reinterpret_cast<float*>(ring) : heads + warp * pf);
+            e.leave(a.g, lane, whole, [&](int j, int c, float v) { dst[j * D + c] = v; },
+                    [&](int j, float m, float l) {
+                        if (whole) {
                             const float z = l == 0.f ? -INFINITY : m + log2f(l);
                             a.lse2[o + j] = z;
                             if (a.lse) a.lse[o + j] = z * LN2;
-                        });
-                return;
-            }
-            float* dst = tail ? reinterpret_cast<float*>(ring) : heads + warp * pf;
-            e.leave(a.g, lane, false, [&](int j, int c, float v) { dst[j * D + c] = v; },
-                    [&](int j, float m, float l) {
-                        dst[a.g * D + j] = m;
-                        dst[a.g * D + a.g + j] = l;
+                        } else {
+                            dst[a.g * D + j] = m;
+                            dst[a.g * D + a.g + j] = l;
+                        }
                     });
-            if (lane == 0) segs[2 * warp + tail] = Seg{u, nt, first};
+            if (lane == 0 && !whole) segs[2 * warp + tail] = Seg{u, nt, first};
         };
         int st = 0, parity = 0;
         // the first NST turns only ask for tiles
@@ -838,27 +739,84 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     if (!works) return;
     __syncthreads();
 
-    const Dest d{a.out, a.lse, a.lse2, a.part, heads, a.g,
-                 (int)blockIdx.x, deal.begin_cta(blockIdx.x), deal.begin_cta(blockIdx.x + 1)};
-    merge_warps<NW>(d, deal, segs, smem, NST * STAGE, shared_units);
-    __syncthreads();
-    // across CTAs: the one that leaves its part of a unit last merges them
-    if (threadIdx.x < 2 && shared_units[threadIdx.x].x >= 0) {
-        int4& su = shared_units[threadIdx.x];
-        const int c0 = deal.cta_of(su.y), c1 = deal.cta_of(su.y + su.z - 1);
-        su.y = c0;
-        su.z = c1;
-        unsigned before;
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + c0) : "memory");
-        if (before == (unsigned)(c1 - c0)) {
-            a.arrived[c0] = 0;  // for the next call
-            last[threadIdx.x] = 1;
+    // ---- merging.  This code runs once a call, and its instructions come from
+    // L2 at some 60 ns per 128 bytes, so that its length counts for more than
+    // its work: round 0 merges the partials of this CTA's warps, in warp order;
+    // later rounds, only in the CTA that is the last to leave its part of a
+    // shared unit, merge the CTAs' parts, in CTA order, copied to the rings.
+    const int cta_begin = deal.begin_cta(blockIdx.x), cta_end = deal.begin_cta(blockIdx.x + 1);
+    const int cap = (int)((size_t)NW * NST * STAGE / (pf * sizeof(float))) - 1;  // parts a round
+    for (int round = 0, x = 0, next = 0;; ++round) {
+        if (round == 0) {
+            if (warp == 0) {
+                // lane l looks after partial l; those of a unit follow one another
+                Seg sg{-1, 0, 0};
+                bool leads = false;
+                if (lane < 2 * NW) {
+                    const int tb = deal.begin_warp(blockIdx.x * NW + (lane >> 1));
+                    sg = segs[lane];
+                    leads = sg.u >= 0 && (sg.a >= tb || tb == cta_begin);
+                }
+                const unsigned held = __ballot_sync(FULL, sg.u >= 0), lead = __ballot_sync(FULL, leads);
+                const unsigned below = (1u << lane) - 1u;
+                if (sg.u >= 0)
+                    src[__popc(held & below)] = lane & 1 ? reinterpret_cast<const float*>(smem + (size_t)(lane >> 1) * NST * STAGE)
+                                                         : heads + (lane >> 1) * pf;
+                if (leads) {
+                    const unsigned after = lead & ~below & ~(1u << lane);  // the next leader ends this job
+                    const unsigned mine = held & ~below & (after ? (after & -after) - 1u : FULL);
+                    const bool began = sg.a >= cta_begin, whole = began && sg.a + sg.nt <= cta_end;
+                    jobs[__popc(lead & below)] = Job{__popc(held & below), __popc(mine), whole ? sg.u : -1,
+                                                     a.part + ((size_t)blockIdx.x * 2 + began) * pf};
+                    if (!whole) {
+                        const int c0 = deal.cta_of(sg.a);
+                        shared_units[began] = make_int4(sg.u, c0, deal.cta_of(sg.a + sg.nt - 1) - c0 + 1, 0);
+                    }
+                }
+                if (lane == 0) n_jobs = __popc(lead);
+            }
+        } else {
+            // the next unit, and of it the next parts: behind what the rounds
+            // before have made of it (in slot 0 of the rings)
+            while (x < 2 && (shared_units[x].x < 0 || next == shared_units[x].z)) {
+                ++x;
+                next = 0;
+            }
+            if (x == 2) break;
+            const int4 su = shared_units[x];
+            const int n = min(su.z - next, cap), had = next > 0;
+            float* slots = reinterpret_cast<float*>(smem);
+            for (int i = threadIdx.x; i < n + had; i += NT) src[i] = slots + (size_t)(i + !had) * pf;
+            if (threadIdx.x == 0) {
+                n_jobs = 1;
+                jobs[0] = Job{0, n + had, next + n == su.z ? su.x : -1, slots};
+            }
+            const int pieces = (int)(pf / 4);  // of 16 bytes in a part
+            for (int i = threadIdx.x; i < n * pieces; i += NT) {
+                const int k = i / pieces, q = su.y + next + k;
+                ptx::cp_async16(slots + (size_t)pf + (size_t)i * 4,
+                                a.part + ((size_t)q * 2 + (q == su.y)) * pf + (size_t)(i - k * pieces) * 4);
+            }
+            ptx::cp_async_wait_all();
+            next += n;
+        }
+        __syncthreads();
+        for (int item = warp; item < n_jobs * a.g; item += NW) {
+            const Job job = jobs[item / a.g];
+            merge_head(a, job, src + job.src, item % a.g, lane);
+        }
+        __syncthreads();
+        if (round == 0) {
+            if (threadIdx.x < 2 && shared_units[threadIdx.x].x >= 0) {
+                const int4 su = shared_units[threadIdx.x];
+                unsigned before;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + su.y) : "memory");
+                if (before == (unsigned)(su.z - 1)) a.arrived[su.y] = 0;  // the last one: for the next call
+                else shared_units[threadIdx.x].x = -1;
+            }
+            __syncthreads();
         }
     }
-    __syncthreads();
-    for (int x = 0; x < 2; ++x)
-        if (last[x])
-            merge_ctas<NT>(d, shared_units[x].x, shared_units[x].y, shared_units[x].z, reinterpret_cast<Merged*>(smem));
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -975,7 +933,6 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
     return r == CUDA_SUCCESS;
 }
 
-constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 constexpr int MAX_WARPS = 12;
 constexpr size_t MAX_SMEM = 227 * 1024;
 
@@ -998,7 +955,7 @@ Layout layout_of(const Cache& c, int g, bool with_mass) {
 
 template <typename E>
 cudaError_t launch(AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
-    static_assert(E::WARPS <= MAX_WARPS && E::WARPS % 4 == 0, "workspace layout, merge_parts");
+    static_assert(E::WARPS <= MAX_WARPS && 2 * E::WARPS <= 32, "workspace layout");
     const long long most = (long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, E::TR);  // tiles
     const long long useful = (most + E::WARPS * MIN_TILES - 1) / (E::WARPS * MIN_TILES);
     int grid = sms < MAX_GRID ? sms : MAX_GRID;
