@@ -397,9 +397,9 @@ __device__ __forceinline__ int reduce_scatter(float* v, int lane) {
 template <int GP>
 struct TilesF32 {
     using T = float;
-    static constexpr int TR = 8, WARPS = 8, NST = 3, SCRATCH = TR * GP;
+    static constexpr int TR = 8, WARPS = GP > 8 ? 8 : 12, NST = GP > 8 ? 3 : 2, SCRATCH = TR * GP;
     static constexpr size_t STATIC_SMEM = 5120 + WARPS * SCRATCH * 8;
-    static constexpr int LPR = GP > 8 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
+    static constexpr int LPR = GP > 8 ? 32 : GP > 2 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
     static constexpr int BR = TR / RP * GP <= 32 ? TR / RP : 32 / GP;  // of those, summed together
@@ -494,9 +494,7 @@ struct TilesF32 {
             }
         }
         __syncwarp();
-#pragma unroll
-        for (int r = 0; r < TR; ++r) {
-            if (r >= n) break;  // rows not held are not read
+        auto row = [&](int r) {
             const ulonglong2 vv = V[r * 32 + lane];
             const uint64_t* pp = reinterpret_cast<const uint64_t*>(ps + r * GP);
 #pragma unroll
@@ -505,6 +503,13 @@ struct TilesF32 {
                 o[jj][0] = fma2(p, vv.x, o[jj][0]);
                 o[jj][1] = fma2(p, vv.y, o[jj][1]);
             }
+        };
+        if (n == TR) {
+#pragma unroll
+            for (int r = 0; r < TR; ++r) row(r);
+        } else {  // rows not held are not read
+#pragma unroll 1
+            for (int r = 0; r < n; ++r) row(r);
         }
     }
     template <typename Put, typename Stat>
@@ -820,71 +825,68 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
 }
 
 // ---------------------------------------------------------------- accumulated weights
-// mass_out = mass_in + sum_j e^{s_j - lse_j}: warp for warp the tiles of the
-// attention kernel, a lane four rows at a time.
+// mass_out = mass_in + sum_j e^{s_j - lse_j} over the tiles of the attention
+// kernel's warps, each share in W_SPLIT parts, a lane four rows at a time: the
+// scores come from L2 or HBM, so what counts is how many are asked for at once.
+constexpr int W_SPLIT = 2, W_THREADS = 384;
+
 template <int TR, int NW>
-__global__ void __launch_bounds__(NW * 32) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(W_THREADS) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gw = blockIdx.x * NW + warp;
+    const int lane = threadIdx.x & 31, w = blockIdx.x * (W_THREADS / 32) + (threadIdx.x >> 5), gw = w / W_SPLIT;
+    if (gw >= MAX_GRID * NW) return;
     const int4 at = a.start[gw];  // stale where the warp had no tiles
     const int2 d = *a.deal;
-    if ((int)blockIdx.x >= d.y || d.x == 0) return;
     const Deal deal(d.x, d.y, NW);
-    const int t1 = deal.begin_warp(gw + 1);
+    if (gw >= d.y * NW || d.x == 0) return;
+    const int b0 = deal.begin_warp(gw), b1 = deal.begin_warp(gw + 1), part = w % W_SPLIT;
+    const int t0 = b0 + (b1 - b0) * part / W_SPLIT, t1 = b0 + (b1 - b0) * (part + 1) / W_SPLIT;
+    if (t0 == t1) return;
     int len = at.w;
     Pos p{at.x, at.y, at.z, (len + TR - 1) / TR};
-    for (int t = deal.begin_warp(gw); t < t1;) {
+    p = advance<TR>(a.c, p, t0 - b0);
+    if (p.s != at.x) len = rows_held(a.c, p.s);
+    for (int t = t0; t < t1;) {
         const int u = p.s * a.c.heads + p.h;
         const int n = min(p.nt - p.k, t1 - t);  // tiles of this unit
         const float* lse2 = a.lse2 + (size_t)u * a.g;
         const float* sc = a.scores + (size_t)u * a.g * a.c.rows;
         const int r1 = min(len, (p.k + n) * TR);
-        for (int r0 = p.k * TR + 4 * lane; r0 < r1; r0 += 256) {
-            float4 w[2], x[2][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                w[e] = a.mass_in && r0 + 128 * e < r1
-                           ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r0 + 128 * e)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-            float4 add[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
+            const size_t o = (size_t)u * a.c.rows + r;
+            float4 v = a.mass_in ? *reinterpret_cast<const float4*>(a.mass_in + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int j = 0; j < a.g; j += 4) {
+                float4 x[4];
                 float lz[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    lz[i] = j + i < a.g ? lse2[j + i] : -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (j + i < a.g && r0 + 128 * e < r1)
-                            x[e][i] = *reinterpret_cast<const float4*>(sc + (size_t)(j + i) * a.c.rows + r0 + 128 * e);
+                    lz[i] = -INFINITY;
+                    if (j + i < a.g) {
+                        x[i] = *reinterpret_cast<const float4*>(sc + (size_t)(j + i) * a.c.rows + r);
+                        lz[i] = lse2[j + i];
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (lz[i] != -INFINITY && r0 + 128 * e < r1) {
-                            add[e].x += ex2(x[e][i].x - lz[i]);
-                            add[e].y += ex2(x[e][i].y - lz[i]);
-                            add[e].z += ex2(x[e][i].z - lz[i]);
-                            add[e].w += ex2(x[e][i].w - lz[i]);
-                        }
+                    if (lz[i] != -INFINITY) {
+                        add.x += ex2(x[i].x - lz[i]);
+                        add.y += ex2(x[i].y - lz[i]);
+                        add.z += ex2(x[i].z - lz[i]);
+                        add.w += ex2(x[i].w - lz[i]);
+                    }
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 128 * e;
-                if (r >= r1) continue;
-                const size_t o = (size_t)u * a.c.rows + r;
-                w[e].x += add[e].x;
-                w[e].y += add[e].y;
-                w[e].z += add[e].z;
-                w[e].w += add[e].w;
-                if (r + 4 <= r1) {
-                    *reinterpret_cast<float4*>(a.mass_out + o) = w[e];
-                } else {  // the rows behind the last one stay as they are
-                    a.mass_out[o] = w[e].x;
-                    if (r + 1 < r1) a.mass_out[o + 1] = w[e].y;
-                    if (r + 2 < r1) a.mass_out[o + 2] = w[e].z;
-                }
+            v.x += add.x;
+            v.y += add.y;
+            v.z += add.z;
+            v.w += add.w;
+            if (r + 4 <= r1) {
+                *reinterpret_cast<float4*>(a.mass_out + o) = v;
+            } else {  // the rows behind the last one stay as they are
+                a.mass_out[o] = v.x;
+                if (r + 1 < r1) a.mass_out[o + 1] = v.y;
+                if (r + 2 < r1) a.mass_out[o + 2] = v.z;
             }
         }
         t += n;
@@ -977,7 +979,8 @@ cudaError_t launch(AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, in
     }
     cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(E::WARPS * 32), smem, s, a, tk, tv);
     if (e == cudaSuccess && a.mass_out)
-        e = launch_dependent(paged_weights_kernel<E::TR, E::WARPS>, dim3(grid), dim3(E::WARPS * 32), 0, s, a);
+        e = launch_dependent(paged_weights_kernel<E::TR, E::WARPS>, dim3(ceil_div(grid * E::WARPS * W_SPLIT, W_THREADS / 32)),
+                             dim3(W_THREADS), 0, s, a);
     return e;
 }
 
