@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(128) paged_advance_kernel(const __grid_constan
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;        // 11 bits of the key a pass: 11, 11 and 10
+constexpr int SEL_CAND = 256;         // keys of one bin that are ranked directly
 constexpr int SEL_MAX_CLUSTER = 8;
 constexpr int SEL_MAX_SLICE = 45056;  // keys of one CTA that stay in shared memory (176 KB)
 
@@ -233,7 +234,10 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 // the key of the budget-th row follows digit by digit from the histograms, to
 // which every CTA adds its occupied bins in all its peers' shared memory (few
 // of the 2048 are occupied; every CTA reading all bins of its peers took 97 us
-// for 32 units of 128k rows where this takes PERIOD us).  Then a row is kept if
+// for 32 units of 128k rows where this takes SEL128 us).  Where a digit
+// leaves at most SEL_CAND keys (a first digit's bin is a quarter of a power of
+// two) they are gathered and the one of the wanted rank is found by counting,
+// which saves the digits behind it.  Then a row is kept if
 // its key is above that one, or equal and among the first that fit.  With
 // gt(r), eq(r) the rows before r above and equal, kept(r) = gt(r) + min(eq(r),
 // fitting) rows are kept before r, so the k-th hole is the row r < budget, not
@@ -247,7 +251,9 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     __shared__ int warp_sum[SEL_WARPS];
     __shared__ int counts[SEL_WARPS][4];  // rows above, equal; the same of rows below the budget
     __shared__ int cta_counts[4];
-    __shared__ int found[2];
+    __shared__ int found[3];
+    __shared__ uint32_t cand[SEL_CAND], own_cand[CS > 1 ? SEL_CAND : 1];
+    __shared__ int n_cand;
     const int u = blockIdx.x / CS, s = u / a.c.heads;
     const int rank = CS > 1 ? (int)cluster_rank() : 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -258,6 +264,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
     if (CS > 1)
         for (int i = tid; i < SEL_BINS; i += SEL_THREADS) mine[i] = 0;
+    if (tid == 0) n_cand = 0;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     if (tid == 0 && rank == 0) check_len(a.c, s);
@@ -295,6 +302,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         const uint32_t digit = pass == 2 ? 1023u : 2047u;
         if (pass > 0) {
             if (CS == 1) local = hist[pass];
+#pragma unroll 4
             for (int i = tid; i < n; i += SEL_THREADS) {
                 const uint32_t k = key_at(i);
                 if ((k & mask) == prefix) atomicAdd(&local[(k >> shift) & digit], 1);
@@ -337,6 +345,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
                 if (before < need && need <= before + c[e]) {
                     found[0] = SEL_BINS - 1 - (tid * BPT + e);
                     found[1] = need - before;
+                    found[2] = c[e];
                 }
                 before += c[e];
             }
@@ -345,11 +354,50 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         prefix |= (uint32_t)found[0] << shift;
         need = found[1];
         mask |= digit << shift;
+        if (pass == 2 || found[2] > SEL_CAND) continue;
+        // the keys of this bin, of all CTAs, in any order
+        uint32_t* list = CS > 1 ? own_cand : cand;
+#pragma unroll 4
+        for (int i = tid; i < n; i += SEL_THREADS) {
+            const uint32_t k = key_at(i);
+            if ((k & mask) == prefix) list[atomicAdd(&n_cand, 1)] = k;
+        }
+        const int all = found[2];
+        sync_all();
+        if (CS > 1) {
+            // warp r copies what CTA r has, behind what the CTAs before it have
+            const int m = lane < CS ? peer_word(&n_cand, lane) : 0;
+            const int mine_n = __shfl_sync(FULL, m, warp & 31);
+            const int to = __reduce_add_sync(FULL, lane < warp ? m : 0);
+            if (warp < CS)
+                for (int i = lane; i < mine_n; i += 32)
+                    cand[to + i] = (uint32_t)peer_word(reinterpret_cast<const int*>(own_cand + i), warp);
+            __syncthreads();
+        }
+        if (tid < all) {
+            const uint32_t k = cand[tid];
+            int above = 0, same = 0;
+#pragma unroll 8
+            for (int x = 0; x < all; ++x) {
+                const uint32_t y = cand[x];
+                above += y > k;
+                same += y == k;
+            }
+            if (above < need && need <= above + same) {  // all rows of that key write the same
+                found[0] = (int)k;
+                found[1] = need - above;
+            }
+        }
+        __syncthreads();
+        prefix = (uint32_t)found[0];
+        need = found[1];
+        break;
     }
     // every warp's share of the slice, in row order
     const int sub = ((n + SEL_WARPS - 1) / SEL_WARPS + 31) / 32 * 32;
     const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
     int gt = 0, eq = 0, gt_b = 0, eq_b = 0;
+#pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
         const uint32_t k = key_at(i);
         const int is_gt = k > prefix, is_eq = k == prefix, low = r0 + i < a.budget;
@@ -394,21 +442,33 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     const int kept_b = gb + min(eb, need);  // rows kept before the budget
     int32_t* out = a.moves + (size_t)u * a.max_moves * 2;
     const unsigned below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane, r = r0 + i;
-        const uint32_t k = i < w1 ? key_at(i) : 0u;
-        const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
-        const unsigned mg = __ballot_sync(FULL, is_gt), me = __ballot_sync(FULL, is_eq);
-        const int eq_before = e + __popc(me & below);
-        const int kept_before = g + __popc(mg & below) + min(eq_before, need);
-        const bool kept = is_gt || (is_eq && eq_before < need);
-        if (i < w1) {
-            const int m = kept_before - kept_b, h = r - kept_before;
-            if (kept && r >= a.budget && m < a.max_moves) out[2 * m] = r;
-            if (!kept && r < a.budget && h < a.max_moves) out[2 * h + 1] = r;
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        uint32_t k4[4];
+        bool any = r0 + i0 < a.budget;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + 32 * q + lane;
+            k4[q] = i < w1 ? key_at(i) : 0u;
+            any |= i < w1 && k4[q] >= prefix;
         }
-        g += __popc(mg);
-        e += __popc(me);
+        if (!__any_sync(FULL, any)) continue;  // past the budget and nothing kept
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + 32 * q + lane, r = r0 + i;
+            const uint32_t k = k4[q];
+            const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
+            const unsigned mg = __ballot_sync(FULL, is_gt), me = __ballot_sync(FULL, is_eq);
+            const int eq_before = e + __popc(me & below);
+            const int kept_before = g + __popc(mg & below) + min(eq_before, need);
+            const bool kept = is_gt || (is_eq && eq_before < need);
+            if (i < w1) {
+                const int m = kept_before - kept_b, h = r - kept_before;
+                if (kept && r >= a.budget && m < a.max_moves) out[2 * m] = r;
+                if (!kept && r < a.budget && h < a.max_moves) out[2 * h + 1] = r;
+            }
+            g += __popc(mg);
+            e += __popc(me);
+        }
     }
     if (tid == 0 && rank == 0) a.n_moves[u] = a.budget - kept_b;
     if (CS > 1) cluster_sync();  // no CTA leaves while a peer may read its counts
@@ -462,6 +522,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, int sms, int dev, cudaStrea
 // ---------------------------------------------------------------- eviction: moves
 constexpr int APPLY_THREADS = 128;
 constexpr int BATCH = 16;  // moves of a warp at a time
+constexpr int APPLY_FLIGHT = 2;  // rows that a lane has under way
 
 struct ApplyArgs {
     Cache c;
@@ -475,7 +536,7 @@ struct ApplyArgs {
 // A warp takes BATCH moves: lane l looks up the page of move l's source, lane
 // 16 + l that of its destination, so that the chain count -> moves -> page ids
 // -> rows is walked once for all of them; then VPR lanes carry a row, 16 bytes
-// of K and of V each, with IN_FLIGHT rows under way.
+// of K and of V each, with APPLY_FLIGHT rows under way.
 template <int VPR>
 __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid_constant__ ApplyArgs a) {
     ptx::grid_dependency_wait();
@@ -517,11 +578,11 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
             if (a.c.pos) a.c.pos[o + dst] = a.c.pos[o + row];
         }
 #pragma unroll
-        for (int b = 0; b < BATCH; b += RP * IN_FLIGHT) {
+        for (int b = 0; b < BATCH; b += RP * APPLY_FLIGHT) {
             if (k0 + b >= n) break;
-            uint4 kv[IN_FLIGHT], vv[IN_FLIGHT];
+            uint4 kv[APPLY_FLIGHT], vv[APPLY_FLIGHT];
 #pragma unroll
-            for (int x = 0; x < IN_FLIGHT; ++x) {
+            for (int x = 0; x < APPLY_FLIGHT; ++x) {
                 const int m = b + x * RP + sub;
                 const long long ks = __shfl_sync(FULL, ko, m), vs = __shfl_sync(FULL, vo, m);
                 if ((good >> m) & 1) {
@@ -530,7 +591,7 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
                 }
             }
 #pragma unroll
-            for (int x = 0; x < IN_FLIGHT; ++x) {
+            for (int x = 0; x < APPLY_FLIGHT; ++x) {
                 const int m = b + x * RP + sub;
                 const long long kd = __shfl_sync(FULL, ko, m + 16), vd = __shfl_sync(FULL, vo, m + 16);
                 if ((good >> m) & 1) {
