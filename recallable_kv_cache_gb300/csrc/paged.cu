@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(128) paged_advance_kernel(const __grid_constan
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;        // 11 bits of the key a pass: 11, 11 and 10
+constexpr int SEL_LIST = 1024;        // keys of one bin that are listed
 constexpr int SEL_CAND = 256;         // keys of one bin that are ranked directly
 constexpr int SEL_MAX_CLUSTER = 8;
 constexpr int SEL_MAX_SLICE = 45056;  // keys of one CTA that stay in shared memory (176 KB)
@@ -235,9 +236,9 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 // which every CTA adds its occupied bins in all its peers' shared memory (few
 // of the 2048 are occupied; every CTA reading all bins of its peers took 97 us
 // for 32 units of 128k rows where this takes SEL128 us).  Where a digit
-// leaves at most SEL_CAND keys (a first digit's bin is a quarter of a power of
-// two) they are gathered and the one of the wanted rank is found by counting,
-// which saves the digits behind it.  Then a row is kept if
+// leaves at most SEL_LIST keys (a first digit's bin is a quarter of a power of
+// two) they are listed, and later digits look at the list alone; where it
+// leaves at most SEL_CAND, the key of the wanted rank is found by counting.  Then a row is kept if
 // its key is above that one, or equal and among the first that fit.  With
 // gt(r), eq(r) the rows before r above and equal, kept(r) = gt(r) + min(eq(r),
 // fitting) rows are kept before r, so the k-th hole is the row r < budget, not
@@ -249,11 +250,13 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     __shared__ int hist[3][SEL_BINS];  // the unit's, one a pass
     __shared__ int mine[CS > 1 ? SEL_BINS : 1];
     __shared__ int warp_sum[SEL_WARPS];
-    __shared__ int counts[SEL_WARPS][4];  // rows above, equal; the same of rows below the budget
-    __shared__ int cta_counts[4];
+    __shared__ int4 counts[SEL_WARPS];  // rows above, equal; the same of rows below the budget
+    __shared__ int4 cta_counts;
     __shared__ int found[3];
-    __shared__ uint32_t cand[SEL_CAND], own_cand[CS > 1 ? SEL_CAND : 1];
-    __shared__ int n_cand;
+    __shared__ uint32_t list[SEL_LIST];  // of this CTA's rows, and where they are in the slice
+    __shared__ int list_at[SEL_LIST];
+    __shared__ uint32_t cand[SEL_CAND], own_cand[SEL_CAND];  // of the unit, of this CTA's rows
+    __shared__ int n_list, n_cand;
     const int u = blockIdx.x / CS, s = u / a.c.heads;
     const int rank = CS > 1 ? (int)cluster_rank() : 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
     if (CS > 1)
         for (int i = tid; i < SEL_BINS; i += SEL_THREADS) mine[i] = 0;
-    if (tid == 0) n_cand = 0;
+    if (tid == 0) n_list = n_cand = 0;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     if (tid == 0 && rank == 0) check_len(a.c, s);
@@ -294,19 +297,47 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         for (int e = 0; e < 4; ++e)
             if (i + e < n) atomicAdd(&local[k[e] >> 21], 1);
     }
+    // every warp's share of the slice, in row order
+    const int sub = ((n + SEL_WARPS - 1) / SEL_WARPS + 127) / 128 * 128;
+    const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
+    // f(key, index) for the warp's rows; a lane has four keys in a row
+    auto each = [&](auto f) {
+#pragma unroll 2
+        for (int i = w0 + 4 * lane; i < w1; i += 128) {
+            uint32_t k[4];
+            if (CACHED) {
+                const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+                k[0] = v.x;
+                k[1] = v.y;
+                k[2] = v.z;
+                k[3] = v.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) k[e] = i + e < w1 ? key_at(i + e) : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < w1) f(k[e], i + e);
+        }
+    };
     uint32_t prefix = 0, mask = 0;
     int need = a.budget;  // rows still to take among those whose key matches the prefix
+    int gt = 0, eq = 0, gt_b = 0, eq_b = 0;  // rows above, equal; the same of rows below the budget
+    bool listed = false;
+    const int low_end = a.budget - r0;  // indices below it are rows below the budget
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         const uint32_t digit = pass == 2 ? 1023u : 2047u;
         if (pass > 0) {
             if (CS == 1) local = hist[pass];
-#pragma unroll 4
-            for (int i = tid; i < n; i += SEL_THREADS) {
-                const uint32_t k = key_at(i);
+            auto add = [&](uint32_t k, int) {
                 if ((k & mask) == prefix) atomicAdd(&local[(k >> shift) & digit], 1);
-            }
+            };
+            if (listed)
+                for (int x = tid; x < n_list; x += SEL_THREADS) add(list[x], 0);
+            else
+                each(add);
         }
         if (CS > 1) {
             __syncthreads();
@@ -354,23 +385,35 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         prefix |= (uint32_t)found[0] << shift;
         need = found[1];
         mask |= digit << shift;
-        if (pass == 2 || found[2] > SEL_CAND) continue;
-        // the keys of this bin, of all CTAs, in any order
-        uint32_t* list = CS > 1 ? own_cand : cand;
-#pragma unroll 4
-        for (int i = tid; i < n; i += SEL_THREADS) {
-            const uint32_t k = key_at(i);
-            if ((k & mask) == prefix) list[atomicAdd(&n_cand, 1)] = k;
-        }
         const int all = found[2];
+        if (!listed && all <= SEL_LIST) {
+            // the keys of this bin, in any order; those above it count whatever
+            // the last digits are
+            each([&](uint32_t k, int i) {
+                if ((k & mask) > prefix) {
+                    ++gt;
+                    gt_b += i < low_end;
+                } else if ((k & mask) == prefix) {
+                    const int at = atomicAdd(&n_list, 1);
+                    list[at] = k;
+                    list_at[at] = i;
+                }
+            });
+            listed = true;
+            __syncthreads();
+        }
+        if (!listed || all > SEL_CAND) continue;
+        uint32_t* own = CS > 1 ? own_cand : cand;
+        for (int x = tid; x < n_list; x += SEL_THREADS)
+            if ((list[x] & mask) == prefix) own[atomicAdd(&n_cand, 1)] = list[x];
         sync_all();
         if (CS > 1) {
             // warp r copies what CTA r has, behind what the CTAs before it have
             const int m = lane < CS ? peer_word(&n_cand, lane) : 0;
-            const int mine_n = __shfl_sync(FULL, m, warp & 31);
+            const int from = __shfl_sync(FULL, m, warp & 31);
             const int to = __reduce_add_sync(FULL, lane < warp ? m : 0);
             if (warp < CS)
-                for (int i = lane; i < mine_n; i += 32)
+                for (int i = lane; i < from; i += 32)
                     cand[to + i] = (uint32_t)peer_word(reinterpret_cast<const int*>(own_cand + i), warp);
             __syncthreads();
         }
@@ -393,69 +436,60 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         need = found[1];
         break;
     }
-    // every warp's share of the slice, in row order
-    const int sub = ((n + SEL_WARPS - 1) / SEL_WARPS + 31) / 32 * 32;
-    const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
-    int gt = 0, eq = 0, gt_b = 0, eq_b = 0;
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key_at(i);
-        const int is_gt = k > prefix, is_eq = k == prefix, low = r0 + i < a.budget;
-        gt += is_gt;
-        eq += is_eq;
-        gt_b += is_gt & low;
-        eq_b += is_eq & low;
-    }
+    auto count = [&](uint32_t k, int i) {
+        gt += k > prefix;
+        eq += k == prefix;
+        gt_b += k > prefix && i < low_end;
+        eq_b += k == prefix && i < low_end;
+    };
+    if (!listed)
+        each(count);
+    else
+        for (int x = lane; x < n_list; x += 32)
+            if (list_at[x] >= w0 && list_at[x] < w1) count(list[x], list_at[x]);
     gt = __reduce_add_sync(FULL, gt);
     eq = __reduce_add_sync(FULL, eq);
     gt_b = __reduce_add_sync(FULL, gt_b);
     eq_b = __reduce_add_sync(FULL, eq_b);
-    if (lane == 0) {
-        counts[warp][0] = gt;
-        counts[warp][1] = eq;
-        counts[warp][2] = gt_b;
-        counts[warp][3] = eq_b;
-    }
+    if (lane == 0) counts[warp] = make_int4(gt, eq, gt_b, eq_b);
     __syncthreads();
-    if (tid < 4) {
-        int t = 0;
-        for (int w = 0; w < SEL_WARPS; ++w) t += counts[w][tid];
-        cta_counts[tid] = t;
-    }
-    sync_all();
-    int g = 0, e = 0, gb = 0, eb = 0;
-#pragma unroll
-    for (int r = 0; r < CS; ++r) {
-        const int v0 = CS == 1 ? cta_counts[0] : peer_word(&cta_counts[0], r);
-        const int v1 = CS == 1 ? cta_counts[1] : peer_word(&cta_counts[1], r);
-        if (r < rank) {
-            g += v0;
-            e += v1;
+    // rows above and equal before this warp's, in this CTA and in those before
+    // it; rows below the budget of the whole unit
+    int4 c = lane < SEL_WARPS ? counts[lane] : make_int4(0, 0, 0, 0);
+    int g = __reduce_add_sync(FULL, lane < warp ? c.x : 0), e = __reduce_add_sync(FULL, lane < warp ? c.y : 0);
+    int gb = __reduce_add_sync(FULL, c.z), eb = __reduce_add_sync(FULL, c.w);
+    if (CS > 1) {
+        const int all_g = __reduce_add_sync(FULL, c.x), all_e = __reduce_add_sync(FULL, c.y);
+        if (tid == 0) cta_counts = make_int4(all_g, all_e, gb, eb);
+        cluster_sync();
+        c = make_int4(0, 0, 0, 0);
+        if (lane < CS) {
+            const int* p = reinterpret_cast<const int*>(&cta_counts);
+            c = make_int4(peer_word(p, lane), peer_word(p + 1, lane), peer_word(p + 2, lane), peer_word(p + 3, lane));
         }
-        gb += CS == 1 ? cta_counts[2] : peer_word(&cta_counts[2], r);
-        eb += CS == 1 ? cta_counts[3] : peer_word(&cta_counts[3], r);
-    }
-    for (int w = 0; w < warp; ++w) {
-        g += counts[w][0];
-        e += counts[w][1];
+        g += __reduce_add_sync(FULL, lane < rank ? c.x : 0);
+        e += __reduce_add_sync(FULL, lane < rank ? c.y : 0);
+        gb = __reduce_add_sync(FULL, c.z);
+        eb = __reduce_add_sync(FULL, c.w);
+        // the peers' shared memory has been read for the last time
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     }
     const int kept_b = gb + min(eb, need);  // rows kept before the budget
     int32_t* out = a.moves + (size_t)u * a.max_moves * 2;
     const unsigned below = (1u << lane) - 1u;
     for (int i0 = w0; i0 < w1; i0 += 128) {
         uint32_t k4[4];
-        bool any = r0 + i0 < a.budget;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int i = i0 + 32 * q + lane;
             k4[q] = i < w1 ? key_at(i) : 0u;
-            any |= i < w1 && k4[q] >= prefix;
         }
-        if (!__any_sync(FULL, any)) continue;  // past the budget and nothing kept
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int i = i0 + 32 * q + lane, r = r0 + i;
             const uint32_t k = k4[q];
+            // past the budget and nothing kept
+            if (!__any_sync(FULL, i < w1 && k >= prefix) && i0 + 32 * q >= low_end) continue;
             const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
             const unsigned mg = __ballot_sync(FULL, is_gt), me = __ballot_sync(FULL, is_eq);
             const int eq_before = e + __popc(me & below);
@@ -471,7 +505,7 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
         }
     }
     if (tid == 0 && rank == 0) a.n_moves[u] = a.budget - kept_b;
-    if (CS > 1) cluster_sync();  // no CTA leaves while a peer may read its counts
+    if (CS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while a peer may read its counts
 }
 
 template <int CS, bool CACHED>
