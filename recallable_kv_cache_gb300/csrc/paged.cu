@@ -180,8 +180,7 @@ __global__ void __launch_bounds__(128) paged_advance_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- eviction: selection
-constexpr int SEL_THREADS = 512;
-constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_LONG = 4096;        // rows of a CTA from which it has 1024 threads, below 512
 constexpr int SEL_BINS = 2048;        // 11 bits of the key a pass: 11, 11 and 10
 constexpr int SEL_LIST = 1024;        // keys of one bin that are listed
 constexpr int SEL_CAND = 256;         // keys of one bin that are ranked directly
@@ -235,7 +234,7 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 // the key of the budget-th row follows digit by digit from the histograms, to
 // which every CTA adds its occupied bins in all its peers' shared memory (few
 // of the 2048 are occupied; every CTA reading all bins of its peers took 97 us
-// for 32 units of 128k rows where this takes SEL128 us).  Where a digit
+// for 32 units of 128k rows where this takes 24 us).  Where a digit
 // leaves at most SEL_LIST keys (a first digit's bin is a quarter of a power of
 // two) they are listed, and later digits look at the list alone; where it
 // leaves at most SEL_CAND, the key of the wanted rank is found by counting.  Then a row is kept if
@@ -244,8 +243,9 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 // fitting) rows are kept before r, so the k-th hole is the row r < budget, not
 // kept, with r - kept(r) = k and the k-th mover the kept row r >= budget with
 // kept(r) - kept(budget) = k: one counting pass and one writing pass.
-template <int CS, bool CACHED>
-__global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_constant__ SelectArgs a) {
+template <int CS, int SEL_THREADS, bool CACHED>
+__global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __grid_constant__ SelectArgs a) {
+    constexpr int SEL_WARPS = SEL_THREADS / 32;
     extern __shared__ uint32_t keys[];
     __shared__ int hist[3][SEL_BINS];  // the unit's, one a pass
     __shared__ int mine[CS > 1 ? SEL_BINS : 1];
@@ -508,20 +508,20 @@ __global__ void __launch_bounds__(SEL_THREADS) paged_select_kernel(const __grid_
     if (CS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while a peer may read its counts
 }
 
-template <int CS, bool CACHED>
+template <int CS, int THREADS, bool CACHED>
 cudaError_t launch_select_cs(const SelectArgs& a, int dev, cudaStream_t s) {
     const int slice = round_up(ceil_div(a.c.rows, CS), 128);
     const size_t smem = CACHED ? (size_t)slice * 4 : 0;
     static std::atomic<bool> set[MAX_DEVICES];
     if (CACHED && !set[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<CS, CACHED>,
+        const cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<CS, THREADS, CACHED>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_MAX_SLICE * 4);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.c.seqs * a.c.heads * CS));
-    cfg.blockDim = dim3(SEL_THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -533,23 +533,33 @@ cudaError_t launch_select_cs(const SelectArgs& a, int dev, cudaStream_t s) {
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = CS > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, paged_select_kernel<CS, CACHED>, a);
+    return cudaLaunchKernelEx(&cfg, paged_select_kernel<CS, THREADS, CACHED>, a);
+}
+
+template <int CS>
+cudaError_t launch_select_rows(const SelectArgs& a, int dev, cudaStream_t s) {
+    // 512 threads are quicker through their barriers, 1024 through many rows:
+    // 6.9 against 7.7 us for 256 units of 1344 rows, 28.0 against 23.8 us for
+    // 32 units of 128k rows on four CTAs each
+    return a.c.rows / CS < SEL_LONG ? launch_select_cs<CS, 512, true>(a, dev, s)
+                                    : launch_select_cs<CS, 1024, true>(a, dev, s);
 }
 
 cudaError_t launch_evict_select(const SelectArgs& a, int sms, int dev, cudaStream_t s) {
     const long long units = (long long)a.c.seqs * a.c.heads;
-    // more CTAs per unit while they would fit side by side (two to an SM) and
-    // have rows to work on, and as many as the keys need
+    // more CTAs per unit while each has an SM of its own and rows to work on
+    // (two to an SM: 19.7 us instead of 12.2 for 128 units of 8k rows), and as
+    // many as the keys need
     int cs = 1;
     while (cs < SEL_MAX_CLUSTER && (a.c.rows > cs * (long long)SEL_MAX_SLICE ||
-                                    (units * cs * 2 <= 2LL * sms && a.c.rows / cs >= 8 * SEL_THREADS)))
+                                    (units * cs * 2 <= sms && a.c.rows / cs >= SEL_LONG)))
         cs *= 2;
-    if (a.c.rows > cs * (long long)SEL_MAX_SLICE) return launch_select_cs<SEL_MAX_CLUSTER, false>(a, dev, s);
+    if (a.c.rows > cs * (long long)SEL_MAX_SLICE) return launch_select_cs<SEL_MAX_CLUSTER, 1024, false>(a, dev, s);
     switch (cs) {
-        case 1: return launch_select_cs<1, true>(a, dev, s);
-        case 2: return launch_select_cs<2, true>(a, dev, s);
-        case 4: return launch_select_cs<4, true>(a, dev, s);
-        default: return launch_select_cs<8, true>(a, dev, s);
+        case 1: return launch_select_rows<1>(a, dev, s);
+        case 2: return launch_select_rows<2>(a, dev, s);
+        case 4: return launch_select_rows<4>(a, dev, s);
+        default: return launch_select_rows<8>(a, dev, s);
     }
 }
 

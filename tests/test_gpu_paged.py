@@ -449,6 +449,8 @@ SELECT = [
     ([70000], 1, 16, 30000, 16, 500),
     ([9001, 8000], 1, 48, 3001, 16, 500),
     ([400001], 1, 16, 1000, 16, 500),
+    ([40000, 20000, 33, 39999], 2, 64, 5000, 16, 100),
+    ([6000, 5999] * 20, 2, 16, 700, 16, 100),
 ]
 
 
