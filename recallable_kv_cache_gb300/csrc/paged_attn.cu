@@ -187,7 +187,11 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0,
 //   S[h][r] = q[h] . K[r]        m16n8k16: M = heads (NB blocks of 8), N = 8 rows
 //   O[c][h] += V[r][c] P[h][r]   M = 16 channels, N = 8 heads, K = 16 rows
 // bf16 products are exact and add up in fp32.  P is fed to the second product
-// as a sum of bf16 terms.
+// as three bf16 terms (P = hi + mid + lo holds all 24 bits; with two, the
+// outputs were off by 1.2e-6 of their norm, now 4e-7).  A tile's products start
+// from zero and join O by ordinary additions: the tensor core truncates what
+// it accumulates, and over the 290 tiles of a warp at 256 units of 32k rows
+// that alone put the outputs off by 1.1e-5.
 template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
@@ -250,7 +254,7 @@ struct TilesBf16 {
             }
         }
         const int r0 = (lane & 3) * 2;
-        uint32_t ph[NB][2], pm[NB][2];
+        uint32_t ph[NB][2], pm[NB][2], pl[NB][2];
         float sc[NB];
         bool grew = false;
 #pragma unroll
@@ -282,11 +286,12 @@ struct TilesBf16 {
             }
             lrun[b] = lrun[b] * sc[b] + ((p[0] + p[1]) + (p[2] + p[3]));
             mrun[b] = mnew;
-            // P = hi + mid, each rounded to bf16: off by at most 2^-17 of itself
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 ph[b][i] = pack2(p[2 * i], p[2 * i + 1]);
-                pm[b][i] = pack2(p[2 * i] - lo_of(ph[b][i]), p[2 * i + 1] - hi_of(ph[b][i]));
+                const float x = p[2 * i] - lo_of(ph[b][i]), y = p[2 * i + 1] - hi_of(ph[b][i]);
+                pm[b][i] = pack2(x, y);
+                pl[b][i] = pack2(x - lo_of(pm[b][i]), y - hi_of(pm[b][i]));
             }
         }
         if (__any_sync(FULL, grew)) {
@@ -311,8 +316,12 @@ struct TilesBf16 {
             ldsm_x4_t(vb + (chunk >> 3) * 2048 + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), a0, a1, a2, a3);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                mma(o[b][mt], a0, a1, a2, a3, ph[b][0], ph[b][1]);
-                mma(o[b][mt], a0, a1, a2, a3, pm[b][0], pm[b][1]);
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma(t, a0, a1, a2, a3, pl[b][0], pl[b][1]);
+                mma(t, a0, a1, a2, a3, pm[b][0], pm[b][1]);
+                mma(t, a0, a1, a2, a3, ph[b][0], ph[b][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[b][mt][e] += t[e];
             }
         }
         // zeros above were written by this thread's view of shared memory: the
