@@ -55,8 +55,6 @@ struct AttnArgs {
     const float* mass_in;
     float* mass_out;
     unsigned* arrived;  // [grid] CTAs that have left their part of the unit that begins in CTA i; zero between calls
-    int4* start;        // [grid][warps] where a warp's tiles begin: sequence, KV head, tile in the unit, rows of the unit
-    int2* deal;         // tiles of the call, CTAs that share them
     float* part;        // [grid][2] partials of units that several CTAs share
     float* head;        // [grid][warps] partials of a unit that a warp entered part-way and left; null: in shared memory
     float* lse2;        // [units][g], base 2
@@ -114,13 +112,13 @@ struct Deal {
     }
 };
 
-// The deal of this call, and where the shares of this CTA's warps begin.  Every
+// The deal of this call, and where the shares of CTA `cta`'s warps begin.  Every
 // thread adds up a chunk of the sequences' tiles; a scan gives the total (below
 // 2^31, checked for the cache's extents) and the thread in whose chunk a
 // warp's first tile falls leaves the chunk's first sequence and how many tiles
 // behind it the warp begins.
 template <int TR, int NT>
-__device__ Deal deal_out(const Cache& c, int2* start) {
+__device__ Deal deal_out(const Cache& c, int2* start, int cta, int grid) {
     constexpr int NW = NT / 32;
     __shared__ int warp_sum[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -143,10 +141,10 @@ __device__ Deal deal_out(const Cache& c, int2* start) {
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const Deal deal(total, Deal::ctas(total, NW, gridDim.x), NW);
+    const Deal deal(total, Deal::ctas(total, NW, grid), NW);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const int t = deal.begin_warp(blockIdx.x * NW + w);
+        const int t = deal.begin_warp(cta * NW + w);
         if (t >= before && t < before + v) start[w] = make_int2(s0, t - before);
     }
     __syncthreads();
@@ -623,7 +621,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     if (threadIdx.x < 2) shared_units[threadIdx.x].x = -1;
     ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
-    const Deal deal = deal_out<TR, NT>(a.c, start);
+    const Deal deal = deal_out<TR, NT>(a.c, start, blockIdx.x, gridDim.x);
     const bool works = (int)blockIdx.x < deal.n_cta && deal.total > 0;
     const int t_begin = works ? deal.begin_warp(blockIdx.x * NW + warp) : 0;
     const int t_end = works ? deal.begin_warp(blockIdx.x * NW + warp + 1) : 0;
@@ -641,7 +639,6 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
             e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
         };
         Pos base = walk<TR>(a.c, start[warp].x, start[warp].y);
-        if (a.mass_out && lane == 0) a.start[blockIdx.x * NW + warp] = make_int4(base.s, base.h, base.k, rows_held(a.c, base.s));
         // q is asked for before the tiles: behind them it would wait for all
         // the copies in flight (some 4 us at full bandwidth)
         enter(base.s, base.h, base.nt, t_begin - base.k);
@@ -739,7 +736,6 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
         leave(true);
     }
     if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) *a.deal = make_int2(deal.total, deal.n_cta);
         for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
     }
     // units without rows: nothing else writes their outputs
@@ -835,28 +831,40 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
 
 // ---------------------------------------------------------------- accumulated weights
 // mass_out = mass_in + sum_j e^{s_j - lse_j} over the tiles of the attention
-// kernel's warps, each share in W_SPLIT parts, a lane four rows at a time: the
-// scores come from L2 or HBM, so what counts is how many are asked for at once.
-constexpr int W_SPLIT = 2, W_THREADS = 384;
+// kernel's warps, W_SPLIT CTAs to one of its, a lane four rows at a time.  Only
+// the scores and the lse come from the attention kernel: the deal is derived
+// again and the first rows' weights are loaded while its last CTAs still run.
+constexpr int W_SPLIT = 2;
 
 template <int TR, int NW>
-__global__ void __launch_bounds__(W_THREADS) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
-    ptx::grid_dependency_wait();
+__global__ void __launch_bounds__(NW * 32) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ int2 start[NW];
     ptx::allow_dependent_launch();
-    const int lane = threadIdx.x & 31, w = blockIdx.x * (W_THREADS / 32) + (threadIdx.x >> 5), gw = w / W_SPLIT;
-    if (gw >= MAX_GRID * NW) return;
-    const int4 at = a.start[gw];  // stale where the warp had no tiles
-    const int2 d = *a.deal;
-    const Deal deal(d.x, d.y, NW);
-    if (gw >= d.y * NW || d.x == 0) return;
-    const int b0 = deal.begin_warp(gw), b1 = deal.begin_warp(gw + 1), part = w % W_SPLIT;
-    const int t0 = b0 + (b1 - b0) * part / W_SPLIT, t1 = b0 + (b1 - b0) * (part + 1) / W_SPLIT;
-    if (t0 == t1) return;
-    int len = at.w;
-    Pos p{at.x, at.y, at.z, (len + TR - 1) / TR};
-    p = advance<TR>(a.c, p, t0 - b0);
-    if (p.s != at.x) len = rows_held(a.c, p.s);
-    for (int t = t0; t < t1;) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x / W_SPLIT, part = blockIdx.x % W_SPLIT;
+    // lens, table and mass_in are not written by the attention kernel, and it
+    // began after what wrote them had ended
+    const Deal deal = deal_out<TR, NW * 32>(a.c, start, cta, gridDim.x / W_SPLIT);
+    int t = 0, t1 = 0;
+    if (cta < deal.n_cta) {
+        const int b0 = deal.begin_warp(cta * NW + warp), n = deal.begin_warp(cta * NW + warp + 1) - b0;
+        t = b0 + n * part / W_SPLIT;
+        t1 = b0 + n * (part + 1) / W_SPLIT;
+    }
+    Pos p{};
+    int len = 0;
+    auto mass_at = [&](int u, int r, int r1) {
+        return a.mass_in && r < r1 ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < t1) {
+        p = advance<TR>(a.c, walk<TR>(a.c, start[warp].x, start[warp].y), t - deal.begin_warp(cta * NW + warp));
+        len = rows_held(a.c, p.s);
+        next = mass_at(p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
+    }
+    ptx::grid_dependency_wait();
+    while (t < t1) {
         const int u = p.s * a.c.heads + p.h;
         const int n = min(p.nt - p.k, t1 - t);  // tiles of this unit
         const float* lse2 = a.lse2 + (size_t)u * a.g;
@@ -864,7 +872,8 @@ __global__ void __launch_bounds__(W_THREADS) paged_weights_kernel(const __grid_c
         const int r1 = min(len, (p.k + n) * TR);
         for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
             const size_t o = (size_t)u * a.c.rows + r;
-            float4 v = a.mass_in ? *reinterpret_cast<const float4*>(a.mass_in + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 v = next;
+            next = mass_at(u, r + 128, r1);
             float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int j = 0; j < a.g; j += 4) {
                 float4 x[4];
@@ -899,9 +908,11 @@ __global__ void __launch_bounds__(W_THREADS) paged_weights_kernel(const __grid_c
             }
         }
         t += n;
-        const int s = p.s;
         p = advance<TR>(a.c, p, n);
-        if (p.s != s && p.nt) len = rows_held(a.c, p.s);
+        if (t < t1) {
+            len = rows_held(a.c, p.s);
+            next = mass_at(p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
+        }
     }
 }
 
@@ -948,15 +959,13 @@ constexpr int MAX_WARPS = 12;
 constexpr size_t MAX_SMEM = 227 * 1024;
 
 struct Layout {
-    size_t deal, start, part, head, lse2, scores, total;  // byte offsets; the arrivals come first
+    size_t part, head, lse2, scores, total;  // byte offsets; the arrivals come first
 };
 Layout layout_of(const Cache& c, int g, bool with_mass) {
     Layout l;
     const size_t units = (size_t)c.seqs * c.heads, pf = part_floats(g) * sizeof(float);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.deal = MAX_GRID * sizeof(unsigned);
-    l.start = l.deal + 256;
-    l.part = l.start + MAX_GRID * MAX_WARPS * sizeof(int4);
+    l.part = MAX_GRID * sizeof(unsigned);
     l.head = l.part + up(MAX_GRID * 2 * pf);
     l.lse2 = l.head + up((size_t)MAX_GRID * MAX_WARPS * pf);
     l.scores = l.lse2 + up(units * g * sizeof(float));
@@ -988,8 +997,7 @@ cudaError_t launch(AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, in
     }
     cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(E::WARPS * 32), smem, s, a, tk, tv);
     if (e == cudaSuccess && a.mass_out)
-        e = launch_dependent(paged_weights_kernel<E::TR, E::WARPS>, dim3(ceil_div(grid * E::WARPS * W_SPLIT, W_THREADS / 32)),
-                             dim3(W_THREADS), 0, s, a);
+        e = launch_dependent(paged_weights_kernel<E::TR, E::WARPS>, dim3(grid * W_SPLIT), dim3(E::WARPS * 32), 0, s, a);
     return e;
 }
 
@@ -1041,8 +1049,6 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.mass_in = mass_in;
     a.mass_out = mass_out;
     a.arrived = reinterpret_cast<unsigned*>(w);
-    a.deal = reinterpret_cast<int2*>(w + l.deal);
-    a.start = reinterpret_cast<int4*>(w + l.start);
     a.part = reinterpret_cast<float*>(w + l.part);
     a.head = reinterpret_cast<float*>(w + l.head);
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
