@@ -718,7 +718,7 @@ extern "C" ckv_status ckv_paged_evict_select(const ckv_paged_cache* cache, int32
     SelectArgs a;
     ckv_status st = check_cache(cache, &a.c);
     if (st != CKV_OK) return st;
-    if (!a.c.mass || !a.c.pos || !a.c.seen || !moves || !n_moves) return CKV_ERR_ARG;
+    if (!a.c.mass || !a.c.pos || !a.c.seen || (!moves && max_moves > 0) || !n_moves) return CKV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(moves) & 7u) return CKV_ERR_ALIGN;
     if (sinks < 0 || recent < 0 || (long long)sinks + recent > budget) return CKV_ERR_ARG;
     st = check_evict(a.c, budget, max_moves);
@@ -743,7 +743,7 @@ extern "C" ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_
     ApplyArgs a;
     ckv_status st = check_cache(cache, &a.c);
     if (st != CKV_OK) return st;
-    if (!moves || !n_moves) return CKV_ERR_ARG;
+    if ((!moves && max_moves > 0) || !n_moves) return CKV_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(moves) & 7u) return CKV_ERR_ALIGN;
     st = check_evict(a.c, budget, max_moves);
     if (st != CKV_OK) return st;

@@ -42,7 +42,13 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
-constexpr int STAGE = 8192;  // K rows, then V rows of one tile
+// A stage holds the K rows, then the V rows of one tile.  Eight warps with two
+// stages each have 128 KB of an SM under way.  More of it lowers the rate (12
+// warps of two stages: 90 instead of 87 us for one sequence of 128k rows and 8
+// KV heads, 642 instead of 627 us for 32 of 32k rows), less does too (four of
+// three: 104 and 744 us).
+constexpr int STAGE = 8192;
+constexpr int WARPS = 8, NST = 2;
 
 struct AttnArgs {
     Cache c;
@@ -56,9 +62,8 @@ struct AttnArgs {
     float* mass_out;
     unsigned* arrived;  // [grid] CTAs that have left their part of the unit that begins in CTA i; zero between calls
     float* part;        // [grid][2] partials of units that several CTAs share
-    float* head;        // [grid][warps] partials of a unit that a warp entered part-way and left; null: in shared memory
     float* lse2;        // [units][g], base 2
-    float* scores;  // [units][g][rows], base 2
+    float* scores;      // [units][g][rows], base 2
     long long wait_limit;
 };
 
@@ -91,9 +96,7 @@ __device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
     return p;
 }
 // The deal: `total` tiles to the warps of n_cta CTAs, in order, as evenly as
-// they go (shares of q + 1 tiles, then of q).  A warp gets at least MIN_TILES
-// before the work is spread over more CTAs.
-constexpr int MIN_TILES = 1;
+// they go (shares of q + 1 tiles, then of q).
 // Merging across CTAs takes some 3 us, as long as two or three tiles of a warp.
 // So where every unit can have a CTA to itself and the largest then has at most
 // OWN_EXTRA tiles a warp more than in an even deal, it gets one: 128 units of
@@ -108,7 +111,7 @@ struct Deal {
         r = total - q * (n_cta * warps);
     }
     static __device__ __forceinline__ int ctas(int total, int warps, int grid) {
-        return max(1, min(grid, (total + warps * MIN_TILES - 1) / (warps * MIN_TILES)));
+        return max(1, min(grid, (total + warps - 1) / warps));
     }
     __device__ __forceinline__ int begin_warp(int w) const { return w * q + min(w, r); }  // w: across CTAs
     __device__ __forceinline__ int begin_cta(int c) const { return begin_warp(c * warps); }
@@ -218,8 +221,7 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0,
 template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
-    static constexpr int TR = 16, WARPS = 8, NST = 2, SCRATCH = 0;
-    static constexpr size_t STATIC_SMEM = 5120;  // what the kernel declares, at most
+    static constexpr int TR = 16, SCRATCH = 0;
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -347,8 +349,7 @@ struct TilesBf16 {
                 for (int e = 0; e < 4; ++e) o[b][mt][e] += t[e];
             }
         }
-        // zeros above were written by this thread's view of shared memory: the
-        // next copy into the stage must come after them
+        // the next copy into the stage must come after the zeros
         if (n < TR) ptx::fence_proxy_async_smem();
     }
     // O[j][c] (times w_j), maxima and sums to `put(j, c, value)`, `stat(j, m, l)`
@@ -429,8 +430,7 @@ __device__ __forceinline__ int reduce_scatter(float* v, int lane) {
 template <int GP>
 struct TilesF32 {
     using T = float;
-    static constexpr int TR = 8, WARPS = 8, NST = 2, SCRATCH = TR * GP;
-    static constexpr size_t STATIC_SMEM = 5120 + WARPS * SCRATCH * 8;
+    static constexpr int TR = 8, SCRATCH = TR * GP;
     static constexpr int LPR = GP > 8 ? 32 : GP > 2 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
@@ -616,10 +616,10 @@ __device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, co
 }
 
 template <typename E>
-__global__ void __launch_bounds__(E::WARPS * 32, 1)
+__global__ void __launch_bounds__(WARPS * 32, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
-    constexpr int TR = E::TR, NW = E::WARPS, NST = E::NST, NT = NW * 32;
+    constexpr int TR = E::TR, NW = WARPS, NT = NW * 32;
     using T = typename E::T;
     extern __shared__ unsigned char smem_raw[];
     // swizzled tiles need 1024-byte alignment
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     __shared__ int2 start[NW];
     __shared__ __align__(8) uint64_t full[NW][NST];
     __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
-    __shared__ Seg segs[2 * NW];    // partials left: [2 w] in a.head, [2 w + 1] in the warp's ring
+    __shared__ Seg segs[2 * NW];    // partials left: [2 w] on the way, behind the rings, [2 w + 1] last, in the warp's ring
     __shared__ __align__(16) float2 scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
     // merging: jobs and their sources; the units shared with other CTAs (unit,
     // first CTA, CTAs; unit -1: none, or not this CTA's to merge)
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
     const int t_end = works ? deal.begin_warp(cta * NW + warp + 1) : 0;
     unsigned char* ring = smem + (size_t)warp * NST * STAGE;
     const size_t pf = part_floats(a.g);
-    float* heads = a.head ? a.head + (size_t)blockIdx.x * NW * pf : reinterpret_cast<float*>(smem + NW * NST * STAGE);
+    float* heads = reinterpret_cast<float*>(smem + NW * NST * STAGE);
 
     if (t_begin < t_end) {
         E e;
@@ -862,8 +862,9 @@ __global__ void __launch_bounds__(E::WARPS * 32, 1)
 // again and the first rows' weights are loaded while its last CTAs still run.
 constexpr int W_SPLIT = 2;
 
-template <int TR, int NW>
-__global__ void __launch_bounds__(NW * 32) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
+template <int TR>
+__global__ void __launch_bounds__(WARPS * 32) paged_weights_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int NW = WARPS;
     __shared__ int2 start[NW];
     ptx::allow_dependent_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -982,50 +983,40 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
     return r == CUDA_SUCCESS;
 }
 
-constexpr int MAX_WARPS = 8;
-constexpr size_t MAX_SMEM = 227 * 1024;
 
 struct Layout {
-    size_t part, head, lse2, scores, total;  // byte offsets; the arrivals come first
+    size_t part, lse2, scores, total;  // byte offsets; the arrivals come first
 };
 Layout layout_of(const Cache& c, int g, bool with_mass) {
     Layout l;
     const size_t units = (size_t)c.seqs * c.heads, pf = part_floats(g) * sizeof(float);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l.part = MAX_GRID * sizeof(unsigned);
-    l.head = l.part + up(MAX_GRID * 2 * pf);
-    l.lse2 = l.head + up((size_t)MAX_GRID * MAX_WARPS * pf);
+    l.lse2 = l.part + up(MAX_GRID * 2 * pf);
     l.scores = l.lse2 + up(units * g * sizeof(float));
     l.total = l.scores + (with_mass ? up(units * g * (size_t)c.rows * sizeof(float)) : 0);
     return l;
 }
 
 template <typename E>
-cudaError_t launch(AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
-    static_assert(E::WARPS <= MAX_WARPS && 2 * E::WARPS <= 32, "workspace layout");
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
     const long long most = (long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, E::TR);  // tiles
-    const long long useful = (most + E::WARPS * MIN_TILES - 1) / (E::WARPS * MIN_TILES);
+    const long long useful = (most + WARPS - 1) / WARPS, units = (long long)a.c.seqs * a.c.heads;
     int grid = sms < MAX_GRID ? sms : MAX_GRID;
-    const long long units = (long long)a.c.seqs * a.c.heads;
     if (grid > useful) grid = (int)(useful > units || units > grid ? useful : units);
-    // partials that warps leave on the way stay in shared memory where there is
-    // room beside the rings (under load, L2 answers in 2 us at the merge)
-    size_t smem = (size_t)E::WARPS * E::NST * STAGE + 1024;
-    const size_t heads = E::WARPS * part_floats(a.g) * sizeof(float);
-    if (smem + heads <= MAX_SMEM - E::STATIC_SMEM) {
-        smem += heads;
-        a.head = nullptr;
-    }
+    // the rings, the partials that warps leave on the way, and room to align
+    const size_t rings = (size_t)WARPS * NST * STAGE + 1024;
+    const size_t smem = rings + WARPS * part_floats(a.g) * sizeof(float);
     static std::atomic<bool> set[MAX_DEVICES];
     if (!set[dev].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   MAX_SMEM - E::STATIC_SMEM);
+                                                   rings + WARPS * part_floats(MAX_G) * sizeof(float));
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(E::WARPS * 32), smem, s, a, tk, tv);
+    cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(WARPS * 32), smem, s, a, tk, tv);
     if (e == cudaSuccess && a.mass_out)
-        e = launch_dependent(paged_weights_kernel<E::TR, E::WARPS>, dim3(grid * W_SPLIT), dim3(E::WARPS * 32), 0, s, a);
+        e = launch_dependent(paged_weights_kernel<E::TR>, dim3(grid * W_SPLIT), dim3(WARPS * 32), 0, s, a);
     return e;
 }
 
@@ -1078,7 +1069,6 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.mass_out = mass_out;
     a.arrived = reinterpret_cast<unsigned*>(w);
     a.part = reinterpret_cast<float*>(w + l.part);
-    a.head = reinterpret_cast<float*>(w + l.head);
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
     a.scores = mass_out ? reinterpret_cast<float*>(w + l.scores) : nullptr;
     a.wait_limit = WAIT_LIMIT;

@@ -147,6 +147,11 @@ ATTEND = [
     ([5000, 1, 77], 4, 1, 64, "bf16", "phd"),
     ([3] * 70, 7, 4, 16, "bf16", "hpd"),
     ([3, 0, 20] * 60, 11, 2, 16, "f32", "hpd"),
+    # more sequences than a CTA has threads, and shares of units across CTAs
+    ([1, 0, 0, 37] * 200, 1, 4, 16, "bf16", "hpd"),
+    ([0, 2, 19] * 250, 1, 1, 16, "f32", "phd"),
+    ([2000, 1900, 1000], 3, 4, 16, "bf16", "hpd"),
+    ([2000, 5, 1000], 3, 16, 48, "f32", "hpd"),
 ]
 
 
@@ -336,6 +341,43 @@ def test_two_handles_and_graphs_at_once():
         assert torch.equal(c.out, out2) and torch.equal(c.lse, lse2)
 
 
+def test_shared_pages():
+    """Sequences that share a prefix's pages: each has its own weights."""
+    c = Case([64, 80, 33], 2, 4, 16, "bf16", width=5)
+    c.table[1, :4] = c.table[0, :4]
+    c.table[2, :2] = c.table[0, :2]
+    c.table[2, 2] = c.table[0, 2]
+    mass = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=mass)
+    torch.cuda.synchronize()
+    c.check_attention(mass_out=mass, mass_before=np.zeros(mass.shape))
+
+
+@pytest.mark.parametrize("dtype,g", [("bf16", 4), ("f32", 2)])
+def test_a_slab_is_a_paged_cache(dtype, g):
+    """The recallable path's [units][max_len][d] slabs under an identity table:
+    the paged attention equals the sparse attention whose budget covers all."""
+    from parity import ATTN_TOL, make_ctx
+    units, max_len, L = 5, 640, 601
+    gen = torch.Generator().manual_seed(2)
+    K, V = (torch.randn(units, max_len, D, generator=gen).to(DT[dtype]).cuda() for _ in range(2))
+    q = torch.randn(units, g, D, generator=gen).to(DT[dtype]).cuda()
+    ctx = make_ctx(units, g, max_len, 8, max_len, dtype)
+    ctx.cluster_prefill(K, L - 3, 7)
+    idx = torch.zeros(units, max_len, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(units, dtype=torch.int32, device="cuda")
+    want, got = (torch.zeros(units, g, D, device="cuda") for _ in range(2))
+    ctx.decode_step(q, K, V, max_len, L, idx, cnt, want)
+    cache = ckv.PagedCache(K.view(-1, 1, 64, D), V.view(-1, 1, 64, D),
+                           torch.arange(units * 10, dtype=torch.int32, device="cuda").view(units, 10),
+                           torch.full((units,), L, dtype=torch.int32, device="cuda"), g=g)
+    cache.decode_attn(q, got)
+    torch.cuda.synchronize()
+    assert ctx.device_error() == 0
+    assert (got - want).abs().max().item() <= ATTN_TOL[dtype]
+    ctx.close()
+
+
 def test_side_stream_argument():
     c = Case([100, 20], 2, 4, 16, "bf16")
     st = torch.cuda.Stream()
@@ -512,6 +554,16 @@ def test_evict_apply(dtype, layout, page, heads):
         for x, t in want.items():
             assert torch.equal(getattr(c, x), t), x
         assert c.lens.tolist() == [130, 130, 100, 0, 130] and int(c.err) == 0
+
+
+def test_eviction_of_nothing():
+    """A budget that the whole capacity fits: no moves, and no room for any needed."""
+    c = Case([64, 10], 2, 1, 16, "bf16", garbage=0.0)
+    moves = torch.zeros(2, 2, 0, 2, dtype=torch.int32, device="cuda")
+    n_moves = torch.full((2, 2), 9, dtype=torch.int32, device="cuda")
+    before = c.K.clone()
+    c.handle.evict(64, 8, 8, moves, n_moves)
+    assert not n_moves.any() and torch.equal(c.K, before) and c.lens.tolist() == [64, 10] and int(c.err) == 0
 
 
 def test_evict_apply_skips_bad_moves():
