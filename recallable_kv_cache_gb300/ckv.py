@@ -359,9 +359,6 @@ def append_kv(k_src, v_src, K, V, pos: int, n: int | None = None, stream=None):
                                ptr(V), _stream(stream)), "ckv_append_kv")
 
 
-_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
-
-
 class PagedCache:
     """A paged K/V cache over the caller's tensors (see the paged cache section
     of ckv.h): ``K``, ``V`` [n_pages, heads, page_size, 128] bf16 or float32, any
@@ -395,7 +392,7 @@ class PagedCache:
         self.seqs, self.heads, self.g, self.rows = seqs, heads, g, width * page
         self.dtype, self._code = K.dtype, code
         self._i32, self._f32 = torch.int32, torch.float32
-        self._per_seq, self._per_row = (seqs,), (seqs, heads, self.rows)
+        self._per_seq, self._per_unit, self._per_row = (seqs,), (seqs, heads), (seqs, heads, self.rows)
         self._q_shape, self._lse_shape = (seqs, heads * g, 128), (seqs, heads * g)
         for name, t, shape, dtype in (
                 ("V", V, tuple(K.shape), K.dtype), ("table", table, (seqs, width), self._i32),
@@ -408,14 +405,16 @@ class PagedCache:
         self.K, self.V, self.table, self.lens = K, V, table, lens
         self.mass, self.pos, self.seen, self.dev_err = mass, pos, seen, dev_err
         self._struct = PagedCacheStruct(
-            ptr(K), ptr(V), _I64x3(*K.stride()[:3]), _I64x3(*V.stride()[:3]), ptr(table),
+            ptr(K), ptr(V), (ctypes.c_int64 * 3)(*K.stride()[:3]), (ctypes.c_int64 * 3)(*V.stride()[:3]), ptr(table),
             ptr(lens), ptr(mass), ptr(pos), ptr(seen), ptr(dev_err), n_pages, heads, page, seqs, width, d, code)
         self._ref = ctypes.addressof(self._struct)
         so = lib()
         self._append, self._attn = so.ckv_paged_append, so.ckv_paged_decode_attn
         self._select, self._apply = so.ckv_paged_evict_select, so.ckv_paged_evict_apply
-        self._cuda, self._current_device = torch.cuda, torch.cuda.current_device
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._cuda, self._index = torch.cuda, self.device.index
+        # the raw calls: making a Stream object takes longer than the launch
+        self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self._stride_arrays = {}
         need = ctypes.c_int64()
         _check(so.ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),
                "ckv_paged_attn_workspace")
@@ -438,14 +437,24 @@ class PagedCache:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         return t.data_ptr()
 
+    def _strides(self, t, n):
+        """The first n strides of t as a C array (made once for equal strides)."""
+        key = t.stride()
+        got = self._stride_arrays.get(key)
+        if got is None:
+            if len(self._stride_arrays) > 256:
+                self._stride_arrays.clear()
+            if key[n] != 1:
+                raise ValueError(f"the channels must be contiguous, got strides {list(key)}")
+            got = self._stride_arrays[key] = (ctypes.c_int64 * n)(*key[:n])
+        return got
+
     def _call(self, fn, stream, *args):
-        index = self.device.index
-        # the raw handle: building a Stream object takes longer than the launch
-        stream = self._raw_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
-        if index == self._current_device():
+        stream = self._raw_stream(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        if self._index == self._current():
             status = fn(self._ref, *args, stream)
         else:
-            with self._cuda.device(index):
+            with self._cuda.device(self._index):
                 status = fn(self._ref, *args, stream)
         if status:
             raise CKVError(status, fn.__name__)
@@ -454,43 +463,38 @@ class PagedCache:
         """counts[s] rows of k, v [seqs, heads, n, 128] (any strides with
         contiguous channels) to every sequence (see ckv_paged_append); k and v
         may live in pinned host memory the device maps."""
-        shape = k.shape
+        shape, device, i32, tensor = k.shape, self.device, self._i32, self._tensor
         if len(shape) != 4 or shape[0] != self.seqs or shape[1] != self.heads or shape[3] != 128 or v.shape != shape:
             raise ValueError(f"k and v must be [{self.seqs}, {self.heads}, n, 128], got {tuple(shape)}, "
                              f"{tuple(v.shape)}")
-        ks, vs = k.stride(), v.stride()
-        if ks[3] != 1 or vs[3] != 1:
-            raise ValueError("the channels of k and v must be contiguous")
         if k.dtype != self.dtype or v.dtype != self.dtype:
             raise TypeError(f"k and v must be {self.dtype}, got {k.dtype}, {v.dtype}")
-        for t in (k, v):
-            if t.device != self.device and not (t.device.type == "cpu" and t.is_pinned()):
-                raise ValueError(f"k and v must be on {self.device} or pinned, got {t.device}")
-        per_seq, i32 = self._per_seq, self._i32
-        self._call(self._append, stream, k.data_ptr(), v.data_ptr(), _I64x3(ks[0], ks[1], ks[2]),
-                   _I64x3(vs[0], vs[1], vs[2]), shape[2],
-                   None if counts is None else self._tensor("counts", counts, per_seq, i32),
-                   None if start is None else self._tensor("start", start, per_seq, i32),
-                   None if first is None else self._tensor("first", first, per_seq, i32))
+        if k.device != device or v.device != device:
+            for t in (k, v):
+                if t.device != device and not (t.device.type == "cpu" and t.is_pinned()):
+                    raise ValueError(f"k and v must be on {device} or pinned, got {t.device}")
+        self._call(self._append, stream, k.data_ptr(), v.data_ptr(), self._strides(k, 3), self._strides(v, 3), shape[2],
+                   None if counts is None else tensor("counts", counts, self._per_seq, i32),
+                   None if start is None else tensor("start", start, self._per_seq, i32),
+                   None if first is None else tensor("first", first, self._per_seq, i32))
 
     def decode_attn(self, q, out, lse=None, mass_in=None, mass_out=None, scale=None, stream=None):
         """Attention of q [seqs, heads * g, 128] over the rows held into out
         [seqs, heads * g, 128] float32 (see ckv_paged_decode_attn).  With
         ``mass_out`` (for instance the cache's own mass, given as mass_in too)
         each row's weight is added to mass_in.  scale: 1 / sqrt(128) if None."""
-        qs = q.stride()
-        if q.shape != self._q_shape or qs[2] != 1:
-            raise ValueError(f"q must be {list(self._q_shape)} with contiguous channels, got {tuple(q.shape)}")
+        if q.shape != self._q_shape:
+            raise ValueError(f"q must be {list(self._q_shape)}, got {tuple(q.shape)}")
         if q.dtype != self.dtype:
             raise TypeError(f"q must be {self.dtype}, got {q.dtype}")
         if q.device != self.device:
             raise ValueError(f"q is on {q.device}, the cache on {self.device}")
-        f32 = self._f32
-        self._call(self._attn, stream, q.data_ptr(), self._code, _I64x2(qs[0], qs[1]), self.g,
-                   128 ** -0.5 if scale is None else scale, self._tensor("out", out, self._q_shape, f32),
-                   None if lse is None else self._tensor("lse", lse, self._lse_shape, f32),
-                   None if mass_in is None else self._tensor("mass_in", mass_in, self._per_row, f32),
-                   None if mass_out is None else self._tensor("mass_out", mass_out, self._per_row, f32),
+        f32, tensor = self._f32, self._tensor
+        self._call(self._attn, stream, q.data_ptr(), self._code, self._strides(q, 2), self.g,
+                   128 ** -0.5 if scale is None else scale, tensor("out", out, self._q_shape, f32),
+                   None if lse is None else tensor("lse", lse, self._lse_shape, f32),
+                   None if mass_in is None else tensor("mass_in", mass_in, self._per_row, f32),
+                   None if mass_out is None else tensor("mass_out", mass_out, self._per_row, f32),
                    *self._workspace)
 
     def _moves(self, moves, n_moves):
@@ -498,7 +502,7 @@ class PagedCache:
         if len(shape) != 4:
             raise ValueError(f"moves must be [seqs, heads, max_moves, 2], got {tuple(shape)}")
         return (shape[2], self._tensor("moves", moves, (self.seqs, self.heads, shape[2], 2), self._i32),
-                self._tensor("n_moves", n_moves, (self.seqs, self.heads), self._i32))
+                self._tensor("n_moves", n_moves, self._per_unit, self._i32))
 
     def evict_select(self, budget: int, sinks: int, recent: int, moves, n_moves, stream=None):
         """The rows to move when every KV head keeps ``budget`` of its rows (see
