@@ -181,11 +181,11 @@ __global__ void __launch_bounds__(128) paged_advance_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- eviction: selection
 constexpr int SEL_LONG = 4096;        // rows of a CTA from which it has 1024 threads, below 512
-constexpr int SEL_BINS = 2048;        // 11 bits of the key a pass: 11, 11 and 10
+constexpr int SEL_BINS = 4096;        // 12 bits of the key a pass: 12, 12 and 8
 constexpr int SEL_LIST = 1024;        // keys of one bin that are listed
 constexpr int SEL_CAND = 256;         // keys of one bin that are ranked directly
 constexpr int SEL_MAX_CLUSTER = 8;
-constexpr int SEL_MAX_SLICE = 45056;  // keys of one CTA that stay in shared memory (176 KB)
+constexpr int SEL_MAX_SLICE = 40960;  // keys of one CTA that stay in shared memory (160 KB)
 
 struct SelectArgs {
     Cache c;
@@ -230,44 +230,55 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 
 // A cluster of CS CTAs per (sequence, KV head), each with a slice of its rows.
 // One pass over mass and pos turns them into keys, kept in shared memory
-// (CACHED; longer caches read them again), and counts the keys' top 11 bits;
+// (CACHED; longer caches read them again), and counts the keys' top 12 bits;
 // the key of the budget-th row follows digit by digit from the histograms, to
 // which every CTA adds its occupied bins in all its peers' shared memory (few
-// of the 2048 are occupied; every CTA reading all bins of its peers took 97 us
-// for 32 units of 128k rows where this takes 24 us).  Where a digit
-// leaves at most SEL_LIST keys (a first digit's bin is a quarter of a power of
-// two) they are listed, and later digits look at the list alone; where it
-// leaves at most SEL_CAND, the key of the wanted rank is found by counting.  Then a row is kept if
-// its key is above that one, or equal and among the first that fit.  With
-// gt(r), eq(r) the rows before r above and equal, kept(r) = gt(r) + min(eq(r),
-// fitting) rows are kept before r, so the k-th hole is the row r < budget, not
-// kept, with r - kept(r) = k and the k-th mover the kept row r >= budget with
-// kept(r) - kept(budget) = k: one counting pass and one writing pass.
-template <int CS, int SEL_THREADS, bool CACHED>
-__global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __grid_constant__ SelectArgs a) {
-    constexpr int SEL_WARPS = SEL_THREADS / 32;
-    extern __shared__ uint32_t keys[];
-    __shared__ int hist[3][SEL_BINS];  // the unit's, one a pass
-    __shared__ int mine[CS > 1 ? SEL_BINS : 1];
-    __shared__ int warp_sum[SEL_WARPS];
-    __shared__ int4 counts[SEL_WARPS];  // rows above, equal; the same of rows below the budget
-    __shared__ int4 cta_counts;
+// are occupied; every CTA reading all bins of its peers took 97 us for 32
+// units of 128k rows where this takes 20 us).  Where a digit leaves at most
+// SEL_LIST keys (a first digit's bin is an eighth of a power of two) they are
+// listed, and later digits look at the list alone; where it leaves at most
+// SEL_CAND, the CTAs exchange them and the key T of the wanted rank is found by
+// counting, with no further digit and no further exchange.
+// A row is kept if its key is above T, or equal and among the first that fit.
+// With gt(r), eq(r) the rows before r above and equal, kept(r) = gt(r) +
+// min(eq(r), fitting) rows are kept before r, so the k-th hole is the row r <
+// budget, not kept, with r - kept(r) = k and the k-th mover the kept row r >=
+// budget with kept(r) - kept(budget) = k.  The pass that lists (or else the one
+// that counts) leaves a bit for every row that may be kept, and the writing pass
+// looks at those rows and at the ones below the budget only.
+template <int CS, int THREADS, bool CACHED>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) paged_select_kernel(const __grid_constant__ SelectArgs a) {
+    constexpr int WARPS = THREADS / 32;
+    constexpr int WORDS = THREADS == 1024 ? SEL_MAX_SLICE / 1024 : SEL_LONG / 512 + 4;  // bits of a warp's rows
+    extern __shared__ __align__(16) int sel_smem[];
+    // two histograms of the unit (the third pass takes the first again), one of this CTA's rows, the keys
+    int* mine = sel_smem + 2 * SEL_BINS;
+    uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + (CS > 1 ? 3 : 2) * SEL_BINS);
+    __shared__ int warp_sum[WARPS];
+    __shared__ int4 counts[WARPS];  // a warp's rows above, equal; those of them below the budget
+    __shared__ int4 totals;         // the CTA's (not ranked)
     __shared__ int found[3];
     __shared__ uint32_t list[SEL_LIST];  // of this CTA's rows, and where they are in the slice
     __shared__ int list_at[SEL_LIST];
-    __shared__ uint32_t cand[SEL_CAND], own_cand[SEL_CAND];  // of the unit, of this CTA's rows
-    __shared__ int n_list, n_cand;
-    const int u = blockIdx.x / CS, s = u / a.c.heads;
+    __shared__ __align__(16) uint32_t cand[SEL_CAND];  // of the unit
+    __shared__ uint32_t own_cand[SEL_CAND];            // of this CTA's rows
+    __shared__ int cand_low[SEL_CAND], own_low[SEL_CAND];    // whether the row is below the budget
+    __shared__ int own_n[4];                         // keys listed, exchanged; rows above them, of those below the budget
+    __shared__ int before_cta[4], unit_low[2];       // rows above and equal in the CTAs before; below the budget
+    __shared__ uint32_t maybe[WARPS][CACHED ? WORDS + 2 : 1];  // read up to two words past a warp's rows
+    const int u = blockIdx.x / CS, s = a.c.by_heads.quot(u);
     const int rank = CS > 1 ? (int)cluster_rank() : 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto sync_all = [] {
         if (CS > 1) cluster_sync();
         else __syncthreads();
     };
-    for (int i = tid; i < 3 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
-    if (CS > 1)
-        for (int i = tid; i < SEL_BINS; i += SEL_THREADS) mine[i] = 0;
-    if (tid == 0) n_list = n_cand = 0;
+    for (int i = tid; i < (CS > 1 ? 3 : 2) * SEL_BINS / 4; i += THREADS)
+        reinterpret_cast<int4*>(sel_smem)[i] = make_int4(0, 0, 0, 0);
+    if (tid < 4) own_n[tid] = before_cta[tid] = 0;
+    if (tid < 2) unit_low[tid] = 0;
+    if (CACHED)
+        for (int i = tid; i < WARPS * (WORDS + 2); i += THREADS) (&maybe[0][0])[i] = 0;
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
     if (tid == 0 && rank == 0) check_len(a.c, s);
@@ -281,13 +292,13 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
     const float* mass = a.c.mass + (size_t)u * a.c.rows + r0;
     const int32_t* pos = a.c.pos + (size_t)u * a.c.rows + r0;
     const int recent_from = a.c.seen[s] - a.recent;
-    int* local = CS > 1 ? mine : hist[0];
+    int* local = CS > 1 ? mine : sel_smem;
     auto key_at = [&](int i) { return CACHED ? keys[i] : evict_key(mass[i], pos[i], a.sinks, recent_from); };
     sync_all();  // every CTA's histograms are cleared
     // rows are a multiple of 16 per (sequence, KV head): reading up to three
     // past n stays inside
 #pragma unroll 2
-    for (int i = 4 * tid; i < n; i += 4 * SEL_THREADS) {
+    for (int i = 4 * tid; i < n; i += 4 * THREADS) {
         const float4 m = *reinterpret_cast<const float4*>(mass + i);
         const int4 p = *reinterpret_cast<const int4*>(pos + i);
         const uint32_t k[4] = {evict_key(m.x, p.x, a.sinks, recent_from), evict_key(m.y, p.y, a.sinks, recent_from),
@@ -295,68 +306,86 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
         if (CACHED) *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (i + e < n) atomicAdd(&local[k[e] >> 21], 1);
+            if (i + e < n) atomicAdd(&local[k[e] >> 20], 1);
     }
     // every warp's share of the slice, in row order
-    const int sub = ((n + SEL_WARPS - 1) / SEL_WARPS + 127) / 128 * 128;
+    const int sub = ((n + WARPS - 1) / WARPS + 127) / 128 * 128;
     const int w0 = min(n, warp * sub), w1 = min(n, w0 + sub);
-    // f(key, index) for the warp's rows; a lane has four keys in a row
-    auto each = [&](auto f) {
+    const int low_end = a.budget - r0;  // indices below it are rows below the budget
+    // f(key, index) for the warp's rows, four in a row to a lane; true for those
+    // that may be kept, and their bits are left where `mark`
+    auto each = [&](bool mark, auto f) {
 #pragma unroll 2
-        for (int i = w0 + 4 * lane; i < w1; i += 128) {
-            uint32_t k[4];
+        for (int b = w0; b < w1; b += 128) {
+            const int i = b + 4 * lane;
+            uint32_t k[4] = {0u, 0u, 0u, 0u};
             if (CACHED) {
-                const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
-                k[0] = v.x;
-                k[1] = v.y;
-                k[2] = v.z;
-                k[3] = v.w;
+                if (i < w1) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+                    k[0] = v.x;
+                    k[1] = v.y;
+                    k[2] = v.z;
+                    k[3] = v.w;
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) k[e] = i + e < w1 ? key_at(i + e) : 0u;
             }
+            unsigned bits = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (i + e < w1) f(k[e], i + e);
+                if (i + e < w1 && f(k[e], i + e)) bits |= 1u << e;
+            if (CACHED && mark) {
+                bits <<= 4 * (lane & 7);
+                bits |= __shfl_xor_sync(FULL, bits, 1);
+                bits |= __shfl_xor_sync(FULL, bits, 2);
+                bits |= __shfl_xor_sync(FULL, bits, 4);
+                if ((lane & 7) == 0) maybe[warp][(b - w0) / 32 + lane / 8] = bits;
+            }
         }
     };
     uint32_t prefix = 0, mask = 0;
     int need = a.budget;  // rows still to take among those whose key matches the prefix
     int gt = 0, eq = 0, gt_b = 0, eq_b = 0;  // rows above, equal; the same of rows below the budget
-    bool listed = false;
-    const int low_end = a.budget - r0;  // indices below it are rows below the budget
-#pragma unroll
+    bool listed = false, ranked = false;
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const uint32_t digit = pass == 2 ? 1023u : 2047u;
+        const int shift = pass == 0 ? 20 : (pass == 1 ? 8 : 0);
+        const uint32_t digit = pass == 2 ? 255u : 4095u;
+        int* unit = sel_smem + (pass & 1) * SEL_BINS;
         if (pass > 0) {
-            if (CS == 1) local = hist[pass];
-            auto add = [&](uint32_t k, int) {
-                if ((k & mask) == prefix) atomicAdd(&local[(k >> shift) & digit], 1);
-            };
-            if (listed)
-                for (int x = tid; x < n_list; x += SEL_THREADS) add(list[x], 0);
-            else
-                each(add);
+            if (CS == 1) local = unit;
+            if (listed) {
+                for (int x = tid; x < own_n[0]; x += THREADS)
+                    if ((list[x] & mask) == prefix) atomicAdd(&local[(list[x] >> shift) & digit], 1);
+            } else {
+                each(false, [&](uint32_t k, int) {
+                    if ((k & mask) == prefix) atomicAdd(&local[(k >> shift) & digit], 1);
+                    return false;
+                });
+            }
         }
         if (CS > 1) {
             __syncthreads();
-            for (int i = tid; i < SEL_BINS; i += SEL_THREADS) {
+            for (int i = tid; i < SEL_BINS; i += THREADS) {
                 const int v = mine[i];
                 if (v == 0) continue;
                 mine[i] = 0;
 #pragma unroll
-                for (int r = 0; r < CS; ++r) peer_add(&hist[pass][i], r, v);
+                for (int r = 0; r < CS; ++r) peer_add(&unit[i], r, v);
             }
         }
         sync_all();
-        // four bins a thread, from the highest down
-        constexpr int BPT = SEL_BINS / SEL_THREADS;
+        // BPT bins a thread, from the highest down
+        constexpr int BPT = SEL_BINS / THREADS;
         int c[BPT], sum = 0;
 #pragma unroll
         for (int e = 0; e < BPT; ++e) {
-            c[e] = hist[pass][SEL_BINS - 1 - (tid * BPT + e)];
+            c[e] = unit[SEL_BINS - 1 - (tid * BPT + e)];
             sum += c[e];
+            // nobody else looks at this copy; the third pass fills it again, and
+            // peers only after the second pass's sync
+            unit[SEL_BINS - 1 - (tid * BPT + e)] = 0;
         }
         int x = sum;
 #pragma unroll
@@ -367,9 +396,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
         if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
         int before = x - sum;
-#pragma unroll
-        for (int w = 0; w < SEL_WARPS; ++w)
-            if (w < warp) before += warp_sum[w];
+        const int mine_w = lane < WARPS ? warp_sum[lane] : 0;
+        before += __reduce_add_sync(FULL, lane < warp ? mine_w : 0);
         if (before < need && need <= before + sum) {
 #pragma unroll
             for (int e = 0; e < BPT; ++e) {
@@ -389,42 +417,70 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
         if (!listed && all <= SEL_LIST) {
             // the keys of this bin, in any order; those above it count whatever
             // the last digits are
-            each([&](uint32_t k, int i) {
+            each(true, [&](uint32_t k, int i) {
+                if ((k & mask) < prefix) return false;
                 if ((k & mask) > prefix) {
                     ++gt;
                     gt_b += i < low_end;
-                } else if ((k & mask) == prefix) {
-                    const int at = atomicAdd(&n_list, 1);
+                } else {
+                    const int at = atomicAdd(&own_n[0], 1);
                     list[at] = k;
                     list_at[at] = i;
                 }
+                return true;
             });
             listed = true;
             __syncthreads();
         }
         if (!listed || all > SEL_CAND) continue;
-        uint32_t* own = CS > 1 ? own_cand : cand;
-        for (int x = tid; x < n_list; x += SEL_THREADS)
-            if ((list[x] & mask) == prefix) own[atomicAdd(&n_cand, 1)] = list[x];
+        if (CS > 1) {
+            // what the peers must know: the rows above the bin, and its keys
+            const int g = __reduce_add_sync(FULL, gt), gb = __reduce_add_sync(FULL, gt_b);
+            if (lane == 0 && g) atomicAdd(&own_n[2], g);
+            if (lane == 0 && gb) atomicAdd(&own_n[3], gb);
+        }
+        for (int x = tid; x < own_n[0]; x += THREADS) {
+            const uint32_t k = list[x];
+            const bool low = list_at[x] < low_end;
+            if ((k & mask) == prefix) {
+                const int at = atomicAdd(&own_n[1], 1);
+                (CS > 1 ? own_cand : cand)[at] = k;
+                own_low[at] = low;
+            } else if (CS > 1 && (k & mask) > prefix) {
+                atomicAdd(&own_n[2], 1);
+                if (low) atomicAdd(&own_n[3], 1);
+            }
+        }
         sync_all();
+        int from = 0, to = 0;
         if (CS > 1) {
             // warp r copies what CTA r has, behind what the CTAs before it have
-            const int m = lane < CS ? peer_word(&n_cand, lane) : 0;
-            const int from = __shfl_sync(FULL, m, warp & 31);
-            const int to = __reduce_add_sync(FULL, lane < warp ? m : 0);
+            const int m = lane < CS ? peer_word(&own_n[1], lane) : 0;
+            from = __shfl_sync(FULL, m, warp & 31);
+            to = __reduce_add_sync(FULL, lane < warp ? m : 0);
             if (warp < CS)
-                for (int i = lane; i < from; i += 32)
+                for (int i = lane; i < from; i += 32) {
                     cand[to + i] = (uint32_t)peer_word(reinterpret_cast<const int*>(own_cand + i), warp);
+                    cand_low[to + i] = peer_word(own_low + i, warp);
+                }
+            if (warp < CS && lane == 0) {
+                if (warp < rank) atomicAdd(&before_cta[0], peer_word(&own_n[2], warp));
+                atomicAdd(&unit_low[0], peer_word(&own_n[3], warp));
+            }
             __syncthreads();
         }
         if (tid < all) {
             const uint32_t k = cand[tid];
-            int above = 0, same = 0;
-#pragma unroll 8
-            for (int x = 0; x < all; ++x) {
-                const uint32_t y = cand[x];
-                above += y > k;
-                same += y == k;
+            int above = 0, same = 0, x = 0;
+#pragma unroll 4
+            for (; x + 4 <= all; x += 4) {
+                const uint4 y = *reinterpret_cast<const uint4*>(cand + x);
+                above += (y.x > k) + (y.y > k) + (y.z > k) + (y.w > k);
+                same += (y.x == k) + (y.y == k) + (y.z == k) + (y.w == k);
+            }
+            for (; x < all; ++x) {
+                above += cand[x] > k;
+                same += cand[x] == k;
             }
             if (above < need && need <= above + same) {  // all rows of that key write the same
                 found[0] = (int)k;
@@ -434,6 +490,15 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
         __syncthreads();
         prefix = (uint32_t)found[0];
         need = found[1];
+        if (CS > 1 && warp < CS)
+            for (int i = lane; i < from; i += 32) {
+                const uint32_t k = cand[to + i];
+                if (k < prefix) continue;
+                const int which = k == prefix;
+                if (warp < rank) atomicAdd(&before_cta[which], 1);
+                if (cand_low[to + i]) atomicAdd(&unit_low[which], 1);
+            }
+        ranked = true;
         break;
     }
     auto count = [&](uint32_t k, int i) {
@@ -441,11 +506,12 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
         eq += k == prefix;
         gt_b += k > prefix && i < low_end;
         eq_b += k == prefix && i < low_end;
+        return k >= prefix;
     };
     if (!listed)
-        each(count);
+        each(true, count);
     else
-        for (int x = lane; x < n_list; x += 32)
+        for (int x = lane; x < own_n[0]; x += 32)
             if (list_at[x] >= w0 && list_at[x] < w1) count(list[x], list_at[x]);
     gt = __reduce_add_sync(FULL, gt);
     eq = __reduce_add_sync(FULL, eq);
@@ -455,67 +521,81 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) paged_select_kernel(const __gr
     __syncthreads();
     // rows above and equal before this warp's, in this CTA and in those before
     // it; rows below the budget of the whole unit
-    int4 c = lane < SEL_WARPS ? counts[lane] : make_int4(0, 0, 0, 0);
+    int4 c = lane < WARPS ? counts[lane] : make_int4(0, 0, 0, 0);
     int g = __reduce_add_sync(FULL, lane < warp ? c.x : 0), e = __reduce_add_sync(FULL, lane < warp ? c.y : 0);
     int gb = __reduce_add_sync(FULL, c.z), eb = __reduce_add_sync(FULL, c.w);
-    if (CS > 1) {
+    if (CS > 1 && ranked) {
+        g += before_cta[0];
+        e += before_cta[1];
+        gb = unit_low[0];
+        eb = unit_low[1];
+    } else if (CS > 1) {
         const int all_g = __reduce_add_sync(FULL, c.x), all_e = __reduce_add_sync(FULL, c.y);
-        if (tid == 0) cta_counts = make_int4(all_g, all_e, gb, eb);
+        if (tid == 0) totals = make_int4(all_g, all_e, gb, eb);
         cluster_sync();
         c = make_int4(0, 0, 0, 0);
         if (lane < CS) {
-            const int* p = reinterpret_cast<const int*>(&cta_counts);
+            const int* p = reinterpret_cast<const int*>(&totals);
             c = make_int4(peer_word(p, lane), peer_word(p + 1, lane), peer_word(p + 2, lane), peer_word(p + 3, lane));
         }
         g += __reduce_add_sync(FULL, lane < rank ? c.x : 0);
         e += __reduce_add_sync(FULL, lane < rank ? c.y : 0);
         gb = __reduce_add_sync(FULL, c.z);
         eb = __reduce_add_sync(FULL, c.w);
-        // the peers' shared memory has been read for the last time
-        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     }
+    // this thread has read its peers' shared memory for the last time
+    if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     const int kept_b = gb + min(eb, need);  // rows kept before the budget
     int32_t* out = a.moves + (size_t)u * a.max_moves * 2;
-    const unsigned below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        uint32_t k4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = i0 + 32 * q + lane;
-            k4[q] = i < w1 ? key_at(i) : 0u;
+    // a lane looks after rpl rows in a row
+    const int rpl = CACHED ? min(32, sub / 32) : 4;
+    for (int b = w0; b < w1; b += 32 * rpl) {
+        const int base = b + rpl * lane;
+        const unsigned own_rows = base + rpl <= w1 ? FULL >> (32 - rpl) : (base < w1 ? (1u << (w1 - base)) - 1u : 0u);
+        unsigned look = own_rows, mg = 0, me = 0;  // rows that may be kept; above, equal
+        if (CACHED) {
+            const int bit = min(base, w1) - w0;
+            look &= __funnelshift_r(maybe[warp][bit >> 5], maybe[warp][(bit >> 5) + 1], bit & 31);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = i0 + 32 * q + lane, r = r0 + i;
-            const uint32_t k = k4[q];
-            // past the budget and nothing kept
-            if (!__any_sync(FULL, i < w1 && k >= prefix) && i0 + 32 * q >= low_end) continue;
-            const bool is_gt = i < w1 && k > prefix, is_eq = i < w1 && k == prefix;
-            const unsigned mg = __ballot_sync(FULL, is_gt), me = __ballot_sync(FULL, is_eq);
-            const int eq_before = e + __popc(me & below);
-            const int kept_before = g + __popc(mg & below) + min(eq_before, need);
-            const bool kept = is_gt || (is_eq && eq_before < need);
-            if (i < w1) {
-                const int m = kept_before - kept_b, h = r - kept_before;
-                if (kept && r >= a.budget && m < a.max_moves) out[2 * m] = r;
-                if (!kept && r < a.budget && h < a.max_moves) out[2 * h + 1] = r;
-            }
-            g += __popc(mg);
-            e += __popc(me);
+        for (unsigned left = look; left; left &= left - 1) {
+            const unsigned bit = left & -left;
+            const uint32_t k = key_at(base + __ffs(left) - 1);
+            if (k > prefix) mg |= bit;
+            else if (k == prefix) me |= bit;
         }
+        const int own = __popc(mg) | __popc(me) << 16;
+        int x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL, x, o);
+            if (lane >= o) x += y;
+        }
+        const int all = __shfl_sync(FULL, x, 31), gl = g + ((x - own) & 0xffff), el = e + ((x - own) >> 16);
+        for (unsigned todo = base < low_end ? own_rows : mg | me; todo; todo &= todo - 1) {
+            const unsigned bit = todo & -todo;
+            const int r = r0 + base + __ffs(todo) - 1, eq_before = el + __popc(me & (bit - 1));
+            const int kept_before = gl + __popc(mg & (bit - 1)) + min(eq_before, need);
+            const bool kept = (mg & bit) || ((me & bit) && eq_before < need);
+            const int m = kept_before - kept_b, h = r - kept_before;
+            if (kept && r >= a.budget && m < a.max_moves) out[2 * m] = r;
+            if (!kept && r < a.budget && h < a.max_moves) out[2 * h + 1] = r;
+        }
+        g += all & 0xffff;
+        e += all >> 16;
     }
     if (tid == 0 && rank == 0) a.n_moves[u] = a.budget - kept_b;
-    if (CS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while a peer may read its counts
+    if (CS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while a peer may read from it
 }
 
 template <int CS, int THREADS, bool CACHED>
 cudaError_t launch_select_cs(const SelectArgs& a, int dev, cudaStream_t s) {
     const int slice = round_up(ceil_div(a.c.rows, CS), 128);
-    const size_t smem = CACHED ? (size_t)slice * 4 : 0;
+    const size_t bins = (size_t)(CS > 1 ? 3 : 2) * SEL_BINS * sizeof(int), smem = bins + (CACHED ? (size_t)slice * 4 : 0);
     static std::atomic<bool> set[MAX_DEVICES];
-    if (CACHED && !set[dev].load(std::memory_order_relaxed)) {
+    if (!set[dev].load(std::memory_order_relaxed)) {
+        const size_t rows = !CACHED ? 0 : (THREADS == 1024 ? SEL_MAX_SLICE : SEL_LONG + 128);
         const cudaError_t e = cudaFuncSetAttribute(paged_select_kernel<CS, THREADS, CACHED>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_MAX_SLICE * 4);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, bins + rows * 4);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
