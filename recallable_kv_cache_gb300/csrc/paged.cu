@@ -670,26 +670,31 @@ __global__ void __launch_bounds__(APPLY_THREADS) paged_apply_kernel(const __grid
     const int u = a.by_warps.quot(blockIdx.x * (APPLY_THREADS / 32) + (threadIdx.x >> 5), &first);
     if (u >= a.units) return;
     const int s = a.c.by_heads.quot(u, &h);
-    int n = a.n_moves[u];
+    // the first moves are read together with their number, used or not
+    const int32_t* mv = a.moves + (size_t)u * a.max_moves * 2;
+    const bool is_dst = lane >= 16;
+    auto move_at = [&](int k0) {
+        const int k = k0 + (lane & 15);
+        return k < a.max_moves ? mv[2 * k + is_dst] : -1;
+    };
+    int next = move_at(first * BATCH), n = a.n_moves[u];
     if (n < 0 || n > a.max_moves) {
         if (first == 0 && lane == 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
         n = n < 0 ? 0 : a.max_moves;
     }
-    const int32_t* mv = a.moves + (size_t)u * a.max_moves * 2;
     const size_t o = (size_t)u * a.c.rows;
     constexpr int RP = 32 / VPR;  // rows at a time
     const int piece = (lane % VPR) * 16, sub = lane / VPR;
     for (int k0 = first * BATCH; k0 < n; k0 += (int)a.by_warps.d * BATCH) {
-        const int k = k0 + (lane & 15);
-        const bool is_dst = lane >= 16;
         int row = -1;
-        if (k < n) {
-            row = mv[2 * k + is_dst];
+        if (k0 + (lane & 15) < n) {
+            row = next;
             if (is_dst ? row < 0 || row >= a.budget || row >= a.c.rows : row < a.budget || row >= a.c.rows) {
                 report(a.c.dev_err, CKV_DEV_BAD_INDEX);
                 row = -1;
             }
         }
+        next = move_at(k0 + (int)a.by_warps.d * BATCH);
         int slot = 0;
         const int pg = row < 0 ? -1 : page_of(a.c, s, row, &slot);
         const long long ko = pg * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2];
