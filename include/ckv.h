@@ -438,7 +438,8 @@ ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, in
 /* Eviction by accumulated attention weight, in two calls.  _select chooses: of
  * every (s, h) with lens[s] > budget it keeps `budget` rows, first those with
  * pos < sinks or pos >= seen[s] - recent, then by mass descending (NaN lowest,
- * -0 = +0), ties to the lower row.  The cache need not stay in order, so only
+ * -0 = +0), ties to the lower row (among the protected rows too, should they
+ * be more than the budget).  The cache need not stay in order, so only
  * the kept rows at or past the budget have to move, into the slots below it
  * that were not kept: moves[s][h][k] = (source row, destination row), k <
  * n_moves[s][h], the k-th mover and the k-th hole in ascending order.  Entries

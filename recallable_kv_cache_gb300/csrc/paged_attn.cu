@@ -585,7 +585,7 @@ __device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, co
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
     const float ms = M == -INFINITY ? 0.f : M;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < job.n; ++i) {
         const float* p = src[i];
         const float f = ex2(p[sm] - ms);

@@ -492,6 +492,9 @@ SELECT = [
     ([9001, 8000], 1, 48, 3001, 16, 500),
     ([400001], 1, 16, 1000, 16, 500),
     ([40000, 20000, 33, 39999], 2, 64, 5000, 16, 100),
+    # the largest slices whose keys stay in shared memory: of a cluster of eight, of a CTA alone
+    ([327001], 1, 16, 1000, 16, 500),
+    ([40950] + [50] * 79, 1, 16, 3000, 16, 100),
     ([6000, 5999] * 20, 2, 16, 700, 16, 100),
 ]
 
