@@ -56,7 +56,8 @@ ckv_status check_cache(const ckv_paged_cache* c, Cache* o) {
     const int32_t extent[3] = {c->n_pages, c->heads, c->page_size};
     if (!strides_ok(c->k_stride, extent, 3, elem, o->ks) || !strides_ok(c->v_stride, extent, 3, elem, o->vs))
         return CKV_ERR_ARG;
-    if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->mass) || !aligned16(c->pos) || !strides_aligned(o->ks, 3) || !strides_aligned(o->vs, 3))
+    if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->mass) || !aligned16(c->pos) ||
+        !strides_aligned(o->ks, 3) || !strides_aligned(o->vs, 3))
         return CKV_ERR_ALIGN;
     if (c->pos && !c->seen) return CKV_ERR_ARG;
     o->K = static_cast<unsigned char*>(c->K);

@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     __shared__ int2 start[NW];
     __shared__ __align__(8) uint64_t full[NW][NST];
     __shared__ int4 meta[NW][NST];  // unit, held rows, tile in the unit, tiles of the unit
-    __shared__ Seg segs[2 * NW];    // partials left: [2 w] on the way, behind the rings, [2 w + 1] last, in the warp's ring
+    __shared__ Seg segs[2 * NW];    // partials of warp w: [2 w] left on the way (heads), [2 w + 1] at the end (its ring)
     __shared__ __align__(16) float2 scratch[NW][E::SCRATCH ? E::SCRATCH : 1];
     // merging: jobs and their sources; the units shared with other CTAs (unit,
     // first CTA, CTAs; unit -1: none, or not this CTA's to merge)
@@ -640,10 +640,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) ptx::mbar_init(&full[warp][i], 1);
         ptx::fence_barrier_init();
+        segs[2 * warp].u = segs[2 * warp + 1].u = -1;
     }
-    if (threadIdx.x < 2) ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
-    if (lane == 0) segs[2 * warp].u = segs[2 * warp + 1].u = -1;
-    if (threadIdx.x < 2) shared_units[threadIdx.x].x = -1;
+    if (threadIdx.x < 2) {
+        ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
+        shared_units[threadIdx.x].x = -1;
+    }
     ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
     int cta = blockIdx.x;
@@ -691,9 +693,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             }
             if (lane == t - block) {
                 meta[warp][st] = make_int4(p.s * a.c.heads + p.h, p_rows, p.k, p.nt);
-                if (dead) {
-                    // nothing more is loaded
-                } else if (p_rows > 0) {
+                if (dead) return;
+                if (p_rows > 0) {
                     ptx::mbar_arrive_expect_tx(&full[warp][st], STAGE);
                     E::load(ring + st * STAGE, &tk, &tv, p_page, p.h, p_slot, &full[warp][st]);
                 } else {
@@ -743,13 +744,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                     const int s = a.c.by_heads.quot(m.x, &h);
                     enter(s, h, m.w, t - m.z);
                 }
-                if (dead) {
-                } else if (m.y > 0)
-                    e.tile(ring + st * STAGE, scratch[warp], m.y, a.qscale, a.g,
-                           a.scores ? a.scores + (size_t)u * a.g * a.c.rows + (size_t)m.z * TR : nullptr, a.c.rows, lane);
-                else if (a.scores)
-                    for (int i = lane; i < TR * a.g; i += 32)
-                        a.scores[((size_t)u * a.g + i / TR) * a.c.rows + (size_t)m.z * TR + i % TR] = -INFINITY;
+                float* sc = a.scores ? a.scores + (size_t)u * a.g * a.c.rows + (size_t)m.z * TR : nullptr;
+                if (m.y > 0 && !dead)
+                    e.tile(ring + st * STAGE, scratch[warp], m.y, a.qscale, a.g, sc, a.c.rows, lane);
+                else if (sc)
+                    for (int i = lane; i < TR * a.g; i += 32) sc[(size_t)(i / TR) * a.c.rows + i % TR] = -INFINITY;
                 __syncwarp();
             }
             if (t + NST < t_end) issue(st, t + NST);
@@ -761,9 +760,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         }
         leave(true);
     }
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0)
         for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
-    }
     // units without rows: nothing else writes their outputs
     for (int s = blockIdx.x; s < a.c.seqs; s += gridDim.x)
         if (rows_held(a.c, s) == 0)
@@ -795,9 +793,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 }
                 const unsigned held = __ballot_sync(FULL, sg.u >= 0), lead = __ballot_sync(FULL, leads);
                 const unsigned below = (1u << lane) - 1u;
-                if (sg.u >= 0)
-                    src[__popc(held & below)] = lane & 1 ? reinterpret_cast<const float*>(smem + (size_t)(lane >> 1) * NST * STAGE)
-                                                         : heads + (lane >> 1) * pf;
+                const float* mine_at = lane & 1 ? reinterpret_cast<const float*>(smem + (size_t)(lane >> 1) * NST * STAGE)
+                                                : heads + (lane >> 1) * pf;
+                if (sg.u >= 0) src[__popc(held & below)] = mine_at;
                 if (leads) {
                     const unsigned after = lead & ~below & ~(1u << lane);  // the next leader ends this job
                     const unsigned mine = held & ~below & (after ? (after & -after) - 1u : FULL);
@@ -846,7 +844,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             if (threadIdx.x < 2 && shared_units[threadIdx.x].x >= 0) {
                 const int4 su = shared_units[threadIdx.x];
                 unsigned before;
-                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.arrived + su.y) : "memory");
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                             : "=r"(before)
+                             : "l"(a.arrived + su.y)
+                             : "memory");
                 if (before == (unsigned)(su.z - 1)) a.arrived[su.y] = 0;  // the last one: for the next call
                 else shared_units[threadIdx.x].x = -1;
             }
@@ -1056,7 +1057,9 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     }
     // tile numbers are 32-bit: 2^31 tiles of fp32 rows are 17 TB of K and V
     if ((long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, 8) > 0x7fff0000LL) return CKV_ERR_ARG;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(mass_in) || !aligned16(mass_out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return CKV_ERR_ALIGN;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(mass_in) || !aligned16(mass_out) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return CKV_ERR_ALIGN;
     const Layout l = layout_of(a.c, g, mass_out != nullptr);
     if (workspace_bytes < (int64_t)l.total) return CKV_ERR_CAPACITY;
     unsigned char* w = static_cast<unsigned char*>(workspace);
