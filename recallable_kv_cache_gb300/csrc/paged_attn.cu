@@ -222,6 +222,7 @@ template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
     static constexpr int TR = 16, SCRATCH = 0;
+    static constexpr bool SWIZZLED = true;
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -431,10 +432,10 @@ template <int GP>
 struct TilesF32 {
     using T = float;
     static constexpr int TR = 8, SCRATCH = TR * GP;
-    static constexpr int LPR = GP > 8 ? 32 : GP > 2 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
+    static constexpr bool SWIZZLED = false;
+    static constexpr int LPR = GP > 2 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
-    static constexpr int BR = TR / RP * GP <= 32 ? TR / RP : 32 / GP;  // of those, summed together
     static constexpr int NV = (TR * GP + 31) / 32;
     uint64_t qv[GP][QV][2];
     uint64_t o[GP][2];
@@ -464,35 +465,29 @@ struct TilesF32 {
                                          size_t rows, int lane) {
         const ulonglong2* K = reinterpret_cast<const ulonglong2*>(stage);
         const ulonglong2* V = reinterpret_cast<const ulonglong2*>(stage + STAGE / 2);
+        float s[TR / RP * GP];
 #pragma unroll
-        for (int b = 0; b < TR / RP; b += BR) {
-            float s[BR * GP];
+        for (int rr = 0; rr < TR / RP; ++rr) {
+            const int row = rr * RP + lane / LPR;
+            uint64_t acc[GP];
 #pragma unroll
-            for (int rr = 0; rr < BR; ++rr) {
-                const int row = (b + rr) * RP + lane / LPR;
-                uint64_t acc[GP];
+            for (int j = 0; j < GP; ++j) acc[j] = 0;
 #pragma unroll
-                for (int j = 0; j < GP; ++j) acc[j] = 0;
+            for (int i = 0; i < QV; ++i) {
+                const ulonglong2 k = K[row * 32 + (lane % LPR) + LPR * i];
 #pragma unroll
-                for (int i = 0; i < QV; ++i) {
-                    const ulonglong2 k = K[row * 32 + (lane % LPR) + LPR * i];
-#pragma unroll
-                    for (int j = 0; j < GP; ++j) acc[j] = fma2(qv[j][i][1], k.y, fma2(qv[j][i][0], k.x, acc[j]));
-                }
-#pragma unroll
-                for (int j = 0; j < GP; ++j) {
-                    const float2 f = unpair(acc[j]);
-                    s[rr * GP + j] = f.x + f.y;
-                }
+                for (int j = 0; j < GP; ++j) acc[j] = fma2(qv[j][i][1], k.y, fma2(qv[j][i][0], k.x, acc[j]));
             }
-            const int x0 = reduce_scatter<BR * GP, LPR>(s, lane % LPR);
-            constexpr int KEPT = BR * GP > LPR ? BR * GP / LPR : 1;
 #pragma unroll
-            for (int i = 0; i < KEPT; ++i) {
-                const int x = x0 + i;
-                ps[((b + x / GP) * RP + lane / LPR) * GP + x % GP].x = s[i];
+            for (int j = 0; j < GP; ++j) {
+                const float2 f = unpair(acc[j]);
+                s[rr * GP + j] = f.x + f.y;
             }
         }
+        const int x0 = reduce_scatter<TR / RP * GP, LPR>(s, lane % LPR);
+        constexpr int KEPT = TR / RP * GP > LPR ? TR / RP * GP / LPR : 1;
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i) ps[((x0 + i) / GP * RP + lane / LPR) * GP + (x0 + i) % GP].x = s[i];
         __syncwarp();
         const int j = lane % GP;
         float v[NV], tm = -INFINITY;
@@ -560,6 +555,191 @@ struct TilesF32 {
                 put(j, 4 * lane + 1, x.y * wj);
                 put(j, 4 * lane + 2, y.x * wj);
                 put(j, 4 * lane + 3, y.y * wj);
+            }
+        }
+    }
+};
+
+// fp32 on the tensor cores, for more than eight heads (96 units of up to 12k
+// rows: 16 heads 155 us where the tiles above took 207; 8 heads 115 where those
+// take 100, so up to eight they are used).  Every operand is taken apart into
+// three bf16 terms (hi + mid + lo, which hold its 24 bits), and of the nine
+// products the six down to 2^-18 of the largest are added up, the small ones
+// first.  8 rows a tile, four quarters of 32 channels, [quarter][row][128
+// bytes], 128-byte swizzled (16-byte chunk c of row r at c ^ r).
+//   S[h][r] = q[h] . K[r]        m16n8k16: M = 16 heads, N = 8 rows
+//   O[c][h] += V[r][c] P[h][r]   m16n8k8:  M = 16 channels, N = 8 heads, K = 8 rows
+// Which channel is which k of the first product, and which m of the second, is
+// free; it is chosen so that a lane reads 16 bytes of a row at a time and the
+// eight lanes that read together read different chunks: in step ks lane (n, t)
+// reads chunk 2 t + ks % 2 of quarter ks / 2 of row n, and of V chunk n of
+// quarter f of rows 2 t and 2 t + 1.
+template <int NB>
+struct TilesF32Tc {
+    using T = float;
+    static constexpr int TR = 8, SCRATCH = 0;
+    static constexpr bool SWIZZLED = true;
+    uint32_t qa[3][8][2 * NB];
+    float o[NB][8][4];
+    float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
+
+    struct Terms {
+        uint32_t t[3];  // hi, mid, lo of two values
+    };
+    static __device__ __forceinline__ Terms split(float x, float y) {
+        Terms r;
+        r.t[0] = pack2(x, y);
+        x -= lo_of(r.t[0]);
+        y -= hi_of(r.t[0]);
+        r.t[1] = pack2(x, y);
+        r.t[2] = pack2(x - lo_of(r.t[1]), y - hi_of(r.t[1]));
+        return r;
+    }
+    static __device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(b0));
+    }
+    static __device__ __forceinline__ void load(unsigned char* dst, const CUtensorMap* tk, const CUtensorMap* tv,
+                                                int page, int h, int slot, uint64_t* bar) {
+        tma_load_5d(dst, tk, 0, slot, 0, h, page, bar);
+        tma_load_5d(dst + STAGE / 2, tv, 0, slot, 0, h, page, bar);
+    }
+    __device__ __forceinline__ void reset(const T* q, long long stride, int g, int lane) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int j = (lane >> 2) + 8 * b;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const float4 x = j < g ? *reinterpret_cast<const float4*>(q + j * stride + 32 * (ks >> 1) +
+                                                                          4 * (2 * (lane & 3) + (ks & 1)))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                const Terms u = split(x.x, x.y), v = split(x.z, x.w);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    qa[i][ks][b] = u.t[i];
+                    qa[i][ks][NB + b] = v.t[i];
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[b][mt][e] = 0.f;
+            mrun[b] = -INFINITY;
+            lrun[b] = 0.f;
+        }
+    }
+    // the terms in the six products, the smallest first; the largest is the last
+    static __host__ __device__ constexpr int left(int i) { return i == 1 ? 2 : (i == 2 || i == 3 ? 1 : 0); }
+    static __host__ __device__ constexpr int right(int i) { return i == 0 ? 2 : (i == 2 || i == 4 ? 1 : 0); }
+
+    __device__ __forceinline__ void tile(unsigned char* stage, float2*, int n, float qscale, int g, float* scores,
+                                         size_t rows, int lane) {
+        const int row = lane >> 2, t = lane & 3;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const float4 k = *reinterpret_cast<const float4*>(stage + (ks >> 1) * 1024 + row * 128 +
+                                                              (((2 * t + (ks & 1)) ^ row) << 4));
+            const Terms u = split(k.x, k.y), v = split(k.z, k.w);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                const uint32_t(&a)[2 * NB] = qa[left(i)][ks];
+                mma(i < 5 ? small : s, a[0], NB == 2 ? a[NB - 1] : 0u, a[NB], NB == 2 ? a[2 * NB - 1] : 0u,
+                    u.t[right(i)], v.t[right(i)]);
+            }
+        }
+        Terms p3[NB];
+        float sc[NB];
+        bool grew = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float v[2], p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                v[e] = 2 * t + e < n ? (s[2 * b + e] + small[2 * b + e]) * qscale : -INFINITY;
+            const int j = row + 8 * b;
+            if (scores && j < g) *reinterpret_cast<float2*>(scores + (size_t)j * rows + 2 * t) = make_float2(v[0], v[1]);
+            float tm = fmaxf(v[0], v[1]);
+            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 1));
+            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 2));
+            const float mnew = fmaxf(mrun[b], tm);
+            const float ms = mnew == -INFINITY ? 0.f : mnew;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[e] = ex2(v[e] - ms);
+            sc[b] = 1.f;
+            if (mnew != mrun[b]) {
+                sc[b] = ex2(mrun[b] - ms);
+                grew = true;
+            }
+            lrun[b] = lrun[b] * sc[b] + (p[0] + p[1]);
+            mrun[b] = mnew;
+            p3[b] = split(p[0], p[1]);
+        }
+        if (__any_sync(FULL, grew)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float sc0 = __shfl_sync(FULL, sc[b], t * 8), sc1 = __shfl_sync(FULL, sc[b], t * 8 + 4);
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    o[b][mt][0] *= sc0;
+                    o[b][mt][1] *= sc1;
+                    o[b][mt][2] *= sc0;
+                    o[b][mt][3] *= sc1;
+                }
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            float x[2][4];  // rows not held count as zero
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * t + e;
+                const float4 v = *reinterpret_cast<const float4*>(stage + STAGE / 2 + f * 1024 + r * 128 + ((row ^ r) << 4));
+                const bool held = r < n;
+                x[e][0] = held ? v.x : 0.f;
+                x[e][1] = held ? v.y : 0.f;
+                x[e][2] = held ? v.z : 0.f;
+                x[e][3] = held ? v.w : 0.f;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const Terms u = split(x[0][2 * half], x[1][2 * half]), v = split(x[0][2 * half + 1], x[1][2 * half + 1]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) mma8(d, u.t[left(i)], v.t[left(i)], p3[b].t[right(i)]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[b][2 * f + half][e] += d[e];
+                }
+            }
+        }
+    }
+    template <typename Put, typename Stat>
+    __device__ __forceinline__ void leave(int g, int lane, bool normalise, Put put, Stat stat) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float l = lrun[b];
+            l += __shfl_xor_sync(FULL, l, 1);
+            l += __shfl_xor_sync(FULL, l, 2);
+            const int j = (lane >> 2) + 8 * b;
+            if ((lane & 3) == 0 && j < g) stat(j, mrun[b], l);
+            const float w = !normalise ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            const float w0 = __shfl_sync(FULL, w, (lane & 3) * 8), w1 = __shfl_sync(FULL, w, (lane & 3) * 8 + 4);
+            const int j0 = (lane & 3) * 2 + 8 * b;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+                const int c = 32 * (mt >> 1) + 4 * (lane >> 2) + 2 * (mt & 1);
+                if (j0 < g) {
+                    put(j0, c, o[b][mt][0] * w0);
+                    put(j0, c + 1, o[b][mt][2] * w0);
+                }
+                if (j0 + 1 < g) {
+                    put(j0 + 1, c, o[b][mt][1] * w1);
+                    put(j0 + 1, c + 1, o[b][mt][3] * w1);
+                }
             }
         }
     }
@@ -960,30 +1140,30 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
 }
 
-// The pool as a tensor map whose boxes are tiles of one page and KV head: bf16
-// [page][head][half][slot][64 channels] (two halves of 128 bytes, swizzled),
-// fp32 [page][head][slot][128 channels].
-bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long long* st, bool bf16, int tile_rows) {
+// The pool as a tensor map whose boxes are tiles of one page and KV head: rows
+// cut into pieces of 128 bytes and swizzled, [page][head][piece][slot][128
+// bytes], or fp32 rows whole, [page][head][slot][128 channels].
+bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long long* st, bool bf16, bool swizzled,
+                 int tile_rows) {
     const auto enc = get_encode();
     if (!enc) return false;
     const cuuint64_t slot = (cuuint64_t)st[2], head = (cuuint64_t)st[1], page = (cuuint64_t)st[0];
-    const cuuint64_t dims5[5] = {64, (cuuint64_t)c.page, 2, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
+    const cuuint32_t wide = bf16 ? 64 : 32, pieces = D / wide;
+    const cuuint64_t dims5[5] = {wide, (cuuint64_t)c.page, pieces, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
     const cuuint64_t str5[4] = {slot, 128, head, page};
-    const cuuint32_t box5[5] = {64, (cuuint32_t)tile_rows, 2, 1, 1};
-    const cuuint64_t dims4[4] = {128, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
+    const cuuint32_t box5[5] = {wide, (cuuint32_t)tile_rows, pieces, 1, 1};
+    const cuuint64_t dims4[4] = {D, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
     const cuuint64_t str4[3] = {slot, head, page};
-    const cuuint32_t box4[4] = {128, (cuuint32_t)tile_rows, 1, 1};
+    const cuuint32_t box4[4] = {D, (cuuint32_t)tile_rows, 1, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const CUresult r =
-        bf16 ? enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims5, str5, box5, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)
-             : enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims4, str4, box4, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        swizzled ? enc(m, type, 5, const_cast<void*>(base), dims5, str5, box5, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)
+                 : enc(m, type, 4, const_cast<void*>(base), dims4, str4, box4, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
-
 
 struct Layout {
     size_t part, lse2, scores, total;  // byte offsets; the arrivals come first
@@ -1000,7 +1180,12 @@ Layout layout_of(const Cache& c, int g, bool with_mass) {
 }
 
 template <typename E>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int sms, int dev, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, int sms, int dev, cudaStream_t s) {
+    constexpr bool bf16 = sizeof(typename E::T) == 2;
+    CUtensorMap tk, tv;
+    if (!encode_pool(&tk, a.c, a.c.K, a.c.ks, bf16, E::SWIZZLED, E::TR) ||
+        !encode_pool(&tv, a.c, a.c.V, a.c.vs, bf16, E::SWIZZLED, E::TR))
+        return cudaErrorInvalidValue;
     const long long most = (long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, E::TR);  // tiles
     const long long useful = (most + WARPS - 1) / WARPS, units = (long long)a.c.seqs * a.c.heads;
     int grid = sms < MAX_GRID ? sms : MAX_GRID;
@@ -1078,17 +1263,13 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     int dev = 0;
     const int grid = sm_count(&dev);
     if (grid < 1) return CKV_ERR_CUDA;
-    const int tile_rows = bf16 ? TilesBf16<1>::TR : TilesF32<1>::TR;
-    CUtensorMap tk, tv;
-    if (!encode_pool(&tk, a.c, a.c.K, a.c.ks, bf16, tile_rows) || !encode_pool(&tv, a.c, a.c.V, a.c.vs, bf16, tile_rows))
-        return CKV_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (bf16) e = g <= 8 ? launch<TilesBf16<1>>(a, tk, tv, grid, dev, s) : launch<TilesBf16<2>>(a, tk, tv, grid, dev, s);
-    else if (g == 1) e = launch<TilesF32<1>>(a, tk, tv, grid, dev, s);
-    else if (g == 2) e = launch<TilesF32<2>>(a, tk, tv, grid, dev, s);
-    else if (g <= 4) e = launch<TilesF32<4>>(a, tk, tv, grid, dev, s);
-    else if (g <= 8) e = launch<TilesF32<8>>(a, tk, tv, grid, dev, s);
-    else e = launch<TilesF32<16>>(a, tk, tv, grid, dev, s);
+    if (bf16) e = g <= 8 ? launch<TilesBf16<1>>(a, grid, dev, s) : launch<TilesBf16<2>>(a, grid, dev, s);
+    else if (g == 1) e = launch<TilesF32<1>>(a, grid, dev, s);
+    else if (g == 2) e = launch<TilesF32<2>>(a, grid, dev, s);
+    else if (g <= 4) e = launch<TilesF32<4>>(a, grid, dev, s);
+    else if (g <= 8) e = launch<TilesF32<8>>(a, grid, dev, s);
+    else e = launch<TilesF32Tc<2>>(a, grid, dev, s);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;
 }

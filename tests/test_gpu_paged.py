@@ -231,7 +231,7 @@ def test_bad_pages_and_lengths_are_reported(dtype):
 
 
 @pytest.mark.parametrize("dtype,n,heads,g,page", [("bf16", 70001, 2, 4, 64), ("f32", 30011, 1, 7, 16),
-                                                  ("bf16", 131071, 1, 16, 128)])
+                                                  ("bf16", 131071, 1, 16, 128), ("f32", 20003, 2, 12, 32)])
 def test_long_sequences(dtype, n, heads, g, page):
     """Against torch in float64 on the GPU; besides the bounds, the relative
     2-norm of the error: the rounding of a score (|s| below 8, some hundred
