@@ -64,6 +64,7 @@ struct AttnArgs {
     float* part;        // [grid][2] partials of units that several CTAs share
     float* lse2;        // [units][g], base 2
     float* scores;      // [units][g][rows], base 2
+    int fuse;           // every unit has a CTA to itself, which adds its weights
     long long wait_limit;
 };
 
@@ -795,6 +796,50 @@ __device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, co
     *reinterpret_cast<float4*>(dst + j * D + 4 * lane) = o;
 }
 
+// mass_in of the four rows from r on, if one of them is below r1
+__device__ __forceinline__ float4 old_weights(const AttnArgs& a, int u, int r, int r1) {
+    return a.mass_in && r < r1 ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+// mass_out = v + sum_j e^{s_j - lse_j} for those of the four rows that are below r1
+__device__ __forceinline__ void add_weights(const AttnArgs& a, int u, int r, int r1, float4 v) {
+    const float* lse2 = a.lse2 + (size_t)u * a.g;
+    const float* sc = a.scores + (size_t)u * a.g * a.c.rows + r;
+    const size_t o = (size_t)u * a.c.rows + r;
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < a.g; j += 4) {
+        float4 x[4];
+        float lz[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lz[i] = -INFINITY;
+            if (j + i < a.g) {
+                x[i] = *reinterpret_cast<const float4*>(sc + (size_t)(j + i) * a.c.rows);
+                lz[i] = lse2[j + i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lz[i] != -INFINITY) {
+                add.x += ex2(x[i].x - lz[i]);
+                add.y += ex2(x[i].y - lz[i]);
+                add.z += ex2(x[i].z - lz[i]);
+                add.w += ex2(x[i].w - lz[i]);
+            }
+    }
+    v.x += add.x;
+    v.y += add.y;
+    v.z += add.z;
+    v.w += add.w;
+    if (r + 4 <= r1) {
+        *reinterpret_cast<float4*>(a.mass_out + o) = v;
+    } else {  // the rows behind the last one stay as they are
+        a.mass_out[o] = v.x;
+        if (r + 1 < r1) a.mass_out[o + 1] = v.y;
+        if (r + 2 < r1) a.mass_out[o + 2] = v.z;
+    }
+}
+
 template <typename E>
 __global__ void __launch_bounds__(WARPS * 32, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tk,
@@ -951,6 +996,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 if (a.lse && i < (long long)a.c.heads * a.g) a.lse[o + i] = -INFINITY;
             }
     if (!works) return;
+    // a CTA that adds its unit's weights itself asks for the old ones in time
+    const int unit_rows = a.fuse ? rows_held(a.c, a.c.by_heads.quot(blockIdx.x)) : 0;
+    const float4 old = old_weights(a, blockIdx.x, 4 * threadIdx.x, unit_rows);
     __syncthreads();
 
     // ---- merging.  This code runs once a call, and its instructions come from
@@ -1034,10 +1082,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             __syncthreads();
         }
     }
+    if (4 * (int)threadIdx.x < unit_rows) add_weights(a, blockIdx.x, 4 * threadIdx.x, unit_rows, old);
 }
 
 // ---------------------------------------------------------------- accumulated weights
-// mass_out = mass_in + sum_j e^{s_j - lse_j} over the tiles of the attention
+// The second pass over the scores: the tiles of the attention
 // kernel's warps, W_SPLIT CTAs to one of its, a lane four rows at a time.  Only
 // the scores and the lse come from the attention kernel: the deal is derived
 // again and the first rows' weights are loaded while its last CTAs still run.
@@ -1062,65 +1111,27 @@ __global__ void __launch_bounds__(WARPS * 32) paged_weights_kernel(const __grid_
     }
     Pos p{};
     int len = 0;
-    auto mass_at = [&](int u, int r, int r1) {
-        return a.mass_in && r < r1 ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
     float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < t1) {
         p = advance<TR>(a.c, walk<TR>(a.c, start[warp].x, start[warp].y), t - deal.begin_warp(cta * NW + warp));
         len = rows_held(a.c, p.s);
-        next = mass_at(p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
+        next = old_weights(a, p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
     }
     ptx::grid_dependency_wait();
     while (t < t1) {
         const int u = p.s * a.c.heads + p.h;
         const int n = min(p.nt - p.k, t1 - t);  // tiles of this unit
-        const float* lse2 = a.lse2 + (size_t)u * a.g;
-        const float* sc = a.scores + (size_t)u * a.g * a.c.rows;
         const int r1 = min(len, (p.k + n) * TR);
         for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
-            const size_t o = (size_t)u * a.c.rows + r;
-            float4 v = next;
-            next = mass_at(u, r + 128, r1);
-            float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < a.g; j += 4) {
-                float4 x[4];
-                float lz[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    lz[i] = -INFINITY;
-                    if (j + i < a.g) {
-                        x[i] = *reinterpret_cast<const float4*>(sc + (size_t)(j + i) * a.c.rows + r);
-                        lz[i] = lse2[j + i];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (lz[i] != -INFINITY) {
-                        add.x += ex2(x[i].x - lz[i]);
-                        add.y += ex2(x[i].y - lz[i]);
-                        add.z += ex2(x[i].z - lz[i]);
-                        add.w += ex2(x[i].w - lz[i]);
-                    }
-            }
-            v.x += add.x;
-            v.y += add.y;
-            v.z += add.z;
-            v.w += add.w;
-            if (r + 4 <= r1) {
-                *reinterpret_cast<float4*>(a.mass_out + o) = v;
-            } else {  // the rows behind the last one stay as they are
-                a.mass_out[o] = v.x;
-                if (r + 1 < r1) a.mass_out[o + 1] = v.y;
-                if (r + 2 < r1) a.mass_out[o + 2] = v.z;
-            }
+            const float4 old = next;
+            next = old_weights(a, u, r + 128, r1);
+            add_weights(a, u, r, r1, old);
         }
         t += n;
         p = advance<TR>(a.c, p, n);
         if (t < t1) {
             len = rows_held(a.c, p.s);
-            next = mass_at(p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
+            next = old_weights(a, p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
         }
     }
 }
@@ -1200,8 +1211,13 @@ cudaError_t launch(const AttnArgs& a, int sms, int dev, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(WARPS * 32), smem, s, a, tk, tv);
-    if (e == cudaSuccess && a.mass_out)
+    // Where the capacity alone says that every unit gets a CTA of its own, that
+    // CTA adds the weights and the second kernel is not launched.
+    AttnArgs b = a;
+    b.fuse = a.mass_out && units <= grid && ceil_div(ceil_div(a.c.rows, E::TR), WARPS) <= 1 + OWN_EXTRA;
+    static_assert((1 + OWN_EXTRA) * WARPS * E::TR <= 4 * WARPS * 32, "a thread adds the weights of four rows at most");
+    cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(WARPS * 32), smem, s, b, tk, tv);
+    if (e == cudaSuccess && a.mass_out && !b.fuse)
         e = launch_dependent(paged_weights_kernel<E::TR>, dim3(grid * W_SPLIT), dim3(WARPS * 32), 0, s, a);
     return e;
 }
@@ -1259,6 +1275,7 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.part = reinterpret_cast<float*>(w + l.part);
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
     a.scores = mass_out ? reinterpret_cast<float*>(w + l.scores) : nullptr;
+    a.fuse = 0;
     a.wait_limit = WAIT_LIMIT;
     int dev = 0;
     const int grid = sm_count(&dev);
