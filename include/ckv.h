@@ -341,9 +341,8 @@ ckv_status ckv_sparse_decode_attn_noalloc(const void* q, int32_t q_dtype, const 
  * dense decode attention over all rows held, and eviction of the rows with the
  * least accumulated attention weight.  It serves what the recallable path does
  * not: layers and sequences attended in full, batches whose sequences grow,
- * end and share memory, and the non-recallable alternative (drop rows for
- * good; ClusterKV page, section "Background and design principles": methods
- * that evict by attention weight) next to the recallable selection.
+ * end and share memory, and the non-recallable alternative to the selection
+ * (rows are dropped for good).  The ClusterKV page has no counterpart of it.
  *
  *   K, V      pools of n_pages pages; element (page, head, slot, channel) at
  *             page * stride[0] + head * stride[1] + slot * stride[2] + channel
@@ -370,8 +369,7 @@ ckv_status ckv_sparse_decode_attn_noalloc(const void* q, int32_t q_dtype, const 
  * skipped with its rows (CKV_DEV_BAD_INDEX).
  * Common errors: CKV_ERR_ARG (null pointer, d != 128, page_size not a multiple
  * of 16, a non-positive extent, R above 2^31 - 17, a stride too small or above
- * 2^37 elements),
- * CKV_ERR_DTYPE, CKV_ERR_ALIGN. */
+ * 2^37 elements), CKV_ERR_DTYPE, CKV_ERR_ALIGN. */
 typedef struct {
     void* K;
     void* V;
@@ -430,7 +428,8 @@ ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int
  * its start zero again).  Calls that can overlap on the GPU (two streams, two
  * graphs) need workspaces of their own.
  * Errors: as above; CKV_ERR_ARG (g outside [1, 16], scale not finite, mass_in
- * without mass_out, seqs * heads * R of 2^34 and more), CKV_ERR_CAPACITY (workspace too small). */
+ * without mass_out, seqs * heads * R of 2^34 and more), CKV_ERR_CAPACITY
+ * (workspace too small). */
 ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, int32_t q_dtype, const int64_t* q_stride,
                                  int32_t g, float scale, float* out, float* lse, const float* mass_in,
                                  float* mass_out, void* workspace, int64_t workspace_bytes, void* stream);
@@ -449,7 +448,8 @@ ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, in
  * _apply carries the moves out for K, V and (where not NULL) mass and pos, and
  * sets lens[s] := min(lens[s], budget); pages past the budget are then free.
  * Sources lie at or past the budget and destinations below it, so the moves
- * have no order and repeating the call changes nothing; a move outside those
+ * have no order and repeating the call changes nothing (two moves of one (s, h)
+ * must not share a destination; _select's never do); a move outside those
  * ranges is skipped (CKV_DEV_BAD_INDEX), n_moves outside [0, max_moves] is
  * clamped (CKV_DEV_BAD_COUNT).
  * Errors: as above; CKV_ERR_ARG (budget < 1, sinks, recent or max_moves < 0,

@@ -341,6 +341,36 @@ def test_two_handles_and_graphs_at_once():
         assert torch.equal(c.out, out2) and torch.equal(c.lse, lse2)
 
 
+@pytest.mark.parametrize("lens", [[900, 64, 2500, 0], [300, 1, 0, 384]])
+def test_weights_in_two_graphs_at_once(lens):
+    """Weights from two handles' graphs on two streams at the same time, added
+    in place replay after replay, in the attention kernel (short capacity) and
+    behind it."""
+    c = Case(lens, 2, 3, 16, "bf16")
+    mass = [torch.zeros_like(c.mass), torch.zeros_like(c.mass)]
+    outs = [torch.empty_like(c.out), torch.empty_like(c.out)]
+    one = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=one)
+    torch.cuda.synchronize()
+    c.check_attention(mass_out=one, mass_before=np.zeros(one.shape))
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st, m, o in zip(streams, mass, outs):
+        handle = c.make()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            handle.decode_attn(c.q, o, mass_in=m, mass_out=m)
+        graphs.append((graph, handle))
+    torch.cuda.synchronize()
+    for _ in range(16):
+        for st, (graph, _) in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    # 16 additions of the same value, each rounded to half a unit in the last place
+    assert torch.equal(mass[0], mass[1]) and torch.equal(outs[0], c.out) and torch.equal(outs[1], c.out)
+    assert ((mass[0].double() - 16 * one.double()).abs() <= 16 * 2.0 ** -24 * 16 * one.double()).all()
+
+
 def test_shared_pages():
     """Sequences that share a prefix's pages: each has its own weights."""
     c = Case([64, 80, 33], 2, 4, 16, "bf16", width=5)
