@@ -398,9 +398,12 @@ typedef struct {
  * first[s], or seen[s] when first is NULL; then lens[s] := r0 + counts[s] and
  * seen[s] := p0 + counts[s].  A sequence whose r0 or count is negative, whose
  * count is above n or that would pass R is left as it is (CKV_DEV_BAD_COUNT).
- * The sources may be mapped pinned host memory.  start and first must not
- * overlap lens and seen unless they are the same pointers.
- * Errors: as above; CKV_ERR_ARG (n < 1, pos without seen). */
+ * The sources may be mapped pinned host memory; they must not overlap the rows
+ * written.  counts, start and first may each be lens or seen themselves (the
+ * values from before the call count).
+ * Errors: as above; CKV_ERR_ARG (n < 1, pos without seen, lens and seen, or
+ * one of counts, start and first and one of lens and seen, overlapping without
+ * being the same). */
 ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void* k_src, const void* v_src,
                             const int64_t* k_src_stride, const int64_t* v_src_stride, int32_t n,
                             const int32_t* counts, const int32_t* start, const int32_t* first, void* stream);

@@ -42,6 +42,13 @@ bool strides_aligned(const long long* b, int n) {
     return true;
 }
 
+// two int32 arrays of n elements that are one and the same (an element is read
+// before it is written) or do not overlap; no array overlaps nothing
+bool same_or_apart(const int32_t* x, const int32_t* y, int n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return !x || !y || a == b || (a < b ? b - a : a - b) >= (uintptr_t)n * sizeof(int32_t);
+}
+
 }  // namespace
 
 ckv_status check_cache(const ckv_paged_cache* c, Cache* o) {
@@ -164,7 +171,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
     }
     if (a.advance) {
         // the plan was read by every thread of the sequence's only block
-        // (advance in place), or from start and first, which nothing writes
+        // (advance in place), or from arrays that nothing here writes
         __syncthreads();
         if (b == 0 && threadIdx.x == 0) append_advance(a, s, r0, p0, cnt);
     }
@@ -776,9 +783,14 @@ extern "C" ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void*
     // a thread's item index plus a step stays below 2^31
     if ((long long)n * a.c.heads + (blocks + 1) * per_pass > 0x7fffffffLL) return CKV_ERR_ARG;
     a.by_blocks = FastDiv((uint32_t)blocks);
-    // lens and seen may be advanced by the copying kernel where no other
-    // block can still read the old values
-    const bool in_place = !a.start || (a.c.seen && !a.first);
+    // lens and seen may be advanced by the copying kernel where no other block
+    // can still read the old values, whichever argument they are read through
+    const int32_t* reads[3] = {a.start ? a.start : a.c.lens, a.first ? a.first : a.c.seen, counts};
+    bool in_place = false;
+    for (const int32_t* r : reads) {
+        if (!same_or_apart(r, a.c.lens, a.c.seqs) || !same_or_apart(r, a.c.seen, a.c.seqs)) return CKV_ERR_ARG;
+        if (r && (r == a.c.lens || r == a.c.seen)) in_place = true;
+    }
     a.advance = !in_place || blocks == 1;
     cudaStream_t s = (cudaStream_t)stream;
     const dim3 grid((unsigned)(blocks * a.c.seqs)), block(APPEND_THREADS);

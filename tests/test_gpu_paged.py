@@ -458,6 +458,37 @@ def test_append(dtype, layout, page, heads, n, given):
     assert int(c.err) == 0 and torch.equal(c.lens, want["lens"]) and torch.equal(c.K, want["K"])
 
 
+@pytest.mark.parametrize("dtype,n,heads", [("bf16", 1, 2), ("bf16", 300, 4), ("f32", 90, 8), ("bf16", 2000, 8)])
+@pytest.mark.parametrize("start,first,counts", [("seen", "own", None), ("own", "lens", None), ("seen", "lens", None),
+                                                ("lens", "own", "lens"), ("own", "own", "seen"), ("own", "own", "lens")])
+def test_append_with_lens_and_seen_as_other_arguments(dtype, n, heads, start, first, counts):
+    """start = seen, first = lens and counts = either: every block of a sequence
+    takes the values from before the call, however many blocks it has."""
+    page, S = 64, 6
+    width = 2 + -(-2 * n // page)
+    c = Case([width * page] * S, heads, 1, page, dtype, "hpd", garbage=0.0)
+    c.lens.copy_(torch.tensor([0, 1, n, 5 % n, n // 2, n]))
+    c.seen.copy_(torch.tensor([n, 0, 3 % n, 1, n, n // 3]))
+    vec = {"lens": c.lens, "seen": c.seen, "own": torch.arange(S, dtype=torch.int32, device="cuda") % n, None: None}
+    old = {k: None if t is None else t.cpu().clone() for k, t in vec.items()}
+    src = torch.randn(2, S, heads, n, D).to(DT[dtype]).cuda()
+    want = {x: getattr(c, x).clone() for x in ("K", "V", "mass", "pos")}
+    cnt = [n] * S if counts is None else old[counts].tolist()
+    for s in range(S):
+        j = torch.arange(cnt[s], device="cuda")
+        r = j + int(old[start][s])
+        pg = c.table[s].long()[r // page]
+        want["K"][pg, :, r % page], want["V"][pg, :, r % page] = (x[s, :, j].transpose(0, 1) for x in src)
+        want["pos"][s][:, r], want["mass"][s][:, r] = (j + int(old[first][s])).int(), 0.0
+    c.handle.append(src[0], src[1], counts=vec[counts], start=vec[start], first=vec[first])
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    for x, t in want.items():
+        assert torch.equal(getattr(c, x), t), x
+    assert c.lens.tolist() == [int(a) + b for a, b in zip(old[start], cnt)]
+    assert c.seen.tolist() == [int(a) + b for a, b in zip(old[first], cnt)]
+
+
 def test_append_bad_counts_and_pages():
     c = Case([64] * 4, 2, 1, 16, "bf16", garbage=0.0)
     c.lens.copy_(torch.tensor([-1, 0, 0, 8]))

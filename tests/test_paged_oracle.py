@@ -135,6 +135,21 @@ def test_append_refusals(lib):
     assert lib.ckv_paged_append(None, P, P, st, st, 1, None, None, None, None) == ARG
 
 
+def test_append_refuses_arrays_that_overlap_in_part(lib):
+    """counts, start and first against lens and seen, and these two: the blocks
+    of other sequences would read what one of them writes."""
+    far = 1 << 24
+    for at in (4, 8, -4, -8):  # three sequences: twelve bytes
+        c = struct(lens=far, seen=2 * far)
+        r = ctypes.addressof(c)
+        for x in (far + at, 2 * far + at):
+            for args in ((x, None, None), (None, x, None), (None, None, x), (x, 4 * far, 5 * far)):
+                assert lib.ckv_paged_append(r, P, P, i64(128, 128, 128), i64(128, 128, 128), 1, *args, None) == ARG
+        c = struct(lens=far, seen=far + at)
+        assert lib.ckv_paged_append(ctypes.addressof(c), P, P, i64(128, 128, 128), i64(128, 128, 128), 1, None, None,
+                                    None, None) == ARG
+
+
 def test_attention_refusals(lib):
     c = struct()
     r = ctypes.addressof(c)
