@@ -423,8 +423,10 @@ ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int
  * [seqs][heads * g][d] float; lse [seqs][heads * g] float or NULL; mass_out
  * [seqs][heads][R] float or NULL, mass_in the same or NULL (taken as 0), and
  * may be mass_out itself; entries of rows not held are left as they are.  fp32
- * arithmetic on products of the operands as they are.  Values of rows not held
- * are never used, whatever they are; held rows must be finite.
+ * arithmetic on products of the operands as they are: sum_i |scale q_i K_ri|
+ * and sum_r e^{s_r - max s} |V_r| have to stay below 2^126, and weights below
+ * 2^-125 of a query head's largest may be lost.  Values of rows not held are
+ * never used, whatever they are; held rows and q must be finite.
  * Results do not depend on the order in which the GPU runs the blocks.
  * workspace: caller-owned, 256-byte aligned, at least the size given above,
  * zeroed by the caller before its first use (every call leaves the counters at

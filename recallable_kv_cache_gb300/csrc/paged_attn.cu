@@ -223,7 +223,7 @@ template <int NB>
 struct TilesBf16 {
     using T = __nv_bfloat16;
     static constexpr int TR = 16, SCRATCH = 0;
-    static constexpr bool SWIZZLED = true;
+    static constexpr bool SWIZZLED = true, CHECKED = false;
     uint32_t qa[8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
@@ -233,7 +233,7 @@ struct TilesBf16 {
         tma_load_5d(dst, tk, 0, slot, 0, h, page, bar);
         tma_load_5d(dst + STAGE / 2, tv, 0, slot, 0, h, page, bar);
     }
-    __device__ __forceinline__ void reset(const T* q, long long stride, int g, int lane) {
+    __device__ __forceinline__ void reset(const T* q, long long stride, int g, float, int lane) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int j = (lane >> 2) + 8 * b;
@@ -433,7 +433,7 @@ template <int GP>
 struct TilesF32 {
     using T = float;
     static constexpr int TR = 8, SCRATCH = TR * GP;
-    static constexpr bool SWIZZLED = false;
+    static constexpr bool SWIZZLED = false, CHECKED = false;
     static constexpr int LPR = GP > 2 ? 16 : 8;  // lanes per row: q takes 128 / LPR * GP registers
     static constexpr int QV = 32 / LPR;          // float4 of a row per lane
     static constexpr int RP = 32 / LPR;          // rows at a time
@@ -447,7 +447,7 @@ struct TilesF32 {
         tma_load_4d(dst, tk, 0, slot, h, page, bar);
         tma_load_4d(dst + STAGE / 2, tv, 0, slot, h, page, bar);
     }
-    __device__ __forceinline__ void reset(const T* q, long long stride, int g, int lane) {
+    __device__ __forceinline__ void reset(const T* q, long long stride, int g, float, int lane) {
 #pragma unroll
         for (int j = 0; j < GP; ++j) {
 #pragma unroll
@@ -566,7 +566,14 @@ struct TilesF32 {
 // take 100, so up to eight they are used).  Every operand is taken apart into
 // three bf16 terms (hi + mid + lo, which hold its 24 bits), and of the nine
 // products the six down to 2^-18 of the largest are added up, the small ones
-// first.  8 rows a tile, four quarters of 32 channels, [quarter][row][128
+// first.  bf16 ends at 2^-133, so that the terms of a value below 2^-110 leave
+// a rest of up to 2^-134.  K's rests put a score, 128 products, off by 2^-127
+// times the largest query value; a weight is at most 1, and fp32's exponential
+// ends at 2^-126; but rests of V or q may be all there is.  So a warp keeps the
+// least value of those that are not zero, and where that is below 2^-110, or a
+// query value times the scale past 2^96, it does its tiles of the unit again in
+// plain fp32 (16 heads above: 158 us without the least value, 163 with it, 181
+// with a look at every tile's).  8 rows a tile, four quarters of 32 channels, [quarter][row][128
 // bytes], 128-byte swizzled (16-byte chunk c of row r at c ^ r).
 //   S[h][r] = q[h] . K[r]        m16n8k16: M = 16 heads, N = 8 rows
 //   O[c][h] += V[r][c] P[h][r]   m16n8k8:  M = 16 channels, N = 8 heads, K = 8 rows
@@ -579,23 +586,28 @@ template <int NB>
 struct TilesF32Tc {
     using T = float;
     static constexpr int TR = 8, SCRATCH = 0;
-    static constexpr bool SWIZZLED = true;
+    static constexpr bool SWIZZLED = true, CHECKED = true;
+    static constexpr uint32_t TINY = (17u << 24) - 1;  // order() of 2^-110
     uint32_t qa[3][8][2 * NB];
     float o[NB][8][4];
     float mrun[NB], lrun[NB];  // of head lane / 4 + 8 b
+    uint32_t least;            // order() of the lane's V and q; 0: a query value is too large
 
     struct Terms {
         uint32_t t[3];  // hi, mid, lo of two values
     };
+    // hi saturates: a value that would round to infinity leaves its rest to mid
     static __device__ __forceinline__ Terms split(float x, float y) {
         Terms r;
-        r.t[0] = pack2(x, y);
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r.t[0]) : "f"(y), "f"(x));
         x -= lo_of(r.t[0]);
         y -= hi_of(r.t[0]);
         r.t[1] = pack2(x, y);
         r.t[2] = pack2(x - lo_of(r.t[1]), y - hi_of(r.t[1]));
         return r;
     }
+    // the order of magnitudes, zero the largest
+    static __device__ __forceinline__ uint32_t order(float x) { return 2u * __float_as_uint(x) - 1u; }
     static __device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
         asm volatile(
             "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
@@ -607,7 +619,9 @@ struct TilesF32Tc {
         tma_load_5d(dst, tk, 0, slot, 0, h, page, bar);
         tma_load_5d(dst + STAGE / 2, tv, 0, slot, 0, h, page, bar);
     }
-    __device__ __forceinline__ void reset(const T* q, long long stride, int g, int lane) {
+    __device__ __forceinline__ void reset(const T* q, long long stride, int g, float qscale, int lane) {
+        float most = 0.f;
+        least = 0xffffffffu;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int j = (lane >> 2) + 8 * b;
@@ -617,12 +631,21 @@ struct TilesF32Tc {
                                                                           4 * (2 * (lane & 3) + (ks & 1)))
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
                 const Terms u = split(x.x, x.y), v = split(x.z, x.w);
+                most = fmaxf(fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+                least = min(min(least, min(order(x.x), order(x.y))), min(order(x.z), order(x.w)));
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     qa[i][ks][b] = u.t[i];
                     qa[i][ks][NB + b] = v.t[i];
                 }
             }
+        }
+        if (!(most * fabsf(qscale) < 0x1p96f)) least = 0;
+        clear();
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -635,6 +658,49 @@ struct TilesF32Tc {
     static __host__ __device__ constexpr int left(int i) { return i == 1 ? 2 : (i == 2 || i == 3 ? 1 : 0); }
     static __host__ __device__ constexpr int right(int i) { return i == 0 ? 2 : (i == 2 || i == 4 ? 1 : 0); }
 
+    // the weights p of a tile's rows 2 t + e from its scores s[2 b + e]; the
+    // running maximum, the sum and O follow
+    __device__ __forceinline__ void weigh(const float (&s)[4], int n, float qscale, int g, float* scores, size_t rows,
+                                          int lane, float (&p)[NB][2]) {
+        const int row = lane >> 2, t = lane & 3;
+        float sc[NB];
+        bool grew = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) v[e] = 2 * t + e < n ? s[2 * b + e] * qscale : -INFINITY;
+            const int j = row + 8 * b;
+            if (scores && j < g) *reinterpret_cast<float2*>(scores + (size_t)j * rows + 2 * t) = make_float2(v[0], v[1]);
+            float tm = fmaxf(v[0], v[1]);
+            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 1));
+            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 2));
+            const float mnew = fmaxf(mrun[b], tm);
+            const float ms = mnew == -INFINITY ? 0.f : mnew;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[b][e] = ex2(v[e] - ms);
+            sc[b] = 1.f;
+            if (mnew != mrun[b]) {
+                sc[b] = ex2(mrun[b] - ms);
+                grew = true;
+            }
+            lrun[b] = lrun[b] * sc[b] + (p[b][0] + p[b][1]);
+            mrun[b] = mnew;
+        }
+        if (__any_sync(FULL, grew)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float sc0 = __shfl_sync(FULL, sc[b], t * 8), sc1 = __shfl_sync(FULL, sc[b], t * 8 + 4);
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    o[b][mt][0] *= sc0;
+                    o[b][mt][1] *= sc1;
+                    o[b][mt][2] *= sc0;
+                    o[b][mt][3] *= sc1;
+                }
+            }
+        }
+    }
     __device__ __forceinline__ void tile(unsigned char* stage, float2*, int n, float qscale, int g, float* scores,
                                          size_t rows, int lane) {
         const int row = lane >> 2, t = lane & 3;
@@ -651,46 +717,13 @@ struct TilesF32Tc {
                     u.t[right(i)], v.t[right(i)]);
             }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += small[e];
+        float p[NB][2];
+        weigh(s, n, qscale, g, scores, rows, lane, p);
         Terms p3[NB];
-        float sc[NB];
-        bool grew = false;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float v[2], p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                v[e] = 2 * t + e < n ? (s[2 * b + e] + small[2 * b + e]) * qscale : -INFINITY;
-            const int j = row + 8 * b;
-            if (scores && j < g) *reinterpret_cast<float2*>(scores + (size_t)j * rows + 2 * t) = make_float2(v[0], v[1]);
-            float tm = fmaxf(v[0], v[1]);
-            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 1));
-            tm = fmaxf(tm, __shfl_xor_sync(FULL, tm, 2));
-            const float mnew = fmaxf(mrun[b], tm);
-            const float ms = mnew == -INFINITY ? 0.f : mnew;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) p[e] = ex2(v[e] - ms);
-            sc[b] = 1.f;
-            if (mnew != mrun[b]) {
-                sc[b] = ex2(mrun[b] - ms);
-                grew = true;
-            }
-            lrun[b] = lrun[b] * sc[b] + (p[0] + p[1]);
-            mrun[b] = mnew;
-            p3[b] = split(p[0], p[1]);
-        }
-        if (__any_sync(FULL, grew)) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const float sc0 = __shfl_sync(FULL, sc[b], t * 8), sc1 = __shfl_sync(FULL, sc[b], t * 8 + 4);
-#pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                    o[b][mt][0] *= sc0;
-                    o[b][mt][1] *= sc1;
-                    o[b][mt][2] *= sc0;
-                    o[b][mt][3] *= sc1;
-                }
-            }
-        }
+        for (int b = 0; b < NB; ++b) p3[b] = split(p[b][0], p[b][1]);
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
             float x[2][4];  // rows not held count as zero
@@ -705,6 +738,8 @@ struct TilesF32Tc {
                 x[e][3] = held ? v.w : 0.f;
             }
 #pragma unroll
+            for (int e = 0; e < 8; ++e) least = min(least, order(x[e / 4][e % 4]));
+#pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const Terms u = split(x[0][2 * half], x[1][2 * half]), v = split(x[0][2 * half + 1], x[1][2 * half + 1]);
 #pragma unroll
@@ -714,6 +749,62 @@ struct TilesF32Tc {
                     for (int i = 0; i < 6; ++i) mma8(d, u.t[left(i)], v.t[left(i)], p3[b].t[right(i)]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[b][2 * f + half][e] += d[e];
+                }
+            }
+        }
+    }
+    // tiles k0 .. k1 of unit u again, on fp32 products of the pool's values
+    __device__ __forceinline__ void again(const AttnArgs& a, int u, int k0, int k1, int lane) {
+        const int row = lane >> 2, t = lane & 3;
+        int h;
+        const int seq = a.c.by_heads.quot(u, &h), len = rows_held(a.c, seq);
+        const float* q = static_cast<const float*>(a.q) + seq * a.qst[0] + (long long)h * a.g * a.qst[1];
+        clear();
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) {
+            const int n = min(TR, len - k * TR);
+            int slot;
+            const int page = page_of(a.c, seq, k * TR, &slot);
+            if (page < 0) continue;
+            const unsigned char* K = a.c.K + page * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2];
+            const unsigned char* V = a.c.V + page * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2];
+            float s[4] = {0.f, 0.f, 0.f, 0.f}, p[NB][2];
+#pragma unroll 1
+            for (int c = 0; c < D / 4; ++c) {
+                float4 x[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    x[e] = 2 * t + e < n ? *reinterpret_cast<const float4*>(K + (2 * t + e) * a.c.ks[2] + 16 * c)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if (row + 8 * b >= a.g) continue;
+                    const float4 y = *reinterpret_cast<const float4*>(q + (row + 8 * b) * a.qst[1] + 4 * c);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        s[2 * b + e] =
+                            fmaf(y.w, x[e].w, fmaf(y.z, x[e].z, fmaf(y.y, x[e].y, fmaf(y.x, x[e].x, s[2 * b + e]))));
+                }
+            }
+            weigh(s, n, a.qscale, a.g, a.scores ? a.scores + (size_t)u * a.g * a.c.rows + (size_t)k * TR : nullptr,
+                  a.c.rows, lane, p);
+#pragma unroll 1
+            for (int r = 0; r < n; ++r) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const float w = r & 1 ? p[b][1] : p[b][0];
+                    const float w0 = __shfl_sync(FULL, w, 8 * t + (r >> 1)), w1 = __shfl_sync(FULL, w, 8 * t + 4 + (r >> 1));
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const float4 v = *reinterpret_cast<const float4*>(V + r * a.c.vs[2] + 128 * f + 16 * row);
+                        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float(&to)[4] = o[b][2 * f + (e >> 1)];
+                            to[2 * (e & 1)] = fmaf(w0, x[e], to[2 * (e & 1)]);
+                            to[2 * (e & 1) + 1] = fmaf(w1, x[e], to[2 * (e & 1) + 1]);
+                        }
+                    }
                 }
             }
         }
@@ -889,7 +980,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             u = s * a.c.heads + h;
             nt = tiles;
             first = at;
-            e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, lane);
+            e.reset(static_cast<const T*>(a.q) + s * a.qst[0] + (long long)h * a.g * a.qst[1], a.qst[1], a.g, a.qscale,
+                    lane);
         };
         Pos base = walk<TR>(a.c, start[warp].x, start[warp].y);
         // q is asked for before the tiles: behind them it would wait for all
@@ -928,6 +1020,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             }
         };
         auto leave = [&](bool tail) {
+            if constexpr (E::CHECKED)
+                if (!dead && __any_sync(FULL, e.least < E::TINY))
+                    e.again(a, u, max(0, t_begin - first), min(nt, t_end - first), lane);
             // final where the whole unit was this warp's, else left to be merged
             const bool whole = first >= t_begin && first + nt <= t_end;
             const size_t o = (size_t)u * a.g;

@@ -211,6 +211,66 @@ def test_rows_not_held_are_never_used(dtype, garbage):
     c.check_attention(mass_out=out, mass_before=np.zeros(out.shape))
 
 
+RANGES = ["small V", "V by channel", "V by row", "large V", "V with zeros", "K against q", "K large", "q large", "scale"]
+
+
+@pytest.mark.parametrize("kind", RANGES)
+@pytest.mark.parametrize("dtype,g", [("f32", 2), ("f32", 8), ("f32", 9), ("f32", 16), ("bf16", 4), ("bf16", 16)])
+def test_operands_over_the_whole_range(dtype, g, kind):
+    """Operands from the smallest subnormal to the largest finite value, at the
+    bounds at the top of this file; below 2^-126 a step of a sum is off by half
+    a unit of 2^-149: one for each row and, where the running maximum grows, one
+    more, and some for what is joined at the end."""
+    c = Case([1, 7, 130, 61, 3000], 2, g, 16, dtype, "hpd", seed=g)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    scale, rows, channels = D ** -0.5, c.K.shape[:3] + (1,), torch.arange(D, device="cuda")
+    if kind == "small V":
+        c.V *= 1e-38
+    elif kind == "V by channel":  # 2^-145 to 2^109
+        c.V.copy_(torch.ldexp(c.V.float(), 2 * channels - 145))
+    elif kind == "V by row":  # 2^-140 to 2^-90, so that only some tiles are small
+        c.V.copy_(torch.ldexp(c.V.float(), torch.randint(-140, -90, rows, generator=gen, device="cuda")))
+    elif kind == "large V":  # rows of the largest value, with weights that all but vanish
+        top = torch.finfo(DT[dtype]).max
+        c.q.copy_(torch.full_like(c.q, 1.0))
+        pick = (torch.rand(rows, generator=gen, device="cuda") < 0.2) & c.K.isfinite()
+        c.V.copy_(torch.where(pick, torch.sign(c.V) * top, c.V))
+        c.K.copy_(torch.where(pick, torch.full_like(c.K, -4.0), c.K))
+    elif kind == "V with zeros":
+        c.V.copy_(torch.where((channels >= 96) & c.V.isfinite(), torch.zeros_like(c.V), c.V))
+    elif kind == "K against q":  # products near 1 of factors from 2^-120 to 2^120
+        e = (channels * 53) % 241 - 120
+        c.K.copy_(torch.ldexp(c.K.float(), e))
+        c.q.copy_(torch.ldexp(c.q.float(), -e))
+    elif kind == "K large":  # the largest values against zeros and tiny ones
+        c.K.copy_(torch.where((channels % 3 == 0) & c.K.isfinite(), torch.full_like(c.K, torch.finfo(DT[dtype]).max), c.K))
+        c.q.copy_(torch.where(channels % 3 == 0, torch.where(channels % 2 == 0, 0.0, 2.0 ** -126), c.q.float()))
+    elif kind == "q large":
+        c.q.copy_(torch.where(channels % 3 == 0, torch.full_like(c.q, torch.finfo(DT[dtype]).max), c.q))
+        c.K.copy_(torch.where((channels % 3 == 0) & c.K.isfinite(), c.K.float() * 2.0 ** -127, c.K.float()))
+    else:  # a large scale over small operands
+        c.K.copy_(torch.ldexp(c.K.float(), torch.tensor(-40, device="cuda")))
+        c.q.copy_(torch.ldexp(c.q.float(), torch.tensor(-60, device="cuda")))
+        scale = 2.0 ** 97
+    mass = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=mass, scale=scale)
+    torch.cuda.synchronize()
+    out, lse, q = (x.double().cpu().numpy() for x in (c.out, c.lse, c.q))
+    for s, n in enumerate(c.lens_list):
+        for h in range(c.heads):
+            k, v, ok = c.rows(s, h)
+            at = slice(h * g, (h + 1) * g)
+            o, z, w = po.attend(q[s, at], k, v, ok, scale)
+            es = 2.0 ** -16 * scale * (np.abs(q[s, at]) @ np.abs(k).T).max()
+            sums = 2.0 ** -23 * (n / 16 + 200)
+            eps = 4 * es + 2.0 ** -16 + 2 * sums
+            p = np.exp(scale * (q[s, at] @ k.T) - z[:, None])
+            bound = eps * (p @ np.abs(v)) + (2 * n + 16) * 2.0 ** -149
+            assert (np.abs(out[s, at] - o) <= bound).all()
+            assert (np.abs(lse[s, at] - z) <= 2 * es + 2.0 ** -19 + sums + 2.0 ** -23 * np.abs(z)).all()
+            assert (np.abs(mass[s, h, :n].double().cpu().numpy() - w) <= eps * w + 2.0 ** -23 * w + 1e-30).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_pages_and_lengths_are_reported(dtype):
     """A bad page id drops its rows, a bad length is clamped; both are reported,
