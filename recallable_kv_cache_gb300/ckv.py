@@ -372,9 +372,12 @@ class PagedCache:
     outside a capture).  Like a Context, one handle
     must not be used from two streams at the same time; another handle over the
     same tensors has a workspace of its own.  Calls run on the tensors' device,
-    on ``stream`` or that device's current stream.  A tensor of another shape,
-    dtype, device or layout raises ValueError (TypeError for dtypes) and nothing
-    is launched."""
+    on ``stream`` or that device's current stream.  The handle may be dropped
+    while calls are under way: the workspace's memory is used again only after
+    them.  A graph captured from its calls keeps nothing alive, so the handle
+    has to outlive it, and a raw stream (not torch's) has to outlive the handle.
+    A tensor of another shape, dtype, device or layout raises ValueError
+    (TypeError for dtypes) and nothing is launched."""
 
     def __init__(self, K, V, table, lens, g: int = 1, mass=None, pos=None, seen=None, dev_err=None):
         import torch
@@ -421,6 +424,7 @@ class PagedCache:
         self.workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
         self.workspace[:4096].zero_()  # the counters; calls leave them zero
         torch.cuda.current_stream(self.device).synchronize()  # whatever stream the first call is on
+        self._streams = {self._raw_stream(self._index)}  # on which the allocator knows the workspace is used
         self._workspace = (ptr(self.workspace), need.value)
 
     def _tensor(self, name, t, shape, dtype, contiguous=True):
@@ -449,8 +453,22 @@ class PagedCache:
             got = self._stride_arrays[key] = (ctypes.c_int64 * n)(*key[:n])
         return got
 
+    def _note_stream(self, raw):
+        """Tells the allocator that the workspace is in use on a stream, once for
+        each: memory that is freed goes to the stream it was allocated on, after
+        what is then queued on the others.  Not while the stream is capturing:
+        nothing runs, and the graph's replays are its owner's."""
+        stream = self._cuda.ExternalStream(raw, device=self.device)
+        with self._cuda.stream(stream):
+            if self._cuda.is_current_stream_capturing():
+                return
+        self.workspace.record_stream(stream)
+        self._streams.add(raw)
+
     def _call(self, fn, stream, *args):
         stream = self._raw_stream(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
+        if stream not in self._streams and fn is self._attn:
+            self._note_stream(stream)
         if self._index == self._current():
             status = fn(self._ref, *args, stream)
         else:

@@ -477,6 +477,38 @@ def test_side_stream_argument():
     c.check_attention()
 
 
+@pytest.mark.parametrize("how", ["argument", "current", "in a pool"])
+def test_handle_dropped_with_work_queued_on_another_stream(how):
+    """The workspace of a handle that dies while a side stream has yet to use it
+    is not handed out on the stream that the handle was made on."""
+    c = Case([900, 64, 2500, 0], 4, 4, 16, "bf16", width=200)
+    want = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=want)
+    mass, out = torch.zeros_like(c.mass), torch.zeros_like(c.out)
+    handle, side = c.make(), torch.cuda.Stream()
+    if how == "in a pool":  # the first call on the stream is captured, the second is not
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            handle.decode_attn(c.q, out, mass_out=mass)
+    torch.cuda.synchronize()
+    at, nbytes = handle.workspace.data_ptr(), handle.workspace.numel()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)  # some 0.2 s
+    if how == "argument":
+        handle.decode_attn(c.q, out, mass_out=mass, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            handle.decode_attn(c.q, out, mass_out=mass)
+    del handle
+    others = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not side.query()
+    for t in others:
+        assert not t.data_ptr() <= at < t.data_ptr() + nbytes
+        t.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(out, c.out) and torch.equal(mass, want)
+
+
 # ---------------------------------------------------------------- append
 @pytest.mark.parametrize("dtype,layout,page,heads,n", [
     ("bf16", "hpd", 16, 2, 1), ("f32", "phd", 16, 3, 1), ("bf16", "kv_in_page", 48, 8, 37), ("f32", "wide", 32, 1, 70),

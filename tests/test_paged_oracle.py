@@ -235,3 +235,42 @@ def tensors(**kw):
 def test_handle_refuses_wrong_tensors(bad, exc):
     with pytest.raises(exc):
         ckv.PagedCache(**tensors(**bad))
+
+
+def test_workspace_is_recorded_once_on_every_other_stream():
+    """The allocator learns of each stream the workspace is used on, before the
+    launch, but not of one that is capturing (nothing runs there)."""
+    import contextlib
+    log, capturing = [], []
+
+    class Cuda:
+        ExternalStream = staticmethod(lambda raw, device: raw)
+
+        @staticmethod
+        @contextlib.contextmanager
+        def stream(raw):
+            log.append(("on", raw))
+            yield
+
+        is_current_stream_capturing = staticmethod(lambda: log[-1][1] in capturing)
+
+    class Workspace:
+        record_stream = staticmethod(lambda raw: log.append(("record", raw)))
+
+    h = ckv.PagedCache.__new__(ckv.PagedCache)
+    h.device, h._index, h._ref, h._cuda, h.workspace, h._streams = "cuda:0", 0, None, Cuda, Workspace, {5}
+    h._raw_stream, h._current = (lambda i: 5), (lambda: 0)
+    h._attn, h._append = (lambda *a: log.append(("attn", a[-1])) or 0), (lambda *a: 0)
+    h._call(h._attn, None)
+    assert log == [("attn", 5)]
+    h._call(h._append, 9)
+    assert log == [("attn", 5)]  # it does not use the workspace
+    h._call(h._attn, 9)
+    h._call(h._attn, 9)
+    assert log[1:] == [("on", 9), ("record", 9), ("attn", 9), ("attn", 9)]
+    capturing.append(7)
+    h._call(h._attn, 7)
+    assert log[5:] == [("on", 7), ("attn", 7)]
+    capturing.clear()
+    h._call(h._attn, 7)
+    assert log[7:] == [("on", 7), ("record", 7), ("attn", 7)]
