@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) paged_select_kernel(c
         return;
     }
     const int slice = ((len + CS - 1) / CS + 127) / 128 * 128;
-    const int r0 = min(len, rank * slice), n = min(len, r0 + slice) - r0;
+    const int r0 = min(len, rank * slice), n = min(slice, len - r0);  // r0 + slice may pass 2^31
     const float* mass = a.c.mass + (size_t)u * a.c.rows + r0;
     const int32_t* pos = a.c.pos + (size_t)u * a.c.rows + r0;
     const int recent_from = a.c.seen[s] - a.recent;

@@ -682,6 +682,49 @@ def test_evict_select(lens, heads, page, budget, sinks, recent, kind):
             assert (got[s, h, len(want):] == -7).all()
 
 
+LONGEST = (43696, 49146)  # page size and pages of 2^31 - 32 rows, the last multiple of 16 that a cache takes
+
+
+def longest_cache(rows_held, mass, pos, **kw):
+    """One unit of 2^31 - 32 rows, every page of which is the same one."""
+    page, width = LONGEST
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    K, V = torch.randn(2, 1, 1, page, D, generator=gen, device="cuda").to(torch.bfloat16)
+    lens = torch.tensor([rows_held], dtype=torch.int32, device="cuda")
+    return ckv.PagedCache(K, V, torch.zeros(1, width, dtype=torch.int32, device="cuda"), lens, mass=mass, pos=pos,
+                          seen=lens.clone(), dev_err=torch.zeros(1, dtype=torch.int32, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("short", [0, 1, 900])
+def test_evict_select_of_the_longest_cache(short):
+    """2^31 - 32 rows, the last CTA's slice of which ends within 2^10 of 2^31:
+    planted rows, protected rows and, all others being equal, the lowest."""
+    R, budget, sinks, recent = LONGEST[0] * LONGEST[1], 1000, 16, 50
+    assert R == 2 ** 31 - 32
+    n = R - short
+    rng = np.random.default_rng(short)
+    planted = np.unique(np.concatenate([rng.integers(0, n, 600), n - 1 - rng.integers(0, 4000, 150),
+                                        rng.integers(0, 1500, 100)]))
+    mass = torch.full((1, 1, R), 0.5, device="cuda")
+    mass[0, 0, torch.tensor(planted, device="cuda")] = 1 + torch.rand(len(planted), device="cuda")
+    mass[0, 0, n:] = 9.0  # not held
+    pos = torch.arange(R, dtype=torch.int32, device="cuda").view(1, 1, R)
+    cache = longest_cache(n, mass, pos)
+    moves = torch.full((1, 1, budget, 2), -7, dtype=torch.int32, device="cuda")
+    n_moves = torch.full((1, 1), -7, dtype=torch.int32, device="cuda")
+    cache.evict_select(budget, sinks, recent, moves, n_moves)
+    kept = set(planted.tolist()) | set(range(sinks)) | set(range(n - recent, n))
+    row = 0
+    while len(kept) < budget:
+        kept.add(row)
+        row += 1
+    movers = sorted(r for r in kept if r >= budget)
+    holes = [r for r in range(budget) if r not in kept]
+    assert int(cache.dev_err) == 0 and int(n_moves) == len(movers) == len(holes)
+    assert moves[0, 0, :len(movers)].tolist() == [list(x) for x in zip(movers, holes)]
+    assert (moves[0, 0, len(movers):] == -7).all()
+
+
 @pytest.mark.parametrize("dtype,layout,page,heads", [("bf16", "hpd", 16, 2), ("f32", "phd", 48, 3),
                                                      ("bf16", "kv_in_page", 64, 1), ("f32", "wide", 16, 2)])
 def test_evict_apply(dtype, layout, page, heads):
