@@ -887,13 +887,14 @@ __device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, co
     *reinterpret_cast<float4*>(dst + j * D + 4 * lane) = o;
 }
 
-// mass_in of the four rows from r on, if one of them is below r1
-__device__ __forceinline__ float4 old_weights(const AttnArgs& a, int u, int r, int r1) {
+// mass_in of the four rows from r on, if one of them is below r1 (r is unsigned:
+// it goes past the last row, which may be just below 2^31)
+__device__ __forceinline__ float4 old_weights(const AttnArgs& a, int u, unsigned r, unsigned r1) {
     return a.mass_in && r < r1 ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 // mass_out = v + sum_j e^{s_j - lse_j} for those of the four rows that are below r1
-__device__ __forceinline__ void add_weights(const AttnArgs& a, int u, int r, int r1, float4 v) {
+__device__ __forceinline__ void add_weights(const AttnArgs& a, int u, unsigned r, unsigned r1, float4 v) {
     const float* lse2 = a.lse2 + (size_t)u * a.g;
     const float* sc = a.scores + (size_t)u * a.g * a.c.rows + r;
     const size_t o = (size_t)u * a.c.rows + r;
@@ -1212,14 +1213,15 @@ __global__ void __launch_bounds__(WARPS * 32) paged_weights_kernel(const __grid_
     if (t < t1) {
         p = advance<TR>(a.c, walk<TR>(a.c, start[warp].x, start[warp].y), t - deal.begin_warp(cta * NW + warp));
         len = rows_held(a.c, p.s);
-        next = old_weights(a, p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
+        next = old_weights(a, p.s * a.c.heads + p.h, (unsigned)p.k * TR + 4 * lane,
+                           min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
     }
     ptx::grid_dependency_wait();
     while (t < t1) {
         const int u = p.s * a.c.heads + p.h;
         const int n = min(p.nt - p.k, t1 - t);  // tiles of this unit
-        const int r1 = min(len, (p.k + n) * TR);
-        for (int r = p.k * TR + 4 * lane; r < r1; r += 128) {
+        const unsigned r1 = min(len, (p.k + n) * TR);
+        for (unsigned r = (unsigned)p.k * TR + 4 * lane; r < r1; r += 128) {
             const float4 old = next;
             next = old_weights(a, u, r + 128, r1);
             add_weights(a, u, r, r1, old);
@@ -1228,7 +1230,8 @@ __global__ void __launch_bounds__(WARPS * 32) paged_weights_kernel(const __grid_
         p = advance<TR>(a.c, p, n);
         if (t < t1) {
             len = rows_held(a.c, p.s);
-            next = old_weights(a, p.s * a.c.heads + p.h, p.k * TR + 4 * lane, min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
+            next = old_weights(a, p.s * a.c.heads + p.h, (unsigned)p.k * TR + 4 * lane,
+                               min(len, (p.k + min(p.nt - p.k, t1 - t)) * TR));
         }
     }
 }

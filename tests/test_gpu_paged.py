@@ -725,6 +725,43 @@ def test_evict_select_of_the_longest_cache(short):
     assert (moves[0, 0, len(movers):] == -7).all()
 
 
+@pytest.mark.parametrize("short", [0, 5])
+def test_attention_and_weights_of_the_longest_cache(short):
+    """2^31 - 32 rows in 49146 pages that are all the same one: a row's weight
+    is that of its slot, and the output that of one page, but for the last rows
+    (relative bounds as above: n / 16 + 200 steps, of which a warp takes 2^17
+    and the joining some hundred, |s| below 8)."""
+    page, width = LONGEST
+    R = page * width
+    n = R - short
+    mass = torch.full((1, 1, R), 2.0 ** -31, device="cuda")
+    cache = longest_cache(n, mass, None, g=2)
+    q = torch.randn(1, 2, D, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(torch.bfloat16)
+    out, lse = torch.zeros(1, 2, D, device="cuda"), torch.zeros(1, 2, device="cuda")
+    cache.decode_attn(q, out, lse=lse, mass_in=mass, mass_out=mass)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err) == 0
+    k, v = cache.K[0, 0].double(), cache.V[0, 0].double()
+    s = q[0].double() @ k.T / math.sqrt(D)
+    times = torch.full((page,), float(width), dtype=torch.float64, device="cuda")
+    times[page - short:] -= 1
+    e = torch.exp(s) * times
+    z = torch.log(e.sum(1))
+    eps = 2.0 ** -23 * (2 ** 17 + 1000) + 2.0 ** -14
+    assert ((lse[0].double() - z).abs() <= eps).all()
+    p = e / e.sum(1, keepdim=True)
+    assert ((out[0].double() - p @ v).abs() <= 2 * eps * (p @ v.abs())).all()
+    want = 2.0 ** -31 + torch.exp(s - z[:, None]).sum(0)
+    got = mass[0, 0].view(width, page)
+    for i in range(0, width, 4096):
+        held = torch.ones(min(4096, width - i), page, dtype=torch.bool, device="cuda")
+        if i + 4096 >= width and short:
+            held[-1, page - short:] = False
+        part = got[i:i + 4096].double()
+        assert ((part - want).abs() <= 2 * eps * want)[held].all()
+        assert (part[~held] == 2.0 ** -31).all()
+
+
 @pytest.mark.parametrize("dtype,layout,page,heads", [("bf16", "hpd", 16, 2), ("f32", "phd", 48, 3),
                                                      ("bf16", "kv_in_page", 64, 1), ("f32", "wide", 16, 2)])
 def test_evict_apply(dtype, layout, page, heads):
