@@ -458,7 +458,8 @@ ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, in
  * ranges is skipped (CKV_DEV_BAD_INDEX), n_moves outside [0, max_moves] is
  * clamped (CKV_DEV_BAD_COUNT).
  * Errors: as above; CKV_ERR_ARG (budget < 1, sinks, recent or max_moves < 0,
- * sinks + recent > budget), CKV_ERR_CAPACITY (max_moves too small). */
+ * max_moves > 2^30, sinks + recent > budget), CKV_ERR_CAPACITY (max_moves too
+ * small). */
 ckv_status ckv_paged_evict_select(const ckv_paged_cache* cache, int32_t budget, int32_t sinks, int32_t recent,
                                   int32_t max_moves, int32_t* moves, int32_t* n_moves, void* stream);
 ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, int32_t max_moves,

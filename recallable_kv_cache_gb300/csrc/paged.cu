@@ -803,7 +803,8 @@ extern "C" ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void*
 
 namespace {
 ckv_status check_evict(const Cache& c, int budget, int max_moves) {
-    if (budget < 1 || max_moves < 0) return CKV_ERR_ARG;
+    // the kernels count the words of a unit's moves in 32 bits; no eviction has more than 2^30 - 16
+    if (budget < 1 || max_moves < 0 || max_moves > 1 << 30) return CKV_ERR_ARG;
     const int most = budget < c.rows - budget ? budget : c.rows - budget;  // negative if nothing can be over budget
     return max_moves < most ? CKV_ERR_CAPACITY : CKV_OK;
 }
@@ -861,8 +862,7 @@ extern "C" ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_
     a.by_warps = FastDiv((uint32_t)warps);
     a.units = (int)units;
     const long long blocks = (warps * units + APPLY_THREADS / 32 - 1) / (APPLY_THREADS / 32);
-    if (blocks * (APPLY_THREADS / 32) > 0x7fffffffLL || (long long)max_moves + warps * BATCH > 0x7fffffffLL)
-        return CKV_ERR_ARG;
+    if (blocks * (APPLY_THREADS / 32) > 0x7fffffffLL) return CKV_ERR_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     const dim3 grid((unsigned)blocks), block(APPLY_THREADS);
     const cudaError_t e = vpr == 16 ? launch_dependent(paged_apply_kernel<16>, grid, block, 0, s, a)

@@ -197,6 +197,14 @@ def test_eviction_refusals(lib):
         assert select(ref=ctypes.addressof(c2)) == ARG
 
 
+@pytest.mark.parametrize("most", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_eviction_refuses_more_moves_than_words_are_counted(lib, most):
+    c = struct()
+    r = ctypes.addressof(c)
+    assert lib.ckv_paged_evict_select(r, 64, 16, 16, most, P, P, None) == ARG
+    assert lib.ckv_paged_evict_apply(r, 64, most, P, P, None) == ARG
+
+
 def test_struct_matches_header():
     import os
     import re
