@@ -439,6 +439,16 @@ ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, in
                                  int32_t g, float scale, float* out, float* lse, const float* mass_in,
                                  float* mass_out, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* The limit of ckv_paged_decode_attn's waits for its copies (see
+ * ckv_set_wait_limit; there is no context here, so it holds for this process's
+ * later launches, and a captured launch keeps the one of its capture).  A warp
+ * that gives up records CKV_DEV_TIMEOUT in the cache's dev_err, waits once more
+ * for the copies it has in flight, and leaves the rest of its rows out: that
+ * call's outputs are not valid, the workspace is as after any call.  stall = 1
+ * makes every other warp leave out its first copy, so that its wait runs out;
+ * this exists to test failure detection.  Errors: CKV_ERR_ARG. */
+ckv_status ckv_paged_set_wait_limit(int64_t cycles, int32_t stall);
+
 /* Eviction by accumulated attention weight, in two calls.  _select chooses: of
  * every (s, h) with lens[s] > budget it keeps `budget` rows, first those with
  * pos < sinks or pos >= seen[s] - recent, then by mass descending (NaN lowest,

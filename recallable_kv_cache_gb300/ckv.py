@@ -50,6 +50,7 @@ SIGNATURES = {
     "ckv_paged_append": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _P], _I),
     "ckv_paged_attn_workspace": ([_P, _I, _I, ctypes.POINTER(ctypes.c_int64)], _I),
     "ckv_paged_decode_attn": ([_P, _P, _I, _P, _I, _F, _P, _P, _P, _P, _P, ctypes.c_int64, _P], _I),
+    "ckv_paged_set_wait_limit": ([ctypes.c_int64, _I], _I),
     "ckv_paged_evict_select": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
     "ckv_paged_evict_apply": ([_P, _I, _I, _P, _P, _P], _I),
     "ckv_sparse_decode_attn_noalloc": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
@@ -357,6 +358,12 @@ def append_kv(k_src, v_src, K, V, pos: int, n: int | None = None, stream=None):
         n = k_src.shape[1] if n is None else n
     _check(lib().ckv_append_kv(ptr(k_src), ptr(v_src), src_len, _dtype_code(K), units, max_len, pos, n, ptr(K),
                                ptr(V), _stream(stream)), "ckv_append_kv")
+
+
+def paged_set_wait_limit(cycles: int = 2_000_000_000, stall: bool = False):
+    """Bounded-wait limit of the paged attention in this process, and its
+    failure detection test switch (see ckv_paged_set_wait_limit)."""
+    _check(lib().ckv_paged_set_wait_limit(int(cycles), 1 if stall else 0), "ckv_paged_set_wait_limit")
 
 
 class PagedCache:

@@ -66,6 +66,7 @@ struct AttnArgs {
     float* scores;      // [units][g][rows], base 2
     int fuse;           // every unit has a CTA to itself, which adds its weights
     long long wait_limit;
+    int stall;  // failure detection test: odd warps do not ask for their first tile
 };
 
 // A partial: O [g][D], then the maxima [g], then the sums [g]; a multiple of
@@ -1011,7 +1012,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             }
             if (lane == t - block) {
                 meta[warp][st] = make_int4(p.s * a.c.heads + p.h, p_rows, p.k, p.nt);
-                if (dead) return;
+                if (dead || (a.stall && (warp & 1) && t == t_begin)) return;
                 if (p_rows > 0) {
                     ptx::mbar_arrive_expect_tx(&full[warp][st], STAGE);
                     E::load(ring + st * STAGE, &tk, &tv, p_page, p.h, p_slot, &full[warp][st]);
@@ -1049,13 +1050,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 if (__any_sync(FULL, dead) && !gave_up) {
                     dead = gave_up = true;
                     if (lane == 0) report(a.c.dev_err, CKV_DEV_TIMEOUT);
-                    // the copies in flight get their time
-                    for (int i = 1, s2 = st, p2 = parity; i < NST && t + i < t_end; ++i) {
+                    // the copies in flight get their time, the late one too:
+                    // the rings are used for partials after this
+                    for (int i = 0, s2 = st, p2 = parity; i < NST && t + i < t_end; ++i) {
+                        ptx::mbar_wait(&full[warp][s2], p2, a.wait_limit, nullptr);
                         if (++s2 == NST) {
                             s2 = 0;
                             p2 ^= 1;
                         }
-                        ptx::mbar_wait(&full[warp][s2], p2, a.wait_limit, nullptr);
                     }
                 }
                 const int4 m = meta[warp][st];
@@ -1329,6 +1331,19 @@ cudaError_t launch(const AttnArgs& a, int sms, int dev, cudaStream_t s) {
 using namespace ckv;
 using namespace ckv::paged;
 
+namespace {
+std::atomic<long long> wait_limit{WAIT_LIMIT};
+std::atomic<int> stall_switch{0};
+}  // namespace
+
+extern "C" ckv_status ckv_paged_set_wait_limit(int64_t cycles, int32_t stall) {
+    CKV_TRACE("ckv_paged_set_wait_limit");
+    if (cycles < 1 || cycles > MAX_WAIT_LIMIT || (stall != 0 && stall != 1)) return CKV_ERR_ARG;
+    wait_limit.store(cycles, std::memory_order_relaxed);
+    stall_switch.store(stall, std::memory_order_relaxed);
+    return CKV_OK;
+}
+
 extern "C" ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int32_t with_mass,
                                                int64_t* bytes) {
     Cache c;
@@ -1376,7 +1391,8 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
     a.scores = mass_out ? reinterpret_cast<float*>(w + l.scores) : nullptr;
     a.fuse = 0;
-    a.wait_limit = WAIT_LIMIT;
+    a.wait_limit = wait_limit.load(std::memory_order_relaxed);
+    a.stall = stall_switch.load(std::memory_order_relaxed);
     int dev = 0;
     const int grid = sm_count(&dev);
     if (grid < 1) return CKV_ERR_CUDA;

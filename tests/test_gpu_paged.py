@@ -359,6 +359,32 @@ def test_offsets_past_32_bits(dtype):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("lens,heads", [([900, 64, 2500, 0, 33], 4), ([20, 300, 0, 129], 2), ([9000], 1), ([8], 1)])
+@pytest.mark.parametrize("dtype,g", [("bf16", 4), ("bf16", 16), ("f32", 2), ("f32", 8), ("f32", 12)])
+def test_a_wait_that_runs_out_is_reported(lens, heads, dtype, g):
+    """Every other warp leaves out its first copy and gives up waiting for it
+    after about a millisecond, in units of a CTA's own and in units that CTAs
+    share: the error word says so, the arrival counters are zero again, and the
+    next call on the handle is right."""
+    c = Case(lens, heads, g, 16, dtype)
+    mass = torch.zeros_like(c.mass)
+    ckv.paged_set_wait_limit(2_000_000, stall=True)
+    try:
+        c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=mass)
+        torch.cuda.synchronize()
+    finally:
+        ckv.paged_set_wait_limit()
+    stalled = max(lens) * heads * len(lens) > 16  # one tile: one warp, and it is not an odd one
+    assert int(c.err) == (1 if stalled else 0)
+    assert not c.handle.workspace[:1024].any()
+    c.err.zero_()
+    mass.zero_()
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=mass)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0 and not c.handle.workspace[:1024].any()
+    c.check_attention(mass_out=mass, mass_before=np.zeros(mass.shape))
+
+
 def test_results_do_not_change_from_run_to_run():
     c = Case([3000, 1, 0, 777, 2048], 3, 5, 16, "bf16")
     first = None

@@ -205,6 +205,12 @@ def test_eviction_refuses_more_moves_than_words_are_counted(lib, most):
     assert lib.ckv_paged_evict_apply(r, 64, most, P, P, None) == ARG
 
 
+def test_wait_limit_refusals(lib):
+    for cycles, stall in ((0, 0), (-1, 0), (4_000_000_001, 0), (1000, 2), (1000, -1)):
+        assert lib.ckv_paged_set_wait_limit(cycles, stall) == ARG
+    assert lib.ckv_paged_set_wait_limit(2_000_000_000, 0) == 0
+
+
 def test_struct_matches_header():
     import os
     import re
