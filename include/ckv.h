@@ -396,8 +396,9 @@ typedef struct {
  * stride[1] + j * stride[2] elements; strides multiples of 16 bytes), pos :=
  * p0 + j, mass := 0.  r0 is start[s], or lens[s] when start is NULL, p0 is
  * first[s], or seen[s] when first is NULL; then lens[s] := r0 + counts[s] and
- * seen[s] := p0 + counts[s].  A sequence whose r0 or count is negative, whose
- * count is above n or that would pass R is left as it is (CKV_DEV_BAD_COUNT).
+ * seen[s] := p0 + counts[s].  A sequence whose r0, p0 or count is negative,
+ * whose count is above n, that would pass R or whose positions would pass
+ * 2^31 - 1 is left as it is (CKV_DEV_BAD_COUNT).
  * The sources may be mapped pinned host memory; they must not overlap the rows
  * written.  counts, start and first may each be lens or seen themselves (the
  * values from before the call count).

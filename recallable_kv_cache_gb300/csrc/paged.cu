@@ -113,6 +113,7 @@ __device__ __forceinline__ int append_plan(const AppendArgs& a, int s, int* r0, 
     *p0 = a.first ? a.first[s] : (a.c.seen ? a.c.seen[s] : 0);
     const int cnt = a.counts ? a.counts[s] : a.n;
     if (*r0 < 0 || cnt < 0 || cnt > a.n || (long long)*r0 + cnt > a.c.rows) return -1;
+    if (a.c.seen && (*p0 < 0 || (long long)*p0 + cnt > 0x7fffffffLL)) return -1;
     return cnt;
 }
 __device__ __forceinline__ void append_advance(const AppendArgs& a, int s, int r0, int p0, int cnt) {

@@ -621,6 +621,28 @@ def test_append_bad_counts_and_pages():
     assert torch.equal(c.K, before)
 
 
+@pytest.mark.parametrize("given", [False, True])
+def test_append_of_positions_past_the_largest(given):
+    """A sequence whose positions would pass 2^31 - 1, or that starts below 0,
+    is left as it is; one that ends there is not."""
+    c = Case([64] * 4, 2, 1, 16, "bf16", garbage=0.0)
+    c.lens.zero_()
+    first = torch.tensor([2 ** 31 - 1, 2 ** 31 - 11, 2 ** 31 - 13, -1], dtype=torch.int32, device="cuda")
+    if not given:
+        c.seen.copy_(first)
+    before = {x: getattr(c, x).clone() for x in ("K", "mass", "pos", "seen")}
+    k = torch.ones(4, 2, 12, D, dtype=torch.bfloat16, device="cuda")
+    c.handle.append(k, k, first=first if given else None)
+    torch.cuda.synchronize()
+    assert int(c.err) == 3 and c.lens.tolist() == [0, 0, 12, 0]
+    before["K"][int(c.table[2, 0]), :, :12] = 1
+    before["mass"][2, :, :12] = 0
+    before["pos"][2, :, :12] = torch.arange(2 ** 31 - 13, 2 ** 31 - 1, device="cuda").int()
+    before["seen"][2] = 2 ** 31 - 1
+    for x, t in before.items():
+        assert torch.equal(getattr(c, x), t), x
+
+
 def test_append_without_row_state_and_from_pinned_memory():
     c = Case([32, 32], 2, 1, 16, "bf16", garbage=0.0)
     c.lens.zero_()
