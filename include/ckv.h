@@ -393,7 +393,8 @@ typedef struct {
 /* Appends counts[s] <= n rows (all n when counts is NULL) to every KV head of
  * every sequence: rows r0 .. r0 + counts[s] - 1 of K and V := rows 0 ..
  * counts[s] - 1 of k_src and v_src (row j of (s, h) at s * stride[0] + h *
- * stride[1] + j * stride[2] elements; strides multiples of 16 bytes), pos :=
+ * stride[1] + j * stride[2] elements; strides not negative, of extents above
+ * one multiples of 16 bytes), pos :=
  * p0 + j, mass := 0.  r0 is start[s], or lens[s] when start is NULL, p0 is
  * first[s], or seen[s] when first is NULL; then lens[s] := r0 + counts[s] and
  * seen[s] := p0 + counts[s].  A sequence whose r0, p0 or count is negative,
@@ -420,7 +421,8 @@ ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int
  *   lse = ln sum_r e^{s_r},  out = sum_r e^{s_r - lse} V_r,
  *   mass_out[s][h][r] = mass_in[s][h][r] + sum_j e^{s_r - lse_j}.
  * A sequence with no rows gives out = 0 and lse = -inf.  q: query head i of
- * sequence s at s * q_stride[0] + i * q_stride[1] elements, of kv_dtype; out
+ * sequence s at s * q_stride[0] + i * q_stride[1] elements, of kv_dtype, the
+ * strides as in ckv_paged_append; out
  * [seqs][heads * g][d] float; lse [seqs][heads * g] float or NULL; mass_out
  * [seqs][heads][R] float or NULL, mass_in the same or NULL (taken as 0), and
  * may be mass_out itself; entries of rows not held are left as they are.  fp32

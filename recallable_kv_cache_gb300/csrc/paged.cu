@@ -760,13 +760,15 @@ extern "C" ckv_status ckv_paged_append(const ckv_paged_cache* cache, const void*
     if (st != CKV_OK) return st;
     if (!k_src || !v_src || !k_src_stride || !v_src_stride || n < 1) return CKV_ERR_ARG;
     const int elem = cache->kv_dtype == CKV_BF16 ? 2 : 4;
+    const int32_t extent[3] = {cache->seqs, cache->heads, n};
     for (int i = 0; i < 3; ++i) {
         // sources are only read: a stride of 0 (one row for all) is allowed
         if (k_src_stride[i] < 0 || v_src_stride[i] < 0 || k_src_stride[i] > MAX_STRIDE ||
             v_src_stride[i] > MAX_STRIDE)
             return CKV_ERR_ARG;
-        a.kst[i] = k_src_stride[i] * elem;
-        a.vst[i] = v_src_stride[i] * elem;
+        // the stride of a single extent is never multiplied by more than 0
+        a.kst[i] = extent[i] > 1 ? k_src_stride[i] * elem : 0;
+        a.vst[i] = extent[i] > 1 ? v_src_stride[i] * elem : 0;
     }
     if (!aligned16(k_src) || !aligned16(v_src) || !strides_aligned(a.kst, 3) || !strides_aligned(a.vst, 3))
         return CKV_ERR_ALIGN;

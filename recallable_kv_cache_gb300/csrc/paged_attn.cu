@@ -1366,10 +1366,11 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     if (q_dtype != cache->kv_dtype) return CKV_ERR_DTYPE;
     if (g < 1 || g > MAX_G || !isfinite(scale) || (mass_in && !mass_out)) return CKV_ERR_ARG;
     const bool bf16 = q_dtype == CKV_BF16;
+    const long long extent[2] = {a.c.seqs, (long long)a.c.heads * g};
     for (int i = 0; i < 2; ++i) {
         if (q_stride[i] < 0 || q_stride[i] > MAX_STRIDE) return CKV_ERR_ARG;
-        if (q_stride[i] * (bf16 ? 2 : 4) & 15) return CKV_ERR_ALIGN;
-        a.qst[i] = q_stride[i];
+        a.qst[i] = extent[i] > 1 ? q_stride[i] : 0;  // a single extent is never multiplied by more than 0
+        if (a.qst[i] * (bf16 ? 2 : 4) & 15) return CKV_ERR_ALIGN;
     }
     // tile numbers are 32-bit: 2^31 tiles of fp32 rows are 17 TB of K and V
     if ((long long)a.c.seqs * a.c.heads * ceil_div(a.c.rows, 8) > 0x7fff0000LL) return CKV_ERR_ARG;

@@ -192,6 +192,25 @@ def test_scale_and_strided_queries(dtype, scale):
     c.check_attention(scale=scale)
 
 
+@pytest.mark.parametrize("dtype,S,heads,g", [("bf16", 1, 2, 3), ("f32", 1, 1, 1), ("bf16", 4, 1, 1), ("f32", 1, 1, 12)])
+def test_strides_of_single_extents_are_free(dtype, S, heads, g):
+    """One sequence, head or row: torch gives such an extent any stride."""
+    c = Case([40] * S, heads, g, 16, dtype, width=3)
+    h = heads * g
+    q = torch.empty_strided(c.q.shape, (3 if S == 1 else h * 136, 5 if h == 1 else 136, 1), dtype=DT[dtype], device="cuda")
+    q.copy_(c.q)
+    c.handle.decode_attn(q, c.out, lse=c.lse)
+    torch.cuda.synchronize()
+    c.check_attention()
+    k = torch.empty_strided((S, heads, 1, D), (7 if S == 1 else heads * 136, 9 if heads == 1 else 136, 1, 1),
+                            dtype=DT[dtype], device="cuda")
+    k.normal_()
+    c.handle.append(k, k)
+    for s in range(S):
+        assert torch.equal(c.K[int(c.table[s, 2]), :, 8], k[s, :, 0])
+    assert int(c.err) == 0 and c.lens.tolist() == [41] * S
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_peaked_and_far_scores(dtype):
     """Scores up to several hundred: the running maximum carries the sum."""
