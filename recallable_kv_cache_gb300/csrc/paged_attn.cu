@@ -1364,7 +1364,7 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     if (st != CKV_OK) return st;
     if (!q || !q_stride || !out || !workspace) return CKV_ERR_ARG;
     if (q_dtype != cache->kv_dtype) return CKV_ERR_DTYPE;
-    if (g < 1 || g > MAX_G || !isfinite(scale) || (mass_in && !mass_out)) return CKV_ERR_ARG;
+    if (g < 1 || g > MAX_G || !isfinite(scale * LOG2E) || (mass_in && !mass_out)) return CKV_ERR_ARG;
     const bool bf16 = q_dtype == CKV_BF16;
     const long long extent[2] = {a.c.seqs, (long long)a.c.heads * g};
     for (int i = 0; i < 2; ++i) {

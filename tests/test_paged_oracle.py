@@ -205,6 +205,13 @@ def test_eviction_refuses_more_moves_than_words_are_counted(lib, most):
     assert lib.ckv_paged_evict_apply(r, 64, most, P, P, None) == ARG
 
 
+@pytest.mark.parametrize("scale", [3e38, -2.4e38])
+def test_attention_refuses_scales_whose_base_2_form_is_infinite(lib, scale):
+    c = struct()
+    assert lib.ckv_paged_decode_attn(ctypes.addressof(c), P, ckv.BF16, i64(1024, 128), 4, scale, P, P, None, None, P,
+                                     1 << 40, None) == ARG
+
+
 def test_wait_limit_refusals(lib):
     for cycles, stall in ((0, 0), (-1, 0), (4_000_000_001, 0), (1000, 2), (1000, -1)):
         assert lib.ckv_paged_set_wait_limit(cycles, stall) == ARG
