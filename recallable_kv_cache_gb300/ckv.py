@@ -360,6 +360,15 @@ def append_kv(k_src, v_src, K, V, pos: int, n: int | None = None, stream=None):
                                ptr(V), _stream(stream)), "ckv_append_kv")
 
 
+def _raw_calls(torch):
+    """(raw current stream of a device, current device): torch's own raw calls,
+    as making a Stream object takes longer than a launch (3 us a call), or the
+    public ones in a build that lacks those."""
+    return (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            or (lambda index: torch.cuda.current_stream(index).cuda_stream),
+            getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
+
+
 def paged_set_wait_limit(cycles: int = 2_000_000_000, stall: bool = False):
     """Bounded-wait limit of the paged attention in this process, and its
     failure detection test switch (see ckv_paged_set_wait_limit)."""
@@ -422,8 +431,7 @@ class PagedCache:
         self._append, self._attn = so.ckv_paged_append, so.ckv_paged_decode_attn
         self._select, self._apply = so.ckv_paged_evict_select, so.ckv_paged_evict_apply
         self._cuda, self._index = torch.cuda, self.device.index
-        # the raw calls: making a Stream object takes longer than the launch
-        self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self._raw_stream, self._current = _raw_calls(torch)
         self._stride_arrays = {}
         need = ctypes.c_int64()
         _check(so.ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),

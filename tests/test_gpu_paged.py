@@ -513,6 +513,14 @@ def test_a_slab_is_a_paged_cache(dtype, g):
     ctx.close()
 
 
+def test_raw_calls_and_public_ones_agree():
+    from types import SimpleNamespace as NS
+    raw, public = ckv._raw_calls(torch), ckv._raw_calls(NS(_C=NS(), cuda=torch.cuda))
+    for st in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(st):
+            assert raw[0](0) == public[0](0) == st.cuda_stream and raw[1]() == public[1]() == 0
+
+
 def test_side_stream_argument():
     c = Case([100, 20], 2, 4, 16, "bf16")
     st = torch.cuda.Stream()

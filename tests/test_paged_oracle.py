@@ -295,3 +295,13 @@ def test_workspace_is_recorded_once_on_every_other_stream():
     capturing.clear()
     h._call(h._attn, 7)
     assert log[7:] == [("on", 7), ("record", 7), ("attn", 7)]
+
+
+def test_raw_calls_have_public_stand_ins():
+    from types import SimpleNamespace as NS
+    cuda = NS(current_stream=lambda i: NS(cuda_stream=100 + i), current_device=lambda: 2)
+    stream, device = ckv._raw_calls(NS(_C=NS(), cuda=cuda))
+    assert stream(1) == 101 and device() == 2
+    own = NS(_cuda_getCurrentRawStream=lambda i: 7, _cuda_getDevice=lambda: 3)
+    stream, device = ckv._raw_calls(NS(_C=own, cuda=cuda))
+    assert stream(1) == 7 and device() == 3
