@@ -309,6 +309,36 @@ def test_bad_pages_and_lengths_are_reported(dtype):
     c.check_attention()
 
 
+@pytest.mark.parametrize("lens,width", [([100, 64, 300], 24), ([5000, 64, 7000], 440)])
+@pytest.mark.parametrize("dtype,g", [("bf16", 4), ("bf16", 16), ("f32", 2), ("f32", 7), ("f32", 12)])
+@pytest.mark.parametrize("bad", ["some", "all of one", "all"])
+def test_bad_pages_with_weights(lens, width, dtype, g, bad):
+    """Rows of bad pages weigh nothing, and a unit that has no others leaves its
+    weights as they were: in the attention kernel (short capacity), in the kernel
+    behind it and through the merge across CTAs, on a workspace that still has
+    the scores of a call with good pages."""
+    c = Case(lens, 2, g, 16, dtype, width=width)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=torch.zeros_like(c.mass))
+    pages = [-(-n // 16) for n in lens]
+    if bad == "some":
+        for s, n in enumerate(pages):
+            c.table[s, :n:3] = -1
+            c.table[s, n // 2] = c.n_pages
+    else:
+        for s in [0] if bad == "all of one" else [0, 1, 2]:
+            c.table[s, :pages[s]] = -7
+    before = c.mass.clone()
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_in=c.mass, mass_out=c.mass)
+    torch.cuda.synchronize()
+    assert int(c.err) == 2
+    host = before.double().cpu().numpy()
+    c.check_attention(mass_in=host, mass_out=c.mass, mass_before=host)
+    for s, n in enumerate(lens):
+        ok = torch.tensor(c.rows(s, 0)[2])
+        assert torch.equal(c.mass[s, :, :n].cpu()[:, ~ok], before[s, :, :n].cpu()[:, ~ok])
+        assert ok.any() == (bad == "some" or (bad == "all of one" and s != 0))
+
+
 @pytest.mark.parametrize("dtype,n,heads,g,page", [("bf16", 70001, 2, 4, 64), ("f32", 30011, 1, 7, 16),
                                                   ("bf16", 131071, 1, 16, 128), ("f32", 20003, 2, 12, 32)])
 def test_long_sequences(dtype, n, heads, g, page):
@@ -634,6 +664,28 @@ def test_append_with_lens_and_seen_as_other_arguments(dtype, n, heads, start, fi
     assert c.seen.tolist() == [int(a) + b for a, b in zip(old[first], cnt)]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_far_into_the_pools_leaves_the_rest_alone(dtype):
+    """Rows past 2^32 bytes into the pools: every other row of the page written,
+    of its neighbours and of the sequence's other pages stays as it was."""
+    heads, page, n_pages = 8, 128, 20000
+    K = torch.empty(n_pages, heads, page, D, dtype=DT[dtype], device="cuda")
+    V = torch.empty_like(K)
+    ids = torch.tensor([[19999, 3, 19998, 16500]], dtype=torch.int32, device="cuda")
+    near = [0, 1, 2, 3, 4, 16499, 16500, 16501, 19997, 19998, 19999]
+    for pool in (K, V):
+        for p in near:
+            pool[p].normal_()
+    lens = torch.tensor([400], dtype=torch.int32, device="cuda")
+    want = [pool[near].clone() for pool in (K, V)]
+    new = torch.randn(2, 1, heads, 100, D, device="cuda").to(DT[dtype])
+    for w, x in zip(want, new):
+        w[near.index(16500), :, 16:116] = x[0]
+    ckv.PagedCache(K, V, ids, lens).append(new[0], new[1])
+    assert int(lens) == 500
+    assert all(torch.equal(pool[near], w) for pool, w in zip((K, V), want))
+
+
 def test_append_bad_counts_and_pages():
     c = Case([64] * 4, 2, 1, 16, "bf16", garbage=0.0)
     c.lens.copy_(torch.tensor([-1, 0, 0, 8]))
@@ -754,6 +806,46 @@ def test_evict_select(lens, heads, page, budget, sinks, recent, kind):
             want = po.moves(kept, budget)
             assert n_got[s, h] == len(want)
             assert np.array_equal(got[s, h, :len(want)], want)
+            assert (got[s, h, len(want):] == -7).all()
+
+
+@pytest.mark.parametrize("kind", ["plain", "equal", "odd"])
+@pytest.mark.parametrize("lens,heads,page,budget,sinks,recent,rows", [
+    ([1344, 1025, 1024, 3], 2, 16, 1024, 16, 256, 33792),
+    ([1344, 1025, 1024, 3], 2, 16, 1024, 16, 256, 131072),
+    ([1344] * 40, 8, 16, 1024, 16, 256, 33792),
+    ([70, 5000, 0, 41], 1, 64, 40, 4, 8, 131072),
+    ([129, 128, 4097], 3, 48, 127, 0, 3, 48 * 1000),
+    ([1344, 20000, 60], 1, 16, 50, 16, 20, 400000),
+])
+def test_evict_select_in_caches_wider_than_their_sequences(lens, heads, page, budget, sinks, recent, rows, kind):
+    """Capacities that give a unit more CTAs, and longer ones, than its rows
+    need; what is not held is NaN and must not count."""
+    gen = torch.Generator().manual_seed(budget)
+    S, width, most = len(lens), rows // page, min(budget, rows - budget)
+    K = torch.zeros(1, heads, page, D, dtype=torch.bfloat16, device="cuda")
+    longest = max(lens)
+    few = weights(kind, S, heads, longest, gen)
+    mass = torch.full((S, heads, rows), float("nan"), device="cuda")
+    pos = torch.zeros(S, heads, rows, dtype=torch.int32, device="cuda")  # of rows not held: protected, if they counted
+    held_pos = torch.stack([torch.randperm(longest, generator=gen).int() for _ in range(S * heads)]).view(S, heads, -1)
+    mass[:, :, :longest], pos[:, :, :longest] = few.cuda(), held_pos.cuda()
+    for s, n in enumerate(lens):
+        mass[s, :, n:], pos[s, :, n:] = float("nan"), 0
+    moves = torch.full((S, heads, most, 2), -7, dtype=torch.int32, device="cuda")
+    n_moves = torch.full((S, heads), -7, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = ckv.PagedCache(K, K.clone(), torch.zeros(S, width, dtype=torch.int32, device="cuda"),
+                           torch.tensor(lens, dtype=torch.int32, device="cuda"), mass=mass, pos=pos,
+                           seen=torch.full((S,), longest, dtype=torch.int32, device="cuda"), dev_err=err)
+    cache.evict_select(budget, sinks, recent, moves, n_moves)
+    got, n_got = moves.cpu().numpy(), n_moves.cpu().numpy()
+    assert int(err) == 0
+    for s, n in enumerate(lens):
+        for h in range(heads):
+            kept = po.keep(few[s, h, :n].numpy(), held_pos[s, h, :n].numpy(), longest, budget, sinks, recent)
+            want = po.moves(kept, budget)
+            assert n_got[s, h] == len(want) and np.array_equal(got[s, h, :len(want)], want)
             assert (got[s, h, len(want):] == -7).all()
 
 
@@ -983,6 +1075,104 @@ def test_decode_loop_with_eviction(dtype, heads, g, page, captured):
     assert int(err) == 0
     # the weights of a row sum to g per step over the rows held
     assert (mass >= 0).all()
+
+
+@pytest.mark.parametrize("dtype,heads,g,page,prompt,budget,rows", [
+    ("bf16", 2, 4, 16, [45, 1, 70], 40, 96), ("f32", 3, 2, 32, [45, 1, 70], 40, 96), ("f32", 1, 12, 16, [45, 1, 70], 40, 96),
+    ("bf16", 2, 4, 16, [700, 300, 1], 250, 1024), ("f32", 1, 8, 64, [700, 300, 1], 250, 1024)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_accumulated_weights_follow_their_tokens(dtype, heads, g, page, prompt, budget, rows, captured):
+    """The weight of every token held, added up on the host from the oracle's
+    weights step by step, against the cache's: over appends (a new row starts
+    from zero, also in a slot that an evicted row had), attention in place, in
+    the attention kernel and behind it, and evictions (a weight moves with its
+    row).  A step is off by eps times what it adds (the bounds at the top of
+    this file) and rounds the sum to half a unit in the last place."""
+    gen = torch.Generator().manual_seed(11)
+    S, every, steps, sinks, recent, dev = len(prompt), 6, 20, 4, 8, "cuda"
+    width = rows // page
+    tokens = max(prompt) + steps
+    tk, tv = (torch.randn(S, tokens, heads, D, generator=gen).to(DT[dtype]) for _ in range(2))
+    qs = (1.5 * torch.randn(steps, S, heads * g, D, generator=gen)).to(DT[dtype])
+    K = torch.full((S * width, heads, page, D), float("nan"), dtype=DT[dtype], device=dev)
+    V = K.clone()
+    table = torch.randperm(S * width, generator=gen).to(torch.int32).view(S, width).to(dev)
+    lens, seen = (torch.zeros(S, dtype=torch.int32, device=dev) for _ in range(2))
+    mass = torch.full((S, heads, rows), 99.0, device=dev)
+    pos, err = torch.zeros(S, heads, rows, dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    cache = ckv.PagedCache(K, V, table, lens, g=g, mass=mass, pos=pos, seen=seen, dev_err=err)
+    moves = torch.zeros(S, heads, budget, 2, dtype=torch.int32, device=dev)
+    n_moves = torch.zeros(S, heads, dtype=torch.int32, device=dev)
+    q, out = qs[0].to(dev), torch.zeros(S, heads * g, D, device=dev)
+    k1, v1 = (torch.zeros(S, heads, 1, D, dtype=DT[dtype], device=dev) for _ in range(2))
+
+    def step():
+        cache.append(k1, v1)
+        cache.decode_attn(q, out, mass_in=mass, mass_out=mass)
+
+    def evict():
+        cache.evict(budget, sinks, recent, moves, n_moves)
+
+    run_step, run_evict = step, evict
+    if captured:  # nothing runs while it is captured
+        graphs = []
+        for fn in (step, evict):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                fn()
+            graphs.append(graph)
+        run_step, run_evict = graphs[0].replay, graphs[1].replay
+    longest = max(prompt)
+    cache.append(tk[:, :longest].transpose(1, 2).to(dev), tv[:, :longest].transpose(1, 2).to(dev),
+                 counts=torch.tensor(prompt, dtype=torch.int32, device=dev))
+    held = [[list(range(n)) for _ in range(heads)] for n in prompt]  # token in each row
+    want, off = np.zeros((S, heads, tokens)), np.zeros((S, heads, tokens))  # weight of a token, and its bound
+    for i in range(steps):
+        k1.copy_(torch.stack([tk[s, n + i] for s, n in enumerate(prompt)]).unsqueeze(2))
+        v1.copy_(torch.stack([tv[s, n + i] for s, n in enumerate(prompt)]).unsqueeze(2))
+        q.copy_(qs[i])
+        run_step()
+        got = mass.double().cpu().numpy()
+        for s in range(S):
+            for h in range(heads):
+                at = held[s][h]
+                at.append(prompt[s] + i)
+                kk, vv = tk[s, at, h].double().numpy(), tv[s, at, h].double().numpy()
+                qq = qs[i, s, h * g:(h + 1) * g].double().numpy()
+                _, _, w = po.attend(qq, kk, vv, np.ones(len(at), dtype=bool), D ** -0.5)
+                es = 2.0 ** -16 * D ** -0.5 * (np.abs(qq) @ np.abs(kk).T).max()
+                eps = 4 * es + 2.0 ** -16 + 2 * 2.0 ** -23 * (len(at) / 16 + 200)
+                want[s, h, at] += w
+                off[s, h, at] += eps * w + 2.0 ** -24 * want[s, h, at] * (1 + eps)
+                assert abs(got[s, h, :len(at)].sum() - want[s, h, at].sum()) <= off[s, h, at].sum()
+                assert (np.abs(got[s, h, :len(at)] - want[s, h, at]) <= off[s, h, at] + 1e-30).all(), (i, s, h)
+                assert (got[s, h, max(len(at), max(prompt) + steps):] == 99.0).all()
+        if i % every == every - 1:
+            before = mass.cpu()
+            run_evict()
+            for s in range(S):
+                for h in range(heads):
+                    at = held[s][h]
+                    kept = po.keep(before[s, h, :len(at)].numpy(), np.array(at), prompt[s] + i + 1, budget, sinks, recent)
+                    for a, b in po.moves(kept, budget):
+                        at[b] = at[a]
+                    del at[budget:]
+                    assert int(lens[s]) == len(at) and pos[s, h, :len(at)].tolist() == at
+    assert int(err) == 0
+
+
+def test_weights_added_call_after_call_on_one_stream():
+    """Sixteen calls in a row that add in place, with nothing between them: each
+    reads what the one before has written, also where it looks ahead."""
+    for lens in ([900, 64, 2500, 0], [300, 1, 0, 384], [5000]):
+        c = Case(lens, 2, 3, 16, "bf16")
+        one, mass = torch.zeros_like(c.mass), torch.zeros_like(c.mass)
+        c.handle.decode_attn(c.q, c.out, mass_out=one)
+        torch.cuda.synchronize()
+        for _ in range(16):
+            c.handle.decode_attn(c.q, c.out, mass_in=mass, mass_out=mass)
+        torch.cuda.synchronize()
+        assert ((mass.double() - 16 * one.double()).abs() <= 16 * 2.0 ** -24 * 16 * one.double()).all()
 
 
 # ---------------------------------------------------------------- refusals of the binding
