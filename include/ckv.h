@@ -436,8 +436,9 @@ ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int
  * its start zero again).  Calls that can overlap on the GPU (two streams, two
  * graphs) need workspaces of their own.
  * Errors: as above; CKV_ERR_ARG (g outside [1, 16], scale times log2(e) not
- * finite, mass_in without mass_out, seqs * heads * R of 2^34 and more), CKV_ERR_CAPACITY
- * (workspace too small). */
+ * finite, mass_in without mass_out or overlapping it without being the same,
+ * seqs * heads * ceil(R / 8) above 2^31 - 2^16), CKV_ERR_CAPACITY (workspace too
+ * small). */
 ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const void* q, int32_t q_dtype, const int64_t* q_stride,
                                  int32_t g, float scale, float* out, float* lse, const float* mass_in,
                                  float* mass_out, void* workspace, int64_t workspace_bytes, void* stream);

@@ -42,13 +42,6 @@ bool strides_aligned(const long long* b, int n) {
     return true;
 }
 
-// two int32 arrays of n elements that are one and the same (an element is read
-// before it is written) or do not overlap; no array overlaps nothing
-bool same_or_apart(const int32_t* x, const int32_t* y, int n) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-    return !x || !y || a == b || (a < b ? b - a : a - b) >= (uintptr_t)n * sizeof(int32_t);
-}
-
 }  // namespace
 
 ckv_status check_cache(const ckv_paged_cache* c, Cache* o) {

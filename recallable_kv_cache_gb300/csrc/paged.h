@@ -52,6 +52,12 @@ ckv_status check_cache(const ckv_paged_cache* c, Cache* out);
 // SM count of the current device (looked up once per device); 0 on failure
 int sm_count(int* dev);
 
+// two arrays of n 32-bit elements that are one and the same (an element is read
+// before it is written) or do not overlap; no array overlaps nothing
+inline bool same_or_apart(const void* x, const void* y, long long n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return !x || !y || a == b || (a < b ? b - a : a - b) >= (uintptr_t)n * 4;
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 __device__ __forceinline__ void report(int32_t* dev_err, int code) {

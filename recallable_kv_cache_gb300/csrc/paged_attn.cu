@@ -1377,6 +1377,7 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     if (!aligned16(q) || !aligned16(out) || !aligned16(mass_in) || !aligned16(mass_out) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return CKV_ERR_ALIGN;
+    if (!same_or_apart(mass_in, mass_out, (long long)a.c.seqs * a.c.heads * a.c.rows)) return CKV_ERR_ARG;
     const Layout l = layout_of(a.c, g, mass_out != nullptr);
     if (workspace_bytes < (int64_t)l.total) return CKV_ERR_CAPACITY;
     unsigned char* w = static_cast<unsigned char*>(workspace);

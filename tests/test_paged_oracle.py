@@ -212,6 +212,16 @@ def test_attention_refuses_scales_whose_base_2_form_is_infinite(lib, scale):
                                      1 << 40, None) == ARG
 
 
+def test_attention_refuses_weights_that_overlap_in_part(lib):
+    """A row's old weight would be read after another row's new one is written."""
+    c = struct()  # 3 * 2 * 256 weights
+    far = 1 << 24
+    for at in (16, 1024, 4 * 1536 - 16):
+        for x, y in ((far, far + at), (far + at, far)):
+            assert lib.ckv_paged_decode_attn(ctypes.addressof(c), P, ckv.BF16, i64(1024, 128), 4, 0.1, P, P, x, y, P,
+                                             1 << 40, None) == ARG
+
+
 def test_wait_limit_refusals(lib):
     for cycles, stall in ((0, 0), (-1, 0), (4_000_000_001, 0), (1000, 2), (1000, -1)):
         assert lib.ckv_paged_set_wait_limit(cycles, stall) == ARG
