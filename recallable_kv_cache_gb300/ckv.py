@@ -382,7 +382,10 @@ class PagedCache:
     [seqs] int32; optionally ``mass`` (float32) and ``pos`` (int32) [seqs, heads,
     max_pages * page_size], ``seen`` [seqs] int32 and ``dev_err`` [1] int32.
 
-    ``g`` is the number of query heads per KV head.  The handle keeps the
+    ``g`` is the number of query heads per KV head.  ``mass`` and ``pos`` are
+    sized by the capacity, 8 bytes for each of seqs * heads * rows, and with
+    ``mass`` so is the workspace, 4 g bytes for each (0.27 g MB without; a handle
+    made without ``mass`` takes no ``mass_out``).  The handle keeps the
     tensors alive and owns the attention's workspace, allocated here (so that
     every call may be captured into a CUDA graph; the handle itself is made
     outside a capture).  Like a Context, one handle

@@ -232,7 +232,8 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
 
 // A cluster of CS CTAs per (sequence, KV head), each with a slice of its rows.
 // One pass over mass and pos turns them into keys, kept in shared memory
-// (CACHED; longer caches read them again), and counts the keys' top 12 bits;
+// (CACHED; longer caches read them again: 32 units of 327001 rows 66 us, of
+// 400001 137 us), and counts the keys' top 12 bits;
 // the key of the budget-th row follows digit by digit from the histograms, to
 // which every CTA adds its occupied bins in all its peers' shared memory (few
 // are occupied; every CTA reading all bins of its peers took 97 us for 32
@@ -621,8 +622,9 @@ cudaError_t launch_select_cs(const SelectArgs& a, int dev, cudaStream_t s) {
 template <int CS>
 cudaError_t launch_select_rows(const SelectArgs& a, int dev, cudaStream_t s) {
     // 512 threads are quicker through their barriers, 1024 through many rows:
-    // 6.9 against 7.7 us for 256 units of 1344 rows, 28.0 against 23.8 us for
-    // 32 units of 128k rows on four CTAs each
+    // as replayed graphs, 8.8 against 12.4 us for 256 units of 1344 rows, 10.3
+    // against 9.6 for 128 of 4096, 28.7 against 22.7 for 32 of 128k on four
+    // CTAs each (10.3 against 10.2 where the limit is, at 4080 rows)
     return a.c.rows / CS < SEL_LONG ? launch_select_cs<CS, 512, true>(a, dev, s)
                                     : launch_select_cs<CS, 1024, true>(a, dev, s);
 }
@@ -631,7 +633,9 @@ cudaError_t launch_evict_select(const SelectArgs& a, int sms, int dev, cudaStrea
     const long long units = (long long)a.c.seqs * a.c.heads;
     // more CTAs per unit while each has an SM of its own and rows to work on
     // (two to an SM: 19.7 us instead of 12.2 for 128 units of 8k rows), and as
-    // many as the keys need
+    // many as the keys need.  lens is not known here, so all this goes by the
+    // capacity: 256 units of 1344 rows take 6.0 us at a capacity of 1344, 9.7
+    // at 33792 and 58 at 131072
     int cs = 1;
     while (cs < SEL_MAX_CLUSTER && (a.c.rows > cs * (long long)SEL_MAX_SLICE ||
                                     (units * cs * 2 <= sms && a.c.rows / cs >= SEL_LONG)))

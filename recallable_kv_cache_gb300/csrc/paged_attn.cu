@@ -563,8 +563,10 @@ struct TilesF32 {
 };
 
 // fp32 on the tensor cores, for more than eight heads (96 units of up to 12k
-// rows: 16 heads 155 us where the tiles above took 207; 8 heads 115 where those
-// take 100, so up to eight they are used).  Every operand is taken apart into
+// rows, before the look at the range below: 16 heads 155 us where the tiles
+// above took 207; 8 heads 115 where those take 100, so up to eight they are
+// used).  Bound by dependent arithmetic on two warps a scheduler (40 % of the
+// issue slots, the tensor pipe 40 % active).  Every operand is taken apart into
 // three bf16 terms (hi + mid + lo, which hold its 24 bits), and of the nine
 // products the six down to 2^-18 of the largest are added up, the small ones
 // first.  bf16 ends at 2^-133, so that the terms of a value below 2^-110 leave
