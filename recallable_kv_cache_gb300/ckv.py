@@ -476,7 +476,9 @@ class PagedCache:
         each: memory that is freed goes to the stream it was allocated on, after
         what is then queued on the others.  Not while the stream is capturing:
         nothing runs, and the graph's replays are its owner's."""
-        stream = self._cuda.ExternalStream(raw, device=self.device)
+        # 0 is the default stream, which is no address for ExternalStream
+        stream = (self._cuda.ExternalStream(raw, device=self.device) if raw
+                  else self._cuda.default_stream(self.device))
         with self._cuda.stream(stream):
             if self._cuda.is_current_stream_capturing():
                 return

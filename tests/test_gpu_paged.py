@@ -592,6 +592,28 @@ def test_handle_dropped_with_work_queued_on_another_stream(how):
     assert torch.equal(out, c.out) and torch.equal(mass, want)
 
 
+def test_handle_made_on_a_side_stream_and_dropped_with_work_on_the_default_one():
+    c = Case([900, 64, 2500, 0], 4, 4, 16, "bf16", width=200)
+    want = torch.zeros_like(c.mass)
+    c.handle.decode_attn(c.q, c.out, lse=c.lse, mass_out=want)
+    mass, out, side = torch.zeros_like(c.mass), torch.zeros_like(c.out), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        handle = c.make()
+    at, nbytes = handle.workspace.data_ptr(), handle.workspace.numel()
+    torch.cuda._sleep(400_000_000)  # some 0.2 s
+    handle.decode_attn(c.q, out, mass_out=mass)
+    del handle
+    with torch.cuda.stream(side):
+        others = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert not torch.cuda.default_stream().query()
+        for t in others:
+            assert not t.data_ptr() <= at < t.data_ptr() + nbytes
+            t.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(out, c.out) and torch.equal(mass, want)
+
+
 # ---------------------------------------------------------------- append
 @pytest.mark.parametrize("dtype,layout,page,heads,n", [
     ("bf16", "hpd", 16, 2, 1), ("f32", "phd", 16, 3, 1), ("bf16", "kv_in_page", 48, 8, 37), ("f32", "wide", 32, 1, 70),

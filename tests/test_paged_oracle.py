@@ -307,6 +307,29 @@ def test_workspace_is_recorded_once_on_every_other_stream():
     assert log[7:] == [("on", 7), ("record", 7), ("attn", 7)]
 
 
+def test_workspace_is_recorded_on_the_default_stream():
+    """Its address is 0, for which torch would make a stream of its own."""
+    import contextlib
+    log = []
+
+    class Cuda:
+        default_stream = staticmethod(lambda device: ("default", device))
+        stream = staticmethod(lambda st: contextlib.nullcontext())
+        is_current_stream_capturing = staticmethod(lambda: False)
+
+        @staticmethod
+        def ExternalStream(raw, device):
+            assert raw
+
+    class Workspace:
+        record_stream = staticmethod(log.append)
+
+    h = ckv.PagedCache.__new__(ckv.PagedCache)
+    h.device, h._cuda, h.workspace, h._streams = "cuda:0", Cuda, Workspace, {5}
+    h._note_stream(0)
+    assert log == [("default", "cuda:0")] and h._streams == {0, 5}
+
+
 def test_raw_calls_have_public_stand_ins():
     from types import SimpleNamespace as NS
     cuda = NS(current_stream=lambda i: NS(cuda_stream=100 + i), current_device=lambda: 2)
