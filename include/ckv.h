@@ -424,8 +424,9 @@ ckv_status ckv_paged_attn_workspace(const ckv_paged_cache* cache, int32_t g, int
  * A sequence with no rows gives out = 0 and lse = -inf.  q: query head i of
  * sequence s at s * q_stride[0] + i * q_stride[1] elements, of kv_dtype, the
  * strides as in ckv_paged_append; out [seqs][heads * g][d] float; lse
- * [seqs][heads * g] float or NULL; mass_out [seqs][heads][R] float or NULL, mass_in the same or NULL (taken as 0), and
- * may be mass_out itself; entries of rows not held are left as they are.  fp32
+ * [seqs][heads * g] float or NULL; mass_out [seqs][heads][R] float or NULL,
+ * mass_in the same or NULL (taken as 0), and may be mass_out itself; entries of
+ * rows not held are left as they are.  fp32
  * arithmetic on products of the operands as they are: sum_i |scale q_i K_ri|
  * and sum_r e^{s_r - max s} |V_r| have to stay below 2^126, and weights below
  * 2^-125 of a query head's largest may be lost.  Values of rows not held are

@@ -576,8 +576,8 @@ struct TilesF32 {
 // least value of those that are not zero, and where that is below 2^-110, or a
 // query value times the scale past 2^96, it does its tiles of the unit again in
 // plain fp32 (16 heads above: 158 us without the least value, 163 with it, 181
-// with a look at every tile's).  8 rows a tile, four quarters of 32 channels, [quarter][row][128
-// bytes], 128-byte swizzled (16-byte chunk c of row r at c ^ r).
+// with a look at every tile's).  8 rows a tile, four quarters of 32 channels,
+// [quarter][row][128 bytes], 128-byte swizzled (16-byte chunk c of row r at c ^ r).
 //   S[h][r] = q[h] . K[r]        m16n8k16: M = 16 heads, N = 8 rows
 //   O[c][h] += V[r][c] P[h][r]   m16n8k8:  M = 16 channels, N = 8 heads, K = 8 rows
 // Which channel is which k of the first product, and which m of the second, is
