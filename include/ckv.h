@@ -484,6 +484,126 @@ ckv_status ckv_paged_evict_select(const ckv_paged_cache* cache, int32_t budget, 
 ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, int32_t max_moves,
                                  const int32_t* moves, const int32_t* n_moves, void* stream);
 
+/* Pages and places for the tokens of a step, from the sequences' lengths: what
+ * a server otherwise works out on the host between two steps.  Sequence s holds
+ * held_in[s] pages (table[s][0 .. held_in[s])), has start[s] rows (lens[s] when
+ * start is NULL), brings counts[s] tokens and has seen first[s] (seen[s] when
+ * first is NULL; start[s] without seen).  Its first shared[s] <= held_in[s] pages (0
+ * when shared is NULL) belong to somebody else, such as a prefix that several
+ * sequences attend, and are never handed back.  With
+ *   need[s] = max(shared[s], ceil((start[s] + counts[s]) / page_size))
+ * a sequence takes need - held_in pages or hands held_in - need back (after an
+ * eviction, or when the caller has set its rows to 0).  Free pages stand in a
+ * ring, free_pages[(head + i) mod free_cap], i < count, (head, count) =
+ * span_in: pages are taken from its head and handed back behind its tail, both
+ * in the order of sequences and then of pages, so a page that is handed back
+ * can be taken from the next call on.  All sequences' takes are added up in
+ * order; one whose sum passes `count` is refused: it is granted no token and
+ * keeps its pages.  Then
+ *   table[s][held_in[s] ..) := the pages taken,  held_out[s] := pages held,
+ *   granted[s] := counts[s], or 0 if refused,
+ *   lens[s] := start[s] + granted[s],  seen[s] := first[s] + granted[s],
+ *   span_out := the ring's new (head, count),
+ *   starts[0 .. seqs] := 0 and the running sums of counts: tokens stand packed,
+ *     sequence after sequence (those of refused ones too),
+ *   slots[t] := (page * page_size + slot, s, row, position) of token t, four
+ *     int32 (16-byte aligned), with row = start[s] + j and position = first[s] +
+ *     j for the sequence's j-th token; four times -1 for tokens of refused
+ *     sequences and behind the last.
+ * A sequence whose start, first or count is negative, that would pass R or
+ * position 2^31 - 1, whose tokens do not fit n_slots, or with shared or held_in
+ * outside 0 <= shared <= held_in <= max_pages, is granted nothing and left as
+ * it is (CKV_DEV_BAD_COUNT; a negative count is no token in starts, which never
+ * pass n_slots).  A span outside the ring counts as empty (head 0, count 0) and
+ * pages handed back to a full ring are lost, CKV_DEV_BAD_COUNT both.  A bad
+ * page id gives no slot (CKV_DEV_BAD_INDEX).  The call
+ * writes the cache's table, lens and seen; K and V are not touched.  counts,
+ * start and first may be lens or seen themselves, held_out may be held_in and
+ * span_out span_in.  free_pages must not overlap anything else.
+ * Errors: as above; CKV_ERR_ARG (a null pointer other than start, first and
+ * shared; n_slots or free_cap < 1; n_pages * page_size above 2^31 - 1; arrays
+ * that overlap without being the same as above). */
+ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t* counts, const int32_t* start,
+                          const int32_t* first, const int32_t* shared, const int32_t* held_in, int32_t* held_out,
+                          int32_t* free_pages, int32_t free_cap, const int32_t* span_in, int32_t* span_out,
+                          int32_t* granted, int32_t* starts, int32_t* slots, int32_t n_slots, void* stream);
+
+/* Norms and rotary positions of queries and keys, in one pass over them.  A row
+ * x of d channels (one head of one token at position p) becomes
+ *   y = x * w / sqrt(mean_i x_i^2 + eps)   (w: the norm's weight; y = x without),
+ *   (y_a, y_b) := amplitude * (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * for pair i < rot / 2 of channels (a, b) = (2 i, 2 i + 1) if interleaved, else
+ * (i, i + rot / 2), where t = 2 pi p turns_i / 2^64; channels from rot on keep
+ * y.  turns is the pair's frequency as a 64-bit fraction of a turn per position,
+ * so that t is exact to 2^-32 of a turn at every position, however far (p *
+ * turns_i wraps as the angle does); scalings for long contexts are a choice of
+ * turns and amplitude.  fp32 arithmetic, rounded once at the end; sum_i x_i^2
+ * has to stay below 2^127. */
+typedef struct {
+    const uint64_t* turns; /* [rot / 2]; NULL only if rot is 0 */
+    const float* q_weight; /* [d], or NULL: queries are not normed */
+    const float* k_weight;
+    float eps;
+    float amplitude;
+    int32_t rot; /* channels rotated: 0 to 128, a multiple of 16 */
+    int32_t interleaved;
+} ckv_rotary;
+
+/* Norms and rotates q (heads_q rows a token) and k (heads_k) into q_out and
+ * k_out: head h of token t at t * stride[0] + h * stride[1] elements (strides as
+ * in ckv_paged_append; of outputs, at least d where the extent is above one).
+ * positions [tokens] int32, any value.  heads_q or heads_k may be 0 (its
+ * pointers are then not used).  q_out may be q itself and k_out k, with the
+ * same strides; outputs must not overlap an input otherwise.
+ * Errors: CKV_ERR_ARG (d != 128, tokens < 1, a negative head count or none at
+ * all, rot, eps < 0 or not finite, amplitude not finite, interleaved not 0 or 1,
+ * null pointers, strides, more than 2^31 - 2^16 rows), CKV_ERR_DTYPE,
+ * CKV_ERR_ALIGN. */
+ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const int64_t* q_stride, void* q_out,
+                      const int64_t* q_out_stride, int32_t heads_q, const void* k, const int64_t* k_stride,
+                      void* k_out, const int64_t* k_out_stride, int32_t heads_k, const int32_t* positions,
+                      int32_t tokens, int32_t d, int32_t dtype, void* stream);
+
+/* The same for a step's packed tokens, keys and values going straight into their
+ * pages: with slots [tokens][4] as ckv_paged_plan leaves them, (slot, s, row, p),
+ *   K[slot] := rotated k,  V[slot] := v,  pos[s][h][row] := p, mass[s][h][row] := 0
+ * for every KV head h, and q_out := rotated q (heads * g rows a token; g = 0: no
+ * queries).  A token with slot -1 is left out, its q_out too.  A slot outside
+ * the pools, or (where the cache has pos or mass) s or row outside the cache,
+ * leaves the token out as well (CKV_DEV_BAD_INDEX).  No two tokens may have the
+ * same slot.  lens, seen and the table are not used: the plan has set them.
+ * Errors: as above; CKV_ERR_ARG (g < 0, n_pages * page_size above 2^31 - 1). */
+ckv_status ckv_paged_append_rotated(const ckv_paged_cache* cache, const ckv_rotary* rotary, const void* q,
+                                    const int64_t* q_stride, int32_t g, void* q_out, const int64_t* q_out_stride,
+                                    const void* k, const int64_t* k_stride, const void* v, const int64_t* v_stride,
+                                    const int32_t* slots, int32_t tokens, void* stream);
+
+/* Bytes of workspace that ckv_paged_shared_attn needs for this cache with g
+ * query heads per KV head, from the extents alone. */
+ckv_status ckv_paged_shared_workspace(const ckv_paged_cache* cache, int32_t g, int64_t* bytes);
+
+/* ckv_paged_decode_attn (without weights) for a batch in which runs of
+ * sequences share their leading rows: a prompt's samples, conversations behind
+ * one instruction, questions about one document.  Sequences group_starts[i] ..
+ * group_starts[i + 1] - 1 (int32, ascending, groups + 1 of them) have their
+ * first prefix[i] rows in common: for those rows the tables of all of them name
+ * the same pages.  out and lse are what ckv_paged_decode_attn gives, up to
+ * rounding, but the common rows are read once for the group's queries (from the
+ * first member's table, rounded down to a multiple of 16) instead of once for
+ * every sequence.  Sequences outside every group, and groups of one, are
+ * attended by themselves.  prefix[i] is clamped to the first member's rows;
+ * other members need at least as many (a shorter one attends the common rows
+ * all the same, CKV_DEV_BAD_COUNT).  A start outside [0, seqs] or below an
+ * earlier one is taken as the nearest that is not, a negative prefix as 0
+ * (CKV_DEV_BAD_COUNT).  fp32 caches are attended sequence by sequence.
+ * Arguments, accuracy, workspace (zeroed before its first use, one for calls
+ * that may overlap) and errors as for ckv_paged_decode_attn; CKV_ERR_ARG also
+ * for groups < 0, or above 0 without group_starts and prefix, or above seqs. */
+ckv_status ckv_paged_shared_attn(const ckv_paged_cache* cache, const void* q, int32_t q_dtype,
+                                 const int64_t* q_stride, int32_t g, float scale, const int32_t* group_starts,
+                                 const int32_t* prefix, int32_t groups, float* out, float* lse, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+
 /* Host-side copy of the context's counters. */
 ckv_status ckv_get_info(ckv_ctx* ctx, ckv_info* info);
 

@@ -9,12 +9,16 @@ been built).
 from __future__ import annotations
 
 import ctypes
+import fractions
+import math
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libckv.so")
 
 F32, BF16 = 0, 1
+# pi to 50 decimals
+_PI = fractions.Fraction("3.14159265358979323846264338327950288419716939937511")
 DEV_ERRORS = {0: "ok", 1: "timeout", 2: "bad index", 3: "bad count", 4: "bad label", 5: "bad csr"}
 
 # Every entry point of include/ckv.h with its argument types.
@@ -53,6 +57,11 @@ SIGNATURES = {
     "ckv_paged_set_wait_limit": ([ctypes.c_int64, _I], _I),
     "ckv_paged_evict_select": ([_P, _I, _I, _I, _I, _P, _P, _P], _I),
     "ckv_paged_evict_apply": ([_P, _I, _I, _P, _P, _P], _I),
+    "ckv_paged_plan": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P], _I),
+    "ckv_rotate": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P], _I),
+    "ckv_paged_append_rotated": ([_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P], _I),
+    "ckv_paged_shared_workspace": ([_P, _I, ctypes.POINTER(ctypes.c_int64)], _I),
+    "ckv_paged_shared_attn": ([_P, _P, _I, _P, _I, _F, _P, _P, _I, _P, _P, _P, ctypes.c_int64, _P], _I),
     "ckv_sparse_decode_attn_noalloc": ([_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
 }
 
@@ -75,6 +84,12 @@ class PagedCacheStruct(ctypes.Structure):
                 + [(n, _P) for n in ("table", "lens", "mass", "pos", "seen", "dev_err")]
                 + [(n, ctypes.c_int32) for n in ("n_pages", "heads", "page_size", "seqs", "max_pages", "d",
                                                  "kv_dtype")])
+
+
+class Rotary(ctypes.Structure):
+    """ckv_rotary."""
+    _fields_ = ([(n, _P) for n in ("turns", "q_weight", "k_weight")] + [("eps", _F), ("amplitude", _F)]
+                + [("rot", _I), ("interleaved", _I)])
 
 
 class CKVError(RuntimeError):
@@ -369,6 +384,138 @@ def _raw_calls(torch):
             getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
 
 
+def rotary_turns(frequencies):
+    """The pairs' angular frequencies (radians per position, floats) as the 64-bit
+    fractions of a turn that the rotary calls take: int64 [rot / 2], on the CPU,
+    holding the bits of round(w / (2 pi) * 2^64) mod 2^64."""
+    import torch
+    tau = 2 * _PI
+    turns = []
+    for w in frequencies:
+        exact = fractions.Fraction(float(w)) / tau * 2 ** 64  # refuses infinities and NaN
+        bits = round(exact) % 2 ** 64
+        turns.append(bits - 2 ** 64 if bits >= 2 ** 63 else bits)
+    return torch.tensor(turns, dtype=torch.int64)
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original: int = 8192, low: float = 1.0, high: float = 32.0):
+    """(frequencies [rot / 2] in radians per position, amplitude) of rotary
+    positions, w_i = base^(-2 i / rot), scaled for contexts ``factor`` times the
+    ``original`` length by one of
+      "linear"  positions interpolated: w_i / factor;
+      "base"    the base raised so that the slowest pair is interpolated and the
+                fastest stays: base * factor^(rot / (rot - 2));
+      "ramp"    pairs that turn more than ``high`` times over the original length
+                stay, those that turn less than ``low`` times are interpolated,
+                and in between the share goes with their number i; the amplitude
+                is 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071);
+      "bands"   the same borders (``high`` = 4 is usual), the share going with
+                the number of turns, and an amplitude of 1."""
+    if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
+        raise ValueError(f"rot must be even and positive, base > 0 and factor >= 1, got {rot}, {base}, {factor}")
+    if scaling not in (None, "linear", "base", "ramp", "bands"):
+        raise ValueError(f"scaling must be None, linear, base, ramp or bands, got {scaling!r}")
+    half, amplitude = rot // 2, 1.0
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2)) if rot > 2 else base
+    w = [base ** (-i / half) for i in range(half)]
+    if scaling == "linear":
+        w = [x / factor for x in w]
+    elif scaling in ("ramp", "bands"):
+        if not 0 < low < high or original < 1:
+            raise ValueError(f"0 < low < high and original >= 1 are needed, got {low}, {high}, {original}")
+        if scaling == "ramp":
+            # the (fractional) pair that turns n times over the original length
+            pair = [half * math.log(original / (2 * math.pi * n)) / math.log(base) for n in (high, low)]
+            first, last = max(math.floor(pair[0]), 0), min(math.ceil(pair[1]), rot - 1)
+            share = [min(1.0, max(0.0, (i - first) / max(last - first, 1e-3))) for i in range(half)]
+            amplitude = 0.1 * math.log(factor) + 1.0
+        else:
+            turned = [original * x / (2 * math.pi) for x in w]
+            share = [min(1.0, max(0.0, (high - n) / (high - low))) for n in turned]
+        w = [x * (1 - s) + x / factor * s for x, s in zip(w, share)]
+    return w, amplitude
+
+
+def _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device):
+    """The ckv_rotary of a call, after the checks."""
+    import torch
+    if turns is not None:
+        if turns.dtype != torch.int64:
+            raise TypeError(f"turns must be int64 (see rotary_turns), got {turns.dtype}")
+        if turns.dim() != 1 or not turns.is_contiguous() or turns.device != device:
+            raise ValueError(f"turns must be contiguous [rot / 2] on {device}, got {list(turns.shape)} on {turns.device}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype != torch.float32:
+                raise TypeError(f"{name} must be float32, got {w.dtype}")
+            if w.shape != (128,) or not w.is_contiguous() or w.device != device:
+                raise ValueError(f"{name} must be contiguous [128] on {device}, got {list(w.shape)} on {w.device}")
+    return Rotary(None if turns is None else turns.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
+                  None if k_weight is None else k_weight.data_ptr(), eps, amplitude,
+                  0 if turns is None else 2 * turns.shape[0], 1 if interleaved else 0)
+
+
+def _heads(name, t, tokens, heads, dtype, device):
+    """(address, strides as a C array) of t [tokens, heads, 128] after the checks."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != 128:
+        raise ValueError(f"{name} must be [{tokens}, {heads}, 128], got {list(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous, got strides {list(st)}")
+    return t.data_ptr(), _Strides(st[0], st[1])
+
+
+_Strides = ctypes.c_int64 * 2
+
+
+def rotate(q, k, positions, turns, q_out, k_out, interleaved: bool = False, q_weight=None, k_weight=None,
+           eps: float = 1e-6, amplitude: float = 1.0, stream=None):
+    """Norms (with q_weight, k_weight [128] float32) and rotary positions of q
+    [tokens, heads_q, 128] and k [tokens, heads_k, 128] into q_out and k_out, which
+    may be q and k (see ckv_rotate).  positions [tokens] int32; turns [rot / 2]
+    int64 (see rotary_turns), or None for norms alone; either of q and k may be
+    None, with its output."""
+    import torch
+    x = k if q is None else q
+    if x is None or x.dim() != 3:
+        raise ValueError("q or k must be given, as [tokens, heads, 128]")
+    tokens, device, code = x.shape[0], x.device, _dtype_code(x)
+    if device.type != "cuda":
+        raise ValueError(f"the rows must be on a CUDA device, got {device}")
+    if positions.dtype != torch.int32:
+        raise TypeError(f"positions must be int32, got {positions.dtype}")
+    if positions.shape != (tokens,) or not positions.is_contiguous() or positions.device != device:
+        raise ValueError(f"positions must be contiguous [{tokens}] on {device}, got {list(positions.shape)} on "
+                         f"{positions.device}")
+    args = []
+    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if (t is None) != (o is None):
+            raise ValueError(f"{name} and {name}_out go together")
+        if t is None:
+            args += [None, None, None, None, 0]
+        else:
+            heads = t.shape[1] if t.dim() == 3 else 0
+            args += [*_heads(name, t, tokens, heads, x.dtype, device),
+                     *_heads(name + "_out", o, tokens, heads, x.dtype, device), heads]
+    rotary = _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device)
+    raw_stream, current = _raw_calls(torch)
+    stream = raw_stream(device.index) if stream is None else getattr(stream, "cuda_stream", stream)
+    call = (ctypes.addressof(rotary), *args, positions.data_ptr(), tokens, 128, code, stream)
+    if device.index == current():
+        status = lib().ckv_rotate(*call)
+    else:
+        with torch.cuda.device(device.index):
+            status = lib().ckv_rotate(*call)
+    _check(status, "ckv_rotate")
+
+
 def paged_set_wait_limit(cycles: int = 2_000_000_000, stall: bool = False):
     """Bounded-wait limit of the paged attention in this process, and its
     failure detection test switch (see ckv_paged_set_wait_limit)."""
@@ -382,7 +529,8 @@ class PagedCache:
     [seqs] int32; optionally ``mass`` (float32) and ``pos`` (int32) [seqs, heads,
     max_pages * page_size], ``seen`` [seqs] int32 and ``dev_err`` [1] int32.
 
-    ``g`` is the number of query heads per KV head.  ``mass`` and ``pos`` are
+    ``g`` is the number of query heads per KV head.  With ``shared`` the handle has
+    the workspace of shared_attn too.  ``mass`` and ``pos`` are
     sized by the capacity, 8 bytes for each of seqs * heads * rows, and with
     ``mass`` so is the workspace, 4 g bytes for each (0.27 g MB without; a handle
     made without ``mass`` takes no ``mass_out``).  The handle keeps the
@@ -398,7 +546,10 @@ class PagedCache:
     A tensor of another shape, dtype, device or layout raises ValueError
     (TypeError for dtypes) and nothing is launched."""
 
-    def __init__(self, K, V, table, lens, g: int = 1, mass=None, pos=None, seen=None, dev_err=None):
+    _shared_attn = None
+
+    def __init__(self, K, V, table, lens, g: int = 1, mass=None, pos=None, seen=None, dev_err=None,
+                 shared: bool = False):
         import torch
         self.device = K.device
         if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype:
@@ -436,9 +587,16 @@ class PagedCache:
         self._cuda, self._index = torch.cuda, self.device.index
         self._raw_stream, self._current = _raw_calls(torch)
         self._stride_arrays = {}
+        self._plan, self._append_rotated = so.ckv_paged_plan, so.ckv_paged_append_rotated
+        self._shared_attn = so.ckv_paged_shared_attn
         need = ctypes.c_int64()
         _check(so.ckv_paged_attn_workspace(self._ref, g, 0 if mass is None else 1, ctypes.byref(need)),
                "ckv_paged_attn_workspace")
+        if shared:
+            more = ctypes.c_int64()
+            _check(so.ckv_paged_shared_workspace(self._ref, g, ctypes.byref(more)), "ckv_paged_shared_workspace")
+            need.value = max(need.value, more.value)
+        self.shared = shared
         self.workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
         self.workspace[:4096].zero_()  # the counters; calls leave them zero
         torch.cuda.current_stream(self.device).synchronize()  # whatever stream the first call is on
@@ -487,7 +645,7 @@ class PagedCache:
 
     def _call(self, fn, stream, *args):
         stream = self._raw_stream(self._index) if stream is None else getattr(stream, "cuda_stream", stream)
-        if stream not in self._streams and fn is self._attn:
+        if stream not in self._streams and (fn is self._attn or fn is self._shared_attn):
             self._note_stream(stream)
         if self._index == self._current():
             status = fn(self._ref, *args, stream)
@@ -556,3 +714,67 @@ class PagedCache:
         """evict_select, then evict_apply."""
         self.evict_select(budget, sinks, recent, moves, n_moves, stream)
         self.evict_apply(budget, moves, n_moves, stream)
+
+    # -- a step's tokens ---------------------------------------------------------
+    def plan(self, counts, held, free, span, slots, starts, granted, shared=None, start=None, first=None,
+             held_out=None, span_out=None, stream=None):
+        """Pages for counts[s] more tokens of every sequence, and where each token
+        goes (see ckv_paged_plan): counts, held, granted, shared, start, first,
+        held_out [seqs], span, span_out [2], starts [seqs + 1], slots [tokens, 4]
+        and the ring of free pages ``free``, all int32.  held_out and span_out are
+        held and span themselves if None; table, lens and seen change."""
+        i32, tensor, per_seq = self._i32, self._tensor, self._per_seq
+        if free.dim() != 1 or slots.dim() != 2:
+            raise ValueError(f"free must be [pages] and slots [tokens, 4], got {list(free.shape)}, {list(slots.shape)}")
+        n_slots, cap = slots.shape[0], free.shape[0]
+        h, sp = tensor("held", held, per_seq, i32), tensor("span", span, (2,), i32)
+        self._call(self._plan, stream, tensor("counts", counts, per_seq, i32), tensor("start", start, per_seq, i32),
+                   tensor("first", first, per_seq, i32), tensor("shared", shared, per_seq, i32), h,
+                   h if held_out is None else tensor("held_out", held_out, per_seq, i32),
+                   tensor("free", free, (cap,), i32), cap, sp,
+                   sp if span_out is None else tensor("span_out", span_out, (2,), i32),
+                   tensor("granted", granted, per_seq, i32), tensor("starts", starts, (self.seqs + 1,), i32),
+                   tensor("slots", slots, (n_slots, 4), i32), n_slots)
+
+    def append_rotated(self, q, k, v, slots, turns, q_out, interleaved: bool = False, q_weight=None, k_weight=None,
+                       eps: float = 1e-6, amplitude: float = 1.0, stream=None):
+        """q, k normed and rotated (see rotate), q into q_out, k and v into the rows
+        that slots [tokens, 4] of a plan gives them (see ckv_paged_append_rotated):
+        q, q_out [tokens, heads * g, 128] (both None: no queries), k, v [tokens,
+        heads, 128], any strides with contiguous channels."""
+        device = self.device
+        if k.dim() != 3:
+            raise ValueError(f"k must be [tokens, {self.heads}, 128], got {list(k.shape)}")
+        tokens = k.shape[0]
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
+        heads_q, dtype = self.heads * self.g, self.dtype
+        rotary = _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device)
+        queries = (None, None) if q is None else _heads("q", q, tokens, heads_q, dtype, device)
+        rotated = (None, None) if q is None else _heads("q_out", q_out, tokens, heads_q, dtype, device)
+        self._call(self._append_rotated, stream, ctypes.addressof(rotary), *queries, 0 if q is None else self.g,
+                   *rotated, *_heads("k", k, tokens, self.heads, dtype, device),
+                   *_heads("v", v, tokens, self.heads, dtype, device),
+                   self._tensor("slots", slots, (tokens, 4), self._i32), tokens)
+
+    def shared_attn(self, q, out, group_starts, prefix, lse=None, scale=None, stream=None):
+        """decode_attn (without weights) where sequences group_starts[i] ..
+        group_starts[i + 1] - 1 have their first prefix[i] rows in common, which
+        are then read once for all of them (see ckv_paged_shared_attn):
+        group_starts [groups + 1] and prefix [groups] int32.  The handle must have
+        been made with shared=True."""
+        if not self.shared:
+            raise ValueError("the handle was made without shared=True and has no workspace for this call")
+        if q.shape != self._q_shape:
+            raise ValueError(f"q must be {list(self._q_shape)}, got {tuple(q.shape)}")
+        if q.dtype != self.dtype:
+            raise TypeError(f"q must be {self.dtype}, got {q.dtype}")
+        if q.device != self.device:
+            raise ValueError(f"q is on {q.device}, the cache on {self.device}")
+        if prefix.dim() != 1:
+            raise ValueError(f"prefix must be [groups], got {list(prefix.shape)}")
+        groups, i32, f32, tensor = prefix.shape[0], self._i32, self._f32, self._tensor
+        self._call(self._shared_attn, stream, q.data_ptr(), self._code, self._strides(q, 2), self.g,
+                   128 ** -0.5 if scale is None else scale, tensor("group_starts", group_starts, (groups + 1,), i32),
+                   tensor("prefix", prefix, (groups,), i32), groups, tensor("out", out, self._q_shape, f32),
+                   None if lse is None else tensor("lse", lse, self._lse_shape, f32), *self._workspace)

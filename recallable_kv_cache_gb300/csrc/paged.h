@@ -1,5 +1,6 @@
 // Declarations shared by the paged cache's kernel files.
 #pragma once
+#include <cuda.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -11,6 +12,7 @@ namespace paged {
 constexpr int TILE = 16;         // pages are multiples of this many rows
 constexpr int MAX_G = 16;        // query heads per KV head
 constexpr int MAX_DEVICES = 64;
+constexpr int MAX_GRID = 256;    // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 constexpr long long MAX_STRIDE = 1LL << 37;  // elements; a tensor map's strides stay below 2^40 bytes
 
 // Quotient by a divisor fixed at launch, for dividends below 2^31: with s =
@@ -48,9 +50,43 @@ struct Cache {
     FastDiv by_page, by_heads;
 };
 
+// The deal: `total` tiles to the warps of n_cta CTAs, in order, as evenly as
+// they go (shares of q + 1 tiles, then of q).
+struct Deal {
+    int total, n_cta, warps, q, r;
+    __device__ __forceinline__ Deal(int total_, int n_cta_, int warps_) : total(total_), n_cta(n_cta_), warps(warps_) {
+        q = total / (n_cta * warps);
+        r = total - q * (n_cta * warps);
+    }
+    static __device__ __forceinline__ int ctas(int total, int warps, int grid) {
+        return max(1, min(grid, (total + warps - 1) / warps));
+    }
+    __device__ __forceinline__ int begin_warp(int w) const { return w * q + min(w, r); }  // w: across CTAs
+    __device__ __forceinline__ int begin_cta(int c) const { return begin_warp(c * warps); }
+    // the CTA whose share holds tile t
+    __device__ __forceinline__ int cta_of(int t) const {
+        const int w = t < (q + 1) * r ? t / (q + 1) : r + (t - (q + 1) * r) / q;
+        return w / warps;
+    }
+};
+
 ckv_status check_cache(const ckv_paged_cache* c, Cache* out);
 // SM count of the current device (looked up once per device); 0 on failure
 int sm_count(int* dev);
+
+bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long long* st, bool bf16, bool swizzled,
+                 int tile_rows, int pieces_a_box = 0);
+// what ckv_paged_set_wait_limit has set
+void waits(long long* limit, int* stall);
+// bytes of the decode attention's workspace without weights, and where the lse
+// (base 2, [seqs][heads * g]) of its calls stands
+size_t attn_workspace(const Cache& c, int g, float** lse2, void* workspace);
+// Decode attention over the rows of each sequence from skip[s] on (device int32,
+// multiples of TILE), bf16.  To follow, as a dependent launch, a kernel that has
+// waited for its own predecessor and that writes nothing this one reads; a
+// kernel behind it that waits for it has waited for both.
+cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const void* q, const long long* q_stride, int g,
+                                 float qscale, float* out, float* lse, void* workspace, cudaStream_t s);
 
 // two arrays of n 32-bit elements that are one and the same (an element is read
 // before it is written) or do not overlap; no array overlaps nothing

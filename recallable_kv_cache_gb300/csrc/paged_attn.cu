@@ -27,6 +27,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mma_sync.cuh"
 #include "paged.h"
@@ -41,7 +42,6 @@ using namespace mmas;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 152 SMs)
 // A stage holds the K rows, then the V rows of one tile.  Eight warps with two
 // stages each have 128 KB of an SM under way.  More of it lowers the rate (12
 // warps of two stages: 90 instead of 87 us for one sequence of 128k rows and 8
@@ -50,8 +50,22 @@ constexpr int MAX_GRID = 256;  // CTAs a workspace is laid out for (a GB300 has 
 constexpr int STAGE = 8192;
 constexpr int WARPS = 8, NST = 2;
 
-struct AttnArgs {
-    Cache c;
+// A cache of whose sequences the first skip[s] rows (a multiple of 16) are left
+// out: they are attended elsewhere, together with those of other sequences.
+struct OwnRows : Cache {
+    const int32_t* skip;
+};
+__device__ __forceinline__ int first_row(const Cache&, int) { return 0; }
+__device__ __forceinline__ int first_row(const OwnRows& c, int s) { return c.skip[s]; }
+// rows to attend: those held from the first on
+template <typename C>
+__device__ __forceinline__ int rows_attended(const C& c, int s) {
+    return max(0, rows_held(c, s) - first_row(c, s));
+}
+
+template <typename C>
+struct AttnArgsOf {
+    C c;
     const void* q;
     long long qst[2];  // element strides: sequence, query head
     int g;
@@ -69,21 +83,23 @@ struct AttnArgs {
     int stall;  // failure detection test: odd warps do not ask for their first tile
 };
 
+using AttnArgs = AttnArgsOf<Cache>;
+
 // A partial: O [g][D], then the maxima [g], then the sums [g]; a multiple of
 // 16 bytes, as O is read and written 16 bytes at a time.
 __host__ __device__ __forceinline__ size_t part_floats(int g) { return ((size_t)g * (D + 2) + 3) / 4 * 4; }
 
 // ---------------------------------------------------------------- the deal
-template <int TR>
-__device__ __forceinline__ int tiles_of(const Cache& c, int s) {
-    return (rows_held(c, s) + TR - 1) / TR;
+template <int TR, typename C>
+__device__ __forceinline__ int tiles_of(const C& c, int s) {
+    return (rows_attended(c, s) + TR - 1) / TR;
 }
 struct Pos {
     int s, h, k, nt;  // nt = 0: past the last tile
 };
 // l tiles further on
-template <int TR>
-__device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
+template <int TR, typename C>
+__device__ __forceinline__ Pos advance(const C& c, Pos p, int l) {
     p.k += l;
     while (p.nt && p.k >= p.nt) {
         p.k -= p.nt;
@@ -97,8 +113,6 @@ __device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
     }
     return p;
 }
-// The deal: `total` tiles to the warps of n_cta CTAs, in order, as evenly as
-// they go (shares of q + 1 tiles, then of q).
 // Merging across CTAs takes some 3 us, as long as two or three tiles of a warp.
 // So where every unit can have a CTA to itself and the largest then has at most
 // OWN_EXTRA tiles a warp more than in an even deal, it gets one: 128 units of
@@ -106,31 +120,13 @@ __device__ __forceinline__ Pos advance(const Cache& c, Pos p, int l) {
 // 9.6, of 384 rows 8.2 instead of 8.5; of 512 rows 9.3 instead of 8.7, which
 // the rule leaves to the even deal.
 constexpr int OWN_EXTRA = 2;
-struct Deal {
-    int total, n_cta, warps, q, r;
-    __device__ __forceinline__ Deal(int total_, int n_cta_, int warps_) : total(total_), n_cta(n_cta_), warps(warps_) {
-        q = total / (n_cta * warps);
-        r = total - q * (n_cta * warps);
-    }
-    static __device__ __forceinline__ int ctas(int total, int warps, int grid) {
-        return max(1, min(grid, (total + warps - 1) / warps));
-    }
-    __device__ __forceinline__ int begin_warp(int w) const { return w * q + min(w, r); }  // w: across CTAs
-    __device__ __forceinline__ int begin_cta(int c) const { return begin_warp(c * warps); }
-    // the CTA whose share holds tile t
-    __device__ __forceinline__ int cta_of(int t) const {
-        const int w = t < (q + 1) * r ? t / (q + 1) : r + (t - (q + 1) * r) / q;
-        return w / warps;
-    }
-};
-
 // The deal of this call, and where the shares of CTA `cta`'s warps begin.  Every
 // thread adds up a chunk of the sequences' tiles; a scan gives the total (below
 // 2^31, checked for the cache's extents) and the thread in whose chunk a
 // warp's first tile falls leaves the chunk's first sequence and how many tiles
 // behind it the warp begins.  `cta` becomes the CTA's number in the deal.
-template <int TR, int NT>
-__device__ Deal deal_out(const Cache& c, int2* start, int& cta, int grid) {
+template <int TR, int NT, typename C>
+__device__ Deal deal_out(const C& c, int2* start, int& cta, int grid) {
     constexpr int NW = NT / 32;
     __shared__ int warp_sum[NW], warp_max[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -181,8 +177,8 @@ __device__ Deal deal_out(const Cache& c, int2* start, int& cta, int grid) {
     return deal;
 }
 // the place of the tile that is `left` tiles behind the first of sequence s
-template <int TR>
-__device__ __forceinline__ Pos walk(const Cache& c, int s, int left) {
+template <int TR, typename C>
+__device__ __forceinline__ Pos walk(const C& c, int s, int left) {
     int nt;
     while (left >= (nt = tiles_of<TR>(c, s)) * c.heads) {
         left -= nt * c.heads;
@@ -852,7 +848,8 @@ struct Job {
     float* dst;  // not final: where the merged partial goes
 };
 // Head j of the partials src[0 .. n), merged in that order by a warp.
-__device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, const float* const* src, int j, int lane) {
+template <typename C>
+__device__ __forceinline__ void merge_head(const AttnArgsOf<C>& a, const Job& job, const float* const* src, int j, int lane) {
     const int sm = a.g * D + j, sl = sm + a.g;  // where a partial keeps its maximum and sum
     float M = -INFINITY, L = 0.f;
     for (int i = lane; i < job.n; i += 32) M = fmaxf(M, src[i][sm]);
@@ -892,12 +889,14 @@ __device__ __forceinline__ void merge_head(const AttnArgs& a, const Job& job, co
 
 // mass_in of the four rows from r on, if one of them is below r1 (r is unsigned:
 // it goes past the last row, which may be just below 2^31)
-__device__ __forceinline__ float4 old_weights(const AttnArgs& a, int u, unsigned r, unsigned r1) {
+template <typename C>
+__device__ __forceinline__ float4 old_weights(const AttnArgsOf<C>& a, int u, unsigned r, unsigned r1) {
     return a.mass_in && r < r1 ? *reinterpret_cast<const float4*>(a.mass_in + (size_t)u * a.c.rows + r)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 // mass_out = v + sum_j e^{s_j - lse_j} for those of the four rows that are below r1
-__device__ __forceinline__ void add_weights(const AttnArgs& a, int u, unsigned r, unsigned r1, float4 v) {
+template <typename C>
+__device__ __forceinline__ void add_weights(const AttnArgsOf<C>& a, int u, unsigned r, unsigned r1, float4 v) {
     const float* lse2 = a.lse2 + (size_t)u * a.g;
     const float* sc = a.scores + (size_t)u * a.g * a.c.rows + r;
     const size_t o = (size_t)u * a.c.rows + r;
@@ -935,11 +934,16 @@ __device__ __forceinline__ void add_weights(const AttnArgs& a, int u, unsigned r
     }
 }
 
-template <typename E>
+template <typename E, typename C>
 __global__ void __launch_bounds__(WARPS * 32, 1)
-    paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tk,
+    paged_attn_kernel(const __grid_constant__ AttnArgsOf<C> a, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
     constexpr int TR = E::TR, NW = WARPS, NT = NW * 32;
+    // OWN: the kernel before is the one that attends the rows left out.  It began
+    // after what wrote the inputs had ended, and the two write nothing of each
+    // other's, so this one takes the SMs that the other leaves and waits for it at
+    // its end only, for the kernel behind both.
+    constexpr bool OWN = !std::is_same<C, Cache>::value;
     using T = typename E::T;
     extern __shared__ unsigned char smem_raw[];
     // swizzled tiles need 1024-byte alignment
@@ -966,8 +970,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
         shared_units[threadIdx.x].x = -1;
     }
-    ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
-    ptx::allow_dependent_launch();
+    if (!OWN) {
+        ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
+        ptx::allow_dependent_launch();
+    }
     int cta = blockIdx.x;
     const Deal deal = deal_out<TR, NT>(a.c, start, cta, gridDim.x);
     const bool works = cta < deal.n_cta && deal.total > 0;
@@ -1001,7 +1007,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 block += 32;
                 if (block + lane < t_end) {
                     p = advance<TR>(a.c, base, lane);
-                    const int row = p.k * TR;
+                    const int row = first_row(a.c, p.s) + p.k * TR;
                     p_rows = min(TR, rows_held(a.c, p.s) - row);
                     p_page = page_of(a.c, p.s, row, &p_slot);
                     if (p_page < 0) p_rows = 0;
@@ -1089,13 +1095,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
     // units without rows: nothing else writes their outputs
     for (int s = blockIdx.x; s < a.c.seqs; s += gridDim.x)
-        if (rows_held(a.c, s) == 0)
+        if (rows_attended(a.c, s) == 0)
             for (long long i = threadIdx.x; i < (long long)a.c.heads * a.g * D; i += NT) {
                 const size_t o = (size_t)s * a.c.heads * a.g;
                 a.out[o * D + i] = 0.f;
                 if (a.lse && i < (long long)a.c.heads * a.g) a.lse[o + i] = -INFINITY;
+                if (OWN && i < (long long)a.c.heads * a.g) a.lse2[o + i] = -INFINITY;
             }
-    if (!works) return;
+    if (!works) {
+        if (OWN) ptx::grid_dependency_wait();
+        return;
+    }
     // a CTA that adds its unit's weights itself asks for the old ones in time
     const int unit_rows = a.fuse ? rows_held(a.c, a.c.by_heads.quot(blockIdx.x)) : 0;
     const float4 old = old_weights(a, blockIdx.x, 4 * threadIdx.x, unit_rows);
@@ -1183,6 +1193,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         }
     }
     if (4 * (int)threadIdx.x < unit_rows) add_weights(a, blockIdx.x, 4 * threadIdx.x, unit_rows, old);
+    if (OWN) ptx::grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -1255,18 +1266,21 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
 }
 
+}  // namespace
+
 // The pool as a tensor map whose boxes are tiles of one page and KV head: rows
 // cut into pieces of 128 bytes and swizzled, [page][head][piece][slot][128
-// bytes], or fp32 rows whole, [page][head][slot][128 channels].
+// bytes], or fp32 rows whole, [page][head][slot][128 channels].  A box has all
+// pieces of its rows, or one where pieces_a_box says so.
 bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long long* st, bool bf16, bool swizzled,
-                 int tile_rows) {
+                 int tile_rows, int pieces_a_box) {
     const auto enc = get_encode();
     if (!enc) return false;
     const cuuint64_t slot = (cuuint64_t)st[2], head = (cuuint64_t)st[1], page = (cuuint64_t)st[0];
     const cuuint32_t wide = bf16 ? 64 : 32, pieces = D / wide;
     const cuuint64_t dims5[5] = {wide, (cuuint64_t)c.page, pieces, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
     const cuuint64_t str5[4] = {slot, 128, head, page};
-    const cuuint32_t box5[5] = {wide, (cuuint32_t)tile_rows, pieces, 1, 1};
+    const cuuint32_t box5[5] = {wide, (cuuint32_t)tile_rows, pieces_a_box ? (cuuint32_t)pieces_a_box : pieces, 1, 1};
     const cuuint64_t dims4[4] = {D, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages};
     const cuuint64_t str4[3] = {slot, head, page};
     const cuuint32_t box4[4] = {D, (cuuint32_t)tile_rows, 1, 1};
@@ -1279,6 +1293,8 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 struct Layout {
     size_t part, lse2, scores, total;  // byte offsets; the arrivals come first
@@ -1294,8 +1310,8 @@ Layout layout_of(const Cache& c, int g, bool with_mass) {
     return l;
 }
 
-template <typename E>
-cudaError_t launch(const AttnArgs& a, int sms, int dev, cudaStream_t s) {
+template <typename E, typename C>
+cudaError_t launch(const AttnArgsOf<C>& a, int sms, int dev, cudaStream_t s) {
     constexpr bool bf16 = sizeof(typename E::T) == 2;
     CUtensorMap tk, tv;
     if (!encode_pool(&tk, a.c, a.c.K, a.c.ks, bf16, E::SWIZZLED, E::TR) ||
@@ -1310,33 +1326,69 @@ cudaError_t launch(const AttnArgs& a, int sms, int dev, cudaStream_t s) {
     const size_t smem = rings + WARPS * part_floats(a.g) * sizeof(float);
     static std::atomic<bool> set[MAX_DEVICES];
     if (!set[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<E, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    rings + WARPS * part_floats(MAX_G) * sizeof(float));
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
     // Where the capacity alone says that every unit gets a CTA of its own, that
     // CTA adds the weights and the second kernel is not launched.
-    AttnArgs b = a;
+    AttnArgsOf<C> b = a;
     b.fuse = a.mass_out && units <= grid && ceil_div(ceil_div(a.c.rows, E::TR), WARPS) <= 1 + OWN_EXTRA;
     static_assert((1 + OWN_EXTRA) * WARPS * E::TR <= 4 * WARPS * 32, "a thread adds the weights of four rows at most");
-    cudaError_t e = launch_dependent(paged_attn_kernel<E>, dim3(grid), dim3(WARPS * 32), smem, s, b, tk, tv);
-    if (e == cudaSuccess && a.mass_out && !b.fuse)
-        e = launch_dependent(paged_weights_kernel<E::TR>, dim3(grid * W_SPLIT), dim3(WARPS * 32), 0, s, a);
+    cudaError_t e = launch_dependent(paged_attn_kernel<E, C>, dim3(grid), dim3(WARPS * 32), smem, s, b, tk, tv);
+    if constexpr (std::is_same<C, Cache>::value)
+        if (e == cudaSuccess && a.mass_out && !b.fuse)
+            e = launch_dependent(paged_weights_kernel<E::TR>, dim3(grid * W_SPLIT), dim3(WARPS * 32), 0, s, a);
     return e;
 }
 
+std::atomic<long long> wait_limit{WAIT_LIMIT};
+std::atomic<int> stall_switch{0};
+
 }  // namespace
+
+void waits(long long* limit, int* stall) {
+    *limit = wait_limit.load(std::memory_order_relaxed);
+    *stall = stall_switch.load(std::memory_order_relaxed);
+}
+
+size_t attn_workspace(const Cache& c, int g, float** lse2, void* workspace) {
+    const Layout l = layout_of(c, g, false);
+    if (lse2) *lse2 = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + l.lse2);
+    return l.total;
+}
+
+cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const void* q, const long long* q_stride, int g,
+                                 float qscale, float* out, float* lse, void* workspace, cudaStream_t s) {
+    AttnArgsOf<OwnRows> a = {};
+    static_cast<Cache&>(a.c) = c;
+    a.c.skip = skip;
+    const Layout l = layout_of(c, g, false);
+    unsigned char* w = static_cast<unsigned char*>(workspace);
+    a.q = q;
+    a.qst[0] = q_stride[0];
+    a.qst[1] = q_stride[1];
+    a.g = g;
+    a.qscale = qscale;
+    a.out = out;
+    a.lse = lse;
+    a.arrived = reinterpret_cast<unsigned*>(w);
+    a.part = reinterpret_cast<float*>(w + l.part);
+    a.lse2 = reinterpret_cast<float*>(w + l.lse2);
+    waits(&a.wait_limit, &a.stall);
+    a.stall = 0;  // the kernel before this one is the one to stall
+    int dev = 0;
+    const int sms = sm_count(&dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    return g <= 8 ? launch<TilesBf16<1>>(a, sms, dev, s) : launch<TilesBf16<2>>(a, sms, dev, s);
+}
+
 }  // namespace paged
 }  // namespace ckv
 
 using namespace ckv;
 using namespace ckv::paged;
-
-namespace {
-std::atomic<long long> wait_limit{WAIT_LIMIT};
-std::atomic<int> stall_switch{0};
-}  // namespace
 
 extern "C" ckv_status ckv_paged_set_wait_limit(int64_t cycles, int32_t stall) {
     CKV_TRACE("ckv_paged_set_wait_limit");
@@ -1395,8 +1447,7 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     a.lse2 = reinterpret_cast<float*>(w + l.lse2);
     a.scores = mass_out ? reinterpret_cast<float*>(w + l.scores) : nullptr;
     a.fuse = 0;
-    a.wait_limit = wait_limit.load(std::memory_order_relaxed);
-    a.stall = stall_switch.load(std::memory_order_relaxed);
+    waits(&a.wait_limit, &a.stall);
     int dev = 0;
     const int grid = sm_count(&dev);
     if (grid < 1) return CKV_ERR_CUDA;
