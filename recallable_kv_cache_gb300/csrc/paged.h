@@ -82,10 +82,10 @@ void waits(long long* limit, int* stall);
 // (base 2, [seqs][heads * g]) of its calls stands
 size_t attn_workspace(const Cache& c, int g, float** lse2, void* workspace);
 // Decode attention over the rows of each sequence from skip[s] on (device int32,
-// multiples of TILE), bf16.  To follow, as a dependent launch, a kernel that has
+// multiples of TILE) by *ctas CTAs, bf16.  To follow, as a dependent launch, a kernel that has
 // waited for its own predecessor and that writes nothing this one reads; a
 // kernel behind it that waits for it has waited for both.
-cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const void* q, const long long* q_stride, int g,
+cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int32_t* ctas, const void* q, const long long* q_stride, int g,
                                  float qscale, float* out, float* lse, void* workspace, cudaStream_t s);
 
 // two arrays of n 32-bit elements that are one and the same (an element is read

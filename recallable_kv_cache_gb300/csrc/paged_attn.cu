@@ -54,7 +54,10 @@ constexpr int WARPS = 8, NST = 2;
 // out: they are attended elsewhere, together with those of other sequences.
 struct OwnRows : Cache {
     const int32_t* skip;
+    const int32_t* ctas;  // how many CTAs of the grid work: the others' SMs are taken
 };
+__device__ __forceinline__ int working_ctas(const Cache&) { return gridDim.x; }
+__device__ __forceinline__ int working_ctas(const OwnRows& c) { return min((int)gridDim.x, max(1, *c.ctas)); }
 __device__ __forceinline__ int first_row(const Cache&, int) { return 0; }
 __device__ __forceinline__ int first_row(const OwnRows& c, int s) { return c.skip[s]; }
 // rows to attend: those held from the first on
@@ -924,8 +927,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     constexpr int TR = E::TR, NW = WARPS, NT = NW * 32;
     // OWN: the kernel before is the one that attends the rows left out.  It began
     // after what wrote the inputs had ended, and the two write nothing of each
-    // other's, so this one takes the SMs that the other leaves and waits for it at
-    // its end only, for the kernel behind both.
+    // other's, so this one runs beside it, on the SMs that the other leaves, and
+    // waits for it at its end only, for the kernel behind both.
     constexpr bool OWN = !std::is_same<C, Cache>::value;
     using T = typename E::T;
     extern __shared__ unsigned char smem_raw[];
@@ -953,12 +956,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
         shared_units[threadIdx.x].x = -1;
     }
-    if (!OWN) {
-        ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
-        ptx::allow_dependent_launch();
+    if (!OWN) ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
+    ptx::allow_dependent_launch();
+    const int grid = working_ctas(a.c);
+    if (OWN && (int)blockIdx.x >= grid) {
+        ptx::grid_dependency_wait();
+        return;
     }
     int cta = blockIdx.x;
-    const Deal deal = deal_out<TR, NT>(a.c, start, cta, gridDim.x);
+    const Deal deal = deal_out<TR, NT>(a.c, start, cta, grid);
     const bool works = cta < deal.n_cta && deal.total > 0;
     const int t_begin = works ? deal.begin_warp(cta * NW + warp) : 0;
     const int t_end = works ? deal.begin_warp(cta * NW + warp + 1) : 0;
@@ -1077,7 +1083,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     if (blockIdx.x == 0)
         for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
     // units without rows: nothing else writes their outputs
-    for (int s = blockIdx.x; s < a.c.seqs; s += gridDim.x)
+    for (int s = blockIdx.x; s < a.c.seqs; s += grid)
         if (rows_attended(a.c, s) == 0)
             for (long long i = threadIdx.x; i < (long long)a.c.heads * a.g * D; i += NT) {
                 const size_t o = (size_t)s * a.c.heads * a.g;
@@ -1342,11 +1348,12 @@ size_t attn_workspace(const Cache& c, int g, float** lse2, void* workspace) {
     return l.total;
 }
 
-cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const void* q, const long long* q_stride, int g,
+cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int32_t* ctas, const void* q, const long long* q_stride, int g,
                                  float qscale, float* out, float* lse, void* workspace, cudaStream_t s) {
     AttnArgsOf<OwnRows> a = {};
     static_cast<Cache&>(a.c) = c;
     a.c.skip = skip;
+    a.c.ctas = ctas;
     const Layout l = layout_of(c, g, false);
     unsigned char* w = static_cast<unsigned char*>(workspace);
     a.q = q;

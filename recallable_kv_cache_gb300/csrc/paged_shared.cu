@@ -32,9 +32,10 @@
 // with a running maximum of its own, and O follows with the larger of both.
 // Warp roles:
 //   warp 0       asks for the tiles (TMA)
-//   warp 1       owns tensor memory, issues the products
-//   warps 2-9    softmax: four of even, four of odd tiles, a thread a query
+//   warp 1       owns tensor memory, issues S
+//   warps 2-9    softmax, a thread 64 rows of a query
 //   warps 10-17  queries to shared memory; O, a thread 64 channels of a query
+//   warp 18      issues T
 // Where a unit is several CTAs' its parts are joined by the last kernel in the
 // order of its rows, so that results do not depend on timing.
 #include <cuda.h>
@@ -64,7 +65,8 @@ constexpr int PANEL = 128 * 128;     // 64 channels of 128 rows
 constexpr int STAGE = 2 * PANEL;     // K or V of a tile
 constexpr int NST = 6;
 constexpr int SOFT_WARPS = 8, OUT_WARPS = 8;
-constexpr int THREADS = 32 * (2 + SOFT_WARPS + OUT_WARPS);
+constexpr int VALUE_WARP = 2 + SOFT_WARPS + OUT_WARPS;
+constexpr int THREADS = 32 * (VALUE_WARP + 1);
 constexpr int PREP_THREADS = 256;
 constexpr int JOIN_ROWS = 8;
 constexpr int JOIN_THREADS = JOIN_ROWS * D / 4;
@@ -72,7 +74,7 @@ constexpr int JOIN_THREADS = JOIN_ROWS * D / 4;
 // and lower terms of 32 weights take the place of their scores, sixteen columns
 // each, and the middle ones stand behind.
 constexpr int NSP = 2;
-constexpr uint32_t MID_COL = 128, SP_COLS = 192, T_COL = NSP * SP_COLS;
+constexpr uint32_t LOW_COL = 16, MID_COL = 128, SP_COLS = 192, T_COL = NSP * SP_COLS;
 
 __device__ __forceinline__ float upper(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
@@ -84,11 +86,25 @@ struct Group {
     int parts, cta;      // of a unit, and the CTA of the group's first one, where units have CTAs of their own
 };
 
+// A CTA's share of a unit.
+struct Run {
+    int first, members, rows;  // of the group
+    int h, block;              // KV head, block of queries
+    int k0, n;                 // tiles [k0, k0 + n) of the unit
+};
+// The tiles [t, t_end) of a CTA, the group of the first, and the run it is in.
+struct __align__(16) Share {
+    int t, t_end, group, pad[2];
+    Run run;
+};
+static_assert(sizeof(Share) == 48, "read as three times 16 bytes");
+
 struct SharedArgs {
     Cache c;
     const unsigned char* q;
     long long qst[2];  // byte strides: sequence, query head
     int g;
+    FastDiv by_g;
     float qscale;  // scale * log2(e)
     const int32_t* group_starts;
     const int32_t* prefix;
@@ -101,7 +117,9 @@ struct SharedArgs {
     int* tile_base;     // [groups + 1] tiles before the group
     int32_t* skip;      // [seqs] rows that the group attends
     int* group_of;      // [seqs]
-    int* ctas;          // [1] CTAs that have a unit's part, 0: the even deal
+    Share* share;       // [grid]
+    int2* deal;         // [1] CTAs with a unit's part, 0: the even deal; CTAs that it goes to
+    int* own_ctas;      // [1] CTAs for the sequences' own rows
     float* own_lse2;    // [seqs * heads * g] of the sequences' own rows, base 2
     // Parts: O as [channel / 4][query of the block] of four, and (maximum, sum) of
     // even and odd tiles.  The CTA in which a unit begins leaves its part behind
@@ -116,118 +134,223 @@ struct SharedArgs {
 };
 
 // ---------------------------------------------------------------- the groups
-// sums (or maxima) of v over the threads before, and over all
+// The prep runs alone, once a call, so that every instruction of it is fetched
+// at some 60 ns for 128 bytes: its length counts for more than its work, and
+// what it does more than once are calls.
+__device__ __noinline__ unsigned quotient(unsigned n, unsigned d) { return n / d; }
+__device__ __forceinline__ int parts_of(int n, int d) { return (int)quotient((unsigned)n + d - 1, d); }
+
+// the sum of v over the threads before (the largest of theirs where MAX), and over all
 template <bool MAX>
-__device__ __forceinline__ int scan(int v, int* warp_val, int* all) {
+__device__ __noinline__ int2 scan(int v, int* warp_val) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(FULL, x, o);
         if (lane >= o) x = MAX ? max(x, y) : x + y;
     }
     if (lane == 31) warp_val[warp] = x;
     __syncthreads();
-    int before = __shfl_up_sync(FULL, x, 1);
+    int before = __shfl_up_sync(FULL, x, 1), all = 0;
     if (lane == 0) before = 0;
-    int total = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < PREP_THREADS / 32; ++w) {
-        if (w < warp) before = MAX ? max(before, warp_val[w]) : before + warp_val[w];
-        total = MAX ? max(total, warp_val[w]) : total + warp_val[w];
+        const int y = warp_val[w];
+        if (w < warp) before = MAX ? max(before, y) : before + y;
+        all = MAX ? max(all, y) : all + y;
     }
     __syncthreads();
-    *all = total;
-    return before;
+    return make_int2(before, all);
 }
 
-// One CTA.  A thread has a chunk of neighbouring groups, then of sequences.
-// How the tiles are dealt out: evenly, a CTA's share beginning and ending
-// anywhere, or every unit in equal parts of its own to whole CTAs.  Where a
-// share passes from one unit to the next the products wait for the new queries
-// and the softmax for the products, as long as some two tiles, so the second
-// deal is taken where its largest part is at most OWN_EXTRA tiles above an even
-// share.
+__device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigned)(gr.rows + KT - 1) / KT); }
+
+// How the SMs and the tiles are dealt out.
+//
+// The shared rows and the sequences' own rows are attended side by side, on SMs
+// of their own (one after the other the second would begin with some 4 us of
+// latency and end with as much, while HBM idles).  One SM would take TILE_COST
+// for a tile of shared rows, OWN_COST for 16 own rows of a KV head and UNIT_COST
+// for each (sequence, KV head) with some, and merging the latter takes
+// MERGE_COST longer at the end: the P SMs of the G there are for the shared rows
+// are those with which both end together, x / P = y / (G - P) + MERGE_COST.
+//
+// The tiles of shared rows go to CTAs evenly, a CTA's share beginning and ending
+// anywhere, or every unit goes in equal parts to CTAs of its own.  Where a share
+// passes from one unit to the next the products wait for the new queries and the
+// softmax for the products, as long as some two tiles, so the second deal is
+// taken where its largest part is at most OWN_EXTRA tiles above an even share.
+constexpr float TILE_COST = 1.7f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 3.f;  // us
 constexpr int OWN_EXTRA = 2;
+// groups, and sequences, up to which their numbers are kept in shared memory
+constexpr int FEW_GROUPS = PREP_THREADS, FEW_SEQS = 1024;
+
+// the run that begins at tile t, in a group whose tiles begin at `base`, of a share that ends at t_end
+__device__ __forceinline__ Run run_in(const Group& gr, int base, int t, int t_end) {
+    const int nt = tiles_of(gr), unit = (int)quotient(t - base, nt), k0 = t - base - unit * nt;
+    const int h = (int)quotient(unit, gr.blocks);
+    return Run{gr.first, gr.members, gr.rows, h, unit - h * gr.blocks, k0, min(nt - k0, t_end - t)};
+}
+
+// One CTA.  A thread has a chunk of neighbouring groups (one, where FEW), then
+// every PREP_THREADS-th sequence, then CTAs.
+template <bool FEW>
 __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_constant__ SharedArgs a) {
     __shared__ int warp_val[PREP_THREADS / 32];
     __shared__ int ctas_with[OWN_EXTRA + 1];
+    __shared__ int own_tiles, own_units;
+    __shared__ Group group_here[FEW ? FEW_GROUPS : 1];
+    __shared__ int base_here[FEW ? FEW_GROUPS : 1], lens_here[FEW ? FEW_SEQS : 1];
     const int tid = threadIdx.x;
     if (tid <= OWN_EXTRA) ctas_with[tid] = 0;
+    if (tid == 0) own_tiles = own_units = 0;
+    Group* group = FEW ? group_here : a.group;
+    int* base = FEW ? base_here : a.tile_base;
+    const int* lens = FEW ? lens_here : a.c.lens;
+    const int chunk = FEW ? 1 : (a.groups + PREP_THREADS - 1) / PREP_THREADS;
+    const int i0 = min(a.groups, tid * chunk), i1 = min(a.groups, i0 + chunk);
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    const int chunk = (a.groups + PREP_THREADS - 1) / PREP_THREADS;
-    const int i0 = min(a.groups, tid * chunk), i1 = min(a.groups, i0 + chunk);
-    auto start_at = [&](int i) { return min(max(a.group_starts[i], 0), a.c.seqs); };
-    auto tiles_of = [](const Group& gr) { return (gr.rows + KT - 1) / KT; };
+    // what goes by no other load, side by side: each takes 0.4 us
+    if (FEW)
+#pragma unroll 1
+        for (int s = tid; s < a.c.seqs; s += PREP_THREADS) lens_here[s] = a.c.lens[s];
     // starts ascend: each is at least the largest before it
-    int top = 0, all;
+    int top = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        const int raw = a.group_starts[i];
-        if (raw < 0 || raw > a.c.seqs || raw > a.group_starts[i + 1] || a.prefix[i] < 0)
-            report(a.c.dev_err, CKV_DEV_BAD_COUNT);
-        top = max(top, start_at(i));
+        const int raw = a.group_starts[i], next = a.group_starts[i + 1];
+        if (raw < 0 || next > a.c.seqs || raw > next || a.prefix[i] < 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+        top = max(top, min(raw, a.c.seqs));
     }
-    int before = scan<true>(top, warp_val, &all), tiles = 0;
+    int before = scan<true>(top, warp_val).x, tiles = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        const int first = max(before, start_at(i)), end = max(first, start_at(i + 1));
+        const int first = max(before, min(a.group_starts[i], a.c.seqs));
+        const int members = max(first, min(a.group_starts[i + 1], a.c.seqs)) - first;
         before = first;
-        Group gr{first, end - first, 0, 0, 0, 0};
-        if (gr.members > 1) {
-            gr.rows = min(max(a.prefix[i], 0), rows_held(a.c, first)) / TILE * TILE;
-            gr.blocks = (int)(((long long)gr.members * a.g + QT - 1) / QT);
+        Group gr{first, members, 0, 0, 0, 0};
+        if (members > 1) {
+            gr.rows = max(0, min(a.prefix[i], min(lens[first], a.c.rows))) & ~(TILE - 1);
+            gr.blocks = (int)(((unsigned)members * a.g + QT - 1) / QT);
         }
-        a.group[i] = gr;
+        group[i] = gr;
         tiles += a.c.heads * gr.blocks * tiles_of(gr);
     }
-    int total, at = scan<false>(tiles, warp_val, &total);
-    const int even = (total + a.grid - 1) / a.grid;
-    int ctas[OWN_EXTRA + 1] = {};
+    const int2 at = scan<false>(tiles, warp_val);
+    const int total = at.y;
+    int sum = at.x;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-        a.tile_base[i] = at;
-        const Group gr = a.group[i];
-        const int nt = tiles_of(gr), units = a.c.heads * gr.blocks;
-        at += units * nt;
-        for (int x = 0; x <= OWN_EXTRA && even > 0; ++x)
-            ctas[x] = min(a.grid + 1, ctas[x] + min(a.grid + 1, units) * min(a.grid + 1, (nt + even + x - 1) / (even + x)));
+        base[i] = sum;
+        sum += a.c.heads * group[i].blocks * tiles_of(group[i]);
     }
-    for (int x = 0; x <= OWN_EXTRA; ++x)
-        if (ctas[x]) atomicAdd(&ctas_with[x], ctas[x]);
-    if (tid == 0) {
-        a.tile_base[a.groups] = total;
-        const int end = a.group_starts[a.groups];
-        if (end < 0 || end > a.c.seqs) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+    __syncthreads();
+    // the sequences
+    int own = 0, units = 0;  // (a thread counts up to 2^20 tiles: more changes no share)
+#pragma unroll 1
+    for (int s = tid; s < a.c.seqs; s += PREP_THREADS) {
+        const int held = lens[s];
+        // the last group that begins at s or before
+        int lo = -1, hi = a.groups;
+#pragma unroll 1
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (group[mid].first <= s) lo = mid;
+            else hi = mid;
+        }
+        const int rows = lo >= 0 && s < group[lo].first + group[lo].members ? group[lo].rows : 0;
+        if (rows > held) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+        a.skip[s] = rows;
+        a.group_of[s] = lo;
+        const int left = max(0, min(held, a.c.rows) - rows);
+        own = min(1 << 20, own + (int)((unsigned)(left + TILE - 1) / TILE));
+        units += left > 0;
+    }
+    if (own) {
+        atomicAdd(&own_tiles, own);
+        atomicAdd(&own_units, units);
+    }
+    __syncthreads();
+    int grid = total ? a.grid : 0;  // CTAs for the shared rows
+    const int own_ctas = a.c.heads * own_units;
+    if (total && own_tiles && total + own_ctas <= a.grid) {
+        grid = total;  // an SM for each
+    } else if (total && own_tiles) {
+        const float x = total * TILE_COST, y = a.c.heads * (own_tiles * OWN_COST) + own_ctas * UNIT_COST;
+        // x / P = t, y / (G - P) = t - MERGE_COST
+        const float b = a.grid * MERGE_COST + x + y, root = __fsqrt_rn(b * b - 4.f * a.grid * MERGE_COST * x);
+        grid = max(1, min(a.grid - 1, (int)(__fdividef(2.f * a.grid * x, b + root) + 0.5f)));
+    }
+    // units with CTAs of their own
+    const int even = grid ? parts_of(total, grid) : 0;
+#pragma unroll 1
+    for (int i = i0; i < i1 && even; ++i) {
+        const int n = min(grid + 1, a.c.heads * group[i].blocks);
+#pragma unroll 1
+        for (int x = 0; x <= OWN_EXTRA; ++x) {
+            const int more = n * min(grid + 1, parts_of(tiles_of(group[i]), even + x));
+            if (more) atomicAdd(&ctas_with[x], min(more, grid + 1));
+        }
     }
     __syncthreads();
     int part = 0;  // tiles of a part, 0: the even deal
     for (int x = OWN_EXTRA; x >= 0; --x)
-        if (total > 0 && ctas_with[x] <= a.grid) part = even + x;
+        if (even && ctas_with[x] <= grid) part = even + x;
     int mine = 0;
+#pragma unroll 1
     for (int i = i0; i < i1 && part; ++i) {
-        const Group gr = a.group[i];
-        mine += a.c.heads * gr.blocks * ((tiles_of(gr) + part - 1) / part);
+        const int parts = parts_of(tiles_of(group[i]), part);
+        group[i].parts = parts;
+        mine += a.c.heads * group[i].blocks * parts;
     }
-    at = scan<false>(mine, warp_val, &all);
-    for (int i = i0; i < i1 && part; ++i) {
-        a.group[i].parts = (tiles_of(a.group[i]) + part - 1) / part;
-        a.group[i].cta = at;
-        at += a.c.heads * a.group[i].blocks * a.group[i].parts;
-    }
-    if (tid == 0) *a.ctas = part ? all : 0;
-    __syncthreads();
-    for (int s = tid; s < a.c.seqs; s += PREP_THREADS) {
-        // the last group that begins at s or before
-        int lo = -1, hi = a.groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (a.group[mid].first <= s) lo = mid;
-            else hi = mid;
+    const int2 cta = scan<false>(mine, warp_val);
+    sum = cta.x;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        group[i].cta = sum;
+        sum += a.c.heads * group[i].blocks * group[i].parts;
+        if (FEW) {
+            a.group[i] = group[i];
+            a.tile_base[i] = base[i];
         }
-        int rows = 0;
-        if (lo >= 0 && s < a.group[lo].first + a.group[lo].members) rows = a.group[lo].rows;
-        if (rows > a.c.lens[s]) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
-        a.skip[s] = rows;
-        a.group_of[s] = lo;
+    }
+    __syncthreads();
+    const int used = part ? cta.y : min(grid, total);
+    const Deal deal(total, max(1, used), 1);
+#pragma unroll 1
+    for (int c = tid; c < a.grid; c += PREP_THREADS) {
+        Share v{};
+        if (c < used) {
+            if (!part) {
+                v.t = deal.begin_cta(c);
+                v.t_end = deal.begin_cta(c + 1);
+            }
+            int lo = 0, hi = a.groups;  // the last group whose CTAs (or tiles) begin at this one or before
+#pragma unroll 1
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (part ? group[mid].cta <= c : base[mid] <= v.t) lo = mid;
+                else hi = mid;
+            }
+            const Group gr = group[lo];
+            if (part) {
+                const int unit = (int)quotient(c - gr.cta, gr.parts), p = c - gr.cta - unit * gr.parts, nt = tiles_of(gr);
+                // the first nt % parts of the equal parts have a tile more
+                const int each = (int)quotient(nt, gr.parts), more = nt - each * gr.parts;
+                v.t = base[lo] + unit * nt + p * each + min(p, more);
+                v.t_end = v.t + each + (p < more);
+            }
+            v.group = lo;
+            v.run = run_in(gr, base[lo], v.t, v.t_end);
+        }
+        a.share[c] = v;
+    }
+    if (tid == 0) {
+        a.tile_base[a.groups] = total;
+        *a.own_ctas = max(1, a.grid - grid);
+        *a.deal = make_int2(part ? used : 0, max(1, used));
     }
 }
 
@@ -240,59 +363,17 @@ __device__ __forceinline__ int group_of_tile(const SharedArgs& a, int t, int fro
     }
     return a.groups - 1;
 }
-// the tiles of a CTA
-__device__ __forceinline__ int2 share_of(const SharedArgs& a, int cta, int lane) {
-    const int total = a.tile_base[a.groups], ctas = *a.ctas;
-    if (ctas == 0) {
-        const Deal deal(total, Deal::ctas(total, 1, a.grid), 1);
-        if (cta >= deal.n_cta || total == 0) return make_int2(0, 0);
-        return make_int2(deal.begin_cta(cta), deal.begin_cta(cta + 1));
-    }
-    if (cta >= ctas) return make_int2(0, 0);
-    // the last group with CTAs that begins at this one or before
-    int i = 0;
-    for (int b = 0; b < a.groups; b += 32) {
-        const bool here = b + lane < a.groups && a.group[b + lane].parts > 0 && a.group[b + lane].cta <= cta;
-        const unsigned m = __ballot_sync(FULL, here);
-        if (m) i = b + 31 - __clz(m);
-    }
-    const Group gr = a.group[i];
-    const int nt = (gr.rows + KT - 1) / KT, unit = (cta - gr.cta) / gr.parts, p = cta - gr.cta - unit * gr.parts;
-    const int t = a.tile_base[i] + unit * nt;
-    return make_int2(t + (int)((long long)nt * p / gr.parts), t + (int)((long long)nt * (p + 1) / gr.parts));
-}
-
-// A CTA's share of one unit.
-struct Run {
-    int group, first, members, rows;
-    int h, block;  // KV head, block of queries
-    int k0, n;     // tiles [k0, k0 + n) of the unit
-    int queries;   // in the block
-    bool begins;   // with the unit's first tile
-    long long row; // of the block's first query among all units'
-};
-// The block's queries in the order of the parts: group, KV head, member, query head.
-__device__ __forceinline__ long long row_of(const SharedArgs& a, const Group& gr, int h, int block) {
-    return ((long long)gr.first * a.c.heads + (long long)h * gr.members) * a.g + (long long)block * QT;
-}
 // The run that begins at tile t of a share that ends at t_end, for a whole warp.
 __device__ __forceinline__ Run run_at(const SharedArgs& a, int t, int t_end, int* from, int lane) {
-    Run r;
-    r.group = *from = group_of_tile(a, t, *from, lane);
-    const Group gr = a.group[r.group];
-    r.first = gr.first;
-    r.members = gr.members;
-    r.rows = gr.rows;
-    const int nt = (gr.rows + KT - 1) / KT;
-    const int left = t - a.tile_base[r.group], unit = left / nt;
-    r.k0 = left - unit * nt;
-    r.h = unit / gr.blocks;
-    r.block = unit - r.h * gr.blocks;
-    r.n = min(nt - r.k0, t_end - t);
-    r.begins = r.k0 == 0;
-    r.queries = min(QT, gr.members * a.g - r.block * QT);
-    r.row = row_of(a, gr, r.h, r.block);
-    return r;
+    const int i = *from = group_of_tile(a, t, *from, lane);
+    return run_in(a.group[i], a.tile_base[i], t, t_end);
+}
+__device__ __forceinline__ int queries_of(const SharedArgs& a, const Run& r) {
+    return min(QT, r.members * a.g - r.block * QT);
+}
+// The block's first query in the order of the parts: group, KV head, member, query head.
+__device__ __forceinline__ long long row_of(const SharedArgs& a, const Run& r) {
+    return ((long long)r.first * a.c.heads + (long long)r.h * r.members) * a.g + (long long)r.block * QT;
 }
 
 // Places of a CTA's j-th K and V in the order of the loads: K0 K1 V0 K2 V1 ...
@@ -302,25 +383,26 @@ __device__ __forceinline__ int v_index(int j) { return 2 * j + 2; }
 struct __align__(8) Bars {
     uint64_t full[NST], empty[NST];
     uint64_t q_full;
-    uint64_t s_full[NSP], p_full[NSP], m_empty[NSP];
+    uint64_t s_full[NSP], p_full[NSP], p_empty[NSP], top_empty[NSP];
+    uint64_t top_full[4];            // of a quarter of the queries
     uint64_t t_full, t_empty;
-    uint64_t never, drain;
+    uint64_t never, drain[2];
     int asked[NST];    // the last phase of a stage that was asked for
     int rows[NST];     // of a K stage's tile: those whose page is good
     int s_rows[NSP], t_rows;
     uint32_t tmem_base;
     int abort;
 };
-struct __align__(1024) Smem {
+struct Smem {
     unsigned char q[STAGE];
     unsigned char ring[NST][STAGE];
-    float m[NSP][QT];  // the maxima that a tile's weights go by
-    Bars bars;
+    float top[NSP][2][QT];  // a tile's largest scores, of either half of its rows
 };
-static_assert(sizeof(Smem) <= 232448 - 1024, "shared memory of a CTA");
+constexpr int SMEM_MOST = 232448;  // of a CTA
+static_assert(sizeof(Smem) + 1024 <= SMEM_MOST && sizeof(Bars) <= 1024, "the barriers take what aligning leaves");
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, const SharedArgs& a) {
-    if (ptx::mbar_wait(bar, parity, a.wait_limit, &b->abort)) return true;
+    if (ptx::mbar_wait_held(bar, parity, a.wait_limit, &b->abort)) return true;
     if (atomicExch(&b->abort, 1) == 0) report(a.c.dev_err, CKV_DEV_TIMEOUT);
     return false;
 }
@@ -329,8 +411,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     paged_shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv) {
     extern __shared__ unsigned char smem_raw[];
+    // swizzled tiles need 1024-byte alignment; the barriers stand before them
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023));
-    Bars* bs = &sm.bars;
+    __shared__ Bars bars;
+    Bars* bs = &bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -341,16 +425,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         ptx::mbar_init(&bs->q_full, OUT_WARPS);
         for (int i = 0; i < NSP; ++i) {
             ptx::mbar_init(&bs->s_full[i], 2);  // the product, and the thread that says of how many rows
-            ptx::mbar_init(&bs->p_full[i], SOFT_WARPS / 2);
-            ptx::mbar_init(&bs->m_empty[i], OUT_WARPS);
+            ptx::mbar_init(&bs->p_full[i], SOFT_WARPS);
+            ptx::mbar_init(&bs->p_empty[i], 1);
+            ptx::mbar_init(&bs->top_empty[i], OUT_WARPS);
         }
         ptx::mbar_init(&bs->t_full, 2);
         ptx::mbar_init(&bs->t_empty, OUT_WARPS);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&bs->top_full[i], 2);
         ptx::mbar_init(&bs->never, 1);
-        ptx::mbar_init(&bs->drain, 1);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&bs->drain[i], 1);
         bs->abort = 0;
         ptx::fence_barrier_init();
     }
+    if (warp == 0 && lane < 2) ptx::prefetch_tmap(lane ? &tv : &tk);
     if (warp == 1) {
         ptx::tmem_alloc(&bs->tmem_base, 512);
         ptx::tmem_relinquish();
@@ -362,18 +449,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
 
-    const int2 share = share_of(a, blockIdx.x, lane);
-    const int t_begin = share.x, t_end = share.y, n_tiles = t_end - t_begin;
+    const Share share = a.share[blockIdx.x];
+    const int t_begin = share.t, t_end = share.t_end, n_tiles = t_end - t_begin;
     bool alive = true;
-    int from = 0;  // the group to look from
+    int from = share.group;  // the group to look from
     int j = 0;     // tiles so far
-    const bool leader = ptx::elect_one();  // the lane of warp 1 that issues the products
+    const bool leader = ptx::elect_one();  // the lane that issues the warp's products
+    // the scale without its sign, which is in the queries; not 0, so that it
+    // leaves -inf what it is
+    const float qs = fmaxf(fabsf(a.qscale), 1.17549435e-38f);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         // In the order in which the products take them: K of a tile, then V of
         // the tile before it.
-        if (lane < 2) ptx::prefetch_tmap(lane ? &tv : &tk);
         const FastDiv& by_page = a.c.by_page;
         // this lane's copy of a tile: its page (-1: none), slot and place in the
         // stage; the tile's copies and rows, and its KV head
@@ -405,8 +494,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             return true;
         };
-        Run r{};
-        int k = 0, k_end = 0;
+        Run r = share.run;
+        int k = r.k0, k_end = r.k0 + r.n;
         for (; j <= n_tiles && alive; ++j) {
             last = now;
             if (j < n_tiles) {
@@ -434,154 +523,182 @@ __global__ void __launch_bounds__(THREADS, 1)
                            __reduce_max_sync(FULL, now.page >= 0 ? max(0, row + a.box_rows - r.rows) : 0);
                 ++k;
                 alive = load(now, k_index(j), &tk);
-                // the first K before all else: with every stage asked for at once
-                // it came with the last of them, 4 us later
-                if (j == 0 && alive) alive = __all_sync(FULL, wait(&bs->full[0], 0, bs, a));
+                // the first K and the queries before all else: with every stage
+                // asked for at once they came with the last of them, 4 us later
+                if (j == 0 && alive)
+                    alive = __all_sync(FULL, wait(&bs->full[0], 0, bs, a) && wait(&bs->q_full, 0, bs, a));
             }
             if (j > 0 && alive) alive = load(last, v_index(j - 1), &tv);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ the products
-        const uint32_t ring = ptx::smem_u32(sm.ring), qa = ptx::smem_u32(sm.q);
+        // ------------------------------------------------------------ S = Q K^T
+        // The lanes keep step for the runs; one waits and issues.  S and T are
+        // issued by warps of their own: a commit holds its thread until the
+        // products before it have begun, and the tensor core would run dry behind
+        // every one of them (3400 instead of 2700 cycles a tile).
+        const uint32_t ring = ptx::smem_u32(sm.ring);
+        const uint64_t q = ptx::smem_desc_sw128(ptx::smem_u32(sm.q));
         constexpr uint32_t ID_S = ptx::idesc_bf16_f32(QT, KT);
-        constexpr uint32_t ID_T = ptx::idesc_bf16_f32(QT, D) | ptx::IDESC_B_MN_MAJOR;
         int runs = 0;
-        // all lanes keep step for the runs; one waits and issues
+        Run r = share.run;
         for (int t = t_begin; t < t_end && alive; ++runs) {
-            const Run r = run_at(a, t, t_end, &from, lane);
+            if (runs > 0) r = run_at(a, t, t_end, &from, lane);
             if (leader) {
                 if (runs == 0 && a.stall && !wait(&bs->never, 0, bs, a)) alive = false;
-                if (alive && !wait(&bs->q_full, runs & 1, bs, a)) alive = false;
-                auto score = [&](int jj) {  // S of the CTA's jj-th tile
-                    const int it = k_index(jj), st = it % NST, b = jj % NSP;
-                    if (!wait(&bs->full[st], (it / NST) & 1, bs, a)) return false;
+                if (alive) alive = wait(&bs->q_full, runs & 1, bs, a);
+                for (int jj = j; jj < j + r.n && alive; ++jj) {
+                    const int it = k_index(jj), st = it % NST, b = jj % NSP, use = jj / NSP;
+                    alive = wait(&bs->full[st], (it / NST) & 1, bs, a) &&
+                            (use == 0 || wait(&bs->p_empty[b], (use - 1) & 1, bs, a));
+                    if (!alive) break;
                     ptx::tc_fence_after();
                     const int n = bs->rows[st];
                     bs->s_rows[b] = n;
-                    const uint64_t qd = ptx::smem_desc_sw128(qa), kd = ptx::smem_desc_sw128(ring + st * STAGE);
+                    ptx::mbar_arrive(&bs->s_full[b]);
+                    const uint64_t kd = ptx::smem_desc_sw128(ring + st * STAGE);
                     if (n > 0)
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
                             const uint32_t at = ((ks >> 2) * PANEL + (ks & 3) * 32) >> 4;
-                            ptx::mma_bf16(tmem + b * SP_COLS, qd + at, kd + at, ID_S, ks > 0);
+                            ptx::mma_bf16(tmem + b * SP_COLS, q + at, kd + at, ID_S, ks > 0);
                         }
-                    ptx::mma_commit(&bs->empty[st]);
                     ptx::mma_commit(&bs->s_full[b]);
-                    ptx::mbar_arrive(&bs->s_full[b]);
-                    return true;
-                };
-                auto value = [&](int jj) {  // T of the CTA's jj-th tile
-                    const int it = v_index(jj), st = it % NST, b = jj % NSP;
-                    if (!wait(&bs->full[st], (it / NST) & 1, bs, a) || !wait(&bs->p_full[b], (jj / NSP) & 1, bs, a) ||
-                        (jj > 0 && !wait(&bs->t_empty, (jj - 1) & 1, bs, a)))
-                        return false;
-                    ptx::tc_fence_after();
-                    const int n = bs->s_rows[b], steps = n / 16;
-                    bs->t_rows = n;
-                    // the low terms first; eight columns hold a term of 16 rows
-                    const uint32_t p = tmem + b * SP_COLS;
-                    const uint64_t v = ptx::smem_desc_sw128_mn(ring + st * STAGE, PANEL);
-#pragma unroll
-                    for (int term = 0; term < 3; ++term)
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) {
-                            const uint32_t at = term == 1 ? MID_COL + 8 * ks : (ks >> 1) * 32 + (ks & 1) * 8 + (term ? 0 : 16);
-                            if (ks < steps)
-                                ptx::mma_bf16_ts(tmem + T_COL, p + at, v + (ks * 2048 >> 4), ID_T, term > 0 || ks > 0);
-                        }
-                    ptx::mma_commit(&bs->empty[st]);
-                    ptx::mma_commit(&bs->t_full);
-                    ptx::mbar_arrive(&bs->t_full);
-                    return true;
-                };
-                // scores run a tile ahead of the values, into the buffer that the
-                // value before has read
-                for (int k = 0; k <= r.n && alive; ++k) {
-                    if (k < r.n) alive = score(j + k);
-                    if (k > 0 && alive) alive = value(j + k - 1);
                 }
             }
             alive = __all_sync(FULL, alive);
             j += r.n;
             t += r.n;
         }
+    } else if (warp == VALUE_WARP) {
+        // ------------------------------------------------------------ T = P V
+        const uint32_t ring = ptx::smem_u32(sm.ring);
+        constexpr uint32_t ID_T = ptx::idesc_bf16_f32(QT, D) | ptx::IDESC_B_MN_MAJOR;
+        if (leader)
+            for (int jj = 0; jj < n_tiles && alive; ++jj) {
+                const int it = v_index(jj), st = it % NST, b = jj % NSP, use = jj / NSP;
+                alive = wait(&bs->full[st], (it / NST) & 1, bs, a) && wait(&bs->p_full[b], use & 1, bs, a);
+                if (!alive) break;
+                const int n = bs->s_rows[b], steps = n / 16;
+                const uint32_t p = tmem + b * SP_COLS;
+                const uint64_t v = ptx::smem_desc_sw128_mn(ring + st * STAGE, PANEL);
+                alive = jj == 0 || wait(&bs->t_empty, (jj - 1) & 1, bs, a);
+                if (!alive) break;
+                ptx::tc_fence_after();
+                bs->t_rows = n;
+                ptx::mbar_arrive(&bs->t_full);
+                // the low terms first; eight columns hold a term of 16 rows.
+                // (Straight code for all 24 products takes 5 us at its first pass,
+                // when it has to be fetched.)
+#pragma unroll 1
+                for (int term = 0; term < 3; ++term) {
+                    uint32_t at = p + (term == 1 ? MID_COL : term ? 0 : LOW_COL);
+                    const uint32_t pairs = term == 1 ? 16 : 32;  // columns from two steps' terms to the next two's
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks += 2) {
+                        if (ks < steps)
+                            ptx::mma_bf16_ts(tmem + T_COL, at, v + (ks * 2048 >> 4), ID_T, term > 0 || ks > 0);
+                        if (ks + 1 < steps)
+                            ptx::mma_bf16_ts(tmem + T_COL, at + 8, v + ((ks + 1) * 2048 >> 4), ID_T, 1);
+                        at += pairs;
+                    }
+                }
+                ptx::mma_commit(&bs->t_full);
+                ptx::mma_commit(&bs->p_empty[b]);
+            }
+        __syncwarp();
     } else if (warp < 2 + SOFT_WARPS) {
         // ------------------------------------------------------------ softmax
-        const int odd = (warp - 2) >> 2, quarter = warp & 3;
+        const int half = (warp - 2) >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
-        // its sign is in the queries; not 0, so that it leaves -inf what it is
-        const float qs = fmaxf(fabsf(a.qscale), 1.17549435e-38f);
         const uint64_t qs2 = pair(qs, qs), minus2 = pair(-1.f, -1.f);
+        int exchanges = 0;
+        Run r = share.run;
         for (int t = t_begin; t < t_end && alive;) {
-            const Run r = run_at(a, t, t_end, &from, lane);
-            const bool busy = quarter * 32 < r.queries;  // some of the warp's queries exist
+            if (t > t_begin) r = run_at(a, t, t_end, &from, lane);
+            const bool busy = quarter * 32 < queries_of(a, r);  // some of the warp's queries exist
             float m = -INFINITY, l = 0.f;
-            for (int k = (j & 1) == odd ? 0 : 1; k < r.n; k += 2) {
+            for (int k = 0; k < r.n; ++k) {
                 const int b = (j + k) % NSP, use = (j + k) / NSP;
                 const uint32_t sp = tmem + ((uint32_t)(quarter * 32) << 16) + b * SP_COLS;
-                if (!__all_sync(FULL, wait(&bs->s_full[b], use & 1, bs, a)) ||
-                    (use > 0 && !__all_sync(FULL, wait(&bs->m_empty[b], (use - 1) & 1, bs, a)))) {
-                    alive = false;
-                    break;
-                }
-                const int n = bs->s_rows[b];
+                alive = __all_sync(FULL, wait(&bs->s_full[b], use & 1, bs, a) &&
+                                             (use == 0 || wait(&bs->top_empty[b], (use - 1) & 1, bs, a)));
+                if (!alive) break;
+                if (warp == 2 && lane == 0) ptx::mbar_arrive(&bs->empty[k_index(j + k) % NST]);
+                const int n = bs->s_rows[b], mine = n - 64 * half;  // rows of this half of the tile
                 if (busy && n > 0) {
                     ptx::tc_fence_after();
-                    const int chunks = (n + 31) / 32;
+                    // 16 rows at a time, of which there are `mine` / 16 at most four
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    for (int c = 0; c < chunks; ++c) {
-                        uint32_t s[32];
-                        ptx::tmem_ld32(sp + c * 32, s);
+#pragma unroll 1
+                    for (int c = 0; c < 64 && c < mine; c += 32) {
+                        uint32_t s[2][16];
+                        ptx::tmem_ld16(sp + half * 64 + c, s[0]);
+                        ptx::tmem_ld16(sp + half * 64 + c + 16, s[1]);
                         ptx::tmem_ld_wait();
+                        const bool both = c + 16 < mine;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
-                        if (c * 32 + 32 <= n)  // else 16 rows
-#pragma unroll
-                            for (int e = 16; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
+                        for (int e = 0; e < 16; ++e) {
+                            const float x = __uint_as_float(s[0][e]), y = __uint_as_float(s[1][e]);
+                            top[e & 3] = fmaxf(fmaxf(top[e & 3], x), both ? y : x);
+                        }
                     }
-                    const float grown = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * qs);
+                    const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    // the other half's, so that all of a query's weights go by one maximum
+                    sm.top[b][half][row] = own;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&bs->top_full[quarter]);
+                    alive = __all_sync(FULL, wait(&bs->top_full[quarter], exchanges & 1, bs, a));
+                    if (!alive) break;
+                    ++exchanges;
+                    const float grown = fmaxf(m, fmaxf(own, sm.top[b][1 - half][row]) * qs);
                     const float ms = grown == -INFINITY ? 0.f : grown;
                     l *= ex2(m - ms);
                     m = grown;
                     const uint64_t ms2 = pair(-ms, -ms);
                     uint64_t sum[2] = {0, 0};
-                    for (int c = 0; c < chunks; ++c) {
+#pragma unroll 1
+                    for (int c = 0; c < 64 && c < mine; c += 32) {
                         uint32_t s[32], hi[16], mid[16], lo[16];
-                        ptx::tmem_ld32(sp + c * 32, s);
+                        ptx::tmem_ld32(sp + half * 64 + c, s);
                         ptx::tmem_ld_wait();
-                        if (c * 32 + 32 > n)  // 16 rows: the others weigh nothing
+                        if (c + 16 >= mine)  // 16 rows: the others weigh nothing
 #pragma unroll
                             for (int e = 16; e < 32; ++e) s[e] = 0xff800000u;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const float2 x = unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), qs2, ms2));
-                            const float p0 = ex2(x.x), p1 = ex2(x.y);
+                            s[e] = __float_as_uint(ex2(x.x));
+                            s[e + 1] = __float_as_uint(ex2(x.y));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float p0 = __uint_as_float(s[e]), p1 = __uint_as_float(s[e + 1]);
                             const uint64_t p = pair(p0, p1);
                             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], p);
                             // a float's upper 16 bits are a bf16, and what they leave is exact
-                            hi[e / 2] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                            hi[e / 2] = __byte_perm(s[e], s[e + 1], 0x7632);
                             const uint64_t rest = fma2(pair(upper(p0), upper(p1)), minus2, p);
                             const float2 y = unpair(rest);
                             mid[e / 2] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
                             const float2 z = unpair(fma2(pair(upper(y.x), upper(y.y)), minus2, rest));
                             lo[e / 2] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
                         }
-                        ptx::tmem_st16(sp + c * 32, hi);
-                        ptx::tmem_st16(sp + c * 32 + 16, lo);
-                        ptx::tmem_st16(sp + MID_COL + c * 16, mid);
+                        // over the scores just read
+                        ptx::tmem_st16(sp + half * 64 + c, hi);
+                        ptx::tmem_st16(sp + half * 64 + c + LOW_COL, lo);
+                        ptx::tmem_st16(sp + MID_COL + half * 32 + c / 2, mid);
                     }
                     ptx::tmem_st_wait();
                     const float2 x = unpair(add2(sum[0], sum[1]));
                     l += x.x + x.y;
                     ptx::tc_fence_before();
-                    sm.m[b][row] = m;
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bs->p_full[b]);
             }
-            if (alive && row < r.queries)
-                reinterpret_cast<float2*>(r.begins ? a.unit_ml + r.row + row
-                                                   : a.cta_ml + (size_t)blockIdx.x * QT + row)[odd] = make_float2(m, l);
+            if (alive && row < queries_of(a, r))
+                reinterpret_cast<float2*>(r.k0 == 0 ? a.unit_ml + row_of(a, r) + row
+                                                    : a.cta_ml + (size_t)blockIdx.x * QT + row)[half] = make_float2(m, l);
             j += r.n;
             t += r.n;
         }
@@ -591,72 +708,71 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int row = quarter * 32 + lane, tid = threadIdx.x - 32 * (2 + SOFT_WARPS);
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + T_COL + half * 64;
         const uint32_t sign = a.qscale < 0.f ? 0x80008000u : 0u;
+        auto both = [](const uint32_t (&v)[16], int e) { return pair(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])); };
         // the run's queries to shared memory, swizzled as TMA does
         auto queries = [&](const Run& r) {
-            const int piece = tid & 15;
-            uint4 v[QT * 16 / (32 * OUT_WARPS)];
+            constexpr int N = QT * 16 / (32 * OUT_WARPS);  // pieces of 16 bytes that a thread brings
+            const int piece = tid & 15, all = queries_of(a, r);
+            const unsigned char* from = a.q + r.first * a.qst[0] + (long long)r.h * a.g * a.qst[1] + piece * 16;
+            uint4 v[N];
+            // all of them under way at once: a row behind the last is the last one again
 #pragma unroll
-            for (int i = 0; i < QT * 16 / (32 * OUT_WARPS); ++i) {
-                const int y = (tid >> 4) + i * 2 * OUT_WARPS;
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (y < r.queries) {
-                    const int x = r.block * QT + y, member = x / a.g;
-                    v[i] = *reinterpret_cast<const uint4*>(a.q + (r.first + member) * a.qst[0] +
-                                                           ((long long)r.h * a.g + (x - member * a.g)) * a.qst[1] + piece * 16);
-                    v[i].x ^= sign, v[i].y ^= sign, v[i].z ^= sign, v[i].w ^= sign;
-                }
+            for (int i = 0; i < N; ++i) {
+                int head;
+                const int member = a.by_g.quot(r.block * QT + min((tid >> 4) + i * 2 * OUT_WARPS, all - 1), &head);
+                v[i] = *reinterpret_cast<const uint4*>(from + member * a.qst[0] + head * a.qst[1]);
             }
 #pragma unroll
-            for (int i = 0; i < QT * 16 / (32 * OUT_WARPS); ++i) {
+            for (int i = 0; i < N; ++i) {
                 const int y = (tid >> 4) + i * 2 * OUT_WARPS;
+                v[i].x ^= sign, v[i].y ^= sign, v[i].z ^= sign, v[i].w ^= sign;
                 *reinterpret_cast<uint4*>(sm.q + (piece >> 3) * PANEL + y * 128 + (((piece & 7) ^ (y & 7)) << 4)) = v[i];
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bs->q_full);
         };
-        Run r{};
-        if (t_begin < t_end) {
-            r = run_at(a, t_begin, t_end, &from, lane);
-            queries(r);
-        }
+        Run r = share.run;
+        if (t_begin < t_end) queries(r);
         for (int t = t_begin; t < t_end && alive;) {
-            const bool busy = quarter * 32 < r.queries;
-            float o[64], m = -INFINITY;
+            const bool busy = quarter * 32 < queries_of(a, r);
+            uint64_t o[32];
+            float m = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) o[c] = 0.f;
+            for (int c = 0; c < 32; ++c) o[c] = 0;
             for (int k = 0; k < r.n; ++k) {
                 const int jj = j + k;
                 if (!__all_sync(FULL, wait(&bs->t_full, jj & 1, bs, a))) {
                     alive = false;
                     break;
                 }
-                if (busy && bs->t_rows > 0) {
+                const int b = jj % NSP, n = bs->t_rows;
+                const float mt = fmaxf(sm.top[b][0][row], sm.top[b][1][row]);
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(&bs->top_empty[b]);
+                    if (warp == VALUE_WARP - 1) ptx::mbar_arrive(&bs->empty[v_index(jj) % NST]);
+                }
+                if (busy && n > 0) {
                     ptx::tc_fence_after();
-                    const float mt = sm.m[jj % NSP][row], grown = fmaxf(m, mt), ms = grown == -INFINITY ? 0.f : grown;
-                    const float x = ex2(m - ms), y = ex2(mt - ms);
+                    // the softmax's running maximum, made the same way
+                    const float grown = fmaxf(m, mt * qs), x = ex2(m - (grown == -INFINITY ? 0.f : grown));
                     m = grown;
-                    const bool plain = __all_sync(FULL, x == 1.f && y == 1.f);
+                    const uint64_t x2 = pair(x, x);
+                    // two loads under way at a time
+                    uint32_t v[2][16];
+                    ptx::tmem_ld16(at, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        uint32_t v[16];
-                        ptx::tmem_ld16(at + c, v);
+                    for (int c = 0; c < 4; ++c) {
                         ptx::tmem_ld_wait();
-                        if (plain) {
+                        if (c < 3) ptx::tmem_ld16(at + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[c + e] += __uint_as_float(v[e]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[c + e] = fmaf(o[c + e], x, __uint_as_float(v[e]) * y);
-                        }
+                        for (int e = 0; e < 8; ++e) o[8 * c + e] = fma2(o[8 * c + e], x2, both(v[c & 1], e));
                     }
                     ptx::tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive(&bs->t_empty);
-                    ptx::mbar_arrive(&bs->m_empty[jj % NSP]);
-                }
+                if (lane == 0) ptx::mbar_arrive(&bs->t_empty);
             }
             if (!alive) break;
             // every product of the run has ended with its last T: the queries make room
@@ -667,13 +783,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 r = run_at(a, t, t_end, &from, lane);
                 queries(r);
             }
-            if (row < done.queries) {
-                const int stride = done.begins ? done.queries : QT;
-                float4* to = (done.begins ? a.unit_o + done.row * (D / 4) : a.cta_o + (size_t)blockIdx.x * QT * (D / 4)) +
+            if (row < queries_of(a, done)) {
+                const int stride = done.k0 == 0 ? queries_of(a, done) : QT;
+                float4* to = (done.k0 == 0 ? a.unit_o + row_of(a, done) * (D / 4) : a.cta_o + (size_t)blockIdx.x * QT * (D / 4)) +
                              half * 16 * stride + row;
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    to[c * stride] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                for (int c = 0; c < 16; ++c) {
+                    const float2 u = unpair(o[2 * c]), v = unpair(o[2 * c + 1]);
+                    to[c * stride] = make_float4(u.x, u.y, v.x, v.y);
+                }
             }
         }
     }
@@ -686,9 +804,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0 && lane == 0)
             for (int i = 0; i < NST; ++i)
                 if (bs->asked[i] >= 0) ptx::mbar_wait(&bs->full[i], bs->asked[i] & 1, a.wait_limit, nullptr);
-        if (warp == 1 && leader) {
-            ptx::mma_commit(&bs->drain);
-            ptx::mbar_wait(&bs->drain, 0, a.wait_limit, nullptr);
+        if ((warp == 1 || warp == VALUE_WARP) && leader) {
+            ptx::mma_commit(&bs->drain[warp == 1]);
+            ptx::mbar_wait(&bs->drain[warp == 1], 0, a.wait_limit, nullptr);
         }
     }
     if (warp == 1) {
@@ -709,12 +827,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
     ptx::allow_dependent_launch();
     const int channel = threadIdx.x / JOIN_ROWS, heads_q = a.c.heads * a.g;  // four channels
     const long long n = (long long)a.c.seqs * heads_q, step = (long long)gridDim.x * JOIN_ROWS;
-    const int total = a.tile_base[a.groups], ctas = *a.ctas;
-    const Deal deal(total, Deal::ctas(total, 1, a.grid), 1);
+    const int total = a.tile_base[a.groups], ctas = a.deal->x;
+    const Deal deal(total, Deal::ctas(total, 1, a.deal->y), 1);
     for (long long row = (long long)blockIdx.x * JOIN_ROWS + threadIdx.x % JOIN_ROWS; row < n; row += step) {
         const int some = (int)(row / heads_q);  // a sequence of the group
-        if (a.skip[some] == 0) continue;
         const int i = a.group_of[some];
+        if (a.skip[some] == 0) continue;
         const Group gr = a.group[i];
         const int nt = (gr.rows + KT - 1) / KT, all = gr.members * a.g;
         const int left = (int)(row - (long long)gr.first * heads_q), h = left / all, x = left - h * all;
@@ -761,7 +879,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
 
 // ---------------------------------------------------------------- host side
 struct Layout {
-    size_t attn, group, tile_base, skip, group_of, ctas, unit_o, unit_ml, cta_o, cta_ml, total;
+    size_t attn, group, tile_base, skip, group_of, share, deal, own_ctas, unit_o, unit_ml, cta_o, cta_ml, total;
 };
 Layout layout_of(const Cache& c, int g) {
     Layout l;
@@ -772,8 +890,10 @@ Layout layout_of(const Cache& c, int g) {
     l.tile_base = l.group + up(S * sizeof(Group));
     l.skip = l.tile_base + up((S + 1) * sizeof(int));
     l.group_of = l.skip + up(S * sizeof(int));
-    l.ctas = l.group_of + up(S * sizeof(int));
-    l.unit_o = l.ctas + up(sizeof(int));
+    l.share = l.group_of + up(S * sizeof(int));
+    l.deal = l.share + up(MAX_GRID * sizeof(Share));
+    l.own_ctas = l.deal + up(sizeof(int2));
+    l.unit_o = l.own_ctas + up(sizeof(int));
     l.unit_ml = l.unit_o + up(queries * D * sizeof(float));
     l.cta_o = l.unit_ml + up(queries * sizeof(float4));
     l.cta_ml = l.cta_o + (size_t)MAX_GRID * QT * D * sizeof(float);
@@ -792,19 +912,25 @@ cudaError_t launch_shared(SharedArgs& a, void* workspace, cudaStream_t s) {
     if (!encode_pool(&tk, a.c, a.c.K, a.c.ks, true, true, a.box_rows, 1) ||
         !encode_pool(&tv, a.c, a.c.V, a.c.vs, true, true, a.box_rows, 1))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = sizeof(Smem) + 1024;
+    // all of an SM's but what the barriers take: aligned behind them the rest is there
+    constexpr size_t smem = SMEM_MOST - (sizeof(Bars) + 15) / 16 * 16;
+    static_assert((sizeof(Bars) + 15) / 16 * 16 + smem >= 1024 + sizeof(Smem), "tiles behind the barriers");
     static std::atomic<bool> set[MAX_DEVICES];
     if (!set[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(paged_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncAttributes at;
+        cudaError_t e = cudaFuncGetAttributes(&at, paged_shared_kernel);
+        if (e == cudaSuccess && at.sharedSizeBytes > (sizeof(Bars) + 15) / 16 * 16) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(paged_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    cudaError_t e = launch_dependent(paged_shared_prep, dim3(1), dim3(PREP_THREADS), 0, s, a);
+    const bool few = a.groups <= FEW_GROUPS && a.c.seqs <= FEW_SEQS;
+    cudaError_t e = launch_dependent(few ? paged_shared_prep<true> : paged_shared_prep<false>, dim3(1), dim3(PREP_THREADS), 0, s, a);
     if (e == cudaSuccess) e = launch_dependent(paged_shared_kernel, dim3(a.grid), dim3(THREADS), smem, s, a, tk, tv);
     const long long qst[2] = {a.qst[0] / 2, a.qst[1] / 2};
     if (e == cudaSuccess)
-        e = launch_attn_own_rows(a.c, a.skip, a.q, qst, a.g, a.qscale, a.out, a.lse, workspace, s);
+        e = launch_attn_own_rows(a.c, a.skip, a.own_ctas, a.q, qst, a.g, a.qscale, a.out, a.lse, workspace, s);
     const long long queries = (long long)a.c.seqs * a.c.heads * a.g, blocks = (queries + JOIN_ROWS - 1) / JOIN_ROWS;
     if (e == cudaSuccess)
         e = launch_dependent(paged_shared_join, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(JOIN_THREADS), 0, s, a);
@@ -859,6 +985,7 @@ extern "C" ckv_status ckv_paged_shared_attn(const ckv_paged_cache* cache, const 
     unsigned char* w = static_cast<unsigned char*>(workspace);
     a.q = static_cast<const unsigned char*>(q);
     a.g = g;
+    a.by_g = FastDiv((uint32_t)g);
     a.group_starts = group_starts;
     a.prefix = prefix;
     a.groups = groups;
@@ -869,7 +996,9 @@ extern "C" ckv_status ckv_paged_shared_attn(const ckv_paged_cache* cache, const 
     a.skip = reinterpret_cast<int32_t*>(w + l.skip);
     a.group_of = reinterpret_cast<int*>(w + l.group_of);
     attn_workspace(a.c, g, &a.own_lse2, workspace);
-    a.ctas = reinterpret_cast<int*>(w + l.ctas);
+    a.share = reinterpret_cast<Share*>(w + l.share);
+    a.deal = reinterpret_cast<int2*>(w + l.deal);
+    a.own_ctas = reinterpret_cast<int*>(w + l.own_ctas);
     a.unit_o = reinterpret_cast<float4*>(w + l.unit_o);
     a.unit_ml = reinterpret_cast<float4*>(w + l.unit_ml);
     a.cta_o = reinterpret_cast<float4*>(w + l.cta_o);
