@@ -134,36 +134,35 @@ struct SharedArgs {
 };
 
 // ---------------------------------------------------------------- the groups
-// The prep runs alone, once a call, so that every instruction of it is fetched
-// at some 60 ns for 128 bytes: its length counts for more than its work, and
-// what it does more than once are calls.
-__device__ __noinline__ unsigned quotient(unsigned n, unsigned d) { return n / d; }
-__device__ __forceinline__ int parts_of(int n, int d) { return (int)quotient((unsigned)n + d - 1, d); }
-
-// the sum of v over the threads before (the largest of theirs where MAX), and over all
+// the sum of v over the lanes before (the largest of theirs where MAX), v not negative
 template <bool MAX>
-__device__ __noinline__ int2 scan(int v, int* warp_val) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll 1
+__device__ __forceinline__ int lanes_before(int v, int lane) {
+    int x = __shfl_up_sync(FULL, v, 1);
+    if (lane == 0) x = 0;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(FULL, x, o);
         if (lane >= o) x = MAX ? max(x, y) : x + y;
     }
-    if (lane == 31) warp_val[warp] = x;
+    return x;
+}
+// the same over the threads of the CTA, and over all
+template <bool MAX>
+__device__ __forceinline__ int2 threads_before(int v, int* warp_val) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = lanes_before<MAX>(v, lane), all = 0;
+    if (lane == 31) warp_val[warp] = MAX ? max(x, v) : x + v;
     __syncthreads();
-    int before = __shfl_up_sync(FULL, x, 1), all = 0;
-    if (lane == 0) before = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < PREP_THREADS / 32; ++w) {
         const int y = warp_val[w];
-        if (w < warp) before = MAX ? max(before, y) : before + y;
+        if (w < warp) x = MAX ? max(x, y) : x + y;
         all = MAX ? max(all, y) : all + y;
     }
     __syncthreads();
-    return make_int2(before, all);
+    return make_int2(x, all);
 }
-
+__device__ __forceinline__ int parts_of(int n, int d) { return (int)(((unsigned)n + d - 1) / (unsigned)d); }
 __device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigned)(gr.rows + KT - 1) / KT); }
 
 // How the SMs and the tiles are dealt out.
@@ -183,26 +182,35 @@ __device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigne
 // taken where its largest part is at most OWN_EXTRA tiles above an even share.
 constexpr float TILE_COST = 1.7f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 3.f;  // us
 constexpr int OWN_EXTRA = 2;
-// groups, and sequences, up to which their numbers are kept in shared memory
-constexpr int FEW_GROUPS = PREP_THREADS, FEW_SEQS = 1024;
-
+// The SMs for the shared rows, of `grid`: `total` tiles of these, and of the own
+// rows `own` tiles of 16 of `units` (sequence, KV head) pairs.
+__device__ __forceinline__ int ctas_for_shared(int grid, int total, float own, int units) {
+    if (total == 0 || units == 0) return total ? grid : 0;
+    if (total + (long long)units <= grid) return total;  // an SM for each
+    const float x = total * TILE_COST, y = own * OWN_COST + units * UNIT_COST;
+    // P = x / t, G - P = y / (t - MERGE_COST)
+    const float b = grid * MERGE_COST + x + y, root = __fsqrt_rn(b * b - 4.f * grid * MERGE_COST * x);
+    return max(1, min(grid - 1, (int)(__fdividef(2.f * grid * x, b + root) + 0.5f)));
+}
 // the run that begins at tile t, in a group whose tiles begin at `base`, of a share that ends at t_end
 __device__ __forceinline__ Run run_in(const Group& gr, int base, int t, int t_end) {
-    const int nt = tiles_of(gr), unit = (int)quotient(t - base, nt), k0 = t - base - unit * nt;
-    const int h = (int)quotient(unit, gr.blocks);
+    const int nt = tiles_of(gr), unit = (int)((unsigned)(t - base) / (unsigned)nt), k0 = t - base - unit * nt;
+    const int h = (int)((unsigned)unit / (unsigned)gr.blocks);
     return Run{gr.first, gr.members, gr.rows, h, unit - h * gr.blocks, k0, min(nt - k0, t_end - t)};
 }
 
-// One CTA.  A thread has a chunk of neighbouring groups (one, where FEW), then
-// every PREP_THREADS-th sequence, then CTAs.
+// One CTA.  A thread has a chunk of neighbouring groups, then every
+// PREP_THREADS-th sequence, then CTAs.  FEW: at most 32 groups, which are warp
+// 0's, a lane each, and FEW_SEQS sequences, with their numbers in shared memory.
+// It is the latency of a chain of small steps, 1.1 us of it the first loads.
+constexpr int FEW_GROUPS = 32, FEW_SEQS = 1024;
 template <bool FEW>
 __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_constant__ SharedArgs a) {
     __shared__ int warp_val[PREP_THREADS / 32];
-    __shared__ int ctas_with[OWN_EXTRA + 1];
-    __shared__ int own_tiles, own_units;
+    __shared__ int ctas_with[OWN_EXTRA + 1], own_tiles, own_units, of_deal[4];
     __shared__ Group group_here[FEW ? FEW_GROUPS : 1];
     __shared__ int base_here[FEW ? FEW_GROUPS : 1], lens_here[FEW ? FEW_SEQS : 1];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid <= OWN_EXTRA) ctas_with[tid] = 0;
     if (tid == 0) own_tiles = own_units = 0;
     Group* group = FEW ? group_here : a.group;
@@ -210,45 +218,64 @@ __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_c
     const int* lens = FEW ? lens_here : a.c.lens;
     const int chunk = FEW ? 1 : (a.groups + PREP_THREADS - 1) / PREP_THREADS;
     const int i0 = min(a.groups, tid * chunk), i1 = min(a.groups, i0 + chunk);
+    auto before = [&](bool largest, int v) {
+        if (FEW) {
+            const int x = largest ? lanes_before<true>(v, lane) : lanes_before<false>(v, lane);
+            return make_int2(x, __shfl_sync(FULL, x + v, 31));  // (the largest of all is not asked for)
+        }
+        return largest ? threads_before<true>(v, warp_val) : threads_before<false>(v, warp_val);
+    };
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
-    // what goes by no other load, side by side: each takes 0.4 us
-    if (FEW)
+    // what goes by no other load, side by side
+    int start = 0, next = 0, shared = 0;
+    if (FEW) {
 #pragma unroll 1
         for (int s = tid; s < a.c.seqs; s += PREP_THREADS) lens_here[s] = a.c.lens[s];
-    // starts ascend: each is at least the largest before it
-    int top = 0;
-#pragma unroll 1
-    for (int i = i0; i < i1; ++i) {
-        const int raw = a.group_starts[i], next = a.group_starts[i + 1];
-        if (raw < 0 || next > a.c.seqs || raw > next || a.prefix[i] < 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
-        top = max(top, min(raw, a.c.seqs));
-    }
-    int before = scan<true>(top, warp_val).x, tiles = 0;
-#pragma unroll 1
-    for (int i = i0; i < i1; ++i) {
-        const int first = max(before, min(a.group_starts[i], a.c.seqs));
-        const int members = max(first, min(a.group_starts[i + 1], a.c.seqs)) - first;
-        before = first;
-        Group gr{first, members, 0, 0, 0, 0};
-        if (members > 1) {
-            gr.rows = max(0, min(a.prefix[i], min(lens[first], a.c.rows))) & ~(TILE - 1);
-            gr.blocks = (int)(((unsigned)members * a.g + QT - 1) / QT);
+        if (i0 < i1) {
+            start = a.group_starts[i0];
+            next = a.group_starts[i0 + 1];
+            shared = a.prefix[i0];
         }
-        group[i] = gr;
-        tiles += a.c.heads * gr.blocks * tiles_of(gr);
+        __syncthreads();
     }
-    const int2 at = scan<false>(tiles, warp_val);
-    const int total = at.y;
-    int sum = at.x;
+    int total = 0, sum = 0;
+    if (!FEW || warp == 0) {
+        // starts ascend: each is at least the largest before it
+        int top = 0, tiles = 0;
 #pragma unroll 1
-    for (int i = i0; i < i1; ++i) {
-        base[i] = sum;
-        sum += a.c.heads * group[i].blocks * tiles_of(group[i]);
+        for (int i = i0; i < i1; ++i) {
+            if (!FEW) start = a.group_starts[i], next = a.group_starts[i + 1], shared = a.prefix[i];
+            if (start < 0 || next > a.c.seqs || start > next || shared < 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+            top = max(top, min(start, a.c.seqs));
+        }
+        int from = before(true, top).x;
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            if (!FEW) start = a.group_starts[i], next = a.group_starts[i + 1], shared = a.prefix[i];
+            const int first = max(from, min(start, a.c.seqs)), members = max(first, min(next, a.c.seqs)) - first;
+            from = first;
+            Group gr{first, members, 0, 0, 0, 0};
+            if (members > 1) {
+                gr.rows = max(0, min(shared, min(lens[first], a.c.rows))) & ~(TILE - 1);
+                gr.blocks = (int)(((unsigned)members * a.g + QT - 1) / QT);
+            }
+            group[i] = gr;
+            tiles += a.c.heads * gr.blocks * tiles_of(gr);
+        }
+        const int2 at = before(false, tiles);
+        total = at.y;
+        sum = at.x;
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            base[i] = sum;
+            sum += a.c.heads * group[i].blocks * tiles_of(group[i]);
+        }
+        if (FEW && i0 < i1) a.tile_base[i0] = base[i0];
     }
     __syncthreads();
-    // the sequences
-    int own = 0, units = 0;  // (a thread counts up to 2^20 tiles: more changes no share)
+    // the sequences; a thread counts up to 2^20 tiles of own rows, more changes no share
+    int own = 0, units = 0;
 #pragma unroll 1
     for (int s = tid; s < a.c.seqs; s += PREP_THREADS) {
         const int held = lens[s];
@@ -268,57 +295,63 @@ __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_c
         own = min(1 << 20, own + (int)((unsigned)(left + TILE - 1) / TILE));
         units += left > 0;
     }
-    if (own) {
+    own = __reduce_add_sync(FULL, own);
+    units = __reduce_add_sync(FULL, units);
+    if (lane == 0 && own) {
         atomicAdd(&own_tiles, own);
         atomicAdd(&own_units, units);
     }
     __syncthreads();
-    int grid = total ? a.grid : 0;  // CTAs for the shared rows
-    const int own_ctas = a.c.heads * own_units;
-    if (total && own_tiles && total + own_ctas <= a.grid) {
-        grid = total;  // an SM for each
-    } else if (total && own_tiles) {
-        const float x = total * TILE_COST, y = a.c.heads * (own_tiles * OWN_COST) + own_ctas * UNIT_COST;
-        // x / P = t, y / (G - P) = t - MERGE_COST
-        const float b = a.grid * MERGE_COST + x + y, root = __fsqrt_rn(b * b - 4.f * a.grid * MERGE_COST * x);
-        grid = max(1, min(a.grid - 1, (int)(__fdividef(2.f * a.grid * x, b + root) + 0.5f)));
-    }
-    // units with CTAs of their own
-    const int even = grid ? parts_of(total, grid) : 0;
+    if (!FEW || warp == 0) {
+        const int grid = ctas_for_shared(a.grid, total, (float)own_tiles * a.c.heads, own_units * a.c.heads);
+        // units with CTAs of their own
+        const int even = grid ? parts_of(total, grid) : 0;
+        int ctas[OWN_EXTRA + 1] = {};
 #pragma unroll 1
-    for (int i = i0; i < i1 && even; ++i) {
-        const int n = min(grid + 1, a.c.heads * group[i].blocks);
-#pragma unroll 1
+        for (int i = i0; i < i1 && even; ++i) {
+            const int n = min(grid + 1, a.c.heads * group[i].blocks);
+#pragma unroll
+            for (int x = 0; x <= OWN_EXTRA; ++x)
+                ctas[x] = min(grid + 1, ctas[x] + n * min(grid + 1, parts_of(tiles_of(group[i]), even + x)));
+        }
+#pragma unroll
         for (int x = 0; x <= OWN_EXTRA; ++x) {
-            const int more = n * min(grid + 1, parts_of(tiles_of(group[i]), even + x));
-            if (more) atomicAdd(&ctas_with[x], min(more, grid + 1));
+            ctas[x] = __reduce_add_sync(FULL, ctas[x]);
+            if (!FEW && lane == 0) atomicAdd(&ctas_with[x], ctas[x]);
+        }
+        if (!FEW) __syncthreads();
+        int part = 0;  // tiles of a part, 0: the even deal
+#pragma unroll
+        for (int x = OWN_EXTRA; x >= 0; --x)
+            if (even && (FEW ? ctas[x] : ctas_with[x]) <= grid) part = even + x;
+        int mine = 0;
+#pragma unroll 1
+        for (int i = i0; i < i1 && part; ++i) {
+            group[i].parts = parts_of(tiles_of(group[i]), part);
+            mine += a.c.heads * group[i].blocks * group[i].parts;
+        }
+        const int2 cta = before(false, mine);
+        sum = cta.x;
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            group[i].cta = sum;
+            sum += a.c.heads * group[i].blocks * group[i].parts;
+            if (FEW) a.group[i] = group[i];
+        }
+        if (tid == 0) {
+            const int used = part ? cta.y : min(grid, total);
+            of_deal[0] = part;
+            of_deal[1] = used;
+            of_deal[2] = total;
+            a.tile_base[a.groups] = total;
+            *a.own_ctas = max(1, a.grid - grid);
+            *a.deal = make_int2(part ? used : 0, max(1, used));
         }
     }
     __syncthreads();
-    int part = 0;  // tiles of a part, 0: the even deal
-    for (int x = OWN_EXTRA; x >= 0; --x)
-        if (even && ctas_with[x] <= grid) part = even + x;
-    int mine = 0;
-#pragma unroll 1
-    for (int i = i0; i < i1 && part; ++i) {
-        const int parts = parts_of(tiles_of(group[i]), part);
-        group[i].parts = parts;
-        mine += a.c.heads * group[i].blocks * parts;
-    }
-    const int2 cta = scan<false>(mine, warp_val);
-    sum = cta.x;
-#pragma unroll 1
-    for (int i = i0; i < i1; ++i) {
-        group[i].cta = sum;
-        sum += a.c.heads * group[i].blocks * group[i].parts;
-        if (FEW) {
-            a.group[i] = group[i];
-            a.tile_base[i] = base[i];
-        }
-    }
-    __syncthreads();
-    const int used = part ? cta.y : min(grid, total);
-    const Deal deal(total, max(1, used), 1);
+    const bool part = of_deal[0];
+    const int used = of_deal[1];
+    const Deal deal(of_deal[2], max(1, used), 1);
 #pragma unroll 1
     for (int c = tid; c < a.grid; c += PREP_THREADS) {
         Share v{};
@@ -336,21 +369,20 @@ __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_c
             }
             const Group gr = group[lo];
             if (part) {
-                const int unit = (int)quotient(c - gr.cta, gr.parts), p = c - gr.cta - unit * gr.parts, nt = tiles_of(gr);
+                const int nt = tiles_of(gr), unit = (int)((unsigned)(c - gr.cta) / (unsigned)gr.parts);
+                const int p = c - gr.cta - unit * gr.parts;
                 // the first nt % parts of the equal parts have a tile more
-                const int each = (int)quotient(nt, gr.parts), more = nt - each * gr.parts;
-                v.t = base[lo] + unit * nt + p * each + min(p, more);
+                const int each = (int)((unsigned)nt / (unsigned)gr.parts), more = nt - each * gr.parts;
+                const int h = (int)((unsigned)unit / (unsigned)gr.blocks), k0 = p * each + min(p, more);
+                v.t = base[lo] + unit * nt + k0;
                 v.t_end = v.t + each + (p < more);
+                v.run = Run{gr.first, gr.members, gr.rows, h, unit - h * gr.blocks, k0, v.t_end - v.t};
+            } else {
+                v.run = run_in(gr, base[lo], v.t, v.t_end);
             }
             v.group = lo;
-            v.run = run_in(gr, base[lo], v.t, v.t_end);
         }
         a.share[c] = v;
-    }
-    if (tid == 0) {
-        a.tile_base[a.groups] = total;
-        *a.own_ctas = max(1, a.grid - grid);
-        *a.deal = make_int2(part ? used : 0, max(1, used));
     }
 }
 
