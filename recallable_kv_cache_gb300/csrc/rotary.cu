@@ -4,12 +4,12 @@
 //
 //   y = x w / sqrt(mean x^2 + eps),  (y_a, y_b) := A (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
 //
-// Every row is read and written once, so long inputs are bound by HBM.  What a
-// row costs besides is kept small: sixteen lanes have a row, eight channels a
-// lane (16 bytes of bf16), the sum of squares and the other half of a pair come
-// by shuffles, and the angles of a token are worked out once for all its heads:
-// the block leaves cos and sin in shared memory, and a lane keeps those of its
-// channels in registers while it goes through rows of one token.
+// Every row is read and written once, so long inputs are bound by HBM and a
+// step's few rows by latency.  Sixteen lanes have a row, eight channels a lane in
+// two pieces of four that hold both channels of its four pairs, whichever way
+// they are paired: nothing is exchanged but the sum of squares.  A lane works out
+// the angles of its pairs once for all rows of a token that its group has, with
+// the first rows under way meanwhile; no block waits for another thread.
 //
 // The angle of pair i at position p is p turns_i / 2^64 of a turn: the product of
 // two integers, whose wrap at 2^64 is the angle's own, so that the angle is as
@@ -20,6 +20,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "mma_sync.cuh"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -61,46 +62,62 @@ __device__ __forceinline__ float2 unit_circle(unsigned long long phase) {
     return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
-template <typename T>
-struct Raw;  // eight channels as they are in memory
-template <>
-struct Raw<__nv_bfloat16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void store(unsigned char* p) const { *reinterpret_cast<uint4*>(p) = v; }
+// a lane's eight channels as they are in memory; TOGETHER: its two pieces follow one another
+template <typename T, bool TOGETHER>
+struct Raw;
+template <bool TOGETHER>
+struct Raw<__nv_bfloat16, TOGETHER> {
+    uint2 v[2];
+    __device__ __forceinline__ void load(const unsigned char* p, int a, int b) {
+        if (TOGETHER) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p + a);
+            v[0] = make_uint2(x.x, x.y);
+            v[1] = make_uint2(x.z, x.w);
+        } else {
+            v[0] = *reinterpret_cast<const uint2*>(p + a);
+            v[1] = *reinterpret_cast<const uint2*>(p + b);
+        }
+    }
+    __device__ __forceinline__ void store(unsigned char* p, int a, int b) const {
+        if (TOGETHER) {
+            *reinterpret_cast<uint4*>(p + a) = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+        } else {
+            *reinterpret_cast<uint2*>(p + a) = v[0];
+            *reinterpret_cast<uint2*>(p + b) = v[1];
+        }
+    }
     __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 2; ++i) {
+            x[4 * i] = __uint_as_float(v[i].x << 16);
+            x[4 * i + 1] = __uint_as_float(v[i].x & 0xffff0000u);
+            x[4 * i + 2] = __uint_as_float(v[i].y << 16);
+            x[4 * i + 3] = __uint_as_float(v[i].y & 0xffff0000u);
         }
     }
     __device__ __forceinline__ void put(const float (&x)[8]) {
-        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 2; ++i) v[i] = make_uint2(mmas::pack2(x[4 * i], x[4 * i + 1]), mmas::pack2(x[4 * i + 2], x[4 * i + 3]));
     }
 };
-template <>
-struct Raw<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const unsigned char* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
+template <bool TOGETHER>
+struct Raw<float, TOGETHER> {
+    float4 v[2];
+    __device__ __forceinline__ void load(const unsigned char* p, int a, int b) {
+        v[0] = *reinterpret_cast<const float4*>(p + a);
+        v[1] = *reinterpret_cast<const float4*>(p + b);
     }
-    __device__ __forceinline__ void store(unsigned char* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
+    __device__ __forceinline__ void store(unsigned char* p, int a, int b) const {
+        *reinterpret_cast<float4*>(p + a) = v[0];
+        *reinterpret_cast<float4*>(p + b) = v[1];
     }
     __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
     }
     __device__ __forceinline__ void put(const float (&x)[8]) {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     }
 };
 
@@ -108,133 +125,115 @@ struct Raw<float> {
 // its token: queries, then keys, then values (PAGED).
 template <typename T, bool PAGED, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rotary_kernel(const __grid_constant__ RotArgs a) {
-    constexpr int CS = INTERLEAVED ? 4 : 8;  // pairs that a lane has channels of
-    constexpr int ROW = 8 * sizeof(T);       // bytes of a lane's channels
-    extern __shared__ float2 turned[];       // [tokens of the block][rot / 2]
-    __shared__ __align__(16) float weight[2][D];
     const int tid = threadIdx.x, lane = tid & (LANES - 1), group = tid / LANES;
-    const int half = a.rot / 2;
-    const int mine = GROUPS / a.per_token;  // tokens of a block
-    const long long t0 = (long long)blockIdx.x * mine;
-    const int local = group / a.per_token, sub = group % a.per_token;
-    const long long t = t0 + local;
-    const int all = a.rows[0] + a.rows[1] + a.rows[2];
+    const int sub = group & (a.per_token - 1);
+    const long long t = (long long)blockIdx.x * (GROUPS / a.per_token) + group / a.per_token;
+    // the lane's channels: pairs 4 lane .. 4 lane + 3, or eight behind the rotated ones
+    const int reach = a.rot / 8;  // lanes that have pairs
+    const bool turns = lane < reach;
+    const int at0 = (INTERLEAVED || !turns ? 8 : 4) * lane * (int)sizeof(T);
+    const int at1 = at0 + (INTERLEAVED || !turns ? 4 : a.rot / 2) * (int)sizeof(T);
     ptx::grid_dependency_wait();
     ptx::allow_dependent_launch();
+    if (t >= a.tokens) return;
     int4 place = make_int4(0, 0, 0, 0);
-    bool live = t < a.tokens;
-    if (PAGED && live) {
+    if (PAGED) {
         place = a.slots[t];
-        live = place.x != -1;
-        const bool bad = place.x < -1 || place.x >= a.slots_held ||
-                         ((a.c.pos || a.c.mass) && (place.y < 0 || place.y >= a.c.seqs || place.z < 0 || place.z >= a.c.rows));
-        if (live && bad) {
+        if (place.x == -1) return;
+        if (place.x < 0 || place.x >= a.slots_held ||
+            ((a.c.pos || a.c.mass) && (place.y < 0 || place.y >= a.c.seqs || place.z < 0 || place.z >= a.c.rows))) {
             if (lane == 0 && sub == 0) report(a.c.dev_err, CKV_DEV_BAD_INDEX);
-            live = false;
+            return;
         }
+    } else {
+        place.w = a.positions[t];
     }
-    // row r of the token: which of q, k, v, and its head
+    const unsigned half_warp = 0xffffu << (tid & LANES);
+    // row r of the token: whether it is of q, k or v, and its head
+    const int all = a.rows[0] + a.rows[1] + (PAGED ? a.rows[2] : 0), first_v = a.rows[0] + a.rows[1];
     auto kind_of = [&](int r, int* h) {
-        const int kind = (r >= a.rows[0]) + (r >= a.rows[0] + a.rows[1]);
-        *h = r - (kind > 0 ? a.rows[0] : 0) - (kind > 1 ? a.rows[1] : 0);
+        const int kind = (r >= a.rows[0]) + (PAGED && r >= first_v);
+        *h = r - (kind == 0 ? 0 : kind == 1 ? a.rows[0] : first_v);
         return kind;
     };
-    Raw<T> raw[FLIGHT];
-    auto ask = [&](int r0) {
-#pragma unroll
-        for (int i = 0; i < FLIGHT; ++i) {
-            const int r = r0 + i * a.per_token;
-            if (live && r < all) {
-                int h;
-                const int kind = kind_of(r, &h);
-                raw[i].load(a.src[kind] + t * a.sst[kind][0] + h * a.sst[kind][1] + lane * ROW);
-            }
-        }
+    Raw<T, INTERLEAVED> raw[FLIGHT];
+    auto ask = [&](Raw<T, INTERLEAVED>& to, int r) {
+        int h;
+        const int kind = kind_of(r, &h);
+        to.load(a.src[kind] + t * a.sst[kind][0] + h * a.sst[kind][1], at0, at1);
     };
-    ask(sub);
-    // the angles, and the weights
-    for (int i = tid; i < 2 * D; i += THREADS) {
-        const float* w = a.weight[i / D];
-        weight[i / D][i % D] = w ? w[i % D] : 1.f;
-    }
-    for (int i = tid; i < mine * half; i += THREADS) {
-        const int token = i / half, pair = i - token * half;
-        float2 cs = make_float2(0.f, 0.f);
-        if (t0 + token < a.tokens) {
-            const int p = PAGED ? a.slots[t0 + token].w : a.positions[t0 + token];
-            cs = unit_circle((unsigned long long)(long long)p * a.turns[pair]);
-        }
-        turned[i] = make_float2(cs.x * a.amplitude, cs.y * a.amplitude);
-    }
-    __syncthreads();
-    // this lane's pairs; channels from rot on keep their value
-    float c[CS], s[CS];
-    const int reach = a.rot / 8;  // lanes that have rotated channels
-    const bool turns = lane < reach;
-    // the other channel of a pair is `reach / 2` lanes on or back
-    const bool low = lane < reach / 2;
-    const int other = INTERLEAVED || !turns ? lane : (low ? lane + reach / 2 : lane - reach / 2);
 #pragma unroll
-    for (int i = 0; i < CS; ++i) {
-        const int pair = INTERLEAVED ? lane * 4 + i : (low ? lane : lane - reach / 2) * 8 + i;
-        const float2 cs = turns ? turned[local * half + pair] : make_float2(1.f, 0.f);
-        c[i] = cs.x;
-        s[i] = INTERLEAVED || !low ? cs.y : -cs.y;
+    for (int i = 0; i < FLIGHT; ++i)
+        if (sub + i * a.per_token < all) ask(raw[i], sub + i * a.per_token);
+    float c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
+    if (turns) {
+        const ulonglong2* w = reinterpret_cast<const ulonglong2*>(a.turns + 4 * lane);
+        const ulonglong2 w0 = w[0], w1 = w[1];
+        const unsigned long long f[4] = {w0.x, w0.y, w1.x, w1.y}, p = (unsigned long long)(long long)place.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 cs = unit_circle(p * f[i]);
+            c[i] = cs.x * a.amplitude;
+            s[i] = cs.y * a.amplitude;
+        }
     }
-    const int page = PAGED && live ? a.c.by_page.quot(place.x, &place.x) : 0;
-    // the two groups of a warp may be at rows of different kinds
-    const unsigned half_warp = 0xffffu << (tid & LANES);
+    int slot = 0;
+    const long long page = PAGED ? a.c.by_page.quot(place.x, &slot) : 0;
+    // each row's registers take the row FLIGHT further on as soon as it is done
+#pragma unroll 1
     for (int r0 = sub; r0 < all; r0 += FLIGHT * a.per_token) {
-        if (r0 != sub) ask(r0);
 #pragma unroll
         for (int i = 0; i < FLIGHT; ++i) {
             const int r = r0 + i * a.per_token;
+            if (r >= all) break;  // the same for the group's lanes
             int h;
             const int kind = kind_of(r, &h);
-            const bool there = live && r < all;
             if (!PAGED || kind < 2) {
                 float x[8];
                 raw[i].get(x);
-                if (a.weight[kind & 1]) {
+                const float* weight = a.weight[kind];
+                if (weight) {
                     float sq = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
 #pragma unroll
                     for (int o = LANES / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(half_warp, sq, o, LANES);
                     const float scale = rsqrtf(sq * (1.f / D) + a.eps);
+                    const float4 u = *reinterpret_cast<const float4*>(weight + at0 / (int)sizeof(T));
+                    const float4 v = *reinterpret_cast<const float4*>(weight + at1 / (int)sizeof(T));
+                    const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= scale * weight[kind & 1][8 * lane + e];
+                    for (int e = 0; e < 8; ++e) x[e] *= scale * w[e];
                 }
-                if (INTERLEAVED) {
+                if (turns) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float u = x[2 * e], v = x[2 * e + 1];
-                        x[2 * e] = turns ? u * c[e] - v * s[e] : u;
-                        x[2 * e + 1] = turns ? v * c[e] + u * s[e] : v;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float y = __shfl_sync(half_warp, x[e], other, LANES);
-                        x[e] = turns ? x[e] * c[e] + y * s[e] : x[e];
+                        // pair e: neighbours, or the two pieces' e-th channels
+                        float& u = x[INTERLEAVED ? 2 * e : e];
+                        float& v = x[INTERLEAVED ? 2 * e + 1 : e + 4];
+                        const float y = u * c[e] - v * s[e];
+                        v = v * c[e] + u * s[e];
+                        u = y;
                     }
                 }
                 raw[i].put(x);
             }
-            if (!there) continue;
             unsigned char* to;
             if (PAGED && kind > 0) {
                 const long long* st = kind == 1 ? a.c.ks : a.c.vs;
-                to = (kind == 1 ? a.c.K : a.c.V) + page * st[0] + h * st[1] + place.x * st[2];
-                if (kind == 1 && lane == 0) {
-                    const size_t o = ((size_t)place.y * a.c.heads + h) * a.c.rows + place.z;
-                    if (a.c.pos) a.c.pos[o] = place.w;
-                    if (a.c.mass) a.c.mass[o] = 0.f;
-                }
+                to = (kind == 1 ? a.c.K : a.c.V) + page * st[0] + slot * st[2] + h * st[1];
             } else {
                 to = a.dst[kind & 1] + t * a.dst_st[kind & 1][0] + h * a.dst_st[kind & 1][1];
             }
-            raw[i].store(to + lane * ROW);
+            raw[i].store(to, at0, at1);
+            if (PAGED && kind == 1 && lane == 0) {
+                const size_t o = ((size_t)place.y * a.c.heads + h) * a.c.rows + place.z;
+                if (a.c.pos) a.c.pos[o] = place.w;
+                if (a.c.mass) a.c.mass[o] = 0.f;
+            }
+            if (r + FLIGHT * a.per_token < all) ask(raw[i], r + FLIGHT * a.per_token);
         }
     }
 }
@@ -243,6 +242,9 @@ bool rotary_ok(const ckv_rotary* r) {
     return r && r->rot >= 0 && r->rot <= D && r->rot % 16 == 0 && (r->rot == 0 || r->turns) && r->eps >= 0.f &&
            isfinite(r->eps) && isfinite(r->amplitude) && (r->interleaved == 0 || r->interleaved == 1);
 }
+
+// its arrays are read 16 bytes at a time
+bool rotary_aligned(const ckv_rotary* r) { return aligned16(r->turns) && aligned16(r->q_weight) && aligned16(r->k_weight); }
 
 // byte strides (token, head) of an operand; sources may stand still
 ckv_status operand(const int64_t* st, int tokens, int heads, int elem, bool output, long long* out) {
@@ -265,19 +267,18 @@ cudaError_t launch(RotArgs& a, cudaStream_t s) {
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     const int all = a.rows[0] + a.rows[1] + a.rows[2];
-    // Lane groups to a token: enough that one has FLIGHT rows at a time and no
-    // more than a few turns of them, as the angles cost as much as some ten rows;
-    // more while there are fewer blocks than SMs, where latency counts.
+    // Lane groups to a token: few, so that one goes through 12 to 24 rows with the
+    // angles of one token (32k tokens of 40 rows: 101 us with 20 rows to a group,
+    // 107 with 10); more while there are fewer blocks than SMs, where latency counts.
     int per = 1;
-    while (per < GROUPS && per * FLIGHT * 3 < all) per *= 2;
+    while (per < GROUPS && per * FLIGHT * 6 < all) per *= 2;
     while (per < GROUPS && per < all && (long long)a.tokens * per / GROUPS < sms) per *= 2;
     a.per_token = per;
     const int mine = GROUPS / per;
     const long long blocks = ((long long)a.tokens + mine - 1) / mine;
-    const size_t smem = (size_t)mine * (a.rot / 2) * sizeof(float2);
     return a.interleaved
-               ? launch_dependent(rotary_kernel<T, PAGED, true>, dim3((unsigned)blocks), dim3(THREADS), smem, s, a)
-               : launch_dependent(rotary_kernel<T, PAGED, false>, dim3((unsigned)blocks), dim3(THREADS), smem, s, a);
+               ? launch_dependent(rotary_kernel<T, PAGED, true>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a)
+               : launch_dependent(rotary_kernel<T, PAGED, false>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
 }
 
 void take_rotary(const ckv_rotary* r, RotArgs* a) {
@@ -307,6 +308,7 @@ extern "C" ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const 
         !positions)
         return CKV_ERR_ARG;
     if (dtype != CKV_F32 && dtype != CKV_BF16) return CKV_ERR_DTYPE;
+    if (!rotary_aligned(rotary)) return CKV_ERR_ALIGN;
     if (((long long)heads_q + heads_k) * tokens > MAX_ROWS) return CKV_ERR_ARG;
     const int elem = dtype == CKV_BF16 ? 2 : 4;
     RotArgs a = {};
@@ -347,6 +349,7 @@ extern "C" ckv_status ckv_paged_append_rotated(const ckv_paged_cache* cache, con
     if (!rotary_ok(rotary) || g < 0 || tokens < 1 || !k || !v || !slots || a.slots_held > 0x7fffffffLL ||
         (long long)a.c.heads * g > MAX_ROWS || ((long long)a.c.heads * g + 2LL * a.c.heads) * tokens > MAX_ROWS)
         return CKV_ERR_ARG;
+    if (!rotary_aligned(rotary)) return CKV_ERR_ALIGN;
     const int elem = cache->kv_dtype == CKV_BF16 ? 2 : 4;
     take_rotary(rotary, &a);
     a.tokens = tokens;
