@@ -29,7 +29,7 @@ def plan(table, counts, start, first, shared, held, ring, span, page, n_slots, n
     for s in range(S):
         n, c, f, h, sh = int(start[s]), int(counts[s]), int(first[s]), int(held[s]), int(shared[s])
         fine = (n >= 0 and c >= 0 and f >= 0 and 0 <= sh <= h <= len(table[s]) and n + c <= rows
-                and f + c <= 2 ** 31 - 1 and starts[s + 1] <= n_slots)
+                and f + c <= 2 ** 31 - 1 and (c == 0 or starts[s + 1] <= n_slots))
         if not fine:
             errors.add("count")
             for key, value in (("held", h), ("granted", 0), ("lens", None), ("seen", None)):

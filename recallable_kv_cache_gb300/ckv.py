@@ -438,41 +438,53 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
     return w, amplitude
 
 
+_ROTARIES, _STRIDES = {}, {}  # ckv_rotary structs and stride arrays, made once for equal values
+
+
 def _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device):
-    """The ckv_rotary of a call, after the checks."""
+    """Address of the ckv_rotary of a call, after the checks."""
     import torch
+    rot = at = 0
     if turns is not None:
-        if turns.dtype != torch.int64:
+        if turns.dtype is not torch.int64:
             raise TypeError(f"turns must be int64 (see rotary_turns), got {turns.dtype}")
         if turns.dim() != 1 or not turns.is_contiguous() or turns.device != device:
             raise ValueError(f"turns must be contiguous [rot / 2] on {device}, got {list(turns.shape)} on {turns.device}")
+        rot, at = 2 * turns.shape[0], turns.data_ptr()
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            if w.dtype != torch.float32:
+            if w.dtype is not torch.float32:
                 raise TypeError(f"{name} must be float32, got {w.dtype}")
             if w.shape != (128,) or not w.is_contiguous() or w.device != device:
                 raise ValueError(f"{name} must be contiguous [128] on {device}, got {list(w.shape)} on {w.device}")
-    return Rotary(None if turns is None else turns.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
-                  None if k_weight is None else k_weight.data_ptr(), eps, amplitude,
-                  0 if turns is None else 2 * turns.shape[0], 1 if interleaved else 0)
+    key = (at, 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), eps,
+           amplitude, rot, interleaved)
+    got = _ROTARIES.get(key)
+    if got is None:
+        if len(_ROTARIES) > 256:
+            _ROTARIES.clear()
+        struct = Rotary(at or None, key[1] or None, key[2] or None, eps, amplitude, rot, 1 if interleaved else 0)
+        got = _ROTARIES[key] = (ctypes.addressof(struct), struct)
+    return got
 
 
 def _heads(name, t, tokens, heads, dtype, device):
     """(address, strides as a C array) of t [tokens, heads, 128] after the checks."""
-    if t.dtype != dtype:
+    shape, st = t.shape, t.stride()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != 128:
+    if shape != (tokens, heads, 128):
         raise ValueError(f"{name} must be [{tokens}, {heads}, 128], got {list(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    st = t.stride()
     if st[2] != 1:
         raise ValueError(f"the channels of {name} must be contiguous, got strides {list(st)}")
-    return t.data_ptr(), _Strides(st[0], st[1])
-
-
-_Strides = ctypes.c_int64 * 2
+    got = _STRIDES.get(st)
+    if got is None:
+        if len(_STRIDES) > 256:
+            _STRIDES.clear()
+        got = _STRIDES[st] = (ctypes.c_int64 * 2)(st[0], st[1])
+    return t.data_ptr(), got
 
 
 def rotate(q, k, positions, turns, q_out, k_out, interleaved: bool = False, q_weight=None, k_weight=None,
@@ -489,7 +501,7 @@ def rotate(q, k, positions, turns, q_out, k_out, interleaved: bool = False, q_we
     tokens, device, code = x.shape[0], x.device, _dtype_code(x)
     if device.type != "cuda":
         raise ValueError(f"the rows must be on a CUDA device, got {device}")
-    if positions.dtype != torch.int32:
+    if positions.dtype is not torch.int32:
         raise TypeError(f"positions must be int32, got {positions.dtype}")
     if positions.shape != (tokens,) or not positions.is_contiguous() or positions.device != device:
         raise ValueError(f"positions must be contiguous [{tokens}] on {device}, got {list(positions.shape)} on "
@@ -499,21 +511,23 @@ def rotate(q, k, positions, turns, q_out, k_out, interleaved: bool = False, q_we
         if (t is None) != (o is None):
             raise ValueError(f"{name} and {name}_out go together")
         if t is None:
-            args += [None, None, None, None, 0]
+            args += (None, None, None, None, 0)
         else:
             heads = t.shape[1] if t.dim() == 3 else 0
-            args += [*_heads(name, t, tokens, heads, x.dtype, device),
-                     *_heads(name + "_out", o, tokens, heads, x.dtype, device), heads]
+            args += _heads(name, t, tokens, heads, x.dtype, device)
+            args += _heads(name + "_out", o, tokens, heads, x.dtype, device)
+            args.append(heads)
     rotary = _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device)
     raw_stream, current = _raw_calls(torch)
-    stream = raw_stream(device.index) if stream is None else getattr(stream, "cuda_stream", stream)
-    call = (ctypes.addressof(rotary), *args, positions.data_ptr(), tokens, 128, code, stream)
-    if device.index == current():
-        status = lib().ckv_rotate(*call)
+    index = device.index
+    stream = raw_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
+    if index == current():
+        status = lib().ckv_rotate(rotary[0], *args, positions.data_ptr(), tokens, 128, code, stream)
     else:
-        with torch.cuda.device(device.index):
-            status = lib().ckv_rotate(*call)
-    _check(status, "ckv_rotate")
+        with torch.cuda.device(index):
+            status = lib().ckv_rotate(rotary[0], *args, positions.data_ptr(), tokens, 128, code, stream)
+    if status:
+        raise CKVError(status, "ckv_rotate")
 
 
 def paged_set_wait_limit(cycles: int = 2_000_000_000, stall: bool = False):
@@ -616,6 +630,13 @@ class PagedCache:
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         return t.data_ptr()
+
+    def _ints(self, name, t, shape):
+        """_tensor of contiguous int32, in one look where all is well: the calls
+        of a step have a dozen of them."""
+        if t.dtype is self._i32 and t.shape == shape and t.is_contiguous() and t.get_device() == self._index:
+            return t.data_ptr()
+        return self._tensor(name, t, shape, self._i32)
 
     def _strides(self, t, n):
         """The first n strides of t as a C array (made once for equal strides)."""
@@ -723,18 +744,18 @@ class PagedCache:
         held_out [seqs], span, span_out [2], starts [seqs + 1], slots [tokens, 4]
         and the ring of free pages ``free``, all int32.  held_out and span_out are
         held and span themselves if None; table, lens and seen change."""
-        i32, tensor, per_seq = self._i32, self._tensor, self._per_seq
+        ints, per_seq = self._ints, self._per_seq
         if free.dim() != 1 or slots.dim() != 2:
             raise ValueError(f"free must be [pages] and slots [tokens, 4], got {list(free.shape)}, {list(slots.shape)}")
         n_slots, cap = slots.shape[0], free.shape[0]
-        h, sp = tensor("held", held, per_seq, i32), tensor("span", span, (2,), i32)
-        self._call(self._plan, stream, tensor("counts", counts, per_seq, i32), tensor("start", start, per_seq, i32),
-                   tensor("first", first, per_seq, i32), tensor("shared", shared, per_seq, i32), h,
-                   h if held_out is None else tensor("held_out", held_out, per_seq, i32),
-                   tensor("free", free, (cap,), i32), cap, sp,
-                   sp if span_out is None else tensor("span_out", span_out, (2,), i32),
-                   tensor("granted", granted, per_seq, i32), tensor("starts", starts, (self.seqs + 1,), i32),
-                   tensor("slots", slots, (n_slots, 4), i32), n_slots)
+        h, sp = ints("held", held, per_seq), ints("span", span, (2,))
+        self._call(self._plan, stream, ints("counts", counts, per_seq),
+                   None if start is None else ints("start", start, per_seq),
+                   None if first is None else ints("first", first, per_seq),
+                   None if shared is None else ints("shared", shared, per_seq), h,
+                   h if held_out is None else ints("held_out", held_out, per_seq), ints("free", free, (cap,)), cap, sp,
+                   sp if span_out is None else ints("span_out", span_out, (2,)), ints("granted", granted, per_seq),
+                   ints("starts", starts, (self.seqs + 1,)), ints("slots", slots, (n_slots, 4)), n_slots)
 
     def append_rotated(self, q, k, v, slots, turns, q_out, interleaved: bool = False, q_weight=None, k_weight=None,
                        eps: float = 1e-6, amplitude: float = 1.0, stream=None):
@@ -742,20 +763,22 @@ class PagedCache:
         that slots [tokens, 4] of a plan gives them (see ckv_paged_append_rotated):
         q, q_out [tokens, heads * g, 128] (both None: no queries), k, v [tokens,
         heads, 128], any strides with contiguous channels."""
-        device = self.device
+        device, heads, dtype = self.device, self.heads, self.dtype
         if k.dim() != 3:
-            raise ValueError(f"k must be [tokens, {self.heads}, 128], got {list(k.shape)}")
-        tokens = k.shape[0]
-        if (q is None) != (q_out is None):
-            raise ValueError("q and q_out go together")
-        heads_q, dtype = self.heads * self.g, self.dtype
+            raise ValueError(f"k must be [tokens, {heads}, 128], got {list(k.shape)}")
+        tokens, g = k.shape[0], self.g
         rotary = _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device)
-        queries = (None, None) if q is None else _heads("q", q, tokens, heads_q, dtype, device)
-        rotated = (None, None) if q is None else _heads("q_out", q_out, tokens, heads_q, dtype, device)
-        self._call(self._append_rotated, stream, ctypes.addressof(rotary), *queries, 0 if q is None else self.g,
-                   *rotated, *_heads("k", k, tokens, self.heads, dtype, device),
-                   *_heads("v", v, tokens, self.heads, dtype, device),
-                   self._tensor("slots", slots, (tokens, 4), self._i32), tokens)
+        if q is None and q_out is None:
+            g = 0
+            queries = rotated = (None, None)
+        elif q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        else:
+            queries = _heads("q", q, tokens, heads * g, dtype, device)
+            rotated = _heads("q_out", q_out, tokens, heads * g, dtype, device)
+        self._call(self._append_rotated, stream, rotary[0], *queries, g, *rotated,
+                   *_heads("k", k, tokens, heads, dtype, device), *_heads("v", v, tokens, heads, dtype, device),
+                   self._ints("slots", slots, (tokens, 4)), tokens)
 
     def shared_attn(self, q, out, group_starts, prefix, lse=None, scale=None, stream=None):
         """decode_attn (without weights) where sequences group_starts[i] ..
@@ -773,8 +796,8 @@ class PagedCache:
             raise ValueError(f"q is on {q.device}, the cache on {self.device}")
         if prefix.dim() != 1:
             raise ValueError(f"prefix must be [groups], got {list(prefix.shape)}")
-        groups, i32, f32, tensor = prefix.shape[0], self._i32, self._f32, self._tensor
+        groups, ints, f32, tensor = prefix.shape[0], self._ints, self._f32, self._tensor
         self._call(self._shared_attn, stream, q.data_ptr(), self._code, self._strides(q, 2), self.g,
-                   128 ** -0.5 if scale is None else scale, tensor("group_starts", group_starts, (groups + 1,), i32),
-                   tensor("prefix", prefix, (groups,), i32), groups, tensor("out", out, self._q_shape, f32),
+                   128 ** -0.5 if scale is None else scale, ints("group_starts", group_starts, (groups + 1,)),
+                   ints("prefix", prefix, (groups,)), groups, tensor("out", out, self._q_shape, f32),
                    None if lse is None else tensor("lse", lse, self._lse_shape, f32), *self._workspace)

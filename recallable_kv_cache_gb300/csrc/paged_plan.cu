@@ -114,10 +114,133 @@ __device__ __forceinline__ int4 slot_entry(const PlanArgs& a, int s, int row, in
     return make_int4(page * a.c.page + slot, s, row, position);
 }
 
-// One CTA.  A thread has a chunk of neighbouring sequences (one, up to NT of
-// them), looks at them three times, the later times in the first-level cache.
+// Sums that stop at `most` (so that 32 bits do for whatever the inputs are):
+// inclusive, of two values at a time.  `warp_sum` is not used again by a call
+// that no barrier parts from this one.
+template <int NT>
+__device__ __forceinline__ uint2 sums_to(uint2 v, uint2 most, uint2* warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto add = [&](uint2& x, int o, bool in) {
+        const unsigned y = __shfl_up_sync(FULL, x.x, o), z = __shfl_up_sync(FULL, x.y, o);
+        if (in) x = make_uint2(min(x.x + y, most.x), min(x.y + z, most.y));
+    };
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) add(v, o, lane >= o);
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    uint2 w = lane < NT / 32 ? warp_sum[lane] : make_uint2(0, 0);
+#pragma unroll
+    for (int o = 1; o < NT / 32; o <<= 1) add(w, o, lane >= o);
+    const unsigned x = __shfl_sync(FULL, w.x, max(warp, 1) - 1), y = __shfl_sync(FULL, w.y, max(warp, 1) - 1);
+    return warp ? make_uint2(min(v.x + x, most.x), min(v.y + y, most.y)) : v;
+}
+// the sequence that item i belongs to: the last of which the items begin at i or before
+template <int NT>
+__device__ __forceinline__ int seq_of(const unsigned* begin, unsigned i) {
+    int lo = 0;
+#pragma unroll
+    for (int step = NT / 2; step > 0; step >>= 1)
+        if (begin[lo + step] <= i) lo += step;
+    return lo;
+}
+
+// Up to NT sequences, one CTA, a thread a sequence.
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+    constexpr int AT_A_TIME = 4;  // pages that a thread has under way
+    __shared__ uint2 warp_sum[2][NT / 32];
+    __shared__ unsigned tokens_from[NT + 1], takes_from[NT + 1], gives_from[NT + 1];  // [NT]: in all
+    __shared__ int4 seq[NT];  // start, first, pages in hand, pages to have
+    __shared__ unsigned taken_here;  // pages really taken
+    const int s = threadIdx.x;
+    if (s == 0) taken_here = tokens_from[0] = takes_from[0] = gives_from[0] = 0;
+    ptx::grid_dependency_wait();
+    ptx::allow_dependent_launch();
+    int head = a.span_in[0], avail = a.span_in[1];
+    Seq q{0, 0, 0, 0, 0, true};
+    if (s < a.c.seqs) q = look(a, s);
+    if (head < 0 || head >= a.cap || avail < 0 || avail > a.cap) {
+        if (s == 0) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+        head = avail = 0;
+    }
+    const unsigned n = max(0, q.count), most = (unsigned)a.n_slots + 1;
+    const unsigned tokens_end = sums_to<NT>(make_uint2(min(n, most), 0), make_uint2(most, 0), warp_sum[0]).x;
+    if (tokens_end > (unsigned)a.n_slots && n) q.ok = false;
+    if (!q.ok) {
+        q.need = q.held;
+        report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+    }
+    const unsigned take = max(0, q.need - q.held), give = max(0, q.held - q.need);
+    const uint2 end = sums_to<NT>(make_uint2(min(take, avail + 1u), min(give, a.cap + 1u)),
+                                  make_uint2(avail + 1u, a.cap + 1u), warp_sum[1]);
+    // served in order while the pages last: of the takes, those served are the first
+    const bool served = q.ok && (take == 0 || end.x <= (unsigned)avail);
+    if (served && take) atomicMax(&taken_here, end.x);
+    // (a sum that has stopped is of items that are not served, or have no place)
+    tokens_from[s + 1] = tokens_end;
+    takes_from[s + 1] = end.x;
+    gives_from[s + 1] = end.y;
+    seq[s] = make_int4(served ? q.start : -1, q.first, q.held, q.need);
+    __syncthreads();
+    const unsigned taken = taken_here, given = min(gives_from[NT], (unsigned)(a.cap - avail));
+    if (s == 0 && given < gives_from[NT]) report(a.c.dev_err, CKV_DEV_BAD_COUNT);
+    // the pages: the first `taken` from the ring's head, then those handed back
+    for (unsigned i0 = s; i0 < taken + given; i0 += NT * AT_A_TIME) {
+        int32_t* to[AT_A_TIME];
+        int32_t page[AT_A_TIME];
+#pragma unroll
+        for (int k = 0; k < AT_A_TIME; ++k) {
+            const unsigned i = i0 + k * NT;
+            to[k] = nullptr;
+            if (i < taken + given) {
+                const bool takes = i < taken;
+                const unsigned item = takes ? i : i - taken;
+                const unsigned* from = takes ? takes_from : gives_from;
+                const int o = seq_of<NT>(from, item);
+                int32_t* row = a.table + (size_t)o * a.c.max_pages + (takes ? seq[o].z : seq[o].w) + (item - from[o]);
+                int32_t* ring = a.ring + ring_at(head, takes ? item : (long long)avail + item, a.cap);
+                page[k] = takes ? *ring : *row;
+                to[k] = takes ? row : ring;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < AT_A_TIME; ++k)
+            if (to[k]) *to[k] = page[k];
+    }
+    if (a.slots_here) {
+        __syncthreads();  // the table is whole
+        for (int t = s; t < a.n_slots; t += NT) {
+            int4 e = make_int4(-1, -1, -1, -1);
+            if (t < (int)tokens_from[NT]) {
+                const int o = seq_of<NT>(tokens_from, t), j = t - (int)tokens_from[o];
+                const int4 v = seq[o];
+                if (v.x >= 0) e = slot_entry(a, o, v.x + j, v.y + j);
+            }
+            a.slots[t] = e;
+        }
+    }
+    // The outputs: a thread wrote what only it has read, and read it before the barriers.
+    if (s < a.c.seqs) {
+        const int got = served ? q.count : 0;
+        a.starts[s] = (int)min(tokens_from[s], (unsigned)a.n_slots);
+        a.granted[s] = got;
+        a.held_out[s] = served ? q.need : q.held;
+        if (q.ok) {
+            a.c.lens[s] = q.start + got;
+            if (a.c.seen) a.c.seen[s] = q.first + got;
+        }
+    }
+    if (s == 0) {
+        a.starts[a.c.seqs] = (int)min(tokens_from[NT], (unsigned)a.n_slots);
+        a.span_out[0] = ring_at(head, taken, a.cap);
+        a.span_out[1] = avail - (int)taken + (int)given;
+    }
+}
+
+// More sequences.  One CTA; a thread has a chunk of neighbouring sequences and
+// looks at them three times, the later times in the first-level cache.
+template <int NT>
+__global__ void __launch_bounds__(NT) paged_plan_many_kernel(const __grid_constant__ PlanArgs a) {
     __shared__ Sums<NT> sums;
     __shared__ long long warp_sum[NT / 32], taken_sum[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -142,7 +265,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
             Seq q = look(a, s);
             const long long t = at;
             at += max(0, q.count);
-            if (at > a.n_slots) q.ok = false;
+            if (at > a.n_slots && q.count > 0) q.ok = false;
             if (!q.ok) q.need = q.held;
             f(s, q, max(0, q.need - q.held), max(0, q.held - q.need), t);
         }
@@ -191,7 +314,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
             long long at = sums.tokens[c];
             for (;;) {
                 at += max(0, q.count);
-                if (at > a.n_slots) q.need = q.held;
+                if (at > a.n_slots && q.count > 0) q.need = q.held;
                 const int n = max(0, takes_page ? q.need - q.held : q.held - q.need);
                 if (left < n) break;
                 left -= n;
@@ -216,7 +339,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
                 Seq q = look(a, s);
                 for (;;) {
                     at += max(0, q.count);
-                    if (at > a.n_slots) q.ok = false;
+                    if (at > a.n_slots && q.count > 0) q.ok = false;
                     if (q.ok) before += max(0, q.need - q.held);
                     if (left < max(0, q.count)) break;
                     left -= max(0, q.count);
@@ -332,8 +455,12 @@ extern "C" ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t
     a.slots_here = n_slots <= SLOTS_HERE;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (S <= 256 && n_slots <= 512) e = launch_dependent(paged_plan_kernel<256>, dim3(1), dim3(256), 0, s, a);
-    else e = launch_dependent(paged_plan_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
+    if (S <= 256 && (n_slots <= 512 || !a.slots_here))
+        e = launch_dependent(paged_plan_kernel<256>, dim3(1), dim3(256), 0, s, a);
+    else if (S <= 1024)
+        e = launch_dependent(paged_plan_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
+    else
+        e = launch_dependent(paged_plan_many_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
     if (e == cudaSuccess && !a.slots_here) {
         // about one token a thread where the sequences are alike
         const long long share = ((long long)n_slots + S - 1) / S;

@@ -190,14 +190,16 @@ def test_bad_sequences_are_left_alone(bad, S):
     assert int(p.err) == 3
 
 
-def test_slots_that_do_not_fit():
-    for n_slots, S in ((9, 4), (9, 1200), (2100, 3)):
-        p = Plan([0] * S, [1000, 5, 4, 3][:S] + [0] * (S - 4) if n_slots > 9 else [4, 3, 3, 1] + [0] * (S - 4), 16,
-                 n_slots=n_slots)
-        p.run()
-        want = p.check()
-        if n_slots <= 9:
-            assert want["granted"][:4] == [4, 3, 0, 0] and int(p.err) == 3
+@pytest.mark.parametrize("S", [4, 300, 1200])
+@pytest.mark.parametrize("counts,n_slots,granted", [([4, 3, 3, 1], 9, [4, 3, 0, 0]), ([4, 3, 900, 0], 9, [4, 3, 0, 0]),
+                                                    ([1000, 5, 1200, 3], 2100, [1000, 5, 0, 0])])
+def test_slots_that_do_not_fit(S, counts, n_slots, granted):
+    """Tokens past the slot map are refused; sequences without any still hand their pages back."""
+    p = Plan([0] * S, counts + [0] * (S - 4), 16, n_slots=n_slots, held=[0] * (S - 1) + [0 if S == 4 else 2], seed=S)
+    p.run()
+    want = p.check()
+    assert want["granted"][:4] == granted and int(p.err) == 3
+    assert want["starts"][3] == n_slots and want["held"][-1] == 0
 
 
 @pytest.mark.parametrize("span", [[-1, 2], [10 ** 6, 2], [0, -1], [0, 10 ** 6]])
