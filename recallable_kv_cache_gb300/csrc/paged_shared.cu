@@ -121,8 +121,8 @@ struct SharedArgs {
     int2* deal;         // [1] CTAs with a unit's part, 0: the even deal; CTAs that it goes to
     int* own_ctas;      // [1] CTAs for the sequences' own rows
     float* own_lse2;    // [seqs * heads * g] of the sequences' own rows, base 2
-    // Parts: O as [channel / 4][query of the block] of four, and (maximum, sum) of
-    // even and odd tiles.  The CTA in which a unit begins leaves its part behind
+    // Parts: O as [channel / 4][query of the block] of four, and for either half of
+    // the tiles' rows (the maximum that O goes by, the sum).  The CTA in which a unit begins leaves its part behind
     // those of the units before it, the others (each continues one at most) by CTA.
     float4* unit_o;     // [seqs * heads * g][D / 4] in all
     float4* unit_ml;    // [seqs * heads * g]
@@ -180,7 +180,7 @@ __device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigne
 // passes from one unit to the next the products wait for the new queries and the
 // softmax for the products, as long as some two tiles, so the second deal is
 // taken where its largest part is at most OWN_EXTRA tiles above an even share.
-constexpr float TILE_COST = 1.7f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 3.f;  // us
+constexpr float TILE_COST = 1.7f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 6.f;  // us
 constexpr int OWN_EXTRA = 2;
 // The SMs for the shared rows, of `grid`: `total` tiles of these, and of the own
 // rows `own` tiles of 16 of `units` (sequence, KV head) pairs.
@@ -855,28 +855,38 @@ __global__ void __launch_bounds__(THREADS, 1)
 // are under way at a time (one after the other 20 parts took 12 us).
 constexpr int PARTS = 8;
 __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_constant__ SharedArgs a) {
-    ptx::grid_dependency_wait();
-    ptx::allow_dependent_launch();
     const int channel = threadIdx.x / JOIN_ROWS, heads_q = a.c.heads * a.g;  // four channels
     const long long n = (long long)a.c.seqs * heads_q, step = (long long)gridDim.x * JOIN_ROWS;
-    const int total = a.tile_base[a.groups], ctas = a.deal->x;
-    const Deal deal(total, Deal::ctas(total, 1, a.deal->y), 1);
+    bool waited = false;
+    ptx::allow_dependent_launch();
+#pragma unroll 1
     for (long long row = (long long)blockIdx.x * JOIN_ROWS + threadIdx.x % JOIN_ROWS; row < n; row += step) {
+        // What the prep has left is whole: the kernel before this one began
+        // after it.  It is looked up while that one is still at work.
         const int some = (int)(row / heads_q);  // a sequence of the group
-        const int i = a.group_of[some];
+        const int i = a.group_of[some], total = a.tile_base[a.groups];
+        const int2 dealt = *a.deal;
         if (a.skip[some] == 0) continue;
         const Group gr = a.group[i];
         const int nt = (gr.rows + KT - 1) / KT, all = gr.members * a.g;
         const int left = (int)(row - (long long)gr.first * heads_q), h = left / all, x = left - h * all;
         const int block = x / QT, y = x - block * QT, queries = min(QT, all - block * QT), unit = h * gr.blocks + block;
-        const int member = x / a.g;
-        const size_t query = (size_t)(gr.first + member) * heads_q + h * a.g + (x - member * a.g);
-        const int t0 = a.tile_base[i] + unit * nt;
-        const int c0 = ctas ? gr.cta + unit * gr.parts : deal.cta_of(t0);
-        const int parts = ctas ? gr.parts : deal.cta_of(t0 + nt - 1) - c0 + 1;
+        int head;
+        const int member = a.by_g.quot(x, &head);
+        const size_t query = (size_t)(gr.first + member) * heads_q + h * a.g + head;
+        int c0 = gr.cta + unit * gr.parts, parts = gr.parts;
+        if (dealt.x == 0) {
+            const Deal deal(total, Deal::ctas(total, 1, dealt.y), 1);
+            const int t0 = a.tile_base[i] + unit * nt;
+            c0 = deal.cta_of(t0);
+            parts = deal.cta_of(t0 + nt - 1) - c0 + 1;
+        }
+        if (!waited) ptx::grid_dependency_wait();
+        waited = true;
         float4* out = reinterpret_cast<float4*>(a.out + query * D) + channel;
         float4 acc = *out;
         float m = a.own_lse2[query], l = m == -INFINITY ? 0.f : 1.f;
+#pragma unroll 1
         for (int p0 = 0; p0 < parts; p0 += PARTS) {
             float4 o[PARTS], ml[PARTS];
 #pragma unroll
@@ -891,11 +901,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
             }
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                const float mp = fmaxf(ml[k].x, ml[k].z);  // the maximum that O goes by
+                const float mp = ml[k].x;  // of either half of the rows
                 if (mp == -INFINITY) continue;
-                const float lp = ml[k].y * ex2(ml[k].x - mp) + ml[k].w * ex2(ml[k].z - mp);
                 const float grown = fmaxf(m, mp), u = ex2(m - grown), v = ex2(mp - grown);
-                l = l * u + lp * v;
+                l = l * u + (ml[k].y + ml[k].w) * v;
                 acc.x = acc.x * u + o[k].x * v;
                 acc.y = acc.y * u + o[k].y * v;
                 acc.z = acc.z * u + o[k].z * v;
@@ -907,6 +916,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
         *out = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
         if (a.lse && channel == 0) a.lse[query] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
     }
+    // the kernel behind waits for this one, and this one for all before it
+    if (!waited) ptx::grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- host side
