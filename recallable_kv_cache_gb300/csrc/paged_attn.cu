@@ -1082,14 +1082,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     }
     if (blockIdx.x == 0)
         for (int s = threadIdx.x; s < a.c.seqs; s += NT) check_len(a.c, s);
-    // units without rows: nothing else writes their outputs
-    for (int s = blockIdx.x; s < a.c.seqs; s += grid)
+    // units without rows: nothing else writes their outputs (OWN: the kernel behind does)
+    for (int s = blockIdx.x; s < a.c.seqs && !OWN; s += grid)
         if (rows_attended(a.c, s) == 0)
             for (long long i = threadIdx.x; i < (long long)a.c.heads * a.g * D; i += NT) {
                 const size_t o = (size_t)s * a.c.heads * a.g;
                 a.out[o * D + i] = 0.f;
                 if (a.lse && i < (long long)a.c.heads * a.g) a.lse[o + i] = -INFINITY;
-                if (OWN && i < (long long)a.c.heads * a.g) a.lse2[o + i] = -INFINITY;
             }
     if (!works) {
         if (OWN) ptx::grid_dependency_wait();

@@ -178,10 +178,10 @@ __device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigne
 // The tiles of shared rows go to CTAs evenly, a CTA's share beginning and ending
 // anywhere, or every unit goes in equal parts to CTAs of its own.  Where a share
 // passes from one unit to the next the products wait for the new queries and the
-// softmax for the products, as long as some two tiles, so the second deal is
+// softmax for the products, as long as some three tiles, so the second deal is
 // taken where its largest part is at most OWN_EXTRA tiles above an even share.
 constexpr float TILE_COST = 1.7f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 6.f;  // us
-constexpr int OWN_EXTRA = 2;
+constexpr int OWN_EXTRA = 3;
 // The SMs for the shared rows, of `grid`: `total` tiles of these, and of the own
 // rows `own` tiles of 16 of `units` (sequence, KV head) pairs.
 __device__ __forceinline__ int ctas_for_shared(int grid, int total, float own, int units) {
@@ -866,7 +866,17 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
         const int some = (int)(row / heads_q);  // a sequence of the group
         const int i = a.group_of[some], total = a.tile_base[a.groups];
         const int2 dealt = *a.deal;
-        if (a.skip[some] == 0) continue;
+        if (a.skip[some] == 0) {
+            // a sequence in no group (its rows are in order of their own): attended, or without rows
+            if (a.c.lens[some] <= 0) {
+                const int hq = (int)(row - (long long)some * heads_q);
+                if (!waited) ptx::grid_dependency_wait();
+                waited = true;
+                reinterpret_cast<float4*>(a.out + ((size_t)some * heads_q + hq) * D)[channel] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (a.lse && channel == 0) a.lse[(size_t)some * heads_q + hq] = -INFINITY;
+            }
+            continue;
+        }
         const Group gr = a.group[i];
         const int nt = (gr.rows + KT - 1) / KT, all = gr.members * a.g;
         const int left = (int)(row - (long long)gr.first * heads_q), h = left / all, x = left - h * all;
@@ -884,8 +894,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
         if (!waited) ptx::grid_dependency_wait();
         waited = true;
         float4* out = reinterpret_cast<float4*>(a.out + query * D) + channel;
-        float4 acc = *out;
-        float m = a.own_lse2[query], l = m == -INFINITY ? 0.f : 1.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -INFINITY, l = 0.f;
+        if (min(a.c.lens[gr.first + member], a.c.rows) > gr.rows) {  // it has rows of its own
+            acc = *out;
+            m = a.own_lse2[query];
+            l = m == -INFINITY ? 0.f : 1.f;
+        }
 #pragma unroll 1
         for (int p0 = 0; p0 < parts; p0 += PARTS) {
             float4 o[PARTS], ml[PARTS];

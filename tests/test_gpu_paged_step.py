@@ -592,6 +592,24 @@ def test_shared_bad_groups_are_reported(starts, prefix):
     assert int(c.err) == 3
 
 
+def test_shared_lengths_outside_the_cache():
+    """A length above the capacity is clamped to it, a negative one is none, inside and outside of groups."""
+    c = Shared([(64, [0, 0]), (0, [5, 7, 0])], 2, 4, 16, width=4)
+    c.lens.copy_(ints([10 ** 9, 64, -3, 7, -1]))
+    c.run()
+    c.lens_list = [64, 64, 0, 7, 0]
+    c.check()
+    assert int(c.err) == 3
+
+
+def test_shared_many_sequences_without_rows_of_their_own():
+    """More groups than one warp has lanes, shares that pass from unit to unit, sequences without any row."""
+    c = Shared([(160 + 16 * (i % 9), [0] * (2 + i % 3)) for i in range(40)] + [(0, [0, 0, 3])], 4, 8, 16, seed=3)
+    c.run()
+    c.check()
+    assert int(c.err) == 0
+
+
 def test_shared_member_shorter_than_the_prefix():
     c = Shared([(64, [0, 5, 30])], 2, 4, 16)
     c.lens[1] = 20
