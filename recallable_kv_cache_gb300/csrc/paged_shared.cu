@@ -65,8 +65,7 @@ constexpr int PANEL = 128 * 128;     // 64 channels of 128 rows
 constexpr int STAGE = 2 * PANEL;     // K or V of a tile
 constexpr int NST = 6;
 constexpr int SOFT_WARPS = 8, OUT_WARPS = 8;
-constexpr int VALUE_WARP = 2 + SOFT_WARPS + OUT_WARPS;
-constexpr int THREADS = 32 * (VALUE_WARP + 1);
+constexpr int THREADS = 32 * (2 + SOFT_WARPS + OUT_WARPS);
 constexpr int PREP_THREADS = 256;
 constexpr int JOIN_ROWS = 8;
 constexpr int JOIN_THREADS = JOIN_ROWS * D / 4;
@@ -415,10 +414,10 @@ __device__ __forceinline__ int v_index(int j) { return 2 * j + 2; }
 struct __align__(8) Bars {
     uint64_t full[NST], empty[NST];
     uint64_t q_full;
-    uint64_t s_full[NSP], p_full[NSP], p_empty[NSP], top_empty[NSP];
+    uint64_t s_full[NSP], p_full[NSP], top_empty[NSP];
     uint64_t top_full[4];            // of a quarter of the queries
     uint64_t t_full, t_empty;
-    uint64_t never, drain[2];
+    uint64_t never, drain;
     int asked[NST];    // the last phase of a stage that was asked for
     int rows[NST];     // of a K stage's tile: those whose page is good
     int s_rows[NSP], t_rows;
@@ -434,7 +433,7 @@ constexpr int SMEM_MOST = 232448;  // of a CTA
 static_assert(sizeof(Smem) + 1024 <= SMEM_MOST && sizeof(Bars) <= 1024, "the barriers take what aligning leaves");
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, const SharedArgs& a) {
-    if (ptx::mbar_wait_held(bar, parity, a.wait_limit, &b->abort)) return true;
+    if (ptx::mbar_wait(bar, parity, a.wait_limit, &b->abort)) return true;
     if (atomicExch(&b->abort, 1) == 0) report(a.c.dev_err, CKV_DEV_TIMEOUT);
     return false;
 }
@@ -458,14 +457,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < NSP; ++i) {
             ptx::mbar_init(&bs->s_full[i], 2);  // the product, and the thread that says of how many rows
             ptx::mbar_init(&bs->p_full[i], SOFT_WARPS);
-            ptx::mbar_init(&bs->p_empty[i], 1);
             ptx::mbar_init(&bs->top_empty[i], OUT_WARPS);
         }
         ptx::mbar_init(&bs->t_full, 2);
         ptx::mbar_init(&bs->t_empty, OUT_WARPS);
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&bs->top_full[i], 2);
         ptx::mbar_init(&bs->never, 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&bs->drain[i], 1);
+        ptx::mbar_init(&bs->drain, 1);
         bs->abort = 0;
         ptx::fence_barrier_init();
     }
@@ -563,14 +561,59 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (j > 0 && alive) alive = load(last, v_index(j - 1), &tv);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ S = Q K^T
-        // The lanes keep step for the runs; one waits and issues.  S and T are
-        // issued by warps of their own: a commit holds its thread until the
-        // products before it have begun, and the tensor core would run dry behind
-        // every one of them (3400 instead of 2700 cycles a tile).
+        // ------------------------------------------------------------ the products
+        // The lanes keep step for the runs; one waits and issues.  S of the tile
+        // two on follows T of a tile, into the buffer whose weights that has read.
         const uint32_t ring = ptx::smem_u32(sm.ring);
         const uint64_t q = ptx::smem_desc_sw128(ptx::smem_u32(sm.q));
-        constexpr uint32_t ID_S = ptx::idesc_bf16_f32(QT, KT);
+        constexpr uint32_t ID_S = ptx::idesc_bf16_f32(QT, KT), ID_T = ptx::idesc_bf16_f32(QT, D) | ptx::IDESC_B_MN_MAJOR;
+        auto scores = [&](int jj) {
+            const int it = k_index(jj), st = it % NST, b = jj % NSP;
+            if (!wait(&bs->full[st], (it / NST) & 1, bs, a)) return false;
+            ptx::tc_fence_after();
+            const int n = bs->rows[st];
+            bs->s_rows[b] = n;
+            ptx::mbar_arrive(&bs->s_full[b]);
+            const uint64_t kd = ptx::smem_desc_sw128(ring + st * STAGE);
+            if (n > 0)
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t at = ((ks >> 2) * PANEL + (ks & 3) * 32) >> 4;
+                    ptx::mma_bf16(tmem + b * SP_COLS, q + at, kd + at, ID_S, ks > 0);
+                }
+            ptx::mma_commit(&bs->s_full[b]);
+            return true;
+        };
+        auto values = [&](int jj) {
+            const int it = v_index(jj), st = it % NST, b = jj % NSP;
+            if (!wait(&bs->full[st], (it / NST) & 1, bs, a) || !wait(&bs->p_full[b], (jj / NSP) & 1, bs, a) ||
+                (jj > 0 && !wait(&bs->t_empty, (jj - 1) & 1, bs, a)))
+                return false;
+            const int n = bs->s_rows[b], steps = n / 16;
+            const uint32_t p = tmem + b * SP_COLS;
+            const uint64_t v = ptx::smem_desc_sw128_mn(ring + st * STAGE, PANEL);
+            ptx::tc_fence_after();
+            bs->t_rows = n;
+            ptx::mbar_arrive(&bs->t_full);
+            // the low terms first; eight columns hold a term of 16 rows.
+            // (Straight code for all 24 products takes 5 us at its first pass,
+            // when it has to be fetched.)
+#pragma unroll 1
+            for (int term = 0; term < 3; ++term) {
+                uint32_t at = p + (term == 1 ? MID_COL : term ? 0 : LOW_COL);
+                const uint32_t pairs = term == 1 ? 16 : 32;  // columns from two steps' terms to the next two's
+#pragma unroll
+                for (int ks = 0; ks < 8; ks += 2) {
+                    if (ks < steps)
+                        ptx::mma_bf16_ts(tmem + T_COL, at, v + (ks * 2048 >> 4), ID_T, term > 0 || ks > 0);
+                    if (ks + 1 < steps)
+                        ptx::mma_bf16_ts(tmem + T_COL, at + 8, v + ((ks + 1) * 2048 >> 4), ID_T, 1);
+                    at += pairs;
+                }
+            }
+            ptx::mma_commit(&bs->t_full);
+            return true;
+        };
         int runs = 0;
         Run r = share.run;
         for (int t = t_begin; t < t_end && alive; ++runs) {
@@ -578,66 +621,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (leader) {
                 if (runs == 0 && a.stall && !wait(&bs->never, 0, bs, a)) alive = false;
                 if (alive) alive = wait(&bs->q_full, runs & 1, bs, a);
-                for (int jj = j; jj < j + r.n && alive; ++jj) {
-                    const int it = k_index(jj), st = it % NST, b = jj % NSP, use = jj / NSP;
-                    alive = wait(&bs->full[st], (it / NST) & 1, bs, a) &&
-                            (use == 0 || wait(&bs->p_empty[b], (use - 1) & 1, bs, a));
-                    if (!alive) break;
-                    ptx::tc_fence_after();
-                    const int n = bs->rows[st];
-                    bs->s_rows[b] = n;
-                    ptx::mbar_arrive(&bs->s_full[b]);
-                    const uint64_t kd = ptx::smem_desc_sw128(ring + st * STAGE);
-                    if (n > 0)
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) {
-                            const uint32_t at = ((ks >> 2) * PANEL + (ks & 3) * 32) >> 4;
-                            ptx::mma_bf16(tmem + b * SP_COLS, q + at, kd + at, ID_S, ks > 0);
-                        }
-                    ptx::mma_commit(&bs->s_full[b]);
+#pragma unroll 1
+                for (int jj = j - 2; jj < j + r.n && alive; ++jj) {
+                    if (jj >= j) alive = values(jj);
+                    if (alive && jj + 2 < j + r.n) alive = scores(jj + 2);
                 }
             }
             alive = __all_sync(FULL, alive);
             j += r.n;
             t += r.n;
         }
-    } else if (warp == VALUE_WARP) {
-        // ------------------------------------------------------------ T = P V
-        const uint32_t ring = ptx::smem_u32(sm.ring);
-        constexpr uint32_t ID_T = ptx::idesc_bf16_f32(QT, D) | ptx::IDESC_B_MN_MAJOR;
-        if (leader)
-            for (int jj = 0; jj < n_tiles && alive; ++jj) {
-                const int it = v_index(jj), st = it % NST, b = jj % NSP, use = jj / NSP;
-                alive = wait(&bs->full[st], (it / NST) & 1, bs, a) && wait(&bs->p_full[b], use & 1, bs, a);
-                if (!alive) break;
-                const int n = bs->s_rows[b], steps = n / 16;
-                const uint32_t p = tmem + b * SP_COLS;
-                const uint64_t v = ptx::smem_desc_sw128_mn(ring + st * STAGE, PANEL);
-                alive = jj == 0 || wait(&bs->t_empty, (jj - 1) & 1, bs, a);
-                if (!alive) break;
-                ptx::tc_fence_after();
-                bs->t_rows = n;
-                ptx::mbar_arrive(&bs->t_full);
-                // the low terms first; eight columns hold a term of 16 rows.
-                // (Straight code for all 24 products takes 5 us at its first pass,
-                // when it has to be fetched.)
-#pragma unroll 1
-                for (int term = 0; term < 3; ++term) {
-                    uint32_t at = p + (term == 1 ? MID_COL : term ? 0 : LOW_COL);
-                    const uint32_t pairs = term == 1 ? 16 : 32;  // columns from two steps' terms to the next two's
-#pragma unroll
-                    for (int ks = 0; ks < 8; ks += 2) {
-                        if (ks < steps)
-                            ptx::mma_bf16_ts(tmem + T_COL, at, v + (ks * 2048 >> 4), ID_T, term > 0 || ks > 0);
-                        if (ks + 1 < steps)
-                            ptx::mma_bf16_ts(tmem + T_COL, at + 8, v + ((ks + 1) * 2048 >> 4), ID_T, 1);
-                        at += pairs;
-                    }
-                }
-                ptx::mma_commit(&bs->t_full);
-                ptx::mma_commit(&bs->p_empty[b]);
-            }
-        __syncwarp();
     } else if (warp < 2 + SOFT_WARPS) {
         // ------------------------------------------------------------ softmax
         const int half = (warp - 2) >> 2, quarter = warp & 3;
@@ -661,18 +654,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ptx::tc_fence_after();
                     // 16 rows at a time, of which there are `mine` / 16 at most four
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < 64 && c < mine; c += 32) {
-                        uint32_t s[2][16];
-                        ptx::tmem_ld16(sp + half * 64 + c, s[0]);
-                        ptx::tmem_ld16(sp + half * 64 + c + 16, s[1]);
+                    {
+                        uint32_t s[2][32];
+                        ptx::tmem_ld32(sp + half * 64, s[0]);
+                        ptx::tmem_ld32(sp + half * 64 + 32, s[1]);
                         ptx::tmem_ld_wait();
-                        const bool both = c + 16 < mine;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float x = __uint_as_float(s[0][e]), y = __uint_as_float(s[1][e]);
-                            top[e & 3] = fmaxf(fmaxf(top[e & 3], x), both ? y : x);
-                        }
+                        for (int c = 0; c < 4; ++c)
+                            if (16 * c < mine)
+#pragma unroll
+                                for (int e = 16 * (c & 1); e < 16 * (c & 1) + 16; e += 2)
+                                    top[(e >> 1) & 3] = fmaxf(fmaxf(top[(e >> 1) & 3], __uint_as_float(s[c >> 1][e])),
+                                                              __uint_as_float(s[c >> 1][e + 1]));
                     }
                     const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     // the other half's, so that all of a query's weights go by one maximum
@@ -783,7 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) {
                     ptx::mbar_arrive(&bs->top_empty[b]);
-                    if (warp == VALUE_WARP - 1) ptx::mbar_arrive(&bs->empty[v_index(jj) % NST]);
+                    if (warp == 1 + SOFT_WARPS + OUT_WARPS) ptx::mbar_arrive(&bs->empty[v_index(jj) % NST]);
                 }
                 if (busy && n > 0) {
                     ptx::tc_fence_after();
@@ -836,9 +829,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0 && lane == 0)
             for (int i = 0; i < NST; ++i)
                 if (bs->asked[i] >= 0) ptx::mbar_wait(&bs->full[i], bs->asked[i] & 1, a.wait_limit, nullptr);
-        if ((warp == 1 || warp == VALUE_WARP) && leader) {
-            ptx::mma_commit(&bs->drain[warp == 1]);
-            ptx::mbar_wait(&bs->drain[warp == 1], 0, a.wait_limit, nullptr);
+        if (warp == 1 && leader) {
+            ptx::mma_commit(&bs->drain);
+            ptx::mbar_wait(&bs->drain, 0, a.wait_limit, nullptr);
         }
     }
     if (warp == 1) {

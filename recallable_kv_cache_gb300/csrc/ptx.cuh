@@ -57,31 +57,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, long l
     }
 }
 
-// The same for waits of microseconds in warps that share a scheduler with busy
-// ones: the hardware may hold the thread for `hold` ns a try, so that it does
-// not take issue slots by asking again.
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity, uint32_t hold) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(hold)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_held(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort) {
-    constexpr uint32_t HOLD = 20000;
-    if (mbar_try_wait(bar, parity, HOLD)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (mbar_try_wait(bar, parity, HOLD)) return true;
-        if (abort != nullptr && *abort) return false;
-        if (clock64() - t0 > limit) return false;
-    }
-}
-
 // ---------------------------------------------------------------- bulk copies
 // Plain (untiled) bulk copy global -> shared; both addresses 16-byte aligned,
 // size a multiple of 16.  Completion is signalled on `bar` as tx bytes.
