@@ -511,15 +511,14 @@ ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, i
  *     j for the sequence's j-th token; four times -1 for tokens of refused
  *     sequences and behind the last.
  * A sequence whose start, first or count is negative, that would pass R or
- * position 2^31 - 1, whose tokens do not fit n_slots, or with shared or held_in
- * outside 0 <= shared <= held_in <= max_pages, is granted nothing and left as
- * it is (CKV_DEV_BAD_COUNT; a negative count is no token in starts, which never
- * pass n_slots).  A span outside the ring counts as empty (head 0, count 0) and
+ * position 2^31 - 1, whose tokens do not fit n_slots (one without tokens always
+ * does), or with shared or held_in outside 0 <= shared <= held_in <= max_pages,
+ * is granted nothing and left as it is (CKV_DEV_BAD_COUNT; a negative count is no
+ * token in starts, which never pass n_slots).  A span outside the ring counts as empty (head 0, count 0) and
  * pages handed back to a full ring are lost, CKV_DEV_BAD_COUNT both.  A bad
- * page id gives no slot (CKV_DEV_BAD_INDEX).  The call
- * writes the cache's table, lens and seen; K and V are not touched.  counts,
- * start and first may be lens or seen themselves, held_out may be held_in and
- * span_out span_in.  free_pages must not overlap anything else.
+ * page id gives no slot (CKV_DEV_BAD_INDEX).  The call writes the cache's table,
+ * lens and seen; K and V are not touched.  counts, start and first may be lens
+ * or seen themselves, held_out may be held_in and span_out span_in.  free_pages must not overlap anything else.
  * Errors: as above; CKV_ERR_ARG (a null pointer other than start, first and
  * shared; n_slots or free_cap < 1; n_pages * page_size above 2^31 - 1; arrays
  * that overlap without being the same as above). */
@@ -540,8 +539,8 @@ ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t* counts, c
  * turns and amplitude.  fp32 arithmetic, rounded once at the end; sum_i x_i^2
  * has to stay below 2^127. */
 typedef struct {
-    const uint64_t* turns; /* [rot / 2]; NULL only if rot is 0 */
-    const float* q_weight; /* [d], or NULL: queries are not normed */
+    const uint64_t* turns; /* [rot / 2], 16-byte aligned; NULL only if rot is 0 */
+    const float* q_weight; /* [d], 16-byte aligned, or NULL: queries are not normed */
     const float* k_weight;
     float eps;
     float amplitude;
@@ -596,8 +595,8 @@ ckv_status ckv_paged_shared_workspace(const ckv_paged_cache* cache, int32_t g, i
  * all the same, CKV_DEV_BAD_COUNT).  A start outside [0, seqs] or below an
  * earlier one is taken as the nearest that is not, a negative prefix as 0
  * (CKV_DEV_BAD_COUNT).  fp32 caches are attended sequence by sequence.
- * Arguments, accuracy, workspace (zeroed before its first use, one for calls
- * that may overlap) and errors as for ckv_paged_decode_attn; CKV_ERR_ARG also
+ * Arguments, accuracy, workspace (zeroed before its first use, one each for
+ * calls that may overlap) and errors as for ckv_paged_decode_attn; CKV_ERR_ARG also
  * for groups < 0, or above 0 without group_starts and prefix, or above seqs. */
 ckv_status ckv_paged_shared_attn(const ckv_paged_cache* cache, const void* q, int32_t q_dtype,
                                  const int64_t* q_stride, int32_t g, float scale, const int32_t* group_starts,

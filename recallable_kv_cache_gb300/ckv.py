@@ -438,11 +438,11 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
     return w, amplitude
 
 
-_ROTARIES, _STRIDES = {}, {}  # ckv_rotary structs and stride arrays, made once for equal values
+_STRIDES = {}  # stride arrays, made once for equal strides
 
 
 def _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device):
-    """Address of the ckv_rotary of a call, after the checks."""
+    """(address, ckv_rotary) of a call, after the checks."""
     import torch
     rot = at = 0
     if turns is not None:
@@ -457,15 +457,9 @@ def _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device):
                 raise TypeError(f"{name} must be float32, got {w.dtype}")
             if w.shape != (128,) or not w.is_contiguous() or w.device != device:
                 raise ValueError(f"{name} must be contiguous [128] on {device}, got {list(w.shape)} on {w.device}")
-    key = (at, 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), eps,
-           amplitude, rot, interleaved)
-    got = _ROTARIES.get(key)
-    if got is None:
-        if len(_ROTARIES) > 256:
-            _ROTARIES.clear()
-        struct = Rotary(at or None, key[1] or None, key[2] or None, eps, amplitude, rot, 1 if interleaved else 0)
-        got = _ROTARIES[key] = (ctypes.addressof(struct), struct)
-    return got
+    struct = Rotary(at or None, None if q_weight is None else q_weight.data_ptr(),
+                    None if k_weight is None else k_weight.data_ptr(), eps, amplitude, rot, 1 if interleaved else 0)
+    return ctypes.addressof(struct), struct
 
 
 def _heads(name, t, tokens, heads, dtype, device):

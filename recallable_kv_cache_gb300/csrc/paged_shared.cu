@@ -17,25 +17,31 @@
 // out evenly to one persistent CTA an SM, which keeps its unit's queries in
 // shared memory and streams K and V tiles through a ring of six 32 KB stages.
 //   S = Q K^T           tcgen05 128 x 128 x 128, into tensor memory
-//   P = 2^{S scale - m}  one thread a query, m its running maximum so far
+//   P = 2^{S scale - m}  m a query's running maximum, P in the place of S
 //   T = P V             P from tensor memory, as three bf16 terms
-//   O = O a + T b       in registers, one thread half of a query's channels
+//   O = O a + T         in registers, a = 2^{m before - m}
 // A weight is the sum of three bf16 terms (its upper, middle and lower eight
-// bits), so that the products are those of fp32 weights; with one term outputs
-// would be off by 2^-9 where the decode attention of this library is off by
-// 2^-21.  That makes four products a tile, some 1.1 us at the measured dense
-// rate, against 1.5 us that an SM's share of HBM takes for the tile's 64 KB.  T starts from
-// zero at each tile and joins O by an ordinary addition, as the tensor core
-// truncates what it accumulates and O grows over hundreds of tiles.  It also
-// leaves O's scaling off the path from one tile's maximum to the next one's
-// product: two groups of four warps take the softmax of every other tile, each
-// with a running maximum of its own, and O follows with the larger of both.
+// bits), so that the products are those of fp32 weights.  With one term outputs
+// would be off by 2^-9, with two by 1.4e-6 of the largest, with three by 4e-7,
+// which is what the decode attention of this library is off by.  That makes four
+// products a tile, some 1.1 us at the measured dense rate, against 1.5 us that an
+// SM's share of HBM takes for the tile's 64 KB.  T starts from zero at each tile
+// and joins O by an ordinary addition, as the tensor core truncates what it
+// accumulates and O grows over hundreds of tiles; that also leaves O's scaling
+// off the path from one tile's maximum to the next one's product.
+// What bounds a long run of tiles is the way of a tile through the roles below,
+// about 1.8 us, of which the softmax is 1.3 (32 sequences behind 64k rows, 8
+// heads of 4 queries: 64 us, 4.2 TB/s of their 268 MB): with all tiles from
+// sixteen pages, so from the caches, these take 59 us, and 160 sequences behind
+// 16k rows 76 instead of 77.  The softmax's two buffers are what tensor memory
+// has room for, and its warps take every tile together: two groups that each
+// took every other tile, T in two halves of 64 channels, and S and T from a warp
+// each were as fast or slower (160 behind 16k rows: 82, 78 to 81, 77 us).
 // Warp roles:
 //   warp 0       asks for the tiles (TMA)
-//   warp 1       owns tensor memory, issues S
+//   warp 1       owns tensor memory, issues S and T
 //   warps 2-9    softmax, a thread 64 rows of a query
 //   warps 10-17  queries to shared memory; O, a thread 64 channels of a query
-//   warp 18      issues T
 // Where a unit is several CTAs' its parts are joined by the last kernel in the
 // order of its rows, so that results do not depend on timing.
 #include <cuda.h>
@@ -120,9 +126,10 @@ struct SharedArgs {
     int2* deal;         // [1] CTAs with a unit's part, 0: the even deal; CTAs that it goes to
     int* own_ctas;      // [1] CTAs for the sequences' own rows
     float* own_lse2;    // [seqs * heads * g] of the sequences' own rows, base 2
-    // Parts: O as [channel / 4][query of the block] of four, and for either half of
-    // the tiles' rows (the maximum that O goes by, the sum).  The CTA in which a unit begins leaves its part behind
-    // those of the units before it, the others (each continues one at most) by CTA.
+    // Parts: O as [channel / 4][query of the block] of four, and for either half
+    // of the tiles' rows (the maximum that O goes by, the sum).  The CTA in which
+    // a unit begins leaves its part behind those of the units before it, the
+    // others (each continues one at most) by CTA.
     float4* unit_o;     // [seqs * heads * g][D / 4] in all
     float4* unit_ml;    // [seqs * heads * g]
     float4* cta_o;      // [MAX_GRID][D / 4][QT]

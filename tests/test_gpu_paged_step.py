@@ -429,6 +429,17 @@ def test_append_rotated(start, counts, heads, g, page, dtype, layout, rot, inter
     assert int(a.err) == 0
 
 
+def test_append_with_queries_in_place():
+    a, b = (Append([3, 0], [40, 33], 2, 4, 16) for _ in range(2))
+    turns = ckv.rotary_turns(ckv.rotary_frequencies(128)[0]).cuda()
+    a.cache.append_rotated(a.q, a.k, a.v, a.slots, turns, a.q_out)
+    b.cache.append_rotated(b.q, b.k, b.v, b.slots, turns, b.q)
+    assert torch.equal(a.q_out, b.q) and torch.equal(a.k, b.k)
+    at = a.slots[:, 0].long()
+    for x, y in ((a.K, b.K), (a.V, b.V)):
+        assert torch.equal(x[at // 16, :, at % 16], y[at // 16, :, at % 16])
+
+
 @pytest.mark.parametrize("column,value,code", [(0, -1, 0), (0, -2, 2), (0, 10 ** 7, 2), (1, -1, 2), (1, 2, 2), (2, -1, 2),
                                                (2, 10 ** 6, 2)])
 def test_tokens_without_a_place_are_left_out(column, value, code):
@@ -533,6 +544,8 @@ SHARED = [
     ([(5120, [9, 100])], 4, 1, 16, "bf16", "hpd"),
     ([(20000, [3, 700, 33])], 1, 7, 32, "bf16", "hpd"),
     ([(32 * (i % 5), [i % 4] * (1 + i % 3)) for i in range(90)], 2, 3, 32, "bf16", "hpd"),
+    ([(64, [0, 1, 2, 0]), (160, [0] * 1100)], 1, 1, 16, "bf16", "hpd"),     # more sequences than fit the prep's shared memory
+    ([(16 * (i % 4), [i % 2, 1]) for i in range(300)], 1, 2, 16, "bf16", "hpd"),  # more groups than it has threads
     ([(16, [1, 1])], 1, 1, 16, "f32", "hpd"),
     ([(480, [31, 1, 300]), (96, [3, 4])], 2, 9, 48, "f32", "wide"),
     ([(2048, [100] * 9)], 2, 4, 16, "f32", "phd"),
@@ -775,6 +788,104 @@ def test_prompts_then_decode_steps_behind_a_prefix():
     mine = [p for s in range(S) for p in table[s, (prefix // page if s else 0):int(held[s])].tolist()]
     left = [int(ring[(int(span[0]) + i) % n_pages]) for i in range(int(span[1]))]
     assert sorted(mine + left) == list(range(n_pages))
+
+
+def batch(seed, S=6, heads=2, g=4, page=16, width=12, prefix=96):
+    """A batch behind a prefix, and its step as a function without host work between the calls."""
+    gen = torch.Generator().manual_seed(seed)
+    n_pages = S * width
+    K, V = pools(n_pages, heads, page, "bf16", "hpd", gen)
+    table = torch.full((S, width), -1, dtype=torch.int32)
+    common = prefix // page
+    table[:, :common] = torch.arange(common, dtype=torch.int32)
+    x = dict(K=K, V=V, table=table.cuda(), lens=ints([prefix] * S), seen=ints([prefix] * S), held=ints([common] * S),
+             ring=ints(list(range(common, n_pages))), span=ints([0, n_pages - common]), granted=ints([0] * S),
+             starts=ints([0] * (S + 1)), counts=ints([1 + s % 3 for s in range(S)]), shared=ints([common] * S),
+             groups=ints([0, S]), prefix=ints([prefix]), err=ints([0]))
+    T = sum(1 + s % 3 for s in range(S))
+    qkv = torch.randn(T, heads * (g + 2), D, generator=gen).to(torch.bfloat16).cuda()
+    x.update(slots=ints([[0] * 4] * T), qkv=qkv, q_out=torch.zeros(T, heads * g, D, dtype=torch.bfloat16, device="cuda"),
+             out=torch.zeros(S, heads * g, D, device="cuda"), lse=torch.zeros(S, heads * g, device="cuda"))
+    turns = ckv.rotary_turns(ckv.rotary_frequencies(128)[0]).cuda()
+    cache = ckv.PagedCache(K, V, x["table"], x["lens"], g=g, seen=x["seen"], dev_err=x["err"], shared=True)
+
+    def step():
+        q, k, v = qkv[:, :heads * g], qkv[:, heads * g:heads * (g + 1)], qkv[:, heads * (g + 1):]
+        cache.plan(x["counts"], x["held"], x["ring"], x["span"], x["slots"], x["starts"], x["granted"], shared=x["shared"])
+        cache.append_rotated(q, k, v, x["slots"], turns, x["q_out"])
+        cache.shared_attn(x["q_out"][:S], x["out"], x["groups"], x["prefix"], lse=x["lse"])
+        # the rows of the step go into the next one's, so that steps depend on one another
+        qkv[:S, :heads * g].add_(x["out"].to(torch.bfloat16))
+
+    return x, step
+
+
+def test_steps_captured_and_side_by_side():
+    """Two batches' steps replayed at once, on streams of their own, against the same steps called one by one."""
+    alone = []
+    for seed in (1, 2):
+        x, step = batch(seed)
+        for _ in range(12):
+            step()
+        torch.cuda.synchronize()
+        alone.append(x)
+    both, graphs = [], []
+    for seed in (1, 2):
+        x, step = batch(seed)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            step()
+        both.append((x, step))
+        graphs.append((graph, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(12):
+        for graph, stream in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for x, (y, _) in zip(alone, both):
+        assert int(x["err"]) == 0 and x["granted"].tolist() == [1 + s % 3 for s in range(6)]
+        assert x["out"].isfinite().all()
+        for name in x:
+            assert torch.equal(x[name], y[name]), name
+
+
+def test_offsets_above_32_bits():
+    """Pools of 5 GB each, with the rows at their ends; token strides of 4 GB."""
+    heads, g, page, n_pages, S, prefix = 8, 2, 128, 20000, 2, 128
+    K, V = (torch.zeros(n_pages, heads, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gen = torch.Generator().manual_seed(0)
+    at = [19999, 19997, 16500]
+    for pool in (K, V):
+        pool[at] = torch.randn(3, heads, page, D, generator=gen).to(torch.bfloat16).cuda()
+    table, lens, err = ints([[19999, 19997], [19999, 16500]]), ints([200, 133]), ints([0])
+    cache = ckv.PagedCache(K, V, table, lens, g=g, dev_err=err, shared=True)
+    q = torch.randn(S, heads * g, D, generator=gen).to(torch.bfloat16).cuda()
+    out, want = (torch.zeros(S, heads * g, D, device="cuda") for _ in range(2))
+    cache.shared_attn(q, out, ints([0, S]), ints([prefix]))
+    for s in range(S):
+        k, v = (x[table[s].long()].transpose(0, 1).reshape(heads, -1, D)[:, :int(lens[s])].double() for x in (K, V))
+        p = torch.softmax(torch.matmul(q[s].double().view(heads, g, D), k.transpose(1, 2)) * D ** -0.5, dim=-1)
+        want[s] = torch.matmul(p, v).view(heads * g, D).float()
+    assert float((out - want).norm() / want.norm()) < 1e-5 and int(err) == 0
+    del cache
+
+    step = 2 ** 31
+    wide = torch.empty(step + 4096, dtype=torch.bfloat16, device="cuda")
+    q, o = (wide.as_strided((2, 4, D), (step, D, 1), x) for x in (0, 1024))
+    rows = torch.randn(2, 4, D, generator=gen).to(torch.bfloat16).cuda()
+    q.copy_(rows)
+    turns = ckv.rotary_turns(ckv.rotary_frequencies(128)[0]).cuda()
+    ckv.rotate(q, None, ints([5, 70000]), turns, o, None)
+    check_rows(o, rows, [5, 70000], turns, 128, False, None, 0, 1.0, "bf16")
+    cache = ckv.PagedCache(K, V, table, lens, g=1, dev_err=err)
+    slots = ints([[19998 * page + 3, 0, 0, 9], [n_pages * page - 1, 1, 1, 8]])
+    k = rows.repeat(1, 2, 1)
+    cache.append_rotated(None, k, k, slots, turns, None)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    check_rows(torch.stack([K[19998, :, 3], K[19999, :, 127]]), k, [9, 8], turns, 128, False, None, 0, 1.0, "bf16")
+    assert torch.equal(V[19998, :, 3], k[0]) and torch.equal(V[19999, :, 127], k[1])
 
 
 # ---------------------------------------------------------------- refusals of the handle

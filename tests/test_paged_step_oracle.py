@@ -222,6 +222,12 @@ def test_bad_rotaries_are_refused(lib, bad):
     assert append(lib, apart(), rot(**bad)) == ARG
 
 
+@pytest.mark.parametrize("bad", [dict(turns=P + 8), dict(q_weight=P + 4), dict(k_weight=P + 8)])
+def test_misaligned_rotaries_are_refused(lib, bad):
+    assert rotate(lib, rot(**bad)) == ALIGN
+    assert append(lib, apart(), rot(**bad)) == ALIGN
+
+
 def test_null_rotary_is_refused(lib):
     assert rotate(lib, None) == ARG and append(lib, apart(), None) == ARG
 
