@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) paged_slots_kernel(const __grid_
     const int s = a.by_blocks.quot(blockIdx.x, &b);
     const int t0 = a.starts[s], t1 = a.starts[s + 1], n = a.granted[s];
     const int row = a.c.lens[s] - n;
-    // first may be lens, which the plan has moved on
+    // first may be lens, which the plan has moved on (start is lens then, too)
     const int position = a.c.seen ? a.c.seen[s] - n : (a.first && a.first != a.c.lens ? a.first[s] : row);
     const int step = a.by_blocks.d * SLOT_THREADS;
     for (int j = b * SLOT_THREADS + threadIdx.x; j < t1 - t0; j += step)
@@ -452,7 +452,9 @@ extern "C" ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t
             if (!apart(writes[i], reads[j]) && !(may_be_same && writes[i].p == reads[j].p)) return CKV_ERR_ARG;
         }
     }
-    a.slots_here = n_slots <= SLOTS_HERE;
+    // (positions that count from the old lens, rows from other numbers, and no
+    // seen: after the plan nothing holds them any more, so it writes the map)
+    a.slots_here = n_slots <= SLOTS_HERE || (!a.c.seen && a.first == a.c.lens && a.start != a.c.lens);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (S <= 256 && (n_slots <= 512 || !a.slots_here))

@@ -174,6 +174,21 @@ def test_plan_counts_from_lens():
     p.check()
 
 
+@pytest.mark.parametrize("n_slots", [300, 5000])
+@pytest.mark.parametrize("S", [3, 1100])
+def test_plan_positions_from_lens(S, n_slots):
+    """Positions count from the old lens, rows from other numbers, and the cache has no seen."""
+    start, counts, lens = rand(S, 0, 9, 1), rand(S, 0, 1, 2), rand(S, 0, 300, 3)
+    counts[1] = 100
+    p = Plan(start, counts, 16, n_slots=n_slots, seen=False)
+    p.lens.copy_(ints(lens))
+    p.run(first=p.lens)
+    h = p.host
+    want = ob.plan(p.table0, counts, start, lens, h["shared"], h["held"], p.ring0, h["span"], 16, n_slots, p.total)
+    torch.cuda.synchronize()
+    assert p.slots.tolist() == want["slots"] and p.lens.tolist() == [n if n is not None else x for n, x in zip(want["lens"], lens)]
+
+
 BAD_SEQS = [dict(start=-1), dict(counts=-1), dict(first=-1), dict(held=-1), dict(held=99), dict(shared=-1), dict(shared=9),
             dict(start=2 ** 31 - 1), dict(counts=2 ** 31 - 1), dict(first=2 ** 31 - 1), dict(counts=200)]
 
