@@ -30,13 +30,14 @@
 // accumulates and O grows over hundreds of tiles; that also leaves O's scaling
 // off the path from one tile's maximum to the next one's product.
 // What bounds a long run of tiles is the way of a tile through the roles below,
-// about 1.8 us, of which the softmax is 1.3 (32 sequences behind 64k rows, 8
-// heads of 4 queries: 64 us, 4.2 TB/s of their 268 MB): with all tiles from
-// sixteen pages, so from the caches, these take 59 us, and 160 sequences behind
-// 16k rows 76 instead of 77.  The softmax's two buffers are what tensor memory
-// has room for, and its warps take every tile together: two groups that each
-// took every other tile, T in two halves of 64 channels, and S and T from a warp
-// each were as fast or slower (160 behind 16k rows: 82, 78 to 81, 77 us).
+// about 1.65 us (32 sequences behind 64k rows, 8 heads of 4 queries: 62 us, 4.3
+// TB/s of their 268 MB): scores, some 2500 cycles of softmax, products and the
+// steps between them come to 6200 for each of the two buffers that tensor memory
+// has room for.  With all tiles from the caches it is a tenth less.  Slower were
+// two groups of softmax warps that each took every other tile, T in two halves of
+// 64 channels, sixteen warps for both softmax and O, and registers moved from the
+// other roles to the softmax's (160 sequences behind 16k rows, 74 us: 82, 78, 80
+// and 78).
 // Warp roles:
 //   warp 0       asks for the tiles (TMA)
 //   warp 1       owns tensor memory, issues S and T
@@ -81,7 +82,11 @@ constexpr int JOIN_THREADS = JOIN_ROWS * D / 4;
 constexpr int NSP = 2;
 constexpr uint32_t LOW_COL = 16, MID_COL = 128, SP_COLS = 192, T_COL = NSP * SP_COLS;
 
-__device__ __forceinline__ float upper(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// Two bf16 in a register, as floats.  (Taken from the packed pair, as the shift
+// can be a multiplication: packing and masking take the other unit up.)
+__device__ __forceinline__ uint64_t floats(uint32_t x) {
+    return pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
 
 // A group as the prep leaves it.
 struct Group {
@@ -709,10 +714,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], p);
                             // a float's upper 16 bits are a bf16, and what they leave is exact
                             hi[e / 2] = __byte_perm(s[e], s[e + 1], 0x7632);
-                            const uint64_t rest = fma2(pair(upper(p0), upper(p1)), minus2, p);
+                            const uint64_t rest = fma2(floats(hi[e / 2]), minus2, p);
                             const float2 y = unpair(rest);
                             mid[e / 2] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
-                            const float2 z = unpair(fma2(pair(upper(y.x), upper(y.y)), minus2, rest));
+                            const float2 z = unpair(fma2(floats(mid[e / 2]), minus2, rest));
                             lo[e / 2] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
                         }
                         // over the scores just read
@@ -774,21 +779,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int c = 0; c < 32; ++c) o[c] = 0;
             for (int k = 0; k < r.n; ++k) {
                 const int jj = j + k;
+                // the softmax's running maximum, made the same way, while T is made:
+                // the next T waits for this one to be read
+                const int b = jj % NSP;
+                if (!__all_sync(FULL, wait(&bs->p_full[b], (jj / NSP) & 1, bs, a))) {
+                    alive = false;
+                    break;
+                }
+                const float grown = fmaxf(m, fmaxf(sm.top[b][0][row], sm.top[b][1][row]) * qs);
+                const float x = ex2(m - (grown == -INFINITY ? 0.f : grown));
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bs->top_empty[b]);
                 if (!__all_sync(FULL, wait(&bs->t_full, jj & 1, bs, a))) {
                     alive = false;
                     break;
                 }
-                const int b = jj % NSP, n = bs->t_rows;
-                const float mt = fmaxf(sm.top[b][0][row], sm.top[b][1][row]);
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive(&bs->top_empty[b]);
-                    if (warp == 1 + SOFT_WARPS + OUT_WARPS) ptx::mbar_arrive(&bs->empty[v_index(jj) % NST]);
-                }
-                if (busy && n > 0) {
+                if (busy && bs->t_rows > 0) {
                     ptx::tc_fence_after();
-                    // the softmax's running maximum, made the same way
-                    const float grown = fmaxf(m, mt * qs), x = ex2(m - (grown == -INFINITY ? 0.f : grown));
                     m = grown;
                     const uint64_t x2 = pair(x, x);
                     // two loads under way at a time
@@ -797,14 +804,21 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         ptx::tmem_ld_wait();
-                        if (c < 3) ptx::tmem_ld16(at + 16 * (c + 1), v[(c + 1) & 1]);
+                        if (c < 3) {
+                            ptx::tmem_ld16(at + 16 * (c + 1), v[(c + 1) & 1]);
+                        } else {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(&bs->t_empty);
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[8 * c + e] = fma2(o[8 * c + e], x2, both(v[c & 1], e));
                     }
-                    ptx::tc_fence_before();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&bs->t_empty);
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bs->t_empty);
+                if (lane == 0 && warp == 1 + SOFT_WARPS + OUT_WARPS) ptx::mbar_arrive(&bs->empty[v_index(jj) % NST]);
             }
             if (!alive) break;
             // every product of the run has ended with its last T: the queries make room
