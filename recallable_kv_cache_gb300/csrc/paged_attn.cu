@@ -928,7 +928,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     // OWN: the kernel before is the one that attends the rows left out.  It began
     // after what wrote the inputs had ended, and the two write nothing of each
     // other's, so this one runs beside it, on the SMs that the other leaves, and
-    // waits for it at its end only, for the kernel behind both.
+    // waits for it at its end only, for the kernel behind both.  CTAs that have no
+    // SM left to them leave at once, so that the kernel behind can be brought in
+    // (there is always one that waits).
     constexpr bool OWN = !std::is_same<C, Cache>::value;
     using T = typename E::T;
     extern __shared__ unsigned char smem_raw[];
@@ -959,10 +961,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     if (!OWN) ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
     const int grid = working_ctas(a.c);
-    if (OWN && (int)blockIdx.x >= grid) {
-        ptx::grid_dependency_wait();
-        return;
-    }
+    if (OWN && (int)blockIdx.x >= grid) return;
     int cta = blockIdx.x;
     const Deal deal = deal_out<TR, NT>(a.c, start, cta, grid);
     const bool works = cta < deal.n_cta && deal.total > 0;

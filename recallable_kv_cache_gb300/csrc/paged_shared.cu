@@ -30,14 +30,13 @@
 // accumulates and O grows over hundreds of tiles; that also leaves O's scaling
 // off the path from one tile's maximum to the next one's product.
 // What bounds a long run of tiles is the way of a tile through the roles below,
-// about 1.65 us (32 sequences behind 64k rows, 8 heads of 4 queries: 62 us, 4.3
+// about 1.5 us (32 sequences behind 64k rows, 8 heads of 4 queries: 59 us, 4.5
 // TB/s of their 268 MB): scores, some 2500 cycles of softmax, products and the
-// steps between them come to 6200 for each of the two buffers that tensor memory
-// has room for.  With all tiles from the caches it is a tenth less.  Slower were
-// two groups of softmax warps that each took every other tile, T in two halves of
-// 64 channels, sixteen warps for both softmax and O, and registers moved from the
-// other roles to the softmax's (160 sequences behind 16k rows, 74 us: 82, 78, 80
-// and 78).
+// steps between them come to 6000 for each of the two buffers that tensor memory
+// has room for.  Slower were two groups of softmax warps that each took every
+// other tile, T in two halves of 64 channels, sixteen warps for both softmax and
+// O, and registers moved from the other roles to the softmax's (by a tenth, a
+// twentieth, 8 % and 4 % for 160 sequences behind 16k rows, which take 69 us).
 // Warp roles:
 //   warp 0       asks for the tiles (TMA)
 //   warp 1       owns tensor memory, issues S and T
@@ -74,7 +73,7 @@ constexpr int NST = 6;
 constexpr int SOFT_WARPS = 8, OUT_WARPS = 8;
 constexpr int THREADS = 32 * (2 + SOFT_WARPS + OUT_WARPS);
 constexpr int PREP_THREADS = 256;
-constexpr int JOIN_ROWS = 8;
+constexpr int JOIN_ROWS = 4;
 constexpr int JOIN_THREADS = JOIN_ROWS * D / 4;
 // columns of tensor memory: scores and weights of two tiles, then T.  The upper
 // and lower terms of 32 weights take the place of their scores, sixteen columns
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_c
             of_deal[1] = used;
             of_deal[2] = total;
             a.tile_base[a.groups] = total;
-            *a.own_ctas = max(1, a.grid - grid);
+            *a.own_ctas = max(1, a.grid - used);
             *a.deal = make_int2(part ? used : 0, max(1, used));
         }
     }
@@ -864,9 +863,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ---------------------------------------------------------------- joining
 // What the sequences' own rows gave, in out and own_lse2, with the parts of the
-// units.  A block has eight queries in the order of the parts, a thread four
-// channels of one, so that a part's channels come in whole lines; PARTS parts
-// are under way at a time (one after the other 20 parts took 12 us).
+// units.  A block has four rows of the output, a thread four channels of one,
+// so that the g heads of a part come side by side; PARTS parts are under way at
+// a time (one after the other 20 parts took 12 us).  Its time is the latency of
+// its loads and of its instructions, which come from L2.
 constexpr int PARTS = 8;
 __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_constant__ SharedArgs a) {
     const int channel = threadIdx.x / JOIN_ROWS, heads_q = a.c.heads * a.g;  // four channels
@@ -877,42 +877,40 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
     for (long long row = (long long)blockIdx.x * JOIN_ROWS + threadIdx.x % JOIN_ROWS; row < n; row += step) {
         // What the prep has left is whole: the kernel before this one began
         // after it.  It is looked up while that one is still at work.
-        const int some = (int)(row / heads_q);  // a sequence of the group
-        const int i = a.group_of[some], total = a.tile_base[a.groups];
+        const int s = (int)(row / heads_q), hq = (int)(row - (long long)s * heads_q);
+        const int i = a.group_of[s], skip = a.skip[s], held = a.c.lens[s], total = a.tile_base[a.groups];
         const int2 dealt = *a.deal;
-        if (a.skip[some] == 0) {
-            // a sequence in no group (its rows are in order of their own): attended, or without rows
-            if (a.c.lens[some] <= 0) {
-                const int hq = (int)(row - (long long)some * heads_q);
-                if (!waited) ptx::grid_dependency_wait();
-                waited = true;
-                reinterpret_cast<float4*>(a.out + ((size_t)some * heads_q + hq) * D)[channel] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (a.lse && channel == 0) a.lse[(size_t)some * heads_q + hq] = -INFINITY;
+        float4* out = reinterpret_cast<float4*>(a.out + row * D) + channel;
+        int c0 = 0, parts = 0;
+        const float4 *unit_o = a.unit_o, *unit_ml = a.unit_ml, *cta_o = a.cta_o, *cta_ml = a.cta_ml;
+        if (skip > 0) {
+            const Group gr = a.group[i];
+            int head;
+            const int h = a.by_g.quot(hq, &head), x = (s - gr.first) * a.g + head;
+            const int block = x / QT, y = x - block * QT, unit = h * gr.blocks + block;
+            c0 = gr.cta + unit * gr.parts;
+            parts = gr.parts;
+            if (dealt.x == 0) {
+                const Deal deal(total, Deal::ctas(total, 1, dealt.y), 1);
+                const int nt = tiles_of(gr), t0 = a.tile_base[i] + unit * nt;
+                c0 = deal.cta_of(t0);
+                parts = deal.cta_of(t0 + nt - 1) - c0 + 1;
             }
-            continue;
-        }
-        const Group gr = a.group[i];
-        const int nt = (gr.rows + KT - 1) / KT, all = gr.members * a.g;
-        const int left = (int)(row - (long long)gr.first * heads_q), h = left / all, x = left - h * all;
-        const int block = x / QT, y = x - block * QT, queries = min(QT, all - block * QT), unit = h * gr.blocks + block;
-        int head;
-        const int member = a.by_g.quot(x, &head);
-        const size_t query = (size_t)(gr.first + member) * heads_q + h * a.g + head;
-        int c0 = gr.cta + unit * gr.parts, parts = gr.parts;
-        if (dealt.x == 0) {
-            const Deal deal(total, Deal::ctas(total, 1, dealt.y), 1);
-            const int t0 = a.tile_base[i] + unit * nt;
-            c0 = deal.cta_of(t0);
-            parts = deal.cta_of(t0 + nt - 1) - c0 + 1;
+            const Run r{gr.first, gr.members, gr.rows, h, block, 0, 0};
+            unit_ml += row_of(a, r) + y;
+            unit_o += row_of(a, r) * (D / 4) + channel * queries_of(a, r) + y;
+            cta_ml += (size_t)c0 * QT + y;
+            cta_o += ((size_t)c0 * (D / 4) + channel) * QT + y;
+        } else if (held > 0) {
+            continue;  // in no group: attended by itself
         }
         if (!waited) ptx::grid_dependency_wait();
         waited = true;
-        float4* out = reinterpret_cast<float4*>(a.out + query * D) + channel;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float m = -INFINITY, l = 0.f;
-        if (min(a.c.lens[gr.first + member], a.c.rows) > gr.rows) {  // it has rows of its own
+        if (min(held, a.c.rows) > skip) {  // it has rows of its own
             acc = *out;
-            m = a.own_lse2[query];
+            m = a.own_lse2[row];
             l = m == -INFINITY ? 0.f : 1.f;
         }
 #pragma unroll 1
@@ -920,30 +918,37 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
             float4 o[PARTS], ml[PARTS];
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                const int p = p0 + k;
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 ml[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                if (p < parts) {
-                    ml[k] = p ? a.cta_ml[(size_t)(c0 + p) * QT + y] : a.unit_ml[row];
-                    o[k] = p ? a.cta_o[((size_t)(c0 + p) * (D / 4) + channel) * QT + y]
-                             : a.unit_o[(row - y) * (D / 4) + channel * queries + y];
+                if (p0 + k < parts) {
+                    const bool first = k == 0 && p0 == 0;
+                    ml[k] = first ? *unit_ml : cta_ml[k * QT];
+                    o[k] = first ? *unit_o : cta_o[k * (D / 4) * QT];
                 }
             }
+            cta_ml += PARTS * QT;
+            cta_o += PARTS * (D / 4) * QT;
+            float grown = m;  // (either half of a part's rows has the same maximum)
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) grown = fmaxf(grown, ml[k].x);
+            if (grown == -INFINITY) continue;
+            const float u = ex2(m - grown);
+            m = grown;
+            l *= u;
+            acc = make_float4(acc.x * u, acc.y * u, acc.z * u, acc.w * u);
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                const float mp = ml[k].x;  // of either half of the rows
-                if (mp == -INFINITY) continue;
-                const float grown = fmaxf(m, mp), u = ex2(m - grown), v = ex2(mp - grown);
-                l = l * u + (ml[k].y + ml[k].w) * v;
-                acc.x = acc.x * u + o[k].x * v;
-                acc.y = acc.y * u + o[k].y * v;
-                acc.z = acc.z * u + o[k].z * v;
-                acc.w = acc.w * u + o[k].w * v;
-                m = grown;
+                const float v = ex2(ml[k].x - grown);
+                l += (ml[k].y + ml[k].w) * v;
+                acc.x += o[k].x * v;
+                acc.y += o[k].y * v;
+                acc.z += o[k].z * v;
+                acc.w += o[k].w * v;
             }
         }
         const float w = l == 0.f ? 0.f : 1.f / l;
         *out = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
-        if (a.lse && channel == 0) a.lse[query] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        if (a.lse && channel == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
     }
     // the kernel behind waits for this one, and this one for all before it
     if (!waited) ptx::grid_dependency_wait();
