@@ -79,14 +79,20 @@ bool encode_pool(CUtensorMap* m, const Cache& c, const void* base, const long lo
 // what ckv_paged_set_wait_limit has set
 void waits(long long* limit, int* stall);
 // bytes of the decode attention's workspace without weights, and where the lse
-// (base 2, [seqs][heads * g]) of its calls stands
-size_t attn_workspace(const Cache& c, int g, float** lse2, void* workspace);
+// (base 2, [seqs][heads * g]) and the parts of its calls stand
+size_t attn_workspace(const Cache& c, int g, float** lse2, float** part, void* workspace);
+// A partial result of g heads: unnormalised outputs [g][D], maxima [g] (base 2), sums [g].
+__host__ __device__ __forceinline__ size_t part_floats(int g) { return ((size_t)g * (D + 2) + 3) / 4 * 4; }
 // Decode attention over the rows of each sequence from skip[s] on (device int32,
 // multiples of TILE) by *ctas CTAs, bf16.  To follow, as a dependent launch, a kernel that has
 // waited for its own predecessor and that writes nothing this one reads; a
-// kernel behind it that waits for it has waited for both.
-cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int32_t* ctas, const void* q, const long long* q_stride, int g,
-                                 float qscale, float* out, float* lse, void* workspace, cudaStream_t s);
+// kernel behind it that waits for it has waited for both.  It finds the units of
+// up to JOINED_PARTS CTAs as their parts: CTA c's is part 2 c, 2 c + 1 where the
+// unit begins in it (left[unit] says which, above its use).
+constexpr int JOINED_PARTS = 8;
+cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int32_t* ctas, int32_t* left, const void* q,
+                                 const long long* q_stride, int g, float qscale, float* out, float* lse, void* workspace,
+                                 cudaStream_t s);
 
 // two arrays of n 32-bit elements that are one and the same (an element is read
 // before it is written) or do not overlap; no array overlaps nothing

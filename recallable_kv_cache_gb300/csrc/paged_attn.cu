@@ -55,6 +55,9 @@ constexpr int WARPS = 8, NST = 2;
 struct OwnRows : Cache {
     const int32_t* skip;
     const int32_t* ctas;  // how many CTAs of the grid work: the others' SMs are taken
+    // [seqs * heads] what the kernel behind finds of each unit with rows: n << 16 |
+    // c, parts of CTAs c .. c + n - 1; n = 0: the result, in out and lse2
+    int32_t* left;
 };
 __device__ __forceinline__ int working_ctas(const Cache&) { return gridDim.x; }
 __device__ __forceinline__ int working_ctas(const OwnRows& c) { return min((int)gridDim.x, max(1, *c.ctas)); }
@@ -90,7 +93,6 @@ using AttnArgs = AttnArgsOf<Cache>;
 
 // A partial: O [g][D], then the maxima [g], then the sums [g]; a multiple of
 // 16 bytes, as O is read and written 16 bytes at a time.
-__host__ __device__ __forceinline__ size_t part_floats(int g) { return ((size_t)g * (D + 2) + 3) / 4 * 4; }
 
 // ---------------------------------------------------------------- the deal
 template <int TR, typename C>
@@ -1037,6 +1039,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                         }
                     });
             if (lane == 0 && !whole) segs[2 * warp + tail] = Seg{u, nt, first};
+            if constexpr (OWN)
+                if (lane == 0 && whole) a.c.left[u] = 0;
         };
         int st = 0, parity = 0;
         // the first NST turns only ask for tiles
@@ -1127,10 +1131,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                     const bool began = sg.a >= cta_begin, whole = began && sg.a + sg.nt <= cta_end;
                     jobs[__popc(lead & below)] = Job{__popc(held & below), __popc(mine), whole ? sg.u : -1,
                                                      a.part + ((size_t)blockIdx.x * 2 + began) * pf};
+                    int c0 = 0, n = 0;
                     if (!whole) {
-                        const int c0 = deal.cta_of(sg.a);
-                        shared_units[began] = make_int4(sg.u, c0, deal.cta_of(sg.a + sg.nt - 1) - c0 + 1, 0);
+                        c0 = deal.cta_of(sg.a);
+                        n = deal.cta_of(sg.a + sg.nt - 1) - c0 + 1;
                     }
+                    if constexpr (OWN) {
+                        // a few parts are merged by the kernel behind, together with the others' rows
+                        const bool joined = n <= JOINED_PARTS;
+                        if (began) a.c.left[sg.u] = joined ? n << 16 | c0 : 0;
+                        if (joined) n = 0;
+                    }
+                    if (n) shared_units[began] = make_int4(sg.u, c0, n, 0);
                 }
                 if (lane == 0) n_jobs = __popc(lead);
             }
@@ -1340,18 +1352,21 @@ void waits(long long* limit, int* stall) {
     *stall = stall_switch.load(std::memory_order_relaxed);
 }
 
-size_t attn_workspace(const Cache& c, int g, float** lse2, void* workspace) {
+size_t attn_workspace(const Cache& c, int g, float** lse2, float** part, void* workspace) {
     const Layout l = layout_of(c, g, false);
     if (lse2) *lse2 = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + l.lse2);
+    if (part) *part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + l.part);
     return l.total;
 }
 
-cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int32_t* ctas, const void* q, const long long* q_stride, int g,
-                                 float qscale, float* out, float* lse, void* workspace, cudaStream_t s) {
+cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int32_t* ctas, int32_t* left, const void* q,
+                                 const long long* q_stride, int g, float qscale, float* out, float* lse, void* workspace,
+                                 cudaStream_t s) {
     AttnArgsOf<OwnRows> a = {};
     static_cast<Cache&>(a.c) = c;
     a.c.skip = skip;
     a.c.ctas = ctas;
+    a.c.left = left;
     const Layout l = layout_of(c, g, false);
     unsigned char* w = static_cast<unsigned char*>(workspace);
     a.q = q;

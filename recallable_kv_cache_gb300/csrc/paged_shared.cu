@@ -129,7 +129,11 @@ struct SharedArgs {
     Share* share;       // [grid]
     int2* deal;         // [1] CTAs with a unit's part, 0: the even deal; CTAs that it goes to
     int* own_ctas;      // [1] CTAs for the sequences' own rows
-    float* own_lse2;    // [seqs * heads * g] of the sequences' own rows, base 2
+    // the sequences' own rows: the lse (base 2) [seqs * heads * g], parts, and
+    // what there is of a unit [seqs * heads]
+    float* own_lse2;
+    const float* own_part;
+    int32_t* own_left;
     // Parts: O as [channel / 4][query of the block] of four, and for either half
     // of the tiles' rows (the maximum that O goes by, the sum).  The CTA in which
     // a unit begins leaves its part behind those of the units before it, the
@@ -862,12 +866,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ---------------------------------------------------------------- joining
-// What the sequences' own rows gave, in out and own_lse2, with the parts of the
-// units.  A block has four rows of the output, a thread four channels of one,
-// so that the g heads of a part come side by side; PARTS parts are under way at
-// a time (one after the other 20 parts took 12 us).  Its time is the latency of
-// its loads and of its instructions, which come from L2.
-constexpr int PARTS = 8;
+// The parts of the units, and what the sequences' own rows gave: results, or
+// parts of up to JOINED_PARTS CTAs (merged here and not by the last of these: 18.1
+// to 15.9 us for 8 sequences behind 512 rows, 83 to 82 for 160 behind 16k).  A
+// block has four rows of the output, a thread four channels of one, so that the g
+// heads of a part come side by side.  Its time is the latency of its loads and of
+// its instructions, which come from L2: PARTS parts are under way at a time (one
+// after the other 20 parts took 12 us; eight at a time 1 to 2 us more than six).
+constexpr int PARTS = 6;
 __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_constant__ SharedArgs a) {
     const int channel = threadIdx.x / JOIN_ROWS, heads_q = a.c.heads * a.g;  // four channels
     const long long n = (long long)a.c.seqs * heads_q, step = (long long)gridDim.x * JOIN_ROWS;
@@ -881,12 +887,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
         const int i = a.group_of[s], skip = a.skip[s], held = a.c.lens[s], total = a.tile_base[a.groups];
         const int2 dealt = *a.deal;
         float4* out = reinterpret_cast<float4*>(a.out + row * D) + channel;
-        int c0 = 0, parts = 0;
+        int head, c0 = 0, parts = 0;
+        const int h = a.by_g.quot(hq, &head);
         const float4 *unit_o = a.unit_o, *unit_ml = a.unit_ml, *cta_o = a.cta_o, *cta_ml = a.cta_ml;
         if (skip > 0) {
             const Group gr = a.group[i];
-            int head;
-            const int h = a.by_g.quot(hq, &head), x = (s - gr.first) * a.g + head;
+            const int x = (s - gr.first) * a.g + head;
             const int block = x / QT, y = x - block * QT, unit = h * gr.blocks + block;
             c0 = gr.cta + unit * gr.parts;
             parts = gr.parts;
@@ -901,18 +907,17 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
             unit_o += row_of(a, r) * (D / 4) + channel * queries_of(a, r) + y;
             cta_ml += (size_t)c0 * QT + y;
             cta_o += ((size_t)c0 * (D / 4) + channel) * QT + y;
-        } else if (held > 0) {
-            continue;  // in no group: attended by itself
         }
+        const bool own = min(held, a.c.rows) > skip;  // it has rows of its own
+        const int32_t* own_left = a.own_left + (size_t)s * a.c.heads + h;
         if (!waited) ptx::grid_dependency_wait();
         waited = true;
+        const int left = own ? *own_left : 0, own_parts = left >> 16;
+        if (skip == 0 && own && own_parts == 0) continue;  // in no group, and whole
+        const float own_m = own ? a.own_lse2[row] : -INFINITY;
+        const float4 own_o = own ? *out : make_float4(0.f, 0.f, 0.f, 0.f);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float m = -INFINITY, l = 0.f;
-        if (min(held, a.c.rows) > skip) {  // it has rows of its own
-            acc = *out;
-            m = a.own_lse2[row];
-            l = m == -INFINITY ? 0.f : 1.f;
-        }
 #pragma unroll 1
         for (int p0 = 0; p0 < parts; p0 += PARTS) {
             float4 o[PARTS], ml[PARTS];
@@ -931,15 +936,51 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
             float grown = m;  // (either half of a part's rows has the same maximum)
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) grown = fmaxf(grown, ml[k].x);
-            if (grown == -INFINITY) continue;
-            const float u = ex2(m - grown);
+            const float ms = grown == -INFINITY ? 0.f : grown;  // (all products NaN: the sum says so)
+            const float u = ex2(m - ms);
             m = grown;
             l *= u;
             acc = make_float4(acc.x * u, acc.y * u, acc.z * u, acc.w * u);
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                const float v = ex2(ml[k].x - grown);
+                const float v = ex2(ml[k].x - ms);
                 l += (ml[k].y + ml[k].w) * v;
+                acc.x += o[k].x * v;
+                acc.y += o[k].y * v;
+                acc.z += o[k].z * v;
+                acc.w += o[k].w * v;
+            }
+        }
+        constexpr int AT_A_TIME = 4;
+#pragma unroll 1
+        for (int p0 = 0; own && p0 < max(1, own_parts); p0 += AT_A_TIME) {
+            float4 o[AT_A_TIME];
+            float pm[AT_A_TIME], pl[AT_A_TIME];
+#pragma unroll
+            for (int k = 0; k < AT_A_TIME; ++k) {
+                const bool whole = k == 0 && own_parts == 0;
+                o[k] = whole ? own_o : make_float4(0.f, 0.f, 0.f, 0.f);
+                pm[k] = whole ? own_m : -INFINITY;
+                pl[k] = whole ? 1.f : 0.f;
+                if (p0 + k < own_parts) {
+                    const float* p = a.own_part + (size_t)(2 * ((left & 0xffff) + p0 + k) + (p0 + k == 0)) * part_floats(a.g);
+                    o[k] = *reinterpret_cast<const float4*>(p + head * D + 4 * channel);
+                    pm[k] = p[a.g * D + head];
+                    pl[k] = p[a.g * D + a.g + head];
+                }
+            }
+            float grown = m;
+#pragma unroll
+            for (int k = 0; k < AT_A_TIME; ++k) grown = fmaxf(grown, pm[k]);
+            const float ms = grown == -INFINITY ? 0.f : grown;  // (all products NaN: the sum says so)
+            const float u = ex2(m - ms);
+            m = grown;
+            l *= u;
+            acc = make_float4(acc.x * u, acc.y * u, acc.z * u, acc.w * u);
+#pragma unroll
+            for (int k = 0; k < AT_A_TIME; ++k) {
+                const float v = ex2(pm[k] - ms);
+                l += pl[k] * v;
                 acc.x += o[k].x * v;
                 acc.y += o[k].y * v;
                 acc.z += o[k].z * v;
@@ -956,21 +997,22 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
 
 // ---------------------------------------------------------------- host side
 struct Layout {
-    size_t attn, group, tile_base, skip, group_of, share, deal, own_ctas, unit_o, unit_ml, cta_o, cta_ml, total;
+    size_t attn, group, tile_base, skip, group_of, share, deal, own_ctas, own_left, unit_o, unit_ml, cta_o, cta_ml, total;
 };
 Layout layout_of(const Cache& c, int g) {
     Layout l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t S = c.seqs, queries = S * c.heads * g;
     l.attn = 0;
-    l.group = up(attn_workspace(c, g, nullptr, nullptr));
+    l.group = up(attn_workspace(c, g, nullptr, nullptr, nullptr));
     l.tile_base = l.group + up(S * sizeof(Group));
     l.skip = l.tile_base + up((S + 1) * sizeof(int));
     l.group_of = l.skip + up(S * sizeof(int));
     l.share = l.group_of + up(S * sizeof(int));
     l.deal = l.share + up(MAX_GRID * sizeof(Share));
     l.own_ctas = l.deal + up(sizeof(int2));
-    l.unit_o = l.own_ctas + up(sizeof(int));
+    l.own_left = l.own_ctas + up(sizeof(int));
+    l.unit_o = l.own_left + up(S * c.heads * sizeof(int32_t));
     l.unit_ml = l.unit_o + up(queries * D * sizeof(float));
     l.cta_o = l.unit_ml + up(queries * sizeof(float4));
     l.cta_ml = l.cta_o + (size_t)MAX_GRID * QT * D * sizeof(float);
@@ -1007,7 +1049,7 @@ cudaError_t launch_shared(SharedArgs& a, void* workspace, cudaStream_t s) {
     if (e == cudaSuccess) e = launch_dependent(paged_shared_kernel, dim3(a.grid), dim3(THREADS), smem, s, a, tk, tv);
     const long long qst[2] = {a.qst[0] / 2, a.qst[1] / 2};
     if (e == cudaSuccess)
-        e = launch_attn_own_rows(a.c, a.skip, a.own_ctas, a.q, qst, a.g, a.qscale, a.out, a.lse, workspace, s);
+        e = launch_attn_own_rows(a.c, a.skip, a.own_ctas, a.own_left, a.q, qst, a.g, a.qscale, a.out, a.lse, workspace, s);
     const long long queries = (long long)a.c.seqs * a.c.heads * a.g, blocks = (queries + JOIN_ROWS - 1) / JOIN_ROWS;
     if (e == cudaSuccess)
         e = launch_dependent(paged_shared_join, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(JOIN_THREADS), 0, s, a);
@@ -1072,7 +1114,10 @@ extern "C" ckv_status ckv_paged_shared_attn(const ckv_paged_cache* cache, const 
     a.tile_base = reinterpret_cast<int*>(w + l.tile_base);
     a.skip = reinterpret_cast<int32_t*>(w + l.skip);
     a.group_of = reinterpret_cast<int*>(w + l.group_of);
-    attn_workspace(a.c, g, &a.own_lse2, workspace);
+    float* own_part;
+    attn_workspace(a.c, g, &a.own_lse2, &own_part, workspace);
+    a.own_part = own_part;
+    a.own_left = reinterpret_cast<int32_t*>(w + l.own_left);
     a.share = reinterpret_cast<Share*>(w + l.share);
     a.deal = reinterpret_cast<int2*>(w + l.deal);
     a.own_ctas = reinterpret_cast<int*>(w + l.own_ctas);

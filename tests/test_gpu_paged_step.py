@@ -689,6 +689,31 @@ def test_shared_rows_of_the_type_s_largest_values():
     c.check()
 
 
+@pytest.mark.parametrize("row,own", [(3, [0, 0]), (3, [5, 40]), (70, [20, 40])])
+def test_shared_nan_in_a_held_row(row, own):
+    """What the decode attention makes of it, in the shared rows and in a sequence's own."""
+    c = Shared([(64, own)], 2, 4, 16)
+    for pool in (c.K, c.V):
+        pool[c.table[0, row // 16].long(), 1, row % 16, 7] = float("nan")
+        d = [torch.zeros_like(c.out), torch.zeros_like(c.lse)]
+        c.run()
+        c.handle.decode_attn(c.q, d[0], lse=d[1])
+        assert torch.equal(c.out.isnan(), d[0].isnan()) and torch.equal(c.lse.isnan(), d[1].isnan())
+        assert c.out.isnan().any()
+
+
+@pytest.mark.parametrize("own", [[40000, 3], [2000, 1999], [5000] * 3])
+def test_shared_long_own_rows(own):
+    """Own rows of more and of fewer blocks than the join takes."""
+    for heads, groups in ((1, [(64, own)]), (2, [(0, own), (0, [700])])):
+        c = Shared(groups, heads, 4, 16)
+        c.run()
+        c.check()
+        first = c.out.clone()
+        c.run()
+        assert torch.equal(c.out, first)
+
+
 def test_shared_captured_and_on_streams():
     """Two handles over the same tensors replayed side by side, lens growing between replays."""
     c = Shared([(512, [5, 30, 100])], 2, 4, 16, width=48)
