@@ -187,7 +187,10 @@ __device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigne
 // for a tile of shared rows, OWN_COST for 16 own rows of a KV head and UNIT_COST
 // for each (sequence, KV head) with some, and merging the latter takes
 // MERGE_COST longer at the end: the P SMs of the G there are for the shared rows
-// are those with which both end together, x / P = y / (G - P) + MERGE_COST.
+// are those with which both end together, x / P = y / (G - P) + MERGE_COST.  (Found
+// by trying over the cases that have both: a tile by itself takes 1.5, the rest is
+// a share of what comes before and after.  TILE_COST 1.5, 1.6 and 1.75, OWN_COST
+// .15 to .18, UNIT_COST .4 and MERGE_COST 3 to 10 were equal to 8 % slower.)
 //
 // The tiles of shared rows go to CTAs evenly, a CTA's share beginning and ending
 // anywhere, or every unit goes in equal parts to CTAs of its own.  Where a share
