@@ -38,7 +38,7 @@
 // O, and registers moved from the other roles to the softmax's (by a tenth, a
 // twentieth, 8 % and 4 % for 160 sequences behind 16k rows, which take 69 us).
 // Warp roles:
-//   warp 0       asks for the tiles (TMA)
+//   warps 0, 18  ask for the tiles of K and of V (TMA)
 //   warp 1       owns tensor memory, issues S and T
 //   warps 2-9    softmax, a thread 64 rows of a query
 //   warps 10-17  queries to shared memory; O, a thread 64 channels of a query
@@ -51,6 +51,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mma_sync.cuh"
 #include "paged.h"
@@ -71,7 +72,8 @@ constexpr int PANEL = 128 * 128;     // 64 channels of 128 rows
 constexpr int STAGE = 2 * PANEL;     // K or V of a tile
 constexpr int NST = 6;
 constexpr int SOFT_WARPS = 8, OUT_WARPS = 8;
-constexpr int THREADS = 32 * (2 + SOFT_WARPS + OUT_WARPS);
+constexpr int V_WARP = 2 + SOFT_WARPS + OUT_WARPS;
+constexpr int THREADS = 32 * (V_WARP + 1);
 constexpr int PREP_THREADS = 256;
 constexpr int JOIN_ROWS = 4;
 constexpr int JOIN_THREADS = JOIN_ROWS * D / 4;
@@ -425,7 +427,8 @@ __device__ __forceinline__ long long row_of(const SharedArgs& a, const Run& r) {
     return ((long long)r.first * a.c.heads + (long long)r.h * r.members) * a.g + (long long)r.block * QT;
 }
 
-// Places of a CTA's j-th K and V in the order of the loads: K0 K1 V0 K2 V1 ...
+// Places of a CTA's j-th K and V in the order in which the products take them:
+// K0 K1 V0 K2 V1 ...
 __device__ __forceinline__ int k_index(int j) { return j < 1 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int v_index(int j) { return 2 * j + 2; }
 
@@ -507,77 +510,71 @@ __global__ void __launch_bounds__(THREADS, 1)
     // leaves -inf what it is
     const float qs = fmaxf(fabsf(a.qscale), 1.17549435e-38f);
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        // In the order in which the products take them: K of a tile, then V of
-        // the tile before it.
+    // ---------------------------------------------------------------- producers
+    // One of K, one of V: each lane's copy takes its own time to ask for, so that
+    // one warp for both was late where pages are short (28 units of 2600 tiles:
+    // 61 us with 16 rows a page, now 49; 48 to 49.5 with 128).
+    auto produce = [&](auto of_v) {
+        constexpr bool values = decltype(of_v)::value;
+        const CUtensorMap* map = values ? &tv : &tk;
         const FastDiv& by_page = a.c.by_page;
-        // this lane's copy of a tile: its page (-1: none), slot and place in the
-        // stage; the tile's copies and rows, and its KV head
-        struct Copy {
-            int page, slot, place, copies, rows, h;
-        };
-        Copy now{}, last{};
-        auto load = [&](const Copy& c, int idx, const CUtensorMap* map) {
-            const int st = idx % NST;
-            if (idx >= NST && !__all_sync(FULL, wait(&bs->empty[st], (idx / NST - 1) & 1, bs, a))) return false;
+        Run r = share.run;
+        int k = r.k0, k_end = r.k0 + r.n;
+        // the first K and the queries before all else: with every stage asked for
+        // at once they came with the last of them, 4 us later
+        auto first = [&] { return __all_sync(FULL, wait(&bs->full[0], 0, bs, a) && wait(&bs->q_full, 0, bs, a)); };
+        if (values && n_tiles > 0) alive = first();
+        for (; j < n_tiles && alive; ++j) {
+            if (k == k_end) {
+                r = run_at(a, t_begin + j, t_end, &from, lane);
+                k = r.k0;
+                k_end = r.k0 + r.n;
+            }
+            // lane l looks after the tile's l-th copy: its page (-1: none), slot
+            // and place in the stage
+            const int row = k * KT + lane * a.box_rows;
+            int page = -1, slot = 0;
+            if (lane * a.box_rows < KT && row < r.rows) {
+                page = a.c.table[(size_t)r.first * a.c.max_pages + by_page.quot(row, &slot)];
+                if (page < 0 || page >= a.c.n_pages) {
+                    if (!values) report(a.c.dev_err, CKV_DEV_BAD_INDEX);
+                    page = -1;
+                }
+            }
+            // rows of bad pages are left out: the others move up
+            const unsigned good = __ballot_sync(FULL, page >= 0);
+            const int place = __popc(good & ((1u << lane) - 1u)), copies = __popc(good);
+            const int rows = copies * a.box_rows - __reduce_max_sync(FULL, page >= 0 ? max(0, row + a.box_rows - r.rows) : 0);
+            ++k;
+            const int idx = values ? v_index(j) : k_index(j), st = idx % NST;
+            alive = idx < NST || __all_sync(FULL, wait(&bs->empty[st], (idx / NST - 1) & 1, bs, a));
+            if (!alive) break;
             if (lane == 0) {
                 bs->asked[st] = idx / NST;
-                bs->rows[st] = c.rows;
-                if (c.copies) ptx::mbar_arrive_expect_tx(&bs->full[st], c.copies * a.box_rows * 256);
+                bs->rows[st] = rows;
+                if (copies) ptx::mbar_arrive_expect_tx(&bs->full[st], copies * a.box_rows * 256);
                 else ptx::mbar_arrive(&bs->full[st]);
             }
             __syncwarp();
-            if (c.page >= 0) {
-                unsigned char* to = sm.ring[st] + c.place * a.box_rows * 128;
+            if (page >= 0) {
+                unsigned char* to = sm.ring[st] + place * a.box_rows * 128;
 #pragma unroll
                 for (int piece = 0; piece < 2; ++piece)
                     asm volatile(
                         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                         "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(ptx::smem_u32(to + piece * PANEL)),
-                        "l"(map), "r"(0), "r"(c.slot), "r"(piece), "r"(c.h), "r"(c.page),
+                        "l"(map), "r"(0), "r"(slot), "r"(piece), "r"(r.h), "r"(page),
                         "r"(ptx::smem_u32(&bs->full[st]))
                         : "memory");
             }
             __syncwarp();
-            return true;
-        };
-        Run r = share.run;
-        int k = r.k0, k_end = r.k0 + r.n;
-        for (; j <= n_tiles && alive; ++j) {
-            last = now;
-            if (j < n_tiles) {
-                if (k == k_end) {
-                    r = run_at(a, t_begin + j, t_end, &from, lane);
-                    k = r.k0;
-                    k_end = r.k0 + r.n;
-                }
-                // lane l looks after the tile's l-th copy
-                const int row = k * KT + lane * a.box_rows;
-                now.page = -1;
-                now.h = r.h;
-                if (lane * a.box_rows < KT && row < r.rows) {
-                    now.page = a.c.table[(size_t)r.first * a.c.max_pages + by_page.quot(row, &now.slot)];
-                    if (now.page < 0 || now.page >= a.c.n_pages) {
-                        report(a.c.dev_err, CKV_DEV_BAD_INDEX);
-                        now.page = -1;
-                    }
-                }
-                // rows of bad pages are left out: the others move up
-                const unsigned good = __ballot_sync(FULL, now.page >= 0);
-                now.place = __popc(good & ((1u << lane) - 1u));
-                now.copies = __popc(good);
-                now.rows = now.copies * a.box_rows -
-                           __reduce_max_sync(FULL, now.page >= 0 ? max(0, row + a.box_rows - r.rows) : 0);
-                ++k;
-                alive = load(now, k_index(j), &tk);
-                // the first K and the queries before all else: with every stage
-                // asked for at once they came with the last of them, 4 us later
-                if (j == 0 && alive)
-                    alive = __all_sync(FULL, wait(&bs->full[0], 0, bs, a) && wait(&bs->q_full, 0, bs, a));
-            }
-            if (j > 0 && alive) alive = load(last, v_index(j - 1), &tv);
+            if (j == 0 && !values) alive = first();
         }
+    };
+    if (warp == 0) {
+        produce(std::integral_constant<bool, false>{});
+    } else if (warp == V_WARP) {
+        produce(std::integral_constant<bool, true>{});
     } else if (warp == 1) {
         // ------------------------------------------------------------ the products
         // The lanes keep step for the runs; one waits and issues.  S of the tile
