@@ -533,6 +533,30 @@ def paged_set_wait_limit(cycles: int = 2_000_000_000, stall: bool = False):
     _check(lib().ckv_paged_set_wait_limit(int(cycles), 1 if stall else 0), "ckv_paged_set_wait_limit")
 
 
+def _address(name, t, shape, dtype, device, contiguous=True):
+    """Address of a paged cache's tensor after the checks."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name} must be {'contiguous ' if contiguous else ''}{list(shape)}, got "
+                         f"{list(t.shape)} with strides {list(t.stride())}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return t.data_ptr()
+
+
+def _addresses(dtype, device):
+    """_address of contiguous tensors of one dtype and device, in one look where all
+    is well: the calls of a step have a dozen of them."""
+    index = device.index
+
+    def address(name, t, shape):
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+            return t.data_ptr()
+        return _address(name, t, shape, dtype, device)
+    return address
+
+
 class PagedCache:
     """A paged K/V cache over the caller's tensors (see the paged cache section
     of ckv.h): ``K``, ``V`` [n_pages, heads, page_size, 128] bf16 or float32, any
@@ -597,6 +621,7 @@ class PagedCache:
         self._select, self._apply = so.ckv_paged_evict_select, so.ckv_paged_evict_apply
         self._cuda, self._index = torch.cuda, self.device.index
         self._raw_stream, self._current = _raw_calls(torch)
+        self._ints, self._floats = _addresses(torch.int32, self.device), _addresses(torch.float32, self.device)
         self._stride_arrays = {}
         self._plan, self._append_rotated = so.ckv_paged_plan, so.ckv_paged_append_rotated
         self._shared_attn = so.ckv_paged_shared_attn
@@ -617,23 +642,7 @@ class PagedCache:
     def _tensor(self, name, t, shape, dtype, contiguous=True):
         """Address of t after the checks; None is passed on (the C call says
         which arguments it needs)."""
-        if t is None:
-            return None
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape or (contiguous and not t.is_contiguous()):
-            raise ValueError(f"{name} must be {'contiguous ' if contiguous else ''}{list(shape)}, got "
-                             f"{list(t.shape)} with strides {list(t.stride())}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        return t.data_ptr()
-
-    def _ints(self, name, t, shape):
-        """_tensor of contiguous int32, in one look where all is well: the calls
-        of a step have a dozen of them."""
-        if t.dtype is self._i32 and t.shape == shape and t.is_contiguous() and t.get_device() == self._index:
-            return t.data_ptr()
-        return self._tensor(name, t, shape, self._i32)
+        return None if t is None else _address(name, t, shape, dtype, self.device, contiguous)
 
     def _strides(self, t, n):
         """The first n strides of t as a C array (made once for equal strides)."""
@@ -793,8 +802,8 @@ class PagedCache:
             raise ValueError(f"q is on {q.device}, the cache on {self.device}")
         if prefix.dim() != 1:
             raise ValueError(f"prefix must be [groups], got {list(prefix.shape)}")
-        groups, ints, f32, tensor = prefix.shape[0], self._ints, self._f32, self._tensor
+        groups, ints, floats = prefix.shape[0], self._ints, self._floats
         self._call(self._shared_attn, stream, q.data_ptr(), self._code, self._strides(q, 2), self.g,
                    128 ** -0.5 if scale is None else scale, ints("group_starts", group_starts, (groups + 1,)),
-                   ints("prefix", prefix, (groups,)), groups, tensor("out", out, self._q_shape, f32),
-                   None if lse is None else tensor("lse", lse, self._lse_shape, f32), *self._workspace)
+                   ints("prefix", prefix, (groups,)), groups, floats("out", out, self._q_shape),
+                   None if lse is None else floats("lse", lse, self._lse_shape), *self._workspace)

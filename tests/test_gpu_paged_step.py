@@ -559,6 +559,7 @@ SHARED = [
     ([(5120, [9, 100])], 4, 1, 16, "bf16", "hpd"),
     ([(20000, [3, 700, 33])], 1, 7, 32, "bf16", "hpd"),
     ([(32 * (i % 5), [i % 4] * (1 + i % 3)) for i in range(90)], 2, 3, 32, "bf16", "hpd"),
+    ([(288, [5, 150, 0])], 2, 4, 144, "bf16", "hpd"), ([(768, [1, 2, 300])], 1, 8, 256, "bf16", "phd"),
     ([(64, [0, 1, 2, 0]), (160, [0] * 1100)], 1, 1, 16, "bf16", "hpd"),     # more sequences than fit the prep's shared memory
     ([(16 * (i % 4), [i % 2, 1]) for i in range(300)], 1, 2, 16, "bf16", "hpd"),  # more groups than it has threads
     ([(16, [1, 1])], 1, 1, 16, "f32", "hpd"),
