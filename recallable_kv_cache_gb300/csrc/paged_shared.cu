@@ -191,15 +191,15 @@ __device__ __forceinline__ int tiles_of(const Group& gr) { return (int)((unsigne
 // MERGE_COST longer at the end: the P SMs of the G there are for the shared rows
 // are those with which both end together, x / P = y / (G - P) + MERGE_COST.  (Found
 // by trying over the cases that have both: a tile by itself takes 1.5, the rest is
-// a share of what comes before and after.  TILE_COST 1.5, 1.6 and 1.75, OWN_COST
-// .15 to .18, UNIT_COST .4 and MERGE_COST 3 to 10 were equal to 8 % slower.)
+// a share of what comes before and after.  TILE_COST 1.5 and 1.7, OWN_COST .15 to
+// .18, UNIT_COST .1 and .4, MERGE_COST 3 to 10 were equal to 8 % slower.)
 //
 // The tiles of shared rows go to CTAs evenly, a CTA's share beginning and ending
 // anywhere, or every unit goes in equal parts to CTAs of its own.  Where a share
 // passes from one unit to the next the products wait for the new queries and the
 // softmax for the products, as long as some three tiles, so the second deal is
 // taken where its largest part is at most OWN_EXTRA tiles above an even share.
-constexpr float TILE_COST = 1.7f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 6.f;  // us
+constexpr float TILE_COST = 1.6f, OWN_COST = 0.13f, UNIT_COST = 0.2f, MERGE_COST = 6.f;  // us
 constexpr int OWN_EXTRA = 3;
 // The SMs for the shared rows, of `grid`: `total` tiles of these, and of the own
 // rows `own` tiles of 16 of `units` (sequence, KV head) pairs.
