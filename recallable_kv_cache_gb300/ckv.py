@@ -388,6 +388,18 @@ def _raw_calls(torch):
             getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
 
 
+_TORCH = None
+
+
+def _torch():
+    """(torch, int32, int64, float32, *_raw_calls), looked up once."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = (torch, torch.int32, torch.int64, torch.float32, *_raw_calls(torch))
+    return _TORCH
+
+
 def rotary_turns(frequencies):
     """The pairs' angular frequencies (radians per position, floats) as the 64-bit
     fractions of a turn that the rotary calls take: int64 [rot / 2], on the CPU,
@@ -447,17 +459,17 @@ _STRIDES = {}  # stride arrays, made once for equal strides
 
 def _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device):
     """ckv_rotary of a call, as bytes, after the checks."""
-    import torch
+    _, _, i64, f32, _, _ = _torch()
     rot = at = 0
     if turns is not None:
-        if turns.dtype is not torch.int64:
+        if turns.dtype is not i64:
             raise TypeError(f"turns must be int64 (see rotary_turns), got {turns.dtype}")
         if turns.dim() != 1 or not turns.is_contiguous() or turns.device != device:
             raise ValueError(f"turns must be contiguous [rot / 2] on {device}, got {list(turns.shape)} on {turns.device}")
         rot, at = 2 * turns.shape[0], turns.data_ptr()
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            if w.dtype is not torch.float32:
+            if w.dtype is not f32:
                 raise TypeError(f"{name} must be float32, got {w.dtype}")
             if w.shape != (128,) or not w.is_contiguous() or w.device != device:
                 raise ValueError(f"{name} must be contiguous [128] on {device}, got {list(w.shape)} on {w.device}")
@@ -491,14 +503,14 @@ def rotate(q, k, positions, turns, q_out, k_out, interleaved: bool = False, q_we
     may be q and k (see ckv_rotate).  positions [tokens] int32; turns [rot / 2]
     int64 (see rotary_turns), or None for norms alone; either of q and k may be
     None, with its output."""
-    import torch
+    torch, i32, _, _, raw_stream, current = _torch()
     x = k if q is None else q
     if x is None or x.dim() != 3:
         raise ValueError("q or k must be given, as [tokens, heads, 128]")
-    tokens, device, code = x.shape[0], x.device, _dtype_code(x)
-    if device.type != "cuda":
+    tokens, device, dtype, code = x.shape[0], x.device, x.dtype, _dtype_code(x)
+    if not x.is_cuda:
         raise ValueError(f"the rows must be on a CUDA device, got {device}")
-    if positions.dtype is not torch.int32:
+    if positions.dtype is not i32:
         raise TypeError(f"positions must be int32, got {positions.dtype}")
     if positions.shape != (tokens,) or not positions.is_contiguous() or positions.device != device:
         raise ValueError(f"positions must be contiguous [{tokens}] on {device}, got {list(positions.shape)} on "
@@ -511,18 +523,17 @@ def rotate(q, k, positions, turns, q_out, k_out, interleaved: bool = False, q_we
             args += (None, None, None, None, 0)
         else:
             heads = t.shape[1] if t.dim() == 3 else 0
-            args += _heads(name, t, tokens, heads, x.dtype, device)
-            args += _heads(name + "_out", o, tokens, heads, x.dtype, device)
+            args += _heads(name, t, tokens, heads, dtype, device)
+            args += _heads(name + "_out", o, tokens, heads, dtype, device)
             args.append(heads)
     rotary = _rotary(turns, q_weight, k_weight, eps, amplitude, interleaved, device)
-    raw_stream, current = _raw_calls(torch)
-    index = device.index
+    index, fn = device.index, lib().ckv_rotate
     stream = raw_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
     if index == current():
-        status = lib().ckv_rotate(rotary, *args, positions.data_ptr(), tokens, 128, code, stream)
+        status = fn(rotary, *args, positions.data_ptr(), tokens, 128, code, stream)
     else:
         with torch.cuda.device(index):
-            status = lib().ckv_rotate(rotary, *args, positions.data_ptr(), tokens, 128, code, stream)
+            status = fn(rotary, *args, positions.data_ptr(), tokens, 128, code, stream)
     if status:
         raise CKVError(status, "ckv_rotate")
 
@@ -620,7 +631,7 @@ class PagedCache:
         self._append, self._attn = so.ckv_paged_append, so.ckv_paged_decode_attn
         self._select, self._apply = so.ckv_paged_evict_select, so.ckv_paged_evict_apply
         self._cuda, self._index = torch.cuda, self.device.index
-        self._raw_stream, self._current = _raw_calls(torch)
+        self._raw_stream, self._current = _torch()[4:]
         self._ints, self._floats = _addresses(torch.int32, self.device), _addresses(torch.float32, self.device)
         self._stride_arrays = {}
         self._plan, self._append_rotated = so.ckv_paged_plan, so.ckv_paged_append_rotated
