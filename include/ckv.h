@@ -488,8 +488,8 @@ ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, i
  * a server otherwise works out on the host between two steps.  Sequence s holds
  * held_in[s] pages (table[s][0 .. held_in[s])), has start[s] rows (lens[s] when
  * start is NULL), brings counts[s] tokens and has seen first[s] (seen[s] when
- * first is NULL; start[s] without seen).  Its first shared[s] <= held_in[s] pages (0
- * when shared is NULL) belong to somebody else, such as a prefix that several
+ * first is NULL; start[s] without seen).  Its first shared[s] <= held_in[s] pages
+ * (0 when shared is NULL) belong to somebody else, such as a prefix that several
  * sequences attend, and are never handed back.  With
  *   need[s] = max(shared[s], ceil((start[s] + counts[s]) / page_size))
  * a sequence takes need - held_in pages or hands held_in - need back (after an
@@ -514,11 +514,12 @@ ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, i
  * position 2^31 - 1, whose tokens do not fit n_slots (one without tokens always
  * does), or with shared or held_in outside 0 <= shared <= held_in <= max_pages,
  * is granted nothing and left as it is (CKV_DEV_BAD_COUNT; a negative count is no
- * token in starts, which never pass n_slots).  A span outside the ring counts as empty (head 0, count 0) and
- * pages handed back to a full ring are lost, CKV_DEV_BAD_COUNT both.  A bad
- * page id gives no slot (CKV_DEV_BAD_INDEX).  The call writes the cache's table,
- * lens and seen; K and V are not touched.  counts, start and first may be lens
- * or seen themselves, held_out may be held_in and span_out span_in.  free_pages must not overlap anything else.
+ * token in starts, which never pass n_slots).  A span outside the ring counts as
+ * empty (head 0, count 0) and pages handed back to a full ring are lost,
+ * CKV_DEV_BAD_COUNT both.  A bad page id gives no slot (CKV_DEV_BAD_INDEX).  The
+ * call writes the cache's table, lens and seen; K and V are not touched.
+ * counts, start and first may be lens or seen themselves, held_out may be held_in
+ * and span_out span_in.  free_pages must not overlap anything else.
  * Errors: as above; CKV_ERR_ARG (a null pointer other than start, first and
  * shared; n_slots or free_cap < 1; n_pages * page_size above 2^31 - 1; arrays
  * that overlap without being the same as above). */
