@@ -741,6 +741,50 @@ def test_shared_captured_and_on_streams():
             x.lens.copy_(ints(x.lens_list))
 
 
+@pytest.mark.parametrize("how", ["argument", "current"])
+def test_shared_handle_dropped_with_work_queued_on_another_stream(how):
+    """Its workspace is not handed out while a side stream has yet to use it."""
+    c = Shared([(4096, [5, 300, 100])], 2, 4, 16)
+    c.run()
+    out, starts, prefix = torch.zeros_like(c.out), ints(c.starts), ints(c.prefix)
+    handle, side = c.make(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    at, nbytes = handle.workspace.data_ptr(), handle.workspace.numel()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)  # some 0.2 s
+        if how == "current":
+            handle.shared_attn(c.q, out, starts, prefix)
+    if how == "argument":
+        handle.shared_attn(c.q, out, starts, prefix, stream=side)
+    del handle
+    others = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not side.query()
+    for t in others:
+        assert not t.data_ptr() <= at < t.data_ptr() + nbytes
+        t.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(out, c.out)
+    c.check()
+
+
+def test_shared_after_a_call_with_weights():
+    """One workspace for calls of both kinds, in any order."""
+    c = Shared([(64, [0, 5, 30]), (0, [100])], 2, 4, 16)
+    mass = torch.zeros(c.S, 2, c.table.shape[1] * 16, device="cuda")
+    pos, seen = torch.zeros_like(mass, dtype=torch.int32), c.lens.clone()
+    handle = ckv.PagedCache(c.K, c.V, c.table, c.lens, g=4, mass=mass, pos=pos, seen=seen, dev_err=c.err, shared=True)
+    plain = torch.zeros_like(c.out)
+    for _ in range(3):
+        c.out.fill_(math.nan)
+        handle.shared_attn(c.q, c.out, ints(c.starts), ints(c.prefix), lse=c.lse)
+        c.check()
+        handle.decode_attn(c.q, plain, mass_in=mass, mass_out=mass)
+        assert float((plain - c.out).norm()) <= 1e-5 * float(plain.norm())
+    total = mass.sum(dim=-1)
+    assert torch.allclose(total, torch.full_like(total, 12.0), rtol=1e-4)
+    assert int(c.err) == 0
+
+
 def test_shared_wait_that_runs_out():
     """Failure detection: the wait is made to run out by the switch, the next call is right."""
     c = Shared([(512, [5, 30])], 2, 4, 16)
