@@ -30,13 +30,14 @@
 // accumulates and O grows over hundreds of tiles; that also leaves O's scaling
 // off the path from one tile's maximum to the next one's product.
 // What bounds a long run of tiles is the way of a tile through the roles below,
-// about 1.5 us (32 sequences behind 64k rows, 8 heads of 4 queries: 59 us, 4.5
+// about 1.5 us (32 sequences behind 64k rows, 8 heads of 4 queries: 61 us, 4.4
 // TB/s of their 268 MB): scores, some 2500 cycles of softmax, products and the
 // steps between them come to 6000 for each of the two buffers that tensor memory
 // has room for.  Slower were two groups of softmax warps that each took every
-// other tile, T in two halves of 64 channels, sixteen warps for both softmax and
-// O, and registers moved from the other roles to the softmax's (by a tenth, a
-// twentieth, 8 % and 4 % for 160 sequences behind 16k rows, which take 69 us).
+// other tile, T in two halves of 64 channels, T begun with half of the rows while
+// the softmax is at the others, sixteen warps for both softmax and O, and
+// registers moved from the other roles to the softmax's (by 3 to 9 % for 160
+// sequences behind 16k rows, which take 71 us).
 // Warp roles:
 //   warps 0, 18  ask for the tiles of K and of V (TMA)
 //   warp 1       owns tensor memory, issues S and T
