@@ -595,7 +595,9 @@ ckv_status ckv_paged_shared_workspace(const ckv_paged_cache* cache, int32_t g, i
  * other members need at least as many (a shorter one attends the common rows
  * all the same, CKV_DEV_BAD_COUNT).  A start outside [0, seqs] or below an
  * earlier one is taken as the nearest that is not, a negative prefix as 0
- * (CKV_DEV_BAD_COUNT).  fp32 caches are attended sequence by sequence.
+ * (CKV_DEV_BAD_COUNT).  The rows of fp32 caches are attended sequence by
+ * sequence, each reading the common ones by itself through its own table;
+ * groups count, and are reported, as with bf16.
  * Arguments, accuracy, workspace (zeroed before its first use, one each for
  * calls that may overlap) and errors as for ckv_paged_decode_attn; CKV_ERR_ARG also
  * for groups < 0, or above 0 without group_starts and prefix, or above seqs. */

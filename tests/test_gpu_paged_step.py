@@ -648,6 +648,34 @@ def test_shared_member_shorter_than_the_prefix():
     assert int(c.err) == 3
 
 
+@pytest.mark.parametrize("starts,prefix,clean", [
+    ([-3, 4], [64], None), ([0, 9], [64], None), ([2, 0, 4], [64, 64], None), ([0, 3, 1, 4], [64, 64, 64], None),
+    ([0, 4], [-5], None), ([0, 4], [64], [64, 69, 94, 64]), ([0, 3, 4], [70, 64], [64, 69, 94, 0]),
+])
+def test_shared_fp32_groups_are_looked_at(starts, prefix, clean):
+    """Bad starts and prefixes are reported, and a member shorter than the prefix attends all of it,
+    as with bf16 (clean: the rows that count once the last member's are set to none)."""
+    c = Shared([(64, [0, 5, 30, 100])], 2, 4, 16, "f32")
+    if clean:
+        c.lens[3], c.lens_list = 0, clean
+    c.run(starts, prefix)
+    c.check()
+    assert int(c.err) == (3 if clean is None or clean[3] else 0)
+
+
+@pytest.mark.parametrize("short", [1, 1099])
+def test_shared_fp32_shorter_member_of_many(short):
+    """More sequences and groups than the look at few of them holds."""
+    c = Shared([(32, [1, 0])] * 40 + [(160, [i % 3 for i in range(1100)])], 1, 2, 16, "f32")
+    c.run()
+    c.check()
+    assert int(c.err) == 0
+    c.lens[80 + short], c.lens_list[80 + short] = 33, 160
+    c.run()
+    c.check()
+    assert int(c.err) == 3
+
+
 @pytest.mark.parametrize("page", [16, 48, 128])
 def test_shared_bad_pages_are_skipped(page):
     """Bad ids in the prefix and in a sequence's own pages; a whole tile of them."""
