@@ -441,6 +441,7 @@ __device__ __forceinline__ int v_index(int j) { return 2 * j + 2; }
 struct __align__(8) Bars {
     uint64_t full[NST], empty[NST];
     uint64_t q_full;
+    uint64_t started;                // the first K and the queries are there, and K's producer has seen it
     uint64_t s_full[NSP], p_full[NSP], top_empty[NSP];
     uint64_t top_full[4];            // of a quarter of the queries
     uint64_t t_full, t_empty;
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bs->asked[i] = -1;
         }
         ptx::mbar_init(&bs->q_full, OUT_WARPS);
+        ptx::mbar_init(&bs->started, 1);
         for (int i = 0; i < NSP; ++i) {
             ptx::mbar_init(&bs->s_full[i], 2);  // the product, and the thread that says of how many rows
             ptx::mbar_init(&bs->p_full[i], SOFT_WARPS);
@@ -526,10 +528,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const FastDiv& by_page = a.c.by_page;
         Run r = share.run;
         int k = r.k0, k_end = r.k0 + r.n;
-        // the first K and the queries before all else: with every stage asked for
-        // at once they came with the last of them, 4 us later
-        auto first = [&] { return __all_sync(FULL, wait(&bs->full[0], 0, bs, a) && wait(&bs->q_full, 0, bs, a)); };
-        if (values && n_tiles > 0) alive = first();
+        // The first K and the queries before all else: with every stage asked for
+        // at once they came with the last of them, 4 us later.  K's producer looks
+        // at them, and V's waits for that: without the first V nothing goes on, so
+        // neither barrier can be a phase further when it looks (a first run of one
+        // tile brings the next queries, and V goes ahead into the first K's stage).
+        if (values && n_tiles > 0) alive = __all_sync(FULL, wait(&bs->started, 0, bs, a));
         for (; j < n_tiles && alive; ++j) {
             if (k == k_end) {
                 r = run_at(a, t_begin + j, t_end, &from, lane);
@@ -574,7 +578,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         : "memory");
             }
             __syncwarp();
-            if (j == 0 && !values) alive = first();
+            if (j == 0 && !values) {
+                alive = __all_sync(FULL, wait(&bs->full[0], 0, bs, a) && wait(&bs->q_full, 0, bs, a));
+                if (alive && lane == 0) ptx::mbar_arrive(&bs->started);
+            }
         }
     };
     if (warp == 0) {

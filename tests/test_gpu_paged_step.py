@@ -701,6 +701,18 @@ def test_shared_equals_itself():
         assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
 
 
+def test_shared_first_runs_of_one_tile():
+    """Units of two tiles dealt out three to a block: every other block begins with the last tile of one."""
+    c = Shared([(256, [0, 0])] * 57, 4, 4, 16)
+    c.run()
+    c.check()
+    first = c.out.clone()
+    for _ in range(300):
+        c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first) and int(c.err) == 0
+
+
 def test_shared_exactness():
     """The error of fp32 weights, over a long prefix: the decode attention's."""
     c = Shared([(32768, [3, 100])], 2, 4, 64)
