@@ -554,10 +554,13 @@ typedef struct {
  * in ckv_paged_append; of outputs, at least d where the extent is above one).
  * positions [tokens] int32, any value.  heads_q or heads_k may be 0 (its
  * pointers are then not used).  q_out may be q itself and k_out k, with the
- * same strides; outputs must not overlap an input otherwise.
+ * same strides.  Rows that are written must not overlap one another or anything
+ * read otherwise; rows of one tensor that lie between each other, such as a
+ * projection's queries and keys, do not.
  * Errors: CKV_ERR_ARG (d != 128, tokens < 1, a negative head count or none at
  * all, rot, eps < 0 or not finite, amplitude not finite, interleaved not 0 or 1,
- * null pointers, strides, more than 2^31 - 2^16 rows), CKV_ERR_DTYPE,
+ * null pointers, strides, more than 2^31 - 2^16 rows, rows that overlap or are
+ * strewn through one another in more than 2^16 ways), CKV_ERR_DTYPE,
  * CKV_ERR_ALIGN. */
 ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const int64_t* q_stride, void* q_out,
                       const int64_t* q_out_stride, int32_t heads_q, const void* k, const int64_t* k_stride,
@@ -571,8 +574,9 @@ ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const int64_t* q_
  * queries).  A token with slot -1 is left out, its q_out too.  A slot outside
  * the pools, or (where the cache has pos or mass) s or row outside the cache,
  * leaves the token out as well (CKV_DEV_BAD_INDEX).  No two tokens may have the
- * same slot.  lens, seen and the table are not used: the plan has set them.
- * Errors: as above; CKV_ERR_ARG (g < 0, n_pages * page_size above 2^31 - 1). */
+ * same slot, and no slot may be one that the call reads.  lens, seen and the
+ * table are not used: the plan has set them.
+ * Errors: as above (of overlaps, q_out's); CKV_ERR_ARG (g < 0, n_pages * page_size above 2^31 - 1). */
 ckv_status ckv_paged_append_rotated(const ckv_paged_cache* cache, const ckv_rotary* rotary, const void* q,
                                     const int64_t* q_stride, int32_t g, void* q_out, const int64_t* q_out_stride,
                                     const void* k, const int64_t* k_stride, const void* v, const int64_t* v_stride,

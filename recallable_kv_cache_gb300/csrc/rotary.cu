@@ -261,6 +261,85 @@ ckv_status operand(const int64_t* st, int tokens, int heads, int elem, bool outp
     return ((out[0] | out[1]) & 15) ? CKV_ERR_ALIGN : CKV_OK;
 }
 
+// Rows of `width` bytes, n[0] tokens by n[1] heads, at byte strides st (where an
+// extent is one its stride is 0, and the other way round).
+struct Rows {
+    const unsigned char* p;
+    long long st[2];
+    int n[2];
+    long long width;
+};
+using Wide = __int128;  // extents times strides, whatever the arguments are
+Rows rows_of(const void* p, const long long* st, int tokens, int heads, int elem) {
+    return Rows{static_cast<const unsigned char*>(p), {st[0], st[1]}, {st[0] ? tokens : 1, st[1] ? heads : 1}, (long long)D * elem};
+}
+Rows array_of(const void* p, long long bytes) { return Rows{static_cast<const unsigned char*>(p), {0, 0}, {1, 1}, bytes}; }
+// bytes from the first row along dimension i to the end of the last
+Wide span(const Rows& r, int i) { return (Wide)(r.n[i] - 1) * r.st[i] + r.width; }
+// whether some k in [lo, hi] has x - before < k step < x + behind
+bool multiple_near(Wide x, Wide before, Wide behind, long long step, long long lo, long long hi) {
+    if (step == 0) return x < before && -x < behind;
+    const Wide from = x - before;
+    Wide k = from / step - (from % step < 0) + 1;  // the first above x - before
+    if (k < lo) k = lo;
+    return k <= hi && k * step < x + behind;
+}
+// whether two of the rows overlap
+bool rows_overlap(const Rows& r) {
+    const int a = r.n[0] <= r.n[1] ? 0 : 1, b = 1 - a;
+    const int inner = r.st[0] <= r.st[1] ? 0 : 1;
+    if (r.n[1 - inner] == 1 || r.st[1 - inner] >= span(r, inner)) return r.n[inner] > 1 && r.st[inner] < r.width;
+    if ((r.n[0] > 1 && r.st[0] < r.width) || (r.n[1] > 1 && r.st[1] < r.width)) return true;
+    for (int i = 1; i < r.n[a]; ++i)
+        if (multiple_near((Wide)i * r.st[a], r.width, r.width, r.st[b], 0, r.n[b] - 1)) return true;
+    return false;
+}
+// Whether a row of x overlaps a row of y.  Rows side by side in one tensor are
+// found apart by the first tests; what these leave is tried row by row, and taken
+// to overlap where that would be long.
+bool rows_meet(const Rows& x, const Rows& y) {
+    const Wide apart = (Wide)(reinterpret_cast<uintptr_t>(y.p)) - (Wide)(reinterpret_cast<uintptr_t>(x.p));
+    if (apart >= span(x, 0) + span(x, 1) - x.width || -apart >= span(y, 0) + span(y, 1) - y.width) return false;
+    for (int i = 0; i < 2; ++i) {
+        const long long step = x.st[i];
+        if (step == 0 || step != y.st[i]) continue;
+        // places modulo the step, which a stride of several steps does not change
+        const Wide at = apart % step + (apart % step < 0 ? step : 0);
+        const Wide long_x = x.st[1 - i] % step ? span(x, 1 - i) : x.width, long_y = y.st[1 - i] % step ? span(y, 1 - i) : y.width;
+        if (at >= long_x && at + long_y <= step) return false;
+    }
+    // Numbers of a dimension come in by their difference where the strides are one,
+    // else y's are gone through: heads h - g, then g, then tokens t - u, then u.
+    auto one = [&](int i) { return x.n[i] == 1 || y.n[i] == 1 || x.st[i] == y.st[i]; };
+    auto step = [&](int i) { return x.n[i] == 1 ? y.st[i] : x.st[i]; };
+    auto least = [&](int i) { return one(i) ? 1 - (long long)y.n[i] : 0; };
+    const int us = one(0) ? 1 : y.n[0], gs = one(1) ? 1 : y.n[1];
+    if ((Wide)(x.n[1] - least(1)) * gs * us > 1 << 16) return true;
+    for (int u = 0; u < us; ++u)
+        for (int g = 0; g < gs; ++g)
+            for (long long h = least(1); h < x.n[1]; ++h)
+                if (multiple_near(apart + (Wide)u * y.st[0] + (Wide)g * y.st[1] - (Wide)h * step(1), x.width, y.width, step(0),
+                                  least(0), x.n[0] - 1))
+                    return true;
+    return false;
+}
+// Whether outputs (out[i] is of the rows in[i], which it may be itself) overlap
+// themselves, one another, another input or what the call reads besides.
+template <int N, int M, int L>
+bool outputs_overlap(const Rows (&out)[N], const Rows (&in)[M], const Rows (&read)[L]) {
+    for (int i = 0; i < N; ++i) {
+        if (!out[i].p) continue;
+        if (rows_overlap(out[i])) return true;
+        for (int j = 0; j < i; ++j)
+            if (out[j].p && rows_meet(out[i], out[j])) return true;
+        for (int j = 0; j < M; ++j)
+            if (in[j].p && !(i == j && out[i].p == in[j].p) && rows_meet(out[i], in[j])) return true;
+        for (int j = 0; j < L; ++j)
+            if (read[j].p && rows_meet(out[i], read[j])) return true;
+    }
+    return false;
+}
+
 template <typename T, bool PAGED>
 cudaError_t launch(RotArgs& a, cudaStream_t s) {
     int dev = 0;
@@ -331,6 +410,15 @@ extern "C" ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const 
         a.src[i] = static_cast<const unsigned char*>(src[i]);
         a.dst[i] = static_cast<unsigned char*>(dst[i]);
     }
+    Rows out[2] = {}, in[2] = {};
+    for (int i = 0; i < 2; ++i) {
+        if (a.rows[i] == 0) continue;
+        out[i] = rows_of(dst[i], a.dst_st[i], tokens, a.rows[i], elem);
+        in[i] = rows_of(src[i], a.sst[i], tokens, a.rows[i], elem);
+    }
+    const Rows read[4] = {array_of(positions, 4LL * tokens), array_of(rotary->turns, 4LL * rotary->rot),
+                          array_of(rotary->q_weight, 4 * D), array_of(rotary->k_weight, 4 * D)};
+    if (outputs_overlap(out, in, read)) return CKV_ERR_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     const cudaError_t e = elem == 2 ? launch<__nv_bfloat16, false>(a, s) : launch<float, false>(a, s);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;
@@ -372,6 +460,14 @@ extern "C" ckv_status ckv_paged_append_rotated(const ckv_paged_cache* cache, con
     if (st != CKV_OK) return st;
     if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return CKV_ERR_ALIGN;
     a.slots = reinterpret_cast<const int4*>(slots);
+    if (g > 0) {
+        const Rows out[1] = {rows_of(q_out, a.dst_st[0], tokens, a.rows[0], elem)};
+        const Rows in[3] = {rows_of(q, a.sst[0], tokens, a.rows[0], elem), rows_of(k, a.sst[1], tokens, a.rows[1], elem),
+                            rows_of(v, a.sst[2], tokens, a.rows[2], elem)};
+        const Rows read[4] = {array_of(slots, 16LL * tokens), array_of(rotary->turns, 4LL * rotary->rot),
+                              array_of(rotary->q_weight, 4 * D), array_of(rotary->k_weight, 4 * D)};
+        if (outputs_overlap(out, in, read)) return CKV_ERR_ARG;
+    }
     cudaStream_t s = (cudaStream_t)stream;
     const cudaError_t e = elem == 2 ? launch<__nv_bfloat16, true>(a, s) : launch<float, true>(a, s);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;

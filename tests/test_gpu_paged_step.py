@@ -341,6 +341,28 @@ def test_rotate_strided(dtype, interleaved):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rotate_rows_between_each_other(dtype):
+    """Outputs between the rows that are read, in one tensor: heads, tokens and projections interleaved."""
+    gen = torch.Generator().manual_seed(6)
+    turns = ckv.rotary_turns(ckv.rotary_frequencies(128)[0]).cuda()
+    positions = torch.randint(0, 10 ** 6, (19,), generator=gen, dtype=torch.int32)
+    for shape, cut in (((19, 5, 2, D), lambda x: (x[:, :, 0], x[:, :, 1])), ((19, 2, 5, D), lambda x: (x[:, 0], x[:, 1])),
+                       ((5, 19, 2, D), lambda x: (x[:, :, 0].transpose(0, 1), x[:, :, 1].transpose(0, 1))),
+                       ((19, 15, D), lambda x: (x[:, :10:2], x[:, 1:10:2])), ((19, 15, D), lambda x: (x[:, ::3], x[:, 1::3]))):
+        x = torch.randn(*shape, generator=gen).to(DT[dtype]).cuda()
+        q, o = cut(x)
+        before, rows = x.clone(), q.clone()
+        ckv.rotate(q, None, positions.cuda(), turns, o, None)
+        check_rows(o, rows, positions.tolist(), turns, 128, False, None, 0, 1.0, dtype)
+        changed = before != x
+        cut(changed)[1].fill_(False)
+        assert not changed.any()
+    for q, o in ((x[:, :5], x[:, 1:6]), (x[:, :5], x[:, 4:9]), (x[:, :5], x[:, 5:10].flip(0)[:1].expand(19, 5, D))):
+        with pytest.raises(ckv.CKVError):
+            ckv.rotate(q, None, positions.cuda(), turns, o, None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rotate_values(dtype):
     """Zero rows, tiny ones, infinities and NaN: what the formula says, row by row."""
     x = torch.ones(6, 1, D)

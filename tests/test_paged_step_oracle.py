@@ -254,6 +254,72 @@ def test_bad_appends_are_refused(lib, bad, code):
     assert append(lib, apart(), rot(), **bad) == code
 
 
+FAR = dict(q=P, k=P + STEP, q_out=P + 2 * STEP, k_out=P + 3 * STEP, positions=P + 4 * STEP)
+ROW = 256  # bytes of a bf16 row
+
+
+@pytest.mark.parametrize("bad", [
+    # rows of an output on one another: equal strides, a token's rows into the next one's, a lattice that meets
+    dict(q_out_stride=i64(128, 128)), dict(k_out_stride=i64(256, 128)), dict(q_out_stride=i64(128, 256)),
+    dict(q_out_stride=i64(384, 256)), dict(q_out_stride=i64(1000, 128)), dict(q_out_stride=i64(128, 632)),
+    # one output on the other, or on an input in part or of the other kind
+    dict(k_out=P + 2 * STEP), dict(k_out=P + 2 * STEP + 7 * ROW), dict(q_out=P + 16), dict(q_out=P - 16), dict(q_out=P + ROW),
+    dict(q_out=P + STEP), dict(k_out=P + STEP + 1024 * 2), dict(k_out=P), dict(q=P + STEP, q_out=P + STEP),
+    dict(q_out=P, q_out_stride=i64(1024, 128), heads_q=9, q_stride=i64(1024, 128)),
+    # an output on the positions, the turns or a weight
+    dict(positions=P + 2 * STEP + 1024 * 2 - 4), dict(positions=P + 3 * STEP + 512), dict(q_out=P + 6 * STEP - 16),
+    dict(k_out=P + 7 * STEP + 496),
+])
+def test_rotations_onto_themselves_are_refused(lib, bad):
+    assert rotate(lib, rot(turns=P + 6 * STEP, k_weight=P + 7 * STEP), **{**FAR, **bad}) == ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q_out_stride=i64(128, 128)), dict(q_out_stride=i64(1024, 1024)), dict(q_out=P + 16), dict(q_out=P + STEP),
+    dict(q_out=P + 2 * STEP + ROW), dict(slots=P + 3 * STEP + 7 * ROW), dict(q_out=P + 6 * STEP),
+])
+def test_appends_onto_their_inputs_are_refused(lib, bad):
+    good = dict(q=P, k=P + STEP, v=P + 2 * STEP, q_out=P + 3 * STEP, slots=P + 4 * STEP)
+    assert append(lib, apart(), rot(turns=P + 6 * STEP), **{**good, **bad}) == ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up, and what is not refused is launched")
+def test_overlaps_equal_row_by_row(lib):
+    """Small layouts of every kind, refused just where two rows, taken byte by byte, overlap."""
+    rng = np.random.default_rng(0)
+    seen = {True: 0, False: 0}
+    for i in range(6000):
+        tokens, hq, hk = (int(x) for x in rng.integers(1, 5, 3))
+        step = lambda lo: 8 * int(rng.choice([16, 17, 24, 32, 33, 40, 48, 64, 80, 96, 112, 128, 160, 200, 256, 320, 384]
+                                             + ([0, 1, 8] if lo == 0 else [])))
+        pick = lambda lo: (step(lo), step(lo))
+        if i % 3 == 0:  # parts of one tensor, as a projection leaves them
+            all_heads = 2 * (hq + hk)
+            st = {n: (128 * all_heads, 128) for n in ("q", "k", "q_out", "k_out")}
+            at = {n: 256 * int(rng.integers(0, all_heads)) for n in st}
+        else:
+            st = {n: pick(0 if n in "qk" else 1) for n in ("q", "k", "q_out", "k_out")}
+            at = {n: 16 * int(rng.integers(0, 400)) for n in st}
+        for n in "qk":
+            if rng.random() < 0.4:
+                at[n + "_out"], st[n + "_out"] = at[n], st[n]
+        heads = dict(q=hq, k=hk, q_out=hq, k_out=hk)
+        rows = {n: [at[n] + 2 * (t * st[n][0] * (tokens > 1) + h * st[n][1] * (heads[n] > 1))
+                    for t in range(tokens) for h in range(heads[n])] for n in st}
+        legal = all(st[n][d] >= 128 or e == 1 for n in ("q_out", "k_out") for d, e in ((0, tokens), (1, heads[n])))
+        meet = lambda x, y, same=False: any(abs(a - b) < 256 for i, a in enumerate(rows[x]) for j, b in enumerate(rows[y])
+                                            if not (same and i == j))
+        bad = not legal
+        for n, other in (("q", "k"), ("k", "q")):
+            bad |= meet(n + "_out", n + "_out", True) or meet(n + "_out", other + "_out") or meet(n + "_out", other)
+            bad |= rows[n] != rows[n + "_out"] and meet(n, n + "_out")
+        code = rotate(lib, rot(turns=P + 6 * STEP, k_weight=P + 7 * STEP), heads_q=hq, heads_k=hk, tokens=tokens,
+                      positions=P + 8 * STEP, **{n: P + at[n] for n in st}, **{n + "_stride": i64(*st[n]) for n in st})
+        assert (code == ARG) == bad, (tokens, heads, st, at, code)
+        seen[bad] += 1
+    assert min(seen.values()) > 500
+
+
 @pytest.mark.parametrize("dtype", [ckv.BF16, ckv.F32])
 @pytest.mark.parametrize("bad,code", [
     (dict(q=None), ARG), (dict(out=None), ARG), (dict(q_stride=None), ARG), (dict(workspace=None), ARG),
