@@ -415,7 +415,7 @@ def rotary_turns(frequencies):
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
-                       original: int = 8192, low: float = 1.0, high: float = 32.0):
+                       original: int = 8192, low: float = 1.0, high: float | None = None):
     """(frequencies [rot / 2] in radians per position, amplitude) of rotary
     positions, w_i = base^(-2 i / rot), scaled for contexts ``factor`` times the
     ``original`` length by one of
@@ -426,8 +426,9 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
                 stay, those that turn less than ``low`` times are interpolated,
                 and in between the share goes with their number i; the amplitude
                 is 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071);
-      "bands"   the same borders (``high`` = 4 is usual), the share going with
-                the number of turns, and an amplitude of 1."""
+      "bands"   the same borders, the share going with the number of turns, and
+                an amplitude of 1.
+    ``high`` is 32 for a ramp and 4 for bands if None, as is usual."""
     if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
         raise ValueError(f"rot must be even and positive, base > 0 and factor >= 1, got {rot}, {base}, {factor}")
     if scaling not in (None, "linear", "base", "ramp", "bands"):
@@ -439,6 +440,8 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = No
     if scaling == "linear":
         w = [x / factor for x in w]
     elif scaling in ("ramp", "bands"):
+        if high is None:
+            high = 32.0 if scaling == "ramp" else 4.0
         if not 0 < low < high or original < 1:
             raise ValueError(f"0 < low < high and original >= 1 are needed, got {low}, {high}, {original}")
         if scaling == "ramp":

@@ -125,6 +125,16 @@ def test_frequency_scalings():
             ckv.rotary_frequencies(**bad)
 
 
+def test_usual_borders_of_the_scalings():
+    """A ramp ends at 32 turns where nothing is said, bands at 4."""
+    for scaling, high in (("ramp", 32.0), ("bands", 4.0)):
+        args = (128, 500000.0, scaling, 8.0, 8192)
+        assert ckv.rotary_frequencies(*args) == ckv.rotary_frequencies(*args, low=1.0, high=high)
+        assert ckv.rotary_frequencies(*args) != ckv.rotary_frequencies(*args, low=1.0, high=36.0 - high)
+    with pytest.raises(ValueError):
+        ckv.rotary_frequencies(128, scaling="bands", factor=8.0, low=4.0)
+
+
 # ---------------------------------------------------------------- refusals of the C ABI
 @pytest.fixture(scope="module")
 def lib():
