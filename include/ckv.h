@@ -521,8 +521,9 @@ ckv_status ckv_paged_evict_apply(const ckv_paged_cache* cache, int32_t budget, i
  * counts, start and first may be lens or seen themselves, held_out may be held_in
  * and span_out span_in.  free_pages must not overlap anything else.
  * Errors: as above; CKV_ERR_ARG (a null pointer other than start, first and
- * shared; n_slots or free_cap < 1; n_pages * page_size above 2^31 - 1; arrays
- * that overlap without being the same as above). */
+ * shared; n_slots or free_cap < 1, n_slots above 2^31 - 2^24 - 1, free_cap above
+ * 2^31 - 2; n_pages * page_size above 2^31 - 1; arrays that overlap without being
+ * the same as above). */
 ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t* counts, const int32_t* start,
                           const int32_t* first, const int32_t* shared, const int32_t* held_in, int32_t* held_out,
                           int32_t* free_pages, int32_t free_cap, const int32_t* span_in, int32_t* span_out,

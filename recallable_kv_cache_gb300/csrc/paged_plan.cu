@@ -114,7 +114,7 @@ __device__ __forceinline__ int4 slot_entry(const PlanArgs& a, int s, int row, in
     return make_int4(page * a.c.page + slot, s, row, position);
 }
 
-// Sums that stop at `most` (so that 32 bits do for whatever the inputs are):
+// Sums that stop at `most`, below 2^31 (so that 32 bits do for whatever the inputs are):
 // inclusive, of two values at a time.  `warp_sum` is not used again by a call
 // that no barrier parts from this one.
 template <int NT>
@@ -412,6 +412,7 @@ extern "C" ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t
         free_cap < 1 || n_slots < 1 || (long long)a.c.n_pages * a.c.page > 0x7fffffffLL)
         return CKV_ERR_ARG;
     if (n_slots > 0x7fffffff - (1 << 24)) return CKV_ERR_ARG;  // indices plus a grid's step stay below 2^31
+    if (free_cap == 0x7fffffff) return CKV_ERR_ARG;  // sums of pages stop at free_cap + 1, and two of them stay below 2^32
     if (!aligned16(slots)) return CKV_ERR_ALIGN;
     a.start = start ? start : a.c.lens;
     a.first = first ? first : a.c.seen;
