@@ -927,12 +927,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgsOf<C> a, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
     constexpr int TR = E::TR, NW = WARPS, NT = NW * 32;
-    // OWN: the kernel before is the one that attends the rows left out.  It began
-    // after what wrote the inputs had ended, and the two write nothing of each
-    // other's, so this one runs beside it, on the SMs that the other leaves, and
-    // waits for it at its end only, for the kernel behind both.  CTAs that have no
-    // SM left to them leave at once, so that the kernel behind can be brought in
-    // (there is always one that waits).
+    // OWN: the kernel before is the one that attends the rows left out.  It let this
+    // one start only when it had itself waited for all that wrote the inputs, and
+    // the two write nothing of each other's, so this one runs beside it, on the SMs
+    // that the other leaves, and waits for it at its end only, for the kernel behind
+    // both.  A wait is what makes writes visible; that the starts come in order does
+    // not promise that no older copy of skip, lens or q is still at hand here, and the
+    // fence drops one (a full fence took 0.6 us, this none).  CTAs that have no SM left
+    // to them leave at once, so that the kernel behind can be brought in (there is
+    // always one that waits).
     constexpr bool OWN = !std::is_same<C, Cache>::value;
     using T = typename E::T;
     extern __shared__ unsigned char smem_raw[];
@@ -960,7 +963,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         ptx::prefetch_tmap(threadIdx.x ? &tv : &tk);
         shared_units[threadIdx.x].x = -1;
     }
-    if (!OWN) ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
+    if (OWN) ptx::fence_acquire();
+    else ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
     const int grid = working_ctas(a.c);
     if (OWN && (int)blockIdx.x >= grid) return;

@@ -892,10 +892,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_shared_join(const __grid_c
     const long long n = (long long)a.c.seqs * heads_q, step = (long long)gridDim.x * JOIN_ROWS;
     bool waited = false;
     ptx::allow_dependent_launch();
+    // What the prep has left is whole: the kernel before this one began after it.
+    // It is looked up while that one is still at work, behind a fence, as no wait of
+    // this kernel's own has made it visible yet.
+    ptx::fence_acquire();
 #pragma unroll 1
     for (long long row = (long long)blockIdx.x * JOIN_ROWS + threadIdx.x % JOIN_ROWS; row < n; row += step) {
-        // What the prep has left is whole: the kernel before this one began
-        // after it.  It is looked up while that one is still at work.
         const int s = (int)(row / heads_q), hq = (int)(row - (long long)s * heads_q);
         const int i = a.group_of[s], skip = a.skip[s], held = a.c.lens[s], total = a.tile_base[a.groups];
         const int2 dealt = *a.deal;

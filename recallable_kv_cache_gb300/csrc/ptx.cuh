@@ -111,6 +111,11 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // scheduled now; it still waits for this one in grid_dependency_wait.
 __device__ __forceinline__ void allow_dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 
+// Loads after this see no older copy of what other grids have written in the
+// meantime.  For a kernel that reads before its wait what a grid behind its
+// predecessor has left.
+__device__ __forceinline__ void fence_acquire() { asm volatile("fence.acquire.gpu;" ::: "memory"); }
+
 // ---------------------------------------------------------------- tcgen05
 // One lane of a converged warp, for what a single thread issues.
 __device__ __forceinline__ bool elect_one() {

@@ -803,6 +803,43 @@ def test_shared_captured_and_on_streams():
             x.lens.copy_(ints(x.lens_list))
 
 
+def test_shared_lookups_follow_the_calls_before():
+    """Lengths, groups, prefixes and queries written just before each call, in one replayed graph:
+    every call sees its own, as a call by itself does."""
+    c = Shared([(512, [5, 30, 100, 64]), (96, [7, 200])], 2, 4, 16)
+    wide = [dict(starts=[0, 4, 6], prefix=[512, 96], cut=0), dict(starts=[0, 2, 6], prefix=[256, 0], cut=3),
+            dict(starts=[1, 4, 6], prefix=[480, 64], cut=0), dict(starts=[0, 4, 5], prefix=[16, 96], cut=5),
+            dict(starts=[3, 3, 6], prefix=[0, 0], cut=1), dict(starts=[0, 4, 6], prefix=[512, 96], cut=2)]
+    starts, prefix, q = ints([0, 0, 0]), ints([0, 0]), torch.zeros_like(c.q)
+    states = [(ints(x["starts"]), ints(x["prefix"]), ints([n - x["cut"] for n in c.lens_list]), c.q * (1 + i))
+              for i, x in enumerate(wide)]
+    outs = [torch.zeros_like(c.out) for _ in states]
+
+    def calls():
+        for (s, p, n, rows), out in zip(states, outs):
+            starts.copy_(s), prefix.copy_(p), c.lens.copy_(n), q.copy_(rows)
+            c.handle.shared_attn(q, out, starts, prefix)
+
+    alone = []
+    for (s, p, n, rows) in states:
+        c.lens.copy_(n)
+        out = torch.zeros_like(c.out)
+        torch.cuda.synchronize()
+        c.handle.shared_attn(rows, out, s, p)
+        torch.cuda.synchronize()
+        alone.append(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        calls()
+    for _ in range(50):
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, alone))
+    assert int(c.err) == 0
+
+
 @pytest.mark.parametrize("how", ["argument", "current"])
 def test_shared_handle_dropped_with_work_queued_on_another_stream(how):
     """Its workspace is not handed out while a side stream has yet to use it."""
