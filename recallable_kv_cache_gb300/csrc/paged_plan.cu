@@ -97,13 +97,14 @@ __device__ __forceinline__ int ring_at(int head, long long i, int cap) {
     const long long x = head + i;
     return (int)(x >= cap ? x - cap : x);
 }
-// the chunk in which item i is: the last entry that is not above i
-template <int NT>
-__device__ __forceinline__ int chunk_of(const long long* sums, long long i) {
+// The sequence (or the chunk of them) that item i belongs to: the last of the NT
+// whose items begin at i or before.
+template <int NT, typename T>
+__device__ __forceinline__ int owner_of(const T* begin, T i) {
     int lo = 0;
 #pragma unroll
     for (int step = NT / 2; step > 0; step >>= 1)
-        if (sums[lo + step] <= i) lo += step;
+        if (begin[lo + step] <= i) lo += step;
     return lo;
 }
 
@@ -133,15 +134,6 @@ __device__ __forceinline__ uint2 sums_to(uint2 v, uint2 most, uint2* warp_sum) {
     for (int o = 1; o < NT / 32; o <<= 1) add(w, o, lane >= o);
     const unsigned x = __shfl_sync(FULL, w.x, max(warp, 1) - 1), y = __shfl_sync(FULL, w.y, max(warp, 1) - 1);
     return warp ? make_uint2(min(v.x + x, most.x), min(v.y + y, most.y)) : v;
-}
-// the sequence that item i belongs to: the last of which the items begin at i or before
-template <int NT>
-__device__ __forceinline__ int seq_of(const unsigned* begin, unsigned i) {
-    int lo = 0;
-#pragma unroll
-    for (int step = NT / 2; step > 0; step >>= 1)
-        if (begin[lo + step] <= i) lo += step;
-    return lo;
 }
 
 // Up to NT sequences, one CTA, a thread a sequence.
@@ -196,7 +188,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
                 const bool takes = i < taken;
                 const unsigned item = takes ? i : i - taken;
                 const unsigned* from = takes ? takes_from : gives_from;
-                const int o = seq_of<NT>(from, item);
+                const int o = owner_of<NT>(from, item);
                 int32_t* row = a.table + (size_t)o * a.c.max_pages + (takes ? seq[o].z : seq[o].w) + (item - from[o]);
                 int32_t* ring = a.ring + ring_at(head, takes ? item : (long long)avail + item, a.cap);
                 page[k] = takes ? *ring : *row;
@@ -212,7 +204,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
         for (int t = s; t < a.n_slots; t += NT) {
             int4 e = make_int4(-1, -1, -1, -1);
             if (t < (int)tokens_from[NT]) {
-                const int o = seq_of<NT>(tokens_from, t), j = t - (int)tokens_from[o];
+                const int o = owner_of<NT>(tokens_from, (unsigned)t), j = t - (int)tokens_from[o];
                 const int4 v = seq[o];
                 if (v.x >= 0) e = slot_entry(a, o, v.x + j, v.y + j);
             }
@@ -305,21 +297,19 @@ __global__ void __launch_bounds__(NT) paged_plan_many_kernel(const __grid_consta
         const bool takes_page = i < taken;
         const long long item = takes_page ? i : i - taken;
         const long long* list = takes_page ? sums.takes : sums.gives;
-        const int c = chunk_of<NT>(list, item);
+        const int c = owner_of<NT>(list, item);
         long long left = item - list[c];
         int s = c * chunk;
         Seq q = look(a, s);
-        if (chunk > 1) {
-            // which sequences have no place for their tokens is settled by the running sum
-            long long at = sums.tokens[c];
-            for (;;) {
-                at += max(0, q.count);
-                if (at > a.n_slots && q.count > 0) q.need = q.held;
-                const int n = max(0, takes_page ? q.need - q.held : q.held - q.need);
-                if (left < n) break;
-                left -= n;
-                q = look(a, ++s);
-            }
+        // which sequences have no place for their tokens is settled by the running sum
+        long long at = sums.tokens[c];
+        for (;;) {
+            at += max(0, q.count);
+            if (at > a.n_slots && q.count > 0) q.need = q.held;
+            const int n = max(0, takes_page ? q.need - q.held : q.held - q.need);
+            if (left < n) break;
+            left -= n;
+            q = look(a, ++s);
         }
         int32_t* row = a.table + (size_t)s * a.c.max_pages;
         if (takes_page) {
@@ -333,7 +323,7 @@ __global__ void __launch_bounds__(NT) paged_plan_many_kernel(const __grid_consta
         for (int t = tid; t < a.n_slots; t += NT) {
             int4 e = make_int4(-1, -1, -1, -1);
             if (t < sums.tokens[NT]) {
-                const int c = chunk_of<NT>(sums.tokens, t);
+                const int c = owner_of<NT>(sums.tokens, (long long)t);
                 long long left = t - sums.tokens[c], before = sums.takes[c], at = sums.tokens[c];
                 int s = c * chunk;
                 Seq q = look(a, s);
