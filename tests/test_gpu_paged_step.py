@@ -318,6 +318,45 @@ def test_rotate(tokens, hq, hk, rot, interleaved, norm, dtype):
     assert all(x is None or torch.equal(x, y) for x, y in ((q2, qo), (k2, ko)))
 
 
+def sample(n, seed):
+    """The first and last tokens and some between."""
+    return sorted({0, 1, n - 2, n - 1} | set(np.random.default_rng(seed).integers(0, n, 12).tolist()))
+
+
+LONG = [
+    # rows a token: queries, keys; enough tokens that a lane group has 20 to 24 of them, or all 12 of a few heads
+    (32, 8, 128, False, True, "bf16"), (32, 8, 128, True, True, "f32"), (40, 8, 96, True, False, "bf16"),
+    (33, 8, 64, False, False, "f32"), (8, 4, 128, True, True, "bf16"), (41, 0, 0, False, True, "f32"),
+]
+
+
+@pytest.mark.parametrize("hq,hk,rot,interleaved,norm,dtype", LONG)
+def test_rotate_long(hq, hk, rot, interleaved, norm, dtype):
+    """Prompts, where every block keeps four rows under way and takes the next as they are done."""
+    gen = torch.Generator(device="cuda").manual_seed(hq + hk)
+    tokens = 5003
+    x = torch.randn(tokens, hq + hk, D, generator=gen, device="cuda").to(DT[dtype])
+    q, k = x[:, :hq], x[:, hq:] if hk else None
+    w = [1 + 0.3 * torch.randn(D, generator=gen, device="cuda") if norm else None for _ in range(2)]
+    positions = torch.arange(tokens, dtype=torch.int32, device="cuda") + 99_000
+    turns = ckv.rotary_turns(ckv.rotary_frequencies(rot)[0]).cuda() if rot else None
+    qo, ko = (None if x is None else torch.full_like(x, 9.0) for x in (q, k))
+    args = dict(interleaved=interleaved, q_weight=w[0], k_weight=w[1])
+    ckv.rotate(q, k, positions, turns, qo, ko, **args)
+    at = sample(tokens, rot)
+    for got, rows, weight in ((qo, q, w[0]), (ko, k, w[1])):
+        if rows is not None:
+            check_rows(got[at], rows[at], positions[at].tolist(), turns, rot, interleaved, weight, 1e-6, 1.0, dtype)
+    # every row is what a call of few tokens, whose blocks share a token's rows out, makes of it, and in place the same
+    few = [None if rows is None else torch.empty_like(rows) for rows in (q, k)]
+    for t in range(0, tokens, 150):
+        part = lambda rows: None if rows is None else rows[t:t + 150]
+        ckv.rotate(part(q), part(k), positions[t:t + 150], turns, part(few[0]), part(few[1]), **args)
+    ckv.rotate(q, k, positions, turns, q, k, **args)
+    for got, rows, one in ((qo, q, few[0]), (ko, k, few[1])):
+        assert rows is None or torch.equal(got, rows) and torch.equal(got, one)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotate_strided(dtype, interleaved):
@@ -464,6 +503,41 @@ def test_append_rotated(start, counts, heads, g, page, dtype, layout, rot, inter
                            q_weight=a.weights[0], k_weight=a.weights[1])
     a.check(turns, rot, interleaved, before)
     assert int(a.err) == 0
+
+
+@pytest.mark.parametrize("heads,g,page,dtype,layout,rot,interleaved", [
+    (8, 4, 16, "bf16", "phd", 128, False), (8, 4, 64, "f32", "hpd", 96, True), (4, 8, 48, "bf16", "hpd", 128, True),
+    (8, 3, 32, "f32", "phd", 128, False),
+])
+def test_append_long(heads, g, page, dtype, layout, rot, interleaved):
+    """Prompts of 40 to 48 rows a token into pages; tokens left out among them."""
+    counts = [1300, 7, 1999]
+    a = Append([3, 0, 40], counts, heads, g, page, dtype, layout)
+    turns = ckv.rotary_turns(ckv.rotary_frequencies(rot)[0]).cuda()
+    a.slots[[100, 2000]] = -1
+    a.pos.fill_(-5)
+    a.cache.append_rotated(a.q, a.k, a.v, a.slots, turns, a.q_out, interleaved=interleaved, q_weight=a.weights[0],
+                           k_weight=a.weights[1])
+    torch.cuda.synchronize()
+    rows = torch.tensor(a.rows, device="cuda")
+    kept = torch.ones(a.T, dtype=torch.bool, device="cuda")
+    kept[[100, 2000]] = False
+    page_of, slot = rows[:, 0] // page, rows[:, 0] % page
+    at = [t for t in sample(a.T, rot) if t not in (100, 2000)]
+    where = rows[at, 3].tolist()
+    check_rows(a.q_out[at], a.q[at], where, turns, rot, interleaved, a.weights[0], 1e-6, 1.0, dtype)
+    check_rows(a.K[page_of[at], :, slot[at]], a.k[at], where, turns, rot, interleaved, a.weights[1], 1e-6, 1.0, dtype)
+    assert torch.equal(a.V[page_of, :, slot][kept], a.v[kept])
+    # all rows: those of the rotation by itself
+    positions = rows[:, 3].int()
+    qo, ko = torch.full_like(a.q, 3.0), torch.empty_like(a.k)
+    ckv.rotate(a.q, a.k, positions, turns, qo, ko, interleaved=interleaved, q_weight=a.weights[0], k_weight=a.weights[1])
+    assert torch.equal(a.q_out[kept], qo[kept]) and (a.q_out[~kept] == 3).all()
+    assert torch.equal(a.K[page_of, :, slot][kept], ko[kept])
+    pos, mass = torch.full_like(a.pos, -5), torch.full_like(a.mass, 4.0)
+    pos[rows[kept, 1], :, rows[kept, 2]] = positions[kept][:, None]
+    mass[rows[kept, 1], :, rows[kept, 2]] = 0.0
+    assert torch.equal(a.pos, pos) and torch.equal(a.mass, mass) and int(a.err) == 0
 
 
 def test_append_with_queries_in_place():

@@ -125,6 +125,39 @@ def test_frequency_scalings():
             ckv.rotary_frequencies(**bad)
 
 
+@pytest.mark.parametrize("factor", [1.0, 4.0, 40.0])
+@pytest.mark.parametrize("rot,base,original,low,high", [
+    (128, 10000.0, 4096, 1.0, 32.0), (64, 10000.0, 32768, 1.0, 4.0), (128, 500000.0, 8192, 1.0, 4.0),
+    (16, 1e6, 4096, 1.0, 32.0), (128, 1e6, 64, 0.25, 7.5),  # borders in front of the first pair
+    (64, 10.0, 10 ** 6, 1.0, 32.0),                         # and behind the last
+])
+def test_every_pair_of_the_scalings(rot, base, factor, original, low, high):
+    """Both published formulas: by wavelengths, and by the pair whose wavelength fits
+    the original length a number of times."""
+    theta = np.float64(base) ** (-np.arange(0, rot, 2) / rot)
+    wavelength = 2 * np.pi / theta
+
+    # bands: wavelengths below original / high stay, above original / low are divided
+    smooth = (original / wavelength - low) / (high - low)
+    want = np.where(wavelength < original / high, theta,
+                    np.where(wavelength > original / low, theta / factor, (1 - smooth) * theta / factor + smooth * theta))
+    got, amplitude = ckv.rotary_frequencies(rot, base, "bands", factor, original, low, high)
+    assert amplitude == 1.0 and np.allclose(got, want, rtol=1e-12, atol=0)
+
+    # ramp: d ln(L / (2 pi n)) / (2 ln base) for the borders, whole and inside [0, d - 1]
+    border = lambda n: rot * np.log(original / (n * 2 * np.pi)) / (2 * np.log(base))
+    first, last = max(np.floor(border(high)), 0), min(np.ceil(border(low)), rot - 1)
+    if first == last:
+        last += 0.001
+    extrapolated = 1 - np.clip((np.arange(rot // 2) - first) / (last - first), 0, 1)
+    if first > last:  # the formula has no ramp here: every pair turns more than `high` times, and stays
+        assert (original / wavelength > high).all()
+        extrapolated = 1.0
+    want = theta / factor * (1 - extrapolated) + theta * extrapolated
+    got, amplitude = ckv.rotary_frequencies(rot, base, "ramp", factor, original, low, high)
+    assert abs(amplitude - (0.1 * np.log(factor) + 1)) < 1e-12 and np.allclose(got, want, rtol=1e-12, atol=0)
+
+
 def test_usual_borders_of_the_scalings():
     """A ramp ends at 32 turns where nothing is said, bands at 4."""
     for scaling, high in (("ramp", 32.0), ("bands", 4.0)):
