@@ -129,7 +129,7 @@ def test_frequency_scalings():
 @pytest.mark.parametrize("rot,base,original,low,high", [
     (128, 10000.0, 4096, 1.0, 32.0), (64, 10000.0, 32768, 1.0, 4.0), (128, 500000.0, 8192, 1.0, 4.0),
     (16, 1e6, 4096, 1.0, 32.0), (128, 1e6, 64, 0.25, 7.5),  # borders in front of the first pair
-    (64, 10.0, 10 ** 6, 1.0, 32.0),                         # and behind the last
+    (128, 10000.0, 10 ** 6, 1.0, 32.0), (128, 10000.0, 10 ** 6, 0.001, 32.0), (64, 10.0, 10 ** 6, 1.0, 32.0),  # behind the last
 ])
 def test_every_pair_of_the_scalings(rot, base, factor, original, low, high):
     """Both published formulas: by wavelengths, and by the pair whose wavelength fits
