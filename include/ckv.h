@@ -536,9 +536,10 @@ ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t* counts, c
  * for pair i < rot / 2 of channels (a, b) = (2 i, 2 i + 1) if interleaved, else
  * (i, i + rot / 2), where t = 2 pi p turns_i / 2^64; channels from rot on keep
  * y.  turns is the pair's frequency as a 64-bit fraction of a turn per position,
- * so that t is exact to 2^-32 of a turn at every position, however far (p *
- * turns_i wraps as the angle does); scalings for long contexts are a choice of
- * turns and amplitude.  fp32 arithmetic, rounded once at the end; sum_i x_i^2
+ * so that t is off by the same at every position, however far (p * turns_i wraps
+ * as the angle does): its upper 32 bits are taken, and what they are from the
+ * nearest quarter turn is rounded to fp32, less than 2^-28 + 2^-32 of a turn in
+ * all.  Scalings for long contexts are a choice of turns and amplitude.  fp32 arithmetic, rounded once at the end; sum_i x_i^2
  * has to stay below 2^127. */
 typedef struct {
     const uint64_t* turns; /* [rot / 2], 16-byte aligned; NULL only if rot is 0 */

@@ -8,7 +8,10 @@
 // by latency: one CTA keeps the sums in shared memory, and moves pages and
 // writes the slot map by items (a page, a token), each finding its sequence in
 // them by bisection, so that one long prompt is as spread out as many short
-// ones.  Slot maps of many tokens are left to a second kernel on all SMs.
+// ones (32 sequences of a token each: 2.9 us).  Where many pages change hands the
+// bisections are what it takes (509 sequences that hand 10.7k pages back: 9.3 us,
+// 60 % of the issue slots busy).  Slot maps of many tokens are left to a second
+// kernel on all SMs (48 prompts of 46k tokens: 5.9 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -230,7 +233,9 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const __grid_constant__ 
 }
 
 // More sequences.  One CTA; a thread has a chunk of neighbouring sequences and
-// looks at them three times, the later times in the first-level cache.
+// looks at them three times, the later times in the first-level cache, and an item
+// that has found its chunk walks through it (1500 / 4096 sequences of a token each
+// 14 / 22 us, and 47 / 144 where they hand 31 / 84 thousand pages back).
 template <int NT>
 __global__ void __launch_bounds__(NT) paged_plan_many_kernel(const __grid_constant__ PlanArgs a) {
     __shared__ Sums<NT> sums;

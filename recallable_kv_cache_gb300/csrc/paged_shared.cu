@@ -24,8 +24,8 @@
 // bits), so that the products are those of fp32 weights.  With one term outputs
 // would be off by 2^-9, with two by 1.4e-6 of the largest, with three by 4e-7,
 // which is what the decode attention of this library is off by.  That makes four
-// products a tile, some 1.1 us at the measured dense rate, against 1.5 us that an
-// SM's share of HBM takes for the tile's 64 KB.  T starts from zero at each tile
+// products a tile, 1.33 us at the measured dense rate, against 1.5 us that an SM's
+// share of HBM takes for the tile's 64 KB.  T starts from zero at each tile
 // and joins O by an ordinary addition, as the tensor core truncates what it
 // accumulates and O grows over hundreds of tiles; that also leaves O's scaling
 // off the path from one tile's maximum to the next one's product.
