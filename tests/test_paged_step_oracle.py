@@ -239,7 +239,7 @@ def test_bad_caches_are_refused(lib, bad, code):
     (dict(counts=None), ARG), (dict(held_in=None), ARG), (dict(held_out=None), ARG), (dict(ring=None), ARG),
     (dict(span_in=None), ARG), (dict(span_out=None), ARG), (dict(granted=None), ARG), (dict(starts=None), ARG),
     (dict(slots=None), ARG), (dict(cap=0), ARG), (dict(n_slots=0), ARG), (dict(n_slots=2 ** 31 - 1), ARG),
-    (dict(slots=P + 8), ALIGN), (dict(cap=2 ** 31 - 1, ring=P + 64 * STEP), ARG),
+    (dict(slots=P + 8), ALIGN),
     # overlaps: an output with another output, with an input that is not its own pair, or in part
     (dict(granted=P + 2 * STEP), ARG), (dict(starts=P + 3 * STEP + 8), ARG), (dict(held_out=P + 2 * STEP), ARG),
     (dict(start=P + 2 * STEP + 4), ARG), (dict(first=P + 3 * STEP - 4), ARG), (dict(ring=P + STEP), ARG),
@@ -247,6 +247,10 @@ def test_bad_caches_are_refused(lib, bad, code):
 ])
 def test_bad_plans_are_refused(lib, bad, code):
     assert plan(lib, apart(), **bad) == code
+
+
+def test_plan_from_the_longest_ring_is_refused(lib):
+    assert plan(lib, apart(), cap=2 ** 31 - 1, ring=P + 64 * STEP) == ARG
 
 
 def test_plan_of_too_many_slots_is_refused(lib):
