@@ -94,6 +94,19 @@ cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int3
                                  const long long* q_stride, int g, float qscale, float* out, float* lse, void* workspace,
                                  cudaStream_t s);
 
+// Groups of sequences with leading rows in common, as ckv_paged_shared_attn takes them.
+struct Groups {
+    const int32_t* starts;
+    const int32_t* prefix;
+    int n;
+};
+// Up to this many groups and sequences a CTA looks them up by itself, a lane a group.
+constexpr int FEW_GROUPS = 32, FEW_SEQS = 1024;
+// Decode attention, fp32, of few groups: a sequence attends its own number of rows, or
+// its group's where that is more.
+cudaError_t launch_attn_in_groups(const Cache& c, const Groups& groups, const void* q, const long long* q_stride, int g,
+                                  float qscale, float* out, float* lse, void* workspace, cudaStream_t s);
+
 // two arrays of n 32-bit elements that are one and the same (an element is read
 // before it is written) or do not overlap; no array overlaps nothing
 inline bool same_or_apart(const void* x, const void* y, long long n) {

@@ -59,6 +59,57 @@ struct OwnRows : Cache {
     // c, parts of CTAs c .. c + n - 1; n = 0: the result, in out and lse2
     int32_t* left;
 };
+// A cache in whose sequences a group's leading rows stand, which each attends by
+// itself.  Its own or the group's rows, whichever are more, are looked up by every
+// CTA into shared memory (0.5 us; by a kernel in front of this one 2).
+struct GroupRows : Cache {
+    Groups groups;
+};
+__device__ __forceinline__ int* rows_here() {
+    __shared__ int rows[FEW_SEQS];
+    return rows;
+}
+__device__ __forceinline__ int rows_held(const GroupRows&, int s) { return rows_here()[s]; }
+template <int NT>
+__device__ __forceinline__ void look_up_rows(const GroupRows& c) {
+    __shared__ int first[FEW_GROUPS], end[FEW_GROUPS], shared[FEW_GROUPS];
+    int* rows = rows_here();
+    const int tid = threadIdx.x, n = c.groups.n;
+    const bool reports = blockIdx.x == 0;
+    int start = c.seqs, next = c.seqs, prefix = 0;
+    if (tid < n) {
+        start = c.groups.starts[tid];
+        next = c.groups.starts[tid + 1];
+        prefix = c.groups.prefix[tid];
+        if (reports && (start < 0 || next > c.seqs || start > next || prefix < 0)) report(c.dev_err, CKV_DEV_BAD_COUNT);
+    }
+    for (int s = tid; s < c.seqs; s += NT) rows[s] = rows_held(static_cast<const Cache&>(c), s);
+    __syncthreads();
+    if (tid < 32) {
+        // starts ascend: each is at least the largest before it
+        int x = max(0, min(start, c.seqs));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL, x, o);
+            if (tid >= o) x = max(x, y);
+        }
+        const int e = max(x, min(next, c.seqs));
+        first[tid] = x;
+        end[tid] = e;
+        shared[tid] = e - x > 1 ? min(max(prefix, 0), rows[x]) & ~(TILE - 1) : 0;
+    }
+    __syncthreads();
+    for (int s = tid; s < c.seqs; s += NT) {
+        int i = -1;  // the last group that begins at s or before
+        for (int k = 0; k < n; ++k)
+            if (first[k] <= s) i = k;
+        if (i >= 0 && s < end[i] && shared[i] > rows[s]) {
+            if (reports) report(c.dev_err, CKV_DEV_BAD_COUNT);
+            rows[s] = shared[i];
+        }
+    }
+    __syncthreads();
+}
 __device__ __forceinline__ int working_ctas(const Cache&) { return gridDim.x; }
 __device__ __forceinline__ int working_ctas(const OwnRows& c) { return min((int)gridDim.x, max(1, *c.ctas)); }
 __device__ __forceinline__ int first_row(const Cache&, int) { return 0; }
@@ -741,7 +792,8 @@ struct TilesF32Tc {
         }
     }
     // tiles k0 .. k1 of unit u again, on fp32 products of the pool's values
-    __device__ __forceinline__ void again(const AttnArgs& a, int u, int k0, int k1, int lane) {
+    template <typename C>
+    __device__ __forceinline__ void again(const AttnArgsOf<C>& a, int u, int k0, int k1, int lane) {
         const int row = lane >> 2, t = lane & 3;
         int h;
         const int seq = a.c.by_heads.quot(u, &h), len = rows_held(a.c, seq);
@@ -936,7 +988,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     // fence drops one (a full fence took 0.6 us, this none).  CTAs that have no SM left
     // to them leave at once, so that the kernel behind can be brought in (there is
     // always one that waits).
-    constexpr bool OWN = !std::is_same<C, Cache>::value;
+    constexpr bool OWN = std::is_same<C, OwnRows>::value;
     using T = typename E::T;
     extern __shared__ unsigned char smem_raw[];
     // swizzled tiles need 1024-byte alignment
@@ -966,6 +1018,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     if (OWN) ptx::fence_acquire();
     else ptx::grid_dependency_wait();  // lens, table, K, V, q may come from the previous kernel
     ptx::allow_dependent_launch();
+    if constexpr (std::is_same<C, GroupRows>::value) look_up_rows<NT>(a.c);
     const int grid = working_ctas(a.c);
     if (OWN && (int)blockIdx.x >= grid) return;
     int cta = blockIdx.x;
@@ -1346,6 +1399,31 @@ cudaError_t launch(const AttnArgsOf<C>& a, int sms, int dev, cudaStream_t s) {
     return e;
 }
 
+template <typename C>
+cudaError_t launch_f32(const AttnArgsOf<C>& a, int sms, int dev, cudaStream_t s) {
+    if (a.g == 1) return launch<TilesF32<1>>(a, sms, dev, s);
+    if (a.g == 2) return launch<TilesF32<2>>(a, sms, dev, s);
+    if (a.g <= 4) return launch<TilesF32<4>>(a, sms, dev, s);
+    if (a.g <= 8) return launch<TilesF32<8>>(a, sms, dev, s);
+    return launch<TilesF32Tc<2>>(a, sms, dev, s);
+}
+// what the calls without weights have in common
+template <typename C>
+void take(AttnArgsOf<C>* a, const void* q, const long long* q_stride, int g, float qscale, float* out, float* lse, void* workspace) {
+    const Layout l = layout_of(a->c, g, false);
+    unsigned char* w = static_cast<unsigned char*>(workspace);
+    a->q = q;
+    a->qst[0] = q_stride[0];
+    a->qst[1] = q_stride[1];
+    a->g = g;
+    a->qscale = qscale;
+    a->out = out;
+    a->lse = lse;
+    a->arrived = reinterpret_cast<unsigned*>(w);
+    a->part = reinterpret_cast<float*>(w + l.part);
+    a->lse2 = reinterpret_cast<float*>(w + l.lse2);
+}
+
 std::atomic<long long> wait_limit{WAIT_LIMIT};
 std::atomic<int> stall_switch{0};
 
@@ -1371,24 +1449,25 @@ cudaError_t launch_attn_own_rows(const Cache& c, const int32_t* skip, const int3
     a.c.skip = skip;
     a.c.ctas = ctas;
     a.c.left = left;
-    const Layout l = layout_of(c, g, false);
-    unsigned char* w = static_cast<unsigned char*>(workspace);
-    a.q = q;
-    a.qst[0] = q_stride[0];
-    a.qst[1] = q_stride[1];
-    a.g = g;
-    a.qscale = qscale;
-    a.out = out;
-    a.lse = lse;
-    a.arrived = reinterpret_cast<unsigned*>(w);
-    a.part = reinterpret_cast<float*>(w + l.part);
-    a.lse2 = reinterpret_cast<float*>(w + l.lse2);
+    take(&a, q, q_stride, g, qscale, out, lse, workspace);
     waits(&a.wait_limit, &a.stall);
     a.stall = 0;  // the kernel before this one is the one to stall
     int dev = 0;
     const int sms = sm_count(&dev);
     if (sms < 1) return cudaErrorInvalidDevice;
     return g <= 8 ? launch<TilesBf16<1>>(a, sms, dev, s) : launch<TilesBf16<2>>(a, sms, dev, s);
+}
+
+cudaError_t launch_attn_in_groups(const Cache& c, const Groups& groups, const void* q, const long long* q_stride, int g,
+                                  float qscale, float* out, float* lse, void* workspace, cudaStream_t s) {
+    AttnArgsOf<GroupRows> a = {};
+    static_cast<Cache&>(a.c) = c;
+    a.c.groups = groups;
+    take(&a, q, q_stride, g, qscale, out, lse, workspace);
+    waits(&a.wait_limit, &a.stall);
+    int dev = 0;
+    const int sms = sm_count(&dev);
+    return sms < 1 ? cudaErrorInvalidDevice : launch_f32(a, sms, dev, s);
 }
 
 }  // namespace paged
@@ -1461,10 +1540,6 @@ extern "C" ckv_status ckv_paged_decode_attn(const ckv_paged_cache* cache, const 
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (bf16) e = g <= 8 ? launch<TilesBf16<1>>(a, grid, dev, s) : launch<TilesBf16<2>>(a, grid, dev, s);
-    else if (g == 1) e = launch<TilesF32<1>>(a, grid, dev, s);
-    else if (g == 2) e = launch<TilesF32<2>>(a, grid, dev, s);
-    else if (g <= 4) e = launch<TilesF32<4>>(a, grid, dev, s);
-    else if (g <= 8) e = launch<TilesF32<8>>(a, grid, dev, s);
-    else e = launch<TilesF32Tc<2>>(a, grid, dev, s);
+    else e = launch_f32(a, grid, dev, s);
     return e == cudaSuccess ? CKV_OK : CKV_ERR_CUDA;
 }

@@ -225,8 +225,8 @@ __device__ __forceinline__ Run run_in(const Group& gr, int base, int t, int t_en
 // It is the latency of a chain of small steps, 1.1 us of it the first loads.
 // LENS: fp32 rows, which every sequence attends by itself.  The groups are looked
 // at all the same, and skip[s] becomes the rows that s attends: its own number, or
-// the group's where that is more (12 sequences of two groups: 20.0 us without, 21.9).
-constexpr int FEW_GROUPS = 32, FEW_SEQS = 1024;
+// the group's where that is more.  (Few groups the attention looks at itself: 12
+// sequences of two groups took 22 us with this in front, 20 without.)
 template <bool FEW, bool LENS>
 __global__ void __launch_bounds__(PREP_THREADS) paged_shared_prep(const __grid_constant__ SharedArgs a) {
     __shared__ int warp_val[PREP_THREADS / 32];
@@ -1035,12 +1035,7 @@ Layout layout_of(const Cache& c, int g) {
     return l;
 }
 
-template <bool LENS>
-cudaError_t launch_prep(const SharedArgs& a, cudaStream_t s) {
-    const bool few = a.groups <= FEW_GROUPS && a.c.seqs <= FEW_SEQS;
-    return launch_dependent(few ? paged_shared_prep<true, LENS> : paged_shared_prep<false, LENS>, dim3(1),
-                            dim3(PREP_THREADS), 0, s, a);
-}
+bool few(const SharedArgs& a) { return a.groups <= FEW_GROUPS && a.c.seqs <= FEW_SEQS; }
 
 cudaError_t launch_shared(SharedArgs& a, void* workspace, cudaStream_t s) {
     int dev = 0;
@@ -1066,7 +1061,8 @@ cudaError_t launch_shared(SharedArgs& a, void* workspace, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    cudaError_t e = launch_prep<false>(a, s);
+    cudaError_t e = launch_dependent(few(a) ? paged_shared_prep<true, false> : paged_shared_prep<false, false>, dim3(1),
+                                     dim3(PREP_THREADS), 0, s, a);
     if (e == cudaSuccess) e = launch_dependent(paged_shared_kernel, dim3(a.grid), dim3(THREADS), smem, s, a, tk, tv);
     const long long qst[2] = {a.qst[0] / 2, a.qst[1] / 2};
     if (e == cudaSuccess)
@@ -1148,7 +1144,15 @@ extern "C" ckv_status ckv_paged_shared_attn(const ckv_paged_cache* cache, const 
     a.cta_o = reinterpret_cast<float4*>(w + l.cta_o);
     a.cta_ml = reinterpret_cast<float4*>(w + l.cta_ml);
     if (!bf16) {
-        if (launch_prep<true>(a, (cudaStream_t)stream) != cudaSuccess) return CKV_ERR_CUDA;
+        cudaStream_t s = (cudaStream_t)stream;
+        if (few(a)) {
+            const Groups of{group_starts, prefix, groups};
+            const long long qst[2] = {a.qst[0] / 4, a.qst[1] / 4};
+            return launch_attn_in_groups(a.c, of, q, qst, g, a.qscale, out, lse, workspace, s) == cudaSuccess ? CKV_OK
+                                                                                                             : CKV_ERR_CUDA;
+        }
+        if (launch_dependent(paged_shared_prep<false, true>, dim3(1), dim3(PREP_THREADS), 0, s, a) != cudaSuccess)
+            return CKV_ERR_CUDA;
         ckv_paged_cache attended = *cache;
         attended.lens = a.skip;
         return ckv_paged_decode_attn(&attended, q, q_dtype, q_stride, g, scale, out, lse, nullptr, nullptr, workspace,

@@ -772,6 +772,18 @@ def test_shared_fp32_shorter_member_of_many(short):
     assert int(c.err) == 3
 
 
+@pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
+def test_shared_fp32_shorter_members_of_few(g):
+    """As many groups and sequences as a block looks up by itself, every form of the fp32 tiles."""
+    c = Shared([(32, [1, 0])] * 31 + [(160, [i % 3 for i in range(962)])], 1, g, 16, "f32")
+    assert len(c.prefix) == 32 and c.S == 1024
+    for s in (1, 61, 63, 700, 1023):
+        c.lens[s], c.lens_list[s] = 5, 160 if s > 61 else 32
+    c.run()
+    c.check()
+    assert int(c.err) == 3
+
+
 @pytest.mark.parametrize("page", [16, 48, 128])
 def test_shared_bad_pages_are_skipped(page):
     """Bad ids in the prefix and in a sequence's own pages; a whole tile of them."""
