@@ -539,8 +539,8 @@ ckv_status ckv_paged_plan(const ckv_paged_cache* cache, const int32_t* counts, c
  * so that t is off by the same at every position, however far (p * turns_i wraps
  * as the angle does): its upper 32 bits are taken, and what they are from the
  * nearest quarter turn is rounded to fp32, less than 2^-28 + 2^-32 of a turn in
- * all.  Scalings for long contexts are a choice of turns and amplitude.  fp32 arithmetic, rounded once at the end; sum_i x_i^2
- * has to stay below 2^127. */
+ * all.  Scalings for long contexts are a choice of turns and amplitude.  fp32
+ * arithmetic, rounded once at the end; sum_i x_i^2 has to stay below 2^127. */
 typedef struct {
     const uint64_t* turns; /* [rot / 2], 16-byte aligned; NULL only if rot is 0 */
     const float* q_weight; /* [d], 16-byte aligned, or NULL: queries are not normed */
@@ -561,9 +561,9 @@ typedef struct {
  * projection's queries and keys, do not.
  * Errors: CKV_ERR_ARG (d != 128, tokens < 1, a negative head count or none at
  * all, rot, eps < 0 or not finite, amplitude not finite, interleaved not 0 or 1,
- * null pointers, strides, more than 2^31 - 2^16 rows, rows that overlap or are
- * strewn through one another in more than 2^16 ways), CKV_ERR_DTYPE,
- * CKV_ERR_ALIGN. */
+ * null pointers, strides, more than 2^31 - 2^16 rows, rows that overlap, or that
+ * lie between each other with strides that differ, where more than 2^16 pairs of
+ * heads (and tokens) would have to be compared), CKV_ERR_DTYPE, CKV_ERR_ALIGN. */
 ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const int64_t* q_stride, void* q_out,
                       const int64_t* q_out_stride, int32_t heads_q, const void* k, const int64_t* k_stride,
                       void* k_out, const int64_t* k_out_stride, int32_t heads_k, const int32_t* positions,
@@ -578,7 +578,8 @@ ckv_status ckv_rotate(const ckv_rotary* rotary, const void* q, const int64_t* q_
  * leaves the token out as well (CKV_DEV_BAD_INDEX).  No two tokens may have the
  * same slot, and no slot may be one that the call reads.  lens, seen and the
  * table are not used: the plan has set them.
- * Errors: as above (of overlaps, q_out's); CKV_ERR_ARG (g < 0, n_pages * page_size above 2^31 - 1). */
+ * Errors: as above (of overlaps, q_out's); CKV_ERR_ARG (g < 0, n_pages *
+ * page_size above 2^31 - 1). */
 ckv_status ckv_paged_append_rotated(const ckv_paged_cache* cache, const ckv_rotary* rotary, const void* q,
                                     const int64_t* q_stride, int32_t g, void* q_out, const int64_t* q_out_stride,
                                     const void* k, const int64_t* k_stride, const void* v, const int64_t* v_stride,

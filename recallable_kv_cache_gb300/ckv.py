@@ -804,8 +804,8 @@ class PagedCache:
         """decode_attn (without weights) where sequences group_starts[i] ..
         group_starts[i + 1] - 1 have their first prefix[i] rows in common, which
         are then read once for all of them (see ckv_paged_shared_attn; those of a
-        float32 cache are read once for each): group_starts [groups + 1] and prefix [groups] int32.  The handle must have
-        been made with shared=True."""
+        float32 cache are read once for each): group_starts [groups + 1] and prefix
+        [groups] int32.  The handle must have been made with shared=True."""
         if not self.shared:
             raise ValueError("the handle was made without shared=True and has no workspace for this call")
         if q.shape != self._q_shape:
